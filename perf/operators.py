@@ -68,7 +68,7 @@ def listed():
              new="1"),
         # the serving batch: 256 sequences of 256 to 8,192 tokens, one new token each
         dict(name="decode-256", kind="decode", dtype="bf16", H=32, dl=512, dr=64, page=64,
-             lens=_text(_uniform(5, 256, 256, 8192)), new=_text([1] * 256)),
+             lens=_text(_uniform(7, 256, 256, 8192)), new=_text([1] * 256)),
         # chunks of 128 new tokens of 16 prompts over their cached prefixes (chunked prefill, resumed prefixes)
         dict(name="decode-chunk-16x128", kind="decode", dtype="bf16", H=32, dl=512, dr=64, page=64,
              lens=_text(_uniform(6, 16, 1024, 4096)), new=_text([128] * 16)),
@@ -77,7 +77,7 @@ def listed():
              new="1,1,3,2"),
         # the cache write of one serving step: 256 sequences, one token each
         dict(name="append-step-256", kind="append", dtype="bf16", dl=512, dr=64, page=64,
-             lens=_text(_uniform(5, 256, 256, 8192)), new=_text([1] * 256), interleaved=True, outs=False),
+             lens=_text(_uniform(7, 256, 256, 8192)), new=_text([1] * 256), interleaved=True, outs=False),
         # the cache write of 16 whole prompts, which also keeps the normalised latents for their expansion
         dict(name="append-prompts-16", kind="append", dtype="bf16", dl=512, dr=64, page=64,
              lens=_text(_uniform(3, 16, 256, 4096)), new=_text(_uniform(3, 16, 256, 4096)), interleaved=False,
