@@ -1,0 +1,214 @@
+// latent_attention.hip -- expanded latent attention, forward.
+//
+// For a sequence with n queries and m keys, per head (scale > 0):
+//   z_ij = scale (q_i . [k_j, k_pe_j]), j <= i + (m - n) when causal
+//   o_i  = sum_j exp(z_ij - z_max) v_j / sum_j exp(z_ij - z_max)
+// in one pass over the keys with the running maximum and sum.  The scores of a
+// tile are formed transposed, S^T = K Q^T (rows = keys), so that a lane holds
+// 4 neighbouring keys of one query row: as they stand, exponentiated, they are
+// the operand of O^T += V^T P^T, whose other operand is V read by columns.
+// Scores and weights never leave the registers, and the row's maximum, sum and
+// rescale factor are one value per lane.
+#include "latent_common.h"
+
+namespace kda {
+
+// A workgroup: 4 waves of 32 query rows (two 16-row tiles, whose operands q
+// and o stay in registers), one head.  Key and value tiles of BN rows are
+// double-buffered in LDS (80 KB, two workgroups a CU): the next tile's global
+// loads are issued before a tile's products and stored to LDS behind them.
+template <typename E, int DN, int DR>
+__global__ __launch_bounds__(256, 2) void latent_attention_kernel(
+    const kda_latent_inputs in, E* __restrict__ o, float* __restrict__ lse, int tiles)
+{
+    constexpr int DQK = DN + DR, DV = DN, BN = 128 / (int)sizeof(E), NQ = 2;
+    constexpr int KS = DQK / 32, TT = BN / 16, CE = CHUNK_ELEMS<E>;
+    typedef typename Vec<E>::v8 v8;
+    __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
+
+    int h, want, seq, tile;
+    head_tile_of_block(in.H, tiles, h, want);
+    const int rows_q = (int)(in.total_q / in.num_seqs);
+    if (!find_tile<LATENT_BQ, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, tiles - 1 - want,
+                                   reinterpret_cast<int*>(&smem[0][0]), seq, tile))
+        return;
+    int q0, q1, k0, k1;
+    sequence_rows(in.cu_seqlens_q, rows_q, (int)in.total_q, seq, q0, q1);
+    sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
+                  (int)in.total_k, seq, k0, k1);
+    const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int wrow = tile * LATENT_BQ + 32 * wave;   // the wave's first row in the sequence
+    const float sc = in.scale * LOG2E;
+
+    const E* kp = (const E*)in.k + (int64_t)k0 * in.k_token_stride + h * in.k_head_stride;
+    const E* vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
+    const E* pp = DR ? (const E*)in.k_pe + (int64_t)k0 * in.k_pe_token_stride : nullptr;
+
+    // this lane's query rows, and the last key each sees
+    v8 q[NQ][KS];
+    int last[NQ];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = wrow + 16 * j + col;
+        const E* row = (const E*)in.q + (int64_t)(q0 + min(r, nq - 1)) * in.q_token_stride + h * in.q_head_stride;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(row, ks, lane);
+        last[j] = in.causal ? min(nk - 1, r + off) : nk - 1;
+    }
+    const int end = in.causal ? min(nk, min(nq, (tile + 1) * LATENT_BQ) + off) : nk;   // keys of the workgroup
+    const int nt = end > 0 ? (end + BN - 1) / BN : 0;
+    const int wave_end = in.causal ? min(nk, min(nq, wrow + 32) + off) : nk;           // of the wave
+    const int wave_full = in.causal ? min(nk, wrow + off + 1) : nk;                    // keys all its rows see
+
+    Stage<E, DQK, BN, 256> sk;
+    Stage<E, DV, BN, 256> sv;
+    auto load = [&](int t) {
+        sk.load(tid, [&](int r, int c) -> const E* {
+            const int key = t * BN + r;
+            if (key >= nk) return nullptr;
+            if (DR && c * CE >= DN) return pp + (int64_t)key * in.k_pe_token_stride + (c * CE - DN);
+            return kp + (int64_t)key * in.k_token_stride + c * CE;
+        });
+        sv.load(tid, [&](int r, int c) -> const E* {
+            const int key = t * BN + r;
+            return key < nk ? vp + (int64_t)key * in.v_token_stride + c * CE : nullptr;
+        });
+    };
+
+    f32x4 acc[NQ][DV / 16];
+    float m[NQ], l[NQ];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        m[j] = neg_inf();
+        l[j] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (nt > 0) {
+        load(0);
+        sk.store(tid, smem[0]);
+        sv.store(tid, smem[0] + BN * DQK);
+    }
+    __syncthreads();
+    for (int t = 0; t < nt; ++t) {
+        const E* K = smem[t & 1];
+        const E* V = K + BN * DQK;
+        if (t + 1 < nt) load(t + 1);
+        if (t * BN < wave_end) {
+            f32x4 s[NQ][TT];
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) s[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const v8 a = row_frag<DQK>(K, 16 * tt, ks, lane);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) s[j][tt] = mma32(a, q[j][ks], s[j][tt]);
+                }
+            }
+            if ((t + 1) * BN > wave_full) {
+#pragma unroll
+                for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (t * BN + 16 * tt + 4 * g + i > last[j]) s[j][tt][i] = neg_inf();
+            }
+            // The running maximum is raised only when a row's grew by more than
+            // 8 (in powers of two): until then the weights stay below 2^8 and
+            // nothing needs rescaling.
+            float top[NQ];
+            bool grew = false;
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                float x = neg_inf();
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x = fmaxf(x, s[j][tt][i]);
+                top[j] = group_max(x) * sc;
+                grew |= top[j] > m[j] + 8.f;
+            }
+            if (__any(grew)) {
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const float mn = fmaxf(m[j], top[j]);
+                    const float f = mn == neg_inf() ? 1.f : exp2_fast(m[j] - mn);
+                    m[j] = mn;
+                    l[j] *= f;
+#pragma unroll
+                    for (int c = 0; c < DV / 16; ++c) acc[j][c] *= f;
+                }
+            }
+            v8 p[NQ][TT / 2];
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                const float base = m[j] == neg_inf() ? 0.f : m[j];   // a row that has seen no key yet
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -base));
+                        l[j] += s[j][tt][i];   // the sum takes the weights before their rounding
+                    }
+#pragma unroll
+                for (int b = 0; b < TT / 2; ++b) p[j][b] = acc_frag(s[j][2 * b], s[j][2 * b + 1], E());
+            }
+#pragma unroll
+            for (int c = 0; c < DV / 16; ++c)
+#pragma unroll
+                for (int b = 0; b < TT / 2; ++b) {
+                    const v8 a = col_frag<DV>(V, 32 * b, 32 * b + 16, 16 * c, lane);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(a, p[j][b], acc[j][c]);
+                }
+        }
+        if (t + 1 < nt) {
+            E* next = smem[(t + 1) & 1];
+            sk.store(tid, next);
+            sv.store(tid, next + BN * DQK);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = wrow + 16 * j + col;
+        const float sum = group_sum(l[j]);
+        if (r >= nq) continue;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        E* row = o + ((int64_t)(q0 + r) * in.H + h) * DV;
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) {
+            typename Vec<E>::v4 x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(acc[j][c][i] * inv);
+            store_vec(row + 16 * c + 4 * g, x);
+        }
+        if (lse && g == 0)
+            lse[(int64_t)(q0 + r) * in.H + h] = sum == 0.f ? neg_inf() : (m[j] + __log2f(sum)) * LN2;
+    }
+}
+
+template <typename E, int DN, int DR>
+static hipError_t launch(const kda_latent_inputs& in, void* o, float* lse, hipStream_t stream) {
+    const int64_t rows = in.total_q / in.num_seqs;
+    const int64_t tiles = in.cu_seqlens_q ? in.total_q / LATENT_BQ + in.num_seqs
+                                          : (rows + LATENT_BQ - 1) / LATENT_BQ * in.num_seqs;
+    hipLaunchKernelGGL((latent_attention_kernel<E, DN, DR>), dim3((unsigned)(tiles * in.H)), dim3(256), 0, stream,
+                       in, (E*)o, lse, (int)tiles);
+    return hipGetLastError();
+}
+
+hipError_t launch_latent_attention(const kda_latent_inputs& in, void* o, float* lse, hipStream_t stream) {
+    if (in.dtype == KDA_DTYPE_BF16) {
+        if (in.dn == 128) return in.dr ? launch<bf16, 128, 64>(in, o, lse, stream) : launch<bf16, 128, 0>(in, o, lse, stream);
+        return in.dr ? launch<bf16, 64, 64>(in, o, lse, stream) : launch<bf16, 64, 0>(in, o, lse, stream);
+    }
+    if (in.dn == 128) return in.dr ? launch<float, 128, 64>(in, o, lse, stream) : launch<float, 128, 0>(in, o, lse, stream);
+    return in.dr ? launch<float, 64, 64>(in, o, lse, stream) : launch<float, 64, 0>(in, o, lse, stream);
+}
+
+}  // namespace kda

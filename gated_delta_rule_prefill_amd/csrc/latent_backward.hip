@@ -1,0 +1,363 @@
+// latent_backward.hip -- gradients of the expanded latent attention.
+//
+// With the forward's weights w_ij = exp(z_ij - lse_i), z = scale q [k, k_pe]^T,
+// the output gradient g_i = dL/do_i and delta_i = g_i . o_i:
+//   dv_j = sum_i w_ij g_i
+//   dz_ij = w_ij (g_i . v_j - delta_i)
+//   dq_i = scale sum_j dz_ij [k_j, k_pe_j]
+//   [dk_j, dk_pe_j] = scale sum_i dz_ij q_i,  dk_pe summed over the heads
+// Two kernels, so that every sum stays in one workgroup's registers and the
+// result does not depend on an order of atomics: one walks the keys for a tile
+// of query rows (dq, and delta on the way), one walks the query rows for a
+// tile of keys (dk, dv and the head's part of dk_pe).  Each forms the weights
+// again from q, k and lse: one of seven products more than a single kernel
+// with atomic sums of dq.  A third kernel sums dk_pe over the heads.
+#include "latent_common.h"
+
+namespace kda {
+
+// Query rows per workgroup: 16 NQ per wave.
+template <typename E> constexpr int DQ_NQ = sizeof(E) == 2 ? 2 : 1;
+
+// dq and delta.  As in the forward kernel the scores are formed transposed
+// (rows = keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.
+template <typename E, int DN, int DR>
+__global__ __launch_bounds__(256, 2) void latent_dq_kernel(
+    const kda_latent_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
+    const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ delta, int tiles)
+{
+    constexpr int DQK = DN + DR, DV = DN, BN = 32, NQ = DQ_NQ<E>, BQ = 64 * NQ;
+    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, CE = CHUNK_ELEMS<E>;
+    typedef typename Vec<E>::v8 v8;
+    __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
+
+    int h, want, seq, tile;
+    head_tile_of_block(in.H, tiles, h, want);
+    const int rows_q = (int)(in.total_q / in.num_seqs);
+    if (!find_tile<BQ, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, tiles - 1 - want,
+                            reinterpret_cast<int*>(&smem[0][0]), seq, tile))
+        return;
+    int q0, q1, k0, k1;
+    sequence_rows(in.cu_seqlens_q, rows_q, (int)in.total_q, seq, q0, q1);
+    sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
+                  (int)in.total_k, seq, k0, k1);
+    const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int wrow = tile * BQ + 16 * NQ * wave;
+    const float sc = in.scale * LOG2E;
+
+    const E* kp = (const E*)in.k + (int64_t)k0 * in.k_token_stride + h * in.k_head_stride;
+    const E* vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
+    const E* pp = DR ? (const E*)in.k_pe + (int64_t)k0 * in.k_pe_token_stride : nullptr;
+
+    v8 q[NQ][KS], go[NQ][VS];
+    float lse2[NQ], dl[NQ];
+    int last[NQ];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = wrow + 16 * j + col, rr = min(r, nq - 1);
+        const E* row = (const E*)in.q + (int64_t)(q0 + rr) * in.q_token_stride + h * in.q_head_stride;
+        const int64_t at = (int64_t)(q0 + rr) * in.H + h;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(row, ks, lane);
+        float sum = 0.f;
+#pragma unroll
+        for (int vs = 0; vs < VS; ++vs) {
+            go[j][vs] = row_frag_global(d_o + at * DV, vs, lane);
+            const v8 ov = row_frag_global(o + at * DV, vs, lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += to_f32(go[j][vs][i]) * to_f32(ov[i]);
+        }
+        dl[j] = group_sum(sum);
+        lse2[j] = lse[at] * LOG2E;
+        last[j] = in.causal ? min(nk - 1, r + off) : nk - 1;
+        if (r < nq && g == 0) delta[at] = dl[j];
+    }
+    const int end = in.causal ? min(nk, min(nq, (tile + 1) * BQ) + off) : nk;
+    const int nt = end > 0 ? (end + BN - 1) / BN : 0;
+    const int wave_end = in.causal ? min(nk, min(nq, wrow + 16 * NQ) + off) : nk;
+    const int wave_full = in.causal ? min(nk, wrow + off + 1) : nk;
+
+    Stage<E, DQK, BN, 256> sk;
+    Stage<E, DV, BN, 256> sv;
+    auto load = [&](int t) {
+        sk.load(tid, [&](int r, int c) -> const E* {
+            const int key = t * BN + r;
+            if (key >= nk) return nullptr;
+            if (DR && c * CE >= DN) return pp + (int64_t)key * in.k_pe_token_stride + (c * CE - DN);
+            return kp + (int64_t)key * in.k_token_stride + c * CE;
+        });
+        sv.load(tid, [&](int r, int c) -> const E* {
+            const int key = t * BN + r;
+            return key < nk ? vp + (int64_t)key * in.v_token_stride + c * CE : nullptr;
+        });
+    };
+
+    f32x4 acc[NQ][DQK / 16];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int c = 0; c < DQK / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (nt > 0) {
+        load(0);
+        sk.store(tid, smem[0]);
+        sv.store(tid, smem[0] + BN * DQK);
+    }
+    __syncthreads();
+    for (int t = 0; t < nt; ++t) {
+        const E* K = smem[t & 1];
+        const E* V = K + BN * DQK;
+        if (t + 1 < nt) load(t + 1);
+        if (t * BN < wave_end) {
+            f32x4 s[NQ][TT], dp[NQ][TT];
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) s[j][tt] = dp[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const v8 a = row_frag<DQK>(K, 16 * tt, ks, lane);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) s[j][tt] = mma32(a, q[j][ks], s[j][tt]);
+                }
+#pragma unroll
+                for (int vs = 0; vs < VS; ++vs) {
+                    const v8 a = row_frag<DV>(V, 16 * tt, vs, lane);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) dp[j][tt] = mma32(a, go[j][vs], dp[j][tt]);
+                }
+            }
+            const bool masked = (t + 1) * BN > wave_full;
+            v8 dz[NQ];
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -lse2[j]));
+                        const float x = w * (dp[j][tt][i] - dl[j]);
+                        s[j][tt][i] = masked && t * BN + 16 * tt + 4 * g + i > last[j] ? 0.f : x;
+                    }
+                dz[j] = acc_frag(s[j][0], s[j][1], E());
+            }
+#pragma unroll
+            for (int c = 0; c < DQK / 16; ++c) {
+                const v8 a = col_frag<DQK>(K, 0, 16, 16 * c, lane);
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(a, dz[j], acc[j][c]);
+            }
+        }
+        if (t + 1 < nt) {
+            E* next = smem[(t + 1) & 1];
+            sk.store(tid, next);
+            sv.store(tid, next + BN * DQK);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = wrow + 16 * j + col;
+        if (r >= nq) continue;
+        E* row = dq + ((int64_t)(q0 + r) * in.H + h) * DQK;
+#pragma unroll
+        for (int c = 0; c < DQK / 16; ++c) {
+            typename Vec<E>::v4 x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(acc[j][c][i] * in.scale);
+            store_vec(row + 16 * c + 4 * g, x);
+        }
+    }
+}
+
+// dk, dv and the head's part of dk_pe.  A wave owns 16 keys, whose k and v
+// operands and gradients stay in registers; the query rows come 32 at a time.
+// The scores are formed with rows = queries, so that the weights and dz are the
+// operands of dv^T += g^T w and dk^T += q^T dz as they stand.
+template <typename E, int DN, int DR>
+__global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
+    const kda_latent_inputs in, const float* __restrict__ lse, const E* __restrict__ d_o,
+    const float* __restrict__ delta, E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
+    E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ pe_part, int tiles)
+{
+    constexpr int DQK = DN + DR, DV = DN, BQ = 32;
+    constexpr int KS = DQK / 32, VS = DV / 32, CE = CHUNK_ELEMS<E>;
+    typedef typename Vec<E>::v8 v8;
+    __shared__ __attribute__((aligned(16))) E smem[2][BQ * (DQK + DV)];
+    __shared__ __attribute__((aligned(16))) float srow[2][2 * BQ];   // lse (base 2), then delta
+
+    int h, want, seq, tile;
+    head_tile_of_block(in.H, tiles, h, want);
+    const int32_t* cu_k = in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
+    const int rows_k = (int)(in.total_k / in.num_seqs);
+    if (!find_tile<LATENT_BK, 256>(cu_k, in.num_seqs, rows_k, (int)in.total_k, want,
+                                   reinterpret_cast<int*>(&smem[0][0]), seq, tile))
+        return;
+    int q0, q1, k0, k1;
+    sequence_rows(in.cu_seqlens_q, (int)(in.total_q / in.num_seqs), (int)in.total_q, seq, q0, q1);
+    sequence_rows(cu_k, rows_k, (int)in.total_k, seq, k0, k1);
+    const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int key0 = tile * LATENT_BK, wkey = key0 + 16 * wave, key = wkey + col;
+    const float sc = in.scale * LOG2E;
+
+    v8 k[KS], v[VS];
+    {
+        const int64_t row = k0 + min(key, nk - 1);
+        const E* kp = (const E*)in.k + row * in.k_token_stride + h * in.k_head_stride;
+        const E* vp = (const E*)in.v + row * in.v_token_stride + h * in.v_head_stride;
+        const E* pp = DR ? (const E*)in.k_pe + row * in.k_pe_token_stride : nullptr;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            k[ks] = 32 * ks < DN ? row_frag_global(kp, ks, lane) : row_frag_global(pp, ks - DN / 32, lane);
+#pragma unroll
+        for (int vs = 0; vs < VS; ++vs) v[vs] = row_frag_global(vp, vs, lane);
+    }
+    const int nt = (nq + BQ - 1) / BQ;
+    const int t0 = in.causal ? min(nt, max(0, key0 - off) / BQ) : 0;   // rows before it see none of the keys
+
+    const E* qp = (const E*)in.q + (int64_t)q0 * in.q_token_stride + h * in.q_head_stride;
+    const E* gp = d_o + ((int64_t)q0 * in.H + h) * DV;
+    Stage<E, DQK, BQ, 256> sq;
+    Stage<E, DV, BQ, 256> sg;
+    float srow_next = 0.f;
+    auto load = [&](int t) {
+        sq.load(tid, [&](int r, int c) -> const E* {
+            const int i = t * BQ + r;
+            return i < nq ? qp + (int64_t)i * in.q_token_stride + c * CE : nullptr;
+        });
+        sg.load(tid, [&](int r, int c) -> const E* {
+            const int i = t * BQ + r;
+            return i < nq ? gp + (int64_t)i * in.H * DV + c * CE : nullptr;
+        });
+        if (tid < 2 * BQ) {   // rows behind the last weigh nothing: lse = inf
+            const int i = t * BQ + (tid & (BQ - 1));
+            const int64_t at = (int64_t)(q0 + min(i, nq - 1)) * in.H + h;
+            if (tid < BQ) srow_next = i < nq ? lse[at] * LOG2E : __builtin_inff();
+            else srow_next = i < nq ? delta[at] : 0.f;
+        }
+    };
+    auto store = [&](int b) {
+        sq.store(tid, smem[b]);
+        sg.store(tid, smem[b] + BQ * DQK);
+        if (tid < 2 * BQ) srow[b][tid] = srow_next;
+    };
+
+    f32x4 ak[DQK / 16], av[DV / 16];
+#pragma unroll
+    for (int c = 0; c < DQK / 16; ++c) ak[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < DV / 16; ++c) av[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (t0 < nt) {
+        load(t0);
+        store(t0 & 1);
+    }
+    __syncthreads();
+    for (int t = t0; t < nt; ++t) {
+        const E* Q = smem[t & 1];
+        const E* G = Q + BQ * DQK;
+        const float* R = srow[t & 1];
+        if (t + 1 < nt) load(t + 1);
+        if (!in.causal || t * BQ + BQ - 1 + off >= wkey) {
+            f32x4 w[2], dz[2];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) s = mma32(row_frag<DQK>(Q, 16 * a, ks, lane), k[ks], s);
+#pragma unroll
+                for (int vs = 0; vs < VS; ++vs) dp = mma32(row_frag<DV>(G, 16 * a, vs, lane), v[vs], dp);
+                const f32x4 ls = *reinterpret_cast<const f32x4*>(R + 16 * a + 4 * g);
+                const f32x4 de = *reinterpret_cast<const f32x4*>(R + BQ + 16 * a + 4 * g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool hidden = in.causal && key > t * BQ + 16 * a + 4 * g + i + off;
+                    w[a][i] = hidden ? 0.f : exp2_fast(__builtin_fmaf(s[i], sc, -ls[i]));
+                    dz[a][i] = hidden ? 0.f : w[a][i] * (dp[i] - de[i]);
+                }
+            }
+            const v8 wf = acc_frag(w[0], w[1], E()), zf = acc_frag(dz[0], dz[1], E());
+#pragma unroll
+            for (int c = 0; c < DV / 16; ++c) av[c] = mma32(col_frag<DV>(G, 0, 16, 16 * c, lane), wf, av[c]);
+#pragma unroll
+            for (int c = 0; c < DQK / 16; ++c) ak[c] = mma32(col_frag<DQK>(Q, 0, 16, 16 * c, lane), zf, ak[c]);
+        }
+        if (t + 1 < nt) store((t + 1) & 1);
+        __syncthreads();
+    }
+    if (key >= nk) return;
+    const int64_t row = k0 + key;
+    E* kr = dk + row * dk_token_stride + h * dk_head_stride;
+    E* vr = dv + row * dv_token_stride + h * dv_head_stride;
+#pragma unroll
+    for (int c = 0; c < DN / 16; ++c) {
+        typename Vec<E>::v4 x, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = from_f32<E>(ak[c][i] * in.scale);
+            y[i] = from_f32<E>(av[c][i]);
+        }
+        store_vec(kr + 16 * c + 4 * g, x);
+        store_vec(vr + 16 * c + 4 * g, y);
+    }
+    if constexpr (DR > 0) {
+        float* pr = pe_part + (row * in.H + h) * DR;
+#pragma unroll
+        for (int c = 0; c < DR / 16; ++c) store_vec(pr + 16 * c + 4 * g, ak[DN / 16 + c] * in.scale);
+    }
+}
+
+// dk_pe = sum over the heads in order, fp32, rounded once.  A thread per 4
+// channels of a key; rows behind the last sequence are left alone.
+template <typename E, int DR>
+__global__ __launch_bounds__(256) void latent_dkpe_kernel(const float* __restrict__ part, E* __restrict__ dk_pe,
+                                                          const int32_t* __restrict__ cu, int N, int total, int H)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = id / (DR / 4);
+    const int c = 4 * (int)(id % (DR / 4));
+    const int first = cu ? clamp_offset(cu[0], total) : 0, last = cu ? clamp_offset(cu[N], total) : total;
+    if (row < first || row >= last) return;
+    const float* p = part + row * H * DR + c;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int h = 0; h < H; ++h) sum += *reinterpret_cast<const f32x4*>(p + (int64_t)h * DR);
+    typename Vec<E>::v4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(sum[i]);
+    store_vec(dk_pe + row * DR + c, x);
+}
+
+static int64_t tile_count(const int32_t* cu, int64_t total, int32_t N, int B) {
+    return cu ? total / B + N : (total / N + B - 1) / B * N;
+}
+
+template <typename E, int DN, int DR>
+static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipStream_t stream) {
+    const int64_t tq = tile_count(in.cu_seqlens_q, in.total_q, in.num_seqs, 64 * DQ_NQ<E>);
+    const int32_t* cu_k = in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
+    const int64_t tk = tile_count(cu_k, in.total_k, in.num_seqs, LATENT_BK);
+    if (tq > 0)
+        hipLaunchKernelGGL((latent_dq_kernel<E, DN, DR>), dim3((unsigned)(tq * in.H)), dim3(256), 0, stream, in,
+                           (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.delta, (int)tq);
+    if (tk > 0)
+        hipLaunchKernelGGL((latent_dkv_kernel<E, DN, DR>), dim3((unsigned)(tk * in.H)), dim3(256), 0, stream, in, a.lse,
+                           (const E*)a.d_o, a.delta, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv,
+                           a.dv_token_stride, a.dv_head_stride, a.pe_part, (int)tk);
+    if constexpr (DR > 0)
+        if (in.total_k > 0)
+            hipLaunchKernelGGL((latent_dkpe_kernel<E, DR>), dim3((unsigned)((in.total_k * (DR / 4) + 255) / 256)),
+                               dim3(256), 0, stream, a.pe_part, (E*)a.dk_pe, cu_k, in.num_seqs, (int)in.total_k, in.H);
+    return hipGetLastError();
+}
+
+hipError_t launch_latent_attention_backward(const kda_latent_inputs& in, const LatentGrads& a, hipStream_t stream) {
+    if (in.dtype == KDA_DTYPE_BF16) {
+        if (in.dn == 128) return in.dr ? launch<bf16, 128, 64>(in, a, stream) : launch<bf16, 128, 0>(in, a, stream);
+        return in.dr ? launch<bf16, 64, 64>(in, a, stream) : launch<bf16, 64, 0>(in, a, stream);
+    }
+    if (in.dn == 128) return in.dr ? launch<float, 128, 64>(in, a, stream) : launch<float, 128, 0>(in, a, stream);
+    return in.dr ? launch<float, 64, 64>(in, a, stream) : launch<float, 64, 0>(in, a, stream);
+}
+
+}  // namespace kda

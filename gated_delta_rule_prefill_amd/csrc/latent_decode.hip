@@ -1,0 +1,501 @@
+// latent_decode.hip -- absorbed latent attention over a paged cache.
+//
+// Every head reads the same cached row [c_j, k_pe_j]; a (token, head) pair is
+// one query row:
+//   z_rj = scale (q_r . [c_j, k_pe_j]),  o_r = sum_j softmax(z_r)_j c_j
+// so a sequence's n new tokens with H heads are n H rows against one matrix of
+// keys whose first dl columns are also the values.  A cached row is fetched
+// once per 16 RT query rows; with 32 rows and 576 channels that is 60 flop per
+// byte and the cache's bytes bound the kernel, with 64 rows and more the
+// matrix products do.
+//
+// A workgroup of 8 waves takes 16 RT query rows of one sequence and walks key
+// tiles of BN rows through LDS.  The scores of a tile are formed transposed
+// (rows = keys) and split over the waves by keys and row tiles; each wave puts
+// its rows' maxima and then its weights into LDS, and the product with the
+// values is split over the waves by value columns, so a tile's elements are
+// read from LDS once for each product and the output (16 RT x dl, fp32) is
+// spread over the waves' registers.
+//
+// The work of a batch (row tiles x key tiles of every sequence, in order) is
+// cut into equal runs, one for each of 256 workgroups, whatever the lengths:
+// a run may end inside a row tile, whose partial results a second kernel
+// joins.  The cut depends on the lengths only, so results are reproducible.
+#include "latent_common.h"
+
+namespace kda {
+
+constexpr int DEC_GRID = 256;    // one workgroup per CU (its LDS tiles take the CU)
+constexpr int DEC_WAVES = 8;
+
+template <typename E> constexpr int DEC_BN = 128 / (int)sizeof(E);   // keys per tile
+
+// A row tile whose keys several workgroups share: its output rows and the
+// workgroups [first, last] that hold its partial results.
+struct DecodeSplit {
+    int64_t row;       // first output row (token * H + head)
+    int32_t rows;      // 0: nothing to join
+    int32_t first, last, pad;
+};
+
+// Workspace: splits, then the partials' (m, l) pairs, then their outputs; a
+// workgroup has two slots of partials: 2b for a row tile begun by an earlier
+// workgroup, 2b + 1 for one that a later workgroup goes on with.
+struct DecodeSpace {
+    DecodeSplit* split;   // [DEC_GRID]
+    float* ml;            // [2 DEC_GRID][rows][2]
+    float* o;             // [2 DEC_GRID][rows][dl]
+};
+static size_t space_bytes(int rows, int dl) {
+    return sizeof(DecodeSplit) * DEC_GRID + (size_t)2 * DEC_GRID * rows * (2 + dl) * 4;
+}
+static DecodeSpace space_of(void* ws, int rows) {
+    DecodeSpace s;
+    s.split = reinterpret_cast<DecodeSplit*>(ws);
+    s.ml = reinterpret_cast<float*>(s.split + DEC_GRID);
+    s.o = s.ml + (size_t)2 * DEC_GRID * rows * 2;
+    return s;
+}
+
+// Work of sequence s: row tiles x key tiles (a sequence without keys counts
+// one, so that its output rows are written).
+template <int BM, int BN>
+__device__ __forceinline__ void sequence_work(const LatentDecode& a, int rows_q, int s, int& q0, int& n, int& len,
+                                              int& row_tiles, int& key_tiles) {
+    int q1;
+    sequence_rows(a.cu_seqlens, rows_q, (int)a.total_tokens, s, q0, q1);
+    n = q1 - q0;
+    const int64_t room = (int64_t)a.max_pages * a.page_size;
+    len = max(0, (int)min((int64_t)a.seq_lens[s], room));
+    row_tiles = (int)(((int64_t)n * a.H + BM - 1) / BM);
+    key_tiles = max(1, (len + BN - 1) / BN);
+}
+
+// by_tile: split entries are indexed by row tile (their number is at most
+// DEC_GRID), otherwise by the workgroup that begins the row tile.
+template <typename E, int DL, int DR, int RT>
+__global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const LatentDecode a, DecodeSpace ws,
+                                                                       int by_tile, int entries)
+{
+    constexpr int W = DL + DR, BN = DEC_BN<E>, BM = 16 * RT, NT = 64 * DEC_WAVES;
+    constexpr int TT = BN / 16, KS = W / 32, CE = CHUNK_ELEMS<E>;
+    constexpr int RQ = RT * TT > DEC_WAVES ? RT * TT / DEC_WAVES : 1;   // row tiles of a wave's scores
+    constexpr int CT = DL / 16 / DEC_WAVES;                             // 16-column value tiles of a wave
+    constexpr int PS = BN + 16 / (int)sizeof(E);                        // row stride of the weights
+    typedef typename Vec<E>::v8 v8;
+    typedef typename Vec<E>::v4 v4;
+    __shared__ __attribute__((aligned(16))) E tilebuf[2][BN * W];
+    __shared__ __attribute__((aligned(16))) E sp[BM * PS];
+    __shared__ __attribute__((aligned(16))) float stat[TT][BM];
+    __shared__ __attribute__((aligned(16))) int ridx[3][BN];            // cache rows of the tiles' keys, -1: none
+    __shared__ int64_t found[4];
+    __shared__ int64_t wsum[DEC_WAVES][2];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int rows_q = (int)(a.total_tokens / a.num_seqs);
+    const float sc = a.scale * LOG2E;
+
+    // this workgroup's run of the batch's work: the sum over the sequences,
+    // then the sequence its run begins in
+    int64_t total = 0, units = 0;
+    for (int s = tid; s < a.num_seqs; s += NT) {
+        int q0, n, len, rt, kt;
+        sequence_work<BM, BN>(a, rows_q, s, q0, n, len, rt, kt);
+        total += (int64_t)rt * kt;
+        units += rt;
+    }
+    const int64_t mine = total, my_units = units;
+    int64_t incl = total, uincl = units;   // inclusive over the lanes; NT sequences or fewer: the prefix itself
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t up = __shfl_up(incl, d), uup = __shfl_up(uincl, d);
+        if (lane >= d) incl += up, uincl += uup;
+    }
+    if (lane == 63) wsum[wave][0] = incl, wsum[wave][1] = uincl;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    int64_t base = 0, ubase = 0;
+    total = units = 0;
+#pragma unroll
+    for (int w = 0; w < DEC_WAVES; ++w) {
+        if (w < wave) base += wsum[w][0], ubase += wsum[w][1];
+        total += wsum[w][0], units += wsum[w][1];
+    }
+    const int64_t per = (total + DEC_GRID - 1) / DEC_GRID;
+    const int64_t begin = per * blockIdx.x, stop = min(total, begin + per);
+    if (!by_tile) {
+        if (tid == 0) ws.split[blockIdx.x].rows = 0;
+    } else if (blockIdx.x == 0) {
+        for (int64_t i = units + tid; i < entries; i += NT) ws.split[i].rows = 0;
+    }
+    if (begin >= stop) return;
+    if (a.num_seqs <= NT) {
+        const int64_t excl = base + incl - mine;
+        if (begin >= excl && begin < excl + mine) found[0] = tid, found[1] = excl, found[2] = ubase + uincl - my_units;
+        __syncthreads();
+    } else {
+        int64_t before = 0, ubefore = 0;
+        for (int s0 = 0; s0 < a.num_seqs; s0 += NT) {
+            const int s = s0 + tid;
+            int64_t x = 0, u = 0;
+            if (s < a.num_seqs) {
+                int q0, n, len, rt, kt;
+                sequence_work<BM, BN>(a, rows_q, s, q0, n, len, rt, kt);
+                x = (int64_t)rt * kt;
+                u = rt;
+            }
+            int64_t xi = x, ui = u;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int64_t up = __shfl_up(xi, d), uup = __shfl_up(ui, d);
+                if (lane >= d) xi += up, ui += uup;
+            }
+            __syncthreads();
+            if (lane == 63) wsum[wave][0] = xi, wsum[wave][1] = ui;
+            __syncthreads();
+            int64_t b = before, ub = ubefore;
+#pragma unroll
+            for (int w = 0; w < DEC_WAVES; ++w) {
+                if (w < wave) b += wsum[w][0], ub += wsum[w][1];
+                before += wsum[w][0], ubefore += wsum[w][1];
+            }
+            const int64_t excl = b + xi - x;
+            if (begin >= excl && begin < excl + x) found[0] = s, found[1] = excl, found[2] = ub + ui - u;
+            __syncthreads();
+            if (found[0] >= 0) break;
+        }
+    }
+    int seq = (int)found[0];
+    int64_t seq_base = found[1], unit_base = found[2];
+
+    const int tw = wave % TT, rg = wave / TT;      // key tile and row group of this wave's scores
+    const bool scores = rg * RQ < RT;
+    const E* cache = (const E*)a.cache;
+    Stage<E, W, BN, NT> st;
+
+    for (int64_t pos = begin; pos < stop;) {
+        int q0, n, len, row_tiles, key_tiles;
+        sequence_work<BM, BN>(a, rows_q, seq, q0, n, len, row_tiles, key_tiles);
+        if (pos >= seq_base + (int64_t)row_tiles * key_tiles) {   // behind this sequence (or it has no rows)
+            seq_base += (int64_t)row_tiles * key_tiles;
+            unit_base += row_tiles;
+            ++seq;
+            continue;
+        }
+        const int unit = (int)((pos - seq_base) / key_tiles), t0 = (int)((pos - seq_base) - (int64_t)unit * key_tiles);
+        const int t1 = (int)min((int64_t)key_tiles, t0 + (stop - pos));
+        const int64_t rows_all = (int64_t)n * a.H;
+        const int64_t row0 = (int64_t)unit * BM;                     // first query row within the sequence
+        const int nrows = (int)min((int64_t)BM, rows_all - row0);
+        // keys that the tile's last row sees; key tiles behind them weigh nothing
+        const int end = max(0, min(len, len - n + (int)((row0 + nrows - 1) / a.H) + 1));
+        const int te = min(t1, (end + BN - 1) / BN);
+        const int32_t* table = a.block_table + (int64_t)seq * a.max_pages;
+
+        auto cache_row = [&](int t) -> int {                         // of key t * BN + tid, tid < BN
+            const int j = t * BN + tid;
+            if (t >= te || j >= len) return -1;
+            const int pg = (int)((unsigned)j / (unsigned)a.page_size);
+            const int page = table[pg];
+            return page < 0 || page >= a.num_pages ? -1 : page * a.page_size + (j - pg * a.page_size);
+        };
+        auto load = [&](const int* rows) {
+            st.load(tid, [&](int r, int c) -> const E* {
+                const int row = rows[r];
+                return row < 0 ? nullptr : cache + (int64_t)row * W + c * CE;
+            });
+        };
+        if (tid < BN) {
+            ridx[0][tid] = cache_row(t0);
+            ridx[1][tid] = cache_row(t0 + 1);
+        }
+        v8 q[RQ][KS];
+        int last[RQ];                                                // last key this lane's row sees
+#pragma unroll
+        for (int r = 0; r < RQ; ++r) {
+            const int64_t row = row0 + min(nrows - 1, 16 * (rg * RQ + r) + col);
+            const int i = (int)(row / a.H), h = (int)(row - (int64_t)i * a.H);
+            const E* qp = (const E*)a.q + (int64_t)(q0 + i) * a.q_token_stride + h * a.q_head_stride;
+            last[r] = len - n + i;
+            if (scores)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) q[r][ks] = row_frag_global(qp, ks, lane);
+        }
+        f32x4 acc[RT][CT];
+        float m[RT], l[RQ];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            m[r] = neg_inf();
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int r = 0; r < RQ; ++r) l[r] = 0.f;
+        __syncthreads();
+        int next_row = -1;
+        if (t0 < te) {
+            load(ridx[0]);
+            st.store(tid, tilebuf[0]);
+            load(ridx[1]);
+            if (tid < BN) next_row = cache_row(t0 + 2);
+        }
+        __syncthreads();
+        for (int t = t0, k = 0, k3 = 0; t < te; ++t, ++k, k3 = k3 == 2 ? 0 : k3 + 1) {
+            const E* tile = tilebuf[k & 1];
+            const int* rows = ridx[k3];
+            const int n3 = k3 == 0 ? 2 : k3 - 1;                     // (k + 2) mod 3
+            f32x4 s[RQ];
+            if (scores) {
+#pragma unroll
+                for (int r = 0; r < RQ; ++r) s[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const v8 x = row_frag<W>(tile, 16 * tw, ks, lane);
+#pragma unroll
+                    for (int r = 0; r < RQ; ++r) s[r] = mma32(x, q[r][ks], s[r]);
+                }
+                int there[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) there[i] = rows[16 * tw + 4 * g + i];
+#pragma unroll
+                for (int r = 0; r < RQ; ++r) {
+                    float top = neg_inf();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = t * BN + 16 * tw + 4 * g + i;
+                        if (there[i] < 0 || j > last[r]) s[r][i] = neg_inf();
+                        top = fmaxf(top, s[r][i]);
+                    }
+                    top = group_max(top) * sc;
+                    if (g == 0) stat[tw][16 * (rg * RQ + r) + col] = top;
+                }
+            }
+            __syncthreads();   // maxima written; the other buffer's last readers are done
+            if (tid < BN) ridx[n3][tid] = next_row;
+            if (t + 1 < te) st.store(tid, tilebuf[(k + 1) & 1]);
+            // the running maximum, raised only when it grew by more than 8 (in
+            // powers of two); every wave takes the same decision for a row
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                float top = stat[0][16 * r + col];
+#pragma unroll
+                for (int w = 1; w < TT; ++w) top = fmaxf(top, stat[w][16 * r + col]);
+                const bool grew = top > m[r] + 8.f;
+                if (__any(grew)) {
+                    const float mn = grew ? top : m[r];
+                    const float f = grew ? exp2_fast(m[r] - mn) : 1.f;
+                    m[r] = mn;
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[r][c] *= f;
+#pragma unroll
+                    for (int x = 0; x < RQ; ++x)
+                        if (rg * RQ + x == r) l[x] *= f;
+                }
+            }
+            if (scores) {
+#pragma unroll
+                for (int r = 0; r < RQ; ++r) {
+                    float mr = m[r];
+#pragma unroll
+                    for (int x = 1; x < RT; ++x) mr = rg * RQ + r == x ? m[x] : mr;
+                    if (rg * RQ + r == 0) mr = m[0];
+                    const float from = mr == neg_inf() ? 0.f : mr;
+                    v4 p;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = exp2_fast(__builtin_fmaf(s[r][i], sc, -from));
+                        l[r] += w;                 // the sum takes the weights before their rounding
+                        p[i] = from_f32<E>(w);     // bf16: the product's operand type
+                    }
+                    store_vec(sp + (16 * (rg * RQ + r) + col) * PS + 16 * tw + 4 * g, p);
+                }
+            }
+            __syncthreads();   // weights, the next tile and the rows of the one after it are there
+            if (t + 2 < te) {
+                load(ridx[n3]);
+                if (tid < BN) next_row = cache_row(t + 3);
+            }
+#pragma unroll
+            for (int b = 0; b < TT / 2; ++b) {
+                v8 p[RT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const E* x = sp + (16 * r + col) * PS + 32 * b + 4 * g;
+                    const v4 lo = load_vec<v4>(x), hi = load_vec<v4>(x + 16);
+                    p[r] = v8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                }
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    const v8 x = col_frag<W>(tile, 32 * b, 32 * b + 16, 16 * (wave * CT + c), lane);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) acc[r][c] = mma32(x, p[r], acc[r][c]);
+                }
+            }
+        }
+        // the rows' sums over the waves
+        __syncthreads();
+        if (scores)
+#pragma unroll
+            for (int r = 0; r < RQ; ++r) {
+                const float x = group_sum(l[r]);
+                if (g == 0) stat[tw][16 * (rg * RQ + r) + col] = x;
+            }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == key_tiles;
+        const int64_t out0 = (int64_t)q0 * a.H + row0;
+        const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            float sum = stat[0][16 * r + col];
+#pragma unroll
+            for (int w = 1; w < TT; ++w) sum += stat[w][16 * r + col];
+            const int row = 16 * r + col;
+            if (row >= nrows) continue;
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                E* op = (E*)a.o + (out0 + row) * DL + 16 * wave * CT + 4 * g;
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    v4 x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(acc[r][c][i] * inv);
+                    store_vec(op + 16 * c, x);
+                }
+                if (a.lse && wave == 0 && g == 0)
+                    a.lse[out0 + row] = sum == 0.f ? neg_inf() : (m[r] + __log2f(sum)) * LN2;
+            } else {
+                float* op = ws.o + ((int64_t)slot * BM + row) * DL + 16 * wave * CT + 4 * g;
+#pragma unroll
+                for (int c = 0; c < CT; ++c) store_vec(op + 16 * c, acc[r][c]);
+                if (wave == 0 && g == 0) {
+                    float* ml = ws.ml + ((int64_t)slot * BM + row) * 2;
+                    ml[0] = m[r];
+                    ml[1] = sum;
+                }
+            }
+        }
+        if (tid == 0) {   // the workgroup that begins a row tile says who holds its parts
+            if (t0 == 0) {
+                const int64_t first_work = seq_base + (int64_t)unit * key_tiles;
+                DecodeSplit x;
+                x.row = out0;
+                x.rows = whole ? 0 : nrows;
+                x.first = (int)blockIdx.x;
+                x.last = (int)((first_work + key_tiles - 1) / per);
+                x.pad = 0;
+                if (by_tile) {
+                    if (unit_base + unit < entries) ws.split[unit_base + unit] = x;
+                } else if (!whole) ws.split[blockIdx.x] = x;
+            }
+        }
+        __syncthreads();   // statistics and tiles are free for the next piece
+        pos += t1 - t0;
+    }
+}
+
+// Joins the partial results of split row tiles: with M = max_p m_p,
+//   o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+// A workgroup per (split, group of rows); SP waves share a row's parts (in a
+// fixed order), the others take further rows.
+template <typename E, int DL, int SP>
+__global__ __launch_bounds__(256) void latent_join_kernel(const DecodeSpace ws, E* __restrict__ o,
+                                                          float* __restrict__ lse, int BM)
+{
+    constexpr int ROWS = 4 / SP, EPL = DL / 64;   // rows of a workgroup, columns of a lane
+    __shared__ float so[4][DL];
+    const DecodeSplit x = ws.split[blockIdx.x];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = blockIdx.y * ROWS + wave / SP, part = wave % SP;
+    const bool live = row < x.rows;
+    if (blockIdx.y * ROWS >= x.rows) return;      // uniform over the workgroup
+    const int parts = x.last - x.first + 1;
+    auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * x.first + 1 : 2 * (x.first + p)) * BM + min(row, x.rows - 1); };
+    float top = neg_inf();
+    for (int p = lane; p < parts; p += 64) top = fmaxf(top, ws.ml[slot(p) * 2]);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float from = top == neg_inf() ? 0.f : top;
+    float sum = 0.f;
+    for (int p = lane; p < parts; p += 64) {
+        const float* ml = ws.ml + slot(p) * 2;
+        sum += exp2_fast(ml[0] - from) * ml[1];
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    f32x4 acc[EPL / 4];
+#pragma unroll
+    for (int e = 0; e < EPL / 4; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = part; p < parts; p += SP) {
+        const float f = exp2_fast(ws.ml[slot(p) * 2] - from);
+        const float* src = ws.o + slot(p) * DL + 4 * lane;
+#pragma unroll
+        for (int e = 0; e < EPL / 4; ++e) acc[e] += f * *reinterpret_cast<const f32x4*>(src + 256 * e);
+    }
+    if (SP > 1) {
+#pragma unroll
+        for (int e = 0; e < EPL / 4; ++e) store_vec(&so[wave][256 * e + 4 * lane], acc[e]);
+        __syncthreads();
+        if (part != 0) return;
+#pragma unroll
+        for (int w = 1; w < SP; ++w)
+#pragma unroll
+            for (int e = 0; e < EPL / 4; ++e) acc[e] += *reinterpret_cast<const f32x4*>(&so[wave + w][256 * e + 4 * lane]);
+    }
+    if (!live) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < EPL / 4; ++e) {
+        typename Vec<E>::v4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = from_f32<E>(acc[e][i] * inv);
+        store_vec(o + (x.row + row) * DL + 256 * e + 4 * lane, y);
+    }
+    if (lse && lane == 0) lse[x.row + row] = sum == 0.f ? neg_inf() : (top + __log2f(sum)) * LN2;
+}
+
+// Row tiles of 32 rows where a sequence's rows fit in one (a tile of 64 would
+// be half empty), else of 64 (each cached row is then fetched half as often).
+static int row_tile(int64_t total_tokens, int32_t N, int32_t H) {
+    return (total_tokens + N - 1) / N * H <= 32 ? 2 : 4;
+}
+
+size_t latent_decode_workspace(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t dl, bool) {
+    return space_bytes(16 * row_tile(total_tokens, num_seqs, H), dl);
+}
+
+template <typename E, int DL, int DR, int RT>
+static hipError_t launch(const LatentDecode& a, hipStream_t stream) {
+    constexpr int BM = 16 * RT;
+    const DecodeSpace ws = space_of(a.workspace, BM);
+    const int64_t rows = a.total_tokens * a.H;
+    const int64_t bound = a.cu_seqlens ? rows / BM + a.num_seqs
+                                       : (a.total_tokens / a.num_seqs * a.H + BM - 1) / BM * a.num_seqs;
+    const bool by_tile = bound <= DEC_GRID;
+    const int entries = by_tile ? (int)bound : DEC_GRID;
+    hipLaunchKernelGGL((latent_decode_kernel<E, DL, DR, RT>), dim3(DEC_GRID), dim3(64 * DEC_WAVES), 0, stream, a, ws,
+                       by_tile ? 1 : 0, entries);
+    // few row tiles: their parts are many, and four waves share each row's
+    if (entries * BM <= 1024)
+        hipLaunchKernelGGL((latent_join_kernel<E, DL, 4>), dim3(entries, BM), dim3(256), 0, stream, ws, (E*)a.o, a.lse, BM);
+    else
+        hipLaunchKernelGGL((latent_join_kernel<E, DL, 1>), dim3(entries, BM / 4), dim3(256), 0, stream, ws, (E*)a.o, a.lse, BM);
+    return hipGetLastError();
+}
+
+template <typename E, int DL, int DR>
+static hipError_t launch_rows(const LatentDecode& a, hipStream_t stream) {
+    return row_tile(a.total_tokens, a.num_seqs, a.H) == 2 ? launch<E, DL, DR, 2>(a, stream)
+                                                          : launch<E, DL, DR, 4>(a, stream);
+}
+
+hipError_t launch_latent_decode(const LatentDecode& a, bool bf16_io, hipStream_t stream) {
+    if (bf16_io) {
+        if (a.dl == 512) return a.dr ? launch_rows<bf16, 512, 64>(a, stream) : launch_rows<bf16, 512, 0>(a, stream);
+        return a.dr ? launch_rows<bf16, 256, 64>(a, stream) : launch_rows<bf16, 256, 0>(a, stream);
+    }
+    if (a.dl == 512) return a.dr ? launch_rows<float, 512, 64>(a, stream) : launch_rows<float, 512, 0>(a, stream);
+    return a.dr ? launch_rows<float, 256, 64>(a, stream) : launch_rows<float, 256, 0>(a, stream);
+}
+
+}  // namespace kda

@@ -17,10 +17,24 @@ LIB_PATH = os.path.join(HERE, "libkda.so")
 KDA_OK, KDA_ERR_INVALID_ARGUMENT, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE, KDA_ERR_HIP = range(5)
 KDA_DTYPE_F32, KDA_DTYPE_BF16 = 0, 1
 KDA_FLAG_L2NORM_QK, KDA_FLAG_BETA_SIGMOID = 1, 2
+KDA_ROTARY_INTERLEAVED, KDA_ROTARY_INVERSE = 1, 2
 CHUNK = 64  # tokens per chunk of the chunkwise prefill (rows of chunk_states)
 
 # name -> (restype, argtypes) for every entry point of include/kda.h
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_f32, _f64, _u32 = ctypes.c_float, ctypes.c_double, ctypes.c_uint32
+
+
+class LatentInputs(ctypes.Structure):
+    """kda_latent_inputs of include/kda.h."""
+    _fields_ = ([(n, _vp) for n in ("q", "k", "v", "k_pe")] +
+                [(n, _i64) for n in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+                                     "v_token_stride", "v_head_stride", "k_pe_token_stride")] +
+                [("cu_seqlens_q", _vp), ("cu_seqlens_k", _vp), ("total_q", _i64), ("total_k", _i64)] +
+                [(n, _i32) for n in ("num_seqs", "H", "dn", "dr", "dv", "dtype", "causal")] +
+                [("scale", _f32)])
+
+
 SIGNATURES = {
     "kda_prefill_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32, ctypes.c_int]),
     "kda_prefill": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32,
@@ -39,6 +53,20 @@ SIGNATURES = {
     "kda_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32,
                                     _i32, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                     _vp, _vp, _sz, _vp]),
+    "kda_latent_attention": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+    "kda_latent_attention_backward_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32]),
+    "kda_latent_attention_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _i64,
+                                                     _i64, _vp, _vp, _sz, _vp]),
+    "kda_latent_decode_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32, ctypes.c_int]),
+    "kda_latent_decode": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _i32,
+                                         _i32, _i32, _i32, ctypes.c_int, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "kda_latent_append": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _i32, _i32, _i32,
+                                         ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _f32, _vp, _f32, _u32, _vp,
+                                         _vp, _vp]),
+    "kda_rotary": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _i32,
+                                  ctypes.c_int, _f32, _u32, _vp]),
+    "kda_rotary_frequencies": (ctypes.c_int, [_i32, _f64, _f64, _i64, ctypes.POINTER(_f32),
+                                              ctypes.POINTER(_f32)]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_last_error_message": (ctypes.c_char_p, []),
     "kda_version": (_i32, []),
@@ -332,3 +360,310 @@ def prefill_kernel_times():
     if n < 0:
         raise RuntimeError("no timed prefill recorded")
     return [(names[i].decode(), float(ms[i])) for i in range(n)]
+
+
+# -- latent attention ------------------------------------------------------------
+
+class _on:
+    """The device and stream a call runs on: the call's own stream argument or
+    the device's current one.  Outputs and workspaces the binding allocates
+    belong to that stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.ctx = None
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index is not None and device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _raw_stream(device) -> int:
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _rows3(t, name, shape, dtype, device) -> None:
+    """A [rows, heads, channels] tensor whose last axis is dense."""
+    _require(tuple(t.shape) == shape, f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    _require(t.dtype == dtype and t.device == device, f"{name}: expected {dtype} on {device}")
+    _require(t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0, f"{name}: the last axis must be dense")
+
+
+def _stride(t, axis: int) -> int:
+    """Elements from one index of an axis to the next (0 for an axis of one)."""
+    return t.stride(axis) if t.shape[axis] > 1 else 0
+
+
+def _dense(t, name, shape, dtype, device) -> None:
+    _require(tuple(t.shape) == shape and t.dtype == dtype and t.device == device and t.is_contiguous(),
+             f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {device}")
+
+
+def _offsets(cu, name, device) -> int:
+    import torch
+    _require(cu.dtype == torch.int32 and cu.dim() == 1 and cu.shape[0] >= 2 and cu.device == device and
+             cu.is_contiguous(), f"{name}: contiguous int32 [N+1] on {device}")
+    return cu.shape[0] - 1
+
+
+def _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale):
+    import torch
+    _require(q.dim() == 3 and k.dim() == 3 and v.dim() == 3, "q, k, v: [tokens, heads, channels]")
+    T, H, dqk = q.shape
+    Tk, _, dn = k.shape
+    dev = q.device
+    dr = dqk - dn
+    _require(dr >= 0, "q must have at least k's channels")
+    _rows3(q, "q", (T, H, dqk), q.dtype, dev)
+    _rows3(k, "k", (Tk, H, dn), q.dtype, dev)
+    _rows3(v, "v", (Tk, H, v.shape[2]), q.dtype, dev)
+    pes = 0
+    if dr:
+        _require(k_pe is not None, f"q has {dr} channels beyond k's: k_pe is needed")
+        _rows3(k_pe, "k_pe", (Tk, dr), q.dtype, dev)
+        pes = _stride(k_pe, 0)
+    else:
+        _require(k_pe is None, "k_pe: q has no channels for it")
+    if cu_seqlens is not None:
+        N = _offsets(cu_seqlens, "cu_seqlens", dev)
+        if cu_seqlens_k is not None:
+            _require(_offsets(cu_seqlens_k, "cu_seqlens_k", dev) == N, "cu_seqlens_k: as many sequences as cu_seqlens")
+    else:
+        _require(cu_seqlens_k is None, "cu_seqlens_k needs cu_seqlens")
+        N = int(num_seqs or 1)
+    if scale is None:
+        scale = dqk ** -0.5
+    return LatentInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_pe), _stride(q, 0), _stride(q, 1),
+                        _stride(k, 0), _stride(k, 1), _stride(v, 0), _stride(v, 1), pes, _ptr(cu_seqlens),
+                        _ptr(cu_seqlens_k), T, Tk, N, H, dn, dr, v.shape[2], _dtype_code(q), 1 if causal else 0,
+                        scale)
+
+
+def latent_attention(q, k, v, k_pe=None, cu_seqlens=None, cu_seqlens_k=None, num_seqs: Optional[int] = None,
+                     causal: bool = True, scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """Expanded latent attention over packed sequences (``kda_latent_attention``).
+
+    q: [T, H, dn + dr]; k: [Tk, H, dn]; v: [Tk, H, dn] (bf16 or fp32; strided
+    views, e.g. the halves of one expansion product); k_pe: [Tk, dr], the rotary
+    key part shared by the heads, or None with dr = 0.  cu_seqlens (and
+    cu_seqlens_k where the keys are more than the queries): int32 [N+1], or
+    ``num_seqs`` equal rows.  scale: default (dn + dr)^-0.5.
+    Returns (o [T, H, dn], lse [T, H] fp32).  Rows behind the last sequence are
+    left as they were."""
+    import torch
+    a = _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale)
+    dev = q.device
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((a.total_q, a.H, a.dv), dtype=q.dtype, device=dev)
+        else:
+            _dense(out, "out", (a.total_q, a.H, a.dv), q.dtype, dev)
+        if lse is None:
+            lse = torch.empty((a.total_q, a.H), dtype=torch.float32, device=dev)
+        else:
+            _dense(lse, "lse", (a.total_q, a.H), torch.float32, dev)
+        st = lib().kda_latent_attention(ctypes.addressof(a), out.data_ptr(), lse.data_ptr(), _raw_stream(dev))
+    _check(st, "kda_latent_attention")
+    return out, lse
+
+
+def latent_attention_backward(q, k, v, o, lse, d_o, k_pe=None, cu_seqlens=None, cu_seqlens_k=None,
+                              num_seqs: Optional[int] = None, causal: bool = True, scale: Optional[float] = None,
+                              dk=None, dv=None, workspace=None, stream=None) -> dict:
+    """Gradients of ``latent_attention`` (``kda_latent_attention_backward``) for
+    dL/do = d_o, from the forward's o and lse: returns dq [T, H, dn + dr], dk and
+    dv [Tk, H, dn] and dk_pe [Tk, dr] or None, in the inputs' type.  dk, dv:
+    tensors to write (strided, e.g. the halves of one [Tk, H, 2 dn] gradient),
+    or None to allocate both halves of one such tensor."""
+    import torch
+    a = _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale)
+    dev = q.device
+    _dense(o, "o", (a.total_q, a.H, a.dv), q.dtype, dev)
+    _dense(d_o, "d_o", (a.total_q, a.H, a.dv), q.dtype, dev)
+    _dense(lse, "lse", (a.total_q, a.H), torch.float32, dev)
+    with _on(dev, stream):
+        if dk is None and dv is None:
+            dkv = torch.empty((a.total_k, a.H, a.dn + a.dv), dtype=q.dtype, device=dev)
+            dk, dv = dkv[..., :a.dn], dkv[..., a.dn:]
+        else:
+            _require(dk is not None and dv is not None, "dk and dv: both or neither")
+            _rows3(dk, "dk", (a.total_k, a.H, a.dn), q.dtype, dev)
+            _rows3(dv, "dv", (a.total_k, a.H, a.dv), q.dtype, dev)
+        dq = torch.empty((a.total_q, a.H, a.dn + a.dr), dtype=q.dtype, device=dev)
+        dk_pe = torch.empty((a.total_k, a.dr), dtype=q.dtype, device=dev) if a.dr else None
+        need = int(lib().kda_latent_attention_backward_workspace_bytes(a.total_q, a.total_k, a.H, a.dr))
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
+        st = lib().kda_latent_attention_backward(
+            ctypes.addressof(a), o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+            _stride(dk, 0), _stride(dk, 1), dv.data_ptr(), _stride(dv, 0), _stride(dv, 1), _ptr(dk_pe),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev))
+    _check(st, "kda_latent_attention_backward")
+    return dict(dq=dq, dk=dk, dv=dv, dk_pe=dk_pe)
+
+
+def _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs, T):
+    """Sequences of a paged call, with its shared arguments checked."""
+    import torch
+    dev = cache.device
+    _require(cache.dim() == 3 and cache.is_contiguous(), "cache: contiguous [pages, page_size, channels]")
+    N = _offsets(cu_seqlens, "cu_seqlens", dev) if cu_seqlens is not None else \
+        int(num_seqs) if num_seqs is not None else seq_lens.shape[0]
+    _require(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == N and
+             block_table.device == dev and block_table.is_contiguous(), "block_table: contiguous int32 [N, max_pages]")
+    _require(seq_lens.dtype == torch.int32 and tuple(seq_lens.shape) == (N,) and seq_lens.device == dev and
+             seq_lens.is_contiguous(), "seq_lens: contiguous int32 [N]")
+    return N
+
+
+def latent_decode_workspace_bytes(total_tokens: int, num_seqs: int, H: int, dl: int, dr: int, bf16: bool) -> int:
+    return int(lib().kda_latent_decode_workspace_bytes(int(total_tokens), int(num_seqs), int(H), int(dl), int(dr),
+                                                       KDA_DTYPE_BF16 if bf16 else KDA_DTYPE_F32))
+
+
+def latent_decode(q, cache, block_table, seq_lens, latent_dim: int, scale: float, cu_seqlens=None,
+                  num_seqs: Optional[int] = None, out=None, lse=None, workspace=None, stream=None):
+    """Absorbed latent attention over a paged cache (``kda_latent_decode``).
+
+    q: [T, H, dl + dr], the queries multiplied into the latent space and their
+    rotated part (strided); cache: [pages, page_size, dl + dr], rows as
+    ``latent_append`` writes them; block_table: int32 [N, max_pages]; seq_lens:
+    int32 [N] cached tokens, the new ones included; cu_seqlens: int32 [N+1]
+    offsets of the new tokens, or None for T / N each.  latent_dim = dl; scale:
+    of the heads before absorption, e.g. (dn + dr)^-0.5.
+    Returns (o [T, H, dl], lse [T, H] fp32)."""
+    import torch
+    _require(q.dim() == 3, "q: [T, H, dl + dr]")
+    T, H, width = q.shape
+    N = _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs, T)
+    dev = cache.device
+    _rows3(q, "q", (T, H, cache.shape[2]), cache.dtype, dev)
+    dl = int(latent_dim)
+    dr = width - dl
+    code = _dtype_code(q)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, H, dl), dtype=q.dtype, device=dev)
+        else:
+            _dense(out, "out", (T, H, dl), q.dtype, dev)
+        if lse is None:
+            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        else:
+            _dense(lse, "lse", (T, H), torch.float32, dev)
+        if workspace is None:
+            workspace = torch.empty(int(lib().kda_latent_decode_workspace_bytes(T, N, H, dl, dr, code)),
+                                    dtype=torch.uint8, device=dev)
+        else:
+            _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
+        st = lib().kda_latent_decode(
+            q.data_ptr(), _stride(q, 0), _stride(q, 1), cache.data_ptr(), cache.shape[0], cache.shape[1],
+            block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), _ptr(cu_seqlens), T, N, H, dl, dr,
+            code, scale, out.data_ptr(), lse.data_ptr(), _ptr(workspace) or None,
+            workspace.numel() * workspace.element_size(), _raw_stream(dev))
+    _check(st, "kda_latent_decode")
+    return out, lse
+
+
+def latent_append(cache, c, block_table, seq_lens, k_pe=None, cu_seqlens=None, num_seqs: Optional[int] = None,
+                  norm_weight=None, eps: float = 1e-6, inv_freq=None, interleaved: bool = False,
+                  mscale: float = 1.0, c_out=None, k_pe_out=None, stream=None):
+    """Write the new tokens' rows of a paged latent cache (``kda_latent_append``).
+
+    cache, block_table, seq_lens, cu_seqlens: as for ``latent_decode`` (seq_lens
+    counts the new tokens).  c: [T, dl] latents and k_pe: [T, dr] rotary key
+    parts (strided rows, e.g. parts of one down projection; k_pe None with
+    dr = 0).  norm_weight: fp32 [dl] of the RMS norm, or None for no norm;
+    inv_freq: fp32 [dr / 2], or None for no rotation; mscale multiplies the
+    rotated part.  c_out, k_pe_out: True (allocate) or a dense tensor for the
+    normalised latents and rotated key parts.  Returns (c_out, k_pe_out)."""
+    import torch
+    _require(c.dim() == 2, "c: [T, dl]")
+    T, dl = c.shape
+    N = _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs, T)
+    dev = cache.device
+    dr = cache.shape[2] - dl
+    _rows3(c, "c", (T, dl), cache.dtype, dev)
+    if dr:
+        _require(k_pe is not None, f"the cache has {dr} channels beyond c's: k_pe is needed")
+        _rows3(k_pe, "k_pe", (T, dr), cache.dtype, dev)
+    else:
+        _require(k_pe is None, "k_pe: the cache has no channels for it")
+    if norm_weight is not None:
+        _dense(norm_weight, "norm_weight", (dl,), torch.float32, dev)
+    if inv_freq is not None:
+        _dense(inv_freq, "inv_freq", (dr // 2,), torch.float32, dev)
+    code = _dtype_code(cache)
+    with _on(dev, stream):
+        if c_out is True:
+            c_out = torch.empty((T, dl), dtype=c.dtype, device=dev)
+        elif c_out is not None and c_out is not False:
+            _dense(c_out, "c_out", (T, dl), c.dtype, dev)
+        else:
+            c_out = None
+        if k_pe_out is True:
+            k_pe_out = torch.empty((T, dr), dtype=c.dtype, device=dev)
+        elif k_pe_out is not None and k_pe_out is not False:
+            _dense(k_pe_out, "k_pe_out", (T, dr), c.dtype, dev)
+        else:
+            k_pe_out = None
+        st = lib().kda_latent_append(
+            cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1],
+            seq_lens.data_ptr(), _ptr(cu_seqlens), T, N, dl, dr, code, c.data_ptr(), _stride(c, 0), _ptr(k_pe),
+            _stride(k_pe, 0) if dr else 0, _ptr(norm_weight), eps, _ptr(inv_freq), mscale,
+            KDA_ROTARY_INTERLEAVED if interleaved else 0, _ptr(c_out), _ptr(k_pe_out), _raw_stream(dev))
+    _check(st, "kda_latent_append")
+    return c_out, k_pe_out
+
+
+def rotary(x, positions, inv_freq, start: int = 0, interleaved: bool = False, mscale: float = 1.0,
+           inverse: bool = False, out=None, stream=None):
+    """Rotary positions on channels [start, start + 2 len(inv_freq)) of every
+    head (``kda_rotary``).  x: [T, H, d] (last axis dense, otherwise strided);
+    positions: int32 [T]; inv_freq: fp32 [dr / 2]; inverse: the gradient of the
+    rotation.  out: None (allocate), x itself (in place), or a [T, H, d] tensor
+    that does not overlap x.  Returns the rotated tensor."""
+    import torch
+    _require(x.dim() == 3, "x: [T, H, d]")
+    T, H, d = x.shape
+    dev = x.device
+    _rows3(x, "x", (T, H, d), x.dtype, dev)
+    _dense(positions, "positions", (T,), torch.int32, dev)
+    _require(inv_freq.dim() == 1, "inv_freq: fp32 [dr / 2]")
+    _dense(inv_freq, "inv_freq", tuple(inv_freq.shape), torch.float32, dev)
+    code = _dtype_code(x)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, H, d), dtype=x.dtype, device=dev)
+        else:
+            _rows3(out, "out", (T, H, d), x.dtype, dev)
+        st = lib().kda_rotary(x.data_ptr(), _stride(x, 0), _stride(x, 1), out.data_ptr(), _stride(out, 0), _stride(out, 1),
+                              positions.data_ptr(), inv_freq.data_ptr(), T, H, d, int(start),
+                              2 * inv_freq.shape[0], code, mscale,
+                              (KDA_ROTARY_INTERLEAVED if interleaved else 0) | (KDA_ROTARY_INVERSE if inverse else 0),
+                              _raw_stream(dev))
+    _check(st, "kda_rotary")
+    return out
+
+
+def rotary_frequencies(dr: int, base: float = 10000.0, factor: float = 1.0, original_context: int = 0,
+                       device=None):
+    """(inv_freq fp32 [dr / 2], amplitude) for ``rotary`` and ``latent_append``
+    (``kda_rotary_frequencies``): plain frequencies, or a context stretched by
+    ``factor`` -- linearly, or by parts with ``original_context``."""
+    import torch
+    f = (_f32 * max(1, dr // 2))()
+    a = _f32()
+    _check(lib().kda_rotary_frequencies(dr, base, factor, original_context, f, ctypes.byref(a)),
+           "kda_rotary_frequencies")
+    return torch.tensor(list(f), dtype=torch.float32, device=device), float(a.value)

@@ -267,6 +267,222 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
                         float *d_initial_state, void *workspace, size_t workspace_bytes,
                         void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Latent attention: the full-attention layer that a hybrid model puts between
+ * its KDA layers.  A token leaves one latent vector c (dl channels, RMS
+ * normalised) and one rotary key part (dr channels) shared by all heads.  Its
+ * per-head keys [c Wk_h, k_pe] and values c Wv_h are expanded from the latent
+ * by a matrix product of the caller's (kda_latent_attention and its
+ * gradients), or Wk_h and Wv_h are multiplied into the query and the output,
+ * so that every head reads the one latent row (kda_latent_decode, over the
+ * paged cache that kda_latent_append writes).  The conventions at the top of
+ * this file hold, with these differences:
+ *   Strides    where a tensor takes strides they count elements; the last axis
+ *              is dense, and strides and pointers are multiples of 16 bytes.
+ *   Offsets    cu_seqlens may end before the last row (c_N <= T): the rows
+ *              behind the last sequence are neither read nor written.  Offsets
+ *              outside [0, T] are clamped to it.
+ *   Empty rows a query row that sees no key gets o = 0, lse = -inf and zero
+ *              gradients.
+ *   Values     NaN and Inf propagate from the keys a row sees.  Rows behind a
+ *              sequence's end and unused cache rows may hold anything.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Inputs of the expanded form (all device memory):
+ *   q      [total_q, H, dn + dr]: the dn channels that meet k, then the dr
+ *          channels that meet k_pe (already rotated, see kda_rotary)
+ *   k, v   [total_k, H, dn], [total_k, H, dv]: strided, so that both may be
+ *          halves of one [total_k, H, dn + dv] product
+ *   k_pe   [total_k, dr], shared by the heads; NULL with dr = 0
+ *   cu_seqlens_q, cu_seqlens_k   [num_seqs + 1] int32 offsets of each
+ *          sequence's queries and keys; cu_seqlens_k NULL = the queries'
+ *          offsets (then total_k = total_q); both NULL = num_seqs equal rows
+ *   causal nonzero: query i of a sequence with n queries and m keys sees the
+ *          keys j <= i + (m - n), i.e. the last query sees all of them; with
+ *          m < n the first n - m queries see none
+ *   scale  finite and > 0, multiplies q . k
+ * dn = dv in {64, 128}; dr in {0, 64}.
+ */
+typedef struct {
+    const void *q;
+    const void *k;
+    const void *v;
+    const void *k_pe;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t k_pe_token_stride;
+    const int32_t *cu_seqlens_q;
+    const int32_t *cu_seqlens_k;
+    int64_t total_q, total_k;
+    int32_t num_seqs, H, dn, dr, dv;
+    int32_t dtype;               /* kda_dtype */
+    int32_t causal;
+    float scale;
+} kda_latent_inputs;
+
+/*
+ * Expanded latent attention over packed sequences, one pass over the keys with
+ * the running maximum and sum of the softmax:
+ *
+ *     z_ij = scale (q_i . [k_j, k_pe_j]),   o_i = sum_j softmax(z_i)_j v_j,
+ *     lse_i = log sum_j exp(z_ij)           over the keys j that i sees
+ *
+ *   o    [total_q, H, dv] dtype (written; must not alias an input)
+ *   lse  [total_q, H] fp32 (written), or NULL; the backward pass needs it
+ */
+kda_status kda_latent_attention(const kda_latent_inputs *in, void *o, float *lse, void *stream);
+
+/* Device workspace kda_latent_attention_backward needs (bytes, 256-aligned; 0 for invalid sizes). */
+size_t kda_latent_attention_backward_workspace_bytes(int64_t total_q, int64_t total_k, int32_t H,
+                                                     int32_t dr);
+
+/*
+ * Gradients of kda_latent_attention for dL/do = d_o, from the forward's o and
+ * lse.  Deterministic; the gradient of the shared k_pe is summed over the heads
+ * in order, in fp32.
+ *   o, d_o   [total_q, H, dv] dtype; lse [total_q, H] fp32   (read)
+ *   dq       [total_q, H, dn + dr] dtype, dense (written)
+ *   dk, dv   strided like k and v, dtype (written): both may be halves of one
+ *            [total_k, H, dn + dv] gradient
+ *   dk_pe    [total_k, dr] dtype, dense (written; NULL with dr = 0)
+ *   workspace at least kda_latent_attention_backward_workspace_bytes(), or
+ *            NULL with 0 (then allocated stream-ordered on `stream`)
+ * Keys of a sequence without queries get zero gradients.  Outputs must not
+ * alias inputs.
+ */
+kda_status kda_latent_attention_backward(const kda_latent_inputs *in, const void *o,
+                                         const float *lse, const void *d_o, void *dq, void *dk,
+                                         int64_t dk_token_stride, int64_t dk_head_stride, void *dv,
+                                         int64_t dv_token_stride, int64_t dv_head_stride,
+                                         void *dk_pe, void *workspace, size_t workspace_bytes,
+                                         void *stream);
+
+/*
+ * Device workspace kda_latent_decode needs (bytes, 256-aligned; 0 for invalid
+ * sizes): the partial results of rows whose keys are split over workgroups.
+ */
+size_t kda_latent_decode_workspace_bytes(int64_t total_tokens, int32_t num_seqs, int32_t H,
+                                         int32_t dl, int32_t dr, kda_dtype dtype);
+
+/*
+ * Absorbed latent attention of one or more new tokens per sequence over a
+ * paged cache of latents (single-token decode, speculative tokens, a chunk of
+ * a prompt over its cached prefix).  All heads read the same cached row:
+ *
+ *     z_ij = scale (q_i . [c_j, k_pe_j]),   o_i = sum_j softmax(z_i)_j c_j
+ *
+ *   q            [T, H, dl + dr] dtype, strided: the query multiplied by Wk_h
+ *                (dl channels), then its rotated part (dr)
+ *   cache        [num_pages, page_size, dl + dr] dtype, dense: rows [c, k_pe]
+ *   block_table  [N, max_pages] int32: sequence s's token j is row
+ *                j % page_size of page block_table[s][j / page_size].  A page
+ *                outside [0, num_pages) is not read: its tokens count as
+ *                absent.  num_pages * page_size < 2^31.
+ *   seq_lens     [N] int32 cached tokens of every sequence, the new ones
+ *                included (they are appended first); clamped to
+ *                [0, max_pages * page_size]
+ *   cu_seqlens   [N+1] int32 offsets of the new tokens, or NULL = T / N each
+ *                (T % N must be 0).  New token i of n sees the tokens
+ *                j <= seq_len - n + i.
+ *   o            [T, H, dl] dtype (written); lse [T, H] fp32 (written), or NULL
+ *   workspace    at least kda_latent_decode_workspace_bytes(), or NULL with 0
+ *                (then allocated stream-ordered on `stream`).  Two calls that
+ *                may overlap need one each.
+ * dl in {256, 512}; dr in {0, 64}; H * (T / N) < 2^31.  The result is
+ * deterministic: how the keys are split depends on the sizes and lengths only.
+ */
+kda_status kda_latent_decode(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                             const void *cache, int32_t num_pages, int32_t page_size,
+                             const int32_t *block_table, int32_t max_pages,
+                             const int32_t *seq_lens, const int32_t *cu_seqlens,
+                             int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t dl,
+                             int32_t dr, kda_dtype dtype, float scale, void *o, float *lse,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary layouts: which channels of the rotated part form pair i of dr / 2.
+ * The default is the half layout (i, i + dr / 2).
+ *   KDA_ROTARY_INTERLEAVED  channels 2i and 2i + 1
+ *   KDA_ROTARY_INVERSE      rotate by minus the angle (the gradient of the
+ *                           rotation; kda_rotary only)
+ */
+enum { KDA_ROTARY_INTERLEAVED = 1u, KDA_ROTARY_INVERSE = 2u };
+
+/*
+ * Writes the new tokens' rows of the paged cache:
+ *
+ *     row = [ c / sqrt(mean(c^2) + eps) * norm_weight,  amplitude R(p f) k_pe ]
+ *
+ * Token i of the n new ones of sequence s sits at position p = seq_len - n + i,
+ * in the row that kda_latent_decode reads for it; a token whose position is
+ * negative or whose page is outside [0, num_pages) is not written to the cache.
+ *   cache, num_pages, page_size, block_table, max_pages, seq_lens, cu_seqlens,
+ *   total_tokens, num_seqs, dl, dr, dtype: as for kda_latent_decode (dl a
+ *                multiple of 64 up to 1024, dr an even number up to 256, a
+ *                multiple of 16 bytes)
+ *   c            [T, dl] dtype and k_pe [T, dr] dtype (read), rows
+ *                c_token_stride and k_pe_token_stride apart: both may be parts
+ *                of one [T, dl + dr] product.  k_pe NULL with dr = 0.
+ *   norm_weight  [dl] fp32, or NULL: c is written as it is
+ *   eps          >= 0, finite
+ *   inv_freq     [dr/2] fp32 radians per position, or NULL: k_pe is written as
+ *                it is (no positions)
+ *   amplitude    finite; multiplies the rotated part (long-context scaling)
+ *   flags        KDA_ROTARY_INTERLEAVED or 0
+ *   c_out        [T, dl] dtype, dense, or NULL: the normalised latents, for
+ *                their expansion (written for every token of a sequence,
+ *                whether or not it has a cache row)
+ *   k_pe_out     [T, dr] dtype, dense, or NULL: the rotated key parts, alike
+ */
+kda_status kda_latent_append(void *cache, int32_t num_pages, int32_t page_size,
+                             const int32_t *block_table, int32_t max_pages,
+                             const int32_t *seq_lens, const int32_t *cu_seqlens,
+                             int64_t total_tokens, int32_t num_seqs, int32_t dl, int32_t dr,
+                             kda_dtype dtype, const void *c, int64_t c_token_stride,
+                             const void *k_pe, int64_t k_pe_token_stride,
+                             const float *norm_weight, float eps, const float *inv_freq,
+                             float amplitude, uint32_t flags, void *c_out, void *k_pe_out,
+                             void *stream);
+
+/*
+ * Rotary positions on channels [start, start + dr) of every head:
+ * y = amplitude R(p f) x per pair, the other channels copied.  The angle
+ * p f is reduced in 64 bits, so far positions keep their accuracy.
+ *   x          [T, H, d] dtype, strided in tokens and heads (read)
+ *   y          [T, H, d] dtype, strided (written).  y = x with x's strides
+ *              rotates in place and leaves the other channels untouched; any
+ *              other overlap is not allowed.
+ *   positions  [T] int32
+ *   inv_freq   [dr/2] fp32 radians per position (see kda_rotary_frequencies)
+ *   flags      KDA_ROTARY_* bits
+ * dr even and >= 2, start >= 0, start + dr <= d <= 4096.  Pointers and strides
+ * need the alignment of one element only (wider accesses are used where they
+ * allow it).
+ */
+kda_status kda_rotary(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,
+                      int64_t y_token_stride, int64_t y_head_stride, const int32_t *positions,
+                      const float *inv_freq, int64_t total_tokens, int32_t H, int32_t d,
+                      int32_t start, int32_t dr, kda_dtype dtype, float amplitude, uint32_t flags,
+                      void *stream);
+
+/*
+ * Rotary frequencies, computed on the host into host memory inv_freq[dr/2]:
+ * f_i = base^(-2i/dr).  With factor > 1 the context is stretched by `factor`:
+ *   original_context = 0  every f_i / factor (linear interpolation)
+ *   original_context > 0  by parts: a pair that makes at least 32 full turns
+ *                         over the original context keeps f_i, one that makes
+ *                         at most one gets f_i / factor, with a linear ramp in
+ *                         the number of turns in between; the amplitude that
+ *                         goes with it is 0.1 ln(factor) + 1
+ * *amplitude (or NULL) receives the amplitude, 1 otherwise.
+ */
+kda_status kda_rotary_frequencies(int32_t dr, double base, double factor,
+                                  int64_t original_context, float *inv_freq, float *amplitude);
+
 /* Static description of a status code. */
 const char *kda_status_string(kda_status status);
 
