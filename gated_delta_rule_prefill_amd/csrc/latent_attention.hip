@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     const kda_latent_inputs in, E* __restrict__ o, float* __restrict__ lse, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BN = 128 / (int)sizeof(E), NQ = 2;
-    constexpr int KS = DQK / 32, TT = BN / 16, CE = CHUNK_ELEMS<E>;
+    constexpr int KS = DQK / 32, TT = BN / 16;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
 
@@ -61,20 +61,15 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     const int wave_end = in.causal ? min(nk, min(nq, wrow + 32) + off) : nk;           // of the wave
     const int wave_full = in.causal ? min(nk, wrow + off + 1) : nk;                    // keys all its rows see
 
-    Stage<E, DQK, BN, 256> sk;
+    Stage<E, DQK, BN, 256, DR> sk;
     Stage<E, DV, BN, 256> sv;
     auto load = [&](int t) {
-        sk.load(tid, [&](int r, int c) -> const E* {
-            const int key = t * BN + r;
-            if (key >= nk) return nullptr;
-            if (DR && c * CE >= DN) return pp + (int64_t)key * in.k_pe_token_stride + (c * CE - DN);
-            return kp + (int64_t)key * in.k_token_stride + c * CE;
-        });
-        sv.load(tid, [&](int r, int c) -> const E* {
-            const int key = t * BN + r;
-            return key < nk ? vp + (int64_t)key * in.v_token_stride + c * CE : nullptr;
-        });
+        sk.load(tid, [&](int r) { return t * BN + r < nk ? kp + (int64_t)(t * BN + r) * in.k_token_stride : nullptr; },
+                [&](int r) { return pp + (int64_t)(t * BN + r) * in.k_pe_token_stride; });
+        sv.load(tid, [&](int r) { return t * BN + r < nk ? vp + (int64_t)(t * BN + r) * in.v_token_stride : nullptr; });
     };
+    const RowReader<E, DQK> k_rows(lane);
+    const ColReader<E, DV, DV / 16> v_cols(lane);
 
     f32x4 acc[NQ][DV / 16];
     float m[NQ], l[NQ];
@@ -103,7 +98,7 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
                 for (int j = 0; j < NQ; ++j) s[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    const v8 a = row_frag<DQK>(K, 16 * tt, ks, lane);
+                    const v8 a = k_rows(K, 16 * tt, ks);
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) s[j][tt] = mma32(a, q[j][ks], s[j][tt]);
                 }
@@ -161,7 +156,7 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
             for (int c = 0; c < DV / 16; ++c)
 #pragma unroll
                 for (int b = 0; b < TT / 2; ++b) {
-                    const v8 a = col_frag<DV>(V, 32 * b, 32 * b + 16, 16 * c, lane);
+                    const v8 a = v_cols(V, 32 * b, 32 * b + 16, c);
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(a, p[j][b], acc[j][c]);
                 }

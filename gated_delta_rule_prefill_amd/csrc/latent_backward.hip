@@ -27,7 +27,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ delta, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BN = 32, NQ = DQ_NQ<E>, BQ = 64 * NQ;
-    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, CE = CHUNK_ELEMS<E>;
+    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
 
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const E* pp = DR ? (const E*)in.k_pe + (int64_t)k0 * in.k_pe_token_stride : nullptr;
 
     v8 q[NQ][KS], go[NQ][VS];
-    float lse2[NQ], dl[NQ];
+    float lse2[NQ], dl[NQ], exact[NQ];   // delta from the rounded o, and from this kernel's own weights
     int last[NQ];
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
@@ -71,27 +71,23 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         dl[j] = group_sum(sum);
         lse2[j] = lse[at] * LOG2E;
         last[j] = in.causal ? min(nk - 1, r + off) : nk - 1;
-        if (r < nq && g == 0) delta[at] = dl[j];
+        exact[j] = 0.f;
     }
     const int end = in.causal ? min(nk, min(nq, (tile + 1) * BQ) + off) : nk;
     const int nt = end > 0 ? (end + BN - 1) / BN : 0;
     const int wave_end = in.causal ? min(nk, min(nq, wrow + 16 * NQ) + off) : nk;
     const int wave_full = in.causal ? min(nk, wrow + off + 1) : nk;
 
-    Stage<E, DQK, BN, 256> sk;
+    Stage<E, DQK, BN, 256, DR> sk;
     Stage<E, DV, BN, 256> sv;
     auto load = [&](int t) {
-        sk.load(tid, [&](int r, int c) -> const E* {
-            const int key = t * BN + r;
-            if (key >= nk) return nullptr;
-            if (DR && c * CE >= DN) return pp + (int64_t)key * in.k_pe_token_stride + (c * CE - DN);
-            return kp + (int64_t)key * in.k_token_stride + c * CE;
-        });
-        sv.load(tid, [&](int r, int c) -> const E* {
-            const int key = t * BN + r;
-            return key < nk ? vp + (int64_t)key * in.v_token_stride + c * CE : nullptr;
-        });
+        sk.load(tid, [&](int r) { return t * BN + r < nk ? kp + (int64_t)(t * BN + r) * in.k_token_stride : nullptr; },
+                [&](int r) { return pp + (int64_t)(t * BN + r) * in.k_pe_token_stride; });
+        sv.load(tid, [&](int r) { return t * BN + r < nk ? vp + (int64_t)(t * BN + r) * in.v_token_stride : nullptr; });
     };
+    const RowReader<E, DQK> k_rows(lane);
+    const RowReader<E, DV> v_rows(lane);
+    const ColReader<E, DQK, DQK / 16> k_cols(lane);
 
     f32x4 acc[NQ][DQK / 16];
 #pragma unroll
@@ -116,13 +112,13 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                 for (int j = 0; j < NQ; ++j) s[j][tt] = dp[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    const v8 a = row_frag<DQK>(K, 16 * tt, ks, lane);
+                    const v8 a = k_rows(K, 16 * tt, ks);
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) s[j][tt] = mma32(a, q[j][ks], s[j][tt]);
                 }
 #pragma unroll
                 for (int vs = 0; vs < VS; ++vs) {
-                    const v8 a = row_frag<DV>(V, 16 * tt, vs, lane);
+                    const v8 a = v_rows(V, 16 * tt, vs);
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) dp[j][tt] = mma32(a, go[j][vs], dp[j][tt]);
                 }
@@ -136,14 +132,15 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float w = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -lse2[j]));
-                        const float x = w * (dp[j][tt][i] - dl[j]);
-                        s[j][tt][i] = masked && t * BN + 16 * tt + 4 * g + i > last[j] ? 0.f : x;
+                        const bool hidden = masked && t * BN + 16 * tt + 4 * g + i > last[j];
+                        exact[j] += hidden ? 0.f : w * dp[j][tt][i];
+                        s[j][tt][i] = hidden ? 0.f : w * (dp[j][tt][i] - dl[j]);
                     }
                 dz[j] = acc_frag(s[j][0], s[j][1], E());
             }
 #pragma unroll
             for (int c = 0; c < DQK / 16; ++c) {
-                const v8 a = col_frag<DQK>(K, 0, 16, 16 * c, lane);
+                const v8 a = k_cols(K, 0, 16, c);
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(a, dz[j], acc[j][c]);
             }
@@ -158,7 +155,9 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;
+        const float sum = group_sum(exact[j]);
         if (r >= nq) continue;
+        if (g == 0) delta[(int64_t)(q0 + r) * in.H + h] = sum;
         E* row = dq + ((int64_t)(q0 + r) * in.H + h) * DQK;
 #pragma unroll
         for (int c = 0; c < DQK / 16; ++c) {
@@ -181,7 +180,7 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
     E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ pe_part, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BQ = 32;
-    constexpr int KS = DQK / 32, VS = DV / 32, CE = CHUNK_ELEMS<E>;
+    constexpr int KS = DQK / 32, VS = DV / 32;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BQ * (DQK + DV)];
     __shared__ __attribute__((aligned(16))) float srow[2][2 * BQ];   // lse (base 2), then delta
@@ -222,14 +221,8 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
     Stage<E, DV, BQ, 256> sg;
     float srow_next = 0.f;
     auto load = [&](int t) {
-        sq.load(tid, [&](int r, int c) -> const E* {
-            const int i = t * BQ + r;
-            return i < nq ? qp + (int64_t)i * in.q_token_stride + c * CE : nullptr;
-        });
-        sg.load(tid, [&](int r, int c) -> const E* {
-            const int i = t * BQ + r;
-            return i < nq ? gp + (int64_t)i * in.H * DV + c * CE : nullptr;
-        });
+        sq.load(tid, [&](int r) { return t * BQ + r < nq ? qp + (int64_t)(t * BQ + r) * in.q_token_stride : nullptr; });
+        sg.load(tid, [&](int r) { return t * BQ + r < nq ? gp + (int64_t)(t * BQ + r) * in.H * DV : nullptr; });
         if (tid < 2 * BQ) {   // rows behind the last weigh nothing: lse = inf
             const int i = t * BQ + (tid & (BQ - 1));
             const int64_t at = (int64_t)(q0 + min(i, nq - 1)) * in.H + h;
@@ -243,6 +236,10 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
         if (tid < 2 * BQ) srow[b][tid] = srow_next;
     };
 
+    const RowReader<E, DQK> q_rows(lane);
+    const RowReader<E, DV> g_rows(lane);
+    const ColReader<E, DQK, DQK / 16> q_cols(lane);
+    const ColReader<E, DV, DV / 16> g_cols(lane);
     f32x4 ak[DQK / 16], av[DV / 16];
 #pragma unroll
     for (int c = 0; c < DQK / 16; ++c) ak[c] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -264,9 +261,9 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
             for (int a = 0; a < 2; ++a) {
                 f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) s = mma32(row_frag<DQK>(Q, 16 * a, ks, lane), k[ks], s);
+                for (int ks = 0; ks < KS; ++ks) s = mma32(q_rows(Q, 16 * a, ks), k[ks], s);
 #pragma unroll
-                for (int vs = 0; vs < VS; ++vs) dp = mma32(row_frag<DV>(G, 16 * a, vs, lane), v[vs], dp);
+                for (int vs = 0; vs < VS; ++vs) dp = mma32(g_rows(G, 16 * a, vs), v[vs], dp);
                 const f32x4 ls = *reinterpret_cast<const f32x4*>(R + 16 * a + 4 * g);
                 const f32x4 de = *reinterpret_cast<const f32x4*>(R + BQ + 16 * a + 4 * g);
 #pragma unroll
@@ -278,9 +275,9 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
             }
             const v8 wf = acc_frag(w[0], w[1], E()), zf = acc_frag(dz[0], dz[1], E());
 #pragma unroll
-            for (int c = 0; c < DV / 16; ++c) av[c] = mma32(col_frag<DV>(G, 0, 16, 16 * c, lane), wf, av[c]);
+            for (int c = 0; c < DV / 16; ++c) av[c] = mma32(g_cols(G, 0, 16, c), wf, av[c]);
 #pragma unroll
-            for (int c = 0; c < DQK / 16; ++c) ak[c] = mma32(col_frag<DQK>(Q, 0, 16, 16 * c, lane), zf, ak[c]);
+            for (int c = 0; c < DQK / 16; ++c) ak[c] = mma32(q_cols(Q, 0, 16, c), zf, ak[c]);
         }
         if (t + 1 < nt) store((t + 1) & 1);
         __syncthreads();

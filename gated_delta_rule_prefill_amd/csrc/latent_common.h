@@ -30,47 +30,74 @@ __device__ __forceinline__ int tile_at(int row, int chunk) {
     return row * W + ((chunk ^ swizzle(row)) * CHUNK_ELEMS<E>);
 }
 
-// Operand by rows: lane l supplies row row0 + (l & 15), slots 8g .. 8g + 7 of
-// the 32-wide block ks (g = l >> 4).
-template <int W>
-__device__ __forceinline__ bf16x8 row_frag(const bf16* t, int row0, int ks, int lane) {
-    return *reinterpret_cast<const bf16x8*>(t + tile_at<bf16, W>(row0 + (lane & 15), 4 * ks + (lane >> 4)));
-}
-template <int W>
-__device__ __forceinline__ f32x8 row_frag(const float* t, int row0, int ks, int lane) {
-    const int r = row0 + (lane & 15), c = 8 * ks + 2 * (lane >> 4);
-    const f32x4 a = *reinterpret_cast<const f32x4*>(t + tile_at<float, W>(r, c));
-    const f32x4 b = *reinterpret_cast<const f32x4*>(t + tile_at<float, W>(r, c + 1));
-    return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-}
-
-// Operand by columns: lane l supplies column c0 + (l & 15), slots 0..3 from
-// rows ra + 4g .. +3 and slots 4..7 from rows rb + 4g .. +3.  The rows 4g + i
-// of two 16-row blocks are what an accumulator tile leaves in lane group g, so
-// the other operand of the product stays in registers.  (bf16: the transposing
-// LDS read, a lane group's 16 lanes fetching 4 rows of 16 columns.)
-template <int W>
-__device__ __forceinline__ bf16x8 col_frag(const bf16* t, int ra, int rb, int c0, int lane) {
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const int r = 4 * (lane >> 4) + ((lane & 15) >> 2), c = c0 + 4 * (lane & 3);
-    const bf16* pa = t + tile_at<bf16, W>(ra + r, c >> 3) + (c & 4);
-    const bf16* pb = t + tile_at<bf16, W>(rb + r, c >> 3) + (c & 4);
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)pa);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)pb);
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
-    return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
-}
-template <int W>
-__device__ __forceinline__ f32x8 col_frag(const float* t, int ra, int rb, int c0, int lane) {
-    const int g4 = 4 * (lane >> 4), c = c0 + (lane & 15);
-    f32x8 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = t[tile_at<float, W>(ra + g4 + i, c >> 2) + (c & 3)];
-        v[4 + i] = t[tile_at<float, W>(rb + g4 + i, c >> 2) + (c & 3)];
+// Operands by rows of a tile: lane l supplies row row0 + (l & 15), slots
+// 8g .. 8g + 7 of the 32-wide block ks (g = l >> 4).  A lane's addresses are
+// two bases and constant offsets from them (the swizzle permutes chunks within
+// groups of 8 only); row0 is a multiple of 16.
+template <typename E, int W> struct RowReader;
+template <int W> struct RowReader<bf16, W> {
+    int at[2];
+    __device__ __forceinline__ explicit RowReader(int lane) {
+        const int r = lane & 15, g = lane >> 4;
+        at[0] = tile_at<bf16, W>(r, g);
+        at[1] = tile_at<bf16, W>(r, 4 + g);
     }
-    return v;
-}
+    __device__ __forceinline__ bf16x8 operator()(const bf16* t, int row0, int ks) const {
+        return *reinterpret_cast<const bf16x8*>(t + at[ks & 1] + (row0 * W + 64 * (ks >> 1)));
+    }
+};
+template <int W> struct RowReader<float, W> {
+    int at[2];
+    __device__ __forceinline__ explicit RowReader(int lane) {
+        const int r = lane & 15, g = lane >> 4;
+        at[0] = tile_at<float, W>(r, 2 * g);
+        at[1] = tile_at<float, W>(r, 2 * g + 1);
+    }
+    __device__ __forceinline__ f32x8 operator()(const float* t, int row0, int ks) const {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(t + at[0] + (row0 * W + 32 * ks));
+        const f32x4 b = *reinterpret_cast<const f32x4*>(t + at[1] + (row0 * W + 32 * ks));
+        return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+};
+
+// Operands by columns: lane l supplies column 16 (ct0 + ct) + (l & 15), slots
+// 0..3 from rows ra + 4g .. +3 and slots 4..7 from rows rb + 4g .. +3 (ra, rb
+// multiples of 16).  The rows 4g + i of two 16-row blocks are what an
+// accumulator tile leaves in lane group g, so the other operand of the product
+// stays in registers.  (bf16: the transposing LDS read, a lane group's 16 lanes
+// fetching 4 rows of 16 columns.)  CT column tiles, ct0 a multiple of min(CT, 4).
+template <typename E, int W, int CT> struct ColReader;
+template <int W, int CT> struct ColReader<bf16, W, CT> {
+    int at[CT < 4 ? CT : 4];
+    __device__ __forceinline__ explicit ColReader(int lane, int ct0 = 0) {
+        const int r = 4 * (lane >> 4) + ((lane & 15) >> 2), c = 4 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < (CT < 4 ? CT : 4); ++i)
+            at[i] = tile_at<bf16, W>(r, 2 * (ct0 + i) + (c >> 3)) + (c & 4);
+    }
+    __device__ __forceinline__ bf16x8 operator()(const bf16* t, int ra, int rb, int ct) const {
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const bf16* p = t + at[ct & 3] + 64 * (ct >> 2);
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + ra * W));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + rb * W));
+        return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+    }
+};
+template <int W, int CT> struct ColReader<float, W, CT> {
+    int lane, ct0;
+    __device__ __forceinline__ explicit ColReader(int lane, int ct0 = 0) : lane(lane), ct0(ct0) {}
+    __device__ __forceinline__ f32x8 operator()(const float* t, int ra, int rb, int ct) const {
+        const int g4 = 4 * (lane >> 4), c = 16 * (ct0 + ct) + (lane & 15);
+        f32x8 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = t[tile_at<float, W>(ra + g4 + i, c >> 2) + (c & 3)];
+            v[4 + i] = t[tile_at<float, W>(rb + g4 + i, c >> 2) + (c & 3)];
+        }
+        return v;
+    }
+};
 
 // Two accumulator tiles (rows 4g + i of two 16-row blocks) as the 8 slots of
 // an operand.  To bf16 each value is rounded to nearest: the products take
@@ -92,29 +119,40 @@ __device__ __forceinline__ f32x8 row_frag_global(const float* row, int ks, int l
 }
 
 // -- staging: global -> registers -> LDS ---------------------------------------
-// ROWS x W elements moved by NT threads; src(row, chunk) returns the chunk's
-// address, or NULL for zeros.  The loads are issued by load() and waited for
-// by store(), a tile of work later.
-template <typename E, int W, int ROWS, int NT>
+// ROWS x W elements moved by NT threads, 8 or more threads to a row (128-byte
+// lines), so that a thread's chunks lie at constant offsets from one address
+// per row it serves.  row(r) returns the row's address, or NULL for zeros; with W1 > 0 the
+// last W1 of the W channels come from row1(r).  The loads are issued by load()
+// and waited for by store(), a tile of work later.
+template <typename E, int W, int ROWS, int NT, int W1 = 0>
 struct Stage {
-    static constexpr int CPR = W / CHUNK_ELEMS<E>, N = ROWS * CPR / NT;
-    static_assert(ROWS * CPR % NT == 0 && CPR % 8 == 0, "whole chunks per thread, 8 per swizzle group");
-    u32x4 r[N];
-    template <typename F>
-    __device__ __forceinline__ void load(int tid, F src) {
+    static constexpr int CE = CHUNK_ELEMS<E>, TPR = ROWS * 8 >= NT ? 8 : NT / ROWS;   // threads per row
+    static constexpr int PASS = NT / TPR, P = ROWS / PASS, S = W / CE / TPR, S0 = (W - W1) / CE / TPR;
+    static_assert(ROWS % PASS == 0 && PASS % 8 == 0 && W % (TPR * CE) == 0 && W1 % (TPR * CE) == 0, "whole passes and steps");
+    u32x4 r[P][S];
+    template <typename F, typename G>
+    __device__ __forceinline__ void load(int tid, F row, G row1) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int id = tid + NT * k;
-            const E* p = src(id / CPR, id % CPR);
-            r[k] = p ? *reinterpret_cast<const u32x4*>(p) : u32x4{0, 0, 0, 0};
+        for (int p = 0; p < P; ++p) {
+            const E* a = row(tid / TPR + PASS * p);
+            const E* b = W1 ? row1(tid / TPR + PASS * p) : nullptr;
+#pragma unroll
+            for (int s = 0; s < S; ++s) r[p][s] = u32x4{0, 0, 0, 0};
+            if (a) {
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    r[p][s] = *reinterpret_cast<const u32x4*>((s < S0 ? a + TPR * CE * s : b + TPR * CE * (s - S0)) + CE * (tid % TPR));
+            }
         }
     }
+    template <typename F>
+    __device__ __forceinline__ void load(int tid, F row) { load(tid, row, row); }
     __device__ __forceinline__ void store(int tid, E* t) const {
+        E* at = t + tile_at<E, W>(tid / TPR, tid % TPR);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int id = tid + NT * k;
-            *reinterpret_cast<u32x4*>(t + tile_at<E, W>(id / CPR, id % CPR)) = r[k];
-        }
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int s = 0; s < S; ++s) *reinterpret_cast<u32x4*>(at + PASS * p * W + TPR * CE * s) = r[p][s];
     }
 };
 

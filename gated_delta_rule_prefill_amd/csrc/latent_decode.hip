@@ -78,15 +78,16 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
                                                                        int by_tile, int entries)
 {
     constexpr int W = DL + DR, BN = DEC_BN<E>, BM = 16 * RT, NT = 64 * DEC_WAVES;
-    constexpr int TT = BN / 16, KS = W / 32, CE = CHUNK_ELEMS<E>;
-    constexpr int RQ = RT * TT > DEC_WAVES ? RT * TT / DEC_WAVES : 1;   // row tiles of a wave's scores
+    constexpr int TT = BN / 16, KS = W / 32;
+    constexpr int TG = DEC_WAVES / RT < TT ? DEC_WAVES / RT : TT;       // a wave's scores: one row tile of RT,
+    constexpr int TW = TT / TG;                                         // TW key tiles (key group of TG)
     constexpr int CT = DL / 16 / DEC_WAVES;                             // 16-column value tiles of a wave
     constexpr int PS = BN + 16 / (int)sizeof(E);                        // row stride of the weights
     typedef typename Vec<E>::v8 v8;
     typedef typename Vec<E>::v4 v4;
     __shared__ __attribute__((aligned(16))) E tilebuf[2][BN * W];
     __shared__ __attribute__((aligned(16))) E sp[BM * PS];
-    __shared__ __attribute__((aligned(16))) float stat[TT][BM];
+    __shared__ __attribute__((aligned(16))) float stat[TG][BM];
     __shared__ __attribute__((aligned(16))) int ridx[3][BN];            // cache rows of the tiles' keys, -1: none
     __shared__ int64_t found[4];
     __shared__ int64_t wsum[DEC_WAVES][2];
@@ -168,10 +169,12 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
     int seq = (int)found[0];
     int64_t seq_base = found[1], unit_base = found[2];
 
-    const int tw = wave % TT, rg = wave / TT;      // key tile and row group of this wave's scores
-    const bool scores = rg * RQ < RT;
+    const int rt = wave % RT, tg = wave / RT;      // row tile and key group of this wave's scores
+    const bool scores = tg < TG;
     const E* cache = (const E*)a.cache;
     Stage<E, W, BN, NT> st;
+    const RowReader<E, W> k_rows(lane);
+    const ColReader<E, W, CT> c_cols(lane, wave * CT);
 
     for (int64_t pos = begin; pos < stop;) {
         int q0, n, len, row_tiles, key_tiles;
@@ -200,37 +203,34 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
             return page < 0 || page >= a.num_pages ? -1 : page * a.page_size + (j - pg * a.page_size);
         };
         auto load = [&](const int* rows) {
-            st.load(tid, [&](int r, int c) -> const E* {
+            st.load(tid, [&](int r) {
                 const int row = rows[r];
-                return row < 0 ? nullptr : cache + (int64_t)row * W + c * CE;
+                return row < 0 ? nullptr : cache + (int64_t)row * W;
             });
         };
         if (tid < BN) {
             ridx[0][tid] = cache_row(t0);
             ridx[1][tid] = cache_row(t0 + 1);
         }
-        v8 q[RQ][KS];
-        int last[RQ];                                                // last key this lane's row sees
-#pragma unroll
-        for (int r = 0; r < RQ; ++r) {
-            const int64_t row = row0 + min(nrows - 1, 16 * (rg * RQ + r) + col);
+        v8 q[KS];
+        int last;                                                    // last key this lane's row sees
+        {
+            const int64_t row = row0 + min(nrows - 1, 16 * rt + col);
             const int i = (int)(row / a.H), h = (int)(row - (int64_t)i * a.H);
             const E* qp = (const E*)a.q + (int64_t)(q0 + i) * a.q_token_stride + h * a.q_head_stride;
-            last[r] = len - n + i;
+            last = len - n + i;
             if (scores)
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) q[r][ks] = row_frag_global(qp, ks, lane);
+                for (int ks = 0; ks < KS; ++ks) q[ks] = row_frag_global(qp, ks, lane);
         }
         f32x4 acc[RT][CT];
-        float m[RT], l[RQ];
+        float m[RT], l = 0.f;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             m[r] = neg_inf();
 #pragma unroll
             for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-#pragma unroll
-        for (int r = 0; r < RQ; ++r) l[r] = 0.f;
         __syncthreads();
         int next_row = -1;
         if (t0 < te) {
@@ -244,31 +244,23 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
             const E* tile = tilebuf[k & 1];
             const int* rows = ridx[k3];
             const int n3 = k3 == 0 ? 2 : k3 - 1;                     // (k + 2) mod 3
-            f32x4 s[RQ];
+            f32x4 s[TW];
             if (scores) {
+                float top = neg_inf();
 #pragma unroll
-                for (int r = 0; r < RQ; ++r) s[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int w = 0; w < TW; ++w) {
+                    const int k0 = 16 * (tg * TW + w);
+                    s[w] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const v8 x = row_frag<W>(tile, 16 * tw, ks, lane);
-#pragma unroll
-                    for (int r = 0; r < RQ; ++r) s[r] = mma32(x, q[r][ks], s[r]);
-                }
-                int there[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) there[i] = rows[16 * tw + 4 * g + i];
-#pragma unroll
-                for (int r = 0; r < RQ; ++r) {
-                    float top = neg_inf();
+                    for (int ks = 0; ks < KS; ++ks) s[w] = mma32(k_rows(tile, k0, ks), q[ks], s[w]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int j = t * BN + 16 * tw + 4 * g + i;
-                        if (there[i] < 0 || j > last[r]) s[r][i] = neg_inf();
-                        top = fmaxf(top, s[r][i]);
+                        if (rows[k0 + 4 * g + i] < 0 || t * BN + k0 + 4 * g + i > last) s[w][i] = neg_inf();
+                        top = fmaxf(top, s[w][i]);
                     }
-                    top = group_max(top) * sc;
-                    if (g == 0) stat[tw][16 * (rg * RQ + r) + col] = top;
                 }
+                top = group_max(top) * sc;
+                if (g == 0) stat[tg][16 * rt + col] = top;
             }
             __syncthreads();   // maxima written; the other buffer's last readers are done
             if (tid < BN) ridx[n3][tid] = next_row;
@@ -279,7 +271,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
             for (int r = 0; r < RT; ++r) {
                 float top = stat[0][16 * r + col];
 #pragma unroll
-                for (int w = 1; w < TT; ++w) top = fmaxf(top, stat[w][16 * r + col]);
+                for (int w = 1; w < TG; ++w) top = fmaxf(top, stat[w][16 * r + col]);
                 const bool grew = top > m[r] + 8.f;
                 if (__any(grew)) {
                     const float mn = grew ? top : m[r];
@@ -287,27 +279,24 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
                     m[r] = mn;
 #pragma unroll
                     for (int c = 0; c < CT; ++c) acc[r][c] *= f;
-#pragma unroll
-                    for (int x = 0; x < RQ; ++x)
-                        if (rg * RQ + x == r) l[x] *= f;
+                    if (r == rt) l *= f;
                 }
             }
             if (scores) {
+                float from = m[0];
 #pragma unroll
-                for (int r = 0; r < RQ; ++r) {
-                    float mr = m[r];
+                for (int r = 1; r < RT; ++r) from = r == rt ? m[r] : from;
+                if (from == neg_inf()) from = 0.f;   // a row that has seen no key yet
 #pragma unroll
-                    for (int x = 1; x < RT; ++x) mr = rg * RQ + r == x ? m[x] : mr;
-                    if (rg * RQ + r == 0) mr = m[0];
-                    const float from = mr == neg_inf() ? 0.f : mr;
+                for (int w = 0; w < TW; ++w) {
                     v4 p;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float w = exp2_fast(__builtin_fmaf(s[r][i], sc, -from));
-                        l[r] += w;                 // the sum takes the weights before their rounding
-                        p[i] = from_f32<E>(w);     // bf16: the product's operand type
+                        const float x = exp2_fast(__builtin_fmaf(s[w][i], sc, -from));
+                        l += x;                // the sum takes the weights before their rounding
+                        p[i] = from_f32<E>(x); // bf16: the product's operand type
                     }
-                    store_vec(sp + (16 * (rg * RQ + r) + col) * PS + 16 * tw + 4 * g, p);
+                    store_vec(sp + (16 * rt + col) * PS + 16 * (tg * TW + w) + 4 * g, p);
                 }
             }
             __syncthreads();   // weights, the next tile and the rows of the one after it are there
@@ -326,7 +315,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
                 }
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
-                    const v8 x = col_frag<W>(tile, 32 * b, 32 * b + 16, 16 * (wave * CT + c), lane);
+                    const v8 x = c_cols(tile, 32 * b, 32 * b + 16, c);
 #pragma unroll
                     for (int r = 0; r < RT; ++r) acc[r][c] = mma32(x, p[r], acc[r][c]);
                 }
@@ -334,12 +323,10 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
         }
         // the rows' sums over the waves
         __syncthreads();
-        if (scores)
-#pragma unroll
-            for (int r = 0; r < RQ; ++r) {
-                const float x = group_sum(l[r]);
-                if (g == 0) stat[tw][16 * (rg * RQ + r) + col] = x;
-            }
+        if (scores) {
+            const float x = group_sum(l);
+            if (g == 0) stat[tg][16 * rt + col] = x;
+        }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == key_tiles;
         const int64_t out0 = (int64_t)q0 * a.H + row0;
@@ -348,7 +335,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
         for (int r = 0; r < RT; ++r) {
             float sum = stat[0][16 * r + col];
 #pragma unroll
-            for (int w = 1; w < TT; ++w) sum += stat[w][16 * r + col];
+            for (int w = 1; w < TG; ++w) sum += stat[w][16 * r + col];
             const int row = 16 * r + col;
             if (row >= nrows) continue;
             if (whole) {
