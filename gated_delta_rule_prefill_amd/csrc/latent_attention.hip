@@ -13,15 +13,15 @@
 
 namespace kda {
 
-// A workgroup: 4 waves of 32 query rows (two 16-row tiles, whose operands q
-// and o stay in registers), one head.  Key and value tiles of BN rows are
+// A workgroup: 4 waves of 32 (bf16) or 16 (fp32) query rows, whose operands q
+// and o stay in registers, one head.  Key and value tiles of BN rows are
 // double-buffered in LDS (80 KB, two workgroups a CU): the next tile's global
 // loads are issued before a tile's products and stored to LDS behind them.
 template <typename E, int DN, int DR>
 __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     const kda_latent_inputs in, E* __restrict__ o, float* __restrict__ lse, int tiles)
 {
-    constexpr int DQK = DN + DR, DV = DN, BN = 128 / (int)sizeof(E), NQ = 2;
+    constexpr int DQK = DN + DR, DV = DN, BN = 128 / (int)sizeof(E), NQ = LATENT_NQ<E>, BQ = 64 * NQ;
     constexpr int KS = DQK / 32, TT = BN / 16;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     int h, want, seq, tile;
     head_tile_of_block(in.H, tiles, h, want);
     const int rows_q = (int)(in.total_q / in.num_seqs);
-    if (!find_tile<LATENT_BQ, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, tiles - 1 - want,
+    if (!find_tile<BQ, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, tiles - 1 - want,
                                    reinterpret_cast<int*>(&smem[0][0]), seq, tile))
         return;
     int q0, q1, k0, k1;
@@ -37,8 +37,8 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
                   (int)in.total_k, seq, k0, k1);
     const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    const int wrow = tile * LATENT_BQ + 32 * wave;   // the wave's first row in the sequence
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
+    const int wrow = tile * BQ + 16 * NQ * wave;   // the wave's first row in the sequence
     const float sc = in.scale * LOG2E;
 
     const E* kp = (const E*)in.k + (int64_t)k0 * in.k_token_stride + h * in.k_head_stride;
@@ -56,9 +56,9 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
         for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(row, ks, lane);
         last[j] = in.causal ? min(nk - 1, r + off) : nk - 1;
     }
-    const int end = in.causal ? min(nk, min(nq, (tile + 1) * LATENT_BQ) + off) : nk;   // keys of the workgroup
+    const int end = in.causal ? min(nk, min(nq, (tile + 1) * BQ) + off) : nk;   // keys of the workgroup
     const int nt = end > 0 ? (end + BN - 1) / BN : 0;
-    const int wave_end = in.causal ? min(nk, min(nq, wrow + 32) + off) : nk;           // of the wave
+    const int wave_end = in.causal ? min(nk, min(nq, wrow + 16 * NQ) + off) : nk;           // of the wave
     const int wave_full = in.causal ? min(nk, wrow + off + 1) : nk;                    // keys all its rows see
 
     Stage<E, DQK, BN, 256, DR> sk;
@@ -189,9 +189,9 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
 
 template <typename E, int DN, int DR>
 static hipError_t launch(const kda_latent_inputs& in, void* o, float* lse, hipStream_t stream) {
-    const int64_t rows = in.total_q / in.num_seqs;
-    const int64_t tiles = in.cu_seqlens_q ? in.total_q / LATENT_BQ + in.num_seqs
-                                          : (rows + LATENT_BQ - 1) / LATENT_BQ * in.num_seqs;
+    constexpr int BQ = 64 * LATENT_NQ<E>;
+    const int64_t tiles = in.cu_seqlens_q ? in.total_q / BQ + in.num_seqs
+                                          : (in.total_q / in.num_seqs + BQ - 1) / BQ * in.num_seqs;
     hipLaunchKernelGGL((latent_attention_kernel<E, DN, DR>), dim3((unsigned)(tiles * in.H)), dim3(256), 0, stream,
                        in, (E*)o, lse, (int)tiles);
     return hipGetLastError();

@@ -16,9 +16,6 @@
 
 namespace kda {
 
-// Query rows per workgroup: 16 NQ per wave.
-template <typename E> constexpr int DQ_NQ = sizeof(E) == 2 ? 2 : 1;
-
 // dq and delta.  As in the forward kernel the scores are formed transposed
 // (rows = keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.
 template <typename E, int DN, int DR>
@@ -26,7 +23,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const kda_latent_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
     const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ delta, int tiles)
 {
-    constexpr int DQK = DN + DR, DV = DN, BN = 32, NQ = DQ_NQ<E>, BQ = 64 * NQ;
+    constexpr int DQK = DN + DR, DV = DN, BN = 32, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
     constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
@@ -42,7 +39,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
                   (int)in.total_k, seq, k0, k1);
     const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
     const int wrow = tile * BQ + 16 * NQ * wave;
     const float sc = in.scale * LOG2E;
 
@@ -196,7 +193,7 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
     sequence_rows(in.cu_seqlens_q, (int)(in.total_q / in.num_seqs), (int)in.total_q, seq, q0, q1);
     sequence_rows(cu_k, rows_k, (int)in.total_k, seq, k0, k1);
     const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
     const int key0 = tile * LATENT_BK, wkey = key0 + 16 * wave, key = wkey + col;
     const float sc = in.scale * LOG2E;
 
@@ -331,7 +328,7 @@ static int64_t tile_count(const int32_t* cu, int64_t total, int32_t N, int B) {
 
 template <typename E, int DN, int DR>
 static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipStream_t stream) {
-    const int64_t tq = tile_count(in.cu_seqlens_q, in.total_q, in.num_seqs, 64 * DQ_NQ<E>);
+    const int64_t tq = tile_count(in.cu_seqlens_q, in.total_q, in.num_seqs, 64 * LATENT_NQ<E>);
     const int32_t* cu_k = in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
     const int64_t tk = tile_count(cu_k, in.total_k, in.num_seqs, LATENT_BK);
     if (tq > 0)

@@ -58,9 +58,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Rotary a, int tokens,
         }
     };
     const int turned = a.dr / IE, items = turned + copies, rows = nt * a.H;
-    const int64_t all = (int64_t)rows * items;
-    for (int64_t id = threadIdx.x; id < all; id += 256) {
-        const int row = (int)(id / items), item = (int)(id - (int64_t)row * items);
+    const int all = rows * items;
+    for (int id = threadIdx.x; id < all; id += 256) {
+        const int row = id / items, item = id - row * items;
         const int t = row / a.H, h = row - t * a.H;
         const E* x = (const E*)a.x + (t0 + t) * a.x_token_stride + h * a.x_head_stride;
         E* y = (E*)a.y + (t0 + t) * a.y_token_stride + h * a.y_head_stride;
@@ -110,11 +110,16 @@ static hipError_t launch_rotary_t(const Rotary& a, hipStream_t stream) {
     const bool wide = ((uintptr_t)a.x | (uintptr_t)a.y) % 16 == 0 && even(a.x_token_stride) && even(a.x_head_stride) &&
                       even(a.y_token_stride) && even(a.y_head_stride) && even(a.start) && even(a.d) &&
                       even(inter ? a.dr : a.dr / 2);
-    // about 2,048 elements a workgroup where heads are few, and its angles in LDS
-    int64_t tokens = 2048 / ((int64_t)a.H * a.d);
+    const int copies = in_place ? 0 : (a.d - a.dr) / (wide ? CE : 1);
+    const int items = a.dr / (wide ? (inter ? CE : 2 * CE) : 2) + copies;
+    // Tokens of a workgroup: about three items a thread (a prompt of 65,536 x 32
+    // x 192 in bf16, one token each: 285 us, 5.65 TB/s, where a copy of as many
+    // bytes takes 306; with runs of four rows per thread, 346), with its angles
+    // in LDS and at least 512 workgroups.
+    int64_t tokens = 768 / ((int64_t)a.H * items);
+    if (tokens > a.total_tokens / 512) tokens = a.total_tokens / 512;
     if (tokens > ROTARY_PAIRS / (a.dr / 2)) tokens = ROTARY_PAIRS / (a.dr / 2);
     if (tokens < 1) tokens = 1;
-    const int copies = in_place ? 0 : (a.d - a.dr) / (wide ? CE : 1);
     const dim3 grid((unsigned)((a.total_tokens + tokens - 1) / tokens));
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, (int)tokens, copies); };
     if (wide) inter ? go(rotary_kernel<E, CE, true>) : go(rotary_kernel<E, CE, false>);

@@ -10,10 +10,23 @@ namespace kda {
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Query rows of a wave in 16-row tiles (forward, dq), and keys of a workgroup
+// (dk, dv).  bf16: two tiles, so that an operand read from LDS serves two
+// products.  fp32: one; its products take eight times as long, LDS is no bound,
+// and the smaller tiles spread a short batch over more CUs (130 tokens x 4
+// heads: 22 us with two tiles).
+template <typename E> constexpr int LATENT_NQ = sizeof(E) == 2 ? 2 : 1;
+constexpr int LATENT_BK = 64;
+
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// A value that is the same in every lane, held in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x));
+}
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 // -- row-major tiles in LDS ------------------------------------------------------
@@ -147,6 +160,20 @@ struct Stage {
     }
     template <typename F>
     __device__ __forceinline__ void load(int tid, F row) { load(tid, row, row); }
+    // store(), each chunk's register refilled at once with the tile after next,
+    // so that a tile's worth of loads stays in flight (one row per thread)
+    template <typename F>
+    __device__ __forceinline__ void store_load(int tid, E* t, F row) {
+        static_assert(P == 1 && W1 == 0, "one row per thread");
+        E* at = t + tile_at<E, W>(tid / TPR, tid % TPR);
+        const E* a = row(tid / TPR);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            *reinterpret_cast<u32x4*>(at + TPR * CE * s) = r[0][s];
+            r[0][s] = u32x4{0, 0, 0, 0};
+            if (a) r[0][s] = *reinterpret_cast<const u32x4*>(a + TPR * CE * s + CE * (tid % TPR));
+        }
+    }
     __device__ __forceinline__ void store(int tid, E* t) const {
         E* at = t + tile_at<E, W>(tid / TPR, tid % TPR);
 #pragma unroll
@@ -215,8 +242,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int N, int rows, in
             scratch[NW + 1] = want - excl;
         }
         __syncthreads();
-        seq = scratch[NW];
-        tile = scratch[NW + 1];
+        seq = uniform(scratch[NW]);
+        tile = uniform(scratch[NW + 1]);
         __syncthreads();
         if (seq >= 0) return true;
         before = all;

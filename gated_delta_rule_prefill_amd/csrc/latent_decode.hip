@@ -18,8 +18,8 @@
 // spread over the waves' registers.
 //
 // The work of a batch (row tiles x key tiles of every sequence, in order) is
-// cut into equal runs, one for each of 256 workgroups, whatever the lengths:
-// a run may end inside a row tile, whose partial results a second kernel
+// cut into equal runs, one for each of 256 workgroups, whatever the lengths: a
+// run may end inside a row tile, whose partial results a second kernel
 // joins.  The cut depends on the lengths only, so results are reproducible.
 #include "latent_common.h"
 
@@ -83,18 +83,23 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
     constexpr int TW = TT / TG;                                         // TW key tiles (key group of TG)
     constexpr int CT = DL / 16 / DEC_WAVES;                             // 16-column value tiles of a wave
     constexpr int PS = BN + 16 / (int)sizeof(E);                        // row stride of the weights
+    constexpr bool QREG = sizeof(E) == 2;   // query rows in registers; fp32 rows would fill them
     typedef typename Vec<E>::v8 v8;
     typedef typename Vec<E>::v4 v4;
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
     __shared__ __attribute__((aligned(16))) E tilebuf[2][BN * W];
     __shared__ __attribute__((aligned(16))) E sp[BM * PS];
     __shared__ __attribute__((aligned(16))) float stat[TG][BM];
-    __shared__ __attribute__((aligned(16))) int ridx[3][BN];            // cache rows of the tiles' keys, -1: none
+    __shared__ __attribute__((aligned(16))) int ridx[4][BN];            // cache rows of the tiles' keys, -1: none
     __shared__ int64_t found[4];
     __shared__ int64_t wsum[DEC_WAVES][2];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
     const int rows_q = (int)(a.total_tokens / a.num_seqs);
     const float sc = a.scale * LOG2E;
+    // Workgroups go round robin over the 8 XCDs: neighbouring runs, which read
+    // the same sequence's keys, go to one XCD and its L2.
+    const int run = (blockIdx.x & 7) * (DEC_GRID / 8) + (blockIdx.x >> 3);
 
     // this workgroup's run of the batch's work: the sum over the sequences,
     // then the sequence its run begins in
@@ -122,11 +127,12 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
         if (w < wave) base += wsum[w][0], ubase += wsum[w][1];
         total += wsum[w][0], units += wsum[w][1];
     }
+    total = uniform(total);
     const int64_t per = (total + DEC_GRID - 1) / DEC_GRID;
-    const int64_t begin = per * blockIdx.x, stop = min(total, begin + per);
+    const int64_t begin = per * run, stop = min(total, begin + per);
     if (!by_tile) {
-        if (tid == 0) ws.split[blockIdx.x].rows = 0;
-    } else if (blockIdx.x == 0) {
+        if (tid == 0) ws.split[run].rows = 0;
+    } else if (run == 0) {
         for (int64_t i = units + tid; i < entries; i += NT) ws.split[i].rows = 0;
     }
     if (begin >= stop) return;
@@ -163,11 +169,11 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
             const int64_t excl = b + xi - x;
             if (begin >= excl && begin < excl + x) found[0] = s, found[1] = excl, found[2] = ub + ui - u;
             __syncthreads();
-            if (found[0] >= 0) break;
+            if (uniform(found[0]) >= 0) break;
         }
     }
-    int seq = (int)found[0];
-    int64_t seq_base = found[1], unit_base = found[2];
+    int seq = (int)uniform(found[0]);
+    int64_t seq_base = uniform(found[1]), unit_base = uniform(found[2]);
 
     const int rt = wave % RT, tg = wave / RT;      // row tile and key group of this wave's scores
     const bool scores = tg < TG;
@@ -202,24 +208,26 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
             const int page = table[pg];
             return page < 0 || page >= a.num_pages ? -1 : page * a.page_size + (j - pg * a.page_size);
         };
-        auto load = [&](const int* rows) {
-            st.load(tid, [&](int r) {
-                const int row = rows[r];
+        auto row_of = [&](int k) {                                   // of the tile t0 + k
+            return [&, k](int r) {
+                const int row = ridx[k & 3][r];
                 return row < 0 ? nullptr : cache + (int64_t)row * W;
-            });
+            };
         };
         if (tid < BN) {
             ridx[0][tid] = cache_row(t0);
             ridx[1][tid] = cache_row(t0 + 1);
+            ridx[2][tid] = cache_row(t0 + 2);
         }
-        v8 q[KS];
+        v8 q[QREG ? KS : 1];
+        const E* qp;
         int last;                                                    // last key this lane's row sees
         {
             const int64_t row = row0 + min(nrows - 1, 16 * rt + col);
             const int i = (int)(row / a.H), h = (int)(row - (int64_t)i * a.H);
-            const E* qp = (const E*)a.q + (int64_t)(q0 + i) * a.q_token_stride + h * a.q_head_stride;
+            qp = (const E*)a.q + (int64_t)(q0 + i) * a.q_token_stride + h * a.q_head_stride;
             last = len - n + i;
-            if (scores)
+            if (QREG && scores)
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) q[ks] = row_frag_global(qp, ks, lane);
         }
@@ -234,28 +242,56 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
         __syncthreads();
         int next_row = -1;
         if (t0 < te) {
-            load(ridx[0]);
-            st.store(tid, tilebuf[0]);
-            load(ridx[1]);
-            if (tid < BN) next_row = cache_row(t0 + 2);
+            Stage<E, W, BN, NT> first;
+            first.load(tid, row_of(0));
+            st.load(tid, row_of(1));
+            if (tid < BN) next_row = cache_row(t0 + 3);
+            first.store(tid, tilebuf[0]);
         }
         __syncthreads();
-        for (int t = t0, k = 0, k3 = 0; t < te; ++t, ++k, k3 = k3 == 2 ? 0 : k3 + 1) {
+        for (int t = t0, k = 0; t < te; ++t, ++k) {
             const E* tile = tilebuf[k & 1];
-            const int* rows = ridx[k3];
-            const int n3 = k3 == 0 ? 2 : k3 - 1;                     // (k + 2) mod 3
+            const int* rows = ridx[k & 3];
             f32x4 s[TW];
             if (scores) {
+                const E* qt = qp;
+                if (!QREG) asm volatile("" : "+v"(qt));   // fetched again for every tile
+#pragma unroll
+                for (int w = 0; w < TW; ++w) s[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+                // the keys' operands are read a group ahead of their products
+                constexpr int GK = KS % 6 == 0 ? 3 : KS % 4 == 0 ? 4 : 5, NG = KS / GK;
+                static_assert(KS % GK == 0, "whole groups");
+                v8 x[2][GK][TW], y[2][QREG ? 1 : GK];
+                auto fetch = [&](int gr) {
+#pragma unroll
+                    for (int i = 0; i < GK; ++i) {
+                        if constexpr (!QREG) y[gr & 1][i] = row_frag_global(qt, gr * GK + i, lane);
+#pragma unroll
+                        for (int w = 0; w < TW; ++w) x[gr & 1][i][w] = k_rows(tile, 16 * TW * tg + 16 * w, gr * GK + i);
+                    }
+                };
+                fetch(0);
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    if (gr + 1 < NG) fetch(gr + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < GK; ++i)
+#pragma unroll
+                        for (int w = 0; w < TW; ++w) {
+                            if constexpr (QREG) s[w] = mma32(x[gr & 1][i][w], q[gr * GK + i], s[w]);
+                            else s[w] = mma32(x[gr & 1][i][w], y[gr & 1][i], s[w]);
+                        }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
                 float top = neg_inf();
 #pragma unroll
                 for (int w = 0; w < TW; ++w) {
-                    const int k0 = 16 * (tg * TW + w);
-                    s[w] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) s[w] = mma32(k_rows(tile, k0, ks), q[ks], s[w]);
+                    const int k0 = 16 * (tg * TW + w) + 4 * g;
+                    const i32x4 there = *reinterpret_cast<const i32x4*>(rows + k0);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (rows[k0 + 4 * g + i] < 0 || t * BN + k0 + 4 * g + i > last) s[w][i] = neg_inf();
+                        if (there[i] < 0 || t * BN + k0 + i > last) s[w][i] = neg_inf();
                         top = fmaxf(top, s[w][i]);
                     }
                 }
@@ -263,8 +299,11 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
                 if (g == 0) stat[tg][16 * rt + col] = top;
             }
             __syncthreads();   // maxima written; the other buffer's last readers are done
-            if (tid < BN) ridx[n3][tid] = next_row;
-            if (t + 1 < te) st.store(tid, tilebuf[(k + 1) & 1]);
+            if (tid < BN) {
+                ridx[(k + 3) & 3][tid] = next_row;
+                next_row = cache_row(t + 4);
+            }
+            if (t + 1 < te) st.store_load(tid, tilebuf[(k + 1) & 1], row_of(k + 2));
             // the running maximum, raised only when it grew by more than 8 (in
             // powers of two); every wave takes the same decision for a row
 #pragma unroll
@@ -299,26 +338,28 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
                     store_vec(sp + (16 * rt + col) * PS + 16 * (tg * TW + w) + 4 * g, p);
                 }
             }
-            __syncthreads();   // weights, the next tile and the rows of the one after it are there
-            if (t + 2 < te) {
-                load(ridx[n3]);
-                if (tid < BN) next_row = cache_row(t + 3);
-            }
-#pragma unroll
-            for (int b = 0; b < TT / 2; ++b) {
-                v8 p[RT];
+            __syncthreads();   // weights and the next tile are there
+            // the values' operands are read one product ahead
+            v8 p[2][RT], x[2];
+            auto weights = [&](int b) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const E* x = sp + (16 * r + col) * PS + 32 * b + 4 * g;
-                    const v4 lo = load_vec<v4>(x), hi = load_vec<v4>(x + 16);
-                    p[r] = v8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                    const E* at = sp + (16 * r + col) * PS + 32 * b + 4 * g;
+                    const v4 lo = load_vec<v4>(at), hi = load_vec<v4>(at + 16);
+                    p[b & 1][r] = v8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
                 }
+            };
+            weights(0);
+            x[0] = c_cols(tile, 0, 16, 0);
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    const v8 x = c_cols(tile, 32 * b, 32 * b + 16, c);
+            for (int e = 0; e < TT / 2 * CT; ++e) {
+                const int b = e / CT, c = e % CT, f = e + 1;
+                if (f < TT / 2 * CT) x[f & 1] = c_cols(tile, 32 * (f / CT), 32 * (f / CT) + 16, f % CT);
+                if (c == CT - 1 && b + 1 < TT / 2) weights(b + 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) acc[r][c] = mma32(x, p[r], acc[r][c]);
-                }
+                for (int r = 0; r < RT; ++r) acc[r][c] = mma32(x[e & 1], p[b & 1][r], acc[r][c]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         // the rows' sums over the waves
@@ -330,7 +371,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
         __syncthreads();
         const bool whole = t0 == 0 && t1 == key_tiles;
         const int64_t out0 = (int64_t)q0 * a.H + row0;
-        const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+        const int slot = 2 * run + (t0 == 0 ? 1 : 0);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             float sum = stat[0][16 * r + col];
@@ -367,12 +408,12 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
                 DecodeSplit x;
                 x.row = out0;
                 x.rows = whole ? 0 : nrows;
-                x.first = (int)blockIdx.x;
+                x.first = run;
                 x.last = (int)((first_work + key_tiles - 1) / per);
                 x.pad = 0;
                 if (by_tile) {
                     if (unit_base + unit < entries) ws.split[unit_base + unit] = x;
-                } else if (!whole) ws.split[blockIdx.x] = x;
+                } else if (!whole) ws.split[run] = x;
             }
         }
         __syncthreads();   // statistics and tiles are free for the next piece
@@ -381,55 +422,36 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
 }
 
 // Joins the partial results of split row tiles: with M = max_p m_p,
-//   o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
-// A workgroup per (split, group of rows); SP waves share a row's parts (in a
-// fixed order), the others take further rows.
-template <typename E, int DL, int SP>
-__global__ __launch_bounds__(256) void latent_join_kernel(const DecodeSpace ws, E* __restrict__ o,
-                                                          float* __restrict__ lse, int BM)
+//   o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,
+// the parts in order.  Many row tiles have few parts each: a wave per row.
+template <typename E, int DL>
+__global__ __launch_bounds__(256) void latent_join_rows_kernel(const DecodeSpace ws, E* __restrict__ o,
+                                                               float* __restrict__ lse, int BM)
 {
-    constexpr int ROWS = 4 / SP, EPL = DL / 64;   // rows of a workgroup, columns of a lane
-    __shared__ float so[4][DL];
+    constexpr int EPL = DL / 64;   // columns of a lane
     const DecodeSplit x = ws.split[blockIdx.x];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row = blockIdx.y * ROWS + wave / SP, part = wave % SP;
-    const bool live = row < x.rows;
-    if (blockIdx.y * ROWS >= x.rows) return;      // uniform over the workgroup
+    const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6);
+    if (row >= x.rows) return;
     const int parts = x.last - x.first + 1;
-    auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * x.first + 1 : 2 * (x.first + p)) * BM + min(row, x.rows - 1); };
+    auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * x.first + 1 : 2 * (x.first + p)) * BM + row; };
     float top = neg_inf();
     for (int p = lane; p < parts; p += 64) top = fmaxf(top, ws.ml[slot(p) * 2]);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
     const float from = top == neg_inf() ? 0.f : top;
-    float sum = 0.f;
-    for (int p = lane; p < parts; p += 64) {
-        const float* ml = ws.ml + slot(p) * 2;
-        sum += exp2_fast(ml[0] - from) * ml[1];
-    }
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
     f32x4 acc[EPL / 4];
+    float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < EPL / 4; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = part; p < parts; p += SP) {
-        const float f = exp2_fast(ws.ml[slot(p) * 2] - from);
+#pragma unroll 2
+    for (int p = 0; p < parts; ++p) {
+        const float* ml = ws.ml + slot(p) * 2;
+        const float f = exp2_fast(ml[0] - from);
         const float* src = ws.o + slot(p) * DL + 4 * lane;
+        sum += f * ml[1];
 #pragma unroll
         for (int e = 0; e < EPL / 4; ++e) acc[e] += f * *reinterpret_cast<const f32x4*>(src + 256 * e);
     }
-    if (SP > 1) {
-#pragma unroll
-        for (int e = 0; e < EPL / 4; ++e) store_vec(&so[wave][256 * e + 4 * lane], acc[e]);
-        __syncthreads();
-        if (part != 0) return;
-#pragma unroll
-        for (int w = 1; w < SP; ++w)
-#pragma unroll
-            for (int e = 0; e < EPL / 4; ++e) acc[e] += *reinterpret_cast<const f32x4*>(&so[wave + w][256 * e + 4 * lane]);
-    }
-    if (!live) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int e = 0; e < EPL / 4; ++e) {
@@ -440,6 +462,58 @@ __global__ __launch_bounds__(256) void latent_join_kernel(const DecodeSpace ws, 
     }
     if (lse && lane == 0) lse[x.row + row] = sum == 0.f ? neg_inf() : (top + __log2f(sum)) * LN2;
 }
+
+// Few row tiles may have a part from every workgroup: a workgroup joins 64
+// columns of a row, 16 threads side by side and the parts over 16 of them, the
+// parts' factors worked out once in LDS.
+template <typename E, int DL>
+__global__ __launch_bounds__(256) void latent_join_parts_kernel(const DecodeSpace ws, E* __restrict__ o,
+                                                                float* __restrict__ lse, int BM)
+{
+    __shared__ float factor[DEC_GRID];
+    __shared__ float red[4][2];
+    __shared__ __attribute__((aligned(16))) f32x4 part[16][16];
+    const DecodeSplit x = ws.split[blockIdx.x];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, row = blockIdx.y;
+    if (row >= x.rows) return;
+    const int parts = x.last - x.first + 1;   // at most DEC_GRID, one per workgroup
+    auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * x.first + 1 : 2 * (x.first + p)) * BM + row; };
+    float m = neg_inf(), l = 0.f;
+    if (tid < parts) {
+        m = ws.ml[slot(tid) * 2];
+        l = ws.ml[slot(tid) * 2 + 1];
+    }
+    float top = m;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0) red[wave][0] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
+    const float f = m == neg_inf() ? 0.f : exp2_fast(m - top);
+    factor[tid] = f;
+    float sum = f * l;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    if (lane == 0) red[wave][1] = sum;
+    __syncthreads();
+    sum = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
+    const int c = 64 * blockIdx.z + 4 * (tid & 15), first = tid >> 4;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int p = first; p < parts; p += 16) acc += factor[p] * *reinterpret_cast<const f32x4*>(ws.o + slot(p) * DL + c);
+    part[first][tid & 15] = acc;
+    __syncthreads();
+    if (first != 0) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) acc += part[i][tid];
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    typename Vec<E>::v4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = from_f32<E>(acc[i] * inv);
+    store_vec(o + (x.row + row) * DL + c, y);
+    if (lse && tid == 0 && blockIdx.z == 0) lse[x.row + row] = sum == 0.f ? neg_inf() : (top + __log2f(sum)) * LN2;
+}
+static_assert(DEC_GRID <= 256, "a thread per part");
 
 // Row tiles of 32 rows where a sequence's rows fit in one (a tile of 64 would
 // be half empty), else of 64 (each cached row is then fetched half as often).
@@ -462,11 +536,12 @@ static hipError_t launch(const LatentDecode& a, hipStream_t stream) {
     const int entries = by_tile ? (int)bound : DEC_GRID;
     hipLaunchKernelGGL((latent_decode_kernel<E, DL, DR, RT>), dim3(DEC_GRID), dim3(64 * DEC_WAVES), 0, stream, a, ws,
                        by_tile ? 1 : 0, entries);
-    // few row tiles: their parts are many, and four waves share each row's
-    if (entries * BM <= 1024)
-        hipLaunchKernelGGL((latent_join_kernel<E, DL, 4>), dim3(entries, BM), dim3(256), 0, stream, ws, (E*)a.o, a.lse, BM);
+    if (entries <= 32)   // 8 parts a row tile and more
+        hipLaunchKernelGGL((latent_join_parts_kernel<E, DL>), dim3(entries, BM, DL / 64), dim3(256), 0, stream, ws,
+                           (E*)a.o, a.lse, BM);
     else
-        hipLaunchKernelGGL((latent_join_kernel<E, DL, 1>), dim3(entries, BM / 4), dim3(256), 0, stream, ws, (E*)a.o, a.lse, BM);
+        hipLaunchKernelGGL((latent_join_rows_kernel<E, DL>), dim3(entries, BM / 4), dim3(256), 0, stream, ws, (E*)a.o,
+                           a.lse, BM);
     return hipGetLastError();
 }
 

@@ -9,10 +9,6 @@
 
 namespace kda {
 
-// Query rows and keys of one workgroup of the expanded attention kernels.
-constexpr int LATENT_BQ = 128;   // query rows (forward, dq)
-constexpr int LATENT_BK = 64;    // keys (dk, dv)
-
 hipError_t launch_latent_attention(const kda_latent_inputs& in, void* o, float* lse,
                                    hipStream_t stream);
 

@@ -7,6 +7,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -364,38 +365,38 @@ def prefill_kernel_times():
 
 # -- latent attention ------------------------------------------------------------
 
-class _on:
-    """The device and stream a call runs on: the call's own stream argument or
-    the device's current one.  Outputs and workspaces the binding allocates
+# A decode step makes several of these calls per layer, so their checks compare
+# first and word a message only for a failure.
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Context of the device and stream a call runs on: its own stream argument
+    or the device's current one.  Outputs and workspaces the binding allocates
     belong to that stream."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.ctx = None
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index is not None and device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return _NOTHING
 
 
 def _raw_stream(device) -> int:
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _rows3(t, name, shape, dtype, device) -> None:
-    """A [rows, heads, channels] tensor whose last axis is dense."""
-    _require(tuple(t.shape) == shape, f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    _require(t.dtype == dtype and t.device == device, f"{name}: expected {dtype} on {device}")
-    _require(t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0, f"{name}: the last axis must be dense")
+    """A tensor whose last axis is dense."""
+    if (t.shape == shape and t.dtype is dtype and t.device == device and
+            (t.stride(-1) == 1 or shape[-1] == 1 or t.numel() == 0)):
+        return
+    raise ValueError(f"{name}: expected {dtype} {shape} on {device} with a dense last axis, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
 def _stride(t, axis: int) -> int:
@@ -404,15 +405,18 @@ def _stride(t, axis: int) -> int:
 
 
 def _dense(t, name, shape, dtype, device) -> None:
-    _require(tuple(t.shape) == shape and t.dtype == dtype and t.device == device and t.is_contiguous(),
-             f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {device}")
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {device}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _offsets(cu, name, device) -> int:
     import torch
-    _require(cu.dtype == torch.int32 and cu.dim() == 1 and cu.shape[0] >= 2 and cu.device == device and
-             cu.is_contiguous(), f"{name}: contiguous int32 [N+1] on {device}")
-    return cu.shape[0] - 1
+    if cu.dtype is torch.int32 and cu.dim() == 1 and cu.shape[0] >= 2 and cu.device == device and cu.is_contiguous():
+        return cu.shape[0] - 1
+    raise ValueError(f"{name}: expected contiguous int32 [N+1] on {device}, got {cu.dtype} {tuple(cu.shape)} "
+                     f"on {cu.device}")
 
 
 def _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale):
@@ -428,7 +432,7 @@ def _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, sc
     _rows3(v, "v", (Tk, H, v.shape[2]), q.dtype, dev)
     pes = 0
     if dr:
-        _require(k_pe is not None, f"q has {dr} channels beyond k's: k_pe is needed")
+        _require(k_pe is not None, "q has channels beyond k's: k_pe is needed")
         _rows3(k_pe, "k_pe", (Tk, dr), q.dtype, dev)
         pes = _stride(k_pe, 0)
     else:
@@ -522,8 +526,7 @@ def _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs, T):
         int(num_seqs) if num_seqs is not None else seq_lens.shape[0]
     _require(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == N and
              block_table.device == dev and block_table.is_contiguous(), "block_table: contiguous int32 [N, max_pages]")
-    _require(seq_lens.dtype == torch.int32 and tuple(seq_lens.shape) == (N,) and seq_lens.device == dev and
-             seq_lens.is_contiguous(), "seq_lens: contiguous int32 [N]")
+    _dense(seq_lens, "seq_lens", (N,), torch.int32, dev)
     return N
 
 
@@ -595,7 +598,7 @@ def latent_append(cache, c, block_table, seq_lens, k_pe=None, cu_seqlens=None, n
     dr = cache.shape[2] - dl
     _rows3(c, "c", (T, dl), cache.dtype, dev)
     if dr:
-        _require(k_pe is not None, f"the cache has {dr} channels beyond c's: k_pe is needed")
+        _require(k_pe is not None, "the cache has channels beyond c's: k_pe is needed")
         _rows3(k_pe, "k_pe", (T, dr), cache.dtype, dev)
     else:
         _require(k_pe is None, "k_pe: the cache has no channels for it")
@@ -640,7 +643,7 @@ def rotary(x, positions, inv_freq, start: int = 0, interleaved: bool = False, ms
     _rows3(x, "x", (T, H, d), x.dtype, dev)
     _dense(positions, "positions", (T,), torch.int32, dev)
     _require(inv_freq.dim() == 1, "inv_freq: fp32 [dr / 2]")
-    _dense(inv_freq, "inv_freq", tuple(inv_freq.shape), torch.float32, dev)
+    _dense(inv_freq, "inv_freq", inv_freq.shape, torch.float32, dev)
     code = _dtype_code(x)
     with _on(dev, stream):
         if out is None:
