@@ -64,9 +64,9 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     Stage<E, DQK, BN, 256, DR> sk;
     Stage<E, DV, BN, 256> sv;
     auto load = [&](int t) {
-        sk.load(tid, [&](int r) { return t * BN + r < nk ? kp + (int64_t)(t * BN + r) * in.k_token_stride : nullptr; },
-                [&](int r) { return pp + (int64_t)(t * BN + r) * in.k_pe_token_stride; });
-        sv.load(tid, [&](int r) { return t * BN + r < nk ? vp + (int64_t)(t * BN + r) * in.v_token_stride : nullptr; });
+        sk.load(tid, [&](int r) { return t * BN + r < nk ? kp + (int64_t)(t * BN + r) * in.k_token_stride : zero_row<E>(); },
+                [&](int r) { return t * BN + r < nk ? pp + (int64_t)(t * BN + r) * in.k_pe_token_stride : zero_row<E>(); });
+        sv.load(tid, [&](int r) { return t * BN + r < nk ? vp + (int64_t)(t * BN + r) * in.v_token_stride : zero_row<E>(); });
     };
     const RowReader<E, DQK> k_rows(lane);
     const ColReader<E, DV, DV / 16> v_cols(lane);

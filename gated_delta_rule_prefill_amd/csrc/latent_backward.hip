@@ -78,9 +78,9 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     Stage<E, DQK, BN, 256, DR> sk;
     Stage<E, DV, BN, 256> sv;
     auto load = [&](int t) {
-        sk.load(tid, [&](int r) { return t * BN + r < nk ? kp + (int64_t)(t * BN + r) * in.k_token_stride : nullptr; },
-                [&](int r) { return pp + (int64_t)(t * BN + r) * in.k_pe_token_stride; });
-        sv.load(tid, [&](int r) { return t * BN + r < nk ? vp + (int64_t)(t * BN + r) * in.v_token_stride : nullptr; });
+        sk.load(tid, [&](int r) { return t * BN + r < nk ? kp + (int64_t)(t * BN + r) * in.k_token_stride : zero_row<E>(); },
+                [&](int r) { return t * BN + r < nk ? pp + (int64_t)(t * BN + r) * in.k_pe_token_stride : zero_row<E>(); });
+        sv.load(tid, [&](int r) { return t * BN + r < nk ? vp + (int64_t)(t * BN + r) * in.v_token_stride : zero_row<E>(); });
     };
     const RowReader<E, DQK> k_rows(lane);
     const RowReader<E, DV> v_rows(lane);
@@ -218,8 +218,8 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
     Stage<E, DV, BQ, 256> sg;
     float srow_next = 0.f;
     auto load = [&](int t) {
-        sq.load(tid, [&](int r) { return t * BQ + r < nq ? qp + (int64_t)(t * BQ + r) * in.q_token_stride : nullptr; });
-        sg.load(tid, [&](int r) { return t * BQ + r < nq ? gp + (int64_t)(t * BQ + r) * in.H * DV : nullptr; });
+        sq.load(tid, [&](int r) { return t * BQ + r < nq ? qp + (int64_t)(t * BQ + r) * in.q_token_stride : zero_row<E>(); });
+        sg.load(tid, [&](int r) { return t * BQ + r < nq ? gp + (int64_t)(t * BQ + r) * in.H * DV : zero_row<E>(); });
         if (tid < 2 * BQ) {   // rows behind the last weigh nothing: lse = inf
             const int i = t * BQ + (tid & (BQ - 1));
             const int64_t at = (int64_t)(q0 + min(i, nq - 1)) * in.H + h;

@@ -31,44 +31,55 @@ __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 // -- row-major tiles in LDS ------------------------------------------------------
 // W elements per row, in 16-byte chunks; chunk c of row r is stored at chunk
-// position c ^ swizzle(r).  The swizzle takes 8 values over 8 consecutive rows
-// (operands read by rows: 16 rows at one chunk column) and 4 different pairs
-// over 4 consecutive rows (operands read by columns: two neighbouring chunks
-// of 4 rows), so both kinds of read spread over the banks.
+// position c ^ swizzle(r).  LDS serves 256 bytes (64 banks) a cycle, so an
+// access by rows (16 rows at one chunk column) is free of conflicts when the 16
+// chunks fall on 16 different positions of 256 bytes, and an access by columns
+// (two neighbouring chunks of 8 rows) when the 8 pairs do.  A row of an odd
+// number of 128 bytes alternates between the halves by itself, and the swizzle
+// permutes groups of 8 chunks; a row of whole 256 bytes takes the half from the
+// row's lowest bit, and the swizzle permutes groups of 16.
 template <typename E> constexpr int CHUNK_ELEMS = 16 / (int)sizeof(E);
-__device__ __forceinline__ int swizzle(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+template <typename E, int W> constexpr bool WHOLE_ROWS = W * (int)sizeof(E) % 256 == 0;
 
 template <typename E, int W>
 __device__ __forceinline__ int tile_at(int row, int chunk) {
-    return row * W + ((chunk ^ swizzle(row)) * CHUNK_ELEMS<E>);
+    static_assert(W * sizeof(E) % 128 == 0, "rows of whole 128 bytes");
+    int f = (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
+    if (WHOLE_ROWS<E, W>) f |= (row & 1) << 3;
+    return row * W + ((chunk ^ f) * CHUNK_ELEMS<E>);
+}
+
+// Element at chunk c + c1 of the row whose chunk c is at `at`, for a constant c1
+// that is a multiple of 8 and a c below 8.
+template <typename E, int W>
+__device__ __forceinline__ int later_chunk(int at, int c1) {
+    constexpr int CE = CHUNK_ELEMS<E>;
+    return WHOLE_ROWS<E, W> ? (at ^ ((c1 & 8) * CE)) + (c1 & ~15) * CE : at + c1 * CE;
 }
 
 // Operands by rows of a tile: lane l supplies row row0 + (l & 15), slots
-// 8g .. 8g + 7 of the 32-wide block ks (g = l >> 4).  A lane's addresses are
-// two bases and constant offsets from them (the swizzle permutes chunks within
-// groups of 8 only); row0 is a multiple of 16.
+// 8g .. 8g + 7 of the 32-wide block ks (g = l >> 4).  A lane's addresses come
+// from two bases and constants; row0 is a multiple of 16.
 template <typename E, int W> struct RowReader;
 template <int W> struct RowReader<bf16, W> {
     int at[2];
     __device__ __forceinline__ explicit RowReader(int lane) {
-        const int r = lane & 15, g = lane >> 4;
-        at[0] = tile_at<bf16, W>(r, g);
-        at[1] = tile_at<bf16, W>(r, 4 + g);
+        at[0] = tile_at<bf16, W>(lane & 15, lane >> 4);
+        at[1] = tile_at<bf16, W>(lane & 15, 4 + (lane >> 4));
     }
     __device__ __forceinline__ bf16x8 operator()(const bf16* t, int row0, int ks) const {
-        return *reinterpret_cast<const bf16x8*>(t + at[ks & 1] + (row0 * W + 64 * (ks >> 1)));
+        return *reinterpret_cast<const bf16x8*>(t + later_chunk<bf16, W>(at[ks & 1], 8 * (ks >> 1)) + row0 * W);
     }
 };
 template <int W> struct RowReader<float, W> {
     int at[2];
     __device__ __forceinline__ explicit RowReader(int lane) {
-        const int r = lane & 15, g = lane >> 4;
-        at[0] = tile_at<float, W>(r, 2 * g);
-        at[1] = tile_at<float, W>(r, 2 * g + 1);
+        at[0] = tile_at<float, W>(lane & 15, 2 * (lane >> 4));
+        at[1] = tile_at<float, W>(lane & 15, 2 * (lane >> 4) + 1);
     }
     __device__ __forceinline__ f32x8 operator()(const float* t, int row0, int ks) const {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(t + at[0] + (row0 * W + 32 * ks));
-        const f32x4 b = *reinterpret_cast<const f32x4*>(t + at[1] + (row0 * W + 32 * ks));
+        const f32x4 a = *reinterpret_cast<const f32x4*>(t + later_chunk<float, W>(at[0], 8 * ks) + row0 * W);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(t + later_chunk<float, W>(at[1], 8 * ks) + row0 * W);
         return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
 };
@@ -78,20 +89,24 @@ template <int W> struct RowReader<float, W> {
 // multiples of 16).  The rows 4g + i of two 16-row blocks are what an
 // accumulator tile leaves in lane group g, so the other operand of the product
 // stays in registers.  (bf16: the transposing LDS read, a lane group's 16 lanes
-// fetching 4 rows of 16 columns.)  CT column tiles, ct0 a multiple of min(CT, 4).
+// fetching 4 rows of 16 columns.)  CT column tiles, ct0 a multiple of CT, and of
+// 4 where CT is more.
 template <typename E, int W, int CT> struct ColReader;
 template <int W, int CT> struct ColReader<bf16, W, CT> {
-    int at[CT < 4 ? CT : 4];
+    int at[CT < 4 ? CT : 4], from;
     __device__ __forceinline__ explicit ColReader(int lane, int ct0 = 0) {
         const int r = 4 * (lane >> 4) + ((lane & 15) >> 2), c = 4 * (lane & 3);
+        from = ct0;
 #pragma unroll
-        for (int i = 0; i < (CT < 4 ? CT : 4); ++i)
-            at[i] = tile_at<bf16, W>(r, 2 * (ct0 + i) + (c >> 3)) + (c & 4);
+        for (int i = 0; i < (CT < 4 ? CT : 4); ++i) {
+            const int chunk = 2 * (ct0 + i) + (c >> 3);
+            at[i] = tile_at<bf16, W>(r, CT <= 4 ? chunk : chunk & 7) + (c & 4);
+        }
     }
     __device__ __forceinline__ bf16x8 operator()(const bf16* t, int ra, int rb, int ct) const {
         typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
         typedef short s16x8 __attribute__((ext_vector_type(8)));
-        const bf16* p = t + at[ct & 3] + 64 * (ct >> 2);
+        const bf16* p = t + (CT <= 4 ? at[ct & 3] : later_chunk<bf16, W>(at[ct & 3], 2 * ((from + ct) & ~3)));
         const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + ra * W));
         const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + rb * W));
         return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
@@ -134,52 +149,55 @@ __device__ __forceinline__ f32x8 row_frag_global(const float* row, int ks, int l
 // -- staging: global -> registers -> LDS ---------------------------------------
 // ROWS x W elements moved by NT threads, 8 or more threads to a row (128-byte
 // lines), so that a thread's chunks lie at constant offsets from one address
-// per row it serves.  row(r) returns the row's address, or NULL for zeros; with W1 > 0 the
-// last W1 of the W channels come from row1(r).  The loads are issued by load()
-// and waited for by store(), a tile of work later.
+// per row it serves.  row(r) returns the row's address (zero_row() for a row
+// that is not there, so that no load is conditional); with W1 > 0 the last W1
+// of the W channels come from row1(r).  The loads are issued by load() and
+// waited for by store(), a tile of work later.
+static __device__ const u32x4 kZeros[144] = {};   // a row of up to 576 fp32 channels
+template <typename E> __device__ __forceinline__ const E* zero_row() { return reinterpret_cast<const E*>(kZeros); }
+
 template <typename E, int W, int ROWS, int NT, int W1 = 0>
 struct Stage {
     static constexpr int CE = CHUNK_ELEMS<E>, TPR = ROWS * 8 >= NT ? 8 : NT / ROWS;   // threads per row
     static constexpr int PASS = NT / TPR, P = ROWS / PASS, S = W / CE / TPR, S0 = (W - W1) / CE / TPR;
-    static_assert(ROWS % PASS == 0 && PASS % 8 == 0 && W % (TPR * CE) == 0 && W1 % (TPR * CE) == 0, "whole passes and steps");
+    static_assert(ROWS % PASS == 0 && PASS % 16 == 0 && W % (TPR * CE) == 0 && W1 % (TPR * CE) == 0, "whole passes and steps");
     u32x4 r[P][S];
     template <typename F, typename G>
     __device__ __forceinline__ void load(int tid, F row, G row1) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const E* a = row(tid / TPR + PASS * p);
-            const E* b = W1 ? row1(tid / TPR + PASS * p) : nullptr;
+            const E* a = row(tid / TPR + PASS * p) + CE * (tid % TPR);
+            const E* b = W1 ? row1(tid / TPR + PASS * p) + CE * (tid % TPR) : nullptr;
 #pragma unroll
-            for (int s = 0; s < S; ++s) r[p][s] = u32x4{0, 0, 0, 0};
-            if (a) {
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-                    r[p][s] = *reinterpret_cast<const u32x4*>((s < S0 ? a + TPR * CE * s : b + TPR * CE * (s - S0)) + CE * (tid % TPR));
-            }
+            for (int s = 0; s < S; ++s)
+                r[p][s] = *reinterpret_cast<const u32x4*>(s < S0 ? a + TPR * CE * s : b + TPR * CE * (s - S0));
         }
     }
     template <typename F>
     __device__ __forceinline__ void load(int tid, F row) { load(tid, row, row); }
     // store(), each chunk's register refilled at once with the tile after next,
-    // so that a tile's worth of loads stays in flight (one row per thread)
+    // so that a tile's worth of loads stays in flight
     template <typename F>
     __device__ __forceinline__ void store_load(int tid, E* t, F row) {
-        static_assert(P == 1 && W1 == 0, "one row per thread");
-        E* at = t + tile_at<E, W>(tid / TPR, tid % TPR);
-        const E* a = row(tid / TPR);
+        static_assert(W1 == 0, "rows of one piece");
+        const int at = tile_at<E, W>(tid / TPR, tid % TPR);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            *reinterpret_cast<u32x4*>(at + TPR * CE * s) = r[0][s];
-            r[0][s] = u32x4{0, 0, 0, 0};
-            if (a) r[0][s] = *reinterpret_cast<const u32x4*>(a + TPR * CE * s + CE * (tid % TPR));
+        for (int p = 0; p < P; ++p) {
+            const E* a = row(tid / TPR + PASS * p) + CE * (tid % TPR);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                *reinterpret_cast<u32x4*>(t + later_chunk<E, W>(at, TPR * s) + PASS * p * W) = r[p][s];
+                r[p][s] = *reinterpret_cast<const u32x4*>(a + TPR * CE * s);
+            }
         }
     }
     __device__ __forceinline__ void store(int tid, E* t) const {
-        E* at = t + tile_at<E, W>(tid / TPR, tid % TPR);
+        const int at = tile_at<E, W>(tid / TPR, tid % TPR);
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int s = 0; s < S; ++s) *reinterpret_cast<u32x4*>(at + PASS * p * W + TPR * CE * s) = r[p][s];
+            for (int s = 0; s < S; ++s)
+                *reinterpret_cast<u32x4*>(t + later_chunk<E, W>(at, TPR * s) + PASS * p * W) = r[p][s];
     }
 };
 

@@ -9,51 +9,63 @@
 // byte and the cache's bytes bound the kernel, with 64 rows and more the
 // matrix products do.
 //
-// A workgroup of 8 waves takes 16 RT query rows of one sequence and walks key
-// tiles of BN rows through LDS.  The scores of a tile are formed transposed
-// (rows = keys) and split over the waves by keys and row tiles; each wave puts
-// its rows' maxima and then its weights into LDS, and the product with the
-// values is split over the waves by value columns, so a tile's elements are
-// read from LDS once for each product and the output (16 RT x dl, fp32) is
-// spread over the waves' registers.
+// A workgroup takes 16 RT query rows of one sequence and walks key tiles of BN
+// rows through LDS.  The scores of a tile are formed transposed (rows = keys)
+// and split over the waves by row tiles and keys; each wave puts its weights
+// into LDS, and the product with the values is split over the waves by value
+// columns, so that the output (16 RT x dl, fp32) is spread over the waves'
+// registers.
 //
 // The work of a batch (row tiles x key tiles of every sequence, in order) is
-// cut into equal runs, one for each of 256 workgroups, whatever the lengths: a
-// run may end inside a row tile, whose partial results a second kernel
-// joins.  The cut depends on the lengths only, so results are reproducible.
+// cut into equal runs, one for each workgroup, whatever the lengths: a run may
+// end inside a row tile, whose partial results a second kernel joins.  The cut
+// depends on the lengths only, so results are reproducible.
 #include "latent_common.h"
 
 namespace kda {
 
-constexpr int DEC_GRID = 256;    // one workgroup per CU (its LDS tiles take the CU)
-constexpr int DEC_WAVES = 8;
-
-template <typename E> constexpr int DEC_BN = 128 / (int)sizeof(E);   // keys per tile
+// Shape of a workgroup: RT row tiles of 16, NW waves with RQ row tiles each in
+// the scores, BN keys a tile, GRID workgroups in a launch (the LDS tiles fill a
+// CU with GRID / 256 of them).
+template <int RT_, int NW_, int RQ_, int BN_, int GRID_> struct DecodeShape {
+    static constexpr int RT = RT_, NW = NW_, RQ = RQ_, BN = BN_, GRID = GRID_, BM = 16 * RT_;
+    static constexpr int WAVES_PER_SIMD = NW_ * (GRID_ / 256) / 4;
+};
+// bf16, up to 32 rows a sequence: the cache's bytes are the bound; two
+// workgroups a CU, so that one's loads run under the other's products.
+typedef DecodeShape<2, 4, 1, 32, 512> DecodeFew;
+// bf16, more rows: 64 of them, so that a cached row is fetched half as often.
+// The products are the bound, and LDS next to them: one wave a SIMD has the
+// registers to hold 32 query rows, so that a key operand read from LDS serves
+// two products (8 waves of 16 rows each: 698 us for 16 x 128 new tokens).
+typedef DecodeShape<4, 8, 1, 64, 256> DecodeMany;
+typedef DecodeShape<2, 8, 1, 32, 256> DecodeFewF32;
+typedef DecodeShape<4, 8, 1, 32, 256> DecodeManyF32;
 
 // A row tile whose keys several workgroups share: its output rows and the
-// workgroups [first, last] that hold its partial results.
+// runs [first, last] that hold its partial results.
 struct DecodeSplit {
     int64_t row;       // first output row (token * H + head)
     int32_t rows;      // 0: nothing to join
     int32_t first, last, pad;
 };
 
-// Workspace: splits, then the partials' (m, l) pairs, then their outputs; a
-// workgroup has two slots of partials: 2b for a row tile begun by an earlier
-// workgroup, 2b + 1 for one that a later workgroup goes on with.
+// Workspace: splits, then the partials' (m, l) pairs, then their outputs; run b
+// has two slots of partials: 2b for a row tile begun in an earlier run, 2b + 1
+// for one that a later run goes on with.
 struct DecodeSpace {
-    DecodeSplit* split;   // [DEC_GRID]
-    float* ml;            // [2 DEC_GRID][rows][2]
-    float* o;             // [2 DEC_GRID][rows][dl]
+    DecodeSplit* split;   // [GRID]
+    float* ml;            // [2 GRID][BM][2]
+    float* o;             // [2 GRID][BM][dl]
 };
-static size_t space_bytes(int rows, int dl) {
-    return sizeof(DecodeSplit) * DEC_GRID + (size_t)2 * DEC_GRID * rows * (2 + dl) * 4;
+template <typename S> static size_t space_bytes(int dl) {
+    return sizeof(DecodeSplit) * S::GRID + (size_t)2 * S::GRID * S::BM * (2 + dl) * 4;
 }
-static DecodeSpace space_of(void* ws, int rows) {
+template <typename S> static DecodeSpace space_of(void* ws) {
     DecodeSpace s;
     s.split = reinterpret_cast<DecodeSplit*>(ws);
-    s.ml = reinterpret_cast<float*>(s.split + DEC_GRID);
-    s.o = s.ml + (size_t)2 * DEC_GRID * rows * 2;
+    s.ml = reinterpret_cast<float*>(s.split + S::GRID);
+    s.o = s.ml + (size_t)2 * S::GRID * S::BM * 2;
     return s;
 }
 
@@ -72,34 +84,37 @@ __device__ __forceinline__ void sequence_work(const LatentDecode& a, int rows_q,
 }
 
 // by_tile: split entries are indexed by row tile (their number is at most
-// DEC_GRID), otherwise by the workgroup that begins the row tile.
-template <typename E, int DL, int DR, int RT>
-__global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const LatentDecode a, DecodeSpace ws,
-                                                                       int by_tile, int entries)
+// GRID), otherwise by the run that begins the row tile.
+template <typename E, int DL, int DR, typename Shape>
+__global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_decode_kernel(const LatentDecode a, DecodeSpace ws,
+                                                                          int by_tile, int entries)
 {
-    constexpr int W = DL + DR, BN = DEC_BN<E>, BM = 16 * RT, NT = 64 * DEC_WAVES;
-    constexpr int TT = BN / 16, KS = W / 32;
-    constexpr int TG = DEC_WAVES / RT < TT ? DEC_WAVES / RT : TT;       // a wave's scores: one row tile of RT,
-    constexpr int TW = TT / TG;                                         // TW key tiles (key group of TG)
-    constexpr int CT = DL / 16 / DEC_WAVES;                             // 16-column value tiles of a wave
-    constexpr int PS = BN + 16 / (int)sizeof(E);                        // row stride of the weights
-    constexpr bool QREG = sizeof(E) == 2;   // query rows in registers; fp32 rows would fill them
+    constexpr int RT = Shape::RT, NW = Shape::NW, BN = Shape::BN, BM = Shape::BM, GRID = Shape::GRID;
+    constexpr int W = DL + DR, NT = 64 * NW, TT = BN / 16, KS = W / 32;
+    constexpr int RQ = Shape::RQ, RG = RT / RQ;        // a wave's scores: RQ row tiles (row group of RG),
+    constexpr int TG = NW / RG < TT ? NW / RG : TT;    // TW key tiles (key group of TG)
+    constexpr int TW = TT / TG;
+    constexpr int CT = DL / 16 / NW;                   // 16-column value tiles of a wave
+    constexpr int PS = BN + 16 / (int)sizeof(E);       // row stride of the weights
+    constexpr bool QREG = sizeof(E) == 2;              // query rows in registers; fp32 rows would fill them
     typedef typename Vec<E>::v8 v8;
     typedef typename Vec<E>::v4 v4;
     typedef int i32x4 __attribute__((ext_vector_type(4)));
     __shared__ __attribute__((aligned(16))) E tilebuf[2][BN * W];
     __shared__ __attribute__((aligned(16))) E sp[BM * PS];
     __shared__ __attribute__((aligned(16))) float stat[TG][BM];
-    __shared__ __attribute__((aligned(16))) int ridx[4][BN];            // cache rows of the tiles' keys, -1: none
+    __shared__ __attribute__((aligned(16))) int ridx[4][BN];   // cache rows of the tiles' keys, -1: none
+    __shared__ int gaps[4];                                    // whether a tile has keys without a row
+    __shared__ int grown[4];                                   // whether a tile raised a row's maximum
     __shared__ int64_t found[4];
-    __shared__ int64_t wsum[DEC_WAVES][2];
+    __shared__ int64_t wsum[NW][2];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
     const int rows_q = (int)(a.total_tokens / a.num_seqs);
     const float sc = a.scale * LOG2E;
     // Workgroups go round robin over the 8 XCDs: neighbouring runs, which read
     // the same sequence's keys, go to one XCD and its L2.
-    const int run = (blockIdx.x & 7) * (DEC_GRID / 8) + (blockIdx.x >> 3);
+    const int run = (blockIdx.x & 7) * (GRID / 8) + (blockIdx.x >> 3);
 
     // this workgroup's run of the batch's work: the sum over the sequences,
     // then the sequence its run begins in
@@ -123,12 +138,12 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
     int64_t base = 0, ubase = 0;
     total = units = 0;
 #pragma unroll
-    for (int w = 0; w < DEC_WAVES; ++w) {
+    for (int w = 0; w < NW; ++w) {
         if (w < wave) base += wsum[w][0], ubase += wsum[w][1];
         total += wsum[w][0], units += wsum[w][1];
     }
     total = uniform(total);
-    const int64_t per = (total + DEC_GRID - 1) / DEC_GRID;
+    const int64_t per = (total + GRID - 1) / GRID;
     const int64_t begin = per * run, stop = min(total, begin + per);
     if (!by_tile) {
         if (tid == 0) ws.split[run].rows = 0;
@@ -162,7 +177,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
             __syncthreads();
             int64_t b = before, ub = ubefore;
 #pragma unroll
-            for (int w = 0; w < DEC_WAVES; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 if (w < wave) b += wsum[w][0], ub += wsum[w][1];
                 before += wsum[w][0], ubefore += wsum[w][1];
             }
@@ -175,7 +190,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
     int seq = (int)uniform(found[0]);
     int64_t seq_base = uniform(found[1]), unit_base = uniform(found[2]);
 
-    const int rt = wave % RT, tg = wave / RT;      // row tile and key group of this wave's scores
+    const int rg = wave % RG, tg = wave / RG;      // row and key group of this wave's scores
     const bool scores = tg < TG;
     const E* cache = (const E*)a.cache;
     Stage<E, W, BN, NT> st;
@@ -211,34 +226,21 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
         auto row_of = [&](int k) {                                   // of the tile t0 + k
             return [&, k](int r) {
                 const int row = ridx[k & 3][r];
-                return row < 0 ? nullptr : cache + (int64_t)row * W;
+                return row < 0 ? zero_row<E>() : cache + (int64_t)row * W;
             };
         };
+        auto keep_row = [&](int k, int row) {                        // tid < BN
+            ridx[k & 3][tid] = row;
+            const bool gap = __any(row < 0);
+            if (tid == 0) gaps[k & 3] = gap;
+        };
         if (tid < BN) {
-            ridx[0][tid] = cache_row(t0);
-            ridx[1][tid] = cache_row(t0 + 1);
-            ridx[2][tid] = cache_row(t0 + 2);
+            const int r0 = cache_row(t0), r1 = cache_row(t0 + 1), r2 = cache_row(t0 + 2);
+            keep_row(0, r0);
+            keep_row(1, r1);
+            keep_row(2, r2);
         }
-        v8 q[QREG ? KS : 1];
-        const E* qp;
-        int last;                                                    // last key this lane's row sees
-        {
-            const int64_t row = row0 + min(nrows - 1, 16 * rt + col);
-            const int i = (int)(row / a.H), h = (int)(row - (int64_t)i * a.H);
-            qp = (const E*)a.q + (int64_t)(q0 + i) * a.q_token_stride + h * a.q_head_stride;
-            last = len - n + i;
-            if (QREG && scores)
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) q[ks] = row_frag_global(qp, ks, lane);
-        }
-        f32x4 acc[RT][CT];
-        float m[RT], l = 0.f;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            m[r] = neg_inf();
-#pragma unroll
-            for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
+        if (tid < 4) grown[tid] = 0;
         __syncthreads();
         int next_row = -1;
         if (t0 < te) {
@@ -248,24 +250,79 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
             if (tid < BN) next_row = cache_row(t0 + 3);
             first.store(tid, tilebuf[0]);
         }
+        v8 q[RQ][QREG ? KS : 1];
+        const E* qp[RQ];
+        int last[RQ];                                                // last key this lane's rows see
+        const int first_last = len - n + (int)(row0 / a.H);          // and the tile's first row
+#pragma unroll
+        for (int j = 0; j < RQ; ++j) {
+            const int64_t row = row0 + min(nrows - 1, 16 * (rg * RQ + j) + col);
+            const int i = (int)(row / a.H), h = (int)(row - (int64_t)i * a.H);
+            qp[j] = (const E*)a.q + (int64_t)(q0 + i) * a.q_token_stride + h * a.q_head_stride;
+            last[j] = len - n + i;
+            if (QREG && scores)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(qp[j], ks, lane);
+        }
+        f32x4 acc[RT][CT];
+        float m[RT], own[RQ], l[RQ];                                 // own: the maxima of this wave's row tiles
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            m[r] = neg_inf();
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int j = 0; j < RQ; ++j) own[j] = neg_inf(), l[j] = 0.f;
         __syncthreads();
         for (int t = t0, k = 0; t < te; ++t, ++k) {
             const E* tile = tilebuf[k & 1];
-            const int* rows = ridx[k & 3];
-            f32x4 s[TW];
-            if (scores) {
-                const E* qt = qp;
-                if (!QREG) asm volatile("" : "+v"(qt));   // fetched again for every tile
+            f32x4 s[RQ][TW];
+            v4 p[RQ][TW];
+            float part[RQ];
+            auto weigh = [&]() {
 #pragma unroll
-                for (int w = 0; w < TW; ++w) s[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < RQ; ++j) {
+                    const float from = own[j] == neg_inf() ? 0.f : own[j];   // a row that has seen no key yet
+                    part[j] = 0.f;
+#pragma unroll
+                    for (int w = 0; w < TW; ++w)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = exp2_fast(__builtin_fmaf(s[j][w][i], sc, -from));
+                            part[j] += x;                // the sum takes the weights before their rounding
+                            p[j][w][i] = from_f32<E>(x); // bf16: the product's operand type
+                        }
+                }
+            };
+            auto put_weights = [&]() {
+#pragma unroll
+                for (int j = 0; j < RQ; ++j)
+#pragma unroll
+                    for (int w = 0; w < TW; ++w)
+                        store_vec(sp + (16 * (rg * RQ + j) + col) * PS + 16 * (tg * TW + w) + 4 * g, p[j][w]);
+            };
+#pragma unroll
+            for (int j = 0; j < RQ; ++j) part[j] = 0.f;
+            if (scores) {
+                const E* qt[RQ];
+#pragma unroll
+                for (int j = 0; j < RQ; ++j) {
+                    qt[j] = qp[j];
+                    if (!QREG) asm volatile("" : "+v"(qt[j]));   // fetched again for every tile
+#pragma unroll
+                    for (int w = 0; w < TW; ++w) s[j][w] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
                 // the keys' operands are read a group ahead of their products
-                constexpr int GK = KS % 6 == 0 ? 3 : KS % 4 == 0 ? 4 : 5, NG = KS / GK;
+                constexpr int GK = TW * RQ > 1 || !QREG ? 2 : KS % 6 == 0 ? 3 : KS % 4 == 0 ? 4 : 5, NG = KS / GK;
                 static_assert(KS % GK == 0, "whole groups");
-                v8 x[2][GK][TW], y[2][QREG ? 1 : GK];
+                v8 x[2][GK][TW], y[2][QREG ? 1 : GK][RQ];
                 auto fetch = [&](int gr) {
 #pragma unroll
                     for (int i = 0; i < GK; ++i) {
-                        if constexpr (!QREG) y[gr & 1][i] = row_frag_global(qt, gr * GK + i, lane);
+                        if constexpr (!QREG)
+#pragma unroll
+                            for (int j = 0; j < RQ; ++j) y[gr & 1][i][j] = row_frag_global(qt[j], gr * GK + i, lane);
 #pragma unroll
                         for (int w = 0; w < TW; ++w) x[gr & 1][i][w] = k_rows(tile, 16 * TW * tg + 16 * w, gr * GK + i);
                     }
@@ -278,96 +335,108 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void latent_decode_kernel(const Lat
 #pragma unroll
                     for (int i = 0; i < GK; ++i)
 #pragma unroll
-                        for (int w = 0; w < TW; ++w) {
-                            if constexpr (QREG) s[w] = mma32(x[gr & 1][i][w], q[gr * GK + i], s[w]);
-                            else s[w] = mma32(x[gr & 1][i][w], y[gr & 1][i], s[w]);
-                        }
+                        for (int w = 0; w < TW; ++w)
+#pragma unroll
+                            for (int j = 0; j < RQ; ++j) {
+                                if constexpr (QREG) s[j][w] = mma32(x[gr & 1][i][w], q[j][gr * GK + i], s[j][w]);
+                                else s[j][w] = mma32(x[gr & 1][i][w], y[gr & 1][i][j], s[j][w]);
+                            }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                float top = neg_inf();
+                if (uniform(gaps[k & 3]) || (t + 1) * BN - 1 > first_last) {
 #pragma unroll
-                for (int w = 0; w < TW; ++w) {
-                    const int k0 = 16 * (tg * TW + w) + 4 * g;
-                    const i32x4 there = *reinterpret_cast<const i32x4*>(rows + k0);
+                    for (int w = 0; w < TW; ++w) {
+                        const int k0 = 16 * (tg * TW + w) + 4 * g;
+                        const i32x4 there = *reinterpret_cast<const i32x4*>(ridx[k & 3] + k0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (there[i] < 0 || t * BN + k0 + i > last) s[w][i] = neg_inf();
-                        top = fmaxf(top, s[w][i]);
+                        for (int j = 0; j < RQ; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (there[i] < 0 || t * BN + k0 + i > last[j]) s[j][w][i] = neg_inf();
                     }
                 }
-                top = group_max(top) * sc;
-                if (g == 0) stat[tg][16 * rt + col] = top;
+                bool grew = false;
+#pragma unroll
+                for (int j = 0; j < RQ; ++j) {
+                    float top = neg_inf();
+#pragma unroll
+                    for (int w = 0; w < TW; ++w)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][w][i]);
+                    top = group_max(top) * sc;
+                    if (g == 0) stat[tg][16 * (rg * RQ + j) + col] = top;
+                    grew |= top > own[j] + 8.f;
+                }
+                if (__any(grew) && lane == 0) grown[k & 3] = 1;
+                weigh();
             }
-            __syncthreads();   // maxima written; the other buffer's last readers are done
+            __syncthreads();   // maxima are there; the other buffer's and the weights' last readers are done
+            if (scores) put_weights();
             if (tid < BN) {
-                ridx[(k + 3) & 3][tid] = next_row;
+                keep_row(k + 3, next_row);
                 next_row = cache_row(t + 4);
             }
+            if (tid == 0) grown[(k + 2) & 3] = 0;
             if (t + 1 < te) st.store_load(tid, tilebuf[(k + 1) & 1], row_of(k + 2));
-            // the running maximum, raised only when it grew by more than 8 (in
-            // powers of two); every wave takes the same decision for a row
+            // The weights are taken against the rows' running maxima as they
+            // stand.  Only when a row's grew by more than 8 (in powers of two;
+            // the first tile always) are the maxima raised, by every wave alike,
+            // the sums rescaled and this tile's weights taken again.
+            if (uniform(grown[k & 3])) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                float top = stat[0][16 * r + col];
+                for (int r = 0; r < RT; ++r) {
+                    float top = stat[0][16 * r + col];
 #pragma unroll
-                for (int w = 1; w < TG; ++w) top = fmaxf(top, stat[w][16 * r + col]);
-                const bool grew = top > m[r] + 8.f;
-                if (__any(grew)) {
-                    const float mn = grew ? top : m[r];
-                    const float f = grew ? exp2_fast(m[r] - mn) : 1.f;
-                    m[r] = mn;
+                    for (int w = 1; w < TG; ++w) top = fmaxf(top, stat[w][16 * r + col]);
+                    const bool grew = top > m[r] + 8.f;
+                    const float f = grew ? exp2_fast(m[r] - top) : 1.f;
+                    m[r] = grew ? top : m[r];
 #pragma unroll
                     for (int c = 0; c < CT; ++c) acc[r][c] *= f;
-                    if (r == rt) l *= f;
+                    if (r / RQ == rg) l[r % RQ] *= f, own[r % RQ] = m[r];
+                }
+                if (scores) {
+                    weigh();
+                    put_weights();
                 }
             }
-            if (scores) {
-                float from = m[0];
 #pragma unroll
-                for (int r = 1; r < RT; ++r) from = r == rt ? m[r] : from;
-                if (from == neg_inf()) from = 0.f;   // a row that has seen no key yet
-#pragma unroll
-                for (int w = 0; w < TW; ++w) {
-                    v4 p;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = exp2_fast(__builtin_fmaf(s[w][i], sc, -from));
-                        l += x;                // the sum takes the weights before their rounding
-                        p[i] = from_f32<E>(x); // bf16: the product's operand type
-                    }
-                    store_vec(sp + (16 * rt + col) * PS + 16 * (tg * TW + w) + 4 * g, p);
-                }
-            }
+            for (int j = 0; j < RQ; ++j) l[j] += part[j];
             __syncthreads();   // weights and the next tile are there
-            // the values' operands are read one product ahead
-            v8 p[2][RT], x[2];
+            // the values' operands are read PD products of RT tiles ahead
+            constexpr int PD = Shape::WAVES_PER_SIMD == 1 ? 3 : 1, NE = TT / 2 * CT;
+            v8 pw[TT / 2][RT], x[PD + 1];
+            auto values = [&](int e) { x[e % (PD + 1)] = c_cols(tile, 32 * (e / CT), 32 * (e / CT) + 16, e % CT); };
             auto weights = [&](int b) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     const E* at = sp + (16 * r + col) * PS + 32 * b + 4 * g;
                     const v4 lo = load_vec<v4>(at), hi = load_vec<v4>(at + 16);
-                    p[b & 1][r] = v8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                    pw[b][r] = v8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
                 }
             };
             weights(0);
-            x[0] = c_cols(tile, 0, 16, 0);
 #pragma unroll
-            for (int e = 0; e < TT / 2 * CT; ++e) {
-                const int b = e / CT, c = e % CT, f = e + 1;
-                if (f < TT / 2 * CT) x[f & 1] = c_cols(tile, 32 * (f / CT), 32 * (f / CT) + 16, f % CT);
-                if (c == CT - 1 && b + 1 < TT / 2) weights(b + 1);
+            for (int e = 0; e < PD; ++e) values(e);
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                const int b = e / CT, c = e % CT;
+                if (e + PD < NE) values(e + PD);
+                if (c == CT - 1 - (PD > 1) && b + 1 < TT / 2) weights(b + 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r][c] = mma32(x[e & 1], p[b & 1][r], acc[r][c]);
+                for (int r = 0; r < RT; ++r) acc[r][c] = mma32(x[e % (PD + 1)], pw[b][r], acc[r][c]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
         // the rows' sums over the waves
         __syncthreads();
-        if (scores) {
-            const float x = group_sum(l);
-            if (g == 0) stat[tg][16 * rt + col] = x;
-        }
+        if (scores)
+#pragma unroll
+            for (int j = 0; j < RQ; ++j) {
+                const float x = group_sum(l[j]);
+                if (g == 0) stat[tg][16 * (rg * RQ + j) + col] = x;
+            }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == key_tiles;
         const int64_t out0 = (int64_t)q0 * a.H + row0;
@@ -470,28 +539,34 @@ template <typename E, int DL>
 __global__ __launch_bounds__(256) void latent_join_parts_kernel(const DecodeSpace ws, E* __restrict__ o,
                                                                 float* __restrict__ lse, int BM)
 {
-    __shared__ float factor[DEC_GRID];
+    __shared__ float factor[512];
     __shared__ float red[4][2];
     __shared__ __attribute__((aligned(16))) f32x4 part[16][16];
     const DecodeSplit x = ws.split[blockIdx.x];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, row = blockIdx.y;
     if (row >= x.rows) return;
-    const int parts = x.last - x.first + 1;   // at most DEC_GRID, one per workgroup
+    const int parts = x.last - x.first + 1;   // at most one per run
     auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * x.first + 1 : 2 * (x.first + p)) * BM + row; };
-    float m = neg_inf(), l = 0.f;
-    if (tid < parts) {
-        m = ws.ml[slot(tid) * 2];
-        l = ws.ml[slot(tid) * 2 + 1];
+    float m[2], l[2], top = neg_inf();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int p = tid + 256 * i;
+        m[i] = p < parts ? ws.ml[slot(p) * 2] : neg_inf();
+        l[i] = p < parts ? ws.ml[slot(p) * 2 + 1] : 0.f;
+        top = fmaxf(top, m[i]);
     }
-    float top = m;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
     if (lane == 0) red[wave][0] = top;
     __syncthreads();
     top = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-    const float f = m == neg_inf() ? 0.f : exp2_fast(m - top);
-    factor[tid] = f;
-    float sum = f * l;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float f = m[i] == neg_inf() ? 0.f : exp2_fast(m[i] - top);
+        factor[tid + 256 * i] = f;
+        sum += f * l[i];
+    }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
     if (lane == 0) red[wave][1] = sum;
@@ -513,42 +588,44 @@ __global__ __launch_bounds__(256) void latent_join_parts_kernel(const DecodeSpac
     store_vec(o + (x.row + row) * DL + c, y);
     if (lse && tid == 0 && blockIdx.z == 0) lse[x.row + row] = sum == 0.f ? neg_inf() : (top + __log2f(sum)) * LN2;
 }
-static_assert(DEC_GRID <= 256, "a thread per part");
+static_assert(DecodeFew::GRID <= 512 && DecodeMany::GRID <= 512, "two parts a thread");
 
-// Row tiles of 32 rows where a sequence's rows fit in one (a tile of 64 would
-// be half empty), else of 64 (each cached row is then fetched half as often).
-static int row_tile(int64_t total_tokens, int32_t N, int32_t H) {
-    return (total_tokens + N - 1) / N * H <= 32 ? 2 : 4;
+// Whether the rows of a sequence fit in a tile of 32 (in one of 64 more than
+// half would be empty).
+static bool few_rows(int64_t total_tokens, int32_t N, int32_t H) { return (total_tokens + N - 1) / N * H <= 32; }
+
+size_t latent_decode_workspace(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t dl, bool bf16_io) {
+    const bool few = few_rows(total_tokens, num_seqs, H);
+    if (bf16_io) return few ? space_bytes<DecodeFew>(dl) : space_bytes<DecodeMany>(dl);
+    return few ? space_bytes<DecodeFewF32>(dl) : space_bytes<DecodeManyF32>(dl);
 }
 
-size_t latent_decode_workspace(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t dl, bool) {
-    return space_bytes(16 * row_tile(total_tokens, num_seqs, H), dl);
-}
-
-template <typename E, int DL, int DR, int RT>
+template <typename E, int DL, int DR, typename S>
 static hipError_t launch(const LatentDecode& a, hipStream_t stream) {
-    constexpr int BM = 16 * RT;
-    const DecodeSpace ws = space_of(a.workspace, BM);
+    const DecodeSpace ws = space_of<S>(a.workspace);
     const int64_t rows = a.total_tokens * a.H;
-    const int64_t bound = a.cu_seqlens ? rows / BM + a.num_seqs
-                                       : (a.total_tokens / a.num_seqs * a.H + BM - 1) / BM * a.num_seqs;
-    const bool by_tile = bound <= DEC_GRID;
-    const int entries = by_tile ? (int)bound : DEC_GRID;
-    hipLaunchKernelGGL((latent_decode_kernel<E, DL, DR, RT>), dim3(DEC_GRID), dim3(64 * DEC_WAVES), 0, stream, a, ws,
+    const int64_t bound = a.cu_seqlens ? rows / S::BM + a.num_seqs
+                                       : (a.total_tokens / a.num_seqs * a.H + S::BM - 1) / S::BM * a.num_seqs;
+    const bool by_tile = bound <= S::GRID;
+    const int entries = by_tile ? (int)bound : S::GRID;
+    hipLaunchKernelGGL((latent_decode_kernel<E, DL, DR, S>), dim3(S::GRID), dim3(64 * S::NW), 0, stream, a, ws,
                        by_tile ? 1 : 0, entries);
     if (entries <= 32)   // 8 parts a row tile and more
-        hipLaunchKernelGGL((latent_join_parts_kernel<E, DL>), dim3(entries, BM, DL / 64), dim3(256), 0, stream, ws,
-                           (E*)a.o, a.lse, BM);
+        hipLaunchKernelGGL((latent_join_parts_kernel<E, DL>), dim3(entries, S::BM, DL / 64), dim3(256), 0, stream, ws,
+                           (E*)a.o, a.lse, S::BM);
     else
-        hipLaunchKernelGGL((latent_join_rows_kernel<E, DL>), dim3(entries, BM / 4), dim3(256), 0, stream, ws, (E*)a.o,
-                           a.lse, BM);
+        hipLaunchKernelGGL((latent_join_rows_kernel<E, DL>), dim3(entries, S::BM / 4), dim3(256), 0, stream, ws,
+                           (E*)a.o, a.lse, S::BM);
     return hipGetLastError();
 }
 
 template <typename E, int DL, int DR>
 static hipError_t launch_rows(const LatentDecode& a, hipStream_t stream) {
-    return row_tile(a.total_tokens, a.num_seqs, a.H) == 2 ? launch<E, DL, DR, 2>(a, stream)
-                                                          : launch<E, DL, DR, 4>(a, stream);
+    const bool few = few_rows(a.total_tokens, a.num_seqs, a.H);
+    if constexpr (sizeof(E) == 2)
+        return few ? launch<E, DL, DR, DecodeFew>(a, stream) : launch<E, DL, DR, DecodeMany>(a, stream);
+    else
+        return few ? launch<E, DL, DR, DecodeFewF32>(a, stream) : launch<E, DL, DR, DecodeManyF32>(a, stream);
 }
 
 hipError_t launch_latent_decode(const LatentDecode& a, bool bf16_io, hipStream_t stream) {
