@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     const kda_latent_inputs in, E* __restrict__ o, float* __restrict__ lse, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BN = 128 / (int)sizeof(E), NQ = LATENT_NQ<E>, BQ = 64 * NQ;
-    constexpr int KS = DQK / 32, TT = BN / 16;
+    constexpr int KS = DQK / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
 
@@ -92,17 +92,19 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
         if (t + 1 < nt) load(t + 1);
         if (t * BN < wave_end) {
             f32x4 s[NQ][TT];
+            v8 x[PD + 1];
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
+            for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) s[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            // two key tiles by turns, so that products in a row do not wait for each other
+            ahead<TT * KS, PD>([&](int e) { x[e % (PD + 1)] = k_rows(K, 16 * (e / (2 * KS) * 2 + e % 2), e / 2 % KS); },
+                               [&](int e) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const v8 a = k_rows(K, 16 * tt, ks);
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) s[j][tt] = mma32(a, q[j][ks], s[j][tt]);
-                }
-            }
+                                   for (int j = 0; j < NQ; ++j)
+                                       s[j][e / (2 * KS) * 2 + e % 2] =
+                                           mma32(x[e % (PD + 1)], q[j][e / 2 % KS], s[j][e / (2 * KS) * 2 + e % 2]);
+                               });
             if ((t + 1) * BN > wave_full) {
 #pragma unroll
                 for (int j = 0; j < NQ; ++j)
@@ -152,14 +154,13 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
 #pragma unroll
                 for (int b = 0; b < TT / 2; ++b) p[j][b] = acc_frag(s[j][2 * b], s[j][2 * b + 1], E());
             }
+            ahead<DV / 16 * (TT / 2), PD>(
+                [&](int e) { x[e % (PD + 1)] = v_cols(V, 32 * (e / (DV / 16)), 32 * (e / (DV / 16)) + 16, e % (DV / 16)); },
+                [&](int e) {
 #pragma unroll
-            for (int c = 0; c < DV / 16; ++c)
-#pragma unroll
-                for (int b = 0; b < TT / 2; ++b) {
-                    const v8 a = v_cols(V, 32 * b, 32 * b + 16, c);
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(a, p[j][b], acc[j][c]);
-                }
+                    for (int j = 0; j < NQ; ++j)
+                        acc[j][e % (DV / 16)] = mma32(x[e % (PD + 1)], p[j][e / (DV / 16)], acc[j][e % (DV / 16)]);
+                });
         }
         if (t + 1 < nt) {
             E* next = smem[(t + 1) & 1];

@@ -16,6 +16,14 @@
 
 namespace kda {
 
+// Key tiles of a wave of the dk, dv kernel and its waves per SIMD.
+#ifndef XNK
+#define XNK 1
+#define XWV 2
+#endif
+template <typename E> constexpr int DKV_NK = sizeof(E) == 2 ? XNK : 1;
+template <typename E> constexpr int DKV_WAVES = sizeof(E) == 2 ? XWV : 2;
+
 // dq and delta.  As in the forward kernel the scores are formed transposed
 // (rows = keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.
 template <typename E, int DN, int DR>
@@ -24,7 +32,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ delta, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BN = 32, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
-    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16;
+    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
 
@@ -103,23 +111,23 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         if (t + 1 < nt) load(t + 1);
         if (t * BN < wave_end) {
             f32x4 s[NQ][TT], dp[NQ][TT];
+            v8 x[PD + 1];
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
+            for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) s[j][tt] = dp[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            ahead<TT * (KS + VS), PD>(
+                [&](int e) {
+                    x[e % (PD + 1)] = e / TT < KS ? k_rows(K, 16 * (e % TT), e / TT) : v_rows(V, 16 * (e % TT), e / TT - KS);
+                },
+                [&](int e) {
+                    const int tt = e % TT, ks = e / TT;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const v8 a = k_rows(K, 16 * tt, ks);
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) s[j][tt] = mma32(a, q[j][ks], s[j][tt]);
-                }
-#pragma unroll
-                for (int vs = 0; vs < VS; ++vs) {
-                    const v8 a = v_rows(V, 16 * tt, vs);
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) dp[j][tt] = mma32(a, go[j][vs], dp[j][tt]);
-                }
-            }
+                    for (int j = 0; j < NQ; ++j) {
+                        if (ks < KS) s[j][tt] = mma32(x[e % (PD + 1)], q[j][ks < KS ? ks : 0], s[j][tt]);
+                        else dp[j][tt] = mma32(x[e % (PD + 1)], go[j][ks < KS ? 0 : ks - KS], dp[j][tt]);
+                    }
+                });
             const bool masked = (t + 1) * BN > wave_full;
             v8 dz[NQ];
 #pragma unroll
@@ -135,12 +143,11 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                     }
                 dz[j] = acc_frag(s[j][0], s[j][1], E());
             }
+            ahead<DQK / 16, PD>([&](int c) { x[c % (PD + 1)] = k_cols(K, 0, 16, c); },
+                                [&](int c) {
 #pragma unroll
-            for (int c = 0; c < DQK / 16; ++c) {
-                const v8 a = k_cols(K, 0, 16, c);
-#pragma unroll
-                for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(a, dz[j], acc[j][c]);
-            }
+                                    for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[c % (PD + 1)], dz[j], acc[j][c]);
+                                });
         }
         if (t + 1 < nt) {
             E* next = smem[(t + 1) & 1];
@@ -166,18 +173,18 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     }
 }
 
-// dk, dv and the head's part of dk_pe.  A wave owns 16 keys, whose k and v
+// dk, dv and the head's part of dk_pe.  A wave owns 16 NK keys, whose k and v
 // operands and gradients stay in registers; the query rows come 32 at a time.
 // The scores are formed with rows = queries, so that the weights and dz are the
 // operands of dv^T += g^T w and dk^T += q^T dz as they stand.
 template <typename E, int DN, int DR>
-__global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
+__global__ __launch_bounds__(256, DKV_WAVES<E>) void latent_dkv_kernel(
     const kda_latent_inputs in, const float* __restrict__ lse, const E* __restrict__ d_o,
     const float* __restrict__ delta, E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
     E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ pe_part, int tiles)
 {
-    constexpr int DQK = DN + DR, DV = DN, BQ = 32;
-    constexpr int KS = DQK / 32, VS = DV / 32;
+    constexpr int DQK = DN + DR, DV = DN, BQ = 32, NK = DKV_NK<E>, BK = 64 * NK;
+    constexpr int KS = DQK / 32, VS = DV / 32, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BQ * (DQK + DV)];
     __shared__ __attribute__((aligned(16))) float srow[2][2 * BQ];   // lse (base 2), then delta
@@ -186,28 +193,29 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
     head_tile_of_block(in.H, tiles, h, want);
     const int32_t* cu_k = in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
     const int rows_k = (int)(in.total_k / in.num_seqs);
-    if (!find_tile<LATENT_BK, 256>(cu_k, in.num_seqs, rows_k, (int)in.total_k, want,
-                                   reinterpret_cast<int*>(&smem[0][0]), seq, tile))
+    if (!find_tile<BK, 256>(cu_k, in.num_seqs, rows_k, (int)in.total_k, want, reinterpret_cast<int*>(&smem[0][0]), seq,
+                            tile))
         return;
     int q0, q1, k0, k1;
     sequence_rows(in.cu_seqlens_q, (int)(in.total_q / in.num_seqs), (int)in.total_q, seq, q0, q1);
     sequence_rows(cu_k, rows_k, (int)in.total_k, seq, k0, k1);
     const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
-    const int key0 = tile * LATENT_BK, wkey = key0 + 16 * wave, key = wkey + col;
+    const int key0 = tile * BK, wkey = key0 + 16 * NK * wave;
     const float sc = in.scale * LOG2E;
 
-    v8 k[KS], v[VS];
-    {
-        const int64_t row = k0 + min(key, nk - 1);
+    v8 k[NK][KS], v[NK][VS];
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+        const int64_t row = k0 + min(wkey + 16 * n + col, nk - 1);
         const E* kp = (const E*)in.k + row * in.k_token_stride + h * in.k_head_stride;
         const E* vp = (const E*)in.v + row * in.v_token_stride + h * in.v_head_stride;
         const E* pp = DR ? (const E*)in.k_pe + row * in.k_pe_token_stride : nullptr;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-            k[ks] = 32 * ks < DN ? row_frag_global(kp, ks, lane) : row_frag_global(pp, ks - DN / 32, lane);
+            k[n][ks] = 32 * ks < DN ? row_frag_global(kp, ks, lane) : row_frag_global(pp, ks - DN / 32, lane);
 #pragma unroll
-        for (int vs = 0; vs < VS; ++vs) v[vs] = row_frag_global(vp, vs, lane);
+        for (int vs = 0; vs < VS; ++vs) v[n][vs] = row_frag_global(vp, vs, lane);
     }
     const int nt = (nq + BQ - 1) / BQ;
     const int t0 = in.causal ? min(nt, max(0, key0 - off) / BQ) : 0;   // rows before it see none of the keys
@@ -237,11 +245,14 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
     const RowReader<E, DV> g_rows(lane);
     const ColReader<E, DQK, DQK / 16> q_cols(lane);
     const ColReader<E, DV, DV / 16> g_cols(lane);
-    f32x4 ak[DQK / 16], av[DV / 16];
+    f32x4 ak[NK][DQK / 16], av[NK][DV / 16];
 #pragma unroll
-    for (int c = 0; c < DQK / 16; ++c) ak[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < NK; ++n) {
 #pragma unroll
-    for (int c = 0; c < DV / 16; ++c) av[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < DQK / 16; ++c) ak[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) av[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     if (t0 < nt) {
         load(t0);
         store(t0 & 1);
@@ -253,51 +264,83 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
         const float* R = srow[t & 1];
         if (t + 1 < nt) load(t + 1);
         if (!in.causal || t * BQ + BQ - 1 + off >= wkey) {
-            f32x4 w[2], dz[2];
+            f32x4 s[NK][2], dp[NK][2];
+            v8 x[PD + 1];
+#pragma unroll
+            for (int n = 0; n < NK; ++n)
+#pragma unroll
+                for (int a = 0; a < 2; ++a) s[n][a] = dp[n][a] = f32x4{0.f, 0.f, 0.f, 0.f};
+            ahead<2 * (KS + VS), PD>(
+                [&](int e) {
+                    x[e % (PD + 1)] = e / 2 < KS ? q_rows(Q, 16 * (e % 2), e / 2) : g_rows(G, 16 * (e % 2), e / 2 - KS);
+                },
+                [&](int e) {
+                    const int a = e % 2, ks = e / 2;
+#pragma unroll
+                    for (int n = 0; n < NK; ++n) {
+                        if (ks < KS) s[n][a] = mma32(x[e % (PD + 1)], k[n][ks < KS ? ks : 0], s[n][a]);
+                        else dp[n][a] = mma32(x[e % (PD + 1)], v[n][ks < KS ? 0 : ks - KS], dp[n][a]);
+                    }
+                });
+            const bool masked = in.causal && t * BQ + off < wkey + 16 * NK - 1;   // some row sees not all of the keys
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-                f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) s = mma32(q_rows(Q, 16 * a, ks), k[ks], s);
-#pragma unroll
-                for (int vs = 0; vs < VS; ++vs) dp = mma32(g_rows(G, 16 * a, vs), v[vs], dp);
                 const f32x4 ls = *reinterpret_cast<const f32x4*>(R + 16 * a + 4 * g);
                 const f32x4 de = *reinterpret_cast<const f32x4*>(R + BQ + 16 * a + 4 * g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool hidden = in.causal && key > t * BQ + 16 * a + 4 * g + i + off;
-                    w[a][i] = hidden ? 0.f : exp2_fast(__builtin_fmaf(s[i], sc, -ls[i]));
-                    dz[a][i] = hidden ? 0.f : w[a][i] * (dp[i] - de[i]);
-                }
+                for (int n = 0; n < NK; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool hidden = masked && wkey + 16 * n + col > t * BQ + 16 * a + 4 * g + i + off;
+                        const float w = exp2_fast(__builtin_fmaf(s[n][a][i], sc, -ls[i]));
+                        const float z = w * (dp[n][a][i] - de[i]);
+                        s[n][a][i] = hidden ? 0.f : w;
+                        dp[n][a][i] = hidden ? 0.f : z;
+                    }
             }
-            const v8 wf = acc_frag(w[0], w[1], E()), zf = acc_frag(dz[0], dz[1], E());
+            v8 wf[NK], zf[NK];
 #pragma unroll
-            for (int c = 0; c < DV / 16; ++c) av[c] = mma32(g_cols(G, 0, 16, c), wf, av[c]);
+            for (int n = 0; n < NK; ++n) {
+                wf[n] = acc_frag(s[n][0], s[n][1], E());
+                zf[n] = acc_frag(dp[n][0], dp[n][1], E());
+            }
+            ahead<DV / 16 + DQK / 16, PD>(
+                [&](int c) { x[c % (PD + 1)] = c < DV / 16 ? g_cols(G, 0, 16, c) : q_cols(Q, 0, 16, c - DV / 16); },
+                [&](int c) {
+                    const int ck = c < DV / 16 ? 0 : c - DV / 16, cv = c < DV / 16 ? c : 0;
 #pragma unroll
-            for (int c = 0; c < DQK / 16; ++c) ak[c] = mma32(q_cols(Q, 0, 16, c), zf, ak[c]);
+                    for (int n = 0; n < NK; ++n) {
+                        if (c < DV / 16) av[n][cv] = mma32(x[c % (PD + 1)], wf[n], av[n][cv]);
+                        else ak[n][ck] = mma32(x[c % (PD + 1)], zf[n], ak[n][ck]);
+                    }
+                });
         }
         if (t + 1 < nt) store((t + 1) & 1);
         __syncthreads();
     }
-    if (key >= nk) return;
-    const int64_t row = k0 + key;
-    E* kr = dk + row * dk_token_stride + h * dk_head_stride;
-    E* vr = dv + row * dv_token_stride + h * dv_head_stride;
 #pragma unroll
-    for (int c = 0; c < DN / 16; ++c) {
-        typename Vec<E>::v4 x, y;
+    for (int n = 0; n < NK; ++n) {
+        const int key = wkey + 16 * n + col;
+        if (key >= nk) continue;
+        const int64_t row = k0 + key;
+        E* kr = dk + row * dk_token_stride + h * dk_head_stride;
+        E* vr = dv + row * dv_token_stride + h * dv_head_stride;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = from_f32<E>(ak[c][i] * in.scale);
-            y[i] = from_f32<E>(av[c][i]);
+        for (int c = 0; c < DN / 16; ++c) {
+            typename Vec<E>::v4 kx, vx;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                kx[i] = from_f32<E>(ak[n][c][i] * in.scale);
+                vx[i] = from_f32<E>(av[n][c][i]);
+            }
+            store_vec(kr + 16 * c + 4 * g, kx);
+            store_vec(vr + 16 * c + 4 * g, vx);
         }
-        store_vec(kr + 16 * c + 4 * g, x);
-        store_vec(vr + 16 * c + 4 * g, y);
-    }
-    if constexpr (DR > 0) {
-        float* pr = pe_part + (row * in.H + h) * DR;
+        if constexpr (DR > 0) {
+            float* pr = pe_part + (row * in.H + h) * DR;
 #pragma unroll
-        for (int c = 0; c < DR / 16; ++c) store_vec(pr + 16 * c + 4 * g, ak[DN / 16 + c] * in.scale);
+            for (int c = 0; c < DR / 16; ++c) store_vec(pr + 16 * c + 4 * g, ak[n][DN / 16 + c] * in.scale);
+        }
     }
 }
 
@@ -330,7 +373,7 @@ template <typename E, int DN, int DR>
 static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipStream_t stream) {
     const int64_t tq = tile_count(in.cu_seqlens_q, in.total_q, in.num_seqs, 64 * LATENT_NQ<E>);
     const int32_t* cu_k = in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
-    const int64_t tk = tile_count(cu_k, in.total_k, in.num_seqs, LATENT_BK);
+    const int64_t tk = tile_count(cu_k, in.total_k, in.num_seqs, 64 * DKV_NK<E>);
     if (tq > 0)
         hipLaunchKernelGGL((latent_dq_kernel<E, DN, DR>), dim3((unsigned)(tq * in.H)), dim3(256), 0, stream, in,
                            (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.delta, (int)tq);

@@ -10,13 +10,11 @@ namespace kda {
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Query rows of a wave in 16-row tiles (forward, dq), and keys of a workgroup
-// (dk, dv).  bf16: two tiles, so that an operand read from LDS serves two
+// Query rows of a wave in 16-row tiles (forward, dq).  bf16: two tiles, so that an operand read from LDS serves two
 // products.  fp32: one; its products take eight times as long, LDS is no bound,
 // and the smaller tiles spread a short batch over more CUs (130 tokens x 4
 // heads: 22 us with two tiles).
 template <typename E> constexpr int LATENT_NQ = sizeof(E) == 2 ? 2 : 1;
-constexpr int LATENT_BK = 64;
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -145,6 +143,22 @@ __device__ __forceinline__ bf16x8 row_frag_global(const bf16* row, int ks, int l
 }
 __device__ __forceinline__ f32x8 row_frag_global(const float* row, int ks, int lane) {
     return load_vec<f32x8, float>(row + 32 * ks + 8 * (lane >> 4));
+}
+
+// N steps use(e), each with an operand that fetch(e) reads from LDS D steps
+// ahead into a ring of D + 1: the compiler, short of registers, otherwise puts
+// every read right before its use and waits for it.
+template <int N, int D, typename F, typename U>
+__device__ __forceinline__ void ahead(F fetch, U use) {
+#pragma unroll
+    for (int e = 0; e < D && e < N; ++e) fetch(e);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (e + D < N) fetch(e + D);
+        __builtin_amdgcn_sched_barrier(0);
+        use(e);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // -- staging: global -> registers -> LDS ---------------------------------------
