@@ -64,6 +64,10 @@ kda_status check_inputs(const kda_latent_inputs* in) {
     for (int64_t s : strides)
         if (!stride_ok(s, in->dtype))
             return fail(KDA_ERR_INVALID_ARGUMENT, "strides must be >= 0 and multiples of 16 bytes");
+    const int64_t rows[] = {in->q_token_stride, in->k_token_stride, in->v_token_stride, in->k_pe_token_stride,
+                            (int64_t)in->H * in->dv};
+    for (int64_t s : rows)   // a tile's 64 rows are addressed with 32-bit offsets
+        if (s >= (int64_t)1 << 23) return fail(KDA_ERR_INVALID_ARGUMENT, "token strides must be below 2^23 elements");
     // every kernel's grid: tiles (at least 64 rows each, and one more per sequence) times heads
     const int64_t most = (in->total_q > in->total_k ? in->total_q : in->total_k) / 64 + in->num_seqs;
     if (most * in->H > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARGUMENT, "too many tiles (rows / 64 * H must be < 2^31)");

@@ -61,12 +61,13 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     const int wave_end = in.causal ? min(nk, min(nq, wrow + 16 * NQ) + off) : nk;           // of the wave
     const int wave_full = in.causal ? min(nk, wrow + off + 1) : nk;                    // keys all its rows see
 
-    Stage<E, DQK, BN, 256, DR> sk;
+    Stage<E, DQK, BN, 256> sk;
     Stage<E, DV, BN, 256> sv;
     auto load = [&](int t) {
-        sk.load(tid, [&](int r) { return t * BN + r < nk ? kp + (int64_t)(t * BN + r) * in.k_token_stride : zero_row<E>(); },
-                [&](int r) { return t * BN + r < nk ? pp + (int64_t)(t * BN + r) * in.k_pe_token_stride : zero_row<E>(); });
-        sv.load(tid, [&](int r) { return t * BN + r < nk ? vp + (int64_t)(t * BN + r) * in.v_token_stride : zero_row<E>(); });
+        const int64_t key = (int64_t)t * BN;
+        sk.template load_rows<DR>(tid, kp + key * in.k_token_stride, in.k_token_stride, pp + key * in.k_pe_token_stride,
+                                  in.k_pe_token_stride, nk - t * BN);
+        sv.load_rows(tid, vp + key * in.v_token_stride, in.v_token_stride, nk - t * BN);
     };
     const RowReader<E, DQK> k_rows(lane);
     const ColReader<E, DV, DV / 16> v_cols(lane);

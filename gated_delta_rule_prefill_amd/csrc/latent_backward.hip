@@ -35,6 +35,9 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
+    // the rows' output gradients, each wave's own, in operand order (registers
+    // hold q and dq already)
+    __shared__ __attribute__((aligned(16))) E sgo[4][NQ][VS][64 * 8];
 
     int h, want, seq, tile;
     head_tile_of_block(in.H, tiles, h, want);
@@ -55,7 +58,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const E* vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
     const E* pp = DR ? (const E*)in.k_pe + (int64_t)k0 * in.k_pe_token_stride : nullptr;
 
-    v8 q[NQ][KS], go[NQ][VS];
+    v8 q[NQ][KS];
     float lse2[NQ], dl[NQ], exact[NQ];   // delta from the rounded o, and from this kernel's own weights
     int last[NQ];
 #pragma unroll
@@ -68,10 +71,10 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         float sum = 0.f;
 #pragma unroll
         for (int vs = 0; vs < VS; ++vs) {
-            go[j][vs] = row_frag_global(d_o + at * DV, vs, lane);
-            const v8 ov = row_frag_global(o + at * DV, vs, lane);
+            const v8 gv = row_frag_global(d_o + at * DV, vs, lane), ov = row_frag_global(o + at * DV, vs, lane);
+            store_frag(sgo[wave][j][vs], lane, gv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += to_f32(go[j][vs][i]) * to_f32(ov[i]);
+            for (int i = 0; i < 8; ++i) sum += to_f32(gv[i]) * to_f32(ov[i]);
         }
         dl[j] = group_sum(sum);
         lse2[j] = lse[at] * LOG2E;
@@ -83,12 +86,13 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const int wave_end = in.causal ? min(nk, min(nq, wrow + 16 * NQ) + off) : nk;
     const int wave_full = in.causal ? min(nk, wrow + off + 1) : nk;
 
-    Stage<E, DQK, BN, 256, DR> sk;
+    Stage<E, DQK, BN, 256> sk;
     Stage<E, DV, BN, 256> sv;
     auto load = [&](int t) {
-        sk.load(tid, [&](int r) { return t * BN + r < nk ? kp + (int64_t)(t * BN + r) * in.k_token_stride : zero_row<E>(); },
-                [&](int r) { return t * BN + r < nk ? pp + (int64_t)(t * BN + r) * in.k_pe_token_stride : zero_row<E>(); });
-        sv.load(tid, [&](int r) { return t * BN + r < nk ? vp + (int64_t)(t * BN + r) * in.v_token_stride : zero_row<E>(); });
+        const int64_t key = (int64_t)t * BN;
+        sk.template load_rows<DR>(tid, kp + key * in.k_token_stride, in.k_token_stride, pp + key * in.k_pe_token_stride,
+                                  in.k_pe_token_stride, nk - t * BN);
+        sv.load_rows(tid, vp + key * in.v_token_stride, in.v_token_stride, nk - t * BN);
     };
     const RowReader<E, DQK> k_rows(lane);
     const RowReader<E, DV> v_rows(lane);
@@ -116,19 +120,41 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
             for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) s[j][tt] = dp[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
-            ahead<TT * (KS + VS), PD>(
-                [&](int e) {
-                    x[e % (PD + 1)] = e / TT < KS ? k_rows(K, 16 * (e % TT), e / TT) : v_rows(V, 16 * (e % TT), e / TT - KS);
-                },
-                [&](int e) {
-                    const int tt = e % TT, ks = e / TT;
+            ahead<TT * KS, PD>([&](int e) { x[e % (PD + 1)] = k_rows(K, 16 * (e % TT), e / TT); },
+                               [&](int e) {
 #pragma unroll
-                    for (int j = 0; j < NQ; ++j) {
-                        if (ks < KS) s[j][tt] = mma32(x[e % (PD + 1)], q[j][ks < KS ? ks : 0], s[j][tt]);
-                        else dp[j][tt] = mma32(x[e % (PD + 1)], go[j][ks < KS ? 0 : ks - KS], dp[j][tt]);
+                                   for (int j = 0; j < NQ; ++j)
+                                       s[j][e % TT] = mma32(x[e % (PD + 1)], q[j][e / TT], s[j][e % TT]);
+                               });
+            // the weights' exponentials run between the products g v^T
+            v8 y[2][NQ];
+            auto row_grads = [&](int vs) {
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) y[vs & 1][j] = load_frag(sgo[wave][j][vs], lane);
+            };
+            row_grads(0);
+            ahead<TT * VS, PD>(
+                [&](int e) { x[e % (PD + 1)] = v_rows(V, 16 * (e % TT), e / TT); },
+                [&](int e) {
+                    if (e % TT == 0 && e / TT + 1 < VS) row_grads(e / TT + 1);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) dp[j][e % TT] = mma32(x[e % (PD + 1)], y[e / TT & 1][j], dp[j][e % TT]);
+                    constexpr int NS = NQ * TT * 4;
+#pragma unroll
+                    for (int n = NS * e / (TT * VS); n < NS * (e + 1) / (TT * VS); ++n) {
+                        const int j = n / (TT * 4), tt = n / 4 % TT, i = n % 4;
+                        s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -lse2[j]));
                     }
                 });
-            const bool masked = (t + 1) * BN > wave_full;
+            if ((t + 1) * BN > wave_full) {   // weights of hidden keys
+#pragma unroll
+                for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (t * BN + 16 * tt + 4 * g + i > last[j]) s[j][tt][i] = 0.f, dp[j][tt][i] = 0.f;
+            }
             v8 dz[NQ];
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
@@ -136,10 +162,8 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                 for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float w = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -lse2[j]));
-                        const bool hidden = masked && t * BN + 16 * tt + 4 * g + i > last[j];
-                        exact[j] += hidden ? 0.f : w * dp[j][tt][i];
-                        s[j][tt][i] = hidden ? 0.f : w * (dp[j][tt][i] - dl[j]);
+                        exact[j] += s[j][tt][i] * dp[j][tt][i];
+                        s[j][tt][i] *= dp[j][tt][i] - dl[j];
                     }
                 dz[j] = acc_frag(s[j][0], s[j][1], E());
             }
@@ -226,8 +250,8 @@ __global__ __launch_bounds__(256, DKV_WAVES<E>) void latent_dkv_kernel(
     Stage<E, DV, BQ, 256> sg;
     float srow_next = 0.f;
     auto load = [&](int t) {
-        sq.load(tid, [&](int r) { return t * BQ + r < nq ? qp + (int64_t)(t * BQ + r) * in.q_token_stride : zero_row<E>(); });
-        sg.load(tid, [&](int r) { return t * BQ + r < nq ? gp + (int64_t)(t * BQ + r) * in.H * DV : zero_row<E>(); });
+        sq.load_rows(tid, qp + (int64_t)t * BQ * in.q_token_stride, in.q_token_stride, nq - t * BQ);
+        sg.load_rows(tid, gp + (int64_t)t * BQ * in.H * DV, (int64_t)in.H * DV, nq - t * BQ);
         if (tid < 2 * BQ) {   // rows behind the last weigh nothing: lse = inf
             const int i = t * BQ + (tid & (BQ - 1));
             const int64_t at = (int64_t)(q0 + min(i, nq - 1)) * in.H + h;
@@ -270,50 +294,54 @@ __global__ __launch_bounds__(256, DKV_WAVES<E>) void latent_dkv_kernel(
             for (int n = 0; n < NK; ++n)
 #pragma unroll
                 for (int a = 0; a < 2; ++a) s[n][a] = dp[n][a] = f32x4{0.f, 0.f, 0.f, 0.f};
-            ahead<2 * (KS + VS), PD>(
-                [&](int e) {
-                    x[e % (PD + 1)] = e / 2 < KS ? q_rows(Q, 16 * (e % 2), e / 2) : g_rows(G, 16 * (e % 2), e / 2 - KS);
-                },
-                [&](int e) {
-                    const int a = e % 2, ks = e / 2;
+            ahead<2 * KS, PD>([&](int e) { x[e % (PD + 1)] = q_rows(Q, 16 * (e % 2), e / 2); },
+                              [&](int e) {
 #pragma unroll
-                    for (int n = 0; n < NK; ++n) {
-                        if (ks < KS) s[n][a] = mma32(x[e % (PD + 1)], k[n][ks < KS ? ks : 0], s[n][a]);
-                        else dp[n][a] = mma32(x[e % (PD + 1)], v[n][ks < KS ? 0 : ks - KS], dp[n][a]);
-                    }
-                });
+                                  for (int n = 0; n < NK; ++n)
+                                      s[n][e % 2] = mma32(x[e % (PD + 1)], k[n][e / 2], s[n][e % 2]);
+                              });
+            const f32x4 ls[2] = {*reinterpret_cast<const f32x4*>(R + 4 * g), *reinterpret_cast<const f32x4*>(R + 16 + 4 * g)};
+            const f32x4 de[2] = {*reinterpret_cast<const f32x4*>(R + BQ + 4 * g),
+                                 *reinterpret_cast<const f32x4*>(R + BQ + 16 + 4 * g)};
             const bool masked = in.causal && t * BQ + off < wkey + 16 * NK - 1;   // some row sees not all of the keys
+            // the weights' exponentials run between the products g v^T, dz between the products for dv
+            ahead<2 * VS, PD>([&](int e) { x[e % (PD + 1)] = g_rows(G, 16 * (e % 2), e / 2); },
+                              [&](int e) {
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const f32x4 ls = *reinterpret_cast<const f32x4*>(R + 16 * a + 4 * g);
-                const f32x4 de = *reinterpret_cast<const f32x4*>(R + BQ + 16 * a + 4 * g);
+                                  for (int n = 0; n < NK; ++n)
+                                      dp[n][e % 2] = mma32(x[e % (PD + 1)], v[n][e / 2], dp[n][e % 2]);
+#pragma unroll
+                                  for (int i = 8 * NK * e / (2 * VS); i < 8 * NK * (e + 1) / (2 * VS); ++i)
+                                      s[i / 8][i / 4 % 2][i % 4] =
+                                          exp2_fast(__builtin_fmaf(s[i / 8][i / 4 % 2][i % 4], sc, -ls[i / 4 % 2][i % 4]));
+                              });
+            if (masked) {
 #pragma unroll
                 for (int n = 0; n < NK; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool hidden = masked && wkey + 16 * n + col > t * BQ + 16 * a + 4 * g + i + off;
-                        const float w = exp2_fast(__builtin_fmaf(s[n][a][i], sc, -ls[i]));
-                        const float z = w * (dp[n][a][i] - de[i]);
-                        s[n][a][i] = hidden ? 0.f : w;
-                        dp[n][a][i] = hidden ? 0.f : z;
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        if (wkey + 16 * n + col > t * BQ + 16 * (i / 4) + 4 * g + i % 4 + off)
+                            s[n][i / 4][i % 4] = 0.f, dp[n][i / 4][i % 4] = 0.f;
             }
             v8 wf[NK], zf[NK];
 #pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                wf[n] = acc_frag(s[n][0], s[n][1], E());
-                zf[n] = acc_frag(dp[n][0], dp[n][1], E());
-            }
-            ahead<DV / 16 + DQK / 16, PD>(
-                [&](int c) { x[c % (PD + 1)] = c < DV / 16 ? g_cols(G, 0, 16, c) : q_cols(Q, 0, 16, c - DV / 16); },
-                [&](int c) {
-                    const int ck = c < DV / 16 ? 0 : c - DV / 16, cv = c < DV / 16 ? c : 0;
+            for (int n = 0; n < NK; ++n) wf[n] = acc_frag(s[n][0], s[n][1], E());
+            ahead<DV / 16, PD>([&](int c) { x[c % (PD + 1)] = g_cols(G, 0, 16, c); },
+                               [&](int c) {
 #pragma unroll
-                    for (int n = 0; n < NK; ++n) {
-                        if (c < DV / 16) av[n][cv] = mma32(x[c % (PD + 1)], wf[n], av[n][cv]);
-                        else ak[n][ck] = mma32(x[c % (PD + 1)], zf[n], ak[n][ck]);
-                    }
-                });
+                                   for (int n = 0; n < NK; ++n) av[n][c] = mma32(x[c % (PD + 1)], wf[n], av[n][c]);
+#pragma unroll
+                                   for (int i = 8 * NK * c / (DV / 16); i < 8 * NK * (c + 1) / (DV / 16); ++i)
+                                       dp[i / 8][i / 4 % 2][i % 4] = s[i / 8][i / 4 % 2][i % 4] *
+                                                                     (dp[i / 8][i / 4 % 2][i % 4] - de[i / 4 % 2][i % 4]);
+                               });
+#pragma unroll
+            for (int n = 0; n < NK; ++n) zf[n] = acc_frag(dp[n][0], dp[n][1], E());
+            ahead<DQK / 16, PD>([&](int c) { x[c % (PD + 1)] = q_cols(Q, 0, 16, c); },
+                                [&](int c) {
+#pragma unroll
+                                    for (int n = 0; n < NK; ++n) ak[n][c] = mma32(x[c % (PD + 1)], zf[n], ak[n][c]);
+                                });
         }
         if (t + 1 < nt) store((t + 1) & 1);
         __syncthreads();

@@ -164,37 +164,70 @@ __device__ __forceinline__ void ahead(F fetch, U use) {
 // -- staging: global -> registers -> LDS ---------------------------------------
 // ROWS x W elements moved by NT threads, 8 or more threads to a row (128-byte
 // lines), so that a thread's chunks lie at constant offsets from one address
-// per row it serves.  row(r) returns the row's address (zero_row() for a row
-// that is not there, so that no load is conditional); with W1 > 0 the last W1
-// of the W channels come from row1(r).  The loads are issued by load() and
-// waited for by store(), a tile of work later.
+// per row it serves.  The loads are issued by load() and waited for by store(),
+// a tile of work later.
 static __device__ const u32x4 kZeros[144] = {};   // a row of up to 576 fp32 channels
 template <typename E> __device__ __forceinline__ const E* zero_row() { return reinterpret_cast<const E*>(kZeros); }
 
-template <typename E, int W, int ROWS, int NT, int W1 = 0>
+template <typename E, int W, int ROWS, int NT>
 struct Stage {
     static constexpr int CE = CHUNK_ELEMS<E>, TPR = ROWS * 8 >= NT ? 8 : NT / ROWS;   // threads per row
-    static constexpr int PASS = NT / TPR, P = ROWS / PASS, S = W / CE / TPR, S0 = (W - W1) / CE / TPR;
-    static_assert(ROWS % PASS == 0 && PASS % 16 == 0 && W % (TPR * CE) == 0 && W1 % (TPR * CE) == 0, "whole passes and steps");
+    static constexpr int PASS = NT / TPR, P = ROWS / PASS, S = W / CE / TPR;
+    static_assert(ROWS % PASS == 0 && PASS % 16 == 0 && W % (TPR * CE) == 0, "whole passes and steps");
     u32x4 r[P][S];
-    template <typename F, typename G>
-    __device__ __forceinline__ void load(int tid, F row, G row1) {
+    // rows in any order: row(r) returns the row's address (zero_row() for a row
+    // that is not there, so that no load is conditional)
+    template <typename F>
+    __device__ __forceinline__ void load(int tid, F row) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const E* a = row(tid / TPR + PASS * p) + CE * (tid % TPR);
-            const E* b = W1 ? row1(tid / TPR + PASS * p) + CE * (tid % TPR) : nullptr;
 #pragma unroll
-            for (int s = 0; s < S; ++s)
-                r[p][s] = *reinterpret_cast<const u32x4*>(s < S0 ? a + TPR * CE * s : b + TPR * CE * (s - S0));
+            for (int s = 0; s < S; ++s) r[p][s] = *reinterpret_cast<const u32x4*>(a + TPR * CE * s);
         }
     }
-    template <typename F>
-    __device__ __forceinline__ void load(int tid, F row) { load(tid, row, row); }
+    // Rows `stride` elements apart from a base that is the same for all threads,
+    // the first `left` of them there and zeros behind: channels [0, W - W1) from
+    // base, the last W1 from base1.  A thread's offset within the tile fits in
+    // 32 bits and stays the same from tile to tile (strides are below 2^23).
+    template <int W1>
+    __device__ __forceinline__ void load_rows(int tid, const E* base, int64_t stride, const E* base1, int64_t stride1,
+                                              int left) {
+        constexpr int S0 = (W - W1) / CE / TPR;
+        static_assert(W1 % (TPR * CE) == 0, "whole steps");
+        const bool whole = left >= ROWS;
+        const uint32_t chunk = 16 * (tid % TPR);
+        if (whole) {
+            const uint32_t at = (uint32_t)(tid / TPR) * (uint32_t)(stride * sizeof(E)) + chunk;
+            const uint32_t at1 = (uint32_t)(tid / TPR) * (uint32_t)(stride1 * sizeof(E)) + chunk;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    r[p][s] = s < S0 ? *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base + PASS * p * stride + TPR * CE * s) + at)
+                                     : *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base1 + PASS * p * stride1 + TPR * CE * (s - S0)) + at1);
+        } else {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int row = tid / TPR + PASS * p, there = min(row, left - 1);
+                const uint32_t at = (uint32_t)there * (uint32_t)(stride * sizeof(E)) + chunk;
+                const uint32_t at1 = (uint32_t)there * (uint32_t)(stride1 * sizeof(E)) + chunk;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    r[p][s] = s < S0 ? *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base + TPR * CE * s) + at)
+                                     : *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base1 + TPR * CE * (s - S0)) + at1);
+                    if (row >= left) r[p][s] = u32x4{0, 0, 0, 0};
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void load_rows(int tid, const E* base, int64_t stride, int left) {
+        load_rows<0>(tid, base, stride, base, stride, left);
+    }
     // store(), each chunk's register refilled at once with the tile after next,
     // so that a tile's worth of loads stays in flight
     template <typename F>
     __device__ __forceinline__ void store_load(int tid, E* t, F row) {
-        static_assert(W1 == 0, "rows of one piece");
         const int at = tile_at<E, W>(tid / TPR, tid % TPR);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
