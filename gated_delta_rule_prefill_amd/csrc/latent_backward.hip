@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ delta, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BN = 32, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
-    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 2 : 1;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
     // the rows' output gradients, each wave's own, in operand order (registers

@@ -195,30 +195,22 @@ struct Stage {
                                               int left) {
         constexpr int S0 = (W - W1) / CE / TPR;
         static_assert(W1 % (TPR * CE) == 0, "whole steps");
-        const bool whole = left >= ROWS;
-        const uint32_t chunk = 16 * (tid % TPR);
-        if (whole) {
-            const uint32_t at = (uint32_t)(tid / TPR) * (uint32_t)(stride * sizeof(E)) + chunk;
-            const uint32_t at1 = (uint32_t)(tid / TPR) * (uint32_t)(stride1 * sizeof(E)) + chunk;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const uint32_t there = min(tid / TPR + PASS * p, left - 1), chunk = 16 * (tid % TPR);
+            const uint32_t at = there * (uint32_t)(stride * sizeof(E)) + chunk;
+            const uint32_t at1 = there * (uint32_t)(stride1 * sizeof(E)) + chunk;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                r[p][s] = s < S0 ? *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base + TPR * CE * s) + at)
+                                 : *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base1 + TPR * CE * (s - S0)) + at1);
+        }
+        if (left < ROWS) {
 #pragma unroll
             for (int p = 0; p < P; ++p)
+                if (tid / TPR + PASS * p >= left)
 #pragma unroll
-                for (int s = 0; s < S; ++s)
-                    r[p][s] = s < S0 ? *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base + PASS * p * stride + TPR * CE * s) + at)
-                                     : *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base1 + PASS * p * stride1 + TPR * CE * (s - S0)) + at1);
-        } else {
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const int row = tid / TPR + PASS * p, there = min(row, left - 1);
-                const uint32_t at = (uint32_t)there * (uint32_t)(stride * sizeof(E)) + chunk;
-                const uint32_t at1 = (uint32_t)there * (uint32_t)(stride1 * sizeof(E)) + chunk;
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    r[p][s] = s < S0 ? *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base + TPR * CE * s) + at)
-                                     : *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base1 + TPR * CE * (s - S0)) + at1);
-                    if (row >= left) r[p][s] = u32x4{0, 0, 0, 0};
-                }
-            }
+                    for (int s = 0; s < S; ++s) r[p][s] = u32x4{0, 0, 0, 0};
         }
     }
     __device__ __forceinline__ void load_rows(int tid, const E* base, int64_t stride, int left) {
