@@ -98,69 +98,80 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
             for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) s[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
-            // two key tiles by turns, so that products in a row do not wait for each other
-            ahead<TT * KS, PD>([&](int e) { x[e % (PD + 1)] = k_rows(K, 16 * (e / (2 * KS) * 2 + e % 2), e / 2 % KS); },
-                               [&](int e) {
+            // One sequence of operands, read ahead across its parts: the scores,
+            // two key tiles by turns so that products in a row do not wait for
+            // each other; and, after the weights, the product with the values.
+            constexpr int E0 = TT * KS;
+            v8 p[NQ][TT / 2];
+            auto take_weights = [&]() {
+                if ((t + 1) * BN > wave_full) {
 #pragma unroll
-                                   for (int j = 0; j < NQ; ++j)
-                                       s[j][e / (2 * KS) * 2 + e % 2] =
-                                           mma32(x[e % (PD + 1)], q[j][e / 2 % KS], s[j][e / (2 * KS) * 2 + e % 2]);
-                               });
-            if ((t + 1) * BN > wave_full) {
+                    for (int j = 0; j < NQ; ++j)
 #pragma unroll
-                for (int j = 0; j < NQ; ++j)
+                        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (t * BN + 16 * tt + 4 * g + i > last[j]) s[j][tt][i] = neg_inf();
+                }
+                // The running maximum is raised only when a row's grew by more than
+                // 8 (in powers of two): until then the weights stay below 2^8 and
+                // nothing needs rescaling.
+                float top[NQ];
+                bool grew = false;
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    float x = neg_inf();
 #pragma unroll
                     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (t * BN + 16 * tt + 4 * g + i > last[j]) s[j][tt][i] = neg_inf();
-            }
-            // The running maximum is raised only when a row's grew by more than
-            // 8 (in powers of two): until then the weights stay below 2^8 and
-            // nothing needs rescaling.
-            float top[NQ];
-            bool grew = false;
+                        for (int i = 0; i < 4; ++i) x = fmaxf(x, s[j][tt][i]);
+                    top[j] = group_max(x) * sc;
+                    grew |= top[j] > m[j] + 8.f;
+                }
+                if (__any(grew)) {
 #pragma unroll
-            for (int j = 0; j < NQ; ++j) {
-                float x = neg_inf();
+                    for (int j = 0; j < NQ; ++j) {
+                        const float mn = fmaxf(m[j], top[j]);
+                        const float f = mn == neg_inf() ? 1.f : exp2_fast(m[j] - mn);
+                        m[j] = mn;
+                        l[j] *= f;
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x = fmaxf(x, s[j][tt][i]);
-                top[j] = group_max(x) * sc;
-                grew |= top[j] > m[j] + 8.f;
-            }
-            if (__any(grew)) {
+                        for (int c = 0; c < DV / 16; ++c) acc[j][c] *= f;
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
-                    const float mn = fmaxf(m[j], top[j]);
-                    const float f = mn == neg_inf() ? 1.f : exp2_fast(m[j] - mn);
-                    m[j] = mn;
-                    l[j] *= f;
+                    const float base = m[j] == neg_inf() ? 0.f : m[j];   // a row that has seen no key yet
 #pragma unroll
-                    for (int c = 0; c < DV / 16; ++c) acc[j][c] *= f;
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -base));
+                            l[j] += s[j][tt][i];   // the sum takes the weights before their rounding
+                        }
+#pragma unroll
+                    for (int b = 0; b < TT / 2; ++b) p[j][b] = acc_frag(s[j][2 * b], s[j][2 * b + 1], E());
                 }
-            }
-            v8 p[NQ][TT / 2];
+            };
+            ahead<E0 + DV / 16 * (TT / 2), PD>(
+                [&](auto step) {
+                    constexpr int e = step, f = e - E0;
+                    if constexpr (e < E0) x[e % (PD + 1)] = k_rows(K, 16 * (e / (2 * KS) * 2 + e % 2), e / 2 % KS);
+                    else x[e % (PD + 1)] = v_cols(V, 32 * (f / (DV / 16)), 32 * (f / (DV / 16)) + 16, f % (DV / 16));
+                },
+                [&](auto step) {
+                    constexpr int e = step, f = e - E0;
+                    if constexpr (e < E0) {
 #pragma unroll
-            for (int j = 0; j < NQ; ++j) {
-                const float base = m[j] == neg_inf() ? 0.f : m[j];   // a row that has seen no key yet
+                        for (int j = 0; j < NQ; ++j)
+                            s[j][e / (2 * KS) * 2 + e % 2] =
+                                mma32(x[e % (PD + 1)], q[j][e / 2 % KS], s[j][e / (2 * KS) * 2 + e % 2]);
+                    } else {
+                        if constexpr (f == 0) take_weights();
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -base));
-                        l[j] += s[j][tt][i];   // the sum takes the weights before their rounding
+                        for (int j = 0; j < NQ; ++j)
+                            acc[j][f % (DV / 16)] = mma32(x[e % (PD + 1)], p[j][f / (DV / 16)], acc[j][f % (DV / 16)]);
                     }
-#pragma unroll
-                for (int b = 0; b < TT / 2; ++b) p[j][b] = acc_frag(s[j][2 * b], s[j][2 * b + 1], E());
-            }
-            ahead<DV / 16 * (TT / 2), PD>(
-                [&](int e) { x[e % (PD + 1)] = v_cols(V, 32 * (e / (DV / 16)), 32 * (e / (DV / 16)) + 16, e % (DV / 16)); },
-                [&](int e) {
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j)
-                        acc[j][e % (DV / 16)] = mma32(x[e % (PD + 1)], p[j][e / (DV / 16)], acc[j][e % (DV / 16)]);
                 });
         }
         if (t + 1 < nt) {

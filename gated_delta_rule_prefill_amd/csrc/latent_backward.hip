@@ -120,58 +120,66 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
             for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) s[j][tt] = dp[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
-            ahead<TT * KS, PD>([&](int e) { x[e % (PD + 1)] = k_rows(K, 16 * (e % TT), e / TT); },
-                               [&](int e) {
-#pragma unroll
-                                   for (int j = 0; j < NQ; ++j)
-                                       s[j][e % TT] = mma32(x[e % (PD + 1)], q[j][e / TT], s[j][e % TT]);
-                               });
-            // the weights' exponentials run between the products g v^T
-            v8 y[2][NQ];
+            // One sequence of operands, read ahead across its parts: z = q k^T;
+            // g v^T, between whose products the weights' exponentials run; and,
+            // after dz, dq^T += K^T dz.
+            constexpr int E0 = TT * KS, E1 = E0 + TT * VS, NS = NQ * TT * 4;
+            v8 y[2][NQ], dz[NQ];
             auto row_grads = [&](int vs) {
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) y[vs & 1][j] = load_frag(sgo[wave][j][vs], lane);
             };
-            row_grads(0);
-            ahead<TT * VS, PD>(
-                [&](int e) { x[e % (PD + 1)] = v_rows(V, 16 * (e % TT), e / TT); },
-                [&](int e) {
-                    if (e % TT == 0 && e / TT + 1 < VS) row_grads(e / TT + 1);
+            ahead<E1 + DQK / 16, PD>(
+                [&](auto step) {
+                    constexpr int e = step;
+                    x[e % (PD + 1)] = e < E0   ? k_rows(K, 16 * (e % TT), e / TT)
+                                      : e < E1 ? v_rows(V, 16 * ((e - E0) % TT), (e - E0) / TT)
+                                               : k_cols(K, 0, 16, e - E1);
+                },
+                [&](auto step) {
+                    constexpr int e = step;
+                    if (e < E0) {
+                        if (e == E0 - 2) row_grads(0);
 #pragma unroll
-                    for (int j = 0; j < NQ; ++j) dp[j][e % TT] = mma32(x[e % (PD + 1)], y[e / TT & 1][j], dp[j][e % TT]);
-                    constexpr int NS = NQ * TT * 4;
+                        for (int j = 0; j < NQ; ++j) s[j][e % TT] = mma32(x[e % (PD + 1)], q[j][e < E0 ? e / TT : 0], s[j][e % TT]);
+                    } else if (e < E1) {
+                        const int f = e - E0;
+                        if (f % TT == 0 && f / TT + 1 < VS) row_grads(f / TT + 1);
 #pragma unroll
-                    for (int n = NS * e / (TT * VS); n < NS * (e + 1) / (TT * VS); ++n) {
-                        const int j = n / (TT * 4), tt = n / 4 % TT, i = n % 4;
-                        s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -lse2[j]));
+                        for (int j = 0; j < NQ; ++j) dp[j][f % TT] = mma32(x[e % (PD + 1)], y[f / TT & 1][j], dp[j][f % TT]);
+#pragma unroll
+                        for (int n = NS * f / (TT * VS); n < NS * (f + 1) / (TT * VS); ++n) {
+                            const int j = n / (TT * 4), tt = n / 4 % TT, i = n % 4;
+                            s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -lse2[j]));
+                        }
+                    } else {
+                        if (e == E1) {
+                            if ((t + 1) * BN > wave_full) {   // weights of hidden keys
+#pragma unroll
+                                for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i)
+                                            if (t * BN + 16 * tt + 4 * g + i > last[j]) s[j][tt][i] = 0.f, dp[j][tt][i] = 0.f;
+                            }
+#pragma unroll
+                            for (int j = 0; j < NQ; ++j) {
+#pragma unroll
+                                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        exact[j] += s[j][tt][i] * dp[j][tt][i];
+                                        s[j][tt][i] *= dp[j][tt][i] - dl[j];
+                                    }
+                                dz[j] = acc_frag(s[j][0], s[j][1], E());
+                            }
+                        }
+                        const int c = e < E1 ? 0 : e - E1;
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[e % (PD + 1)], dz[j], acc[j][c]);
                     }
                 });
-            if ((t + 1) * BN > wave_full) {   // weights of hidden keys
-#pragma unroll
-                for (int j = 0; j < NQ; ++j)
-#pragma unroll
-                    for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (t * BN + 16 * tt + 4 * g + i > last[j]) s[j][tt][i] = 0.f, dp[j][tt][i] = 0.f;
-            }
-            v8 dz[NQ];
-#pragma unroll
-            for (int j = 0; j < NQ; ++j) {
-#pragma unroll
-                for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        exact[j] += s[j][tt][i] * dp[j][tt][i];
-                        s[j][tt][i] *= dp[j][tt][i] - dl[j];
-                    }
-                dz[j] = acc_frag(s[j][0], s[j][1], E());
-            }
-            ahead<DQK / 16, PD>([&](int c) { x[c % (PD + 1)] = k_cols(K, 0, 16, c); },
-                                [&](int c) {
-#pragma unroll
-                                    for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[c % (PD + 1)], dz[j], acc[j][c]);
-                                });
         }
         if (t + 1 < nt) {
             E* next = smem[(t + 1) & 1];
@@ -294,54 +302,66 @@ __global__ __launch_bounds__(256, DKV_WAVES<E>) void latent_dkv_kernel(
             for (int n = 0; n < NK; ++n)
 #pragma unroll
                 for (int a = 0; a < 2; ++a) s[n][a] = dp[n][a] = f32x4{0.f, 0.f, 0.f, 0.f};
-            ahead<2 * KS, PD>([&](int e) { x[e % (PD + 1)] = q_rows(Q, 16 * (e % 2), e / 2); },
-                              [&](int e) {
-#pragma unroll
-                                  for (int n = 0; n < NK; ++n)
-                                      s[n][e % 2] = mma32(x[e % (PD + 1)], k[n][e / 2], s[n][e % 2]);
-                              });
             const f32x4 ls[2] = {*reinterpret_cast<const f32x4*>(R + 4 * g), *reinterpret_cast<const f32x4*>(R + 16 + 4 * g)};
             const f32x4 de[2] = {*reinterpret_cast<const f32x4*>(R + BQ + 4 * g),
                                  *reinterpret_cast<const f32x4*>(R + BQ + 16 + 4 * g)};
             const bool masked = in.causal && t * BQ + off < wkey + 16 * NK - 1;   // some row sees not all of the keys
-            // the weights' exponentials run between the products g v^T, dz between the products for dv
-            ahead<2 * VS, PD>([&](int e) { x[e % (PD + 1)] = g_rows(G, 16 * (e % 2), e / 2); },
-                              [&](int e) {
-#pragma unroll
-                                  for (int n = 0; n < NK; ++n)
-                                      dp[n][e % 2] = mma32(x[e % (PD + 1)], v[n][e / 2], dp[n][e % 2]);
-#pragma unroll
-                                  for (int i = 8 * NK * e / (2 * VS); i < 8 * NK * (e + 1) / (2 * VS); ++i)
-                                      s[i / 8][i / 4 % 2][i % 4] =
-                                          exp2_fast(__builtin_fmaf(s[i / 8][i / 4 % 2][i % 4], sc, -ls[i / 4 % 2][i % 4]));
-                              });
-            if (masked) {
-#pragma unroll
-                for (int n = 0; n < NK; ++n)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (wkey + 16 * n + col > t * BQ + 16 * (i / 4) + 4 * g + i % 4 + off)
-                            s[n][i / 4][i % 4] = 0.f, dp[n][i / 4][i % 4] = 0.f;
-            }
+            // One sequence of operands, read ahead across its parts: z = q k^T;
+            // g v^T, between whose products the weights' exponentials run;
+            // dv^T += g^T w, between whose products dz is formed; dk^T += q^T dz.
+            constexpr int E0 = 2 * KS, E1 = E0 + 2 * VS, E2 = E1 + DV / 16, NS = 8 * NK;
             v8 wf[NK], zf[NK];
+            ahead<E2 + DQK / 16, PD>(
+                [&](auto step) {
+                    constexpr int e = step;
+                    x[e % (PD + 1)] = e < E0   ? q_rows(Q, 16 * (e % 2), e / 2)
+                                      : e < E1 ? g_rows(G, 16 * ((e - E0) % 2), (e - E0) / 2)
+                                      : e < E2 ? g_cols(G, 0, 16, e - E1)
+                                               : q_cols(Q, 0, 16, e - E2);
+                },
+                [&](auto step) {
+                    constexpr int e = step;
+                    const v8& a = x[e % (PD + 1)];
+                    if (e < E0) {
 #pragma unroll
-            for (int n = 0; n < NK; ++n) wf[n] = acc_frag(s[n][0], s[n][1], E());
-            ahead<DV / 16, PD>([&](int c) { x[c % (PD + 1)] = g_cols(G, 0, 16, c); },
-                               [&](int c) {
+                        for (int n = 0; n < NK; ++n) s[n][e % 2] = mma32(a, k[n][e < E0 ? e / 2 : 0], s[n][e % 2]);
+                    } else if (e < E1) {
+                        const int f = e < E1 ? e - E0 : 0;
 #pragma unroll
-                                   for (int n = 0; n < NK; ++n) av[n][c] = mma32(x[c % (PD + 1)], wf[n], av[n][c]);
+                        for (int n = 0; n < NK; ++n) dp[n][f % 2] = mma32(a, v[n][f / 2], dp[n][f % 2]);
 #pragma unroll
-                                   for (int i = 8 * NK * c / (DV / 16); i < 8 * NK * (c + 1) / (DV / 16); ++i)
-                                       dp[i / 8][i / 4 % 2][i % 4] = s[i / 8][i / 4 % 2][i % 4] *
-                                                                     (dp[i / 8][i / 4 % 2][i % 4] - de[i / 4 % 2][i % 4]);
-                               });
+                        for (int i = NS * f / (2 * VS); i < NS * (f + 1) / (2 * VS); ++i)
+                            s[i / 8][i / 4 % 2][i % 4] =
+                                exp2_fast(__builtin_fmaf(s[i / 8][i / 4 % 2][i % 4], sc, -ls[i / 4 % 2][i % 4]));
+                    } else if (e < E2) {
+                        const int c = e < E2 ? e - E1 : 0;
+                        if (c == 0) {
+                            if (masked) {
 #pragma unroll
-            for (int n = 0; n < NK; ++n) zf[n] = acc_frag(dp[n][0], dp[n][1], E());
-            ahead<DQK / 16, PD>([&](int c) { x[c % (PD + 1)] = q_cols(Q, 0, 16, c); },
-                                [&](int c) {
+                                for (int n = 0; n < NK; ++n)
 #pragma unroll
-                                    for (int n = 0; n < NK; ++n) ak[n][c] = mma32(x[c % (PD + 1)], zf[n], ak[n][c]);
-                                });
+                                    for (int i = 0; i < 8; ++i)
+                                        if (wkey + 16 * n + col > t * BQ + 16 * (i / 4) + 4 * g + i % 4 + off)
+                                            s[n][i / 4][i % 4] = 0.f, dp[n][i / 4][i % 4] = 0.f;
+                            }
+#pragma unroll
+                            for (int n = 0; n < NK; ++n) wf[n] = acc_frag(s[n][0], s[n][1], E());
+                        }
+#pragma unroll
+                        for (int n = 0; n < NK; ++n) av[n][c] = mma32(a, wf[n], av[n][c]);
+#pragma unroll
+                        for (int i = NS * c / (DV / 16); i < NS * (c + 1) / (DV / 16); ++i)
+                            dp[i / 8][i / 4 % 2][i % 4] =
+                                s[i / 8][i / 4 % 2][i % 4] * (dp[i / 8][i / 4 % 2][i % 4] - de[i / 4 % 2][i % 4]);
+                    } else {
+                        const int c = e < E2 ? 0 : e - E2;
+                        if (c == 0)
+#pragma unroll
+                            for (int n = 0; n < NK; ++n) zf[n] = acc_frag(dp[n][0], dp[n][1], E());
+#pragma unroll
+                        for (int n = 0; n < NK; ++n) ak[n][c] = mma32(a, zf[n], ak[n][c]);
+                    }
+                });
         }
         if (t + 1 < nt) store((t + 1) & 1);
         __syncthreads();

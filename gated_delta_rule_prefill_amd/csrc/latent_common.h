@@ -2,6 +2,9 @@
 // LDS, their matrix operands, and the search for a workgroup's sequence.
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "kda_common.h"
 #include "latent_launch.h"
 
@@ -148,17 +151,24 @@ __device__ __forceinline__ f32x8 row_frag_global(const float* row, int ks, int l
 // N steps use(e), each with an operand that fetch(e) reads from LDS D steps
 // ahead into a ring of D + 1: the compiler, short of registers, otherwise puts
 // every read right before its use and waits for it.
+template <int I> using Int = std::integral_constant<int, I>;
+template <int N, int D, int E, typename F, typename U>
+__device__ __forceinline__ void ahead_step(F& fetch, U& use) {
+    if constexpr (E + D < N) fetch(Int<E + D>());
+    __builtin_amdgcn_sched_barrier(0);
+    use(Int<E>());
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int N, int D, typename F, typename U, int... E, int... S>
+__device__ __forceinline__ void ahead_all(F& fetch, U& use, std::integer_sequence<int, E...>, std::integer_sequence<int, S...>) {
+    (fetch(Int<S>()), ...);
+    (ahead_step<N, D, E>(fetch, use), ...);
+}
+// fetch and use take the step as an Int<e>, so that what they index is known
+// when they are compiled.
 template <int N, int D, typename F, typename U>
 __device__ __forceinline__ void ahead(F fetch, U use) {
-#pragma unroll
-    for (int e = 0; e < D && e < N; ++e) fetch(e);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        if (e + D < N) fetch(e + D);
-        __builtin_amdgcn_sched_barrier(0);
-        use(e);
-        __builtin_amdgcn_sched_barrier(0);
-    }
+    ahead_all<N, D>(fetch, use, std::make_integer_sequence<int, N>(), std::make_integer_sequence<int, (D < N ? D : N)>());
 }
 
 // -- staging: global -> registers -> LDS ---------------------------------------
