@@ -24,23 +24,19 @@
 
 namespace kda {
 
-// Shape of a workgroup: RT row tiles of 16, NW waves with RQ row tiles each in
-// the scores, BN keys a tile, GRID workgroups in a launch (the LDS tiles fill a
-// CU with GRID / 256 of them).
-template <int RT_, int NW_, int RQ_, int BN_, int GRID_> struct DecodeShape {
-    static constexpr int RT = RT_, NW = NW_, RQ = RQ_, BN = BN_, GRID = GRID_, BM = 16 * RT_;
-    static constexpr int WAVES_PER_SIMD = NW_ * (GRID_ / 256) / 4;
+constexpr int DEC_RUNS = 256;   // one workgroup per CU (its LDS tiles take the CU)
+constexpr int DEC_WAVES = 8;
+
+// Shape of a workgroup: RT row tiles of 16, BN keys a tile.  Where a sequence
+// has up to 32 rows the cache's bytes are the bound and 32 rows are taken (two
+// workgroups a CU with 4 waves and 32 keys each read as fast but leave twice the
+// partial results: 260 against 256 us for 256 sequences, 39 against 34 for one);
+// with more rows 64, so that a cached row is fetched half as often.
+template <int RT_, int BN_> struct DecodeShape {
+    static constexpr int RT = RT_, BN = BN_, BM = 16 * RT_;
 };
-// bf16, up to 32 rows a sequence: the cache's bytes are the bound; two
-// workgroups a CU, so that one's loads run under the other's products.
-typedef DecodeShape<2, 4, 1, 32, 512> DecodeFew;
-// bf16, more rows: 64 of them, so that a cached row is fetched half as often.
-// The products are the bound, and LDS next to them: one wave a SIMD has the
-// registers to hold 32 query rows, so that a key operand read from LDS serves
-// two products (8 waves of 16 rows each: 698 us for 16 x 128 new tokens).
-typedef DecodeShape<4, 8, 1, 64, 256> DecodeMany;
-typedef DecodeShape<2, 8, 1, 32, 256> DecodeFewF32;
-typedef DecodeShape<4, 8, 1, 32, 256> DecodeManyF32;
+template <typename E> using DecodeFew = DecodeShape<2, 128 / (int)sizeof(E)>;
+template <typename E> using DecodeMany = DecodeShape<4, 128 / (int)sizeof(E)>;
 
 // A row tile whose keys several workgroups share: its output rows and the
 // runs [first, last] that hold its partial results.
@@ -54,18 +50,18 @@ struct DecodeSplit {
 // has two slots of partials: 2b for a row tile begun in an earlier run, 2b + 1
 // for one that a later run goes on with.
 struct DecodeSpace {
-    DecodeSplit* split;   // [GRID]
-    float* ml;            // [2 GRID][BM][2]
-    float* o;             // [2 GRID][BM][dl]
+    DecodeSplit* split;   // [DEC_RUNS]
+    float* ml;            // [2 DEC_RUNS][BM][2]
+    float* o;             // [2 DEC_RUNS][BM][dl]
 };
 template <typename S> static size_t space_bytes(int dl) {
-    return sizeof(DecodeSplit) * S::GRID + (size_t)2 * S::GRID * S::BM * (2 + dl) * 4;
+    return sizeof(DecodeSplit) * DEC_RUNS + (size_t)2 * DEC_RUNS * S::BM * (2 + dl) * 4;
 }
 template <typename S> static DecodeSpace space_of(void* ws) {
     DecodeSpace s;
     s.split = reinterpret_cast<DecodeSplit*>(ws);
-    s.ml = reinterpret_cast<float*>(s.split + S::GRID);
-    s.o = s.ml + (size_t)2 * S::GRID * S::BM * 2;
+    s.ml = reinterpret_cast<float*>(s.split + DEC_RUNS);
+    s.o = s.ml + (size_t)2 * DEC_RUNS * S::BM * 2;
     return s;
 }
 
@@ -84,16 +80,15 @@ __device__ __forceinline__ void sequence_work(const LatentDecode& a, int rows_q,
 }
 
 // by_tile: split entries are indexed by row tile (their number is at most
-// GRID), otherwise by the run that begins the row tile.
+// DEC_RUNS), otherwise by the run that begins the row tile.
 template <typename E, int DL, int DR, typename Shape>
-__global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_decode_kernel(const LatentDecode a, DecodeSpace ws,
+__global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const LatentDecode a, DecodeSpace ws,
                                                                           int by_tile, int entries)
 {
-    constexpr int RT = Shape::RT, NW = Shape::NW, BN = Shape::BN, BM = Shape::BM, GRID = Shape::GRID;
+    constexpr int RT = Shape::RT, NW = DEC_WAVES, BN = Shape::BN, BM = Shape::BM;
     constexpr int W = DL + DR, NT = 64 * NW, TT = BN / 16, KS = W / 32;
-    constexpr int RQ = Shape::RQ, RG = RT / RQ;        // a wave's scores: RQ row tiles (row group of RG),
-    constexpr int TG = NW / RG < TT ? NW / RG : TT;    // TW key tiles (key group of TG)
-    constexpr int TW = TT / TG;
+    constexpr int TG = NW / RT < TT ? NW / RT : TT;    // a wave's scores: one row tile and
+    constexpr int TW = TT / TG;                        // TW key tiles (key group of TG)
     constexpr int CT = DL / 16 / NW;                   // 16-column value tiles of a wave
     constexpr int PS = BN + 16 / (int)sizeof(E);       // row stride of the weights
     constexpr bool QREG = sizeof(E) == 2;              // query rows in registers; fp32 rows would fill them
@@ -114,7 +109,7 @@ __global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_
     const float sc = a.scale * LOG2E;
     // Workgroups go round robin over the 8 XCDs: neighbouring runs, which read
     // the same sequence's keys, go to one XCD and its L2.
-    const int run = (blockIdx.x & 7) * (GRID / 8) + (blockIdx.x >> 3);
+    const int run = (blockIdx.x & 7) * (DEC_RUNS / 8) + (blockIdx.x >> 3);
 
     // this workgroup's run of the batch's work: the sum over the sequences,
     // then the sequence its run begins in
@@ -143,7 +138,7 @@ __global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_
         total += wsum[w][0], units += wsum[w][1];
     }
     total = uniform(total);
-    const int64_t per = (total + GRID - 1) / GRID;
+    const int64_t per = (total + DEC_RUNS - 1) / DEC_RUNS;
     const int64_t begin = per * run, stop = min(total, begin + per);
     if (!by_tile) {
         if (tid == 0) ws.split[run].rows = 0;
@@ -190,7 +185,7 @@ __global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_
     int seq = (int)uniform(found[0]);
     int64_t seq_base = uniform(found[1]), unit_base = uniform(found[2]);
 
-    const int rg = wave % RG, tg = wave / RG;      // row and key group of this wave's scores
+    const int rt = wave % RT, tg = wave / RT;      // row tile and key group of this wave's scores
     const bool scores = tg < TG;
     const E* cache = (const E*)a.cache;
     Stage<E, W, BN, NT> st;
@@ -216,14 +211,22 @@ __global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_
         const int te = min(t1, (end + BN - 1) / BN);
         const int32_t* table = a.block_table + (int64_t)seq * a.max_pages;
 
-        auto cache_row = [&](int t) -> int {                         // of key t * BN + tid, tid < BN
-            const int j = t * BN + tid;
-            if (t >= te || j >= len) return -1;
+        // Whole row tiles take their keys in a rotation that starts where the
+        // run stands, so that workgroups of an XCD that work on different rows
+        // of one sequence read the same keys at the same time, through its L2.
+        const bool whole = t0 == 0 && t1 == key_tiles;
+        const int count = max(0, te - t0), turn = whole && count > 0 ? (int)((pos - begin) % count) : 0;
+        auto tile_of = [&](int k) { return t0 + (turn + k < count ? turn + k : turn + k - count); };   // k < count
+
+        auto cache_row = [&](int k) -> int {                         // of the piece's tile k, key tid < BN
+            if (k >= count) return -1;
+            const int j = tile_of(k) * BN + tid;
+            if (j >= len) return -1;
             const int pg = (int)((unsigned)j / (unsigned)a.page_size);
             const int page = table[pg];
             return page < 0 || page >= a.num_pages ? -1 : page * a.page_size + (j - pg * a.page_size);
         };
-        auto row_of = [&](int k) {                                   // of the tile t0 + k
+        auto row_of = [&](int k) {                                   // of the piece's tile k
             return [&, k](int r) {
                 const int row = ridx[k & 3][r];
                 return row < 0 ? zero_row<E>() : cache + (int64_t)row * W;
@@ -235,7 +238,7 @@ __global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_
             if (tid == 0) gaps[k & 3] = gap;
         };
         if (tid < BN) {
-            const int r0 = cache_row(t0), r1 = cache_row(t0 + 1), r2 = cache_row(t0 + 2);
+            const int r0 = cache_row(0), r1 = cache_row(1), r2 = cache_row(2);
             keep_row(0, r0);
             keep_row(1, r1);
             keep_row(2, r2);
@@ -243,141 +246,103 @@ __global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_
         if (tid < 4) grown[tid] = 0;
         __syncthreads();
         int next_row = -1;
-        if (t0 < te) {
+        if (count > 0) {
             Stage<E, W, BN, NT> first;
             first.load(tid, row_of(0));
             st.load(tid, row_of(1));
-            if (tid < BN) next_row = cache_row(t0 + 3);
+            if (tid < BN) next_row = cache_row(3);
             first.store(tid, tilebuf[0]);
         }
-        v8 q[RQ][QREG ? KS : 1];
-        const E* qp[RQ];
-        int last[RQ];                                                // last key this lane's rows see
+        v8 q[QREG ? KS : 1];
+        const E* qp;
+        int last;                                                    // last key this lane's row sees
         const int first_last = len - n + (int)(row0 / a.H);          // and the tile's first row
-#pragma unroll
-        for (int j = 0; j < RQ; ++j) {
-            const int64_t row = row0 + min(nrows - 1, 16 * (rg * RQ + j) + col);
+        {
+            const int64_t row = row0 + min(nrows - 1, 16 * rt + col);
             const int i = (int)(row / a.H), h = (int)(row - (int64_t)i * a.H);
-            qp[j] = (const E*)a.q + (int64_t)(q0 + i) * a.q_token_stride + h * a.q_head_stride;
-            last[j] = len - n + i;
+            qp = (const E*)a.q + (int64_t)(q0 + i) * a.q_token_stride + h * a.q_head_stride;
+            last = len - n + i;
             if (QREG && scores)
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(qp[j], ks, lane);
+                for (int ks = 0; ks < KS; ++ks) q[ks] = row_frag_global(qp, ks, lane);
         }
         f32x4 acc[RT][CT];
-        float m[RT], own[RQ], l[RQ];                                 // own: the maxima of this wave's row tiles
+        float m[RT], own = neg_inf(), l = 0.f;                       // own: the maxima of this wave's row tile
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             m[r] = neg_inf();
 #pragma unroll
             for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-#pragma unroll
-        for (int j = 0; j < RQ; ++j) own[j] = neg_inf(), l[j] = 0.f;
         __syncthreads();
-        for (int t = t0, k = 0; t < te; ++t, ++k) {
+        for (int k = 0; k < count; ++k) {
+            const int t = tile_of(k);
             const E* tile = tilebuf[k & 1];
-            f32x4 s[RQ][TW];
-            v4 p[RQ][TW];
-            float part[RQ];
+            f32x4 s[TW];
+            v4 p[TW];
+            float part = 0.f;
             auto weigh = [&]() {
+                const float from = own == neg_inf() ? 0.f : own;     // a row that has seen no key yet
+                part = 0.f;
 #pragma unroll
-                for (int j = 0; j < RQ; ++j) {
-                    const float from = own[j] == neg_inf() ? 0.f : own[j];   // a row that has seen no key yet
-                    part[j] = 0.f;
+                for (int w = 0; w < TW; ++w)
 #pragma unroll
-                    for (int w = 0; w < TW; ++w)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float x = exp2_fast(__builtin_fmaf(s[j][w][i], sc, -from));
-                            part[j] += x;                // the sum takes the weights before their rounding
-                            p[j][w][i] = from_f32<E>(x); // bf16: the product's operand type
-                        }
-                }
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = exp2_fast(__builtin_fmaf(s[w][i], sc, -from));
+                        part += x;                // the sum takes the weights before their rounding
+                        p[w][i] = from_f32<E>(x); // bf16: the product's operand type
+                    }
             };
             auto put_weights = [&]() {
 #pragma unroll
-                for (int j = 0; j < RQ; ++j)
-#pragma unroll
-                    for (int w = 0; w < TW; ++w)
-                        store_vec(sp + (16 * (rg * RQ + j) + col) * PS + 16 * (tg * TW + w) + 4 * g, p[j][w]);
+                for (int w = 0; w < TW; ++w) store_vec(sp + (16 * rt + col) * PS + 16 * (tg * TW + w) + 4 * g, p[w]);
             };
-#pragma unroll
-            for (int j = 0; j < RQ; ++j) part[j] = 0.f;
             if (scores) {
-                const E* qt[RQ];
+                const E* qt = qp;
+                if (!QREG) asm volatile("" : "+v"(qt));              // fetched again for every tile
 #pragma unroll
-                for (int j = 0; j < RQ; ++j) {
-                    qt[j] = qp[j];
-                    if (!QREG) asm volatile("" : "+v"(qt[j]));   // fetched again for every tile
-#pragma unroll
-                    for (int w = 0; w < TW; ++w) s[j][w] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-                // the keys' operands are read a group ahead of their products
-                constexpr int GK = TW * RQ > 1 || !QREG ? 2 : KS % 6 == 0 ? 3 : KS % 4 == 0 ? 4 : 5, NG = KS / GK;
-                static_assert(KS % GK == 0, "whole groups");
-                v8 x[2][GK][TW], y[2][QREG ? 1 : GK][RQ];
-                auto fetch = [&](int gr) {
-#pragma unroll
-                    for (int i = 0; i < GK; ++i) {
-                        if constexpr (!QREG)
-#pragma unroll
-                            for (int j = 0; j < RQ; ++j) y[gr & 1][i][j] = row_frag_global(qt[j], gr * GK + i, lane);
-#pragma unroll
-                        for (int w = 0; w < TW; ++w) x[gr & 1][i][w] = k_rows(tile, 16 * TW * tg + 16 * w, gr * GK + i);
-                    }
-                };
-                fetch(0);
-#pragma unroll
-                for (int gr = 0; gr < NG; ++gr) {
-                    if (gr + 1 < NG) fetch(gr + 1);
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int i = 0; i < GK; ++i)
-#pragma unroll
-                        for (int w = 0; w < TW; ++w)
-#pragma unroll
-                            for (int j = 0; j < RQ; ++j) {
-                                if constexpr (QREG) s[j][w] = mma32(x[gr & 1][i][w], q[j][gr * GK + i], s[j][w]);
-                                else s[j][w] = mma32(x[gr & 1][i][w], y[gr & 1][i][j], s[j][w]);
-                            }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+                for (int w = 0; w < TW; ++w) s[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+                constexpr int PD = QREG ? 4 : 1;
+                v8 x[PD + 1], y[2];
+                ahead<KS * TW, PD>(
+                    [&](auto step) {
+                        constexpr int e = step;
+                        if constexpr (!QREG && e % TW == 0) y[e / TW & 1] = row_frag_global(qt, e / TW, lane);
+                        x[e % (PD + 1)] = k_rows(tile, 16 * (TW * tg + e % TW), e / TW);
+                    },
+                    [&](auto step) {
+                        constexpr int e = step;
+                        if constexpr (QREG) s[e % TW] = mma32(x[e % (PD + 1)], q[e / TW], s[e % TW]);
+                        else s[e % TW] = mma32(x[e % (PD + 1)], y[e / TW & 1], s[e % TW]);
+                    });
                 if (uniform(gaps[k & 3]) || (t + 1) * BN - 1 > first_last) {
 #pragma unroll
                     for (int w = 0; w < TW; ++w) {
                         const int k0 = 16 * (tg * TW + w) + 4 * g;
                         const i32x4 there = *reinterpret_cast<const i32x4*>(ridx[k & 3] + k0);
 #pragma unroll
-                        for (int j = 0; j < RQ; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (there[i] < 0 || t * BN + k0 + i > last[j]) s[j][w][i] = neg_inf();
+                        for (int i = 0; i < 4; ++i)
+                            if (there[i] < 0 || t * BN + k0 + i > last) s[w][i] = neg_inf();
                     }
                 }
-                bool grew = false;
+                float top = neg_inf();
 #pragma unroll
-                for (int j = 0; j < RQ; ++j) {
-                    float top = neg_inf();
+                for (int w = 0; w < TW; ++w)
 #pragma unroll
-                    for (int w = 0; w < TW; ++w)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][w][i]);
-                    top = group_max(top) * sc;
-                    if (g == 0) stat[tg][16 * (rg * RQ + j) + col] = top;
-                    grew |= top > own[j] + 8.f;
-                }
-                if (__any(grew) && lane == 0) grown[k & 3] = 1;
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, s[w][i]);
+                top = group_max(top) * sc;
+                if (g == 0) stat[tg][16 * rt + col] = top;
+                if (__any(top > own + 8.f) && lane == 0) grown[k & 3] = 1;
                 weigh();
             }
             __syncthreads();   // maxima are there; the other buffer's and the weights' last readers are done
             if (scores) put_weights();
             if (tid < BN) {
                 keep_row(k + 3, next_row);
-                next_row = cache_row(t + 4);
+                next_row = cache_row(k + 4);
             }
             if (tid == 0) grown[(k + 2) & 3] = 0;
-            if (t + 1 < te) st.store_load(tid, tilebuf[(k + 1) & 1], row_of(k + 2));
+            if (k + 1 < count) st.store_load(tid, tilebuf[(k + 1) & 1], row_of(k + 2));
             // The weights are taken against the rows' running maxima as they
             // stand.  Only when a row's grew by more than 8 (in powers of two;
             // the first tile always) are the maxima raised, by every wave alike,
@@ -393,52 +358,45 @@ __global__ __launch_bounds__(64 * Shape::NW, Shape::WAVES_PER_SIMD) void latent_
                     m[r] = grew ? top : m[r];
 #pragma unroll
                     for (int c = 0; c < CT; ++c) acc[r][c] *= f;
-                    if (r / RQ == rg) l[r % RQ] *= f, own[r % RQ] = m[r];
+                    if (r == rt) l *= f, own = m[r];
                 }
                 if (scores) {
                     weigh();
                     put_weights();
                 }
             }
-#pragma unroll
-            for (int j = 0; j < RQ; ++j) l[j] += part[j];
+            l += part;
             __syncthreads();   // weights and the next tile are there
-            // the values' operands are read PD products of RT tiles ahead
-            constexpr int PD = Shape::WAVES_PER_SIMD == 1 ? 3 : 1, NE = TT / 2 * CT;
-            v8 pw[TT / 2][RT], x[PD + 1];
-            auto values = [&](int e) { x[e % (PD + 1)] = c_cols(tile, 32 * (e / CT), 32 * (e / CT) + 16, e % CT); };
+            constexpr int PD = 2, NE = TT / 2 * CT;
+            v8 pw[2][RT], x[PD + 1];
             auto weights = [&](int b) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     const E* at = sp + (16 * r + col) * PS + 32 * b + 4 * g;
                     const v4 lo = load_vec<v4>(at), hi = load_vec<v4>(at + 16);
-                    pw[b][r] = v8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                    pw[b & 1][r] = v8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
                 }
             };
             weights(0);
+            ahead<NE, PD>(
+                [&](auto step) {
+                    constexpr int e = step;
+                    x[e % (PD + 1)] = c_cols(tile, 32 * (e / CT), 32 * (e / CT) + 16, e % CT);
+                },
+                [&](auto step) {
+                    constexpr int e = step, b = e / CT, c = e % CT;
+                    if constexpr (c == CT - 1 && b + 1 < TT / 2) weights(b + 1);
 #pragma unroll
-            for (int e = 0; e < PD; ++e) values(e);
-#pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                const int b = e / CT, c = e % CT;
-                if (e + PD < NE) values(e + PD);
-                if (c == CT - 1 - (PD > 1) && b + 1 < TT / 2) weights(b + 1);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r][c] = mma32(x[e % (PD + 1)], pw[b][r], acc[r][c]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+                    for (int r = 0; r < RT; ++r) acc[r][c] = mma32(x[e % (PD + 1)], pw[b & 1][r], acc[r][c]);
+                });
         }
         // the rows' sums over the waves
         __syncthreads();
-        if (scores)
-#pragma unroll
-            for (int j = 0; j < RQ; ++j) {
-                const float x = group_sum(l[j]);
-                if (g == 0) stat[tg][16 * (rg * RQ + j) + col] = x;
-            }
+        if (scores) {
+            const float x = group_sum(l);
+            if (g == 0) stat[tg][16 * rt + col] = x;
+        }
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == key_tiles;
         const int64_t out0 = (int64_t)q0 * a.H + row0;
         const int slot = 2 * run + (t0 == 0 ? 1 : 0);
 #pragma unroll
@@ -539,7 +497,7 @@ template <typename E, int DL>
 __global__ __launch_bounds__(256) void latent_join_parts_kernel(const DecodeSpace ws, E* __restrict__ o,
                                                                 float* __restrict__ lse, int BM)
 {
-    __shared__ float factor[512];
+    __shared__ float factor[DEC_RUNS];
     __shared__ float red[4][2];
     __shared__ __attribute__((aligned(16))) f32x4 part[16][16];
     const DecodeSplit x = ws.split[blockIdx.x];
@@ -547,26 +505,20 @@ __global__ __launch_bounds__(256) void latent_join_parts_kernel(const DecodeSpac
     if (row >= x.rows) return;
     const int parts = x.last - x.first + 1;   // at most one per run
     auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * x.first + 1 : 2 * (x.first + p)) * BM + row; };
-    float m[2], l[2], top = neg_inf();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int p = tid + 256 * i;
-        m[i] = p < parts ? ws.ml[slot(p) * 2] : neg_inf();
-        l[i] = p < parts ? ws.ml[slot(p) * 2 + 1] : 0.f;
-        top = fmaxf(top, m[i]);
+    float m = neg_inf(), l = 0.f;
+    if (tid < parts) {
+        m = ws.ml[slot(tid) * 2];
+        l = ws.ml[slot(tid) * 2 + 1];
     }
+    float top = m;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
     if (lane == 0) red[wave][0] = top;
     __syncthreads();
     top = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float f = m[i] == neg_inf() ? 0.f : exp2_fast(m[i] - top);
-        factor[tid + 256 * i] = f;
-        sum += f * l[i];
-    }
+    const float f = m == neg_inf() ? 0.f : exp2_fast(m - top);
+    factor[tid] = f;
+    float sum = f * l;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
     if (lane == 0) red[wave][1] = sum;
@@ -588,7 +540,7 @@ __global__ __launch_bounds__(256) void latent_join_parts_kernel(const DecodeSpac
     store_vec(o + (x.row + row) * DL + c, y);
     if (lse && tid == 0 && blockIdx.z == 0) lse[x.row + row] = sum == 0.f ? neg_inf() : (top + __log2f(sum)) * LN2;
 }
-static_assert(DecodeFew::GRID <= 512 && DecodeMany::GRID <= 512, "two parts a thread");
+static_assert(DEC_RUNS <= 256, "a thread per part");
 
 // Whether the rows of a sequence fit in a tile of 32 (in one of 64 more than
 // half would be empty).
@@ -596,8 +548,8 @@ static bool few_rows(int64_t total_tokens, int32_t N, int32_t H) { return (total
 
 size_t latent_decode_workspace(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t dl, bool bf16_io) {
     const bool few = few_rows(total_tokens, num_seqs, H);
-    if (bf16_io) return few ? space_bytes<DecodeFew>(dl) : space_bytes<DecodeMany>(dl);
-    return few ? space_bytes<DecodeFewF32>(dl) : space_bytes<DecodeManyF32>(dl);
+    (void)bf16_io;   // partial results are fp32 in either case
+    return few ? space_bytes<DecodeFew<float>>(dl) : space_bytes<DecodeMany<float>>(dl);
 }
 
 template <typename E, int DL, int DR, typename S>
@@ -606,9 +558,9 @@ static hipError_t launch(const LatentDecode& a, hipStream_t stream) {
     const int64_t rows = a.total_tokens * a.H;
     const int64_t bound = a.cu_seqlens ? rows / S::BM + a.num_seqs
                                        : (a.total_tokens / a.num_seqs * a.H + S::BM - 1) / S::BM * a.num_seqs;
-    const bool by_tile = bound <= S::GRID;
-    const int entries = by_tile ? (int)bound : S::GRID;
-    hipLaunchKernelGGL((latent_decode_kernel<E, DL, DR, S>), dim3(S::GRID), dim3(64 * S::NW), 0, stream, a, ws,
+    const bool by_tile = bound <= DEC_RUNS;
+    const int entries = by_tile ? (int)bound : DEC_RUNS;
+    hipLaunchKernelGGL((latent_decode_kernel<E, DL, DR, S>), dim3(DEC_RUNS), dim3(64 * DEC_WAVES), 0, stream, a, ws,
                        by_tile ? 1 : 0, entries);
     if (entries <= 32)   // 8 parts a row tile and more
         hipLaunchKernelGGL((latent_join_parts_kernel<E, DL>), dim3(entries, S::BM, DL / 64), dim3(256), 0, stream, ws,
@@ -622,10 +574,7 @@ static hipError_t launch(const LatentDecode& a, hipStream_t stream) {
 template <typename E, int DL, int DR>
 static hipError_t launch_rows(const LatentDecode& a, hipStream_t stream) {
     const bool few = few_rows(a.total_tokens, a.num_seqs, a.H);
-    if constexpr (sizeof(E) == 2)
-        return few ? launch<E, DL, DR, DecodeFew>(a, stream) : launch<E, DL, DR, DecodeMany>(a, stream);
-    else
-        return few ? launch<E, DL, DR, DecodeFewF32>(a, stream) : launch<E, DL, DR, DecodeManyF32>(a, stream);
+    return few ? launch<E, DL, DR, DecodeFew<E>>(a, stream) : launch<E, DL, DR, DecodeMany<E>>(a, stream);
 }
 
 hipError_t launch_latent_decode(const LatentDecode& a, bool bf16_io, hipStream_t stream) {
