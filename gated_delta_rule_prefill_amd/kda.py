@@ -7,9 +7,9 @@ raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -24,18 +24,6 @@ CHUNK = 64  # tokens per chunk of the chunkwise prefill (rows of chunk_states)
 # name -> (restype, argtypes) for every entry point of include/kda.h
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _f32, _f64, _u32 = ctypes.c_float, ctypes.c_double, ctypes.c_uint32
-
-
-class LatentInputs(ctypes.Structure):
-    """kda_latent_inputs of include/kda.h."""
-    _fields_ = ([(n, _vp) for n in ("q", "k", "v", "k_pe")] +
-                [(n, _i64) for n in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
-                                     "v_token_stride", "v_head_stride", "k_pe_token_stride")] +
-                [("cu_seqlens_q", _vp), ("cu_seqlens_k", _vp), ("total_q", _i64), ("total_k", _i64)] +
-                [(n, _i32) for n in ("num_seqs", "H", "dn", "dr", "dv", "dtype", "causal")] +
-                [("scale", _f32)])
-
-
 SIGNATURES = {
     "kda_prefill_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32, ctypes.c_int]),
     "kda_prefill": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32,
@@ -365,29 +353,47 @@ def prefill_kernel_times():
 
 # -- latent attention ------------------------------------------------------------
 
-# A decode step makes several of these calls per layer, so their checks compare
-# first and word a message only for a failure.
+# A decode step makes several of these calls per layer, so they look torch up
+# once, compare before they word a message, and enter a context only where one
+# is needed.
 
-_NOTHING = contextlib.nullcontext()
+_torch = None
 
 
-def _on(device, stream):
-    """Context of the device and stream a call runs on: its own stream argument
-    or the device's current one.  Outputs and workspaces the binding allocates
-    belong to that stream."""
-    import torch
+def _lib_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+_CODES = {}   # torch dtype -> KDA_DTYPE_*, filled on first use
+
+
+def _code(t) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        code = _CODES[t.dtype] = _dtype_code(t)
+    return code
+
+
+def _elsewhere(device, stream):
+    """Context that a call must enter: its stream argument's, or its tensors'
+    device's; None where they are on the current device and stream.  Outputs and
+    workspaces the binding allocates belong to the stream the call runs on."""
+    torch = _lib_torch()
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {device}")
     if stream is not None:
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
-    return _NOTHING
+    return None
 
 
 def _raw_stream(device) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _rows3(t, name, shape, dtype, device) -> None:
@@ -419,37 +425,49 @@ def _offsets(cu, name, device) -> int:
                      f"on {cu.device}")
 
 
+_INPUTS = struct.Struct("@4P7q2P2q7if")   # kda_latent_inputs of include/kda.h
+
+
 def _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale):
-    import torch
-    _require(q.dim() == 3 and k.dim() == 3 and v.dim() == 3, "q, k, v: [tokens, heads, channels]")
+    """The packed kda_latent_inputs, and (T, Tk, H, dn, dr, dv)."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v: [tokens, heads, channels]")
     T, H, dqk = q.shape
     Tk, _, dn = k.shape
-    dev = q.device
+    dv = v.shape[2]
+    dev, dt = q.device, q.dtype
     dr = dqk - dn
-    _require(dr >= 0, "q must have at least k's channels")
-    _rows3(q, "q", (T, H, dqk), q.dtype, dev)
-    _rows3(k, "k", (Tk, H, dn), q.dtype, dev)
-    _rows3(v, "v", (Tk, H, v.shape[2]), q.dtype, dev)
-    pes = 0
+    if dr < 0:
+        raise ValueError("q must have at least k's channels")
+    _rows3(q, "q", (T, H, dqk), dt, dev)
+    _rows3(k, "k", (Tk, H, dn), dt, dev)
+    _rows3(v, "v", (Tk, H, dv), dt, dev)
+    pe = pes = 0
     if dr:
-        _require(k_pe is not None, "q has channels beyond k's: k_pe is needed")
-        _rows3(k_pe, "k_pe", (Tk, dr), q.dtype, dev)
-        pes = _stride(k_pe, 0)
-    else:
-        _require(k_pe is None, "k_pe: q has no channels for it")
+        if k_pe is None:
+            raise ValueError("q has channels beyond k's: k_pe is needed")
+        _rows3(k_pe, "k_pe", (Tk, dr), dt, dev)
+        pe, pes = k_pe.data_ptr(), _stride(k_pe, 0)
+    elif k_pe is not None:
+        raise ValueError("k_pe: q has no channels for it")
+    cu = cuk = 0
     if cu_seqlens is not None:
         N = _offsets(cu_seqlens, "cu_seqlens", dev)
+        cu = cu_seqlens.data_ptr()
         if cu_seqlens_k is not None:
-            _require(_offsets(cu_seqlens_k, "cu_seqlens_k", dev) == N, "cu_seqlens_k: as many sequences as cu_seqlens")
+            if cu_seqlens_k is not cu_seqlens and _offsets(cu_seqlens_k, "cu_seqlens_k", dev) != N:
+                raise ValueError("cu_seqlens_k: as many sequences as cu_seqlens")
+            cuk = cu_seqlens_k.data_ptr()
     else:
-        _require(cu_seqlens_k is None, "cu_seqlens_k needs cu_seqlens")
+        if cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
         N = int(num_seqs or 1)
     if scale is None:
         scale = dqk ** -0.5
-    return LatentInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_pe), _stride(q, 0), _stride(q, 1),
-                        _stride(k, 0), _stride(k, 1), _stride(v, 0), _stride(v, 1), pes, _ptr(cu_seqlens),
-                        _ptr(cu_seqlens_k), T, Tk, N, H, dn, dr, v.shape[2], _dtype_code(q), 1 if causal else 0,
-                        scale)
+    packed = _INPUTS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), pe, _stride(q, 0), _stride(q, 1),
+                          _stride(k, 0), _stride(k, 1), _stride(v, 0), _stride(v, 1), pes, cu, cuk, T, Tk, N, H, dn,
+                          dr, dv, _code(q), 1 if causal else 0, scale)
+    return packed, (T, Tk, H, dn, dr, dv)
 
 
 def latent_attention(q, k, v, k_pe=None, cu_seqlens=None, cu_seqlens_k=None, num_seqs: Optional[int] = None,
@@ -463,20 +481,24 @@ def latent_attention(q, k, v, k_pe=None, cu_seqlens=None, cu_seqlens_k=None, num
     ``num_seqs`` equal rows.  scale: default (dn + dr)^-0.5.
     Returns (o [T, H, dn], lse [T, H] fp32).  Rows behind the last sequence are
     left as they were."""
-    import torch
-    a = _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale)
+    packed, (T, _, H, _, _, dv) = _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale)
     dev = q.device
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((a.total_q, a.H, a.dv), dtype=q.dtype, device=dev)
-        else:
-            _dense(out, "out", (a.total_q, a.H, a.dv), q.dtype, dev)
-        if lse is None:
-            lse = torch.empty((a.total_q, a.H), dtype=torch.float32, device=dev)
-        else:
-            _dense(lse, "lse", (a.total_q, a.H), torch.float32, dev)
-        st = lib().kda_latent_attention(ctypes.addressof(a), out.data_ptr(), lse.data_ptr(), _raw_stream(dev))
-    _check(st, "kda_latent_attention")
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return latent_attention(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale, out, lse)
+    torch = _torch
+    if out is None:
+        out = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+    else:
+        _dense(out, "out", (T, H, dv), q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _dense(lse, "lse", (T, H), torch.float32, dev)
+    st = lib().kda_latent_attention(packed, out.data_ptr(), lse.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "kda_latent_attention")
     return out, lse
 
 
@@ -488,45 +510,53 @@ def latent_attention_backward(q, k, v, o, lse, d_o, k_pe=None, cu_seqlens=None, 
     dv [Tk, H, dn] and dk_pe [Tk, dr] or None, in the inputs' type.  dk, dv:
     tensors to write (strided, e.g. the halves of one [Tk, H, 2 dn] gradient),
     or None to allocate both halves of one such tensor."""
-    import torch
-    a = _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale)
-    dev = q.device
-    _dense(o, "o", (a.total_q, a.H, a.dv), q.dtype, dev)
-    _dense(d_o, "d_o", (a.total_q, a.H, a.dv), q.dtype, dev)
-    _dense(lse, "lse", (a.total_q, a.H), torch.float32, dev)
-    with _on(dev, stream):
-        if dk is None and dv is None:
-            dkv = torch.empty((a.total_k, a.H, a.dn + a.dv), dtype=q.dtype, device=dev)
-            dk, dv = dkv[..., :a.dn], dkv[..., a.dn:]
-        else:
-            _require(dk is not None and dv is not None, "dk and dv: both or neither")
-            _rows3(dk, "dk", (a.total_k, a.H, a.dn), q.dtype, dev)
-            _rows3(dv, "dv", (a.total_k, a.H, a.dv), q.dtype, dev)
-        dq = torch.empty((a.total_q, a.H, a.dn + a.dr), dtype=q.dtype, device=dev)
-        dk_pe = torch.empty((a.total_k, a.dr), dtype=q.dtype, device=dev) if a.dr else None
-        need = int(lib().kda_latent_attention_backward_workspace_bytes(a.total_q, a.total_k, a.H, a.dr))
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
-        st = lib().kda_latent_attention_backward(
-            ctypes.addressof(a), o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-            _stride(dk, 0), _stride(dk, 1), dv.data_ptr(), _stride(dv, 0), _stride(dv, 1), _ptr(dk_pe),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev))
-    _check(st, "kda_latent_attention_backward")
+    packed, (T, Tk, H, dn, dr, dvw) = _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, scale)
+    dev, dt = q.device, q.dtype
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return latent_attention_backward(q, k, v, o, lse, d_o, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal,
+                                             scale, dk, dv, workspace)
+    torch = _torch
+    _dense(o, "o", (T, H, dvw), dt, dev)
+    _dense(d_o, "d_o", (T, H, dvw), dt, dev)
+    _dense(lse, "lse", (T, H), torch.float32, dev)
+    if dk is None and dv is None:
+        dkv = torch.empty((Tk, H, dn + dvw), dtype=dt, device=dev)
+        dk, dv = dkv[..., :dn], dkv[..., dn:]
+    else:
+        _require(dk is not None and dv is not None, "dk and dv: both or neither")
+        _rows3(dk, "dk", (Tk, H, dn), dt, dev)
+        _rows3(dv, "dv", (Tk, H, dvw), dt, dev)
+    dq = torch.empty((T, H, dn + dr), dtype=dt, device=dev)
+    dk_pe = torch.empty((Tk, dr), dtype=dt, device=dev) if dr else None
+    if workspace is None:
+        workspace = torch.empty(lib().kda_latent_attention_backward_workspace_bytes(T, Tk, H, dr), dtype=torch.uint8,
+                                device=dev)
+    else:
+        _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
+    st = lib().kda_latent_attention_backward(
+        packed, o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), _stride(dk, 0),
+        _stride(dk, 1), dv.data_ptr(), _stride(dv, 0), _stride(dv, 1), _ptr(dk_pe), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(dev))
+    if st:
+        _check(st, "kda_latent_attention_backward")
     return dict(dq=dq, dk=dk, dv=dv, dk_pe=dk_pe)
 
 
-def _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs, T):
-    """Sequences of a paged call, with its shared arguments checked."""
-    import torch
-    dev = cache.device
-    _require(cache.dim() == 3 and cache.is_contiguous(), "cache: contiguous [pages, page_size, channels]")
-    N = _offsets(cu_seqlens, "cu_seqlens", dev) if cu_seqlens is not None else \
-        int(num_seqs) if num_seqs is not None else seq_lens.shape[0]
-    _require(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == N and
-             block_table.device == dev and block_table.is_contiguous(), "block_table: contiguous int32 [N, max_pages]")
-    _dense(seq_lens, "seq_lens", (N,), torch.int32, dev)
+def _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs) -> int:
+    """Number of sequences of a paged call, with its shared arguments checked."""
+    int32, dev = _lib_torch().int32, cache.device
+    if cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError("cache: contiguous [pages, page_size, channels]")
+    if cu_seqlens is not None:
+        N = _offsets(cu_seqlens, "cu_seqlens", dev)
+    else:
+        N = int(num_seqs) if num_seqs is not None else seq_lens.shape[0]
+    if not (block_table.dtype is int32 and block_table.dim() == 2 and block_table.shape[0] == N and
+            block_table.device == dev and block_table.is_contiguous()):
+        raise ValueError("block_table: contiguous int32 [N, max_pages], on the cache's device")
+    _dense(seq_lens, "seq_lens", (N,), int32, dev)
     return N
 
 
@@ -546,35 +576,42 @@ def latent_decode(q, cache, block_table, seq_lens, latent_dim: int, scale: float
     offsets of the new tokens, or None for T / N each.  latent_dim = dl; scale:
     of the heads before absorption, e.g. (dn + dr)^-0.5.
     Returns (o [T, H, dl], lse [T, H] fp32)."""
-    import torch
-    _require(q.dim() == 3, "q: [T, H, dl + dr]")
+    if q.dim() != 3:
+        raise ValueError("q: [T, H, dl + dr]")
     T, H, width = q.shape
-    N = _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs, T)
-    dev = cache.device
-    _rows3(q, "q", (T, H, cache.shape[2]), cache.dtype, dev)
+    N = _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs)
+    dev, dt = cache.device, cache.dtype
+    P, page, cw = cache.shape
+    _rows3(q, "q", (T, H, cw), dt, dev)
     dl = int(latent_dim)
-    dr = width - dl
-    code = _dtype_code(q)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((T, H, dl), dtype=q.dtype, device=dev)
-        else:
-            _dense(out, "out", (T, H, dl), q.dtype, dev)
-        if lse is None:
-            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-        else:
-            _dense(lse, "lse", (T, H), torch.float32, dev)
-        if workspace is None:
-            workspace = torch.empty(int(lib().kda_latent_decode_workspace_bytes(T, N, H, dl, dr, code)),
-                                    dtype=torch.uint8, device=dev)
-        else:
-            _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
-        st = lib().kda_latent_decode(
-            q.data_ptr(), _stride(q, 0), _stride(q, 1), cache.data_ptr(), cache.shape[0], cache.shape[1],
-            block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), _ptr(cu_seqlens), T, N, H, dl, dr,
-            code, scale, out.data_ptr(), lse.data_ptr(), _ptr(workspace) or None,
-            workspace.numel() * workspace.element_size(), _raw_stream(dev))
-    _check(st, "kda_latent_decode")
+    dr, code = width - dl, _code(q)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return latent_decode(q, cache, block_table, seq_lens, latent_dim, scale, cu_seqlens, num_seqs, out, lse,
+                                 workspace)
+    torch = _torch
+    if out is None:
+        out = torch.empty((T, H, dl), dtype=dt, device=dev)
+    else:
+        _dense(out, "out", (T, H, dl), dt, dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _dense(lse, "lse", (T, H), torch.float32, dev)
+    handle = lib()
+    if workspace is None:
+        need = handle.kda_latent_decode_workspace_bytes(T, N, H, dl, dr, code)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
+        need = workspace.numel() * workspace.element_size()
+    st = handle.kda_latent_decode(
+        q.data_ptr(), _stride(q, 0), _stride(q, 1), cache.data_ptr(), P, page, block_table.data_ptr(),
+        block_table.shape[1], seq_lens.data_ptr(), _ptr(cu_seqlens), T, N, H, dl, dr, code, scale, out.data_ptr(),
+        lse.data_ptr(), workspace.data_ptr() or None, need, _raw_stream(dev))
+    if st:
+        _check(st, "kda_latent_decode")
     return out, lse
 
 
@@ -590,42 +627,50 @@ def latent_append(cache, c, block_table, seq_lens, k_pe=None, cu_seqlens=None, n
     inv_freq: fp32 [dr / 2], or None for no rotation; mscale multiplies the
     rotated part.  c_out, k_pe_out: True (allocate) or a dense tensor for the
     normalised latents and rotated key parts.  Returns (c_out, k_pe_out)."""
-    import torch
-    _require(c.dim() == 2, "c: [T, dl]")
+    if c.dim() != 2:
+        raise ValueError("c: [T, dl]")
     T, dl = c.shape
-    N = _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs, T)
-    dev = cache.device
-    dr = cache.shape[2] - dl
-    _rows3(c, "c", (T, dl), cache.dtype, dev)
+    N = _paged(cache, block_table, seq_lens, cu_seqlens, num_seqs)
+    dev, dt, float32 = cache.device, cache.dtype, _torch.float32
+    P, page, width = cache.shape
+    dr = width - dl
+    _rows3(c, "c", (T, dl), dt, dev)
+    pe = pes = None
     if dr:
-        _require(k_pe is not None, "the cache has channels beyond c's: k_pe is needed")
-        _rows3(k_pe, "k_pe", (T, dr), cache.dtype, dev)
-    else:
-        _require(k_pe is None, "k_pe: the cache has no channels for it")
+        if k_pe is None:
+            raise ValueError("the cache has channels beyond c's: k_pe is needed")
+        _rows3(k_pe, "k_pe", (T, dr), dt, dev)
+        pe, pes = k_pe.data_ptr(), _stride(k_pe, 0)
+    elif k_pe is not None:
+        raise ValueError("k_pe: the cache has no channels for it")
     if norm_weight is not None:
-        _dense(norm_weight, "norm_weight", (dl,), torch.float32, dev)
+        _dense(norm_weight, "norm_weight", (dl,), float32, dev)
     if inv_freq is not None:
-        _dense(inv_freq, "inv_freq", (dr // 2,), torch.float32, dev)
-    code = _dtype_code(cache)
-    with _on(dev, stream):
-        if c_out is True:
-            c_out = torch.empty((T, dl), dtype=c.dtype, device=dev)
-        elif c_out is not None and c_out is not False:
-            _dense(c_out, "c_out", (T, dl), c.dtype, dev)
-        else:
-            c_out = None
-        if k_pe_out is True:
-            k_pe_out = torch.empty((T, dr), dtype=c.dtype, device=dev)
-        elif k_pe_out is not None and k_pe_out is not False:
-            _dense(k_pe_out, "k_pe_out", (T, dr), c.dtype, dev)
-        else:
-            k_pe_out = None
-        st = lib().kda_latent_append(
-            cache.data_ptr(), cache.shape[0], cache.shape[1], block_table.data_ptr(), block_table.shape[1],
-            seq_lens.data_ptr(), _ptr(cu_seqlens), T, N, dl, dr, code, c.data_ptr(), _stride(c, 0), _ptr(k_pe),
-            _stride(k_pe, 0) if dr else 0, _ptr(norm_weight), eps, _ptr(inv_freq), mscale,
-            KDA_ROTARY_INTERLEAVED if interleaved else 0, _ptr(c_out), _ptr(k_pe_out), _raw_stream(dev))
-    _check(st, "kda_latent_append")
+        _dense(inv_freq, "inv_freq", (dr // 2,), float32, dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return latent_append(cache, c, block_table, seq_lens, k_pe, cu_seqlens, num_seqs, norm_weight, eps,
+                                 inv_freq, interleaved, mscale, c_out, k_pe_out)
+    if c_out is True:
+        c_out = _torch.empty((T, dl), dtype=dt, device=dev)
+    elif c_out is None or c_out is False:
+        c_out = None
+    else:
+        _dense(c_out, "c_out", (T, dl), dt, dev)
+    if k_pe_out is True:
+        k_pe_out = _torch.empty((T, dr), dtype=dt, device=dev)
+    elif k_pe_out is None or k_pe_out is False:
+        k_pe_out = None
+    else:
+        _dense(k_pe_out, "k_pe_out", (T, dr), dt, dev)
+    st = lib().kda_latent_append(
+        cache.data_ptr(), P, page, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
+        _ptr(cu_seqlens), T, N, dl, dr, _code(cache), c.data_ptr(), _stride(c, 0), pe, pes or 0, _ptr(norm_weight), eps,
+        _ptr(inv_freq), mscale, KDA_ROTARY_INTERLEAVED if interleaved else 0, _ptr(c_out), _ptr(k_pe_out),
+        _raw_stream(dev))
+    if st:
+        _check(st, "kda_latent_append")
     return c_out, k_pe_out
 
 
@@ -636,26 +681,29 @@ def rotary(x, positions, inv_freq, start: int = 0, interleaved: bool = False, ms
     positions: int32 [T]; inv_freq: fp32 [dr / 2]; inverse: the gradient of the
     rotation.  out: None (allocate), x itself (in place), or a [T, H, d] tensor
     that does not overlap x.  Returns the rotated tensor."""
-    import torch
-    _require(x.dim() == 3, "x: [T, H, d]")
+    if x.dim() != 3 or inv_freq.dim() != 1:
+        raise ValueError("x: [T, H, d]; inv_freq: [dr / 2]")
+    torch = _lib_torch()
     T, H, d = x.shape
-    dev = x.device
-    _rows3(x, "x", (T, H, d), x.dtype, dev)
+    dev, dt = x.device, x.dtype
+    _rows3(x, "x", (T, H, d), dt, dev)
     _dense(positions, "positions", (T,), torch.int32, dev)
-    _require(inv_freq.dim() == 1, "inv_freq: fp32 [dr / 2]")
-    _dense(inv_freq, "inv_freq", inv_freq.shape, torch.float32, dev)
-    code = _dtype_code(x)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((T, H, d), dtype=x.dtype, device=dev)
-        else:
-            _rows3(out, "out", (T, H, d), x.dtype, dev)
-        st = lib().kda_rotary(x.data_ptr(), _stride(x, 0), _stride(x, 1), out.data_ptr(), _stride(out, 0), _stride(out, 1),
-                              positions.data_ptr(), inv_freq.data_ptr(), T, H, d, int(start),
-                              2 * inv_freq.shape[0], code, mscale,
-                              (KDA_ROTARY_INTERLEAVED if interleaved else 0) | (KDA_ROTARY_INVERSE if inverse else 0),
-                              _raw_stream(dev))
-    _check(st, "kda_rotary")
+    half = inv_freq.shape[0]
+    _dense(inv_freq, "inv_freq", (half,), torch.float32, dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return rotary(x, positions, inv_freq, start, interleaved, mscale, inverse, out)
+    if out is None:
+        out = torch.empty((T, H, d), dtype=dt, device=dev)
+    else:
+        _rows3(out, "out", (T, H, d), dt, dev)
+    st = lib().kda_rotary(x.data_ptr(), _stride(x, 0), _stride(x, 1), out.data_ptr(), _stride(out, 0), _stride(out, 1),
+                          positions.data_ptr(), inv_freq.data_ptr(), T, H, d, start, 2 * half, _code(x), mscale,
+                          (KDA_ROTARY_INTERLEAVED if interleaved else 0) | (KDA_ROTARY_INVERSE if inverse else 0),
+                          _raw_stream(dev))
+    if st:
+        _check(st, "kda_rotary")
     return out
 
 

@@ -239,18 +239,16 @@ def test_other_stream():
 
 def test_workspace_of_the_library():
     """NULL workspace through the C ABI: allocated on the stream; the same gradients."""
-    import ctypes
-
     from gated_delta_rule_prefill_amd import kda as b
     lens = [65, 20]
     x = make(25, "bf16", 2, 128, 64, lens, lens)
     want = both(x, lens, lens, True)
     cu = offsets(lens)
-    a = b._latent_inputs(x["q"], x["k"], x["v"], x["k_pe"], cu, None, None, True, x["scale"])
+    a, _ = b._latent_inputs(x["q"], x["k"], x["v"], x["k_pe"], cu, None, None, True, x["scale"])
     got = {n: torch.empty_like(t).contiguous() for n, t in want.items()}
     dk, dv = got["dk"], got["dv"]
     st = b.lib().kda_latent_attention_backward(
-        ctypes.addressof(a), want["o"].data_ptr(), want["lse"].data_ptr(), x["d_o"].data_ptr(), got["dq"].data_ptr(),
+        a, want["o"].data_ptr(), want["lse"].data_ptr(), x["d_o"].data_ptr(), got["dq"].data_ptr(),
         dk.data_ptr(), dk.stride(0), dk.stride(1), dv.data_ptr(), dv.stride(0), dv.stride(1), got["dk_pe"].data_ptr(),
         None, 0, torch.cuda.current_stream().cuda_stream)
     assert st == b.KDA_OK, b.last_error()

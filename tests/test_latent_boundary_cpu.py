@@ -1,6 +1,5 @@
 """The latent-attention entry points without a GPU: bad arguments are rejected
 before any HIP call, with the status the header documents."""
-import ctypes
 import math
 
 import pytest
@@ -15,9 +14,9 @@ def _inputs(**kw):
     d = dict(q=A, k=A, v=A, k_pe=A, q_token_stride=768, q_head_stride=192, k_token_stride=1024, k_head_stride=256,
              v_token_stride=1024, v_head_stride=256, k_pe_token_stride=64, cu_seqlens_q=A, cu_seqlens_k=None,
              total_q=100, total_k=100, num_seqs=2, H=4, dn=128, dr=64, dv=128, dtype=kda.KDA_DTYPE_BF16, causal=1,
-             scale=0.1)
+             scale=0.1)   # in the order of kda_latent_inputs
     d.update(kw)
-    return kda.LatentInputs(**d)
+    return kda._INPUTS.pack(*(x or 0 for x in d.values()))
 
 
 BAD_INPUTS = [
@@ -28,31 +27,31 @@ BAD_INPUTS = [
     (dict(total_k=99), INVALID), (dict(cu_seqlens_q=None, cu_seqlens_k=A), INVALID),
     (dict(cu_seqlens_q=None, num_seqs=3), INVALID), (dict(q=None), INVALID), (dict(v=None), INVALID),
     (dict(k_pe=None), INVALID), (dict(k=A + 8), INVALID), (dict(q_token_stride=7), INVALID),
-    (dict(k_head_stride=-8), INVALID), (dict(total_q=2 ** 30, total_k=2 ** 30, H=65535), INVALID),
+    (dict(k_head_stride=-8), INVALID), (dict(total_q=2 ** 30, total_k=2 ** 30, H=65535), INVALID), (dict(k_token_stride=1 << 23), INVALID),
 ]
 
 
 @pytest.mark.parametrize("kw,status", BAD_INPUTS)
 def test_attention_rejects(kw, status):
     a = _inputs(**kw)
-    assert kda.lib().kda_latent_attention(ctypes.addressof(a), A, A, None) == status
+    assert kda.lib().kda_latent_attention(a, A, A, None) == status
     assert kda.last_error()
 
 
 def test_attention_rejects_outputs_and_accepts_nothing_to_do():
     lib, a = kda.lib(), _inputs()
     assert lib.kda_latent_attention(None, A, A, None) == INVALID
-    assert lib.kda_latent_attention(ctypes.addressof(a), None, A, None) == INVALID
-    assert lib.kda_latent_attention(ctypes.addressof(a), A + 4, A, None) == INVALID
+    assert lib.kda_latent_attention(a, None, A, None) == INVALID
+    assert lib.kda_latent_attention(a, A + 4, A, None) == INVALID
     a = _inputs(total_q=0, total_k=0)
-    assert lib.kda_latent_attention(ctypes.addressof(a), None, None, None) == kda.KDA_OK
+    assert lib.kda_latent_attention(a, None, None, None) == kda.KDA_OK
 
 
 def _backward(inputs=None, **kw):
     d = dict(o=A, lse=A, d_o=A, dq=A, dk=A, dkt=1024, dkh=256, dv=A, dvt=1024, dvh=256, pe=A, ws=A, wsb=1 << 40)
     d.update(kw)
     a = _inputs(**(inputs or {}))
-    return kda.lib().kda_latent_attention_backward(ctypes.addressof(a), d["o"], d["lse"], d["d_o"], d["dq"], d["dk"],
+    return kda.lib().kda_latent_attention_backward(a, d["o"], d["lse"], d["d_o"], d["dq"], d["dk"],
                                                    d["dkt"], d["dkh"], d["dv"], d["dvt"], d["dvh"], d["pe"], d["ws"],
                                                    d["wsb"], None)
 
