@@ -69,6 +69,11 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
                                   in.k_pe_token_stride, nk - t * BN);
         sv.load_rows(tid, vp + key * in.v_token_stride, in.v_token_stride, nk - t * BN);
     };
+    auto store = [&](int t, bool hides) {
+        if (hides) move_bad_rows(tid, sv, sk);
+        sk.store(tid, smem[t & 1]);
+        sv.store(tid, smem[t & 1] + BN * DQK);
+    };
     const RowReader<E, DQK> k_rows(lane);
     const ColReader<E, DV, DV / 16> v_cols(lane);
 
@@ -83,11 +88,12 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     }
     if (nt > 0) {
         load(0);
-        sk.store(tid, smem[0]);
-        sv.store(tid, smem[0] + BN * DQK);
+        store(0, true);
     }
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
+    // Tile t of the keys; hides: some row does not see all of the keys of it or
+    // of the next one.
+    auto step = [&](int t, auto hides) {
         const E* K = smem[t & 1];
         const E* V = K + BN * DQK;
         if (t + 1 < nt) load(t + 1);
@@ -104,7 +110,7 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
             constexpr int E0 = TT * KS;
             v8 p[NQ][TT / 2];
             auto take_weights = [&]() {
-                if ((t + 1) * BN > wave_full) {
+                if (hides && (t + 1) * BN > wave_full) {
 #pragma unroll
                     for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -154,13 +160,13 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
                 }
             };
             ahead<E0 + DV / 16 * (TT / 2), PD>(
-                [&](auto step) {
-                    constexpr int e = step, f = e - E0;
+                [&](auto n) {
+                    constexpr int e = n, f = e - E0;
                     if constexpr (e < E0) x[e % (PD + 1)] = k_rows(K, 16 * (e / (2 * KS) * 2 + e % 2), e / 2 % KS);
                     else x[e % (PD + 1)] = v_cols(V, 32 * (f / (DV / 16)), 32 * (f / (DV / 16)) + 16, f % (DV / 16));
                 },
-                [&](auto step) {
-                    constexpr int e = step, f = e - E0;
+                [&](auto n) {
+                    constexpr int e = n, f = e - E0;
                     if constexpr (e < E0) {
 #pragma unroll
                         for (int j = 0; j < NQ; ++j)
@@ -174,13 +180,13 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
                     }
                 });
         }
-        if (t + 1 < nt) {
-            E* next = smem[(t + 1) & 1];
-            sk.store(tid, next);
-            sv.store(tid, next + BN * DQK);
-        }
+        if (t + 1 < nt) store(t + 1, hides);
         __syncthreads();
-    }
+    };
+    const int full = in.causal ? min(nk, tile * BQ + off + 1) : nk;   // keys all the workgroup's rows see
+    int t = 0;
+    for (; t < full / BN - 1; ++t) step(t, Int<0>());
+    for (; t < nt; ++t) step(t, Int<1>());
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;

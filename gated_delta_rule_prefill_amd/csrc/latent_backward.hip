@@ -16,14 +16,6 @@
 
 namespace kda {
 
-// Key tiles of a wave of the dk, dv kernel and its waves per SIMD.
-#ifndef XNK
-#define XNK 1
-#define XWV 2
-#endif
-template <typename E> constexpr int DKV_NK = sizeof(E) == 2 ? XNK : 1;
-template <typename E> constexpr int DKV_WAVES = sizeof(E) == 2 ? XWV : 2;
-
 // dq and delta.  As in the forward kernel the scores are formed transposed
 // (rows = keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.
 template <typename E, int DN, int DR>
@@ -94,6 +86,11 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                                   in.k_pe_token_stride, nk - t * BN);
         sv.load_rows(tid, vp + key * in.v_token_stride, in.v_token_stride, nk - t * BN);
     };
+    auto store = [&](int t, bool hides) {
+        if (hides) move_bad_rows(tid, sk, sv);
+        sk.store(tid, smem[t & 1]);
+        sv.store(tid, smem[t & 1] + BN * DQK);
+    };
     const RowReader<E, DQK> k_rows(lane);
     const RowReader<E, DV> v_rows(lane);
     const ColReader<E, DQK, DQK / 16> k_cols(lane);
@@ -105,11 +102,12 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         for (int c = 0; c < DQK / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (nt > 0) {
         load(0);
-        sk.store(tid, smem[0]);
-        sv.store(tid, smem[0] + BN * DQK);
+        store(0, true);
     }
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
+    // Tile t of the keys; hides: some row does not see all of the keys of it or
+    // of the next one.
+    auto step = [&](int t, auto hides) {
         const E* K = smem[t & 1];
         const E* V = K + BN * DQK;
         if (t + 1 < nt) load(t + 1);
@@ -130,14 +128,14 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                 for (int j = 0; j < NQ; ++j) y[vs & 1][j] = load_frag(sgo[wave][j][vs], lane);
             };
             ahead<E1 + DQK / 16, PD>(
-                [&](auto step) {
-                    constexpr int e = step;
+                [&](auto n) {
+                    constexpr int e = n;
                     x[e % (PD + 1)] = e < E0   ? k_rows(K, 16 * (e % TT), e / TT)
                                       : e < E1 ? v_rows(V, 16 * ((e - E0) % TT), (e - E0) / TT)
                                                : k_cols(K, 0, 16, e - E1);
                 },
-                [&](auto step) {
-                    constexpr int e = step;
+                [&](auto n) {
+                    constexpr int e = n;
                     if (e < E0) {
                         if (e == E0 - 2) row_grads(0);
 #pragma unroll
@@ -154,7 +152,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                         }
                     } else {
                         if (e == E1) {
-                            if ((t + 1) * BN > wave_full) {   // weights of hidden keys
+                            if (hides && (t + 1) * BN > wave_full) {   // weights of hidden keys
 #pragma unroll
                                 for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -181,13 +179,13 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                     }
                 });
         }
-        if (t + 1 < nt) {
-            E* next = smem[(t + 1) & 1];
-            sk.store(tid, next);
-            sv.store(tid, next + BN * DQK);
-        }
+        if (t + 1 < nt) store(t + 1, hides);
         __syncthreads();
-    }
+    };
+    const int full = in.causal ? min(nk, tile * BQ + off + 1) : nk;   // keys all the workgroup's rows see
+    int t = 0;
+    for (; t < full / BN - 1; ++t) step(t, Int<0>());
+    for (; t < nt; ++t) step(t, Int<1>());
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;
@@ -205,17 +203,17 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     }
 }
 
-// dk, dv and the head's part of dk_pe.  A wave owns 16 NK keys, whose k and v
+// dk, dv and the head's part of dk_pe.  A wave owns 16 keys, whose k and v
 // operands and gradients stay in registers; the query rows come 32 at a time.
 // The scores are formed with rows = queries, so that the weights and dz are the
 // operands of dv^T += g^T w and dk^T += q^T dz as they stand.
 template <typename E, int DN, int DR>
-__global__ __launch_bounds__(256, DKV_WAVES<E>) void latent_dkv_kernel(
+__global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
     const kda_latent_inputs in, const float* __restrict__ lse, const E* __restrict__ d_o,
     const float* __restrict__ delta, E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
     E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ pe_part, int tiles)
 {
-    constexpr int DQK = DN + DR, DV = DN, BQ = 32, NK = DKV_NK<E>, BK = 64 * NK;
+    constexpr int DQK = DN + DR, DV = DN, BQ = 32, BK = 64;
     constexpr int KS = DQK / 32, VS = DV / 32, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BQ * (DQK + DV)];
@@ -233,162 +231,159 @@ __global__ __launch_bounds__(256, DKV_WAVES<E>) void latent_dkv_kernel(
     sequence_rows(cu_k, rows_k, (int)in.total_k, seq, k0, k1);
     const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
-    const int key0 = tile * BK, wkey = key0 + 16 * NK * wave;
+    const int key0 = tile * BK, wkey = key0 + 16 * wave;
     const float sc = in.scale * LOG2E;
 
-    v8 k[NK][KS], v[NK][VS];
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-        const int64_t row = k0 + min(wkey + 16 * n + col, nk - 1);
+    v8 k[KS], v[VS];
+    {
+        const int64_t row = k0 + min(wkey + col, nk - 1);
         const E* kp = (const E*)in.k + row * in.k_token_stride + h * in.k_head_stride;
         const E* vp = (const E*)in.v + row * in.v_token_stride + h * in.v_head_stride;
         const E* pp = DR ? (const E*)in.k_pe + row * in.k_pe_token_stride : nullptr;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-            k[n][ks] = 32 * ks < DN ? row_frag_global(kp, ks, lane) : row_frag_global(pp, ks - DN / 32, lane);
+            k[ks] = 32 * ks < DN ? row_frag_global(kp, ks, lane) : row_frag_global(pp, ks - DN / 32, lane);
 #pragma unroll
-        for (int vs = 0; vs < VS; ++vs) v[n][vs] = row_frag_global(vp, vs, lane);
+        for (int vs = 0; vs < VS; ++vs) v[vs] = row_frag_global(vp, vs, lane);
     }
     const int nt = (nq + BQ - 1) / BQ;
     const int t0 = in.causal ? min(nt, max(0, key0 - off) / BQ) : 0;   // rows before it see none of the keys
 
     const E* qp = (const E*)in.q + (int64_t)q0 * in.q_token_stride + h * in.q_head_stride;
     const E* gp = d_o + ((int64_t)q0 * in.H + h) * DV;
-    Stage<E, DQK, BQ, 256> sq;
+    typedef Stage<E, DQK, BQ, 256> SQ;
+    SQ sq;
     Stage<E, DV, BQ, 256> sg;
+    static_assert(SQ::P == 1 && SQ::TPR == 8, "a row per 8 threads");
     float srow_next = 0.f;
-    auto load = [&](int t) {
+    // Each of 2 BQ threads carries a row's lse or delta: the first wave where all
+    // keys are seen (one load for the workgroup: dkv 2.95 ms instead of 3.09);
+    // else the row's own first and second thread, which know whether it is finite.
+    auto part = [&](bool hides) { return !hides ? tid : tid % SQ::TPR < 2 ? tid % SQ::TPR * BQ + tid / SQ::TPR : 2 * BQ; };
+    auto load = [&](int t, bool hides) {
         sq.load_rows(tid, qp + (int64_t)t * BQ * in.q_token_stride, in.q_token_stride, nq - t * BQ);
         sg.load_rows(tid, gp + (int64_t)t * BQ * in.H * DV, (int64_t)in.H * DV, nq - t * BQ);
-        if (tid < 2 * BQ) {   // rows behind the last weigh nothing: lse = inf
-            const int i = t * BQ + (tid & (BQ - 1));
+        if (part(hides) < 2 * BQ) {   // rows behind the last weigh nothing: lse = inf
+            const int i = t * BQ + part(hides) % BQ;
             const int64_t at = (int64_t)(q0 + min(i, nq - 1)) * in.H + h;
-            if (tid < BQ) srow_next = i < nq ? lse[at] * LOG2E : __builtin_inff();
+            if (part(hides) < BQ) srow_next = i < nq ? lse[at] * LOG2E : __builtin_inff();
             else srow_next = i < nq ? delta[at] : 0.f;
         }
     };
-    auto store = [&](int b) {
-        sq.store(tid, smem[b]);
-        sg.store(tid, smem[b] + BQ * DQK);
-        if (tid < 2 * BQ) srow[b][tid] = srow_next;
+    auto store = [&](int t, bool hides) {
+        if (hides) {
+            const bool bad_delta = tid % SQ::TPR == 1 && !(__builtin_fabsf(srow_next) < __builtin_inff());
+            if (sq.bad_row(tid, 0) | sg.bad_row(tid, 0, bad_delta)) {   // as move_bad_rows: lse becomes NaN
+                sq.fill_row(0, 0u);
+                sg.fill_row(0, 0u);
+                srow_next = tid % SQ::TPR == 0 ? __builtin_nanf("") : 0.f;
+            }
+        }
+        sq.store(tid, smem[t & 1]);
+        sg.store(tid, smem[t & 1] + BQ * DQK);
+        if (part(hides) < 2 * BQ) srow[t & 1][part(hides)] = srow_next;
     };
 
     const RowReader<E, DQK> q_rows(lane);
     const RowReader<E, DV> g_rows(lane);
     const ColReader<E, DQK, DQK / 16> q_cols(lane);
     const ColReader<E, DV, DV / 16> g_cols(lane);
-    f32x4 ak[NK][DQK / 16], av[NK][DV / 16];
+    f32x4 ak[DQK / 16], av[DV / 16];
 #pragma unroll
-    for (int n = 0; n < NK; ++n) {
+    for (int c = 0; c < DQK / 16; ++c) ak[c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < DQK / 16; ++c) ak[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < DV / 16; ++c) av[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int c = 0; c < DV / 16; ++c) av[c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (t0 < nt) {
-        load(t0);
-        store(t0 & 1);
+        load(t0, in.causal);
+        store(t0, in.causal);
     }
     __syncthreads();
-    for (int t = t0; t < nt; ++t) {
+    // Tile t of the rows; hides: some row of it does not see all of the keys.
+    auto step = [&](int t, auto hides) {
         const E* Q = smem[t & 1];
         const E* G = Q + BQ * DQK;
         const float* R = srow[t & 1];
-        if (t + 1 < nt) load(t + 1);
-        if (!in.causal || t * BQ + BQ - 1 + off >= wkey) {
-            f32x4 s[NK][2], dp[NK][2];
+        if (t + 1 < nt) load(t + 1, hides);
+        if (!hides || t * BQ + BQ - 1 + off >= wkey) {
+            f32x4 s[2], dp[2];
             v8 x[PD + 1];
 #pragma unroll
-            for (int n = 0; n < NK; ++n)
-#pragma unroll
-                for (int a = 0; a < 2; ++a) s[n][a] = dp[n][a] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int a = 0; a < 2; ++a) s[a] = dp[a] = f32x4{0.f, 0.f, 0.f, 0.f};
             const f32x4 ls[2] = {*reinterpret_cast<const f32x4*>(R + 4 * g), *reinterpret_cast<const f32x4*>(R + 16 + 4 * g)};
             const f32x4 de[2] = {*reinterpret_cast<const f32x4*>(R + BQ + 4 * g),
                                  *reinterpret_cast<const f32x4*>(R + BQ + 16 + 4 * g)};
-            const bool masked = in.causal && t * BQ + off < wkey + 16 * NK - 1;   // some row sees not all of the keys
             // One sequence of operands, read ahead across its parts: z = q k^T;
             // g v^T, between whose products the weights' exponentials run;
             // dv^T += g^T w, between whose products dz is formed; dk^T += q^T dz.
-            constexpr int E0 = 2 * KS, E1 = E0 + 2 * VS, E2 = E1 + DV / 16, NS = 8 * NK;
-            v8 wf[NK], zf[NK];
+            constexpr int E0 = 2 * KS, E1 = E0 + 2 * VS, E2 = E1 + DV / 16, NS = 8;
+            v8 wf, zf;
             ahead<E2 + DQK / 16, PD>(
-                [&](auto step) {
-                    constexpr int e = step;
+                [&](auto n) {
+                    constexpr int e = n;
                     x[e % (PD + 1)] = e < E0   ? q_rows(Q, 16 * (e % 2), e / 2)
                                       : e < E1 ? g_rows(G, 16 * ((e - E0) % 2), (e - E0) / 2)
                                       : e < E2 ? g_cols(G, 0, 16, e - E1)
                                                : q_cols(Q, 0, 16, e - E2);
                 },
-                [&](auto step) {
-                    constexpr int e = step;
+                [&](auto n) {
+                    constexpr int e = n;
                     const v8& a = x[e % (PD + 1)];
                     if (e < E0) {
-#pragma unroll
-                        for (int n = 0; n < NK; ++n) s[n][e % 2] = mma32(a, k[n][e < E0 ? e / 2 : 0], s[n][e % 2]);
+                        s[e % 2] = mma32(a, k[e < E0 ? e / 2 : 0], s[e % 2]);
                     } else if (e < E1) {
                         const int f = e < E1 ? e - E0 : 0;
-#pragma unroll
-                        for (int n = 0; n < NK; ++n) dp[n][f % 2] = mma32(a, v[n][f / 2], dp[n][f % 2]);
+                        dp[f % 2] = mma32(a, v[f / 2], dp[f % 2]);
 #pragma unroll
                         for (int i = NS * f / (2 * VS); i < NS * (f + 1) / (2 * VS); ++i)
-                            s[i / 8][i / 4 % 2][i % 4] =
-                                exp2_fast(__builtin_fmaf(s[i / 8][i / 4 % 2][i % 4], sc, -ls[i / 4 % 2][i % 4]));
+                            s[i / 4][i % 4] = exp2_fast(__builtin_fmaf(s[i / 4][i % 4], sc, -ls[i / 4][i % 4]));
                     } else if (e < E2) {
                         const int c = e < E2 ? e - E1 : 0;
                         if (c == 0) {
-                            if (masked) {
+                            if (hides && t * BQ + off < wkey + 15) {   // weights of hidden keys
 #pragma unroll
-                                for (int n = 0; n < NK; ++n)
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        if (wkey + 16 * n + col > t * BQ + 16 * (i / 4) + 4 * g + i % 4 + off)
-                                            s[n][i / 4][i % 4] = 0.f, dp[n][i / 4][i % 4] = 0.f;
+                                for (int i = 0; i < 8; ++i)
+                                    if (wkey + col > t * BQ + 16 * (i / 4) + 4 * g + i % 4 + off)
+                                        s[i / 4][i % 4] = 0.f, dp[i / 4][i % 4] = 0.f;
                             }
-#pragma unroll
-                            for (int n = 0; n < NK; ++n) wf[n] = acc_frag(s[n][0], s[n][1], E());
+                            wf = acc_frag(s[0], s[1], E());
                         }
-#pragma unroll
-                        for (int n = 0; n < NK; ++n) av[n][c] = mma32(a, wf[n], av[n][c]);
+                        av[c] = mma32(a, wf, av[c]);
 #pragma unroll
                         for (int i = NS * c / (DV / 16); i < NS * (c + 1) / (DV / 16); ++i)
-                            dp[i / 8][i / 4 % 2][i % 4] =
-                                s[i / 8][i / 4 % 2][i % 4] * (dp[i / 8][i / 4 % 2][i % 4] - de[i / 4 % 2][i % 4]);
+                            dp[i / 4][i % 4] = s[i / 4][i % 4] * (dp[i / 4][i % 4] - de[i / 4][i % 4]);
                     } else {
                         const int c = e < E2 ? 0 : e - E2;
-                        if (c == 0)
-#pragma unroll
-                            for (int n = 0; n < NK; ++n) zf[n] = acc_frag(dp[n][0], dp[n][1], E());
-#pragma unroll
-                        for (int n = 0; n < NK; ++n) ak[n][c] = mma32(a, zf[n], ak[n][c]);
+                        if (c == 0) zf = acc_frag(dp[0], dp[1], E());
+                        ak[c] = mma32(a, zf, ak[c]);
                     }
                 });
         }
-        if (t + 1 < nt) store((t + 1) & 1);
+        if (t + 1 < nt) store(t + 1, hides);
         __syncthreads();
+    };
+    int t = t0;
+    for (const int th = in.causal ? min(nt, (key0 + BK - 1 - off + BQ - 1) / BQ) : t0; t < th; ++t) step(t, Int<1>());
+    for (; t < nt; ++t) step(t, Int<0>());
+    const int key = wkey + col;
+    if (key >= nk) return;
+    const int64_t row = k0 + key;
+    E* kr = dk + row * dk_token_stride + h * dk_head_stride;
+    E* vr = dv + row * dv_token_stride + h * dv_head_stride;
+#pragma unroll
+    for (int c = 0; c < DN / 16; ++c) {
+        typename Vec<E>::v4 kx, vx;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            kx[i] = from_f32<E>(ak[c][i] * in.scale);
+            vx[i] = from_f32<E>(av[c][i]);
+        }
+        store_vec(kr + 16 * c + 4 * g, kx);
+        store_vec(vr + 16 * c + 4 * g, vx);
     }
+    if constexpr (DR > 0) {
+        float* pr = pe_part + (row * in.H + h) * DR;
 #pragma unroll
-    for (int n = 0; n < NK; ++n) {
-        const int key = wkey + 16 * n + col;
-        if (key >= nk) continue;
-        const int64_t row = k0 + key;
-        E* kr = dk + row * dk_token_stride + h * dk_head_stride;
-        E* vr = dv + row * dv_token_stride + h * dv_head_stride;
-#pragma unroll
-        for (int c = 0; c < DN / 16; ++c) {
-            typename Vec<E>::v4 kx, vx;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                kx[i] = from_f32<E>(ak[n][c][i] * in.scale);
-                vx[i] = from_f32<E>(av[n][c][i]);
-            }
-            store_vec(kr + 16 * c + 4 * g, kx);
-            store_vec(vr + 16 * c + 4 * g, vx);
-        }
-        if constexpr (DR > 0) {
-            float* pr = pe_part + (row * in.H + h) * DR;
-#pragma unroll
-            for (int c = 0; c < DR / 16; ++c) store_vec(pr + 16 * c + 4 * g, ak[n][DN / 16 + c] * in.scale);
-        }
+        for (int c = 0; c < DR / 16; ++c) store_vec(pr + 16 * c + 4 * g, ak[DN / 16 + c] * in.scale);
     }
 }
 
@@ -421,7 +416,7 @@ template <typename E, int DN, int DR>
 static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipStream_t stream) {
     const int64_t tq = tile_count(in.cu_seqlens_q, in.total_q, in.num_seqs, 64 * LATENT_NQ<E>);
     const int32_t* cu_k = in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
-    const int64_t tk = tile_count(cu_k, in.total_k, in.num_seqs, 64 * DKV_NK<E>);
+    const int64_t tk = tile_count(cu_k, in.total_k, in.num_seqs, 64);
     if (tq > 0)
         hipLaunchKernelGGL((latent_dq_kernel<E, DN, DR>), dim3((unsigned)(tq * in.H)), dim3(256), 0, stream, in,
                            (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.delta, (int)tq);

@@ -226,6 +226,24 @@ struct Stage {
     __device__ __forceinline__ void load_rows(int tid, const E* base, int64_t stride, int left) {
         load_rows<0>(tid, base, stride, base, stride, left);
     }
+    // Whether row tid / TPR + PASS p of the loaded tile has a value that is not
+    // finite: the same answer in the row's TPR threads.
+    __device__ __forceinline__ bool bad_row(int tid, int p, bool bad = false) const {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const unsigned x = r[p][s][i];
+                bad |= (x & 0x7f800000u) == 0x7f800000u;
+                if (sizeof(E) == 2) bad |= (x & 0x7f80u) == 0x7f80u;
+            }
+        const unsigned long long any = __ballot(bad) >> (tid & 63 & ~(TPR - 1));
+        return (any & ((1ull << TPR) - 1)) != 0;
+    }
+    __device__ __forceinline__ void fill_row(int p, unsigned x) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) r[p][s] = u32x4{x, x, x, x};
+    }
     // store(), each chunk's register refilled at once with the tile after next,
     // so that a tile's worth of loads stays in flight
     template <typename F>
@@ -250,6 +268,25 @@ struct Stage {
                 *reinterpret_cast<u32x4*>(t + later_chunk<E, W>(at, TPR * s) + PASS * p * W) = r[p][s];
     }
 };
+
+// A product over keys that some rows do not see multiplies their weights, 0, with
+// what such a key holds, and 0 times NaN or Inf is NaN.  In the tiles where that
+// can happen a row with values that are not finite is therefore cleared from the
+// operand of that product, and put as NaN (QUIET: in bf16 as in fp32) into the
+// operand or statistic that the weights come from: there the rows that do not see
+// the key are masked, and those that do get NaN.
+constexpr unsigned QUIET = 0x7fff7fffu;
+
+template <typename A, typename B>
+__device__ __forceinline__ void move_bad_rows(int tid, A& product, B& weights) {
+    static_assert(A::P == B::P && A::TPR == B::TPR, "the same rows in the same threads");
+#pragma unroll
+    for (int p = 0; p < A::P; ++p)
+        if (product.bad_row(tid, p)) {
+            product.fill_row(p, 0u);
+            weights.fill_row(p, QUIET);
+        }
+}
 
 // -- a workgroup's tile of a packed batch ----------------------------------------
 __device__ __forceinline__ int clamp_offset(int x, int total) { return min(max(x, 0), total); }

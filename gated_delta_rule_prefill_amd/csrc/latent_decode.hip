@@ -246,17 +246,31 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
         if (tid < 4) grown[tid] = 0;
         __syncthreads();
         int next_row = -1;
+        // Rows with values that are not finite, in tiles that hold keys some query
+        // rows do not see: cleared, and marked -2 for those that do (their weight
+        // becomes NaN; a weight of 0 would make 0 * NaN of a hidden key).
+        const int first_last = len - n + (int)(row0 / a.H);          // last key that the tile's first row sees
+        auto hides = [&](int k) { return (tile_of(k) + 1) * BN - 1 > first_last; };
+        auto mark_bad_rows = [&](Stage<E, W, BN, NT>& rows, int k) {
+            typedef Stage<E, W, BN, NT> S;
+#pragma unroll
+            for (int p = 0; p < S::P; ++p)
+                if (rows.bad_row(tid, p)) {
+                    rows.fill_row(p, 0u);
+                    if (tid % S::TPR == 0) ridx[k & 3][tid / S::TPR + S::PASS * p] = -2;
+                }
+        };
         if (count > 0) {
             Stage<E, W, BN, NT> first;
             first.load(tid, row_of(0));
             st.load(tid, row_of(1));
             if (tid < BN) next_row = cache_row(3);
+            if (hides(0)) mark_bad_rows(first, 0);
             first.store(tid, tilebuf[0]);
         }
         v8 q[QREG ? KS : 1];
         const E* qp;
         int last;                                                    // last key this lane's row sees
-        const int first_last = len - n + (int)(row0 / a.H);          // and the tile's first row
         {
             const int64_t row = row0 + min(nrows - 1, 16 * rt + col);
             const int i = (int)(row / a.H), h = (int)(row - (int64_t)i * a.H);
@@ -321,8 +335,10 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
                         const int k0 = 16 * (tg * TW + w) + 4 * g;
                         const i32x4 there = *reinterpret_cast<const i32x4*>(ridx[k & 3] + k0);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (there[i] < 0 || t * BN + k0 + i > last) s[w][i] = neg_inf();
+                        for (int i = 0; i < 4; ++i) {
+                            if (there[i] == -2) s[w][i] = __builtin_nanf("");
+                            if (there[i] == -1 || t * BN + k0 + i > last) s[w][i] = neg_inf();
+                        }
                     }
                 }
                 float top = neg_inf();
@@ -342,7 +358,10 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
                 next_row = cache_row(k + 4);
             }
             if (tid == 0) grown[(k + 2) & 3] = 0;
-            if (k + 1 < count) st.store_load(tid, tilebuf[(k + 1) & 1], row_of(k + 2));
+            if (k + 1 < count) {
+                if (hides(k + 1)) mark_bad_rows(st, k + 1);
+                st.store_load(tid, tilebuf[(k + 1) & 1], row_of(k + 2));
+            }
             // The weights are taken against the rows' running maxima as they
             // stand.  Only when a row's grew by more than 8 (in powers of two;
             // the first tile always) are the maxima raised, by every wave alike,

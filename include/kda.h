@@ -285,8 +285,10 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  *              outside [0, T] are clamped to it.
  *   Empty rows a query row that sees no key gets o = 0, lse = -inf and zero
  *              gradients.
- *   Values     NaN and Inf propagate from the keys a row sees.  Rows behind a
- *              sequence's end and unused cache rows may hold anything.
+ *   Values     NaN and Inf propagate from the keys a row sees to its result, and
+ *              from a row to the gradients of the keys it sees, and no further:
+ *              keys that the mask hides, rows behind a sequence's end and unused
+ *              cache rows may hold anything.
  * ---------------------------------------------------------------------------
  */
 

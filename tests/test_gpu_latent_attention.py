@@ -255,3 +255,66 @@ def test_workspace_of_the_library():
     torch.cuda.synchronize()
     for n in ("dq", "dk", "dv", "dk_pe"):
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what,value", [("k", "nan"), ("v", "nan"), ("v", "inf"), ("k_pe", "inf"), ("k", "-inf")])
+def test_hidden_keys_that_are_not_finite(dtype, what, value):
+    """NaN or Inf in keys that the causal mask hides reaches no output or
+    gradient of the rows before them; the rows that see them get NaN."""
+    lens, bad = [200, 70], 150
+    x = make(26, dtype, 2, 128, 64, lens, lens)
+    clean = {n: (t.clone() if isinstance(t, torch.Tensor) else t) for n, t in x.items()}
+    kv = torch.cat([x["k"], x["v"]], dim=2)
+    x["k"], x["v"] = kv[..., :128], kv[..., 128:]
+    x[what][bad, ..., 5] = float(value)
+    x[what][199, ..., 63] = float(value)
+    got = both(x, lens, lens, True)
+    want = ref.attention(clean["q"], clean["k"], clean["v"], clean["k_pe"], lens, lens, True, x["scale"], x["d_o"])
+    for name in ("o", "lse", "dq"):
+        value_, bound = want[name]
+        for part in (slice(0, bad), slice(200, 270)):
+            ref.check(f"hidden {what} {value} {name}", got[name][part], value_[part], bound[part])
+    if value == "nan":
+        assert torch.isnan(got["o"][bad:200].float()).any(dim=-1).all()
+        assert torch.isnan(got["dq"][bad:200].float()).any(dim=-1).all()
+    # the other sequence's keys are untouched
+    for name in ("dk", "dv", "dk_pe"):
+        ref.check(f"other sequence {name}", got[name][200:], want[name][0][200:], want[name][1][200:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["q", "d_o"])
+def test_rows_that_are_not_finite_leave_later_keys_clean(dtype, what):
+    """A query row with NaN spoils the gradients of the keys it sees, not of the
+    keys behind it."""
+    lens, bad = [200], 20
+    x = make(27, dtype, 2, 128, 64, lens, lens)
+    clean = {n: (t.clone() if isinstance(t, torch.Tensor) else t) for n, t in x.items()}
+    clean["q"][bad] = 0.0
+    clean["d_o"][bad] = 0.0      # the row adds nothing
+    x[what][bad, 0, 3] = float("nan")
+    x[what][bad, 1, 100] = float("inf")
+    got = both(x, lens, lens, True)
+    want = ref.attention(clean["q"], clean["k"], clean["v"], clean["k_pe"], lens, lens, True, x["scale"], clean["d_o"])
+    for name in ("dk", "dv", "dk_pe"):
+        ref.check(f"keys behind a bad {what} {name}", got[name][bad + 1:], want[name][0][bad + 1:], want[name][1][bad + 1:])
+    rows = torch.arange(200) != bad
+    for name in ("o", "dq") if what == "q" else ("dq",):
+        ref.check(f"other rows {name}", got[name][rows.cuda()], want[name][0][rows], want[name][1][rows])
+
+
+def test_padded_rows_of_garbage():
+    """Equal rows padded on the right with NaN: the rows before the padding."""
+    import gated_delta_rule_prefill_amd as kda
+    lens, n = [128, 128, 128], [100, 1, 127]
+    x = make(28, "bf16", 4, 128, 64, lens, lens)
+    want = ref.attention(x["q"], x["k"], x["v"], x["k_pe"], lens, lens, True, x["scale"])
+    for i, m in enumerate(n):
+        for name in ("q", "k", "v", "k_pe"):
+            x[name][128 * i + m:128 * (i + 1)] = float("nan")
+    o, lse = kda.latent_attention(x["q"], x["k"], x["v"], k_pe=x["k_pe"], num_seqs=3, scale=x["scale"])
+    for i, m in enumerate(n):
+        part = slice(128 * i, 128 * i + m)
+        ref.check(f"padded row {i} o", o[part], want["o"][0][part], want["o"][1][part])
+        ref.check(f"padded row {i} lse", lse[part], want["lse"][0][part], want["lse"][1][part])

@@ -131,6 +131,22 @@ def test_bad_pages_and_lengths():
     check("bad lengths", x, 256, [2 ** 31 - 1, -3], [1] * 2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,value", [(1, "nan"), (32, "inf")])
+def test_hidden_rows_that_are_not_finite(dtype, H, value):
+    """Of a chunk of new tokens, those before a row with NaN or Inf are clean."""
+    lens, new, bad = [150, 90], [30, 5], 130
+    x = make(44, dtype, H, 256, 64, 16, lens, new, poison=False)
+    (wo, eo), (wl, el) = ref.decode(x["q"], x["cache"], x["table"], lens, new, 256, x["scale"])
+    x["cache"][int(x["table"][0, bad // 16]), bad % 16, 7] = float(value)
+    x["cache"][int(x["table"][0, 149 // 16]), 149 % 16, 300] = float(value)
+    o, lse = run(x, 256)
+    for part in (slice(0, bad - 120), slice(30, 35)):
+        ref.check("clean rows o", o[part], wo[part], eo[part])
+        ref.check("clean rows lse", lse[part], wl[part], el[part])
+    assert torch.isnan(o[bad - 120:30].float()).any(dim=-1).all()
+
+
 def test_rows_behind_the_last_sequence_are_left():
     lens, new = [100, 30], [1, 2]
     x = make(40, "bf16", 32, 512, 64, 64, lens, new, behind=5)
