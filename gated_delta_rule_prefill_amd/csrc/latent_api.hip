@@ -113,7 +113,7 @@ size_t kda_latent_attention_backward_workspace_bytes(int64_t total_q, int64_t to
     if (total_q < 0 || total_k < 0 || total_q > kMaxRows || total_k > kMaxRows || H <= 0 || H > 65535 ||
         (dr != 0 && dr != 64))
         return 0;
-    return align256((size_t)total_q * H * 4) + align256((size_t)total_k * H * dr * 4) + 256;
+    return align256((size_t)total_q * H * 8) + align256((size_t)total_k * H * dr * 4) + 256;
 }
 
 kda_status kda_latent_attention_backward(const kda_latent_inputs* in, const void* o, const float* lse,
@@ -153,7 +153,7 @@ kda_status kda_latent_attention_backward(const kda_latent_inputs* in, const void
                 return st;
         kda::LatentGrads g{o, lse, d_o, dq, dk, dk_token_stride, dk_head_stride, dv, dv_token_stride, dv_head_stride,
                            dk_pe, reinterpret_cast<float*>(ws),
-                           reinterpret_cast<float*>(ws + align256((size_t)in->total_q * in->H * 4))};
+                           reinterpret_cast<float*>(ws + align256((size_t)in->total_q * in->H * 8))};
         kda_status st = launched(kda::launch_latent_attention_backward(*in, g, stream), "latent backward kernels");
         if (!workspace) {
             const kda_status fr = launched(hipFreeAsync(ws, stream), "hipFreeAsync");

@@ -74,8 +74,8 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
         sk.store(tid, smem[t & 1]);
         sv.store(tid, smem[t & 1] + BN * DQK);
     };
-    const RowReader<E, DQK> k_rows(lane);
-    const ColReader<E, DV, DV / 16> v_cols(lane);
+    RowReader<E, DQK> k_rows(lane);
+    ColReader<E, DV, DV / 16> v_cols(lane);
 
     f32x4 acc[NQ][DV / 16];
     float m[NQ], l[NQ];
@@ -91,9 +91,14 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
         store(0, true);
     }
     __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]);
     // Tile t of the keys; hides: some row does not see all of the keys of it or
     // of the next one.
     auto step = [&](int t, auto hides) {
+        k_rows.keep(), v_cols.keep();
         const E* K = smem[t & 1];
         const E* V = K + BN * DQK;
         if (t + 1 < nt) load(t + 1);

@@ -21,15 +21,16 @@ namespace kda {
 template <typename E, int DN, int DR>
 __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const kda_latent_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
-    const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ delta, int tiles)
+    const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ row_stats, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BN = 32, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
-    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 2 : 1;
+    constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
     __shared__ __attribute__((aligned(16))) E smem[2][BN * (DQK + DV)];
-    // the rows' output gradients, each wave's own, in operand order (registers
-    // hold q and dq already)
-    __shared__ __attribute__((aligned(16))) E sgo[4][NQ][VS][64 * 8];
+    // the rows' output gradients and, where registers are short, the last block
+    // of q: each wave's own, in operand order
+    constexpr int QL = sizeof(E) == 2 && KS > 4 ? 1 : 0, QR = KS - QL;
+    __shared__ __attribute__((aligned(16))) E sgo[4][NQ][VS + QL][64 * 8];
 
     int h, want, seq, tile;
     head_tile_of_block(in.H, tiles, h, want);
@@ -50,16 +51,16 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const E* vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
     const E* pp = DR ? (const E*)in.k_pe + (int64_t)k0 * in.k_pe_token_stride : nullptr;
 
-    v8 q[NQ][KS];
+    v8 q[NQ][QR];
     float lse2[NQ], dl[NQ], exact[NQ];   // delta from the rounded o, and from this kernel's own weights
-    int last[NQ];
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col, rr = min(r, nq - 1);
         const E* row = (const E*)in.q + (int64_t)(q0 + rr) * in.q_token_stride + h * in.q_head_stride;
         const int64_t at = (int64_t)(q0 + rr) * in.H + h;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(row, ks, lane);
+        for (int ks = 0; ks < QR; ++ks) q[j][ks] = row_frag_global(row, ks, lane);
+        if (QL) store_frag(sgo[wave][j][VS], lane, row_frag_global(row, KS - 1, lane));
         float sum = 0.f;
 #pragma unroll
         for (int vs = 0; vs < VS; ++vs) {
@@ -70,7 +71,6 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         }
         dl[j] = group_sum(sum);
         lse2[j] = lse[at] * LOG2E;
-        last[j] = in.causal ? min(nk - 1, r + off) : nk - 1;
         exact[j] = 0.f;
     }
     const int end = in.causal ? min(nk, min(nq, (tile + 1) * BQ) + off) : nk;
@@ -91,9 +91,9 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         sk.store(tid, smem[t & 1]);
         sv.store(tid, smem[t & 1] + BN * DQK);
     };
-    const RowReader<E, DQK> k_rows(lane);
-    const RowReader<E, DV> v_rows(lane);
-    const ColReader<E, DQK, DQK / 16> k_cols(lane);
+    RowReader<E, DQK> k_rows(lane);
+    RowReader<E, DV> v_rows(lane);
+    ColReader<E, DQK, DQK / 16> k_cols(lane);
 
     f32x4 acc[NQ][DQK / 16];
 #pragma unroll
@@ -105,9 +105,14 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         store(0, true);
     }
     __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int ks = 0; ks < QR; ++ks) arrived(q[j][ks]);
     // Tile t of the keys; hides: some row does not see all of the keys of it or
     // of the next one.
     auto step = [&](int t, auto hides) {
+        k_rows.keep(), v_rows.keep(), k_cols.keep();
         const E* K = smem[t & 1];
         const E* V = K + BN * DQK;
         if (t + 1 < nt) load(t + 1);
@@ -123,9 +128,9 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
             // after dz, dq^T += K^T dz.
             constexpr int E0 = TT * KS, E1 = E0 + TT * VS, NS = NQ * TT * 4;
             v8 y[2][NQ], dz[NQ];
-            auto row_grads = [&](int vs) {
+            auto row_grads = [&](int vs) {   // (or q's last block, into y[1])
 #pragma unroll
-                for (int j = 0; j < NQ; ++j) y[vs & 1][j] = load_frag(sgo[wave][j][vs], lane);
+                for (int j = 0; j < NQ; ++j) y[vs == VS ? 1 : vs & 1][j] = load_frag(sgo[wave][j][vs], lane);
             };
             ahead<E1 + DQK / 16, PD>(
                 [&](auto n) {
@@ -136,30 +141,37 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                 },
                 [&](auto n) {
                     constexpr int e = n;
-                    if (e < E0) {
-                        if (e == E0 - 2) row_grads(0);
+                    if constexpr (e < E0) {
+                        constexpr int ks = e / TT;
+                        if (QL && e == E0 - 2 * TT) row_grads(VS);
+                        if (e == E0 - TT) row_grads(0);
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j) s[j][e % TT] = mma32(x[e % (PD + 1)], q[j][e < E0 ? e / TT : 0], s[j][e % TT]);
-                    } else if (e < E1) {
-                        const int f = e - E0;
+                        for (int j = 0; j < NQ; ++j) {
+                            if constexpr (ks < QR) s[j][e % TT] = mma32(x[e % (PD + 1)], q[j][ks], s[j][e % TT]);
+                            else s[j][e % TT] = mma32(x[e % (PD + 1)], y[1][j], s[j][e % TT]);
+                        }
+                    } else if constexpr (e < E1) {
+                        constexpr int f = e - E0;
                         if (f % TT == 0 && f / TT + 1 < VS) row_grads(f / TT + 1);
 #pragma unroll
                         for (int j = 0; j < NQ; ++j) dp[j][f % TT] = mma32(x[e % (PD + 1)], y[f / TT & 1][j], dp[j][f % TT]);
 #pragma unroll
-                        for (int n = NS * f / (TT * VS); n < NS * (f + 1) / (TT * VS); ++n) {
-                            const int j = n / (TT * 4), tt = n / 4 % TT, i = n % 4;
+                        for (int m = NS * f / (TT * VS); m < NS * (f + 1) / (TT * VS); ++m) {
+                            const int j = m / (TT * 4), tt = m / 4 % TT, i = m % 4;
                             s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -lse2[j]));
                         }
                     } else {
                         if (e == E1) {
                             if (hides && (t + 1) * BN > wave_full) {   // weights of hidden keys
 #pragma unroll
-                                for (int j = 0; j < NQ; ++j)
+                                for (int j = 0; j < NQ; ++j) {
+                                    const int last = in.causal ? min(nk - 1, wrow + 16 * j + col + off) : nk - 1;
 #pragma unroll
                                     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                                         for (int i = 0; i < 4; ++i)
-                                            if (t * BN + 16 * tt + 4 * g + i > last[j]) s[j][tt][i] = 0.f, dp[j][tt][i] = 0.f;
+                                            if (t * BN + 16 * tt + 4 * g + i > last) s[j][tt][i] = 0.f, dp[j][tt][i] = 0.f;
+                                }
                             }
 #pragma unroll
                             for (int j = 0; j < NQ; ++j) {
@@ -173,7 +185,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
                                 dz[j] = acc_frag(s[j][0], s[j][1], E());
                             }
                         }
-                        const int c = e < E1 ? 0 : e - E1;
+                        constexpr int c = e - E1;
 #pragma unroll
                         for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[e % (PD + 1)], dz[j], acc[j][c]);
                     }
@@ -191,7 +203,11 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         const int r = wrow + 16 * j + col;
         const float sum = group_sum(exact[j]);
         if (r >= nq) continue;
-        if (g == 0) delta[(int64_t)(q0 + r) * in.H + h] = sum;
+        if (g == 0) {
+            float* stats = row_stats + 2 * ((int64_t)h * in.total_q + q0 + r);
+            stats[0] = lse2[j];
+            stats[1] = sum;
+        }
         E* row = dq + ((int64_t)(q0 + r) * in.H + h) * DQK;
 #pragma unroll
         for (int c = 0; c < DQK / 16; ++c) {
@@ -208,9 +224,9 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
 // The scores are formed with rows = queries, so that the weights and dz are the
 // operands of dv^T += g^T w and dk^T += q^T dz as they stand.
 template <typename E, int DN, int DR>
-__global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
-    const kda_latent_inputs in, const float* __restrict__ lse, const E* __restrict__ d_o,
-    const float* __restrict__ delta, E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel(
+    const kda_latent_inputs in, const E* __restrict__ d_o, const float* __restrict__ row_stats,
+    E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
     E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ pe_part, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BQ = 32, BK = 64;
@@ -255,39 +271,44 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
     SQ sq;
     Stage<E, DV, BQ, 256> sg;
     static_assert(SQ::P == 1 && SQ::TPR == 8, "a row per 8 threads");
-    float srow_next = 0.f;
-    // Each of 2 BQ threads carries a row's lse or delta: the first wave where all
-    // keys are seen (one load for the workgroup: dkv 2.95 ms instead of 3.09);
-    // else the row's own first and second thread, which know whether it is finite.
-    auto part = [&](bool hides) { return !hides ? tid : tid % SQ::TPR < 2 ? tid % SQ::TPR * BQ + tid / SQ::TPR : 2 * BQ; };
+    // lse and delta of a row travel with one thread: where all keys are seen the
+    // first BQ threads (few and whole lines to load), else the row's own first
+    // thread, which knows whether the row is finite.
+    const float* stats = row_stats + 2 * ((int64_t)h * in.total_q + q0);
+    float next_lse = 0.f, next_delta = 0.f;
+    auto carried = [&](bool hides) { return !hides ? tid : tid % SQ::TPR == 0 ? tid / SQ::TPR : BQ; };
     auto load = [&](int t, bool hides) {
         sq.load_rows(tid, qp + (int64_t)t * BQ * in.q_token_stride, in.q_token_stride, nq - t * BQ);
         sg.load_rows(tid, gp + (int64_t)t * BQ * in.H * DV, (int64_t)in.H * DV, nq - t * BQ);
-        if (part(hides) < 2 * BQ) {   // rows behind the last weigh nothing: lse = inf
-            const int i = t * BQ + part(hides) % BQ;
-            const int64_t at = (int64_t)(q0 + min(i, nq - 1)) * in.H + h;
-            if (part(hides) < BQ) srow_next = i < nq ? lse[at] * LOG2E : __builtin_inff();
-            else srow_next = i < nq ? delta[at] : 0.f;
+        if (carried(hides) < BQ) {   // rows behind the last weigh nothing: lse = inf
+            const int i = t * BQ + carried(hides);
+            const float* at = stats + 2 * (int64_t)min(i, nq - 1);
+            next_lse = i < nq ? at[0] : __builtin_inff();
+            next_delta = i < nq ? at[1] : 0.f;
         }
     };
     auto store = [&](int t, bool hides) {
         if (hides) {
-            const bool bad_delta = tid % SQ::TPR == 1 && !(__builtin_fabsf(srow_next) < __builtin_inff());
+            const bool bad_delta = carried(hides) < BQ && !(__builtin_fabsf(next_delta) < __builtin_inff());
             if (sq.bad_row(tid, 0) | sg.bad_row(tid, 0, bad_delta)) {   // as move_bad_rows: lse becomes NaN
                 sq.fill_row(0, 0u);
                 sg.fill_row(0, 0u);
-                srow_next = tid % SQ::TPR == 0 ? __builtin_nanf("") : 0.f;
+                next_lse = __builtin_nanf("");
+                next_delta = 0.f;
             }
         }
         sq.store(tid, smem[t & 1]);
         sg.store(tid, smem[t & 1] + BQ * DQK);
-        if (part(hides) < 2 * BQ) srow[t & 1][part(hides)] = srow_next;
+        if (carried(hides) < BQ) {
+            srow[t & 1][carried(hides)] = next_lse;
+            srow[t & 1][BQ + carried(hides)] = next_delta;
+        }
     };
 
-    const RowReader<E, DQK> q_rows(lane);
-    const RowReader<E, DV> g_rows(lane);
-    const ColReader<E, DQK, DQK / 16> q_cols(lane);
-    const ColReader<E, DV, DV / 16> g_cols(lane);
+    RowReader<E, DQK> q_rows(lane);
+    RowReader<E, DV> g_rows(lane);
+    ColReader<E, DQK, DQK / 16> q_cols(lane);
+    ColReader<E, DV, DV / 16> g_cols(lane);
     f32x4 ak[DQK / 16], av[DV / 16];
 #pragma unroll
     for (int c = 0; c < DQK / 16; ++c) ak[c] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -298,13 +319,19 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
         store(t0, in.causal);
     }
     __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) arrived(k[ks]);
+#pragma unroll
+    for (int vs = 0; vs < VS; ++vs) arrived(v[vs]);
     // Tile t of the rows; hides: some row of it does not see all of the keys.
     auto step = [&](int t, auto hides) {
+        q_rows.keep(), g_rows.keep(), q_cols.keep(), g_cols.keep();
         const E* Q = smem[t & 1];
         const E* G = Q + BQ * DQK;
         const float* R = srow[t & 1];
+        const int row0 = t * BQ;
         if (t + 1 < nt) load(t + 1, hides);
-        if (!hides || t * BQ + BQ - 1 + off >= wkey) {
+        if (!hides || row0 + BQ - 1 + off >= wkey) {
             f32x4 s[2], dp[2];
             v8 x[PD + 1];
 #pragma unroll
@@ -328,21 +355,21 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
                 [&](auto n) {
                     constexpr int e = n;
                     const v8& a = x[e % (PD + 1)];
-                    if (e < E0) {
-                        s[e % 2] = mma32(a, k[e < E0 ? e / 2 : 0], s[e % 2]);
-                    } else if (e < E1) {
-                        const int f = e < E1 ? e - E0 : 0;
+                    if constexpr (e < E0) {
+                        s[e % 2] = mma32(a, k[e / 2], s[e % 2]);
+                    } else if constexpr (e < E1) {
+                        constexpr int f = e - E0;
                         dp[f % 2] = mma32(a, v[f / 2], dp[f % 2]);
 #pragma unroll
                         for (int i = NS * f / (2 * VS); i < NS * (f + 1) / (2 * VS); ++i)
                             s[i / 4][i % 4] = exp2_fast(__builtin_fmaf(s[i / 4][i % 4], sc, -ls[i / 4][i % 4]));
-                    } else if (e < E2) {
-                        const int c = e < E2 ? e - E1 : 0;
+                    } else if constexpr (e < E2) {
+                        constexpr int c = e - E1;
                         if (c == 0) {
-                            if (hides && t * BQ + off < wkey + 15) {   // weights of hidden keys
+                            if (hides && row0 + off < wkey + 15) {   // weights of hidden keys
 #pragma unroll
                                 for (int i = 0; i < 8; ++i)
-                                    if (wkey + col > t * BQ + 16 * (i / 4) + 4 * g + i % 4 + off)
+                                    if (wkey + col > row0 + 16 * (i / 4) + 4 * g + i % 4 + off)
                                         s[i / 4][i % 4] = 0.f, dp[i / 4][i % 4] = 0.f;
                             }
                             wf = acc_frag(s[0], s[1], E());
@@ -352,7 +379,7 @@ __global__ __launch_bounds__(256, 2) void latent_dkv_kernel(
                         for (int i = NS * c / (DV / 16); i < NS * (c + 1) / (DV / 16); ++i)
                             dp[i / 4][i % 4] = s[i / 4][i % 4] * (dp[i / 4][i % 4] - de[i / 4][i % 4]);
                     } else {
-                        const int c = e < E2 ? 0 : e - E2;
+                        constexpr int c = e - E2;
                         if (c == 0) zf = acc_frag(dp[0], dp[1], E());
                         ak[c] = mma32(a, zf, ak[c]);
                     }
@@ -419,10 +446,10 @@ static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipS
     const int64_t tk = tile_count(cu_k, in.total_k, in.num_seqs, 64);
     if (tq > 0)
         hipLaunchKernelGGL((latent_dq_kernel<E, DN, DR>), dim3((unsigned)(tq * in.H)), dim3(256), 0, stream, in,
-                           (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.delta, (int)tq);
+                           (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, (int)tq);
     if (tk > 0)
-        hipLaunchKernelGGL((latent_dkv_kernel<E, DN, DR>), dim3((unsigned)(tk * in.H)), dim3(256), 0, stream, in, a.lse,
-                           (const E*)a.d_o, a.delta, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv,
+        hipLaunchKernelGGL((latent_dkv_kernel<E, DN, DR>), dim3((unsigned)(tk * in.H)), dim3(256), 0, stream, in,
+                           (const E*)a.d_o, a.row_stats, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv,
                            a.dv_token_stride, a.dv_head_stride, a.pe_part, (int)tk);
     if constexpr (DR > 0)
         if (in.total_k > 0)

@@ -62,15 +62,21 @@ __device__ __forceinline__ int later_chunk(int at, int c1) {
 // Operands by rows of a tile: lane l supplies row row0 + (l & 15), slots
 // 8g .. 8g + 7 of the 32-wide block ks (g = l >> 4).  A lane's addresses come
 // from two bases and constants; row0 is a multiple of 16.
+// keep() in a loop's body makes the compiler derive the addresses there again
+// rather than hold all of them in registers, which the largest kernels lack: an
+// operand that is spilled costs far more than its read, as the wait for it also
+// waits for the next tile's loads (dq 2.36 ms with three spilled operands in the
+// loop, 1.67 without).
 template <typename E, int W> struct RowReader;
 template <int W> struct RowReader<bf16, W> {
-    int at[2];
-    __device__ __forceinline__ explicit RowReader(int lane) {
-        at[0] = tile_at<bf16, W>(lane & 15, lane >> 4);
-        at[1] = tile_at<bf16, W>(lane & 15, 4 + (lane >> 4));
-    }
+    int at;   // in bytes
+    __device__ __forceinline__ explicit RowReader(int lane) : at(2 * tile_at<bf16, W>(lane & 15, lane >> 4)) {}
+    __device__ __forceinline__ void keep() { asm volatile("" : "+v"(at)); }
     __device__ __forceinline__ bf16x8 operator()(const bf16* t, int row0, int ks) const {
-        return *reinterpret_cast<const bf16x8*>(t + later_chunk<bf16, W>(at[ks & 1], 8 * (ks >> 1)) + row0 * W);
+        constexpr int HALF = WHOLE_ROWS<bf16, W> ? 128 : 0;
+        const int flip = 64 * (ks & 1) + (HALF && (ks >> 1 & 1) ? 128 : 0);
+        const int on = HALF ? 256 * (ks >> 2) : 128 * (ks >> 1);
+        return *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(t) + (at ^ flip) + on + 2 * row0 * W);
     }
 };
 template <int W> struct RowReader<float, W> {
@@ -79,6 +85,7 @@ template <int W> struct RowReader<float, W> {
         at[0] = tile_at<float, W>(lane & 15, 2 * (lane >> 4));
         at[1] = tile_at<float, W>(lane & 15, 2 * (lane >> 4) + 1);
     }
+    __device__ __forceinline__ void keep() {}
     __device__ __forceinline__ f32x8 operator()(const float* t, int row0, int ks) const {
         const f32x4 a = *reinterpret_cast<const f32x4*>(t + later_chunk<float, W>(at[0], 8 * ks) + row0 * W);
         const f32x4 b = *reinterpret_cast<const f32x4*>(t + later_chunk<float, W>(at[1], 8 * ks) + row0 * W);
@@ -95,28 +102,29 @@ template <int W> struct RowReader<float, W> {
 // 4 where CT is more.
 template <typename E, int W, int CT> struct ColReader;
 template <int W, int CT> struct ColReader<bf16, W, CT> {
-    int at[CT < 4 ? CT : 4], from;
-    __device__ __forceinline__ explicit ColReader(int lane, int ct0 = 0) {
+    int at, from;   // at in bytes
+    __device__ __forceinline__ explicit ColReader(int lane, int ct0 = 0) : from(ct0) {
         const int r = 4 * (lane >> 4) + ((lane & 15) >> 2), c = 4 * (lane & 3);
-        from = ct0;
-#pragma unroll
-        for (int i = 0; i < (CT < 4 ? CT : 4); ++i) {
-            const int chunk = 2 * (ct0 + i) + (c >> 3);
-            at[i] = tile_at<bf16, W>(r, CT <= 4 ? chunk : chunk & 7) + (c & 4);
-        }
+        const int chunk = 2 * ct0 + (c >> 3);
+        at = 2 * (tile_at<bf16, W>(r, CT <= 4 ? chunk : chunk & 7) + (c & 4));
     }
+    __device__ __forceinline__ void keep() { asm volatile("" : "+v"(at)); }
     __device__ __forceinline__ bf16x8 operator()(const bf16* t, int ra, int rb, int ct) const {
         typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
         typedef short s16x8 __attribute__((ext_vector_type(8)));
-        const bf16* p = t + (CT <= 4 ? at[ct & 3] : later_chunk<bf16, W>(at[ct & 3], 2 * ((from + ct) & ~3)));
-        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + ra * W));
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + rb * W));
+        const int far = CT <= 4 ? 0 : (from + ct) >> 2;   // 128-byte groups behind the first
+        const int flip = 32 * (ct & 3) + (WHOLE_ROWS<bf16, W> ? 128 * (far & 1) : 0);
+        const int on = WHOLE_ROWS<bf16, W> ? 256 * (far >> 1) : 128 * far;
+        const char* p = reinterpret_cast<const char*>(t) + (at ^ flip) + on;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 2 * ra * W));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 2 * rb * W));
         return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     }
 };
 template <int W, int CT> struct ColReader<float, W, CT> {
     int lane, ct0;
     __device__ __forceinline__ explicit ColReader(int lane, int ct0 = 0) : lane(lane), ct0(ct0) {}
+    __device__ __forceinline__ void keep() {}
     __device__ __forceinline__ f32x8 operator()(const float* t, int ra, int rb, int ct) const {
         const int g4 = 4 * (lane >> 4), c = 16 * (ct0 + ct) + (lane & 15);
         f32x8 v;
@@ -147,6 +155,13 @@ __device__ __forceinline__ bf16x8 row_frag_global(const bf16* row, int ks, int l
 __device__ __forceinline__ f32x8 row_frag_global(const float* row, int ks, int lane) {
     return load_vec<f32x8, float>(row + 32 * ks + 8 * (lane >> 4));
 }
+
+// Called between the load of operands that a loop keeps in registers and the
+// loop: the wait for them then stands here.  The compiler otherwise puts it where
+// the loop first uses them, in every pass, where it also waits for the loads
+// that the pass has just issued for the next tile (forward of the packed training
+// step 1.24 ms with these waits in the loop, 1.17 without).
+template <typename T> __device__ __forceinline__ void arrived(T& x) { asm volatile("" : "+v"(x)); }
 
 // N steps use(e), each with an operand that fetch(e) reads from LDS D steps
 // ahead into a ring of D + 1: the compiler, short of registers, otherwise puts
@@ -212,8 +227,9 @@ struct Stage {
             const uint32_t at1 = there * (uint32_t)(stride1 * sizeof(E)) + chunk;
 #pragma unroll
             for (int s = 0; s < S; ++s)
-                r[p][s] = s < S0 ? *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base + TPR * CE * s) + at)
-                                 : *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base1 + TPR * CE * (s - S0)) + at1);
+                r[p][s] = *reinterpret_cast<const u32x4*>(
+                    s < S0 ? reinterpret_cast<const char*>(base + TPR * CE * s) + at
+                           : reinterpret_cast<const char*>(base1 + TPR * CE * (s - S0)) + at1);
         }
         if (left < ROWS) {
 #pragma unroll

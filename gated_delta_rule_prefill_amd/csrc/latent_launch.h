@@ -12,7 +12,7 @@ namespace kda {
 hipError_t launch_latent_attention(const kda_latent_inputs& in, void* o, float* lse,
                                    hipStream_t stream);
 
-// delta: [total_q, H] fp32; pe_part: [total_k, H, dr] fp32
+// row_stats: [H, total_q, 2] fp32 (lse in powers of two, delta); pe_part: [total_k, H, dr] fp32
 struct LatentGrads {
     const void* o;
     const float* lse;
@@ -23,7 +23,7 @@ struct LatentGrads {
     void* dv;
     int64_t dv_token_stride, dv_head_stride;
     void* dk_pe;
-    float* delta;
+    float* row_stats;
     float* pe_part;
 };
 hipError_t launch_latent_attention_backward(const kda_latent_inputs& in, const LatentGrads& g,
