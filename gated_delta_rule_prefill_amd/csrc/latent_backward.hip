@@ -232,14 +232,16 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
     constexpr int DQK = DN + DR, DV = DN, BQ = 32, BK = 64;
     constexpr int KS = DQK / 32, VS = DV / 32, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
-    __shared__ __attribute__((aligned(16))) E smem[2][BQ * (DQK + DV)];
+    // two arrays, so that a read of one is seen not to wait for loads into the other
+    __shared__ __attribute__((aligned(16))) E even[BQ * (DQK + DV)];
+    __shared__ __attribute__((aligned(16))) E odd[BQ * (DQK + DV)];
     __shared__ __attribute__((aligned(16))) float srow[2][2 * BQ];   // lse (base 2), then delta
 
     int h, want, seq, tile;
     head_tile_of_block(in.H, tiles, h, want);
     const int32_t* cu_k = in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
     const int rows_k = (int)(in.total_k / in.num_seqs);
-    if (!find_tile<BK, 256>(cu_k, in.num_seqs, rows_k, (int)in.total_k, want, reinterpret_cast<int*>(&smem[0][0]), seq,
+    if (!find_tile<BK, 256>(cu_k, in.num_seqs, rows_k, (int)in.total_k, want, reinterpret_cast<int*>(even), seq,
                             tile))
         return;
     int q0, q1, k0, k1;
@@ -265,6 +267,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
     const int nt = (nq + BQ - 1) / BQ;
     const int t0 = in.causal ? min(nt, max(0, key0 - off) / BQ) : 0;   // rows before it see none of the keys
 
+    // first row tile whose rows see all of the workgroup's keys
+    const int th = in.causal ? max(t0, min(nt, (key0 + BK - 1 - off + BQ - 1) / BQ)) : t0;
+    // tile t lies in even or odd by its distance from th
+    auto parity = [&](int t) { return (t - th) & 1; };
+
     const E* qp = (const E*)in.q + (int64_t)q0 * in.q_token_stride + h * in.q_head_stride;
     const E* gp = d_o + ((int64_t)q0 * in.H + h) * DV;
     typedef Stage<E, DQK, BQ, 256> SQ;
@@ -277,9 +284,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
     const float* stats = row_stats + 2 * ((int64_t)h * in.total_q + q0);
     float next_lse = 0.f, next_delta = 0.f;
     auto carried = [&](bool hides) { return !hides ? tid : tid % SQ::TPR == 0 ? tid / SQ::TPR : BQ; };
-    auto load = [&](int t, bool hides) {
-        sq.load_rows(tid, qp + (int64_t)t * BQ * in.q_token_stride, in.q_token_stride, nq - t * BQ);
-        sg.load_rows(tid, gp + (int64_t)t * BQ * in.H * DV, (int64_t)in.H * DV, nq - t * BQ);
+    auto load_stats = [&](int t, bool hides) {
         if (carried(hides) < BQ) {   // rows behind the last weigh nothing: lse = inf
             const int i = t * BQ + carried(hides);
             const float* at = stats + 2 * (int64_t)min(i, nq - 1);
@@ -287,8 +292,35 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
             next_delta = i < nq ? at[1] : 0.f;
         }
     };
-    auto store = [&](int t, bool hides) {
-        if (hides) {
+    auto store_stats = [&](int t, bool hides) {
+        if (carried(hides) < BQ) {
+            srow[parity(t)][carried(hides)] = next_lse;
+            srow[parity(t)][BQ + carried(hides)] = next_delta;
+        }
+    };
+    // Tiles of rows that all see all of the keys go straight to LDS (2.84 -> 2.42
+    // ms); the others through registers, where rows that are not finite are found
+    // and taken out.
+    Direct<E, DQK, BQ, 256> direct_q;
+    Direct<E, DV, BQ, 256> direct_g;
+    auto load = [&](int t, auto hides, E* to) {
+        const E* qt = qp + (int64_t)t * BQ * in.q_token_stride;
+        const E* gt = gp + (int64_t)t * BQ * in.H * DV;
+        load_stats(t, hides);
+        if constexpr (hides) {
+            sq.load_rows(tid, qt, in.q_token_stride, nq - t * BQ);
+            sg.load_rows(tid, gt, (int64_t)in.H * DV, nq - t * BQ);
+        } else {
+            if (nq - t * BQ < BQ) {
+                direct_q.rows(tid, in.q_token_stride, nq - t * BQ - 1);
+                direct_g.rows(tid, (int64_t)in.H * DV, nq - t * BQ - 1);
+            }
+            direct_q.fetch(wave, qt, to);
+            direct_g.fetch(wave, gt, to + BQ * DQK);
+        }
+    };
+    auto store = [&](int t, auto hides, E* to) {
+        if constexpr (hides) {
             const bool bad_delta = carried(hides) < BQ && !(__builtin_fabsf(next_delta) < __builtin_inff());
             if (sq.bad_row(tid, 0) | sg.bad_row(tid, 0, bad_delta)) {   // as move_bad_rows: lse becomes NaN
                 sq.fill_row(0, 0u);
@@ -296,12 +328,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
                 next_lse = __builtin_nanf("");
                 next_delta = 0.f;
             }
-        }
-        sq.store(tid, smem[t & 1]);
-        sg.store(tid, smem[t & 1] + BQ * DQK);
-        if (carried(hides) < BQ) {
-            srow[t & 1][carried(hides)] = next_lse;
-            srow[t & 1][BQ + carried(hides)] = next_delta;
+            sq.store(tid, to);
+            sg.store(tid, to + BQ * DQK);
+            store_stats(t, hides);
+        } else {
+            store_stats(t, hides);
+            landed();
         }
     };
 
@@ -315,8 +347,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
 #pragma unroll
     for (int c = 0; c < DV / 16; ++c) av[c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (t0 < nt) {
-        load(t0, in.causal);
-        store(t0, in.causal);
+        E* to = parity(t0) ? odd : even;
+        load(t0, Int<1>(), to);
+        store(t0, Int<1>(), to);
     }
     __syncthreads();
 #pragma unroll
@@ -324,13 +357,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
 #pragma unroll
     for (int vs = 0; vs < VS; ++vs) arrived(v[vs]);
     // Tile t of the rows; hides: some row of it does not see all of the keys.
-    auto step = [&](int t, auto hides) {
+    auto step = [&](int t, auto hides, const E* Q, E* next) {
         q_rows.keep(), g_rows.keep(), q_cols.keep(), g_cols.keep();
-        const E* Q = smem[t & 1];
         const E* G = Q + BQ * DQK;
-        const float* R = srow[t & 1];
+        const float* R = srow[parity(t)];
         const int row0 = t * BQ;
-        if (t + 1 < nt) load(t + 1, hides);
+        if (t + 1 < nt) load(t + 1, hides, next);
         if (!hides || row0 + BQ - 1 + off >= wkey) {
             f32x4 s[2], dp[2];
             v8 x[PD + 1];
@@ -385,12 +417,18 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
                     }
                 });
         }
-        if (t + 1 < nt) store(t + 1, hides);
+        if (t + 1 < nt) store(t + 1, hides, next);
         __syncthreads();
     };
     int t = t0;
-    for (const int th = in.causal ? min(nt, (key0 + BK - 1 - off + BQ - 1) / BQ) : t0; t < th; ++t) step(t, Int<1>());
-    for (; t < nt; ++t) step(t, Int<0>());
+    for (; t < th; ++t) step(t, Int<1>(), parity(t) ? odd : even, parity(t) ? even : odd);
+    direct_q.rows(tid, in.q_token_stride, BQ);
+    direct_g.rows(tid, (int64_t)in.H * DV, BQ);
+    for (; t + 1 < nt; t += 2) {
+        step(t, Int<0>(), even, odd);
+        step(t + 1, Int<0>(), odd, even);
+    }
+    if (t < nt) step(t, Int<0>(), even, odd);
     const int key = wkey + col;
     if (key >= nk) return;
     const int64_t row = k0 + key;

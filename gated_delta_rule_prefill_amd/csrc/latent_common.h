@@ -285,6 +285,34 @@ struct Stage {
     }
 };
 
+// The same from global memory straight into LDS, without registers between: for
+// tiles whose rows need no look.  Every wave writes 1 KB of the tile in a row, its
+// lanes fetch the chunks that belong there; the `left` rows there are repeated
+// behind the last.  fetch() issues the loads; landed() and a barrier end them.
+template <typename E, int W, int ROWS, int NT>
+struct Direct {
+    static constexpr int CE = CHUNK_ELEMS<E>, CH = W / CE, N = ROWS * CH / NT;
+    static_assert(ROWS * CH % NT == 0, "whole waves");
+    uint32_t at[N];
+    __device__ __forceinline__ void rows(int tid, int64_t stride, int last) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int n = i * NT + tid, r = n / CH;
+            const int chunk = (tile_at<E, W>(r, n % CH) - r * W) / CE;
+            at[i] = (uint32_t)min(r, last) * (uint32_t)(stride * sizeof(E)) + 16u * chunk;
+        }
+    }
+    __device__ __forceinline__ void fetch(int wave, const E* base, E* t) const {
+        typedef __attribute__((address_space(1))) const void global_void;
+        typedef __attribute__((address_space(3))) void lds_void;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            __builtin_amdgcn_global_load_lds((global_void*)(reinterpret_cast<const char*>(base) + at[i]),
+                                             (lds_void*)(t + (i * NT + 64 * wave) * CE), 16, 0, 0);
+    }
+};
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // A product over keys that some rows do not see multiplies their weights, 0, with
 // what such a key holds, and 0 times NaN or Inf is NaN.  In the tiles where that
 // can happen a row with values that are not finite is therefore cleared from the
