@@ -320,6 +320,15 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
 #pragma unroll
                 for (int w = 0; w < TW; ++w) s[w] = f32x4{0.f, 0.f, 0.f, 0.f};
                 constexpr int PD = QREG ? 4 : 1;
+                // fp32: each score is summed in four parts, whose rounding errors
+                // stay smaller than one sum's over 576 channels and whose products
+                // do not wait for each other
+                constexpr int NA = sizeof(E) == 4 ? 4 : 1;
+                f32x4 more[NA][TW];
+#pragma unroll
+                for (int i = 1; i < NA; ++i)
+#pragma unroll
+                    for (int w = 0; w < TW; ++w) more[i][w] = f32x4{0.f, 0.f, 0.f, 0.f};
                 v8 x[PD + 1], y[2];
                 ahead<KS * TW, PD>(
                     [&](auto step) {
@@ -330,8 +339,14 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
                     [&](auto step) {
                         constexpr int e = step;
                         if constexpr (QREG) s[e % TW] = mma32(x[e % (PD + 1)], q[e / TW], s[e % TW]);
-                        else s[e % TW] = mma32(x[e % (PD + 1)], y[e / TW & 1], s[e % TW]);
+                        else {
+                            f32x4& sum = e / TW % NA ? more[e / TW % NA][e % TW] : s[e % TW];
+                            sum = mma32(x[e % (PD + 1)], y[e / TW & 1], sum);
+                        }
                     });
+#pragma unroll
+                for (int w = 0; w < TW; ++w)
+                    if constexpr (NA == 4) s[w] = (s[w] + more[1][w]) + (more[2][w] + more[3][w]);
                 if (uniform(gaps[k & 3]) || (t + 1) * BN - 1 > first_last) {
 #pragma unroll
                     for (int w = 0; w < TW; ++w) {
