@@ -170,7 +170,7 @@ size_t kda_latent_decode_workspace_bytes(int64_t total_tokens, int32_t num_seqs,
     if (total_tokens < 0 || total_tokens > kMaxRows || num_seqs <= 0 || H <= 0 || H > 65535 ||
         (dl != 256 && dl != 512) || (dr != 0 && dr != 64) || !dtype_ok(dtype))
         return 0;
-    return align256(kda::latent_decode_workspace(total_tokens, num_seqs, H, dl, dtype == KDA_DTYPE_BF16));
+    return align256(kda::latent_decode_workspace(total_tokens, num_seqs, H, dl));
 }
 
 kda_status kda_latent_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* cache,

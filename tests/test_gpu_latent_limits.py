@@ -1,0 +1,156 @@
+"""Latent attention at its limits: guard bytes around every output, workspaces
+that hold anything, offsets that do not start at 0, head counts that no tile
+divides, and calls that run at the same time."""
+import pytest
+import torch
+
+import latent_reference as ref
+import test_gpu_latent_attention as ta
+import test_gpu_latent_decode as td
+from test_gpu_guards import PATTERN, Guarded, _check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def ones(n):
+    """A workspace whose every word is NaN, as bf16 and as fp32."""
+    return torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dr", [64, 0])
+def test_attention_writes_stay_in_bounds(dtype, dr):
+    import gated_delta_rule_prefill_amd as kda
+    from gated_delta_rule_prefill_amd import kda as b
+    lens, H, d = [1, 65, 0, 130], 3, 64
+    x = ta.make(60, dtype, H, d, dr, lens, lens)
+    T, t = sum(lens), ta.DT[dtype]
+    args = dict(k_pe=x["k_pe"], cu_seqlens=ta.offsets(lens), scale=x["scale"])
+    out = dict(o=Guarded((T, H, d), t), lse=Guarded((T, H), torch.float32))
+    o, lse = kda.latent_attention(x["q"], x["k"], x["v"], out=out["o"].t, lse=out["lse"].t, **args)
+    need = b.lib().kda_latent_attention_backward_workspace_bytes(T, T, H, dr)
+    out.update(dk=Guarded((T, H, d), t), dv=Guarded((T, H, d), t), ws=Guarded((need,), torch.uint8, init=ones(need)))
+    grads = kda.latent_attention_backward(x["q"], x["k"], x["v"], o, lse, x["d_o"], dk=out["dk"].t, dv=out["dv"].t,
+                                          workspace=out["ws"].t, **args)
+    _check(out, f"latent attention {dtype} dr={dr}")
+    ta.check_all("guarded", x, dict(o=o, lse=lse, **grads), lens, lens, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,new", [(3, [1, 1, 1]), (32, [70, 0, 3])])
+def test_decode_writes_stay_in_bounds(dtype, H, new):
+    from gated_delta_rule_prefill_amd import kda as b
+    lens = [300, 17, 64]
+    x = td.make(61, dtype, H, 256, 64, 16, lens, new)
+    T, t = sum(new), td.DT[dtype]
+    need = b.latent_decode_workspace_bytes(T, 3, H, 256, 64, dtype == "bf16")
+    out = dict(o=Guarded((T, H, 256), t), lse=Guarded((T, H), torch.float32),
+               ws=Guarded((need,), torch.uint8, init=ones(need)))
+    td.check("guarded", x, 256, lens, new, out=out["o"].t, lse=out["lse"].t, workspace=out["ws"].t)
+    _check(out, f"latent decode {dtype} H={H}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_and_rotary_writes_stay_in_bounds(dtype):
+    import gated_delta_rule_prefill_amd as kda
+    t, dl, dr, page, lens, new = td.DT[dtype], 256, 64, 16, [20, 5], [7, 5]
+    T = sum(new)
+    g = torch.Generator().manual_seed(62)
+    r = lambda *s: torch.randn(*s, generator=g).to(t).cuda()  # noqa: E731
+    table = torch.tensor([[2, 0], [1, -1]], dtype=torch.int32, device="cuda")
+    freq, _ = kda.rotary_frequencies(dr, device="cuda")
+    out = dict(cache=Guarded((3, page, dl + dr), t), c=Guarded((T, dl), t), pe=Guarded((T, dr), t),
+               y=Guarded((T, 3, 200), t))
+    kda.latent_append(out["cache"].t, r(T, dl), table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                      k_pe=r(T, dr), cu_seqlens=td.offsets(new), norm_weight=torch.ones(dl, device="cuda"),
+                      inv_freq=freq, c_out=out["c"].t, k_pe_out=out["pe"].t)
+    kda.rotary(r(T, 3, 200), torch.arange(T, dtype=torch.int32, device="cuda"), freq, start=104, out=out["y"].t)
+    _check(out, f"latent append {dtype}")
+    # of the cache only the new tokens' rows
+    written = (out["cache"].t.view(torch.uint8) != PATTERN).reshape(3 * page, -1).any(dim=1).nonzero().flatten().tolist()
+    rows = [16 * (2 if p < 16 else 0) + p % 16 for p in range(13, 20)] + [16 + p for p in range(5)]
+    assert written == sorted(rows)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_that_start_late(dtype):
+    """The first sequence starts behind row 0: the rows before it stay as they are."""
+    import gated_delta_rule_prefill_amd as kda
+    lens, first, H = [70, 130], 5, 5
+    x = ta.make(63, dtype, H, 128, 64, lens, lens, behind=first)
+    cu = ta.offsets(lens) + first
+    mark = lambda *s: torch.full(s, 7.0, dtype=ta.DT[dtype], device="cuda")  # noqa: E731
+    o, dk, dv = mark(205, H, 128), mark(205, H, 128), mark(205, H, 128)
+    args = dict(k_pe=x["k_pe"], cu_seqlens=cu, scale=x["scale"])
+    lse = torch.full((205, H), 7.0, device="cuda")
+    kda.latent_attention(x["q"], x["k"], x["v"], out=o, lse=lse, **args)
+    grads = kda.latent_attention_backward(x["q"], x["k"], x["v"], o, lse, x["d_o"], dk=dk, dv=dv, **args)
+    part = {n: t[first:] if t is not None and n != "scale" else t for n, t in x.items() if n != "scale"}
+    part["scale"] = x["scale"]
+    got = dict(o=o, lse=lse, **grads)
+    ta.check_all("late", part, {n: t[first:] for n, t in got.items()}, lens, lens, True)
+    for t in (o, lse, dk, dv):
+        assert (t[:first] == 7.0).all()
+
+
+@pytest.mark.parametrize("H", [3, 13, 16])
+def test_head_counts(H):
+    lens = [257, 1, 90]
+    x = ta.make(64, "bf16", H, 128, 64, lens, lens)
+    ta.check_all(f"H={H}", x, ta.both(x, lens, lens, True), lens, lens, True)
+
+
+def test_more_new_tokens_than_cached_ones():
+    """New tokens beyond the cache's length: the first of them see no key."""
+    lens, new = [3, 0], [6, 2]
+    x = td.make(65, "bf16", 2, 256, 64, 16, lens, new)
+    td.check("more new than cached", x, 256, lens, new)
+    o, lse = td.run(x, 256)
+    assert (o[:3] == 0).all() and torch.isneginf(lse[:3]).all() and (o[6:] == 0).all()
+
+
+def test_calls_at_the_same_time():
+    """Decode and training steps on two streams at once, each with its own
+    workspace, give what they give alone."""
+    import gated_delta_rule_prefill_amd as kda
+    lens, new = [5000, 700, 64], [1, 1, 1]
+    xs = [td.make(66 + i, "bf16", 32, 512, 64, 64, lens, new) for i in range(2)]
+    ts = [ta.make(68 + i, "bf16", 8, 128, 64, [300, 212], [300, 212]) for i in range(2)]
+
+    def train(x):
+        args = dict(k_pe=x["k_pe"], cu_seqlens=ta.offsets([300, 212]), scale=x["scale"])
+        o, lse = kda.latent_attention(x["q"], x["k"], x["v"], **args)
+        return kda.latent_attention_backward(x["q"], x["k"], x["v"], o, lse, x["d_o"], **args)
+
+    want = [(td.run(x, 512), train(y)) for x, y in zip(xs, ts)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s, x, y in zip(streams, xs, ts):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append((td.run(x, 512), train(y)))
+        torch.cuda.synchronize()
+        for (a, ga), (b, gb) in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            for n in ("dq", "dk", "dv", "dk_pe"):
+                assert torch.equal(ga[n], gb[n])
+
+
+def test_dirty_workspaces_change_nothing():
+    """The library's own workspaces come from memory that held NaN."""
+    from gated_delta_rule_prefill_amd import kda as b
+    lens, new = [900, 64, 5, 1], [1, 1, 1, 1]
+    x = td.make(70, "bf16", 32, 512, 64, 64, lens, new)
+    need = b.latent_decode_workspace_bytes(4, 4, 32, 512, 64, True)
+    got = td.run(x, 512, workspace=ones(need))
+    want = td.run(x, 512, workspace=torch.zeros(need, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ref.check("dirty", got[0], *ref.decode(x["q"], x["cache"], x["table"], lens, new, 512, x["scale"])[0])
