@@ -19,8 +19,8 @@ namespace kda {
 // loads are issued before a tile's products and stored to LDS behind them.
 // Bound by the matrix products: 16,384 causal tokens x 32 heads, 128 + 64
 // channels, bf16: 2.50 ms, 1.10 PFLOP/s, where a large library product reaches
-// 1.15 here; documents of 256 to 4,096 tokens (37,700 in all) 1.17 ms.  fp32,
-// 495 tokens x 4 heads: 15 us, one row tile's walk over its keys.
+// 1.15 here; documents of 256 to 4,096 tokens (36,755 in all) 1.20 ms.  fp32,
+// 6 sequences of 1 to 130 tokens x 4 heads: 15 us, one row tile's walk over its keys.
 template <typename E, int DN, int DR>
 __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     const kda_latent_inputs in, E* __restrict__ o, float* __restrict__ lse, int tiles)

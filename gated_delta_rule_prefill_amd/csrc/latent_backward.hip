@@ -20,7 +20,7 @@ namespace kda {
 // (rows = keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.
 // dq itself takes delta from the rounded o, as its own sum is complete only
 // behind the last key; the second kernel takes that sum.  Bound by the matrix
-// products: 37,700 tokens in 16 documents x 32 heads, bf16: 1.69 ms, 1.07 PFLOP/s.
+// products: 36,755 tokens in 16 documents x 32 heads, bf16: 1.69 ms, 1.07 PFLOP/s.
 template <typename E, int DN, int DR>
 __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const kda_latent_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
