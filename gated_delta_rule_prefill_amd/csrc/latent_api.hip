@@ -70,7 +70,8 @@ kda_status check_inputs(const kda_latent_inputs* in) {
         if (s >= (int64_t)1 << 23) return fail(KDA_ERR_INVALID_ARGUMENT, "token strides must be below 2^23 elements");
     // every kernel's grid: tiles (at least 64 rows each, and one more per sequence) times heads
     const int64_t most = (in->total_q > in->total_k ? in->total_q : in->total_k) / 64 + in->num_seqs;
-    if (most * in->H > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARGUMENT, "too many tiles (rows / 64 * H must be < 2^31)");
+    if (most * in->H >= (int64_t)1 << 24)   // of 256 threads each, in one dimension
+        return fail(KDA_ERR_INVALID_ARGUMENT, "too many tiles ((rows / 64 + num_seqs) * H must be below 2^24)");
     return KDA_OK;
 }
 

@@ -465,7 +465,7 @@ template <typename E, int DR>
 __global__ __launch_bounds__(256) void latent_dkpe_kernel(const float* __restrict__ part, E* __restrict__ dk_pe,
                                                           const int32_t* __restrict__ cu, int N, int total, int H)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t id = block_of_grid() * 256 + threadIdx.x;
     const int64_t row = id / (DR / 4);
     const int c = 4 * (int)(id % (DR / 4));
     const int first = cu ? clamp_offset(cu[0], total) : 0, last = cu ? clamp_offset(cu[N], total) : total;
@@ -498,8 +498,7 @@ static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipS
                            a.dv_token_stride, a.dv_head_stride, a.pe_part, (int)tk);
     if constexpr (DR > 0)
         if (in.total_k > 0)
-            hipLaunchKernelGGL((latent_dkpe_kernel<E, DR>), dim3((unsigned)((in.total_k * (DR / 4) + 255) / 256)),
-                               dim3(256), 0, stream, a.pe_part, (E*)a.dk_pe, cu_k, in.num_seqs, (int)in.total_k, in.H);
+            hipLaunchKernelGGL((latent_dkpe_kernel<E, DR>), grid_of((in.total_k * (DR / 4) + 255) / 256), dim3(256), 0, stream, a.pe_part, (E*)a.dk_pe, cu_k, in.num_seqs, (int)in.total_k, in.H);
     return hipGetLastError();
 }
 

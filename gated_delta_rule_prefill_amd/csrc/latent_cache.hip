@@ -31,7 +31,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Rotary a, int tokens,
     __shared__ float2 cs[ROTARY_PAIRS];
     constexpr int IE = INTERLEAVED ? (VE == 1 ? 2 : VE) : 2 * VE;   // elements of a rotated item
     const int half = a.dr / 2;
-    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int64_t t0 = block_of_grid() * tokens;
     const int nt = (int)min((int64_t)tokens, a.total_tokens - t0);
     for (int i = threadIdx.x; i < nt * half; i += 256) {
         float c, s;
@@ -120,7 +120,7 @@ static hipError_t launch_rotary_t(const Rotary& a, hipStream_t stream) {
     if (tokens > a.total_tokens / 512) tokens = a.total_tokens / 512;
     if (tokens > ROTARY_PAIRS / (a.dr / 2)) tokens = ROTARY_PAIRS / (a.dr / 2);
     if (tokens < 1) tokens = 1;
-    const dim3 grid((unsigned)((a.total_tokens + tokens - 1) / tokens));
+    const dim3 grid = grid_of((a.total_tokens + tokens - 1) / tokens);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, (int)tokens, copies); };
     if (wide) inter ? go(rotary_kernel<E, CE, true>) : go(rotary_kernel<E, CE, false>);
     else inter ? go(rotary_kernel<E, 1, true>) : go(rotary_kernel<E, 1, false>);
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppend a
     constexpr int CE = CHUNK_ELEMS<E>, NC = 1024 / CE / 64;   // 16-byte chunks of a lane
     typedef E vec __attribute__((ext_vector_type(CE)));
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t t = block_of_grid() * 4 + (threadIdx.x >> 6);
     if (t >= a.total_tokens) return;
     const int chunks = a.dl / CE;
     // the token's own loads do not wait for its place
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppend a
 }
 
 hipError_t launch_latent_append(const LatentAppend& a, bool bf16_io, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.total_tokens + 3) / 4));
+    const dim3 grid = grid_of((a.total_tokens + 3) / 4);
     if (bf16_io) hipLaunchKernelGGL(latent_append_kernel<bf16>, grid, dim3(256), 0, stream, a);
     else hipLaunchKernelGGL(latent_append_kernel<float>, grid, dim3(256), 0, stream, a);
     return hipGetLastError();

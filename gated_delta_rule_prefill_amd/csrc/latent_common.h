@@ -332,6 +332,13 @@ __device__ __forceinline__ void move_bad_rows(int tid, A& product, B& weights) {
         }
 }
 
+// A grid has fewer than 2^32 threads a dimension: workgroups in rows of 65,536.
+// The last row may be longer than the work; the kernels test what they are given.
+static inline dim3 grid_of(int64_t blocks) {
+    return blocks <= 65536 ? dim3((unsigned)blocks) : dim3(65536, (unsigned)((blocks + 65535) / 65536));
+}
+__device__ __forceinline__ int64_t block_of_grid() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // -- a workgroup's tile of a packed batch ----------------------------------------
 __device__ __forceinline__ int clamp_offset(int x, int total) { return min(max(x, 0), total); }
 

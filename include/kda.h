@@ -306,7 +306,8 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  *          keys j <= i + (m - n), i.e. the last query sees all of them; with
  *          m < n the first n - m queries see none
  *   scale  finite and > 0, multiplies q . k
- * dn = dv in {64, 128}; dr in {0, 64}; token strides and H * dv below 2^23.
+ * dn = dv in {64, 128}; dr in {0, 64}; token strides and H * dv below 2^23;
+ * (rows / 64 + num_seqs) * H below 2^24.
  */
 typedef struct {
     const void *q;

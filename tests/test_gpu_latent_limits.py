@@ -154,3 +154,36 @@ def test_dirty_workspaces_change_nothing():
     want = td.run(x, 512, workspace=torch.zeros(need, dtype=torch.uint8, device="cuda"))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     ref.check("dirty", got[0], *ref.decode(x["q"], x["cache"], x["table"], lens, new, 512, x["scale"])[0])
+
+
+def test_grids_of_more_than_one_row():
+    """Batches whose workgroups go into several rows of the grid end like the
+    same tokens alone."""
+    import gated_delta_rule_prefill_amd as kda
+    g = torch.Generator(device="cuda").manual_seed(71)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    freq, _ = kda.rotary_frequencies(64, device="cuda")
+    # rotary: a token a workgroup
+    T, tail = 66000, 500
+    x, pos = r(T, 32, 192), torch.arange(T, dtype=torch.int32, device="cuda")
+    y = kda.rotary(x, pos, freq, start=128)
+    assert torch.equal(y[-tail:], kda.rotary(x[-tail:].contiguous(), pos[-tail:].contiguous(), freq, start=128))
+    # append: four tokens a workgroup, into one long sequence's pages
+    T = 263000
+    c, pe = r(T, 64), r(T, 64)
+    table = torch.arange(-(-T // 64), dtype=torch.int32, device="cuda")[None]
+    cache = torch.zeros(table.numel(), 64, 128, dtype=torch.bfloat16, device="cuda")
+    kda.latent_append(cache, c, table, torch.tensor([T], dtype=torch.int32, device="cuda"), k_pe=pe, num_seqs=1)
+    assert torch.equal(cache.view(-1, 128)[:T], torch.cat([c, pe], dim=1))
+    # the sum of dk_pe: 16 keys a workgroup
+    N, tail = 16500, 20
+    T = 64 * N
+    q, k, v, pe, do = r(T, 1, 128), r(T, 1, 64), r(T, 1, 64), r(T, 64), r(T, 1, 64)
+
+    def step(a, n):
+        part = [t[a:].contiguous() for t in (q, k, v, pe, do)]
+        o, lse = kda.latent_attention(*part[:3], k_pe=part[3], num_seqs=n)
+        return kda.latent_attention_backward(*part[:3], o, lse, part[4], k_pe=part[3], num_seqs=n)
+    whole, alone = step(0, N), step(64 * (N - tail), tail)
+    for n in ("dq", "dk", "dv", "dk_pe"):
+        assert torch.equal(whole[n][-64 * tail:], alone[n])

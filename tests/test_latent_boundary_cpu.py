@@ -184,3 +184,10 @@ def test_binding_rejects_shapes_before_the_library():
         kda.latent_append(cache, torch.zeros(2, 256), table, lens)          # k_pe is missing
     with pytest.raises(ValueError):
         kda.rotary(torch.zeros(2, 1, 64), torch.zeros(2, dtype=torch.int64), torch.zeros(32))
+
+
+def test_attention_rejects_more_tiles_than_a_grid_has():
+    for kw in (dict(total_q=2 ** 28, total_k=2 ** 28, H=4, num_seqs=1), dict(num_seqs=2 ** 22, H=4)):
+        a = _inputs(**kw)
+        assert kda.lib().kda_latent_attention(a, A, A, None) == INVALID
+        assert "too many tiles" in kda.last_error()
