@@ -287,29 +287,38 @@ struct Stage {
 
 // The same from global memory straight into LDS, without registers between: for
 // tiles whose rows need no look.  Every wave writes 1 KB of the tile in a row, its
-// lanes fetch the chunks that belong there; the `left` rows there are repeated
-// behind the last.  fetch() issues the loads; landed() and a barrier end them.
-template <typename E, int W, int ROWS, int NT>
+// lanes fetch the chunks that belong there; channels [0, W - W1) come from one
+// base, the last W1 from another.  The rows up to `last` are there, and that one
+// is repeated behind it.  fetch() issues the loads; landed() and a barrier end them.
+template <typename E, int W, int ROWS, int NT, int W1 = 0>
 struct Direct {
     static constexpr int CE = CHUNK_ELEMS<E>, CH = W / CE, N = ROWS * CH / NT;
     static_assert(ROWS * CH % NT == 0, "whole waves");
-    uint32_t at[N];
-    __device__ __forceinline__ void rows(int tid, int64_t stride, int last) {
+    uint32_t at[N], second;   // byte offsets; a bit for each chunk of the second base
+    __device__ __forceinline__ void rows(int tid, int64_t stride, int64_t stride1, int last) {
+        second = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int n = i * NT + tid, r = n / CH;
             const int chunk = (tile_at<E, W>(r, n % CH) - r * W) / CE;
-            at[i] = (uint32_t)min(r, last) * (uint32_t)(stride * sizeof(E)) + 16u * chunk;
+            const bool from1 = W1 > 0 && chunk >= (W - W1) / CE;
+            second |= from1 ? 1u << i : 0u;
+            at[i] = (uint32_t)min(r, last) * (uint32_t)((from1 ? stride1 : stride) * sizeof(E)) +
+                    16u * (from1 ? chunk - (W - W1) / CE : chunk);
         }
     }
-    __device__ __forceinline__ void fetch(int wave, const E* base, E* t) const {
+    __device__ __forceinline__ void rows(int tid, int64_t stride, int last) { rows(tid, stride, 0, last); }
+    __device__ __forceinline__ void fetch(int wave, const E* base, const E* base1, E* t) const {
         typedef __attribute__((address_space(1))) const void global_void;
         typedef __attribute__((address_space(3))) void lds_void;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            __builtin_amdgcn_global_load_lds((global_void*)(reinterpret_cast<const char*>(base) + at[i]),
+        for (int i = 0; i < N; ++i) {
+            const E* from = W1 > 0 && (second >> i & 1) ? base1 : base;
+            __builtin_amdgcn_global_load_lds((global_void*)(reinterpret_cast<const char*>(from) + at[i]),
                                              (lds_void*)(t + (i * NT + 64 * wave) * CE), 16, 0, 0);
+        }
     }
+    __device__ __forceinline__ void fetch(int wave, const E* base, E* t) const { fetch(wave, base, base, t); }
 };
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
