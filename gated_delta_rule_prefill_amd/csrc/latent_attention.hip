@@ -18,8 +18,8 @@ namespace kda {
 // double-buffered in LDS (80 KB, two workgroups a CU): the next tile's global
 // loads are issued before a tile's products and stored to LDS behind them.
 // Bound by the matrix products: 16,384 causal tokens x 32 heads, 128 + 64
-// channels, bf16: 2.50 ms, 1.10 PFLOP/s, where a large library product reaches
-// 1.15 here; documents of 256 to 4,096 tokens (36,755 in all) 1.20 ms.  fp32,
+// channels, bf16: 2.4 ms, 1.13 PFLOP/s, where a large library product reaches
+// 1.15 here; documents of 256 to 4,096 tokens (36,755 in all) 1.16 ms.  fp32,
 // 6 sequences of 1 to 130 tokens x 4 heads: 15 us, one row tile's walk over its keys.
 template <typename E, int DN, int DR>
 __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
@@ -69,8 +69,9 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
 
     Stage<E, DQK, BN, 256> sk;
     Stage<E, DV, BN, 256> sv;
-    // Tiles that all rows see whole go straight to LDS; the others through
-    // registers, where rows that are not finite are found and taken out.
+    // Tiles that all rows see whole go straight to LDS (2.48 -> 2.38 ms for 16,384
+    // tokens); the others through registers, where rows that are not finite are
+    // found and taken out.
     Direct<E, DQK, BN, 256, DR> direct_k;
     Direct<E, DV, BN, 256> direct_v;
     auto load = [&](int t, auto hides, E* to) {

@@ -14,7 +14,7 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // Query rows of a wave in 16-row tiles (forward, dq).  bf16: two tiles, so that an operand read from LDS serves two
-// products.  fp32: one; its products take eight times as long, LDS is no bound,
+// products.  fp32: one; its products take sixteen times as long, LDS is no bound,
 // and the smaller tiles spread a short batch over more CUs (130 tokens x 4
 // heads: 22 us with two tiles).
 template <typename E> constexpr int LATENT_NQ = sizeof(E) == 2 ? 2 : 1;
