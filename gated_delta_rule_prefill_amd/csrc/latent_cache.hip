@@ -25,7 +25,7 @@ __device__ __forceinline__ void rotation(int position, float inv_freq, bool inve
 // 16-byte access, or 1 where alignment or sizes do not allow it.
 constexpr int ROTARY_PAIRS = 2048;   // angles of a workgroup
 
-template <typename E, int VE, bool INTERLEAVED>
+template <typename E, int VE, bool INTERLEAVED, bool FAR>
 __global__ __launch_bounds__(256) void rotary_kernel(const Rotary a, int tokens, int copies)
 {
     __shared__ float2 cs[ROTARY_PAIRS];
@@ -48,13 +48,17 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Rotary a, int tokens,
             for (int i = 0; i < VE; ++i) v[i] = to_f32(x[i]);
         }
     };
-    auto put = [](E* p, const float* v) {
+    auto store = [](E* p, vec x) {
+        if constexpr (FAR) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, x), reinterpret_cast<u32x4*>(p));
+        else *reinterpret_cast<vec*>(p) = x;
+    };
+    auto put = [store](E* p, const float* v) {
         if constexpr (VE == 1) p[0] = from_f32<E>(v[0]);
         else {
             vec x;
 #pragma unroll
             for (int i = 0; i < VE; ++i) x[i] = from_f32<E>(v[i]);
-            *reinterpret_cast<vec*>(p) = x;
+            store(p, x);
         }
     };
     const int turned = a.dr / IE, items = turned + copies, rows = nt * a.H;
@@ -68,7 +72,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Rotary a, int tokens,
             int at = (item - turned) * VE;
             if (at >= a.start) at += a.dr;
             if constexpr (VE == 1) y[at] = x[at];
-            else *reinterpret_cast<vec*>(y + at) = *reinterpret_cast<const vec*>(x + at);
+            else store(y + at, *reinterpret_cast<const vec*>(x + at));
             continue;
         }
         const float2* w = cs + t * half;
@@ -113,7 +117,7 @@ static hipError_t launch_rotary_t(const Rotary& a, hipStream_t stream) {
     const int copies = in_place ? 0 : (a.d - a.dr) / (wide ? CE : 1);
     const int items = a.dr / (wide ? (inter ? CE : 2 * CE) : 2) + copies;
     // Tokens of a workgroup: about three items a thread (a prompt of 65,536 x 32
-    // x 192 in bf16, one token each: 285 us, 5.65 TB/s, where a copy of as many
+    // x 192 in bf16, one token each: 275 us, 5.85 TB/s, where a copy of as many
     // bytes takes 306; with runs of four rows per thread, 346), with its angles
     // in LDS and at least 512 workgroups.
     int64_t tokens = 768 / ((int64_t)a.H * items);
@@ -121,9 +125,13 @@ static hipError_t launch_rotary_t(const Rotary& a, hipStream_t stream) {
     if (tokens > ROTARY_PAIRS / (a.dr / 2)) tokens = ROTARY_PAIRS / (a.dr / 2);
     if (tokens < 1) tokens = 1;
     const dim3 grid = grid_of((a.total_tokens + tokens - 1) / tokens);
+    // More than the 256 MB of the last-level cache is stored past the caches (that
+    // prompt 284 us without; what fits may stay there for its reader).
+    const bool far = a.total_tokens * a.H * (int64_t)(in_place ? a.dr : a.d) * (int64_t)sizeof(E) > (int64_t)256 << 20;
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, (int)tokens, copies); };
-    if (wide) inter ? go(rotary_kernel<E, CE, true>) : go(rotary_kernel<E, CE, false>);
-    else inter ? go(rotary_kernel<E, 1, true>) : go(rotary_kernel<E, 1, false>);
+    if (wide && far) inter ? go(rotary_kernel<E, CE, true, true>) : go(rotary_kernel<E, CE, false, true>);
+    else if (wide) inter ? go(rotary_kernel<E, CE, true, false>) : go(rotary_kernel<E, CE, false, false>);
+    else inter ? go(rotary_kernel<E, 1, true, false>) : go(rotary_kernel<E, 1, false, false>);
     return hipGetLastError();
 }
 

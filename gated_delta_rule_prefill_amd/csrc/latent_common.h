@@ -201,14 +201,19 @@ struct Stage {
     static_assert(ROWS % PASS == 0 && PASS % 16 == 0 && W % (TPR * CE) == 0, "whole passes and steps");
     u32x4 r[P][S];
     // rows in any order: row(r) returns the row's address (zero_row() for a row
-    // that is not there, so that no load is conditional)
-    template <typename F>
+    // that is not there, so that no load is conditional).  ONCE: rows that no other
+    // workgroup reads, which the caches need not keep.
+    template <bool ONCE>
+    static __device__ __forceinline__ u32x4 chunk(const E* a) {
+        return ONCE ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(a)) : *reinterpret_cast<const u32x4*>(a);
+    }
+    template <bool ONCE, typename F>
     __device__ __forceinline__ void load(int tid, F row) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const E* a = row(tid / TPR + PASS * p) + CE * (tid % TPR);
 #pragma unroll
-            for (int s = 0; s < S; ++s) r[p][s] = *reinterpret_cast<const u32x4*>(a + TPR * CE * s);
+            for (int s = 0; s < S; ++s) r[p][s] = chunk<ONCE>(a + TPR * CE * s);
         }
     }
     // Rows `stride` elements apart from a base that is the same for all threads,
@@ -262,7 +267,7 @@ struct Stage {
     }
     // store(), each chunk's register refilled at once with the tile after next,
     // so that a tile's worth of loads stays in flight
-    template <typename F>
+    template <bool ONCE, typename F>
     __device__ __forceinline__ void store_load(int tid, E* t, F row) {
         const int at = tile_at<E, W>(tid / TPR, tid % TPR);
 #pragma unroll
@@ -271,7 +276,7 @@ struct Stage {
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 *reinterpret_cast<u32x4*>(t + later_chunk<E, W>(at, TPR * s) + PASS * p * W) = r[p][s];
-                r[p][s] = *reinterpret_cast<const u32x4*>(a + TPR * CE * s);
+                r[p][s] = chunk<ONCE>(a + TPR * CE * s);
             }
         }
     }

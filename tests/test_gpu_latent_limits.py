@@ -187,3 +187,19 @@ def test_grids_of_more_than_one_row():
     whole, alone = step(0, N), step(64 * (N - tail), tail)
     for n in ("dq", "dk", "dv", "dk_pe"):
         assert torch.equal(whole[n][-64 * tail:], alone[n])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rotary_of_more_than_the_caches_hold(interleaved, in_place):
+    """Outputs beyond 256 MB are stored another way: the same values."""
+    import gated_delta_rule_prefill_amd as kda
+    T, H, d = 33000, 32, 192 if not in_place else 128
+    x = torch.randn(T, H, d, generator=torch.Generator(device="cuda").manual_seed(72), device="cuda").bfloat16()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    freq, _ = kda.rotary_frequencies(128, device="cuda")
+    parts = [slice(0, 100), slice(16000, 16100), slice(T - 100, T)]
+    want = [kda.rotary(x[p].contiguous(), pos[p].contiguous(), freq, start=d - 128, interleaved=interleaved) for p in parts]
+    y = kda.rotary(x, pos, freq, start=d - 128, interleaved=interleaved, out=x if in_place else None)
+    for p, w in zip(parts, want):
+        assert torch.equal(y[p], w)
