@@ -93,6 +93,19 @@ kda_status check_pages(const void* cache, int32_t num_pages, int32_t page_size, 
     return KDA_OK;
 }
 
+// Byte offsets of the backward pass's workspace; the splits' sums (small batches
+// only) are sized for 128 channels.
+struct BackwardSpace {
+    size_t pe, part_k, part_q, bytes;
+    BackwardSpace(int64_t total_q, int64_t total_k, int32_t H, int32_t dr) {
+        const int sk = kda::latent_splits(total_k, H), sq = kda::latent_splits(total_q, H);
+        pe = align256((size_t)total_q * H * 8);
+        part_k = pe + align256((size_t)total_k * H * dr * 4);
+        part_q = part_k + (sk > 1 ? align256((size_t)sk * total_k * H * (256 + dr) * 4) : 0);
+        bytes = part_q + (sq > 1 ? align256((size_t)sq * total_q * H * (128 + dr) * 4) : 0) + 256;
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -114,7 +127,8 @@ size_t kda_latent_attention_backward_workspace_bytes(int64_t total_q, int64_t to
     if (total_q < 0 || total_k < 0 || total_q > kMaxRows || total_k > kMaxRows || H <= 0 || H > 65535 ||
         (dr != 0 && dr != 64))
         return 0;
-    return align256((size_t)total_q * H * 8) + align256((size_t)total_k * H * dr * 4) + 256;
+    const BackwardSpace s(total_q, total_k, H, dr);
+    return s.bytes;
 }
 
 kda_status kda_latent_attention_backward(const kda_latent_inputs* in, const void* o, const float* lse,
@@ -152,9 +166,10 @@ kda_status kda_latent_attention_backward(const kda_latent_inputs* in, const void
         if (!ws)
             if (kda_status st = launched(hipMallocAsync(reinterpret_cast<void**>(&ws), need, stream), "hipMallocAsync"))
                 return st;
+        const BackwardSpace s(in->total_q, in->total_k, in->H, in->dr);
         kda::LatentGrads g{o, lse, d_o, dq, dk, dk_token_stride, dk_head_stride, dv, dv_token_stride, dv_head_stride,
-                           dk_pe, reinterpret_cast<float*>(ws),
-                           reinterpret_cast<float*>(ws + align256((size_t)in->total_q * in->H * 8))};
+                           dk_pe, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + s.pe),
+                           reinterpret_cast<float*>(ws + s.part_k), reinterpret_cast<float*>(ws + s.part_q)};
         kda_status st = launched(kda::launch_latent_attention_backward(*in, g, stream), "latent backward kernels");
         if (!workspace) {
             const kda_status fr = launched(hipFreeAsync(ws, stream), "hipFreeAsync");

@@ -12,9 +12,22 @@
 // tile of keys (dk, dv and the head's part of dk_pe).  Each forms the weights
 // again from q, k and lse: one of seven products more than a single kernel
 // with atomic sums of dq.  A third kernel sums dk_pe over the heads.
+#include <algorithm>
+
 #include "latent_common.h"
 
 namespace kda {
+
+// fp32: a batch of few tiles has each one's walk split over workgroups (the grid's
+// second dimension), whose sums latent_sum_kernel adds in order.  One row tile's
+// products fill a CU's matrix units for 5 us a step, on 40 CUs of 256 for 495
+// tokens x 4 heads: 55 + 68 us without, 26 + 30 and the sum's 9 with.  Delta then comes from o, which in
+// fp32 is as exact as the sum.
+template <typename E> constexpr bool SPLIT = sizeof(E) == 4;
+int latent_splits(int64_t rows, int32_t H) {
+    const int64_t tiles = (rows + 63) / 64 * H;
+    return tiles >= 128 || tiles == 0 ? 1 : (int)std::min<int64_t>(8, 256 / tiles);
+}
 
 // dq and delta.  As in the forward kernel the scores are formed transposed
 // (rows = keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.
@@ -24,7 +37,7 @@ namespace kda {
 template <typename E, int DN, int DR>
 __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     const kda_latent_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
-    const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ row_stats, int tiles)
+    const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ row_stats, float* __restrict__ part, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BN = 32, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
     constexpr int KS = DQK / 32, VS = DV / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
@@ -79,7 +92,10 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         exact[j] = 0.f;
     }
     const int end = in.causal ? min(nk, min(nq, (tile + 1) * BQ) + off) : nk;
-    const int nt = end > 0 ? (end + BN - 1) / BN : 0;
+    const int all = end > 0 ? (end + BN - 1) / BN : 0;
+    // the key tiles of this split (fp32)
+    const int tb = SPLIT<E> ? (int)((int64_t)all * blockIdx.y / gridDim.y) : 0;
+    const int nt = SPLIT<E> ? (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y) : all;
     const int wave_end = in.causal ? min(nk, min(nq, wrow + 16 * NQ) + off) : nk;
     const int wave_full = in.causal ? min(nk, wrow + off + 1) : nk;
 
@@ -121,8 +137,8 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
         for (int c = 0; c < DQK / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (nt > 0) {
-        load(0, Int<1>(), even);
+    if (tb < nt) {
+        load(tb, Int<1>(), even);
         store(Int<1>(), even);
     }
     __syncthreads();
@@ -215,16 +231,16 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         __syncthreads();
     };
     const int full = in.causal ? min(nk, tile * BQ + off + 1) : nk;   // keys all the workgroup's rows see
-    const int td = full / BN - 1;                                      // tiles up to here are seen whole
+    const int td = min(full / BN - 1, nt);                             // tiles up to here are seen whole
     direct_k.rows(tid, in.k_token_stride, in.k_pe_token_stride, BN);
     direct_v.rows(tid, in.v_token_stride, BN);
-    int t = 0;
+    int t = tb;
     for (; t + 1 < td; t += 2) {
         step(t, Int<0>(), even, odd);
         step(t + 1, Int<0>(), odd, even);
     }
     if (t < td) step(t++, Int<0>(), even, odd);
-    for (; t < nt; ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
+    for (; t < nt; ++t) step(t, Int<1>(), (t - tb) & 1 ? odd : even, (t - tb) & 1 ? even : odd);
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;
@@ -233,7 +249,13 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
         if (g == 0) {
             float* stats = row_stats + 2 * ((int64_t)h * in.total_q + q0 + r);
             stats[0] = lse2[j];
-            stats[1] = sum;
+            stats[1] = SPLIT<E> && gridDim.y > 1 ? dl[j] : sum;
+        }
+        if (SPLIT<E> && gridDim.y > 1) {
+            float* to = part + (((int64_t)blockIdx.y * in.total_q + q0 + r) * in.H + h) * DQK + 4 * g;
+#pragma unroll
+            for (int c = 0; c < DQK / 16; ++c) store_vec(to + 16 * c, acc[j][c] * in.scale);
+            continue;
         }
         E* row = dq + ((int64_t)(q0 + r) * in.H + h) * DQK;
 #pragma unroll
@@ -258,7 +280,8 @@ template <typename E, int DN, int DR>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel(
     const kda_latent_inputs in, const E* __restrict__ d_o, const float* __restrict__ row_stats,
     E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
-    E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ pe_part, int tiles)
+    E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ pe_part,
+    float* __restrict__ part, int tiles)
 {
     constexpr int DQK = DN + DR, DV = DN, BQ = 32, BK = 64;
     constexpr int KS = DQK / 32, VS = DV / 32, PD = sizeof(E) == 2 ? 3 : 1;
@@ -295,9 +318,11 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
 #pragma unroll
         for (int vs = 0; vs < VS; ++vs) v[vs] = row_frag_global(vp, vs, lane);
     }
-    const int nt = (nq + BQ - 1) / BQ;
-    const int t0 = in.causal ? min(nt, max(0, key0 - off) / BQ) : 0;   // rows before it see none of the keys
-
+    const int all = (nq + BQ - 1) / BQ;
+    const int first = in.causal ? min(all, max(0, key0 - off) / BQ) : 0;   // rows before it see none of the keys
+    // the row tiles of this split (fp32)
+    const int t0 = SPLIT<E> ? first + (int)((int64_t)(all - first) * blockIdx.y / gridDim.y) : first;
+    const int nt = SPLIT<E> ? first + (int)((int64_t)(all - first) * (blockIdx.y + 1) / gridDim.y) : all;
     // first row tile whose rows see all of the workgroup's keys
     const int th = in.causal ? max(t0, min(nt, (key0 + BK - 1 - off + BQ - 1) / BQ)) : t0;
     // tile t lies in even or odd by its distance from th
@@ -463,6 +488,14 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void latent_dkv_kernel
     const int key = wkey + col;
     if (key >= nk) return;
     const int64_t row = k0 + key;
+    if (SPLIT<E> && gridDim.y > 1) {
+        float* to = part + (((int64_t)blockIdx.y * in.total_k + row) * in.H + h) * (DQK + DV) + 4 * g;
+#pragma unroll
+        for (int c = 0; c < DQK / 16; ++c) store_vec(to + 16 * c, ak[c] * in.scale);
+#pragma unroll
+        for (int c = 0; c < DV / 16; ++c) store_vec(to + DQK + 16 * c, av[c]);
+        return;
+    }
     E* kr = dk + row * dk_token_stride + h * dk_head_stride;
     E* vr = dv + row * dv_token_stride + h * dv_head_stride;
 #pragma unroll
@@ -504,6 +537,43 @@ __global__ __launch_bounds__(256) void latent_dkpe_kernel(const float* __restric
     store_vec(dk_pe + row * DR + c, x);
 }
 
+// The splits' sums: dk, dv and dk_pe (over the heads too) of a key, dq of a query.
+// A thread per 4 channels.
+template <typename E, int DN, int DR>
+__global__ __launch_bounds__(256) void latent_sum_kernel(const kda_latent_inputs in, const LatentGrads a, int splits_k,
+                                                         int splits_q)
+{
+    constexpr int DQK = DN + DR, DV = DN, KC = (DN + DV) / 4, QC = DQK / 4;
+    int64_t id = block_of_grid() * 256 + threadIdx.x;
+    const int64_t per_key = splits_k > 1 ? in.H * KC + DR / 4 : 0, keys = in.total_k * per_key;
+    const bool key = id < keys;
+    if (!key) id -= keys;
+    const int64_t per = key ? per_key : in.H * QC, total = key ? in.total_k : in.total_q, row = id / per;
+    if (!key && (splits_q == 1 || row >= total)) return;
+    const int j = (int)(id - row * per), splits = key ? splits_k : splits_q;
+    const int32_t* cu = key && in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
+    if (cu && (row < clamp_offset(cu[0], (int)total) || row >= clamp_offset(cu[in.num_seqs], (int)total))) return;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    E* to;
+    if (!key || j < in.H * KC) {
+        const int h = j / (key ? KC : QC), c = 4 * (j - h * (key ? KC : QC)), W = key ? DQK + DV : DQK;
+        const float* from = (key ? a.part_k : a.part_q) + (row * in.H + h) * W + (key && c >= DN ? DR + c : c);
+#pragma unroll 8
+        for (int s = 0; s < splits; ++s) sum += *reinterpret_cast<const f32x4*>(from + s * total * in.H * W);
+        to = !key     ? (E*)a.dq + (row * in.H + h) * DQK + c
+             : c < DN ? (E*)a.dk + row * a.dk_token_stride + h * a.dk_head_stride + c
+                      : (E*)a.dv + row * a.dv_token_stride + h * a.dv_head_stride + c - DN;
+    } else {
+        const int c = 4 * (j - in.H * KC);
+        const float* from = a.part_k + row * in.H * (DQK + DV) + DN + c;
+#pragma unroll 16
+        for (int i = 0; i < splits * in.H; ++i)
+            sum += *reinterpret_cast<const f32x4*>(from + (i / in.H * total * in.H + i % in.H) * (DQK + DV));
+        to = (E*)a.dk_pe + row * DR + c;
+    }
+    store_vec(to, sum);
+}
+
 static int64_t tile_count(const int32_t* cu, int64_t total, int32_t N, int B) {
     return cu ? total / B + N : (total / N + B - 1) / B * N;
 }
@@ -513,16 +583,24 @@ static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipS
     const int64_t tq = tile_count(in.cu_seqlens_q, in.total_q, in.num_seqs, 64 * LATENT_NQ<E>);
     const int32_t* cu_k = in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q;
     const int64_t tk = tile_count(cu_k, in.total_k, in.num_seqs, 64);
+    const int sq = SPLIT<E> ? latent_splits(in.total_q, in.H) : 1, sk = SPLIT<E> ? latent_splits(in.total_k, in.H) : 1;
     if (tq > 0)
-        hipLaunchKernelGGL((latent_dq_kernel<E, DN, DR>), dim3((unsigned)(tq * in.H)), dim3(256), 0, stream, in,
-                           (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, (int)tq);
+        hipLaunchKernelGGL((latent_dq_kernel<E, DN, DR>), dim3((unsigned)(tq * in.H), sq), dim3(256), 0, stream, in,
+                           (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, a.part_q, (int)tq);
     if (tk > 0)
-        hipLaunchKernelGGL((latent_dkv_kernel<E, DN, DR>), dim3((unsigned)(tk * in.H)), dim3(256), 0, stream, in,
+        hipLaunchKernelGGL((latent_dkv_kernel<E, DN, DR>), dim3((unsigned)(tk * in.H), sk), dim3(256), 0, stream, in,
                            (const E*)a.d_o, a.row_stats, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv,
-                           a.dv_token_stride, a.dv_head_stride, a.pe_part, (int)tk);
+                           a.dv_token_stride, a.dv_head_stride, a.pe_part, a.part_k, (int)tk);
+    if constexpr (SPLIT<E>)
+        if (sk > 1 || sq > 1) {
+            const int64_t items = (sk > 1 ? in.total_k * (in.H * (2 * DN) / 4 + DR / 4) : 0) +
+                                  (sq > 1 ? in.total_q * in.H * (DN + DR) / 4 : 0);
+            hipLaunchKernelGGL((latent_sum_kernel<E, DN, DR>), grid_of((items + 255) / 256), dim3(256), 0, stream, in, a, sk, sq);
+        }
     if constexpr (DR > 0)
-        if (in.total_k > 0)
-            hipLaunchKernelGGL((latent_dkpe_kernel<E, DR>), grid_of((in.total_k * (DR / 4) + 255) / 256), dim3(256), 0, stream, a.pe_part, (E*)a.dk_pe, cu_k, in.num_seqs, (int)in.total_k, in.H);
+        if (in.total_k > 0 && sk == 1)
+            hipLaunchKernelGGL((latent_dkpe_kernel<E, DR>), grid_of((in.total_k * (DR / 4) + 255) / 256), dim3(256), 0,
+                               stream, a.pe_part, (E*)a.dk_pe, cu_k, in.num_seqs, (int)in.total_k, in.H);
     return hipGetLastError();
 }
 

@@ -25,7 +25,11 @@ struct LatentGrads {
     void* dk_pe;
     float* row_stats;
     float* pe_part;
+    float* part_k;   // [splits, total_k, H, dn + dr + dv], [splits, total_q, H, dn + dr]
+    float* part_q;
 };
+// Workgroups that share an fp32 tile of a batch of so many rows.
+int latent_splits(int64_t rows, int32_t H);
 hipError_t launch_latent_attention_backward(const kda_latent_inputs& in, const LatentGrads& g,
                                             hipStream_t stream);
 

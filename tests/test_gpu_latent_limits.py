@@ -203,3 +203,13 @@ def test_rotary_of_more_than_the_caches_hold(interleaved, in_place):
     y = kda.rotary(x, pos, freq, start=d - 128, interleaved=interleaved, out=x if in_place else None)
     for p, w in zip(parts, want):
         assert torch.equal(y[p], w)
+
+
+@pytest.mark.parametrize("lens_q,lens_k,H", [([2100], [2100], 4), ([700, 5, 0], [700, 5, 0], 3), ([64, 0], [9000, 70], 1),
+                                             ([9000], [40], 1), ([1], [1], 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_fp32_gradients_split_and_whole(lens_q, lens_k, H, causal):
+    """fp32 batches on either side of the size from which a tile's walk is no
+    longer shared by several workgroups, queries and keys apart."""
+    x = ta.make(73, "f32", H, 64, 64, lens_q, lens_k)
+    ta.check_all("split", x, ta.both(x, lens_q, lens_k, causal), lens_q, lens_k, causal)
