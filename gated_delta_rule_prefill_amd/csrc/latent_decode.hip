@@ -264,6 +264,14 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
                     if (tid % S::TPR == 0) ridx[k & 3][tid / S::TPR + S::PASS * p] = -2;
                 }
         };
+        if (count > 0) {
+            Stage<E, W, BN, NT> first;
+            first.template load<ONCE>(tid, row_of(0));
+            st.template load<ONCE>(tid, row_of(1));
+            if (tid < BN) next_row = cache_row(3);
+            if (hides(0)) mark_bad_rows(first, 0);
+            first.store(tid, tilebuf[0]);
+        }
         v8 q[QREG ? KS : 1];
         const E* qp;
         int last;                                                    // last key this lane's row sees
@@ -276,14 +284,6 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) q[ks] = row_frag_global(qp, ks, lane);
         }
-        if (count > 0) {
-            Stage<E, W, BN, NT> first;
-            first.template load<ONCE>(tid, row_of(0));
-            st.template load<ONCE>(tid, row_of(1));
-            if (tid < BN) next_row = cache_row(3);
-            if (hides(0)) mark_bad_rows(first, 0);
-            first.store(tid, tilebuf[0]);
-        }
         f32x4 acc[RT][CT];
         float m[RT], own = neg_inf(), l = 0.f;                       // own: the maxima of this wave's row tile
 #pragma unroll
@@ -293,7 +293,9 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
             for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
         __syncthreads();
-        if (QREG)
+        // (256 sequences 240 us with this wait here, 255 without; chunks, whose pieces
+        // have more tiles, 535 with and 520 without)
+        if (QREG && RT == 2)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) arrived(q[ks]);
         for (int k = 0; k < count; ++k) {
