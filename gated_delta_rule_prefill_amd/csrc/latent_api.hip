@@ -2,6 +2,7 @@
 // checks, workspace and launches (host code only).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <string>
@@ -93,16 +94,18 @@ kda_status check_pages(const void* cache, int32_t num_pages, int32_t page_size, 
     return KDA_OK;
 }
 
-// Byte offsets of the backward pass's workspace; the splits' sums (small batches
-// only) are sized for 128 channels.
+// Byte offsets of the backward pass's workspace.  The splits' sums (fp32 only) are
+// sized for 128 channels and for any number of rows up to these: a tile of 64
+// rows is shared by at most 8 workgroups, and all shared tiles by at most 256.
+// So a workspace for a large batch also serves a small one, which is split.
 struct BackwardSpace {
     size_t pe, part_k, part_q, bytes;
-    BackwardSpace(int64_t total_q, int64_t total_k, int32_t H, int32_t dr) {
-        const int sk = kda::latent_splits(total_k, H), sq = kda::latent_splits(total_q, H);
+    static size_t split_rows(int64_t rows, int32_t H) { return std::min<size_t>(8 * (size_t)rows * H, 256 * 64); }
+    BackwardSpace(int64_t total_q, int64_t total_k, int32_t H, int32_t dr, bool fp32) {
         pe = align256((size_t)total_q * H * 8);
         part_k = pe + align256((size_t)total_k * H * dr * 4);
-        part_q = part_k + (sk > 1 ? align256((size_t)sk * total_k * H * (256 + dr) * 4) : 0);
-        bytes = part_q + (sq > 1 ? align256((size_t)sq * total_q * H * (128 + dr) * 4) : 0) + 256;
+        part_q = part_k + (fp32 ? align256(split_rows(total_k, H) * (256 + dr) * 4) : 0);
+        bytes = part_q + (fp32 ? align256(split_rows(total_q, H) * (128 + dr) * 4) : 0) + 256;
     }
 };
 
@@ -127,8 +130,7 @@ size_t kda_latent_attention_backward_workspace_bytes(int64_t total_q, int64_t to
     if (total_q < 0 || total_k < 0 || total_q > kMaxRows || total_k > kMaxRows || H <= 0 || H > 65535 ||
         (dr != 0 && dr != 64))
         return 0;
-    const BackwardSpace s(total_q, total_k, H, dr);
-    return s.bytes;
+    return BackwardSpace(total_q, total_k, H, dr, true).bytes;
 }
 
 kda_status kda_latent_attention_backward(const kda_latent_inputs* in, const void* o, const float* lse,
@@ -155,7 +157,8 @@ kda_status kda_latent_attention_backward(const kda_latent_inputs* in, const void
             return fail(KDA_ERR_INVALID_ARGUMENT, "strides of dk and dv must be at least dn and dv");
         if (!workspace && workspace_bytes != 0)
             return fail(KDA_ERR_INVALID_ARGUMENT, "workspace_bytes given without a workspace");
-        const size_t need = kda_latent_attention_backward_workspace_bytes(in->total_q, in->total_k, in->H, in->dr);
+        const BackwardSpace s(in->total_q, in->total_k, in->H, in->dr, in->dtype == KDA_DTYPE_F32);
+        const size_t need = s.bytes;
         if (workspace && workspace_bytes < need) {
             kda::set_last_error("workspace too small: need " + std::to_string(need) + " bytes");
             return KDA_ERR_WORKSPACE;
@@ -166,7 +169,6 @@ kda_status kda_latent_attention_backward(const kda_latent_inputs* in, const void
         if (!ws)
             if (kda_status st = launched(hipMallocAsync(reinterpret_cast<void**>(&ws), need, stream), "hipMallocAsync"))
                 return st;
-        const BackwardSpace s(in->total_q, in->total_k, in->H, in->dr);
         kda::LatentGrads g{o, lse, d_o, dq, dk, dk_token_stride, dk_head_stride, dv, dv_token_stride, dv_head_stride,
                            dk_pe, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + s.pe),
                            reinterpret_cast<float*>(ws + s.part_k), reinterpret_cast<float*>(ws + s.part_q)};
@@ -186,7 +188,7 @@ size_t kda_latent_decode_workspace_bytes(int64_t total_tokens, int32_t num_seqs,
     if (total_tokens < 0 || total_tokens > kMaxRows || num_seqs <= 0 || H <= 0 || H > 65535 ||
         (dl != 256 && dl != 512) || (dr != 0 && dr != 64) || !dtype_ok(dtype))
         return 0;
-    return align256(kda::latent_decode_workspace(total_tokens, num_seqs, H, dl));
+    return align256(kda::latent_decode_workspace(dl));
 }
 
 kda_status kda_latent_decode(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* cache,

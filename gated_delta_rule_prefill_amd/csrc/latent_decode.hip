@@ -589,9 +589,11 @@ static_assert(DEC_RUNS <= 256, "a thread per part");
 // half would be empty).
 static bool few_rows(int64_t total_tokens, int32_t N, int32_t H) { return (total_tokens + N - 1) / N * H <= 32; }
 
-size_t latent_decode_workspace(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t dl) {
-    // partial results are fp32 for either type, and a tile has as many rows
-    return few_rows(total_tokens, num_seqs, H) ? space_bytes<DecodeFew<float>>(dl) : space_bytes<DecodeMany<float>>(dl);
+size_t latent_decode_workspace(int32_t dl) {
+    // Partial results are fp32 for either type, and a tile has as many rows.  Sized
+    // for the larger shape whatever the batch, as a batch with more tokens may
+    // take the smaller one.
+    return space_bytes<DecodeMany<float>>(dl);
 }
 
 template <typename E, int DL, int DR, typename S>

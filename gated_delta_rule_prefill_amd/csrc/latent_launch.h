@@ -49,7 +49,7 @@ struct LatentDecode {
     float* lse;
     void* workspace;
 };
-size_t latent_decode_workspace(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t dl);
+size_t latent_decode_workspace(int32_t dl);
 hipError_t launch_latent_decode(const LatentDecode& a, bool bf16_io, hipStream_t stream);
 
 struct LatentAppend {

@@ -339,7 +339,11 @@ typedef struct {
  */
 kda_status kda_latent_attention(const kda_latent_inputs *in, void *o, float *lse, void *stream);
 
-/* Device workspace kda_latent_attention_backward needs (bytes, 256-aligned; 0 for invalid sizes). */
+/*
+ * Device workspace that suffices for kda_latent_attention_backward with either
+ * dtype (bytes, 256-aligned; 0 for invalid sizes).  It never falls as an argument
+ * grows: a workspace for the largest batch serves every smaller one.
+ */
 size_t kda_latent_attention_backward_workspace_bytes(int64_t total_q, int64_t total_k, int32_t H,
                                                      int32_t dr);
 
@@ -366,7 +370,8 @@ kda_status kda_latent_attention_backward(const kda_latent_inputs *in, const void
 
 /*
  * Device workspace kda_latent_decode needs (bytes, 256-aligned; 0 for invalid
- * sizes): the partial results of rows whose keys are split over workgroups.
+ * sizes): the partial results of rows whose keys are split over workgroups.  It
+ * depends on dl only, so that one workspace serves batches of any size.
  */
 size_t kda_latent_decode_workspace_bytes(int64_t total_tokens, int32_t num_seqs, int32_t H,
                                          int32_t dl, int32_t dr, kda_dtype dtype);

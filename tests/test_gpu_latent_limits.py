@@ -213,3 +213,26 @@ def test_fp32_gradients_split_and_whole(lens_q, lens_k, H, causal):
     longer shared by several workgroups, queries and keys apart."""
     x = ta.make(73, "f32", H, 64, 64, lens_q, lens_k)
     ta.check_all("split", x, ta.both(x, lens_q, lens_k, causal), lens_q, lens_k, causal)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_workspace_for_batches_of_any_size(dtype):
+    """A workspace sized for the largest batch, reused for smaller ones, whose
+    walks are split or whose row tiles are of another shape."""
+    from gated_delta_rule_prefill_amd import kda as b
+    need = b.lib().kda_latent_attention_backward_workspace_bytes(3000, 3000, 4, 64)
+    ws = ones(need)
+    import gated_delta_rule_prefill_amd as kda
+    for n in (3000, 1024, 495, 1):
+        x = ta.make(74, dtype, 4, 64, 64, [n], [n])
+        args = dict(k_pe=x["k_pe"], scale=x["scale"])
+        o, lse = kda.latent_attention(x["q"], x["k"], x["v"], **args)
+        got = kda.latent_attention_backward(x["q"], x["k"], x["v"], o, lse, x["d_o"], workspace=ws, **args)
+        want = kda.latent_attention_backward(x["q"], x["k"], x["v"], o, lse, x["d_o"], **args)
+        for name in ("dq", "dk", "dv", "dk_pe"):
+            assert torch.equal(got[name], want[name]), (n, name)
+    ws = ones(b.latent_decode_workspace_bytes(256, 256, 32, 256, 64, dtype == "bf16"))
+    for lens, new in (([300] * 40, [1] * 40), ([900, 70, 5], [20, 1, 1]), ([2000], [1])):
+        x = td.make(75, dtype, 32, 256, 64, 16, lens, new)
+        got, want = td.run(x, 256, workspace=ws), td.run(x, 256)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

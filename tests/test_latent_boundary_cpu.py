@@ -191,3 +191,32 @@ def test_attention_rejects_more_tiles_than_a_grid_has():
         a = _inputs(**kw)
         assert kda.lib().kda_latent_attention(a, A, A, None) == INVALID
         assert "too many tiles" in kda.last_error()
+
+
+def test_workspace_of_a_large_batch_serves_smaller_ones():
+    """The sizes never fall as an argument grows, though small batches are split
+    over more workgroups and long rows take larger tiles."""
+    import itertools
+    lib = kda.lib()
+    rows, heads = [0, 1, 63, 64, 65, 495, 1024, 2040, 2048, 4096, 30000], [1, 3, 4, 32, 128]
+    for dr in (0, 64):
+        size = {(q, k, h): lib.kda_latent_attention_backward_workspace_bytes(q, k, h, dr)
+                for q, k, h in itertools.product(rows, rows, heads)}
+        for (q, k, h), n in size.items():
+            for bigger in ((rows[min(rows.index(q) + 1, 10)], k, h), (q, rows[min(rows.index(k) + 1, 10)], h),
+                           (q, k, heads[min(heads.index(h) + 1, 4)])):
+                assert size[bigger] >= n, (dr, (q, k, h), bigger)
+    for dl, bf16 in itertools.product((256, 512), (True, False)):
+        size = [kda.latent_decode_workspace_bytes(t, n, h, dl, 64, bf16)
+                for t, n, h in ((1, 1, 1), (64, 64, 32), (64, 16, 32), (256, 256, 32), (257, 256, 32), (4096, 16, 128))]
+        assert size == sorted(size) and size[0] > 0
+
+
+def test_backward_bf16_needs_no_room_for_splits():
+    """bf16 calls are never split: they ask for their row statistics and the heads'
+    parts of dk_pe only."""
+    rows = 100 * 4
+    need = -(-rows * 8 // 256) * 256 + -(-rows * 64 * 4 // 256) * 256 + 256
+    assert _backward(wsb=need - 1) == WORKSPACE
+    assert "need %d bytes" % need in kda.last_error()
+    assert _backward(inputs=dict(dtype=kda.KDA_DTYPE_F32), wsb=need) == WORKSPACE
