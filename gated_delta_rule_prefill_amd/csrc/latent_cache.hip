@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppend a
         seq = sequence_of(a.cu_seqlens, a.num_seqs, t, lane);
         if (seq < 0) return;
         const int first = a.cu_seqlens[seq];
-        n = a.cu_seqlens[seq + 1] - first;
+        n = (int)min((int64_t)a.cu_seqlens[seq + 1], a.total_tokens) - first;   // as decode counts them
         i = (int)(t - first);
     } else {
         n = (int)(a.total_tokens / a.num_seqs);

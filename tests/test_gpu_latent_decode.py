@@ -392,3 +392,20 @@ def test_a_layer_step_by_step():
     err = (got.double().cpu() - want).norm() / want.norm()
     print(f"[latent] layer: rel-L2 {float(err):.2e}", flush=True)
     assert err <= 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_offsets_outside_the_tokens(dtype):
+    """Offsets before 0 and behind T are clamped: the same rows as with offsets
+    of 0 and T, which decode reads."""
+    import gated_delta_rule_prefill_amd as kda
+    c = torch.randn(6, 320, device="cuda").to(DT[dtype])
+    for cu in ([0, 2, 6], [-3, 2, 11]):
+        x = make(53, dtype, 8, 256, 64, 16, [20, 33], [2, 4], poison=False)
+        offs = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        kda.latent_append(x["cache"], c[:, :256], x["table"], x["seq_lens"], k_pe=c[:, 256:], cu_seqlens=offs)
+        rows = x["cache"].view(-1, 320)
+        for t, (s, j) in enumerate([(0, 18), (0, 19), (1, 29), (1, 30), (1, 31), (1, 32)]):
+            assert torch.equal(rows[int(x["table"][s, j // 16]) * 16 + j % 16], c[t]), (cu, t)
+        for a, b in zip(run(x, 256), run(x, 256, cu_seqlens=offs)):
+            assert torch.equal(a, b)
