@@ -87,7 +87,8 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += to_f32(gv[i]) * to_f32(ov[i]);
         }
-        dl[j] = group_sum(sum);
+        // a row that sees no key has o = 0, and 0 times a d_o of NaN or Inf is NaN
+        dl[j] = (in.causal ? min(nk - 1, r + off) : nk - 1) < 0 ? 0.f : group_sum(sum);
         lse2[j] = lse[at] * LOG2E;
         exact[j] = 0.f;
     }

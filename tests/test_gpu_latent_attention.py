@@ -318,3 +318,23 @@ def test_padded_rows_of_garbage():
         part = slice(128 * i, 128 * i + m)
         ref.check(f"padded row {i} o", o[part], want["o"][0][part], want["o"][1][part])
         ref.check(f"padded row {i} lse", lse[part], want["lse"][0][part], want["lse"][1][part])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens_q,lens_k", [([70, 40], [20, 33]), ([150, 9], [140, 0])])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_rows_without_keys_and_gradients_that_are_not_finite(dtype, lens_q, lens_k, value):
+    """Rows that see no key have zero gradients whatever d_o holds there, in the
+    same wave as rows that see keys or not, and leave the keys' gradients clean."""
+    x = make(29, dtype, 2, 128, 64, lens_q, lens_k)
+    clean = dict(x, d_o=x["d_o"].clone())
+    at, empty = 0, []
+    for n, m in zip(lens_q, lens_k):
+        empty += range(at, at + n - m)
+        at += n
+    x["d_o"][empty, :, 5] = float(value)
+    x["d_o"][empty[::2]] = float(value)
+    clean["d_o"][empty] = 0.0
+    got = both(x, lens_q, lens_k, True)
+    check_all(f"no keys, d_o {value} {dtype}", clean, got, lens_q, lens_k, True)
+    assert (got["dq"][empty] == 0).all()
