@@ -588,10 +588,12 @@ static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipS
     if (tq > 0)
         hipLaunchKernelGGL((latent_dq_kernel<E, DN, DR>), dim3((unsigned)(tq * in.H), sq), dim3(256), 0, stream, in,
                            (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, a.part_q, (int)tq);
+    if (const hipError_t e = hipGetLastError()) return e;
     if (tk > 0)
         hipLaunchKernelGGL((latent_dkv_kernel<E, DN, DR>), dim3((unsigned)(tk * in.H), sk), dim3(256), 0, stream, in,
                            (const E*)a.d_o, a.row_stats, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv,
                            a.dv_token_stride, a.dv_head_stride, a.pe_part, a.part_k, (int)tk);
+    if (const hipError_t e = hipGetLastError()) return e;
     if constexpr (SPLIT<E>)
         if (sk > 1 || sq > 1) {
             const int64_t items = (sk > 1 ? in.total_k * (in.H * (2 * DN) / 4 + DR / 4) : 0) +

@@ -606,6 +606,8 @@ static hipError_t launch(const LatentDecode& a, hipStream_t stream) {
     const int entries = by_tile ? (int)bound : DEC_RUNS;
     hipLaunchKernelGGL((latent_decode_kernel<E, DL, DR, S>), dim3(DEC_RUNS), dim3(64 * DEC_WAVES), 0, stream, a, ws,
                        by_tile ? 1 : 0, entries);
+    // the join goes where the decode kernel's entries point
+    if (const hipError_t e = hipGetLastError()) return e;
     if (entries <= 32)   // 8 parts a row tile and more
         hipLaunchKernelGGL((latent_join_parts_kernel<E, DL>), dim3(entries, S::BM, DL / 64), dim3(256), 0, stream, ws,
                            (E*)a.o, a.lse, S::BM);

@@ -1,0 +1,32 @@
+"""The latent operators' host side over a stand-in for HIP (hip_stub.py): what
+is launched, and what happens when a launch is refused."""
+import pytest
+
+import hip_stub
+from gated_delta_rule_prefill_amd import kda
+
+CALLS = {   # call -> its launches
+    "decode": ("decode", 2), "decode many rows": ("decode, T=200, H=32", 2), "decode fp32": ("decode, bf16=False", 2),
+    "decode without a workspace": ("decode, ws=None", 2), "append": ("append", 1), "rotary": ("rotary", 1),
+    "forward": ("forward", 1), "backward": ("backward", 3), "backward without key parts": ("backward, dr=0", 2),
+    "backward in fp32, split": ("backward, bf16=False", 3), "backward in fp32, whole": ("backward, bf16=False, T=9000", 3),
+}
+
+
+@pytest.fixture(scope="module")
+def calls(tmp_path_factory):
+    code = "".join(f"result[{name!r}] = [call({f.split(',')[0]}, r{','.join([''] + f.split(',')[1:])}) "
+                   f"for r in range({n + 1})]\n" for name, (f, n) in CALLS.items())
+    return hip_stub.run(tmp_path_factory.mktemp("stub"), code)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_refused_launch_ends_the_call(calls, name):
+    """Nothing is launched behind a refused launch: the next kernel would read
+    what the refused one did not write (a join follows row numbers that the
+    decode kernel leaves in the workspace)."""
+    plain, *refused = calls[name]
+    n = CALLS[name][1]
+    assert plain == dict(status=kda.KDA_OK, launches=n, syncs=0, text="")
+    for at, got in enumerate(refused, 1):
+        assert (got["status"], got["launches"]) == (kda.KDA_ERR_HIP, at) and "refused" in got["text"]
