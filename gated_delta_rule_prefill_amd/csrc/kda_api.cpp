@@ -188,36 +188,8 @@ struct Timer {
     }
 };
 
-bool debug_sync() {
-    static const bool on = [] {
-        const char* e = std::getenv("KDA_DEBUG_SYNC");
-        return e && e[0] && e[0] != '0';
-    }();
-    return on;
-}
-
-// KDA_DEBUG_SYNC: copy the device offsets to the host and check what the
-// kernels take as a precondition (0 = c_0 <= c_1 <= ... <= c_N = T).
-kda_status debug_check_cu_seqlens(const int32_t* cu, int32_t N, int64_t T, hipStream_t stream) {
-    if (!cu || !debug_sync()) return KDA_OK;
-    std::vector<int32_t> h((size_t)N + 1);
-    hipError_t e = hipMemcpyAsync(h.data(), cu, ((size_t)N + 1) * sizeof(int32_t),
-                                  hipMemcpyDeviceToHost, stream);
-    if (e == hipSuccess) e = hipStreamSynchronize(stream);
-    if (e != hipSuccess)
-        return fail(KDA_ERR_HIP, std::string("KDA_DEBUG_SYNC copy of cu_seqlens: ") + hipGetErrorString(e));
-    if (h[0] != 0) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[0] must be 0");
-    for (int32_t i = 0; i < N; ++i)
-        if (h[i + 1] < h[i])
-            return fail(KDA_ERR_INVALID_ARGUMENT,
-                        "cu_seqlens must be non-decreasing (entry " + std::to_string(i + 1) + ")");
-    if ((int64_t)h[N] != T)
-        return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[N] must equal total_tokens");
-    return KDA_OK;
-}
-
 kda_status check_launch(hipError_t e, const char* what, hipStream_t stream) {
-    if (e == hipSuccess && debug_sync()) e = hipStreamSynchronize(stream);
+    if (e == hipSuccess && kda::debug_sync()) e = hipStreamSynchronize(stream);
     if (e != hipSuccess)
         return fail(KDA_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
     return KDA_OK;
@@ -264,6 +236,32 @@ namespace kda {
 
 void set_last_error(const std::string& msg) { g_last_error = msg; }
 
+bool debug_sync() {
+    static const bool on = [] {
+        const char* e = std::getenv("KDA_DEBUG_SYNC");
+        return e && e[0] && e[0] != '0';
+    }();
+    return on;
+}
+
+kda_status debug_check_offsets(const int32_t* cu, int32_t N, int64_t T, bool whole, hipStream_t stream) {
+    if (!cu || !debug_sync()) return KDA_OK;
+    std::vector<int32_t> h((size_t)N + 1);
+    hipError_t e = hipMemcpyAsync(h.data(), cu, ((size_t)N + 1) * sizeof(int32_t),
+                                  hipMemcpyDeviceToHost, stream);
+    if (e == hipSuccess) e = hipStreamSynchronize(stream);
+    if (e != hipSuccess)
+        return fail(KDA_ERR_HIP, std::string("KDA_DEBUG_SYNC copy of cu_seqlens: ") + hipGetErrorString(e));
+    if (whole && h[0] != 0) return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[0] must be 0");
+    for (int32_t i = 0; i < N; ++i)
+        if (h[i + 1] < h[i])
+            return fail(KDA_ERR_INVALID_ARGUMENT,
+                        "cu_seqlens must be non-decreasing (entry " + std::to_string(i + 1) + ")");
+    if (whole && (int64_t)h[N] != T)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[N] must equal total_tokens");
+    return KDA_OK;
+}
+
 kda_status prefill_impl(const void* q, const void* k, const void* v, const float* log_alpha,
                         const float* beta, const float* initial_state, const int32_t* cu_seqlens,
                         int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t dk, int32_t dv,
@@ -307,7 +305,7 @@ kda_status prefill_impl(const void* q, const void* k, const void* v, const float
             return fail(KDA_ERR_INVALID_ARGUMENT, "num_seqs * H too large");
 
         hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
-        if (kda_status dc = debug_check_cu_seqlens(cu_seqlens, num_seqs, total_tokens, stream))
+        if (kda_status dc = kda::debug_check_offsets(cu_seqlens, num_seqs, total_tokens, true, stream))
             return dc;
         const bool bf16 = dtype == KDA_DTYPE_BF16;
         unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -448,7 +446,7 @@ kda_status kda_backward(const void* q, const void* k, const void* v, const float
                                                " bytes");
 
         hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
-        if (kda_status dc = debug_check_cu_seqlens(cu_seqlens, num_seqs, total_tokens, stream))
+        if (kda_status dc = kda::debug_check_offsets(cu_seqlens, num_seqs, total_tokens, true, stream))
             return dc;
         const bool bf16 = dtype == KDA_DTYPE_BF16;
         unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -555,7 +553,7 @@ kda_status kda_decode_tokens(float* state_pool, int32_t num_slots, const int32_t
             if (p && !aligned16(p))
                 return fail(KDA_ERR_INVALID_ARGUMENT, "every pointer must be 16-byte aligned");
         hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
-        if (kda_status dc = debug_check_cu_seqlens(cu_seqlens, num_seqs, total_tokens, stream))
+        if (kda_status dc = kda::debug_check_offsets(cu_seqlens, num_seqs, total_tokens, true, stream))
             return dc;
         const int rows = cu_seqlens ? -1 : (int)(total_tokens / num_seqs);
         // Exactly one token per sequence (equal rows of one, no options): the

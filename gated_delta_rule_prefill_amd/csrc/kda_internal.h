@@ -2,6 +2,7 @@
 // files (not part of the public interface).
 #pragma once
 
+#include <hip/hip_runtime_api.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -13,6 +14,15 @@ namespace kda {
 
 // Sets the calling thread's kda_last_error_message() text.
 void set_last_error(const std::string& msg);
+
+// Whether KDA_DEBUG_SYNC is set in the environment (read once).
+bool debug_sync();
+
+// KDA_DEBUG_SYNC: copies the device offsets cu[N + 1] to the host and checks what
+// the kernels take as a precondition: c_0 <= c_1 <= ... <= c_N, and where the
+// sequences are all of the tokens (whole) also c_0 = 0 and c_N = T.  Without
+// offsets or the variable: KDA_OK.
+kda_status debug_check_offsets(const int32_t* cu, int32_t N, int64_t T, bool whole, hipStream_t stream);
 
 // kda_prefill_ex with one more switch: with may_allocate false a NULL
 // workspace is an error (KDA_ERR_WORKSPACE) instead of a stream-ordered

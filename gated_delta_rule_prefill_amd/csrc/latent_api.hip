@@ -76,6 +76,12 @@ kda_status check_inputs(const kda_latent_inputs* in) {
     return KDA_OK;
 }
 
+// KDA_DEBUG_SYNC: both sets of offsets.  Sequences need not be all of the rows.
+kda_status check_offsets(const kda_latent_inputs* in, hipStream_t stream) {
+    if (kda_status st = kda::debug_check_offsets(in->cu_seqlens_q, in->num_seqs, in->total_q, false, stream)) return st;
+    return kda::debug_check_offsets(in->cu_seqlens_k, in->num_seqs, in->total_k, false, stream);
+}
+
 // The paged cache's arguments, shared by decode and append.
 kda_status check_pages(const void* cache, int32_t num_pages, int32_t page_size, const int32_t* block_table,
                        int32_t max_pages, const int32_t* seq_lens, const int32_t* cu_seqlens, int64_t total_tokens,
@@ -111,6 +117,15 @@ struct BackwardSpace {
 
 }  // namespace
 
+namespace kda {
+
+hipError_t launch_result(hipStream_t stream) {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess && debug_sync() ? hipStreamSynchronize(stream) : e;
+}
+
+}  // namespace kda
+
 extern "C" {
 
 kda_status kda_latent_attention(const kda_latent_inputs* in, void* o, float* lse, void* stream) {
@@ -119,8 +134,9 @@ kda_status kda_latent_attention(const kda_latent_inputs* in, void* o, float* lse
         if (in->total_q == 0) return KDA_OK;
         if (!o) return fail(KDA_ERR_INVALID_ARGUMENT, "o must be non-NULL");
         if (!aligned16(o) || !aligned16(lse)) return fail(KDA_ERR_INVALID_ARGUMENT, "every pointer must be 16-byte aligned");
-        return launched(kda::launch_latent_attention(*in, o, lse, reinterpret_cast<hipStream_t>(stream)),
-                        "latent attention kernel");
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        if (kda_status st = check_offsets(in, s)) return st;
+        return launched(kda::launch_latent_attention(*in, o, lse, s), "latent attention kernel");
     } catch (...) {
         return fail(KDA_ERR_HIP, "unexpected C++ exception inside kda_latent_attention");
     }
@@ -165,6 +181,7 @@ kda_status kda_latent_attention_backward(const kda_latent_inputs* in, const void
         }
         if (in->total_q == 0 && in->total_k == 0) return KDA_OK;
         hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
+        if (kda_status st = check_offsets(in, stream)) return st;
         unsigned char* ws = static_cast<unsigned char*>(workspace);
         if (!ws)
             if (kda_status st = launched(hipMallocAsync(reinterpret_cast<void**>(&ws), need, stream), "hipMallocAsync"))
@@ -220,6 +237,7 @@ kda_status kda_latent_decode(const void* q, int64_t q_token_stride, int64_t q_he
         }
         if (total_tokens == 0) return KDA_OK;
         hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
+        if (kda_status st = kda::debug_check_offsets(cu_seqlens, num_seqs, total_tokens, false, stream)) return st;
         void* ws = workspace;
         if (!ws)
             if (kda_status st = launched(hipMallocAsync(&ws, need, stream), "hipMallocAsync")) return st;
@@ -264,11 +282,12 @@ kda_status kda_latent_append(void* cache, int32_t num_pages, int32_t page_size, 
         if (!stride_ok(c_token_stride, dtype) || !stride_ok(k_pe_token_stride, dtype))
             return fail(KDA_ERR_INVALID_ARGUMENT, "strides must be >= 0 and multiples of 16 bytes");
         if (total_tokens == 0) return KDA_OK;
+        hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+        if (kda_status st = kda::debug_check_offsets(cu_seqlens, num_seqs, total_tokens, false, s)) return st;
         const kda::LatentAppend a{cache, num_pages, page_size, block_table, max_pages, seq_lens, cu_seqlens,
                                   total_tokens, num_seqs, dl, dr, c, c_token_stride, k_pe, k_pe_token_stride,
                                   norm_weight, eps, inv_freq, amplitude, flags, c_out, k_pe_out};
-        return launched(kda::launch_latent_append(a, dtype == KDA_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)),
-                        "latent append kernel");
+        return launched(kda::launch_latent_append(a, dtype == KDA_DTYPE_BF16, s), "latent append kernel");
     } catch (...) {
         return fail(KDA_ERR_HIP, "unexpected C++ exception inside kda_latent_append");
     }

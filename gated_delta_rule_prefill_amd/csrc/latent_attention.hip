@@ -246,7 +246,7 @@ static hipError_t launch(const kda_latent_inputs& in, void* o, float* lse, hipSt
                                           : (in.total_q / in.num_seqs + BQ - 1) / BQ * in.num_seqs;
     hipLaunchKernelGGL((latent_attention_kernel<E, DN, DR>), dim3((unsigned)(tiles * in.H)), dim3(256), 0, stream,
                        in, (E*)o, lse, (int)tiles);
-    return hipGetLastError();
+    return launch_result(stream);
 }
 
 hipError_t launch_latent_attention(const kda_latent_inputs& in, void* o, float* lse, hipStream_t stream) {

@@ -588,23 +588,26 @@ static hipError_t launch(const kda_latent_inputs& in, const LatentGrads& a, hipS
     if (tq > 0)
         hipLaunchKernelGGL((latent_dq_kernel<E, DN, DR>), dim3((unsigned)(tq * in.H), sq), dim3(256), 0, stream, in,
                            (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, a.part_q, (int)tq);
-    if (const hipError_t e = hipGetLastError()) return e;
+    if (const hipError_t e = launch_result(stream)) return e;
     if (tk > 0)
         hipLaunchKernelGGL((latent_dkv_kernel<E, DN, DR>), dim3((unsigned)(tk * in.H), sk), dim3(256), 0, stream, in,
                            (const E*)a.d_o, a.row_stats, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv,
                            a.dv_token_stride, a.dv_head_stride, a.pe_part, a.part_k, (int)tk);
-    if (const hipError_t e = hipGetLastError()) return e;
+    if (const hipError_t e = launch_result(stream)) return e;
     if constexpr (SPLIT<E>)
         if (sk > 1 || sq > 1) {
             const int64_t items = (sk > 1 ? in.total_k * (in.H * (2 * DN) / 4 + DR / 4) : 0) +
                                   (sq > 1 ? in.total_q * in.H * (DN + DR) / 4 : 0);
             hipLaunchKernelGGL((latent_sum_kernel<E, DN, DR>), grid_of((items + 255) / 256), dim3(256), 0, stream, in, a, sk, sq);
+            if (const hipError_t e = launch_result(stream)) return e;
         }
     if constexpr (DR > 0)
-        if (in.total_k > 0 && sk == 1)
+        if (in.total_k > 0 && sk == 1) {
             hipLaunchKernelGGL((latent_dkpe_kernel<E, DR>), grid_of((in.total_k * (DR / 4) + 255) / 256), dim3(256), 0,
                                stream, a.pe_part, (E*)a.dk_pe, cu_k, in.num_seqs, (int)in.total_k, in.H);
-    return hipGetLastError();
+            return launch_result(stream);
+        }
+    return hipSuccess;
 }
 
 hipError_t launch_latent_attention_backward(const kda_latent_inputs& in, const LatentGrads& a, hipStream_t stream) {

@@ -132,7 +132,7 @@ static hipError_t launch_rotary_t(const Rotary& a, hipStream_t stream) {
     if (wide && far) inter ? go(rotary_kernel<E, CE, true, true>) : go(rotary_kernel<E, CE, false, true>);
     else if (wide) inter ? go(rotary_kernel<E, CE, true, false>) : go(rotary_kernel<E, CE, false, false>);
     else inter ? go(rotary_kernel<E, 1, true, false>) : go(rotary_kernel<E, 1, false, false>);
-    return hipGetLastError();
+    return launch_result(stream);
 }
 
 hipError_t launch_rotary(const Rotary& a, bool bf16_io, hipStream_t stream) {
@@ -248,7 +248,7 @@ hipError_t launch_latent_append(const LatentAppend& a, bool bf16_io, hipStream_t
     const dim3 grid = grid_of((a.total_tokens + 3) / 4);
     if (bf16_io) hipLaunchKernelGGL(latent_append_kernel<bf16>, grid, dim3(256), 0, stream, a);
     else hipLaunchKernelGGL(latent_append_kernel<float>, grid, dim3(256), 0, stream, a);
-    return hipGetLastError();
+    return launch_result(stream);
 }
 
 }  // namespace kda

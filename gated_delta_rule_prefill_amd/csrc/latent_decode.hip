@@ -607,14 +607,14 @@ static hipError_t launch(const LatentDecode& a, hipStream_t stream) {
     hipLaunchKernelGGL((latent_decode_kernel<E, DL, DR, S>), dim3(DEC_RUNS), dim3(64 * DEC_WAVES), 0, stream, a, ws,
                        by_tile ? 1 : 0, entries);
     // the join goes where the decode kernel's entries point
-    if (const hipError_t e = hipGetLastError()) return e;
+    if (const hipError_t e = launch_result(stream)) return e;
     if (entries <= 32)   // 8 parts a row tile and more
         hipLaunchKernelGGL((latent_join_parts_kernel<E, DL>), dim3(entries, S::BM, DL / 64), dim3(256), 0, stream, ws,
                            (E*)a.o, a.lse, S::BM);
     else
         hipLaunchKernelGGL((latent_join_rows_kernel<E, DL>), dim3(entries, S::BM / 4), dim3(256), 0, stream, ws,
                            (E*)a.o, a.lse, S::BM);
-    return hipGetLastError();
+    return launch_result(stream);
 }
 
 template <typename E, int DL, int DR>

@@ -9,6 +9,10 @@
 
 namespace kda {
 
+// To be called behind every kernel's launch: its error, or under KDA_DEBUG_SYNC
+// that of its execution.
+hipError_t launch_result(hipStream_t stream);
+
 hipError_t launch_latent_attention(const kda_latent_inputs& in, void* o, float* lse,
                                    hipStream_t stream);
 

@@ -282,7 +282,8 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  *              is dense, and strides and pointers are multiples of 16 bytes.
  *   Offsets    cu_seqlens may end before the last row (c_N <= T): the rows
  *              behind the last sequence are neither read nor written.  Offsets
- *              outside [0, T] are clamped to it.
+ *              outside [0, T] are clamped to it.  They must not decrease
+ *              (all that KDA_DEBUG_SYNC=1 checks of them).
  *   Empty rows a query row that sees no key gets o = 0, lse = -inf and zero
  *              gradients.
  *   Values     NaN and Inf propagate from the keys a row sees to its result, and

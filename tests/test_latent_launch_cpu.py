@@ -30,3 +30,26 @@ def test_a_refused_launch_ends_the_call(calls, name):
     assert plain == dict(status=kda.KDA_OK, launches=n, syncs=0, text="")
     for at, got in enumerate(refused, 1):
         assert (got["status"], got["launches"]) == (kda.KDA_ERR_HIP, at) and "refused" in got["text"]
+
+
+def test_debug_sync(tmp_path):
+    """With KDA_DEBUG_SYNC=1 the latent operators wait for the stream behind every
+    kernel, and refuse offsets that decrease before they launch any."""
+    code = "".join(f"result[{name!r}] = call({f.split(',')[0]}{','.join([''] + f.split(',')[1:])})\n"
+                   for name, (f, n) in CALLS.items())
+    code += """
+down, rising = offsets(0, 200, 150), offsets(5, 200, 290)
+for name, f, kw in (("q", forward, "cu_q"), ("k", forward, "cu_k"), ("dq", backward, "cu_q"), ("dk", backward, "cu_k"),
+                    ("decode", decode, "cu"), ("append", append, "cu")):
+    result["offsets " + name] = [call(f, **dict({"cu_q": rising} if kw == "cu_k" else {}, **{kw: cu}))
+                                 for cu in (down, rising)]
+"""
+    got = hip_stub.run(tmp_path, code, KDA_DEBUG_SYNC="1")
+    for name, (_, n) in CALLS.items():
+        assert got[name] == dict(status=kda.KDA_OK, launches=n, syncs=n, text=""), name
+    for name in ("q", "k", "dq", "dk", "decode", "append"):
+        down, rising = got["offsets " + name]
+        assert down["status"] == kda.KDA_ERR_INVALID_ARGUMENT and "non-decreasing" in down["text"], name
+        assert down["launches"] == 0
+        copies = 2 if name in ("k", "dk") else 1
+        assert rising["status"] == kda.KDA_OK and rising["syncs"] == rising["launches"] + copies, name
