@@ -386,6 +386,8 @@ def _elsewhere(device, stream):
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {device}")
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream: it belongs to {stream.device}, the tensors are on {device}")
         return torch.cuda.stream(stream)
     if device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)

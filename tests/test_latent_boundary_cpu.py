@@ -220,3 +220,13 @@ def test_backward_bf16_needs_no_room_for_splits():
     assert _backward(wsb=need - 1) == WORKSPACE
     assert "need %d bytes" % need in kda.last_error()
     assert _backward(inputs=dict(dtype=kda.KDA_DTYPE_F32), wsb=need) == WORKSPACE
+
+
+def test_stream_of_another_device_is_refused():
+    """Such a stream was dropped: the call ran on its tensors' device's current one."""
+    from types import SimpleNamespace
+
+    import torch
+    there = SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream"):
+        kda._elsewhere(torch.device("cuda", 0), there)
