@@ -463,7 +463,7 @@ def _latent_inputs(q, k, v, k_pe, cu_seqlens, cu_seqlens_k, num_seqs, causal, sc
     else:
         if cu_seqlens_k is not None:
             raise ValueError("cu_seqlens_k needs cu_seqlens")
-        N = int(num_seqs or 1)
+        N = 1 if num_seqs is None else int(num_seqs)
     if scale is None:
         scale = dqk ** -0.5
     packed = _INPUTS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), pe, _stride(q, 0), _stride(q, 1),

@@ -230,3 +230,14 @@ def test_stream_of_another_device_is_refused():
     there = SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream"):
         kda._elsewhere(torch.device("cuda", 0), there)
+
+
+def test_no_sequences_are_refused():
+    """num_seqs=0 is passed on, for the library to refuse, and not taken for 1."""
+    import torch
+    q, k = torch.zeros(4, 2, 64), torch.zeros(4, 2, 64)
+    for num_seqs, n in ((None, 1), (2, 2), (0, 0), (-1, -1)):
+        packed, _ = kda._latent_inputs(q, k, k, None, None, None, num_seqs, True, None)
+        assert kda._INPUTS.unpack(packed)[15] == n
+        if n < 1:
+            assert kda.lib().kda_latent_attention(packed, A, A, None) == INVALID and "num_seqs" in kda.last_error()
