@@ -219,6 +219,8 @@ kda_status kda_latent_decode(const void* q, int64_t q_token_stride, int64_t q_he
                                         total_tokens, num_seqs))
             return st;
         if (H <= 0 || H > 65535) return fail(KDA_ERR_INVALID_ARGUMENT, "H must be in [1, 65535]");
+        if (total_tokens * H > kMaxRows)   // a sequence's row tiles are counted in 32 bits
+            return fail(KDA_ERR_INVALID_ARGUMENT, "total_tokens * H must be <= 2^31 - 4096");
         if ((dl != 256 && dl != 512) || (dr != 0 && dr != 64))
             return fail(KDA_ERR_UNSUPPORTED, "dl must be 256 or 512, dr 0 or 64");
         if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KDA_ERR_INVALID_ARGUMENT, "scale must be finite and > 0");

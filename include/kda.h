@@ -401,7 +401,7 @@ size_t kda_latent_decode_workspace_bytes(int64_t total_tokens, int32_t num_seqs,
  *   workspace    at least kda_latent_decode_workspace_bytes(), or NULL with 0
  *                (then allocated stream-ordered on `stream`).  Two calls that
  *                may overlap need one each.
- * dl in {256, 512}; dr in {0, 64}; H * (T / N) < 2^31.  The result is
+ * dl in {256, 512}; dr in {0, 64}; H * T <= 2^31 - 4096.  The result is
  * deterministic: how the keys are split depends on the sizes and lengths only.
  */
 kda_status kda_latent_decode(const void *q, int64_t q_token_stride, int64_t q_head_stride,

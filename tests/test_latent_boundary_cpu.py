@@ -241,3 +241,11 @@ def test_no_sequences_are_refused():
         assert kda._INPUTS.unpack(packed)[15] == n
         if n < 1:
             assert kda.lib().kda_latent_attention(packed, A, A, None) == INVALID and "num_seqs" in kda.last_error()
+
+
+def test_decode_rejects_more_rows_than_it_counts():
+    for kw in (dict(T=1 << 26, N=1, H=32), dict(T=1 << 20, N=1 << 20, H=4096), dict(T=32769, N=32769, H=65535)):
+        assert _decode(**kw) == INVALID
+        assert "total_tokens * H" in kda.last_error()
+    # the largest that is counted goes on to the next check
+    assert _decode(T=(1 << 31) - 4096, N=1, H=1, q=None) == INVALID and "q and o" in kda.last_error()
