@@ -248,10 +248,12 @@ struct Stage {
         load_rows<0>(tid, base, stride, base, stride, left);
     }
     // Whether row tid / TPR + PASS p of the loaded tile has a value that is not
-    // finite: the same answer in the row's TPR threads.
+    // finite, the last W1 channels aside: the same answer in the row's TPR threads.
+    template <int W1 = 0>
     __device__ __forceinline__ bool bad_row(int tid, int p, bool bad = false) const {
+        static_assert(W1 % (TPR * CE) == 0, "whole steps");
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int s = 0; s < (W - W1) / CE / TPR; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const unsigned x = r[p][s][i];

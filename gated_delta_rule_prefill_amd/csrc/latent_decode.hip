@@ -250,16 +250,17 @@ __global__ __launch_bounds__(64 * DEC_WAVES, 2) void latent_decode_kernel(const 
         if (tid < 4) grown[tid] = 0;
         __syncthreads();
         int next_row = -1;
-        // Rows with values that are not finite, in tiles that hold keys some query
+        // Rows with latents that are not finite, in tiles that hold keys some query
         // rows do not see: cleared, and marked -2 for those that do (their weight
-        // becomes NaN; a weight of 0 would make 0 * NaN of a hidden key).
+        // becomes NaN; a weight of 0 would make 0 * NaN of a hidden key).  The key
+        // part is in no product with weights: it gives the scores that it gives.
         const int first_last = len - n + (int)(row0 / a.H);          // last key that the tile's first row sees
         auto hides = [&](int k) { return (tile_of(k) + 1) * BN - 1 > first_last; };
         auto mark_bad_rows = [&](Stage<E, W, BN, NT>& rows, int k) {
             typedef Stage<E, W, BN, NT> S;
 #pragma unroll
             for (int p = 0; p < S::P; ++p)
-                if (rows.bad_row(tid, p)) {
+                if (rows.template bad_row<DR>(tid, p)) {
                     rows.fill_row(p, 0u);
                     if (tid % S::TPR == 0) ridx[k & 3][tid / S::TPR + S::PASS * p] = -2;
                 }

@@ -409,3 +409,16 @@ def test_append_offsets_outside_the_tokens(dtype):
             assert torch.equal(rows[int(x["table"][s, j // 16]) * 16 + j % 16], c[t]), (cu, t)
         for a, b in zip(run(x, 256), run(x, 256, cu_seqlens=offs)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [1, 32])
+def test_key_parts_of_minus_infinity(dtype, H):
+    """A key part that makes a score -inf takes its key out, as by the formula,
+    in tiles that all rows see and in those that some do not: k_pe is no value."""
+    lens, new = [150, 90], [30, 5]
+    x = make(45, dtype, H, 256, 64, 16, lens, new, poison=False)
+    x["q"][..., 300] = x["q"][..., 300].abs() + 0.5
+    for s, j in ((0, 3), (0, 70), (0, 125), (0, 149), (1, 88)):
+        x["cache"][int(x["table"][s, j // 16]), j % 16, 300] = -math.inf
+    check(f"key parts of -inf {dtype} H={H}", x, 256, lens, new)
