@@ -87,8 +87,7 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += to_f32(gv[i]) * to_f32(ov[i]);
         }
-        // a row that sees no key has o = 0, and 0 times a d_o of NaN or Inf is NaN
-        dl[j] = (in.causal ? min(nk - 1, r + off) : nk - 1) < 0 ? 0.f : group_sum(sum);
+        dl[j] = group_sum(sum);
         lse2[j] = lse[at] * LOG2E;
         exact[j] = 0.f;
     }
@@ -147,6 +146,13 @@ __global__ __launch_bounds__(256, 2) void latent_dq_kernel(
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
         for (int ks = 0; ks < QR; ++ks) arrived(q[j][ks]);
+    // A row that sees no key has o = 0, and 0 times a d_o of NaN or Inf is NaN.
+    // (Where delta is summed the test costs two spilled registers, 2 % of the
+    // packed training step.)
+    if (wave_full <= 0)
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+            if (lse2[j] == neg_inf()) dl[j] = 0.f;
     // Tile t of the keys; hides: some row does not see all of the keys of it or
     // of the next one.
     auto step = [&](int t, auto hides, const E* K, E* next) {
