@@ -13,6 +13,65 @@
 
 namespace kda {
 
+// The values that the kernel below took out of tile 0 and of those that some row
+// of the workgroup does not see whole, found again.  With a weight above 0 such a
+// value makes its channel Inf or NaN whatever the others add, so it may follow
+// the output's rounding.  m: the final maxima of this lane's rows.
+template <typename E, int DN, int DR>
+__device__ __forceinline__ void put_taken(E* o, int h, int seq, int tile, const float (&m)[LATENT_NQ<E>])
+{
+    constexpr int KS = (DN + DR) / 32, DV = DN, BN = 128 / (int)sizeof(E), NQ = LATENT_NQ<E>, BQ = 64 * NQ;
+    // The inputs are read from the kernel's first argument again, and nothing of this
+    // is worked out ahead of the walk, whose registers are short.
+    int tid = threadIdx.x;
+    auto args = (const __attribute__((address_space(4))) kda_latent_inputs*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+v"(tid), "+s"(args));
+    const auto& in = *args;
+    const int lane = tid & 63, col = lane & 15, g = lane >> 4;
+    int q0, q1, k0, k1;
+    sequence_rows(in.cu_seqlens_q, (int)(in.total_q / in.num_seqs), (int)in.total_q, seq, q0, q1);
+    sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
+                  (int)in.total_k, seq, k0, k1);
+    const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
+    const int full = in.causal ? min(nk, tile * BQ + off + 1) : nk;                   // as in the kernel
+    const int end = in.causal ? min(nk, min(nq, (tile + 1) * BQ) + off) : nk;
+    auto finite = [](float x) { return __builtin_fabsf(x) < __builtin_inff(); };
+#pragma unroll 1
+    for (int key = 0; key < end; key = key == BN - 1 ? max(BN, full / BN * BN) : key + 1) {
+        const E* v = (const E*)in.v + (int64_t)(k0 + key) * in.v_token_stride + h * in.v_head_stride;
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < DV; c += 64) bad |= !finite(to_f32(v[c + lane]));
+        if (!__any(bad)) continue;
+        const E* k = (const E*)in.k + (int64_t)(k0 + key) * in.k_token_stride + h * in.k_head_stride;
+        const E* pe = DR ? (const E*)in.k_pe + (int64_t)(k0 + key) * in.k_pe_token_stride : nullptr;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            const int r = tile * BQ + 16 * (NQ * (tid >> 6) + j) + col;
+            const int64_t at = q0 + min(r, nq - 1);
+            const E* q = (const E*)in.q + at * in.q_token_stride + h * in.q_head_stride;
+            float z = 0.f;
+#pragma unroll 1
+            for (int ks = 0; ks < KS; ++ks) {
+                const auto a = row_frag_global(q, ks, lane);
+                const auto b = 32 * ks < DN ? row_frag_global(k, ks, lane) : row_frag_global(pe, ks - DN / 32, lane);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z += to_f32(a[i]) * to_f32(b[i]);
+            }
+            z = group_sum(z) * in.scale * LOG2E;
+            if (r >= nq || key > (in.causal ? min(nk - 1, r + off) : nk - 1)) continue;
+            const float w = exp2_fast(z - (m[j] == neg_inf() ? 0.f : m[j]));
+            E* row = o + (at * in.H + h) * DV;
+#pragma unroll 1
+            for (int i = 0; i < DV / 4; ++i) {   // the channels that this lane has written
+                const int c = 16 * (i / 4) + 4 * g + i % 4;
+                const float x = to_f32(v[c]);
+                if (!finite(x)) row[c] = from_f32<E>(to_f32(row[c]) + w * x);
+            }
+        }
+    }
+}
+
 // A workgroup: 4 waves of 32 (bf16) or 16 (fp32) query rows, whose operands q
 // and o stay in registers, one head.  Key and value tiles of BN rows are
 // double-buffered in LDS (80 KB, two workgroups a CU): the next tile's global
@@ -70,8 +129,10 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     Stage<E, DQK, BN, 256> sk;
     Stage<E, DV, BN, 256> sv;
     // Tiles that all rows see whole go straight to LDS (2.48 -> 2.38 ms for 16,384
-    // tokens); the others through registers, where rows that are not finite are
-    // found and taken out.
+    // tokens); the others through registers, where values that are not finite are
+    // taken out: a hidden key's weight is 0, and 0 times NaN or Inf is NaN.  What
+    // they give the rows that see them follows the outputs (put_taken).
+    unsigned long long taken = 0;
     Direct<E, DQK, BN, 256, DR> direct_k;
     Direct<E, DV, BN, 256> direct_v;
     auto load = [&](int t, auto hides, E* to) {
@@ -89,7 +150,12 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     };
     auto store = [&](auto hides, E* to) {
         if constexpr (hides) {
-            move_bad_rows(tid, sv, sk);
+#pragma unroll
+            for (int p = 0; p < decltype(sv)::P; ++p) {
+                const bool bad = sv.bad_row(tid, p);
+                if (bad) sv.clear_bad(p);
+                taken |= __ballot(bad);
+            }
             sk.store(tid, to);
             sv.store(tid, to + BN * DQK);
         } else {
@@ -237,6 +303,10 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
         if (lse && g == 0)
             lse[(int64_t)(q0 + r) * in.H + h] = sum == 0.f ? neg_inf() : (m[j] + __log2f(sum)) * LN2;
     }
+    int* any = reinterpret_cast<int*>(even);
+    if (lane == 0) any[wave] = taken != 0;
+    __syncthreads();
+    if (uniform(any[0] | any[1] | any[2] | any[3])) put_taken<E, DN, DR>(o, h, seq, tile, m);
 }
 
 template <typename E, int DN, int DR>

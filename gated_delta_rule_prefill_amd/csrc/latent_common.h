@@ -263,6 +263,22 @@ struct Stage {
         const unsigned long long any = __ballot(bad) >> (tid & 63 & ~(TPR - 1));
         return (any & ((1ull << TPR) - 1)) != 0;
     }
+    // The row's values that are not finite, and only those, set to 0.
+    __device__ __forceinline__ void clear_bad(int p) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                unsigned x = r[p][s][i];
+                if (sizeof(E) == 2) {
+                    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+                    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+                } else if ((x & 0x7f800000u) == 0x7f800000u) {
+                    x = 0u;
+                }
+                r[p][s][i] = x;
+            }
+    }
     __device__ __forceinline__ void fill_row(int p, unsigned x) {
 #pragma unroll
         for (int s = 0; s < S; ++s) r[p][s] = u32x4{x, x, x, x};

@@ -289,7 +289,12 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  *   Values     NaN and Inf propagate from the keys a row sees to its result, and
  *              from a row to the gradients of the keys it sees, and no further:
  *              keys that the mask hides, rows behind a sequence's end and unused
- *              cache rows may hold anything.
+ *              cache rows may hold anything.  In kda_latent_attention a value of
+ *              v that is not finite reaches its own channel of o only, and never
+ *              lse.  Elsewhere how far it spreads is not specified: a latent of
+ *              the cache may turn all of o and lse of the rows that see it into
+ *              NaN where the formula gives some of it as Inf or finite, and an
+ *              input of the backward pass any gradient that it takes part in.
  * ---------------------------------------------------------------------------
  */
 

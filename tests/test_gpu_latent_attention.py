@@ -338,3 +338,32 @@ def test_rows_without_keys_and_gradients_that_are_not_finite(dtype, lens_q, lens
     got = both(x, lens_q, lens_k, True)
     check_all(f"no keys, d_o {value} {dtype}", clean, got, lens_q, lens_k, True)
     assert (got["dq"][empty] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,dr", [(128, 64), (64, 0)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_values_of_infinity_reach_their_channel_only(dtype, d, dr, causal):
+    """Inf and NaN in a value reach that channel of the rows that see it, in
+    every tile alike; the other channels and lse are those without it."""
+    import gated_delta_rule_prefill_amd as kda
+    lens, first = [400, 70], [0, 400]
+    x = make(30, dtype, 3, d, dr, lens, lens)
+    bad = [(0, 3, 1, 9, math.inf), (0, 150, 0, 5, -math.inf), (0, 151, 2, 7, math.nan), (0, 399, 1, 60, math.inf),
+           (1, 64, 0, 0, math.nan)]
+    v = x["v"].clone()
+    for s, j, h, c, value in bad:
+        x["v"][first[s] + j, h, c] = value
+        v[first[s] + j, h, c] = 0.0
+    o, lse = kda.latent_attention(x["q"], x["k"], x["v"], k_pe=x["k_pe"], cu_seqlens=offsets(lens), causal=causal,
+                                  scale=x["scale"])
+    want = ref.attention(x["q"], x["k"], v, x["k_pe"], lens, lens, causal, x["scale"])
+    ref.check("lse", lse, *want["lse"])
+    o = o.double().cpu()
+    for s, j, h, c, value in bad:
+        rows = slice(first[s] + (j if causal else 0), first[s] + lens[s])
+        seen = o[rows, h, c]
+        assert torch.equal(torch.nan_to_num(seen, 1.0, 2.0, 3.0),
+                           torch.nan_to_num(torch.full_like(seen, value), 1.0, 2.0, 3.0)), (s, j, h, c)
+        o[rows, h, c] = want["o"][0][rows, h, c]
+    ref.check("o elsewhere", o, *want["o"])
