@@ -236,3 +236,69 @@ def test_one_workspace_for_batches_of_any_size(dtype):
         x = td.make(75, dtype, 32, 256, 64, 16, lens, new)
         got, want = td.run(x, 256, workspace=ws), td.run(x, 256)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# 128 tiles of 64 rows and more (times heads): fp32 gradients that are not split
+WHOLE = [([2100], [2100], 4), ([300, 1, 65, 129], [300, 1, 65, 129], 32), ([70, 40], [1000, 33], 32)]
+
+
+@pytest.mark.parametrize("d,dr", [(128, 64), (128, 0), (64, 64), (64, 0)])
+@pytest.mark.parametrize("lens_q,lens_k,H", WHOLE)
+def test_fp32_gradients_of_batches_that_are_not_split(d, dr, lens_q, lens_k, H):
+    x = ta.make(76, "f32", H, d, dr, lens_q, lens_k)
+    ta.check_all("whole", x, ta.both(x, lens_q, lens_k, True), lens_q, lens_k, True)
+
+
+@pytest.mark.parametrize("what", ["k", "v", "q", "d_o"])
+def test_fp32_values_that_are_not_finite_in_batches_that_are_not_split(what):
+    """NaN in a key reaches no row before it, NaN in a row no key behind it."""
+    lens, H, bad = [300, 70], 32, 150
+    x = ta.make(77, "f32", H, 128, 64, lens, lens)
+    clean = dict(x)
+    clean.update({n: x[n].clone() for n in ("q", "d_o")})
+    if what in ("q", "d_o"):
+        clean["q"][bad], clean["d_o"][bad] = 0.0, 0.0
+    x[what] = x[what].clone()
+    x[what][bad, :, 5] = float("nan")
+    got = ta.both(x, lens, lens, True)
+    want = ref.attention(clean["q"], clean["k"], clean["v"], clean["k_pe"], lens, lens, True, x["scale"], clean["d_o"])
+    if what in ("k", "v"):
+        names, parts = ("o", "lse", "dq"), (slice(0, bad), slice(300, 370))
+    else:
+        names, parts = ("dk", "dv", "dk_pe"), (slice(bad + 1, 370),)
+    for n in names:
+        for part in parts:
+            ref.check(f"{what} {n}", got[n][part], want[n][0][part], want[n][1][part])
+
+
+def test_fp32_is_fp32():
+    """The element-wise bounds allow for errors that all have one sign.  In the
+    norm they add like independent ones: a sum of n <= 400 terms is off by about
+    sqrt(400) half steps of 2^-24, 1.2e-6, relative to its terms; a gradient has
+    four such sums on its way (scores, g . v, delta, its own), 2.4e-6 together, and
+    exponentials within 2^-22.  Operands cut to 16 bits would be off by 2^-17 each,
+    1e-5 and more in all."""
+    lens = [400, 90]
+    for H, d, dr in ((2, 128, 64), (32, 64, 64)):            # split and whole
+        x = ta.make(78, "f32", H, d, dr, lens, lens)
+        got = ta.both(x, lens, lens, True)
+        want = ref.attention(x["q"], x["k"], x["v"], x["k_pe"], lens, lens, True, x["scale"], x["d_o"])
+        for n in ("o", "dq", "dk", "dv", "dk_pe"):
+            rel = ref.check(f"fp32 {n}", got[n], *want[n])
+            assert rel <= 4e-6, n
+    for dl in (256, 512):
+        x = td.make(79, "f32", 8, dl, 64, 16, [400, 90], [1, 3])
+        o, _ = td.run(x, dl)
+        assert ref.check("fp32 decode", o, *ref.decode(x["q"], x["cache"], x["table"], [400, 90], [1, 3], dl,
+                                                        x["scale"])[0]) <= 4e-6
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,new", [
+    ([(97 * i) % 400 + 1 for i in range(40)], [1] * 40),     # 40 row tiles, joined row by row
+    ([(13 * i) % 90 for i in range(300)], [1] * 300),        # more row tiles than workgroups
+    ([900, 40, 200], [130, 40, 3]),                          # tiles of 64 rows, over 32 of them
+])
+def test_decode_of_512_channels_in_many_row_tiles(dtype, lens, new):
+    x = td.make(80, dtype, 32, 512, 64, 16, lens, new)
+    td.check(f"{len(lens)} sequences", x, 512, lens, new)
