@@ -320,9 +320,9 @@ kda_status kda_rotary(const void* x, int64_t x_token_stride, int64_t x_head_stri
             if (s < 0 || s >= ((int64_t)1 << 40)) return fail(KDA_ERR_INVALID_ARGUMENT, "strides must be in [0, 2^40)");
         if ((H > 1 && y_head_stride < d) || (total_tokens > 1 && y_token_stride < d))
             return fail(KDA_ERR_INVALID_ARGUMENT, "strides of y must be at least d");
-        if (x == y && (x_token_stride != y_token_stride || x_head_stride != y_head_stride))
-            return fail(KDA_ERR_INVALID_ARGUMENT, "in place, x and y must have the same strides");
         if (total_tokens == 0) return KDA_OK;
+        if (x == y && ((total_tokens > 1 && x_token_stride != y_token_stride) || (H > 1 && x_head_stride != y_head_stride)))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "in place, x and y must have the same strides");
         const kda::Rotary a{x, x_token_stride, x_head_stride, y, y_token_stride, y_head_stride, positions, inv_freq,
                             total_tokens, H, d, start, dr, amplitude, flags};
         return launched(kda::launch_rotary(a, dtype == KDA_DTYPE_BF16, reinterpret_cast<hipStream_t>(stream)),

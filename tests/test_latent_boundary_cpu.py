@@ -249,3 +249,12 @@ def test_decode_rejects_more_rows_than_it_counts():
         assert "total_tokens * H" in kda.last_error()
     # the largest that is counted goes on to the next check
     assert _decode(T=(1 << 31) - 4096, N=1, H=1, q=None) == INVALID and "q and o" in kda.last_error()
+
+
+def test_rotary_of_no_tokens():
+    """Two empty tensors may have one address (NULL) and different strides."""
+    for at in (None, A):
+        assert _rotary(T=0, x=at, y=at, xt=320 * 4, xh=320, pos=None) == kda.KDA_OK
+    # in place, strides of axes of one do not matter; those of others do
+    assert _rotary(T=1, x=A, y=A, xh=128) == INVALID and "in place" in kda.last_error()
+    assert _rotary(T=2, H=1, x=A, y=A, xt=512) == INVALID and "in place" in kda.last_error()

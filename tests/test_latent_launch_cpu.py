@@ -53,3 +53,14 @@ for name, f, kw in (("q", forward, "cu_q"), ("k", forward, "cu_k"), ("dq", backw
         assert down["launches"] == 0
         copies = 2 if name in ("k", "dk") else 1
         assert rising["status"] == kda.KDA_OK and rising["syncs"] == rising["launches"] + copies, name
+
+
+def test_rotary_in_place_with_strides_of_axes_of_one(tmp_path):
+    """The stride of one token, or of one head, is not looked at."""
+    code = """
+def turn(T, H, xt, xh):
+    return lib.kda_rotary(A, xt, xh, A, 256, 64, A, A, T, H, 64, 0, 64, 1, 1.0, 0, None)
+result["token"], result["head"] = call(turn, T=1, H=4, xt=0, xh=64), call(turn, T=3, H=1, xt=256, xh=0)
+"""
+    for got in hip_stub.run(tmp_path, code).values():
+        assert got["status"] == kda.KDA_OK and got["launches"] == 1
