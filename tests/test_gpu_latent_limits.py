@@ -302,3 +302,77 @@ def test_fp32_is_fp32():
 def test_decode_of_512_channels_in_many_row_tiles(dtype, lens, new):
     x = td.make(80, dtype, 32, 512, 64, 16, lens, new)
     td.check(f"{len(lens)} sequences", x, 512, lens, new)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,Tk", [(0, 0), (0, 70), (70, 0), (1, 0)])
+@pytest.mark.parametrize("packed", [True, False])
+def test_no_queries_or_no_keys(dtype, T, Tk, packed):
+    import gated_delta_rule_prefill_amd as kda
+    x = ta.make(81, dtype, 3, 128, 64, [T], [Tk])
+    args = dict(k_pe=x["k_pe"], scale=x["scale"])
+    if packed:
+        args.update(cu_seqlens=ta.offsets([T]), cu_seqlens_k=ta.offsets([Tk]))
+    o, lse = kda.latent_attention(x["q"], x["k"], x["v"], **args)
+    g = kda.latent_attention_backward(x["q"], x["k"], x["v"], o, lse, x["d_o"], **args)
+    assert o.shape == (T, 3, 128) and (o == 0).all() and torch.isneginf(lse).all()
+    for n, rows in (("dq", T), ("dk", Tk), ("dv", Tk), ("dk_pe", Tk)):
+        assert g[n].shape[0] == rows and (g[n] == 0).all(), n
+
+
+def test_no_tokens_in_the_paged_and_rotary_calls():
+    import gated_delta_rule_prefill_amd as kda
+    x = td.make(82, "bf16", 4, 256, 64, 16, [20, 5], [0, 0])
+    before = x["cache"].clone()
+    c = torch.zeros(0, 320, device="cuda", dtype=torch.bfloat16)
+    for cu in (x["cu"], None):
+        o, lse = td.run(x, 256, cu_seqlens=cu)
+        assert o.shape == (0, 4, 256) and lse.shape == (0, 4)
+        kda.latent_append(x["cache"], c[:, :256], x["table"], x["seq_lens"], k_pe=c[:, 256:], cu_seqlens=cu, c_out=True)
+    assert torch.equal(x["cache"].view(torch.int16), before.view(torch.int16))
+    freq, _ = kda.rotary_frequencies(64, device="cuda")
+    assert kda.rotary(x["q"][..., :64], torch.zeros(0, dtype=torch.int32, device="cuda"), freq).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_keys_and_values_that_the_heads_share(dtype):
+    """Keys and values broadcast over the heads (stride 0), queries too: as dense copies."""
+    import gated_delta_rule_prefill_amd as kda
+    lens, H = [70, 200], 4
+    x = ta.make(83, dtype, H, 128, 64, lens, lens)
+    k, v = x["k"][:, :1].expand(-1, H, -1), x["v"][:, :1].expand(-1, H, -1)
+    q = x["q"][:1, :1].expand(270, H, -1)
+    args = dict(k_pe=x["k_pe"][:1].expand(270, -1), cu_seqlens=ta.offsets(lens), scale=x["scale"])
+    dense = dict(args, k_pe=args["k_pe"].contiguous())
+    o, lse = kda.latent_attention(q, k, v, **args)
+    want = kda.latent_attention(q.contiguous(), k.contiguous(), v.contiguous(), **dense)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    got = kda.latent_attention_backward(q, k, v, o, lse, x["d_o"], **args)
+    want = kda.latent_attention_backward(q.contiguous(), k.contiguous(), v.contiguous(), o, lse, x["d_o"], **dense)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [5, 32])
+def test_paged_offsets_that_start_late(dtype, H):
+    """New tokens behind rows of no sequence, in decode and in append."""
+    import gated_delta_rule_prefill_amd as kda
+    lens, new, first = [150, 20], [30, 2], 7
+    x = td.make(84, dtype, H, 256, 64, 16, lens, new, poison=False)
+    want = td.run(x, 256)
+    y = dict(x, q=torch.cat([x["q"][:first] * float("nan"), x["q"]]), cu=x["cu"] + first)
+    out = torch.full((39, H, 256), 7.0, dtype=td.DT[dtype], device="cuda")
+    lse = torch.full((39, H), 7.0, device="cuda")
+    td.run(y, 256, out=out, lse=lse)
+    assert (out[:first] == 7.0).all() and (lse[:first] == 7.0).all()
+    wo, wl = ref.decode(x["q"], x["cache"], x["table"], lens, new, 256, x["scale"])
+    ref.check("late o", out[first:], *wo)
+    ref.check("late lse", lse[first:], *wl)
+    ref.check("o", want[0], *wo)
+    c = torch.randn(32, 320, device="cuda").to(td.DT[dtype])
+    caches = [x["cache"].clone() for _ in range(2)]
+    kda.latent_append(caches[0], c[:, :256], x["table"], x["seq_lens"], k_pe=c[:, 256:], cu_seqlens=x["cu"])
+    late = torch.cat([c[:first], c])
+    kda.latent_append(caches[1], late[:, :256], x["table"], x["seq_lens"], k_pe=late[:, 256:], cu_seqlens=y["cu"])
+    assert torch.equal(caches[0], caches[1])
