@@ -139,7 +139,7 @@ template <int W, int CT> struct ColReader<float, W, CT> {
 
 // Two accumulator tiles (rows 4g + i of two 16-row blocks) as the 8 slots of
 // an operand.  To bf16 each value is rounded to nearest: the products take
-// bf16 operands, and a relative error of at most 2^-9 per weight is that of
+// bf16 operands, and a relative error of at most 2^-8 per weight is that of
 // the inputs themselves.
 __device__ __forceinline__ bf16x8 acc_frag(f32x4 a, f32x4 b, bf16) {
     return bf16x8{(bf16)a[0], (bf16)a[1], (bf16)a[2], (bf16)a[3], (bf16)b[0], (bf16)b[1], (bf16)b[2], (bf16)b[3]};
