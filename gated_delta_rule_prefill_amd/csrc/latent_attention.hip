@@ -14,60 +14,86 @@
 namespace kda {
 
 // The values that the kernel below took out of tile 0 and of those that some row
-// of the workgroup does not see whole, found again.  With a weight above 0 such a
-// value makes its channel Inf or NaN whatever the others add, so it may follow
-// the output's rounding.  m: the final maxima of this lane's rows.
+// of the workgroup does not see whole, found again: per channel the first key
+// with Inf or NaN and the first with -Inf or NaN.  Weights of keys that a row sees
+// are above 0, so it takes the one, the other or NaN, whatever its other keys add
+// and thus behind the output's rounding.  It reads the values of those tiles once
+// more: 8 rows of 2,048 tokens x 32 heads, 128 + 64 channels, padded with NaN from
+// 1,500 on 456 us (436 with finite padding), from 1 on 505; 64 rows of 256 padded
+// from 100 on 265 (166).  (With each key's weight worked out as well: 10.7 ms,
+// 48 ms and 28 ms.)
 template <typename E, int DN, int DR>
-__device__ __forceinline__ void put_taken(E* o, int h, int seq, int tile, const float (&m)[LATENT_NQ<E>])
+__device__ __forceinline__ void put_taken(E* o, int h, int seq, int tile, int* first /* [2][DN] in LDS */)
 {
-    constexpr int KS = (DN + DR) / 32, DV = DN, BN = 128 / (int)sizeof(E), NQ = LATENT_NQ<E>, BQ = 64 * NQ;
+    constexpr int DV = DN, BN = 128 / (int)sizeof(E), NQ = LATENT_NQ<E>, BQ = 64 * NQ;
+    constexpr int CE = CHUNK_ELEMS<E>, CH = DV / CE, PASS = 256 / CH, NONE = 0x7fffffff;
+    typedef E vec __attribute__((ext_vector_type(CE)));
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
     // The inputs are read from the kernel's first argument again, and nothing of this
     // is worked out ahead of the walk, whose registers are short.
     int tid = threadIdx.x;
     auto args = (const __attribute__((address_space(4))) kda_latent_inputs*)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+v"(tid), "+s"(args));
     const auto& in = *args;
-    const int lane = tid & 63, col = lane & 15, g = lane >> 4;
     int q0, q1, k0, k1;
     sequence_rows(in.cu_seqlens_q, (int)(in.total_q / in.num_seqs), (int)in.total_q, seq, q0, q1);
     sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
                   (int)in.total_k, seq, k0, k1);
     const int nq = q1 - q0, nk = k1 - k0, off = nk - nq;
-    const int full = in.causal ? min(nk, tile * BQ + off + 1) : nk;                   // as in the kernel
+    const int full = in.causal ? min(nk, tile * BQ + off + 1) : nk;   // as in the kernel
     const int end = in.causal ? min(nk, min(nq, (tile + 1) * BQ) + off) : nk;
-    auto finite = [](float x) { return __builtin_fabsf(x) < __builtin_inff(); };
-#pragma unroll 1
-    for (int key = 0; key < end; key = key == BN - 1 ? max(BN, full / BN * BN) : key + 1) {
-        const E* v = (const E*)in.v + (int64_t)(k0 + key) * in.v_token_stride + h * in.v_head_stride;
-        bool bad = false;
+
+    for (int i = tid; i < 2 * DV; i += 256) first[i] = NONE;
+    __syncthreads();
+    int up[CE], down[CE];
 #pragma unroll
-        for (int c = 0; c < DV; c += 64) bad |= !finite(to_f32(v[c + lane]));
-        if (!__any(bad)) continue;
-        const E* k = (const E*)in.k + (int64_t)(k0 + key) * in.k_token_stride + h * in.k_head_stride;
-        const E* pe = DR ? (const E*)in.k_pe + (int64_t)(k0 + key) * in.k_pe_token_stride : nullptr;
+    for (int e = 0; e < CE; ++e) up[e] = down[e] = NONE;
+    const int behind = max(BN, full / BN * BN);   // first key behind the tiles that are seen whole
+    const E* v = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride + tid % CH * CE;
+    const int count = min(end, BN) + max(0, end - behind);
+    for (int i = tid / CH; i < count; i += 4 * PASS) {
+        vec x[4];
+        int key[4];
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-            const int r = tile * BQ + 16 * (NQ * (tid >> 6) + j) + col;
-            const int64_t at = q0 + min(r, nq - 1);
-            const E* q = (const E*)in.q + at * in.q_token_stride + h * in.q_head_stride;
-            float z = 0.f;
-#pragma unroll 1
-            for (int ks = 0; ks < KS; ++ks) {
-                const auto a = row_frag_global(q, ks, lane);
-                const auto b = 32 * ks < DN ? row_frag_global(k, ks, lane) : row_frag_global(pe, ks - DN / 32, lane);
+        for (int n = 0; n < 4; ++n) {
+            const int at = min(i + n * PASS, count - 1);
+            key[n] = at < BN ? at : at - BN + behind;
+            x[n] = *reinterpret_cast<const vec*>(v + (int64_t)key[n] * in.v_token_stride);
+        }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z += to_f32(a[i]) * to_f32(b[i]);
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < CE; ++e) {
+                if (!(to_f32(x[n][e]) < __builtin_inff())) up[e] = min(up[e], key[n]);
+                if (!(to_f32(x[n][e]) > neg_inf())) down[e] = min(down[e], key[n]);
             }
-            z = group_sum(z) * in.scale * LOG2E;
-            if (r >= nq || key > (in.causal ? min(nk - 1, r + off) : nk - 1)) continue;
-            const float w = exp2_fast(z - (m[j] == neg_inf() ? 0.f : m[j]));
-            E* row = o + (at * in.H + h) * DV;
-#pragma unroll 1
-            for (int i = 0; i < DV / 4; ++i) {   // the channels that this lane has written
-                const int c = 16 * (i / 4) + 4 * g + i % 4;
-                const float x = to_f32(v[c]);
-                if (!finite(x)) row[c] = from_f32<E>(to_f32(row[c]) + w * x);
+    }
+#pragma unroll
+    for (int e = 0; e < CE; ++e) {
+        if (up[e] != NONE) atomicMin(first + tid % CH * CE + e, up[e]);
+        if (down[e] != NONE) atomicMin(first + DV + tid % CH * CE + e, down[e]);
+    }
+    __syncthreads();
+    const int col = tid & 15, g = tid >> 4 & 3;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = tile * BQ + 16 * (NQ * (tid >> 6) + j) + col;
+        const int last = in.causal ? min(nk - 1, r + off) : nk - 1;
+        if (r >= nq) continue;
+        E* row = o + ((int64_t)(q0 + r) * in.H + h) * DV;
+#pragma unroll
+        for (int c = 4 * g; c < DV; c += 16) {   // the channels that this lane has written
+            const i32x4 u = *reinterpret_cast<const i32x4*>(first + c), d = *reinterpret_cast<const i32x4*>(first + DV + c);
+            if (min(min(min(u[0], u[1]), min(u[2], u[3])), min(min(d[0], d[1]), min(d[2], d[3]))) > last) continue;
+            typename Vec<E>::v4 x = load_vec<typename Vec<E>::v4>(row + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y = to_f32(x[i]);
+                if (u[i] <= last) y += __builtin_inff();
+                if (d[i] <= last) y += neg_inf();
+                x[i] = from_f32<E>(y);
             }
+            store_vec(row + c, x);
         }
     }
 }
@@ -306,7 +332,7 @@ __global__ __launch_bounds__(256, 2) void latent_attention_kernel(
     int* any = reinterpret_cast<int*>(even);
     if (lane == 0) any[wave] = taken != 0;
     __syncthreads();
-    if (uniform(any[0] | any[1] | any[2] | any[3])) put_taken<E, DN, DR>(o, h, seq, tile, m);
+    if (uniform(any[0] | any[1] | any[2] | any[3])) put_taken<E, DN, DR>(o, h, seq, tile, reinterpret_cast<int*>(odd));
 }
 
 template <typename E, int DN, int DR>

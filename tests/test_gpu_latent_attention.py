@@ -367,3 +367,38 @@ def test_values_of_infinity_reach_their_channel_only(dtype, d, dr, causal):
                            torch.nan_to_num(torch.full_like(seen, value), 1.0, 2.0, 3.0)), (s, j, h, c)
         o[rows, h, c] = want["o"][0][rows, h, c]
     ref.check("o elsewhere", o, *want["o"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,dr", [(128, 64), (128, 0), (64, 64), (64, 0)])
+@pytest.mark.parametrize("lens_q,lens_k", [([70, 300, 1], [500, 200, 129]), ([257, 33], [257, 33]), ([300, 64], [40, 64])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_values_that_are_not_finite_anywhere(dtype, d, dr, lens_q, lens_k, causal):
+    """Inf, -Inf and NaN strewn over the values: each channel of a row is what
+    the values it sees make of it, whatever tiles they lie in."""
+    import gated_delta_rule_prefill_amd as kda
+    H = 3
+    x = make(32, dtype, H, d, dr, lens_q, lens_k)
+    g = torch.Generator().manual_seed(33)
+    odd = torch.randint(0, 400, x["v"].shape, generator=g).cuda()      # 0.75 % of the values
+    clean = x["v"].masked_fill(odd < 3, 0.0)
+    for i, value in enumerate((math.inf, -math.inf, math.nan)):
+        x["v"].masked_fill_(odd == i, value)
+    o, lse = kda.latent_attention(x["q"], x["k"], x["v"], k_pe=x["k_pe"], cu_seqlens=offsets(lens_q),
+                                  cu_seqlens_k=offsets(lens_k), causal=causal, scale=x["scale"])
+    want = ref.attention(x["q"], x["k"], clean, x["k_pe"], lens_q, lens_k, causal, x["scale"])
+    ref.check("lse", lse, *want["lse"])
+    value, bound = want["o"]
+    a = b = 0
+    for n, m in zip(lens_q, lens_k):
+        i, j = torch.arange(n)[:, None], torch.arange(m)[None]
+        sees = ((j <= i + (m - n)) if causal else (j >= 0)).expand(n, m).double()
+        up, down = (torch.einsum("nm,mhc->nhc", sees, ((odd[b:b + m] == s) | (odd[b:b + m] == 2)).double().cpu()) > 0
+                    for s in (0, 1))
+        part = value[a:a + n]
+        part[up], part[down], part[up & down] = math.inf, -math.inf, math.nan
+        a, b = a + n, b + m
+    got = o.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(value))
+    there = ~torch.isnan(value)
+    ref.check("o", got.masked_fill(~there, 0.0), value.masked_fill(~there, 0.0), bound)
