@@ -103,7 +103,7 @@ __device__ __forceinline__ void put_taken(E* o, int h, int seq, int tile, int* f
 // double-buffered in LDS (80 KB, two workgroups a CU): the next tile's global
 // loads are issued before a tile's products and stored to LDS behind them.
 // Bound by the matrix products: 16,384 causal tokens x 32 heads, 128 + 64
-// channels, bf16: 2.44 to 2.62 ms by lease, 1.13 to 1.05 PFLOP/s, where a large
+// channels, bf16: 2.44 to 2.62 ms from card to card, 1.13 to 1.05 PFLOP/s, where a large
 // library product reaches 1.15; documents of 256 to 4,096 tokens (36,755 in all) 1.16 ms.  fp32,
 // 6 sequences of 1 to 130 tokens x 4 heads: 15 us, one row tile's walk over its keys.
 template <typename E, int DN, int DR>
