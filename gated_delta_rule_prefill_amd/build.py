@@ -20,7 +20,9 @@ ARCH = "gfx950"
 KERNEL_SOURCES = ["chunk_table.hip", "prefill_intra.hip", "prefill_state.hip", "prefill_chain.hip",
                   "decode.hip", "recurrent.hip", "backward.hip", "backward_chunk.hip",
                   "kda_noalloc.hip", "latent_attention.hip", "latent_backward.hip",
-                  "latent_decode.hip", "latent_cache.hip", "latent_api.hip"]
+                  "latent_decode.hip", "latent_cache.hip", "latent_api.hip",
+                  "window_attention.hip", "window_backward.hip", "window_decode.hip",
+                  "head_norm.hip", "window_api.hip"]
 HOST_SOURCES = ["kda_api.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", CSRC, "-I", INCLUDE]

@@ -8,32 +8,12 @@
 #include <string>
 
 #include "../../include/kda.h"
-#include "kda_internal.h"
+#include "api_checks.h"
 #include "latent_launch.h"
 
 namespace {
 
-kda_status fail(kda_status s, const char* msg) {
-    kda::set_last_error(msg);
-    return s;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 4096;   // row indices and tile ends stay in 32 bits
-
-kda_status launched(hipError_t e, const char* what) {
-    if (e == hipSuccess) return KDA_OK;
-    kda::set_last_error(std::string(what) + ": " + hipGetErrorString(e));
-    return KDA_ERR_HIP;
-}
-
-bool dtype_ok(int32_t d) { return d == KDA_DTYPE_F32 || d == KDA_DTYPE_BF16; }
-int elem_size(int32_t d) { return d == KDA_DTYPE_BF16 ? 2 : 4; }
-
-// a stride in elements that keeps 16-byte alignment
-bool stride_ok(int64_t s, int32_t dtype) { return s * elem_size(dtype) % 16 == 0 && s >= 0 && s < ((int64_t)1 << 40); }
+using namespace kda::api;
 
 kda_status check_inputs(const kda_latent_inputs* in) {
     if (!in) return fail(KDA_ERR_INVALID_ARGUMENT, "inputs must be non-NULL");

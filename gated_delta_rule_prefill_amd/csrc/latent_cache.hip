@@ -6,16 +6,6 @@
 
 namespace kda {
 
-// cos and sin of position * frequency (radians).  The product and its
-// reduction to a fraction of a turn are in 64 bits: at position 10^6 a product
-// in 32 bits is off by 0.06 radians.
-__device__ __forceinline__ void rotation(int position, float inv_freq, bool inverse, float& c, float& s) {
-    const double turns = (double)position * (double)inv_freq * 0.15915494309189535;
-    const float r = (float)(turns - rint(turns));
-    sincospif(2.f * r, &s, &c);
-    if (inverse) s = -s;
-}
-
 // -- rotary positions ---------------------------------------------------------------
 // A workgroup takes `tokens` tokens: their dr / 2 angles go to LDS once for all
 // heads, then its threads walk (token, head, item).  An item of the rotated
@@ -140,22 +130,6 @@ hipError_t launch_rotary(const Rotary& a, bool bf16_io, hipStream_t stream) {
 }
 
 // -- cache rows ---------------------------------------------------------------------
-// Sequence of packed token t: the first s with cu[s + 1] > t, or -1 for a row
-// outside the sequences.  A 64-way search, one probe per lane and step.
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int N, int64_t t, int lane) {
-    int lo = 0, hi = N;   // the answer is in [lo, hi]
-    while (lo < hi) {
-        const int step = (hi - lo + 63) / 64, at = lo + lane * step + step - 1;
-        const bool past = at >= hi || cu[at + 1] > t;
-        const unsigned long long b = __ballot(past);
-        const int first = b ? __builtin_ctzll(b) : 64;
-        const int nlo = lo + first * step;
-        hi = min(hi, nlo + step - 1);
-        lo = min(nlo, hi);
-    }
-    return lo < N && t >= cu[0] ? lo : -1;
-}
-
 // One wave per token: the latent stays in registers between its sum of squares
 // and its write.
 template <typename E>

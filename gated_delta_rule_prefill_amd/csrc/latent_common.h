@@ -385,31 +385,19 @@ __device__ __forceinline__ void sequence_rows(const int32_t* cu, int rows, int t
     }
 }
 
-// Sequence and tile within it of the batch's tile number `want` (tiles of B
-// rows, counted through the sequences in order); false behind the last tile.
-// Packed batches: one pass over the offsets, NT of them at a time (a scan per
-// wave, the waves' sums through scratch).  Called by all NT threads.
-template <int B, int NT>
-__device__ __forceinline__ bool find_tile(const int32_t* cu, int N, int rows, int total, int want,
-                                          int* scratch /* [NT / 64 + 2] in LDS */, int& seq, int& tile) {
-    if (!cu) {
-        const int per = (rows + B - 1) / B;
-        if (per == 0 || want >= per * N) return false;
-        seq = want / per;
-        tile = want - seq * per;
-        return true;
-    }
+// Sequence and item within it of the batch's item number `want`, where sequence
+// s has count(s) of them; false behind the last.  One pass over the sequences, NT
+// at a time (a scan per wave, the waves' sums through scratch).  Called by all NT
+// threads.
+template <int NT, typename F>
+__device__ __forceinline__ bool find_item(int N, int want, int* scratch /* [NT / 64 + 2] in LDS */, int& seq, int& item,
+                                          F count) {
     constexpr int NW = NT / 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int before = 0;
     for (int base = 0; base < N; base += NT) {
         const int s = base + tid;
-        int n = 0;
-        if (s < N) {
-            int a, b;
-            sequence_rows(cu, rows, total, s, a, b);
-            n = (b - a + B - 1) / B;
-        }
+        const int n = s < N ? count(s) : 0;
         int incl = n;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -431,12 +419,33 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int N, int rows, in
         }
         __syncthreads();
         seq = uniform(scratch[NW]);
-        tile = uniform(scratch[NW + 1]);
+        item = uniform(scratch[NW + 1]);
         __syncthreads();
         if (seq >= 0) return true;
         before = all;
     }
     return false;
+}
+
+// Sequence and tile within it of the batch's tile number `want` (tiles of B
+// rows, counted through the sequences in order); false behind the last tile.
+// A token counts as `each` rows.
+// Called by all NT threads.
+template <int B, int NT>
+__device__ __forceinline__ bool find_tile(const int32_t* cu, int N, int rows, int total, int want,
+                                          int* scratch /* [NT / 64 + 2] in LDS */, int& seq, int& tile, int each = 1) {
+    if (!cu) {
+        const int per = (rows * each + B - 1) / B;
+        if (per == 0 || want >= per * N) return false;
+        seq = want / per;
+        tile = want - seq * per;
+        return true;
+    }
+    return find_item<NT>(N, want, scratch, seq, tile, [&](int s) {
+        int a, b;
+        sequence_rows(cu, rows, total, s, a, b);
+        return ((b - a) * each + B - 1) / B;
+    });
 }
 
 // Workgroup -> (head, tile): the heads go round robin over the 8 XCDs (as the
@@ -452,6 +461,33 @@ __device__ __forceinline__ void head_tile_of_block(int H, int tiles, int& h, int
         h = L / tiles;
         tile = L % tiles;
     }
+}
+
+// -- tokens and positions ---------------------------------------------------------
+// cos and sin of position * frequency (radians).  The product and its
+// reduction to a fraction of a turn are in 64 bits: at position 10^6 a product
+// in 32 bits is off by 0.06 radians.
+__device__ __forceinline__ void rotation(int position, float inv_freq, bool inverse, float& c, float& s) {
+    const double turns = (double)position * (double)inv_freq * 0.15915494309189535;
+    const float r = (float)(turns - rint(turns));
+    sincospif(2.f * r, &s, &c);
+    if (inverse) s = -s;
+}
+
+// Sequence of packed token t: the first s with cu[s + 1] > t, or -1 for a row
+// outside the sequences.  A 64-way search, one probe per lane and step.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int N, int64_t t, int lane) {
+    int lo = 0, hi = N;   // the answer is in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + 63) / 64, at = lo + lane * step + step - 1;
+        const bool past = at >= hi || cu[at + 1] > t;
+        const unsigned long long b = __ballot(past);
+        const int first = b ? __builtin_ctzll(b) : 64;
+        const int nlo = lo + first * step;
+        hi = min(hi, nlo + step - 1);
+        lo = min(nlo, hi);
+    }
+    return lo < N && t >= cu[0] ? lo : -1;
 }
 
 // max and sum over the lanes that share l & 15 (the 4 lane groups)

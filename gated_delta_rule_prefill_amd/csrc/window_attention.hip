@@ -1,0 +1,304 @@
+// window_attention.hip -- window attention, forward: over packed keys, and over a
+// paged cache for chunks of new tokens.
+//
+// Per query head, row i at position p:
+//   z_ij = scale q_i . k_j  for j <= p with p - j < W or j < sinks
+//   o_i  = sum_j exp(z_ij - z_max) v_j / sum_j exp(z_ij - z_max)
+// in one pass over the keys of a tile of rows (KeyRange: the sinks, then the run
+// that the window covers) with the running maximum and sum.  The scores of a tile
+// are formed transposed, S^T = K Q^T (rows = keys), so that a lane holds 4
+// neighbouring keys of one query row: as they stand, exponentiated, they are the
+// operand of O^T += V^T P^T, whose other operand is V read by columns.  Scores and
+// weights never leave the registers, and a row's maximum, sum and rescale factor
+// are one value per lane.
+#include "window_common.h"
+
+namespace kda {
+
+// A workgroup: 4 waves of 32 (bf16) or 16 (fp32) query rows, whose operands q and
+// o stay in registers, one key head.  Key and value tiles of BN rows are
+// double-buffered in LDS: the next tile's global loads are issued before a tile's
+// products and stored to LDS behind them.
+template <typename E, int D, bool PAGED>
+__global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowArgs a, int tiles)
+{
+    constexpr int BN = 128 / (int)sizeof(E), NQ = LATENT_NQ<E>, BQ = 64 * NQ;
+    constexpr int KS = D / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
+    typedef typename Vec<E>::v8 v8;
+    // two arrays, so that a read of one is seen not to wait for loads into the other
+    __shared__ __attribute__((aligned(16))) E even[BN * 2 * D];
+    __shared__ __attribute__((aligned(16))) E odd[BN * 2 * D];
+    __shared__ int64_t place[4][PAGED ? BN : 1];   // cache rows of the tiles' keys, -1: none
+    __shared__ int gaps[4];                        // whether a tile has keys without a row
+
+    const kda_window_inputs& in = a.in;
+    int h, want, seq, tile;
+    key_head_of_block(in.Hk, tiles, blockIdx.x, h, want);
+    const int rows_q = (int)(in.total_q / in.num_seqs), G = in.H / in.Hk;
+    if (!find_tile<BQ, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, tiles - 1 - want,
+                            reinterpret_cast<int*>(even), seq, tile, G))
+        return;
+    int q0, q1, k0 = 0, nk;
+    sequence_rows(in.cu_seqlens_q, rows_q, (int)in.total_q, seq, q0, q1);
+    if constexpr (PAGED) {
+        nk = uniform(cached_tokens(a.pages, seq));
+    } else {
+        int k1;
+        sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
+                      (int)in.total_k, seq, k0, k1);
+        nk = k1 - k0;
+    }
+    const int nq = q1 - q0, off = nk - nq, rows = nq * G;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
+    const int wrow = tile * BQ + 16 * NQ * wave;   // the wave's first row
+    const float sc = in.scale * LOG2E;
+    auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
+    const KeyRange kr(uniform(token(tile * BQ)), uniform(token(tile * BQ + BQ - 1)), off, in.window, in.sinks, nk);
+    const int nt = (kr.total + BN - 1) / BN;
+
+    const E *kp, *vp;
+    if constexpr (PAGED) {
+        kp = (const E*)a.pages.k + h * a.pages.head_stride;
+        vp = (const E*)a.pages.v + h * a.pages.head_stride;
+    } else {
+        kp = (const E*)in.k + (int64_t)k0 * in.k_token_stride + h * in.k_head_stride;
+        vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
+    }
+
+    // this lane's query rows, and the keys each sees
+    v8 q[NQ][KS];
+    int last[NQ], first[NQ];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = min(wrow + 16 * j + col, rows - 1), i = token(r);
+        const E* row = (const E*)in.q + (int64_t)(q0 + i) * in.q_token_stride + (h * G + r - i * G) * in.q_head_stride;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(row, ks, lane);
+        last[j] = kr.last(i + off);
+        first[j] = kr.first(i + off);
+    }
+    // of the wave's rows
+    const int w0 = uniform(token(wrow)) + off, w1 = uniform(token(wrow + 16 * NQ - 1)) + off;
+    const int last_lo = kr.last(w0), last_hi = kr.last(w1), first_lo = kr.first(w0), first_hi = kr.first(w1);
+
+    Stage<E, D, BN, 256> sk, sv;
+    auto load = [&](int t) {
+        if constexpr (PAGED) {
+            auto row = [&](const E* base) {
+                return [&, base](int r) {
+                    const int64_t at = place[t & 3][r];
+                    return at < 0 ? zero_row<E>() : base + at;
+                };
+            };
+            sk.template load<false>(tid, row(kp));
+            sv.template load<false>(tid, row(vp));
+        } else {
+            auto row = [&](const E* base, int64_t stride) {
+                return [&, base, stride](int r) {
+                    const int n = t * BN + r;
+                    return n < kr.total ? base + kr.position(n) * stride : zero_row<E>();
+                };
+            };
+            sk.template load<false>(tid, row(kp, in.k_token_stride));
+            sv.template load<false>(tid, row(vp, in.v_token_stride));
+        }
+    };
+    auto store = [&](E* to) {
+        // a hidden key's weight is 0, and 0 times NaN or Inf is NaN
+        move_bad_rows(tid, sv, sk);
+        sk.store(tid, to);
+        sv.store(tid, to + BN * D);
+    };
+    // PAGED: the cache row of key tid of tile t (tid < BN)
+    auto look_up = [&](int t) -> int64_t {
+        const int n = t * BN + tid;
+        return n < kr.total ? cached_row(a.pages, seq, kr.position(n)) : -1;
+    };
+    auto keep = [&](int t, int64_t at) {
+        place[t & 3][tid] = at;
+        const bool gap = __any(at < 0);
+        if (tid == 0) gaps[t & 3] = gap;
+    };
+    int64_t next_place = -1;
+    if constexpr (PAGED) {
+        static_assert(BN <= 64, "one wave looks the rows up");
+        if (tid < BN) {
+            const int64_t p0 = look_up(0), p1 = look_up(1);
+            keep(0, p0);
+            keep(1, p1);
+            next_place = look_up(2);
+        }
+        __syncthreads();
+    }
+    RowReader<E, D> k_rows(lane);
+    ColReader<E, D, D / 16> v_cols(lane);
+
+    f32x4 acc[NQ][D / 16];
+    float m[NQ], l[NQ];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        m[j] = neg_inf();
+        l[j] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (nt > 0) {
+        load(0);
+        store(even);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]);
+    auto step = [&](int t, const E* K, E* next) {
+        k_rows.keep(), v_cols.keep();
+        const E* V = K + BN * D;
+        const int n0 = t * BN;
+        if (t + 1 < nt) load(t + 1);
+        if constexpr (PAGED)
+            if (tid < BN) {
+                keep(t + 2, next_place);
+                next_place = look_up(t + 3);
+            }
+        if (wrow < rows && n0 <= last_hi && (n0 < kr.ns || n0 + BN > first_lo)) {
+            f32x4 s[NQ][TT];
+            v8 x[PD + 1];
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) s[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            // One sequence of operands, read ahead across its parts: the scores,
+            // two key tiles by turns so that products in a row do not wait for
+            // each other; and, after the weights, the product with the values.
+            constexpr int E0 = TT * KS;
+            v8 p[NQ][TT / 2];
+            auto take_weights = [&]() {
+                if (!kr.whole(n0, n0 + BN, last_lo, first_hi)) {
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int n = n0 + 16 * tt + 4 * g + i;
+                                if (n > last[j] || (n < first[j] && n >= kr.ns)) s[j][tt][i] = neg_inf();
+                            }
+                }
+                if constexpr (PAGED)
+                    if (uniform(gaps[t & 3])) {
+#pragma unroll
+                        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (place[t & 3][16 * tt + 4 * g + i] < 0)
+#pragma unroll
+                                    for (int j = 0; j < NQ; ++j) s[j][tt][i] = neg_inf();
+                    }
+                // The running maximum is raised only when a row's grew by more than
+                // 8 (in powers of two): until then the weights stay below 2^8 and
+                // nothing needs rescaling.
+                float top[NQ];
+                bool grew = false;
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    float x = neg_inf();
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x = fmaxf(x, s[j][tt][i]);
+                    top[j] = group_max(x) * sc;
+                    grew |= top[j] > m[j] + 8.f;
+                }
+                if (__any(grew)) {
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) {
+                        const float mn = fmaxf(m[j], top[j]);
+                        const float f = mn == neg_inf() ? 1.f : exp2_fast(m[j] - mn);
+                        m[j] = mn;
+                        l[j] *= f;
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) acc[j][c] *= f;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const float base = m[j] == neg_inf() ? 0.f : m[j];   // a row that has seen no key yet
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -base));
+                            l[j] += s[j][tt][i];   // the sum takes the weights before their rounding
+                        }
+#pragma unroll
+                    for (int b = 0; b < TT / 2; ++b) p[j][b] = acc_frag(s[j][2 * b], s[j][2 * b + 1], E());
+                }
+            };
+            ahead<E0 + D / 16 * (TT / 2), PD>(
+                [&](auto n) {
+                    constexpr int e = n, f = e - E0;
+                    if constexpr (e < E0) x[e % (PD + 1)] = k_rows(K, 16 * (e / (2 * KS) * 2 + e % 2), e / 2 % KS);
+                    else x[e % (PD + 1)] = v_cols(V, 32 * (f / (D / 16)), 32 * (f / (D / 16)) + 16, f % (D / 16));
+                },
+                [&](auto n) {
+                    constexpr int e = n, f = e - E0;
+                    if constexpr (e < E0) {
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j)
+                            s[j][e / (2 * KS) * 2 + e % 2] =
+                                mma32(x[e % (PD + 1)], q[j][e / 2 % KS], s[j][e / (2 * KS) * 2 + e % 2]);
+                    } else {
+                        if constexpr (f == 0) take_weights();
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j)
+                            acc[j][f % (D / 16)] = mma32(x[e % (PD + 1)], p[j][f / (D / 16)], acc[j][f % (D / 16)]);
+                    }
+                });
+        }
+        if (t + 1 < nt) store(next);
+        __syncthreads();
+    };
+    for (int t = 0; t < nt; ++t) step(t, t & 1 ? odd : even, t & 1 ? even : odd);
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = wrow + 16 * j + col;
+        const float sum = group_sum(l[j]);
+        if (r >= rows) continue;
+        const int i = token(r);
+        const int64_t out = (int64_t)(q0 + i) * in.H + h * G + r - i * G;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        E* row = (E*)a.o + out * D;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            typename Vec<E>::v4 x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(acc[j][c][i] * inv);
+            store_vec(row + 16 * c + 4 * g, x);
+        }
+        if (a.lse && g == 0) a.lse[out] = sum == 0.f ? neg_inf() : (m[j] + __log2f(sum)) * LN2;
+    }
+}
+
+template <typename E, int D, bool PAGED>
+static hipError_t launch(const WindowArgs& a, hipStream_t stream) {
+    constexpr int BQ = 64 * LATENT_NQ<E>;
+    const kda_window_inputs& in = a.in;
+    const int64_t G = in.H / in.Hk;
+    const int64_t tiles = in.cu_seqlens_q ? in.total_q * G / BQ + in.num_seqs
+                                          : (in.total_q / in.num_seqs * G + BQ - 1) / BQ * in.num_seqs;
+    hipLaunchKernelGGL((window_attention_kernel<E, D, PAGED>), dim3((unsigned)(tiles * in.Hk)), dim3(256), 0, stream, a,
+                       (int)tiles);
+    return launch_result(stream);
+}
+
+hipError_t launch_window_attention(const WindowArgs& a, bool paged, hipStream_t stream) {
+    if (a.in.dtype == KDA_DTYPE_BF16) {
+        if (a.in.d == 128) return paged ? launch<bf16, 128, true>(a, stream) : launch<bf16, 128, false>(a, stream);
+        return paged ? launch<bf16, 64, true>(a, stream) : launch<bf16, 64, false>(a, stream);
+    }
+    if (a.in.d == 128) return paged ? launch<float, 128, true>(a, stream) : launch<float, 128, false>(a, stream);
+    return paged ? launch<float, 64, true>(a, stream) : launch<float, 64, false>(a, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,503 @@
+// window_backward.hip -- gradients of the window attention.
+//
+// With the forward's weights w_ij = exp(z_ij - lse_i), z = scale q k^T, the output
+// gradient g_i = dL/do_i and delta_i = g_i . o_i, over the pairs that see each other:
+//   dv_j = sum_i w_ij g_i
+//   dz_ij = w_ij (g_i . v_j - delta_i)
+//   dq_i = scale sum_j dz_ij k_j,   dk_j = scale sum_i dz_ij q_i
+// where i runs over the rows of all query heads that share the key head.  Two
+// kernels, so that every sum stays in one workgroup's registers and the result does
+// not depend on an order of atomics: one walks the keys for a tile of query rows
+// (dq, and delta on the way), one walks the query rows for a tile of keys (dk, dv).
+// Each forms z and g v^T: two of the seven products are repeated.
+//
+// The sinks are seen by every later row of their sequence: their walk is cut into
+// pieces of WINDOW_PIECE tokens behind the window of the first key tile, whose parts
+// of dk and dv a third kernel adds up in order, with the first tile's own.
+#include "window_common.h"
+
+namespace kda {
+
+// dq and delta.  As in the forward kernel the scores are formed transposed (rows =
+// keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.  dq itself
+// takes delta from the rounded o, as its own sum is complete only behind the last
+// key; the second kernel takes that sum.
+template <typename E, int D>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
+    const kda_window_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
+    const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ row_stats, int tiles)
+{
+    constexpr int BN = 32, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
+    constexpr int KS = D / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
+    typedef typename Vec<E>::v8 v8;
+    // two arrays, so that a read of one is seen not to wait for loads into the other
+    __shared__ __attribute__((aligned(16))) E even[BN * 2 * D];
+    __shared__ __attribute__((aligned(16))) E odd[BN * 2 * D];
+    // the rows' output gradients: each wave's own, in operand order
+    __shared__ __attribute__((aligned(16))) E sgo[4][NQ][KS][64 * 8];
+
+    int h, want, seq, tile;
+    key_head_of_block(in.Hk, tiles, blockIdx.x, h, want);
+    const int rows_q = (int)(in.total_q / in.num_seqs), G = in.H / in.Hk;
+    if (!find_tile<BQ, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, tiles - 1 - want,
+                            reinterpret_cast<int*>(even), seq, tile, G))
+        return;
+    int q0, q1, k0, k1;
+    sequence_rows(in.cu_seqlens_q, rows_q, (int)in.total_q, seq, q0, q1);
+    sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
+                  (int)in.total_k, seq, k0, k1);
+    const int nq = q1 - q0, nk = k1 - k0, off = nk - nq, rows = nq * G;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
+    const int wrow = tile * BQ + 16 * NQ * wave;
+    const float sc = in.scale * LOG2E;
+    auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
+    const KeyRange kr(uniform(token(tile * BQ)), uniform(token(tile * BQ + BQ - 1)), off, in.window, in.sinks, nk);
+    const int nt = (kr.total + BN - 1) / BN;
+
+    const E* kp = (const E*)in.k + (int64_t)k0 * in.k_token_stride + h * in.k_head_stride;
+    const E* vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
+
+    v8 q[NQ][KS];
+    int last[NQ], first[NQ];
+    float lse2[NQ], dl[NQ], exact[NQ];   // delta from the rounded o, and from this kernel's own weights
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = min(wrow + 16 * j + col, rows - 1), i = token(r), head = h * G + r - i * G;
+        const E* row = (const E*)in.q + (int64_t)(q0 + i) * in.q_token_stride + head * in.q_head_stride;
+        const int64_t at = (int64_t)(q0 + i) * in.H + head;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(row, ks, lane);
+        float sum = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const v8 gv = row_frag_global(d_o + at * D, ks, lane), ov = row_frag_global(o + at * D, ks, lane);
+            store_frag(sgo[wave][j][ks], lane, gv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += to_f32(gv[e]) * to_f32(ov[e]);
+        }
+        lse2[j] = lse[at] * LOG2E;
+        // a row that sees no key has o = 0, and 0 times a d_o of NaN or Inf is NaN
+        dl[j] = group_sum(sum);
+        if (lse2[j] == neg_inf()) dl[j] = 0.f;
+        exact[j] = 0.f;
+        last[j] = kr.last(i + off);
+        first[j] = kr.first(i + off);
+    }
+    const int w0 = uniform(token(wrow)) + off, w1 = uniform(token(wrow + 16 * NQ - 1)) + off;
+    const int last_lo = kr.last(w0), last_hi = kr.last(w1), first_lo = kr.first(w0), first_hi = kr.first(w1);
+
+    Stage<E, D, BN, 256> sk, sv;
+    auto load = [&](int t) {
+        auto row = [&](const E* base, int64_t stride) {
+            return [&, base, stride](int r) {
+                const int n = t * BN + r;
+                return n < kr.total ? base + kr.position(n) * stride : zero_row<E>();
+            };
+        };
+        sk.template load<false>(tid, row(kp, in.k_token_stride));
+        sv.template load<false>(tid, row(vp, in.v_token_stride));
+    };
+    auto store = [&](E* to) {
+        move_bad_rows(tid, sk, sv);
+        sk.store(tid, to);
+        sv.store(tid, to + BN * D);
+    };
+    RowReader<E, D> rows_of(lane);
+    ColReader<E, D, D / 16> k_cols(lane);
+
+    f32x4 acc[NQ][D / 16];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (nt > 0) {
+        load(0);
+        store(even);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]);
+    auto step = [&](int t, const E* K, E* next) {
+        rows_of.keep(), k_cols.keep();
+        const E* V = K + BN * D;
+        const int n0 = t * BN;
+        if (t + 1 < nt) load(t + 1);
+        if (wrow < rows && n0 <= last_hi && (n0 < kr.ns || n0 + BN > first_lo)) {
+            f32x4 s[NQ][TT], dp[NQ][TT];
+            v8 x[PD + 1];
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) s[j][tt] = dp[j][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            // One sequence of operands, read ahead across its parts: z = q k^T;
+            // g v^T, between whose products the weights' exponentials run; and,
+            // after dz, dq^T += K^T dz.
+            constexpr int E0 = TT * KS, E1 = 2 * E0, NS = NQ * TT * 4;
+            v8 y[2][NQ], dz[NQ];
+            auto row_grads = [&](int ks) {
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) y[ks & 1][j] = load_frag(sgo[wave][j][ks], lane);
+            };
+            ahead<E1 + D / 16, PD>(
+                [&](auto n) {
+                    constexpr int e = n;
+                    x[e % (PD + 1)] = e < E0   ? rows_of(K, 16 * (e % TT), e / TT)
+                                      : e < E1 ? rows_of(V, 16 * ((e - E0) % TT), (e - E0) / TT)
+                                               : k_cols(K, 0, 16, e - E1);
+                },
+                [&](auto n) {
+                    constexpr int e = n;
+                    if constexpr (e < E0) {
+                        if (e == E0 - TT) row_grads(0);
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j) s[j][e % TT] = mma32(x[e % (PD + 1)], q[j][e / TT], s[j][e % TT]);
+                    } else if constexpr (e < E1) {
+                        constexpr int f = e - E0;
+                        if (f % TT == 0 && f / TT + 1 < KS) row_grads(f / TT + 1);
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j) dp[j][f % TT] = mma32(x[e % (PD + 1)], y[f / TT & 1][j], dp[j][f % TT]);
+#pragma unroll
+                        for (int m = NS * f / E0; m < NS * (f + 1) / E0; ++m) {
+                            const int j = m / (TT * 4), tt = m / 4 % TT, i = m % 4;
+                            s[j][tt][i] = exp2_fast(__builtin_fmaf(s[j][tt][i], sc, -lse2[j]));
+                        }
+                    } else {
+                        if (e == E1) {
+                            if (!kr.whole(n0, n0 + BN, last_lo, first_hi)) {   // weights of hidden keys
+#pragma unroll
+                                for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const int n = n0 + 16 * tt + 4 * g + i;
+                                            if (n > last[j] || (n < first[j] && n >= kr.ns))
+                                                s[j][tt][i] = 0.f, dp[j][tt][i] = 0.f;
+                                        }
+                            }
+#pragma unroll
+                            for (int j = 0; j < NQ; ++j) {
+#pragma unroll
+                                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        exact[j] += s[j][tt][i] * dp[j][tt][i];
+                                        s[j][tt][i] *= dp[j][tt][i] - dl[j];
+                                    }
+                                dz[j] = acc_frag(s[j][0], s[j][1], E());
+                            }
+                        }
+                        constexpr int c = e - E1;
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[e % (PD + 1)], dz[j], acc[j][c]);
+                    }
+                });
+        }
+        if (t + 1 < nt) store(next);
+        __syncthreads();
+    };
+    for (int t = 0; t < nt; ++t) step(t, t & 1 ? odd : even, t & 1 ? even : odd);
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+        const int r = wrow + 16 * j + col;
+        const float sum = group_sum(exact[j]);
+        if (r >= rows) continue;
+        const int i = token(r), head = h * G + r - i * G;
+        if (g == 0) {
+            float* stats = row_stats + 2 * ((int64_t)head * in.total_q + q0 + i);
+            stats[0] = lse2[j];
+            stats[1] = sum;
+        }
+        E* row = dq + ((int64_t)(q0 + i) * in.H + head) * D;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            typename Vec<E>::v4 x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(acc[j][c][i] * in.scale);
+            store_vec(row + 16 * c + 4 * g, x);
+        }
+    }
+}
+
+// Work of a sequence in the second kernel: its key tiles, and behind them the
+// pieces of the sinks' walk.  The first tile walks the tokens before `behind`,
+// piece c those from behind + c WINDOW_PIECE on: no other key of the first tile is
+// in their window.
+constexpr int DKV_KEYS = 64;
+static_assert(WINDOW_MAX_SINKS <= DKV_KEYS, "the sinks lie in the first tile");
+struct KeyWork {
+    int q0, nq, k0, nk, behind, tiles, pieces;
+    __device__ __forceinline__ KeyWork(const kda_window_inputs& in, int s) {
+        int q1, k1;
+        sequence_rows(in.cu_seqlens_q, (int)(in.total_q / in.num_seqs), (int)in.total_q, s, q0, q1);
+        sequence_rows(in.cu_seqlens_k ? in.cu_seqlens_k : in.cu_seqlens_q, (int)(in.total_k / in.num_seqs),
+                      (int)in.total_k, s, k0, k1);
+        nq = q1 - q0;
+        nk = k1 - k0;
+        tiles = (nk + DKV_KEYS - 1) / DKV_KEYS;
+        // the first token that no key of the first tile has in its window
+        behind = in.sinks > 0 ? min(nq, max(0, min(in.window, nk) + DKV_KEYS - 1 - (nk - nq))) : nq;
+        pieces = nk > 0 ? (nq - behind + WINDOW_PIECE - 1) / WINDOW_PIECE : 0;
+    }
+    // The first slot of its partial gradients: one for the first tile, then one for
+    // each piece (see window_slots).
+    __device__ __forceinline__ int64_t slot(int s) const { return q0 / WINDOW_PIECE + 2 * (int64_t)s; }
+};
+
+// dk and dv.  A wave owns 16 keys, whose k and v operands and gradients stay in
+// registers; the query rows come 32 tokens of one head at a time, head after head
+// of the group.  The scores are formed with rows = queries, so that the weights and
+// dz are the operands of dv^T += g^T w and dk^T += q^T dz as they stand.
+template <typename E, int D>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(
+    const kda_window_inputs in, const E* __restrict__ d_o, const float* __restrict__ row_stats,
+    E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
+    E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ part, int items)
+{
+    constexpr int BQ = 32, BK = DKV_KEYS, KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    typedef typename Vec<E>::v8 v8;
+    // two arrays, so that a read of one is seen not to wait for loads into the other
+    __shared__ __attribute__((aligned(16))) E even[BQ * 2 * D];
+    __shared__ __attribute__((aligned(16))) E odd[BQ * 2 * D];
+    __shared__ __attribute__((aligned(16))) float srow[2][2 * BQ];   // lse (base 2), then delta
+
+    int h, want, seq, item;
+    key_head_of_block(in.Hk, items, blockIdx.x, h, want);
+    if (!find_item<256>(in.num_seqs, want, reinterpret_cast<int*>(even), seq, item, [&](int s) {
+            const KeyWork w(in, s);
+            return w.tiles + w.pieces;
+        }))
+        return;
+    const KeyWork work(in, seq);
+    const int nq = work.nq, nk = work.nk, off = nk - nq, G = in.H / in.Hk;
+    const int piece = item < work.tiles ? -1 : item - work.tiles;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
+    const int key0 = piece < 0 ? item * BK : 0, wkey = key0 + 16 * wave, key = wkey + col;
+    const int W = min(in.window, nk);
+    const float sc = in.scale * LOG2E;
+    // the tokens [ta, te) to walk
+    const int ta = piece < 0 ? min(nq, max(0, key0 - off)) : work.behind + piece * WINDOW_PIECE;
+    const int te = piece >= 0 ? min(nq, ta + WINDOW_PIECE)
+                              : max(ta, (int)min((int64_t)nq, (int64_t)key0 + BK - 1 + W - off));
+    const int per = (te - ta + BQ - 1) / BQ, nu = per * G;   // tiles of a head, and all
+
+    v8 k[KS], v[KS];
+    {
+        const int64_t row = work.k0 + min(key, nk - 1);
+        const E* kp = (const E*)in.k + row * in.k_token_stride + h * in.k_head_stride;
+        const E* vp = (const E*)in.v + row * in.v_token_stride + h * in.v_head_stride;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) k[ks] = row_frag_global(kp, ks, lane), v[ks] = row_frag_global(vp, ks, lane);
+    }
+    const E* qp = (const E*)in.q + (int64_t)(work.q0 + ta) * in.q_token_stride + h * G * in.q_head_stride;
+    const E* gp = d_o + ((int64_t)(work.q0 + ta) * in.H + h * G) * D;
+    const float* sp = row_stats + 2 * ((int64_t)h * G * in.total_q + work.q0 + ta);
+
+    typedef Stage<E, D, BQ, 256> S;
+    S sq, sg;
+    static_assert(S::P == 1 && S::TPR == 8, "a row per 8 threads");
+    // lse and delta of a row travel with the row's own first thread, which knows
+    // whether the row is finite
+    float next_lse = 0.f, next_delta = 0.f;
+    auto load = [&](int head, int t) {
+        const int left = te - ta - t * BQ;
+        sq.load_rows(tid, qp + head * in.q_head_stride + (int64_t)t * BQ * in.q_token_stride, in.q_token_stride, left);
+        sg.load_rows(tid, gp + (int64_t)head * D + (int64_t)t * BQ * in.H * D, (int64_t)in.H * D, left);
+        if (tid % S::TPR == 0) {   // rows behind the last weigh nothing: lse = inf
+            const int i = tid / S::TPR;
+            const float* at = sp + 2 * ((int64_t)head * in.total_q + t * BQ + min(i, left - 1));
+            next_lse = i < left ? at[0] : __builtin_inff();
+            next_delta = i < left ? at[1] : 0.f;
+        }
+    };
+    auto store = [&](int u, E* to) {
+        const bool bad_delta = tid % S::TPR == 0 && !(__builtin_fabsf(next_delta) < __builtin_inff());
+        const bool bad_q = sq.bad_row(tid, 0), bad_g = sg.bad_row(tid, 0, bad_delta);
+        if (bad_q || bad_g) {   // as move_bad_rows: lse becomes NaN
+            sq.fill_row(0, 0u);
+            sg.fill_row(0, 0u);
+            next_lse = __builtin_nanf("");
+            next_delta = 0.f;
+        }
+        sq.store(tid, to);
+        sg.store(tid, to + BQ * D);
+        if (tid % S::TPR == 0) {
+            srow[u & 1][tid / S::TPR] = next_lse;
+            srow[u & 1][BQ + tid / S::TPR] = next_delta;
+        }
+    };
+    RowReader<E, D> rows_of(lane);
+    ColReader<E, D, D / 16> cols_of(lane);
+    f32x4 ak[D / 16], av[D / 16];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) ak[c] = av[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (nu > 0) {
+        load(0, 0);
+        store(0, even);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) arrived(k[ks]), arrived(v[ks]);
+    // Tile t of a head's tokens, number u of all; the next one is nt of nhead.
+    auto step = [&](int u, int t, int nhead, int nt, const E* Q, E* next) {
+        rows_of.keep(), cols_of.keep();
+        const E* Gt = Q + BQ * D;
+        const float* R = srow[u & 1];
+        const int p0 = ta + t * BQ + off, p1 = min(p0 + BQ, te + off) - 1;   // positions of the tile's rows
+        if (u + 1 < nu) load(nhead, nt);
+        if (p1 >= wkey && (p0 - (wkey + 15) < W || wkey < in.sinks)) {
+            f32x4 s[2], dp[2];
+            v8 x[PD + 1];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) s[a] = dp[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const f32x4 ls[2] = {*reinterpret_cast<const f32x4*>(R + 4 * g), *reinterpret_cast<const f32x4*>(R + 16 + 4 * g)};
+            const f32x4 de[2] = {*reinterpret_cast<const f32x4*>(R + BQ + 4 * g),
+                                 *reinterpret_cast<const f32x4*>(R + BQ + 16 + 4 * g)};
+            // One sequence of operands, read ahead across its parts: z = q k^T;
+            // g v^T, between whose products the weights' exponentials run;
+            // dv^T += g^T w, between whose products dz is formed; dk^T += q^T dz.
+            constexpr int E0 = 2 * KS, E1 = 2 * E0, E2 = E1 + D / 16, NS = 8;
+            v8 wf, zf;
+            ahead<E2 + D / 16, PD>(
+                [&](auto n) {
+                    constexpr int e = n;
+                    x[e % (PD + 1)] = e < E0   ? rows_of(Q, 16 * (e % 2), e / 2)
+                                      : e < E1 ? rows_of(Gt, 16 * ((e - E0) % 2), (e - E0) / 2)
+                                      : e < E2 ? cols_of(Gt, 0, 16, e - E1)
+                                               : cols_of(Q, 0, 16, e - E2);
+                },
+                [&](auto n) {
+                    constexpr int e = n;
+                    const v8& a = x[e % (PD + 1)];
+                    if constexpr (e < E0) {
+                        s[e % 2] = mma32(a, k[e / 2], s[e % 2]);
+                    } else if constexpr (e < E1) {
+                        constexpr int f = e - E0;
+                        dp[f % 2] = mma32(a, v[f / 2], dp[f % 2]);
+#pragma unroll
+                        for (int i = NS * f / E0; i < NS * (f + 1) / E0; ++i)
+                            s[i / 4][i % 4] = exp2_fast(__builtin_fmaf(s[i / 4][i % 4], sc, -ls[i / 4][i % 4]));
+                    } else if constexpr (e < E2) {
+                        constexpr int c = e - E1;
+                        if (c == 0) {
+                            // weights of hidden keys
+                            if (p0 < wkey + 15 || (p1 - wkey >= W && wkey + 15 >= in.sinks)) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int p = p0 + 16 * (i / 4) + 4 * g + i % 4;
+                                    if (key > p || (p - key >= W && key >= in.sinks))
+                                        s[i / 4][i % 4] = 0.f, dp[i / 4][i % 4] = 0.f;
+                                }
+                            }
+                            wf = acc_frag(s[0], s[1], E());
+                        }
+                        av[c] = mma32(a, wf, av[c]);
+#pragma unroll
+                        for (int i = NS * c / (D / 16); i < NS * (c + 1) / (D / 16); ++i)
+                            dp[i / 4][i % 4] = s[i / 4][i % 4] * (dp[i / 4][i % 4] - de[i / 4][i % 4]);
+                    } else {
+                        constexpr int c = e - E2;
+                        if (c == 0) zf = acc_frag(dp[0], dp[1], E());
+                        ak[c] = mma32(a, zf, ak[c]);
+                    }
+                });
+        }
+        if (u + 1 < nu) store(u + 1, next);
+        __syncthreads();
+    };
+    int head = 0, t = 0;
+    for (int u = 0; u < nu; ++u) {
+        const int nt = t + 1 < per ? t + 1 : 0, nhead = nt ? head : head + 1;
+        step(u, t, nhead, nt, u & 1 ? odd : even, u & 1 ? even : odd);
+        t = nt;
+        head = nhead;
+    }
+    if (key >= nk) return;
+    const bool sink = key < in.sinks && work.pieces > 0 && key0 == 0;
+    if (piece >= 0 && !sink) return;
+    if (sink) {
+        float* to = part + (((work.slot(seq) + piece + 1) * in.Hk + h) * in.sinks + key) * 2 * D + 4 * g;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            store_vec(to + 16 * c, ak[c] * in.scale);
+            store_vec(to + D + 16 * c, av[c]);
+        }
+        return;
+    }
+    const int64_t row = work.k0 + key;
+    E* kr = dk + row * dk_token_stride + h * dk_head_stride;
+    E* vr = dv + row * dv_token_stride + h * dv_head_stride;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+        typename Vec<E>::v4 kx, vx;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            kx[i] = from_f32<E>(ak[c][i] * in.scale);
+            vx[i] = from_f32<E>(av[c][i]);
+        }
+        store_vec(kr + 16 * c + 4 * g, kx);
+        store_vec(vr + 16 * c + 4 * g, vx);
+    }
+}
+
+// The sinks' gradients: the parts of the first key tile and of the pieces, in order,
+// rounded once.  A workgroup per sequence and key head, a thread per 4 channels.
+template <typename E, int D>
+__global__ __launch_bounds__(256) void window_sinks_kernel(
+    const kda_window_inputs in, const float* __restrict__ part, E* __restrict__ dk, int64_t dk_token_stride,
+    int64_t dk_head_stride, E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride)
+{
+    const int seq = (int)(block_of_grid() / in.Hk), h = (int)(block_of_grid() % in.Hk);
+    if (seq >= in.num_seqs) return;
+    const KeyWork work(in, seq);
+    if (work.pieces == 0) return;
+    const int64_t stride = (int64_t)in.Hk * in.sinks * 2 * D;   // from slot to slot
+    const float* from = part + (work.slot(seq) * in.Hk + h) * in.sinks * 2 * D;
+    for (int id = threadIdx.x; id < min(in.sinks, work.nk) * (D / 2); id += 256) {
+        const int key = id / (D / 2), c = 4 * (id % (D / 2));
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int p = 0; p <= work.pieces; ++p)
+            sum += *reinterpret_cast<const f32x4*>(from + p * stride + key * 2 * D + c);
+        typename Vec<E>::v4 x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(sum[i]);
+        const int64_t row = work.k0 + key;
+        store_vec(c < D ? dk + row * dk_token_stride + h * dk_head_stride + c
+                        : dv + row * dv_token_stride + h * dv_head_stride + c - D, x);
+    }
+}
+
+template <typename E, int D>
+static hipError_t launch(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
+    constexpr int BQ = 64 * LATENT_NQ<E>;
+    const int64_t G = in.H / in.Hk, N = in.num_seqs;
+    const int64_t tq = in.cu_seqlens_q ? in.total_q * G / BQ + N : (in.total_q / N * G + BQ - 1) / BQ * N;
+    // Pieces exist only where a token stands behind the first tile's window.
+    const bool pieces = in.sinks > 0 && in.total_k > (int64_t)in.window + DKV_KEYS - 1;
+    const int64_t items = in.total_k / DKV_KEYS + N + (pieces ? in.total_q / WINDOW_PIECE + N : 0);
+    if (in.total_q > 0) {
+        hipLaunchKernelGGL((window_dq_kernel<E, D>), dim3((unsigned)(tq * in.Hk)), dim3(256), 0, stream, in,
+                           (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, (int)tq);
+        if (const hipError_t e = launch_result(stream)) return e;
+    }
+    if (in.total_k == 0) return hipSuccess;
+    hipLaunchKernelGGL((window_dkv_kernel<E, D>), dim3((unsigned)(items * in.Hk)), dim3(256), 0, stream, in,
+                       (const E*)a.d_o, a.row_stats, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv,
+                       a.dv_token_stride, a.dv_head_stride, a.part, (int)items);
+    if (const hipError_t e = launch_result(stream)) return e;
+    if (!pieces) return hipSuccess;
+    hipLaunchKernelGGL((window_sinks_kernel<E, D>), grid_of(N * in.Hk), dim3(256), 0, stream, in, a.part, (E*)a.dk,
+                       a.dk_token_stride, a.dk_head_stride, (E*)a.dv, a.dv_token_stride, a.dv_head_stride);
+    return launch_result(stream);
+}
+
+hipError_t launch_window_attention_backward(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
+    if (in.dtype == KDA_DTYPE_BF16)
+        return in.d == 128 ? launch<bf16, 128>(in, a, stream) : launch<bf16, 64>(in, a, stream);
+    return in.d == 128 ? launch<float, 128>(in, a, stream) : launch<float, 64>(in, a, stream);
+}
+
+}  // namespace kda

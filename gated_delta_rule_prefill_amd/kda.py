@@ -56,6 +56,20 @@ SIGNATURES = {
                                   ctypes.c_int, _f32, _u32, _vp]),
     "kda_rotary_frequencies": (ctypes.c_int, [_i32, _f64, _f64, _i64, ctypes.POINTER(_f32),
                                               ctypes.POINTER(_f32)]),
+    "kda_window_attention": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+    "kda_window_attention_backward_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32]),
+    "kda_window_attention_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
+                                                     _sz, _vp]),
+    "kda_window_decode_workspace_bytes": (_sz, [_i32]),
+    "kda_window_decode": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i32, _i32, _i32, _i32, ctypes.c_int, _i32,
+                                         _i32, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "kda_kv_append": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i32, _i32, _i32, ctypes.c_int,
+                                     _vp, _f32, _vp, _i32, _i32, _f32, _u32, _vp, _vp]),
+    "kda_qk_norm_rotary": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, ctypes.c_int, _f32, _f32, _u32,
+                                          _vp]),
+    "kda_qk_norm_rotary_backward_workspace_bytes": (_sz, [_i32]),
+    "kda_qk_norm_rotary_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, ctypes.c_int, _f32,
+                                                   _f32, _u32, _vp, _sz, _vp]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_last_error_message": (ctypes.c_char_p, []),
     "kda_version": (_i32, []),
@@ -720,3 +734,377 @@ def rotary_frequencies(dr: int, base: float = 10000.0, factor: float = 1.0, orig
     _check(lib().kda_rotary_frequencies(dr, base, factor, original_context, f, ctypes.byref(a)),
            "kda_rotary_frequencies")
     return torch.tensor(list(f), dtype=torch.float32, device=device), float(a.value)
+
+
+# -- window attention --------------------------------------------------------------
+
+_WINDOW = struct.Struct("@3P6q2P2q7if")            # kda_window_inputs of include/kda.h
+_KV_CACHE = struct.Struct("@2P3q2P3i4x")           # kda_kv_cache
+_NORM_HEADS = struct.Struct("@P2qP2q2P2qP2qPi4x")  # kda_norm_heads
+
+
+def _int32(x, name) -> int:
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}: {x} does not fit in 32 bits")
+    return x
+
+
+def _window_inputs(q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs, scale):
+    """The packed kda_window_inputs, and (T, Tk, N, H, Hk, d)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k, v: [tokens, heads, channels]")
+    T, H, d = q.shape
+    Tk, Hk, _ = k.shape
+    dev, dt = q.device, q.dtype
+    _rows3(q, "q", (T, H, d), dt, dev)
+    _rows3(k, "k", (Tk, Hk, d), dt, dev)
+    _rows3(v, "v", (Tk, Hk, d), dt, dev)
+    cu = cuk = 0
+    if cu_seqlens is not None:
+        N = _offsets(cu_seqlens, "cu_seqlens", dev)
+        cu = cu_seqlens.data_ptr()
+        if cu_seqlens_k is not None:
+            if cu_seqlens_k is not cu_seqlens and _offsets(cu_seqlens_k, "cu_seqlens_k", dev) != N:
+                raise ValueError("cu_seqlens_k: as many sequences as cu_seqlens")
+            cuk = cu_seqlens_k.data_ptr()
+    else:
+        if cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+        N = 1 if num_seqs is None else _int32(num_seqs, "num_seqs")
+    if scale is None:
+        scale = d ** -0.5
+    packed = _WINDOW.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), _stride(q, 0), _stride(q, 1), _stride(k, 0),
+                          _stride(k, 1), _stride(v, 0), _stride(v, 1), cu, cuk, T, Tk, N, H, Hk, d, _code(q),
+                          _int32(window, "window"), _int32(sinks, "sinks"), scale)
+    return packed, (T, Tk, N, H, Hk, d)
+
+
+def window_attention(q, k, v, window: int, sinks: int = 0, cu_seqlens=None, cu_seqlens_k=None,
+                     num_seqs: Optional[int] = None, scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """Attention over a window of the last ``window`` tokens, the row's own
+    included, and the first ``sinks`` of its sequence, packed sequences
+    (``kda_window_attention``).
+
+    q: [T, H, d]; k, v: [Tk, Hk, d], H a multiple of Hk (bf16 or fp32; strided
+    views, e.g. parts of one projection).  cu_seqlens (and cu_seqlens_k where the
+    keys are more than the queries): int32 [N+1], or ``num_seqs`` equal rows.
+    scale: default d^-0.5.  Returns (o [T, H, d], lse [T, H] fp32).  Rows behind
+    the last sequence are left as they were."""
+    packed, (T, _, _, H, _, d) = _window_inputs(q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs, scale)
+    dev = q.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return window_attention(q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs, scale, out, lse)
+    torch = _torch
+    if out is None:
+        out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+    else:
+        _dense(out, "out", (T, H, d), q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _dense(lse, "lse", (T, H), torch.float32, dev)
+    st = lib().kda_window_attention(packed, out.data_ptr(), lse.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "kda_window_attention")
+    return out, lse
+
+
+def window_attention_backward_workspace_bytes(total_q: int, num_seqs: int, H: int, Hk: int, d: int, sinks: int) -> int:
+    return int(lib().kda_window_attention_backward_workspace_bytes(int(total_q), int(num_seqs), int(H), int(Hk),
+                                                                   int(d), int(sinks)))
+
+
+def window_attention_backward(q, k, v, o, lse, d_o, window: int, sinks: int = 0, cu_seqlens=None, cu_seqlens_k=None,
+                              num_seqs: Optional[int] = None, scale: Optional[float] = None, dk=None, dv=None,
+                              workspace=None, stream=None) -> dict:
+    """Gradients of ``window_attention`` (``kda_window_attention_backward``) for
+    dL/do = d_o, from the forward's o and lse: returns dq [T, H, d], dk and dv
+    [Tk, Hk, d], in the inputs' type.  dk, dv: tensors to write (strided, e.g. parts
+    of one gradient), or None to allocate both as the halves of one [Tk, 2 Hk, d]
+    tensor."""
+    packed, (T, Tk, N, H, Hk, d) = _window_inputs(q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs, scale)
+    dev, dt = q.device, q.dtype
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return window_attention_backward(q, k, v, o, lse, d_o, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs,
+                                             scale, dk, dv, workspace)
+    torch = _torch
+    _dense(o, "o", (T, H, d), dt, dev)
+    _dense(d_o, "d_o", (T, H, d), dt, dev)
+    _dense(lse, "lse", (T, H), torch.float32, dev)
+    if dk is None and dv is None:
+        dkv = torch.empty((Tk, 2 * Hk, d), dtype=dt, device=dev)
+        dk, dv = dkv[:, :Hk], dkv[:, Hk:]
+    else:
+        _require(dk is not None and dv is not None, "dk and dv: both or neither")
+        _rows3(dk, "dk", (Tk, Hk, d), dt, dev)
+        _rows3(dv, "dv", (Tk, Hk, d), dt, dev)
+    dq = torch.empty((T, H, d), dtype=dt, device=dev)
+    handle = lib()
+    if workspace is None:
+        need = handle.kda_window_attention_backward_workspace_bytes(T, N, H, Hk, d, sinks)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
+        need = workspace.numel() * workspace.element_size()
+    st = handle.kda_window_attention_backward(
+        packed, o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), _stride(dk, 0),
+        _stride(dk, 1), dv.data_ptr(), _stride(dv, 0), _stride(dv, 1), workspace.data_ptr() or None, need,
+        _raw_stream(dev))
+    if st:
+        _check(st, "kda_window_attention_backward")
+    return dict(dq=dq, dk=dk, dv=dv)
+
+
+def _kv_cache(k_cache, v_cache, block_table, seq_lens, cu_seqlens, num_seqs):
+    """The packed kda_kv_cache, and the number of sequences."""
+    int32, dev = _lib_torch().int32, k_cache.device
+    if k_cache.dim() != 4 or not (k_cache.stride(3) == 1 or k_cache.shape[3] == 1):
+        raise ValueError("k_cache: [pages, page_size, heads, channels] with a dense last axis")
+    if not (v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride() and
+            v_cache.dtype is k_cache.dtype and v_cache.device == dev):
+        raise ValueError("v_cache: shape, strides, type and device of k_cache")
+    if cu_seqlens is not None:
+        N = _offsets(cu_seqlens, "cu_seqlens", dev)
+    else:
+        N = _int32(num_seqs, "num_seqs") if num_seqs is not None else seq_lens.shape[0]
+    if not (block_table.dtype is int32 and block_table.dim() == 2 and block_table.shape[0] == N and
+            block_table.device == dev and block_table.is_contiguous()):
+        raise ValueError("block_table: contiguous int32 [N, max_pages], on the cache's device")
+    _dense(seq_lens, "seq_lens", (N,), int32, dev)
+    P, page = k_cache.shape[:2]
+    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), _stride(k_cache, 0), _stride(k_cache, 1),
+                          _stride(k_cache, 2), block_table.data_ptr(), seq_lens.data_ptr(), P, page,
+                          block_table.shape[1]), N
+
+
+def window_decode_workspace_bytes(d: int) -> int:
+    return int(lib().kda_window_decode_workspace_bytes(int(d)))
+
+
+def window_decode(q, k_cache, v_cache, block_table, seq_lens, window: int, sinks: int = 0,
+                  scale: Optional[float] = None, cu_seqlens=None, num_seqs: Optional[int] = None, out=None, lse=None,
+                  workspace=None, stream=None):
+    """``window_attention`` of new tokens over a paged cache that already holds
+    them (``kda_window_decode``).
+
+    q: [T, H, d] (strided); k_cache, v_cache: [pages, page_size, Hk, d], two views
+    of the same strides (e.g. a [pages, Hk, page_size, d] tensor with two axes
+    swapped, or halves of one tensor); block_table: int32 [N, max_pages], a page
+    outside the pool marks absent tokens; seq_lens: int32 [N] cached tokens, the new
+    ones included; cu_seqlens: int32 [N+1] offsets of the new tokens, or None for
+    T / N each.  Returns (o [T, H, d], lse [T, H] fp32)."""
+    if q.dim() != 3:
+        raise ValueError("q: [T, H, d]")
+    T, H, d = q.shape
+    cache, N = _kv_cache(k_cache, v_cache, block_table, seq_lens, cu_seqlens, num_seqs)
+    dev, dt = k_cache.device, k_cache.dtype
+    Hk = k_cache.shape[2]
+    _rows3(q, "q", (T, H, k_cache.shape[3]), dt, dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return window_decode(q, k_cache, v_cache, block_table, seq_lens, window, sinks, scale, cu_seqlens, num_seqs,
+                                 out, lse, workspace)
+    torch = _torch
+    if out is None:
+        out = torch.empty((T, H, d), dtype=dt, device=dev)
+    else:
+        _dense(out, "out", (T, H, d), dt, dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _dense(lse, "lse", (T, H), torch.float32, dev)
+    handle = lib()
+    if workspace is None:
+        need = handle.kda_window_decode_workspace_bytes(d)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
+        need = workspace.numel() * workspace.element_size()
+    st = handle.kda_window_decode(
+        cache, q.data_ptr(), _stride(q, 0), _stride(q, 1), _ptr(cu_seqlens), T, N, H, Hk, d, _code(q),
+        _int32(window, "window"), _int32(sinks, "sinks"), d ** -0.5 if scale is None else scale, out.data_ptr(),
+        lse.data_ptr(), workspace.data_ptr() or None, need, _raw_stream(dev))
+    if st:
+        _check(st, "kda_window_decode")
+    return out, lse
+
+
+def kv_append(k_cache, v_cache, k, v, block_table, seq_lens, cu_seqlens=None, num_seqs: Optional[int] = None,
+              norm_weight=None, eps: float = 1e-6, inv_freq=None, start: int = 0, interleaved: bool = False,
+              mscale: float = 1.0, k_out=None, stream=None):
+    """Write the new tokens' keys and values to a paged cache (``kda_kv_append``).
+
+    k_cache, v_cache, block_table, seq_lens, cu_seqlens: as for ``window_decode``
+    (seq_lens counts the new tokens).  k, v: [T, Hk, d] (strided, e.g. parts of one
+    projection).  norm_weight: fp32 [d] of the keys' RMS norm per head, or None for
+    no norm; inv_freq: fp32 [dr / 2], or None for no rotation, of channels [start,
+    start + dr); mscale multiplies the rotated part.  k_out: True (allocate) or a
+    dense [T, Hk, d] tensor for the keys as they are cached.  Returns k_out."""
+    if k.dim() != 3:
+        raise ValueError("k, v: [T, Hk, d]")
+    T, Hk, d = k.shape
+    cache, N = _kv_cache(k_cache, v_cache, block_table, seq_lens, cu_seqlens, num_seqs)
+    dev, dt, float32 = k_cache.device, k_cache.dtype, _torch.float32
+    shape = (T, k_cache.shape[2], k_cache.shape[3])
+    _rows3(k, "k", shape, dt, dev)
+    _rows3(v, "v", shape, dt, dev)
+    if norm_weight is not None:
+        _dense(norm_weight, "norm_weight", (d,), float32, dev)
+    dr = 0
+    if inv_freq is not None:
+        dr = 2 * inv_freq.numel()
+        _dense(inv_freq, "inv_freq", (dr // 2,), float32, dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_append(k_cache, v_cache, k, v, block_table, seq_lens, cu_seqlens, num_seqs, norm_weight, eps,
+                             inv_freq, start, interleaved, mscale, k_out)
+    if k_out is True:
+        k_out = _torch.empty((T, Hk, d), dtype=dt, device=dev)
+    elif k_out is None or k_out is False:
+        k_out = None
+    else:
+        _dense(k_out, "k_out", (T, Hk, d), dt, dev)
+    st = lib().kda_kv_append(
+        cache, k.data_ptr(), _stride(k, 0), _stride(k, 1), v.data_ptr(), _stride(v, 0), _stride(v, 1), _ptr(cu_seqlens),
+        T, N, Hk, d, _code(k), _ptr(norm_weight), eps, _ptr(inv_freq) if dr else None, _int32(start, "start"), dr, mscale,
+        KDA_ROTARY_INTERLEAVED if interleaved else 0, _ptr(k_out), _raw_stream(dev))
+    if st:
+        _check(st, "kda_kv_append")
+    return k_out
+
+
+def _norm_tensors(x, name, weight, shape, dtype, device):
+    _rows3(x, name, shape, dtype, device)
+    if weight is not None:
+        _dense(weight, f"{name}_weight", (shape[2],), _torch.float32, device)
+
+
+def _norm_rotation(q, positions, inv_freq, T, dev):
+    """Rotated channels, with the rotation's arguments checked."""
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq: both or neither")
+    if inv_freq is None:
+        return 0
+    half = inv_freq.numel()
+    _dense(inv_freq, "inv_freq", (half,), _torch.float32, dev)
+    _dense(positions, "positions", (T,), _torch.int32, dev)
+    return 2 * half
+
+
+def qk_norm_rotary(q, k=None, q_weight=None, k_weight=None, positions=None, inv_freq=None, start: int = 0,
+                   interleaved: bool = False, mscale: float = 1.0, eps: float = 1e-6, q_out=None, k_out=None,
+                   stream=None):
+    """RMS norm of every query and key head and rotary positions in one pass
+    (``kda_qk_norm_rotary``).
+
+    q: [T, H, d]; k: [T, Hk, d] or None (strided, e.g. parts of one projection);
+    q_weight, k_weight: fp32 [d], or None for ones; positions: int32 [T] and
+    inv_freq: fp32 [dr / 2], or both None for no rotation, of channels [start,
+    start + dr); mscale multiplies the rotated part.  q_out, k_out: None (allocate),
+    the input itself (in place), or a tensor that overlaps no other.  Returns
+    (q_out, k_out)."""
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q, k: [T, heads, channels]")
+    torch = _lib_torch()
+    T, H, d = q.shape
+    dev, dt = q.device, q.dtype
+    _norm_tensors(q, "q", q_weight, (T, H, d), dt, dev)
+    if k is not None:
+        _norm_tensors(k, "k", k_weight, (T, k.shape[1], d), dt, dev)
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    dr = _norm_rotation(q, positions, inv_freq, T, dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return qk_norm_rotary(q, k, q_weight, k_weight, positions, inv_freq, start, interleaved, mscale, eps, q_out,
+                                  k_out)
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=dt, device=dev)
+    elif q_out is not q:
+        _rows3(q_out, "q_out", (T, H, d), dt, dev)
+    a = _NORM_HEADS.pack(q.data_ptr(), _stride(q, 0), _stride(q, 1), q_out.data_ptr(), _stride(q_out, 0),
+                         _stride(q_out, 1), _ptr(q_weight) or 0, 0, 0, 0, 0, 0, 0, 0, H)
+    b = None
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dt, device=dev)
+        elif k_out is not k:
+            _rows3(k_out, "k_out", (T, k.shape[1], d), dt, dev)
+        b = _NORM_HEADS.pack(k.data_ptr(), _stride(k, 0), _stride(k, 1), k_out.data_ptr(), _stride(k_out, 0),
+                             _stride(k_out, 1), _ptr(k_weight) or 0, 0, 0, 0, 0, 0, 0, 0, k.shape[1])
+    st = lib().kda_qk_norm_rotary(a, b, _ptr(positions) if dr else None, _ptr(inv_freq) if dr else None, T, d,
+                                  _int32(start, "start"), dr, _code(q), eps, mscale,
+                                  KDA_ROTARY_INTERLEAVED if interleaved else 0, _raw_stream(dev))
+    if st:
+        _check(st, "kda_qk_norm_rotary")
+    return q_out, k_out
+
+
+def qk_norm_rotary_backward_workspace_bytes(d: int) -> int:
+    return int(lib().kda_qk_norm_rotary_backward_workspace_bytes(int(d)))
+
+
+def qk_norm_rotary_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, positions=None, inv_freq=None,
+                            start: int = 0, interleaved: bool = False, mscale: float = 1.0, eps: float = 1e-6, dq=None,
+                            dk=None, workspace=None, stream=None) -> dict:
+    """Gradients of ``qk_norm_rotary`` (``kda_qk_norm_rotary_backward``) from its
+    inputs q and k (k and dk_out may be None) and dL/dq_out, dL/dk_out (strided):
+    returns dq, dk in the inputs' type, and dq_weight, dk_weight (fp32 [d], None
+    without that weight).  dq, dk: None (allocate), or tensors to write: dq_out or q
+    itself (in place), or one that overlaps no other, e.g. part of the projection's
+    gradient."""
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q, k: [T, heads, channels]")
+    torch = _lib_torch()
+    T, H, d = q.shape
+    dev, dt = q.device, q.dtype
+    _norm_tensors(q, "q", q_weight, (T, H, d), dt, dev)
+    _rows3(dq_out, "dq_out", (T, H, d), dt, dev)
+    if k is not None:
+        if dk_out is None:
+            raise ValueError("dk_out: it goes with k")
+        _norm_tensors(k, "k", k_weight, (T, k.shape[1], d), dt, dev)
+        _rows3(dk_out, "dk_out", (T, k.shape[1], d), dt, dev)
+    elif k_weight is not None or dk_out is not None or dk is not None:
+        raise ValueError("k_weight, dk_out and dk need k")
+    dr = _norm_rotation(q, positions, inv_freq, T, dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return qk_norm_rotary_backward(q, k, dq_out, dk_out, q_weight, k_weight, positions, inv_freq, start,
+                                           interleaved, mscale, eps, dq, dk, workspace)
+
+    def heads(x, name, dy, dx, weight):
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=dt, device=dev)
+        else:
+            _rows3(dx, name, tuple(x.shape), dt, dev)
+        dw = torch.empty(d, dtype=torch.float32, device=dev) if weight is not None else None
+        packed = _NORM_HEADS.pack(x.data_ptr(), _stride(x, 0), _stride(x, 1), 0, 0, 0, _ptr(weight) or 0, dy.data_ptr(),
+                                  _stride(dy, 0), _stride(dy, 1), dx.data_ptr(), _stride(dx, 0), _stride(dx, 1),
+                                  _ptr(dw) or 0, x.shape[1])
+        return packed, dx, dw
+
+    a, dq, dqw = heads(q, "dq", dq_out, dq, q_weight)
+    b, dk, dkw = heads(k, "dk", dk_out, dk, k_weight) if k is not None else (None, None, None)
+    handle = lib()
+    if workspace is None:
+        need = handle.kda_qk_norm_rotary_backward_workspace_bytes(d)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
+        need = workspace.numel() * workspace.element_size()
+    st = handle.kda_qk_norm_rotary_backward(
+        a, b, _ptr(positions) if dr else None, _ptr(inv_freq) if dr else None, T, d, _int32(start, "start"), dr, _code(q),
+        eps, mscale, KDA_ROTARY_INTERLEAVED if interleaved else 0, workspace.data_ptr() or None, need, _raw_stream(dev))
+    if st:
+        _check(st, "kda_qk_norm_rotary_backward")
+    return dict(dq=dq, dk=dk, dq_weight=dqw, dk_weight=dkw)

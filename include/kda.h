@@ -497,6 +497,243 @@ kda_status kda_rotary(const void *x, int64_t x_token_stride, int64_t x_head_stri
 kda_status kda_rotary_frequencies(int32_t dr, double base, double factor,
                                   int64_t original_context, float *inv_freq, float *amplitude);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Window attention: the local-attention layer beside KDA layers.  A token sees
+ * the last `window` tokens of its sequence, itself included, and the first
+ * `sinks` of them.  H query heads share Hk key and value heads: query head h
+ * reads key head h / (H / Hk).  kda_qk_norm_rotary leaves its queries and keys,
+ * kda_window_attention takes whole prompts and training batches (with
+ * kda_window_attention_backward), kda_kv_append writes keys and values to a paged
+ * cache and kda_window_decode attends over that.  The conventions of the latent
+ * operators above (strides, offsets, empty rows) hold, with this difference:
+ *   Values     NaN and Inf propagate from the keys a row sees to its result, and
+ *              from a row to the gradients of the keys it sees, and no further:
+ *              keys that the mask hides, rows behind a sequence's end and unused
+ *              cache rows may hold anything.  How far a value that is not finite
+ *              spreads within a row that sees it (its other channels, lse) is not
+ *              specified.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Inputs of the window attention over packed sequences (all device memory):
+ *   q      [total_q, H, d]; k, v [total_k, Hk, d]: strided, so that they may be
+ *          parts of one projection
+ *   cu_seqlens_q, cu_seqlens_k   [num_seqs + 1] int32 offsets of each
+ *          sequence's queries and keys; cu_seqlens_k NULL = the queries'
+ *          offsets (then total_k = total_q); both NULL = num_seqs equal rows
+ *   window >= 1, sinks in [0, 64]: of a sequence with n queries and m keys,
+ *          query i stands at position p = i + (m - n) and sees the keys j <= p
+ *          with p - j < window or j < sinks; with m < n the first n - m queries
+ *          see none
+ *   scale  finite and > 0, multiplies q . k
+ * d in {64, 128}; Hk divides H; token strides and H * d below 2^23;
+ * total_q * H / Hk <= 2^31 - 4096; (rows / 64 + num_seqs) * Hk below 2^24, where
+ * rows is the larger of total_q * H / Hk and total_k (backward: also
+ * (total_k / 64 + total_q / 1024 + 2 num_seqs) * Hk).
+ */
+typedef struct {
+    const void *q;
+    const void *k;
+    const void *v;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    const int32_t *cu_seqlens_q;
+    const int32_t *cu_seqlens_k;
+    int64_t total_q, total_k;
+    int32_t num_seqs, H, Hk, d;
+    int32_t dtype;               /* kda_dtype */
+    int32_t window, sinks;
+    float scale;
+} kda_window_inputs;
+
+/*
+ * z_ij = scale (q_i . k_j),  o_i = sum_j softmax(z_i)_j v_j,
+ * lse_i = log sum_j exp(z_ij)  over the keys j that i sees.
+ *   o    [total_q, H, d] dtype (written; must not alias an input)
+ *   lse  [total_q, H] fp32 (written), or NULL; the backward pass needs it
+ */
+kda_status kda_window_attention(const kda_window_inputs *in, void *o, float *lse, void *stream);
+
+/*
+ * Device workspace that suffices for kda_window_attention_backward with either
+ * dtype, any window and any sinks up to these (bytes, 256-aligned; 0 for invalid
+ * sizes).  It never falls as an argument grows.
+ */
+size_t kda_window_attention_backward_workspace_bytes(int64_t total_q, int32_t num_seqs, int32_t H,
+                                                     int32_t Hk, int32_t d, int32_t sinks);
+
+/*
+ * Gradients of kda_window_attention for dL/do = d_o, from the forward's o and
+ * lse.  Deterministic; the gradients of a key head are summed over the query
+ * heads that share it in fp32.
+ *   o, d_o   [total_q, H, d] dtype; lse [total_q, H] fp32   (read)
+ *   dq       [total_q, H, d] dtype, dense (written)
+ *   dk, dv   strided like k and v, dtype (written): both may be parts of one
+ *            gradient
+ *   workspace at least kda_window_attention_backward_workspace_bytes(), or
+ *            NULL with 0 (then allocated stream-ordered on `stream`)
+ * Keys that no query sees get zero gradients.  Outputs must not alias inputs.
+ */
+kda_status kda_window_attention_backward(const kda_window_inputs *in, const void *o,
+                                         const float *lse, const void *d_o, void *dq, void *dk,
+                                         int64_t dk_token_stride, int64_t dk_head_stride, void *dv,
+                                         int64_t dv_token_stride, int64_t dv_head_stride,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A paged cache of keys and values.  Token j of sequence s is row
+ * j % page_size of page block_table[s][j / page_size]; head h of that row starts
+ * at page * page_stride + row * token_stride + h * head_stride elements from k
+ * and from v (both in the same layout: [pages, page_size, Hk, d],
+ * [pages, Hk, page_size, d], or the halves of one tensor), its d channels dense.
+ *   block_table  [num_seqs, max_pages] int32 (device).  A page outside
+ *                [0, num_pages) is neither read nor written: its tokens count as
+ *                absent, so pages that the window has left may be given back.
+ *   seq_lens     [num_seqs] int32 (device) cached tokens of every sequence, the
+ *                new ones included; clamped to [0, max_pages * page_size]
+ * num_pages * page_size and max_pages * page_size <= 2^31 - 4096.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t page_stride, token_stride, head_stride;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    int32_t num_pages, page_size, max_pages;
+} kda_kv_cache;
+
+/*
+ * Device workspace kda_window_decode needs (bytes, 256-aligned; 0 for invalid
+ * sizes): the partial results of rows whose keys are split over workgroups.  It
+ * depends on d only, so that one workspace serves batches of any size.
+ */
+size_t kda_window_decode_workspace_bytes(int32_t d);
+
+/*
+ * Window attention of one or more new tokens per sequence over a paged cache
+ * that already holds them (single-token decode, speculative tokens, a chunk of a
+ * prompt over its cached prefix).
+ *   q            [T, H, d] dtype, strided (read)
+ *   cu_seqlens   [N+1] int32 offsets of the new tokens, or NULL = T / N each
+ *                (T % N must be 0).  New token i of n stands at position
+ *                p = seq_len - n + i and sees the cached tokens j <= p with
+ *                p - j < window or j < sinks.
+ *   o            [T, H, d] dtype (written); lse [T, H] fp32 (written), or NULL
+ *   workspace    at least kda_window_decode_workspace_bytes(), or NULL with 0
+ *                (then allocated stream-ordered on `stream`).  Two calls that
+ *                may overlap need one each.
+ * d in {64, 128}; Hk divides H; window >= 1; sinks in [0, 64];
+ * T * H <= 2^31 - 4096; (T * H / Hk / 16 + N) * Hk below 2^24.  The result is
+ * deterministic: how the keys are split depends on the sizes only.
+ */
+kda_status kda_window_decode(const kda_kv_cache *cache, const void *q, int64_t q_token_stride,
+                             int64_t q_head_stride, const int32_t *cu_seqlens,
+                             int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t Hk,
+                             int32_t d, kda_dtype dtype, int32_t window, int32_t sinks, float scale,
+                             void *o, float *lse, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * Writes the new tokens' keys and values to a paged cache: token i of the n new
+ * ones of sequence s, at position p = seq_len - n + i,
+ *
+ *     key row = R(p f) (k / sqrt(mean(k^2) + eps) * norm_weight),  value row = v
+ *
+ * where R turns channels [start, start + dr) and multiplies them by `amplitude`.
+ * A token whose position is negative or whose page is outside [0, num_pages) is
+ * not written to the cache.
+ *   k, v         [T, Hk, d] dtype, strided (read)
+ *   cu_seqlens, total_tokens, num_seqs: as for kda_window_decode
+ *   norm_weight  [d] fp32, or NULL: keys are not normalised
+ *   eps          >= 0, finite
+ *   inv_freq     [dr/2] fp32 radians per position, or NULL with dr = 0: keys are
+ *                not turned
+ *   flags        KDA_ROTARY_INTERLEAVED or 0
+ *   k_out        [T, Hk, d] dtype, dense, or NULL: the key rows, for the
+ *                tokens' own attention (written for every token of a sequence,
+ *                whether or not it has a cache row)
+ * d in {64, 128}, dr even, start + dr <= d.
+ */
+kda_status kda_kv_append(const kda_kv_cache *cache, const void *k, int64_t k_token_stride,
+                         int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                         int64_t v_head_stride, const int32_t *cu_seqlens, int64_t total_tokens,
+                         int32_t num_seqs, int32_t Hk, int32_t d, kda_dtype dtype,
+                         const float *norm_weight, float eps, const float *inv_freq, int32_t start,
+                         int32_t dr, float amplitude, uint32_t flags, void *k_out, void *stream);
+
+/*
+ * RMS norm of every head and rotary positions in one pass, for the queries and
+ * the keys of the same tokens:
+ *
+ *     n = x / sqrt(mean(x^2) + eps),   y = R(p f) (n * weight)
+ *
+ * R turns the pairs of channels [start, start + dr) (KDA_ROTARY_INTERLEAVED as for
+ * kda_rotary) and multiplies them by `amplitude`.
+ *   x       [T, H, d] dtype, strided (read)
+ *   y       [T, H, d] dtype, strided (written).  y = x with x's strides works in
+ *           place; any other overlap, and one of the queries' with the keys'
+ *           tensors, is not allowed.
+ *   weight  [d] fp32, or NULL = ones
+ *   dy      [T, H, d] dtype, strided: dL/dy (backward, read)
+ *   dx      [T, H, d] dtype, strided: dL/dx (backward, written).  dx = dy, or
+ *           dx = x, with the same strides works in place.
+ *   dweight [d] fp32: dL/dweight, summed over tokens and heads (backward,
+ *           written), or NULL
+ * The forward call looks at x, y and weight only, the backward call at all but y.
+ */
+typedef struct {
+    const void *x;
+    int64_t x_token_stride, x_head_stride;
+    void *y;
+    int64_t y_token_stride, y_head_stride;
+    const float *weight;
+    const void *dy;
+    int64_t dy_token_stride, dy_head_stride;
+    void *dx;
+    int64_t dx_token_stride, dx_head_stride;
+    float *dweight;
+    int32_t H;
+} kda_norm_heads;
+
+/*
+ *   q, k       the two kinds of heads; k may be NULL
+ *   positions  [T] int32, inv_freq [dr/2] fp32 radians per position; both NULL
+ *              with dr = 0: no rotation
+ * d <= 256, even; dr even, 0 <= start, start + dr <= d.  Pointers and strides of
+ * the heads need the alignment of one element only (wider accesses are used
+ * where they allow it); positions, inv_freq and weights 16 bytes.
+ */
+kda_status kda_qk_norm_rotary(const kda_norm_heads *q, const kda_norm_heads *k,
+                              const int32_t *positions, const float *inv_freq, int64_t total_tokens,
+                              int32_t d, int32_t start, int32_t dr, kda_dtype dtype, float eps,
+                              float amplitude, uint32_t flags, void *stream);
+
+/*
+ * Device workspace kda_qk_norm_rotary_backward needs (bytes, 256-aligned): the
+ * workgroups' parts of the weights' gradients.  It depends on d only; 0 for an
+ * invalid d.
+ */
+size_t kda_qk_norm_rotary_backward_workspace_bytes(int32_t d);
+
+/*
+ * Gradients of kda_qk_norm_rotary, from its inputs x and dy = dL/dy:
+ *
+ *     g = R(p f)^T dy,  h = g * weight,  r = 1 / sqrt(mean(x^2) + eps),  n = r x
+ *     dx = r (h - n mean(h n)),   dweight = sum over tokens and heads of g * n
+ *
+ * Deterministic.  Without total_tokens the dweight are zero.
+ *   workspace  at least kda_qk_norm_rotary_backward_workspace_bytes(), or NULL
+ *              with 0 (then allocated stream-ordered on `stream`)
+ */
+kda_status kda_qk_norm_rotary_backward(const kda_norm_heads *q, const kda_norm_heads *k,
+                                       const int32_t *positions, const float *inv_freq,
+                                       int64_t total_tokens, int32_t d, int32_t start, int32_t dr,
+                                       kda_dtype dtype, float eps, float amplitude, uint32_t flags,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *kda_status_string(kda_status status);
 
