@@ -82,8 +82,15 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
     const int last_lo = kr.last(w0), last_hi = kr.last(w1), first_lo = kr.first(w0), first_hi = kr.first(w1);
 
     Stage<E, D, BN, 256> sk, sv;
-    auto load = [&](int t) {
-        if constexpr (PAGED) {
+    // Tiles that all rows see whole go straight to LDS; the others through registers,
+    // where rows that are not finite are found and taken out.
+    Direct<E, D, BN, 256> direct_k, direct_v;
+    auto load = [&](int t, auto hides, E* to) {
+        if constexpr (!hides) {
+            const int64_t key = (int64_t)t * BN + kr.shift;
+            direct_k.fetch(wave, kp + key * in.k_token_stride, to);
+            direct_v.fetch(wave, vp + key * in.v_token_stride, to + BN * D);
+        } else if constexpr (PAGED) {
             auto row = [&](const E* base) {
                 return [&, base](int r) {
                     const int64_t at = place[t & 3][r];
@@ -93,21 +100,19 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
             sk.template load<false>(tid, row(kp));
             sv.template load<false>(tid, row(vp));
         } else {
-            auto row = [&](const E* base, int64_t stride) {
-                return [&, base, stride](int r) {
-                    const int n = t * BN + r;
-                    return n < kr.total ? base + kr.position(n) * stride : zero_row<E>();
-                };
-            };
-            sk.template load<false>(tid, row(kp, in.k_token_stride));
-            sv.template load<false>(tid, row(vp, in.v_token_stride));
+            load_keys(sk, tid, kr, t * BN, kp, in.k_token_stride);
+            load_keys(sv, tid, kr, t * BN, vp, in.v_token_stride);
         }
     };
-    auto store = [&](E* to) {
-        // a hidden key's weight is 0, and 0 times NaN or Inf is NaN
-        move_bad_rows(tid, sv, sk);
-        sk.store(tid, to);
-        sv.store(tid, to + BN * D);
+    auto store = [&](auto hides, E* to) {
+        if constexpr (hides) {
+            // a hidden key's weight is 0, and 0 times NaN or Inf is NaN
+            move_bad_rows(tid, sv, sk);
+            sk.store(tid, to);
+            sv.store(tid, to + BN * D);
+        } else {
+            landed();
+        }
     };
     // PAGED: the cache row of key tid of tile t (tid < BN)
     auto look_up = [&](int t) -> int64_t {
@@ -143,19 +148,21 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
         for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     if (nt > 0) {
-        load(0);
-        store(even);
+        load(0, Int<1>(), even);
+        store(Int<1>(), even);
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]);
-    auto step = [&](int t, const E* K, E* next) {
+    // Tile t of the keys; hides: some row does not see all of the keys of it or of
+    // the next one.
+    auto step = [&](int t, auto hides, const E* K, E* next) {
         k_rows.keep(), v_cols.keep();
         const E* V = K + BN * D;
         const int n0 = t * BN;
-        if (t + 1 < nt) load(t + 1);
+        if (t + 1 < nt) load(t + 1, hides, next);
         if constexpr (PAGED)
             if (tid < BN) {
                 keep(t + 2, next_place);
@@ -174,7 +181,7 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
             constexpr int E0 = TT * KS;
             v8 p[NQ][TT / 2];
             auto take_weights = [&]() {
-                if (!kr.whole(n0, n0 + BN, last_lo, first_hi)) {
+                if (hides && !kr.whole(n0, n0 + BN, last_lo, first_hi)) {
 #pragma unroll
                     for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -256,10 +263,24 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
                     }
                 });
         }
-        if (t + 1 < nt) store(next);
+        if (t + 1 < nt) store(hides, next);
         __syncthreads();
     };
-    for (int t = 0; t < nt; ++t) step(t, t & 1 ? odd : even, t & 1 ? even : odd);
+    int td = 0, te = 0;   // the tiles [td, te) are seen whole by all rows
+    if constexpr (!PAGED) {
+        kr.whole_tiles(BN, td, te);
+        direct_k.rows(tid, in.k_token_stride, BN);
+        direct_v.rows(tid, in.v_token_stride, BN);
+    }
+    int t = 0;
+    if (!PAGED && td + 2 < te) {
+        for (; t < td || (t & 1); ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
+        for (; t + 2 < te; t += 2) {
+            step(t, Int<0>(), even, odd);
+            step(t + 1, Int<0>(), odd, even);
+        }
+    }
+    for (; t < nt; ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;

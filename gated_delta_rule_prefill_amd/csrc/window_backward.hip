@@ -87,20 +87,27 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     const int last_lo = kr.last(w0), last_hi = kr.last(w1), first_lo = kr.first(w0), first_hi = kr.first(w1);
 
     Stage<E, D, BN, 256> sk, sv;
-    auto load = [&](int t) {
-        auto row = [&](const E* base, int64_t stride) {
-            return [&, base, stride](int r) {
-                const int n = t * BN + r;
-                return n < kr.total ? base + kr.position(n) * stride : zero_row<E>();
-            };
-        };
-        sk.template load<false>(tid, row(kp, in.k_token_stride));
-        sv.template load<false>(tid, row(vp, in.v_token_stride));
+    // Tiles that all rows see whole go straight to LDS; the others through registers,
+    // where rows that are not finite are found and taken out.
+    Direct<E, D, BN, 256> direct_k, direct_v;
+    auto load = [&](int t, auto hides, E* to) {
+        if constexpr (!hides) {
+            const int64_t key = (int64_t)t * BN + kr.shift;
+            direct_k.fetch(wave, kp + key * in.k_token_stride, to);
+            direct_v.fetch(wave, vp + key * in.v_token_stride, to + BN * D);
+            return;
+        }
+        load_keys(sk, tid, kr, t * BN, kp, in.k_token_stride);
+        load_keys(sv, tid, kr, t * BN, vp, in.v_token_stride);
     };
-    auto store = [&](E* to) {
-        move_bad_rows(tid, sk, sv);
-        sk.store(tid, to);
-        sv.store(tid, to + BN * D);
+    auto store = [&](auto hides, E* to) {
+        if constexpr (hides) {
+            move_bad_rows(tid, sk, sv);
+            sk.store(tid, to);
+            sv.store(tid, to + BN * D);
+        } else {
+            landed();
+        }
     };
     RowReader<E, D> rows_of(lane);
     ColReader<E, D, D / 16> k_cols(lane);
@@ -111,19 +118,21 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (nt > 0) {
-        load(0);
-        store(even);
+        load(0, Int<1>(), even);
+        store(Int<1>(), even);
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]);
-    auto step = [&](int t, const E* K, E* next) {
+    // Tile t of the keys; hides: some row does not see all of the keys of it or of
+    // the next one.
+    auto step = [&](int t, auto hides, const E* K, E* next) {
         rows_of.keep(), k_cols.keep();
         const E* V = K + BN * D;
         const int n0 = t * BN;
-        if (t + 1 < nt) load(t + 1);
+        if (t + 1 < nt) load(t + 1, hides, next);
         if (wrow < rows && n0 <= last_hi && (n0 < kr.ns || n0 + BN > first_lo)) {
             f32x4 s[NQ][TT], dp[NQ][TT];
             v8 x[PD + 1];
@@ -165,7 +174,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                         }
                     } else {
                         if (e == E1) {
-                            if (!kr.whole(n0, n0 + BN, last_lo, first_hi)) {   // weights of hidden keys
+                            if (hides && !kr.whole(n0, n0 + BN, last_lo, first_hi)) {   // weights of hidden keys
 #pragma unroll
                                 for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -195,10 +204,22 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                     }
                 });
         }
-        if (t + 1 < nt) store(next);
+        if (t + 1 < nt) store(hides, next);
         __syncthreads();
     };
-    for (int t = 0; t < nt; ++t) step(t, t & 1 ? odd : even, t & 1 ? even : odd);
+    int td, te;   // the tiles [td, te) are seen whole by all rows
+    kr.whole_tiles(BN, td, te);
+    direct_k.rows(tid, in.k_token_stride, BN);
+    direct_v.rows(tid, in.v_token_stride, BN);
+    int t = 0;
+    if (td + 2 < te) {
+        for (; t < td || (t & 1); ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
+        for (; t + 2 < te; t += 2) {
+            step(t, Int<0>(), even, odd);
+            step(t + 1, Int<0>(), odd, even);
+        }
+    }
+    for (; t < nt; ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;
@@ -298,35 +319,50 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     typedef Stage<E, D, BQ, 256> S;
     S sq, sg;
     static_assert(S::P == 1 && S::TPR == 8, "a row per 8 threads");
-    // lse and delta of a row travel with the row's own first thread, which knows
-    // whether the row is finite
+    // lse and delta of a row travel with one thread: where all keys are seen the first
+    // BQ threads (few and whole lines to load), else the row's own first thread, which
+    // knows whether the row is finite.
     float next_lse = 0.f, next_delta = 0.f;
-    auto load = [&](int head, int t) {
-        const int left = te - ta - t * BQ;
-        sq.load_rows(tid, qp + head * in.q_head_stride + (int64_t)t * BQ * in.q_token_stride, in.q_token_stride, left);
-        sg.load_rows(tid, gp + (int64_t)head * D + (int64_t)t * BQ * in.H * D, (int64_t)in.H * D, left);
-        if (tid % S::TPR == 0) {   // rows behind the last weigh nothing: lse = inf
-            const int i = tid / S::TPR;
+    auto carried = [&](bool hides) { return !hides ? tid : tid % S::TPR == 0 ? tid / S::TPR : BQ; };
+    // Tiles of rows that all see all of the keys go straight to LDS; the others
+    // through registers, where rows that are not finite are found and taken out.
+    Direct<E, D, BQ, 256> direct_q, direct_g;
+    auto load = [&](int head, int t, auto hides, E* to) {
+        const int left = te - ta - t * BQ, i = carried(hides);
+        const E* qt = qp + head * in.q_head_stride + (int64_t)t * BQ * in.q_token_stride;
+        const E* gt = gp + (int64_t)head * D + (int64_t)t * BQ * in.H * D;
+        if (i < BQ) {   // rows behind the last weigh nothing: lse = inf
             const float* at = sp + 2 * ((int64_t)head * in.total_q + t * BQ + min(i, left - 1));
             next_lse = i < left ? at[0] : __builtin_inff();
             next_delta = i < left ? at[1] : 0.f;
         }
+        if constexpr (hides) {
+            sq.load_rows(tid, qt, in.q_token_stride, left);
+            sg.load_rows(tid, gt, (int64_t)in.H * D, left);
+        } else {
+            direct_q.fetch(wave, qt, to);
+            direct_g.fetch(wave, gt, to + BQ * D);
+        }
     };
-    auto store = [&](int u, E* to) {
-        const bool bad_delta = tid % S::TPR == 0 && !(__builtin_fabsf(next_delta) < __builtin_inff());
-        const bool bad_q = sq.bad_row(tid, 0), bad_g = sg.bad_row(tid, 0, bad_delta);
-        if (bad_q || bad_g) {   // as move_bad_rows: lse becomes NaN
-            sq.fill_row(0, 0u);
-            sg.fill_row(0, 0u);
-            next_lse = __builtin_nanf("");
-            next_delta = 0.f;
+    auto store = [&](int u, auto hides, E* to) {
+        const int i = carried(hides);
+        if constexpr (hides) {
+            const bool bad_delta = i < BQ && !(__builtin_fabsf(next_delta) < __builtin_inff());
+            const bool bad_q = sq.bad_row(tid, 0), bad_g = sg.bad_row(tid, 0, bad_delta);
+            if (bad_q || bad_g) {   // as move_bad_rows: lse becomes NaN
+                sq.fill_row(0, 0u);
+                sg.fill_row(0, 0u);
+                next_lse = __builtin_nanf("");
+                next_delta = 0.f;
+            }
+            sq.store(tid, to);
+            sg.store(tid, to + BQ * D);
         }
-        sq.store(tid, to);
-        sg.store(tid, to + BQ * D);
-        if (tid % S::TPR == 0) {
-            srow[u & 1][tid / S::TPR] = next_lse;
-            srow[u & 1][BQ + tid / S::TPR] = next_delta;
+        if (i < BQ) {
+            srow[u & 1][i] = next_lse;
+            srow[u & 1][BQ + i] = next_delta;
         }
+        if constexpr (!hides) landed();
     };
     RowReader<E, D> rows_of(lane);
     ColReader<E, D, D / 16> cols_of(lane);
@@ -334,20 +370,21 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) ak[c] = av[c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (nu > 0) {
-        load(0, 0);
-        store(0, even);
+        load(0, 0, Int<1>(), even);
+        store(0, Int<1>(), even);
     }
     __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) arrived(k[ks]), arrived(v[ks]);
     // Tile t of a head's tokens, number u of all; the next one is nt of nhead.
-    auto step = [&](int u, int t, int nhead, int nt, const E* Q, E* next) {
+    // hides: some row of it or of the next does not see all of the keys.
+    auto step = [&](int u, int t, int nhead, int nt, auto hides, const E* Q, E* next) {
         rows_of.keep(), cols_of.keep();
         const E* Gt = Q + BQ * D;
         const float* R = srow[u & 1];
         const int p0 = ta + t * BQ + off, p1 = min(p0 + BQ, te + off) - 1;   // positions of the tile's rows
-        if (u + 1 < nu) load(nhead, nt);
-        if (p1 >= wkey && (p0 - (wkey + 15) < W || wkey < in.sinks)) {
+        if (u + 1 < nu) load(nhead, nt, hides, next);
+        if (!hides || (p1 >= wkey && (p0 - (wkey + 15) < W || wkey < in.sinks))) {
             f32x4 s[2], dp[2];
             v8 x[PD + 1];
 #pragma unroll
@@ -383,7 +420,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
                         constexpr int c = e - E1;
                         if (c == 0) {
                             // weights of hidden keys
-                            if (p0 < wkey + 15 || (p1 - wkey >= W && wkey + 15 >= in.sinks)) {
+                            if (hides && (p0 < wkey + 15 || (p1 - wkey >= W && wkey + 15 >= in.sinks))) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     const int p = p0 + 16 * (i / 4) + 4 * g + i % 4;
@@ -404,15 +441,29 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
                     }
                 });
         }
-        if (u + 1 < nu) store(u + 1, next);
+        if (u + 1 < nu) store(u + 1, hides, next);
         __syncthreads();
     };
-    int head = 0, t = 0;
-    for (int u = 0; u < nu; ++u) {
-        const int nt = t + 1 < per ? t + 1 : 0, nhead = nt ? head : head + 1;
-        step(u, t, nhead, nt, u & 1 ? odd : even, u & 1 ? even : odd);
-        t = nt;
-        head = nhead;
+    // A head's tiles [td, tw): 32 rows that all see all of the workgroup's keys.
+    const int td = max(0, key0 + BK - 1 - (ta + off) + BQ - 1) / BQ;
+    const int tw = min((te - ta) / BQ, max(0, key0 + W - (ta + off)) / BQ);
+    direct_q.rows(tid, in.q_token_stride, BQ);
+    direct_g.rows(tid, (int64_t)in.H * D, BQ);
+    for (int head = 0, u = 0; head < G; ++head) {
+        int t = 0;
+        auto masked = [&]() {
+            const int nt = t + 1 < per ? t + 1 : 0;
+            step(u, t, nt ? head : head + 1, nt, Int<1>(), u & 1 ? odd : even, u & 1 ? even : odd);
+            ++u, ++t;
+        };
+        if (td + 2 < tw) {
+            while (t < td || (u & 1)) masked();
+            for (; t + 2 < tw; t += 2, u += 2) {
+                step(u, t, head, t + 1, Int<0>(), even, odd);
+                step(u + 1, t + 1, head, t + 2, Int<0>(), odd, even);
+            }
+        }
+        while (t < per) masked();
     }
     if (key >= nk) return;
     const bool sink = key < in.sinks && work.pieces > 0 && key0 == 0;

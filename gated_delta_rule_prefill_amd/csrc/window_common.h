@@ -35,11 +35,36 @@ struct KeyRange {
     __device__ __forceinline__ int last(int p) const { return p - shift; }
     __device__ __forceinline__ int first(int p) const { return p - W + 1 - shift; }
     __device__ __forceinline__ int position(int n) const { return n < ns ? n : n + shift; }
+    // The tiles [a, b) of n keys that all rows see whole and whose keys lie in one run.
+    __device__ __forceinline__ void whole_tiles(int n, int& a, int& b) const {
+        a = shift == 0 && first_max <= ns ? 0 : (max(first_max, ns) + n - 1) / n;
+        b = (last_min + 1) / n;
+    }
     // Whether rows between these two see all of the numbers [a, b).
     __device__ __forceinline__ bool whole(int a, int b, int last_of_first, int first_of_last) const {
         return b - 1 <= last_of_first && (a >= first_of_last || b <= ns);
     }
 };
+
+// Tile t of the keys (rows `stride` elements apart from base, the sequence's first)
+// into registers: sinks, then the run behind them, zeros behind the last key.  An
+// offset within the tile fits in 32 bits, as strides are below 2^23.
+template <typename S, typename E>
+__device__ __forceinline__ void load_keys(S& st, int tid, const KeyRange& kr, int n0, const E* base, int64_t stride) {
+    const E *sinks = base + n0 * stride, *run = base + ((int64_t)n0 + kr.shift) * stride;
+    const int left = kr.total - n0, split = kr.ns - n0;
+#pragma unroll
+    for (int p = 0; p < S::P; ++p) {
+        const int r = tid / S::TPR + S::PASS * p;
+        const uint32_t at = (uint32_t)min(r, left - 1) * (uint32_t)(stride * sizeof(E)) + 16 * (tid % S::TPR);
+        const char* row = reinterpret_cast<const char*>(min(r, left - 1) < split ? sinks : run);
+#pragma unroll
+        for (int s = 0; s < S::S; ++s) {
+            st.r[p][s] = *reinterpret_cast<const u32x4*>(row + at + 16 * S::TPR * s);
+            if (r >= left) st.r[p][s] = u32x4{0, 0, 0, 0};
+        }
+    }
+}
 
 // Cached tokens of a sequence.
 __device__ __forceinline__ int cached_tokens(const kda_kv_cache& c, int seq) {
