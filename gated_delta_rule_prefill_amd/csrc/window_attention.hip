@@ -55,6 +55,8 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
     auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
     const KeyRange kr(uniform(token(tile * BQ)), uniform(token(tile * BQ + BQ - 1)), off, in.window, in.sinks, nk);
     const int nt = (kr.total + BN - 1) / BN;
+    int td = 0, te = 0;   // the tiles [td, te) are seen whole by all rows; tile t lies in even or odd by its distance from td
+    if constexpr (!PAGED) kr.whole_tiles(BN, td, te);
 
     const E *kp, *vp;
     if constexpr (PAGED) {
@@ -148,8 +150,9 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
         for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     if (nt > 0) {
-        load(0, Int<1>(), even);
-        store(Int<1>(), even);
+        E* to = td & 1 ? odd : even;
+        load(0, Int<1>(), to);
+        store(Int<1>(), to);
     }
     __syncthreads();
 #pragma unroll
@@ -266,21 +269,21 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
         if (t + 1 < nt) store(hides, next);
         __syncthreads();
     };
-    int td = 0, te = 0;   // the tiles [td, te) are seen whole by all rows
+    auto masked = [&](int t) __attribute__((always_inline)) { step(t, Int<1>(), (t - td) & 1 ? odd : even, (t - td) & 1 ? even : odd); };
+    int t = 0;
     if constexpr (!PAGED) {
-        kr.whole_tiles(BN, td, te);
         direct_k.rows(tid, in.k_token_stride, BN);
         direct_v.rows(tid, in.v_token_stride, BN);
-    }
-    int t = 0;
-    if (!PAGED && td + 2 < te) {
-        for (; t < td || (t & 1); ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
-        for (; t + 2 < te; t += 2) {
-            step(t, Int<0>(), even, odd);
-            step(t + 1, Int<0>(), odd, even);
+        if (td + 1 < te) {
+            for (; t < td; ++t) masked(t);
+            for (; t + 2 < te; t += 2) {
+                step(t, Int<0>(), even, odd);
+                step(t + 1, Int<0>(), odd, even);
+            }
+            if (t + 1 < te) step(t++, Int<0>(), even, odd);
         }
     }
-    for (; t < nt; ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
+    for (; t < nt; ++t) masked(t);
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;

@@ -53,6 +53,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
     const KeyRange kr(uniform(token(tile * BQ)), uniform(token(tile * BQ + BQ - 1)), off, in.window, in.sinks, nk);
     const int nt = (kr.total + BN - 1) / BN;
+    int td, te;   // the tiles [td, te) are seen whole by all rows; tile t lies in even or odd by its distance from td
+    kr.whole_tiles(BN, td, te);
 
     const E* kp = (const E*)in.k + (int64_t)k0 * in.k_token_stride + h * in.k_head_stride;
     const E* vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
@@ -118,8 +120,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (nt > 0) {
-        load(0, Int<1>(), even);
-        store(Int<1>(), even);
+        E* to = td & 1 ? odd : even;
+        load(0, Int<1>(), to);
+        store(Int<1>(), to);
     }
     __syncthreads();
 #pragma unroll
@@ -207,19 +210,19 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
         if (t + 1 < nt) store(hides, next);
         __syncthreads();
     };
-    int td, te;   // the tiles [td, te) are seen whole by all rows
-    kr.whole_tiles(BN, td, te);
     direct_k.rows(tid, in.k_token_stride, BN);
     direct_v.rows(tid, in.v_token_stride, BN);
+    auto masked = [&](int t) __attribute__((always_inline)) { step(t, Int<1>(), (t - td) & 1 ? odd : even, (t - td) & 1 ? even : odd); };
     int t = 0;
-    if (td + 2 < te) {
-        for (; t < td || (t & 1); ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
+    if (td + 1 < te) {
+        for (; t < td; ++t) masked(t);
         for (; t + 2 < te; t += 2) {
             step(t, Int<0>(), even, odd);
             step(t + 1, Int<0>(), odd, even);
         }
+        if (t + 1 < te) step(t++, Int<0>(), even, odd);
     }
-    for (; t < nt; ++t) step(t, Int<1>(), t & 1 ? odd : even, t & 1 ? even : odd);
+    for (; t < nt; ++t) masked(t);
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;
@@ -451,17 +454,20 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     direct_g.rows(tid, (int64_t)in.H * D, BQ);
     for (int head = 0, u = 0; head < G; ++head) {
         int t = 0;
-        auto masked = [&]() {
+        auto masked = [&]() __attribute__((always_inline)) {
             const int nt = t + 1 < per ? t + 1 : 0;
             step(u, t, nt ? head : head + 1, nt, Int<1>(), u & 1 ? odd : even, u & 1 ? even : odd);
             ++u, ++t;
         };
-        if (td + 2 < tw) {
-            while (t < td || (u & 1)) masked();
+        auto whole = [&](int n, const E* Q, E* next) __attribute__((always_inline)) { step(u + n, t + n, head, t + n + 1, Int<0>(), Q, next); };
+        if (td + 1 < tw) {
+            while (t < td) masked();
+            if (u & 1) whole(0, odd, even), ++u, ++t;
             for (; t + 2 < tw; t += 2, u += 2) {
-                step(u, t, head, t + 1, Int<0>(), even, odd);
-                step(u + 1, t + 1, head, t + 2, Int<0>(), odd, even);
+                whole(0, even, odd);
+                whole(1, odd, even);
             }
+            if (t + 1 < tw) whole(0, even, odd), ++u, ++t;
         }
         while (t < per) masked();
     }
