@@ -67,16 +67,15 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
         vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
     }
 
-    // this lane's query rows, and the keys each sees
+    // this lane's query rows
     v8 q[NQ][KS];
-    int last[NQ], first[NQ];
+    int first[NQ];   // the first key number behind the sinks that the row sees
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = min(wrow + 16 * j + col, rows - 1), i = token(r);
         const E* row = (const E*)in.q + (int64_t)(q0 + i) * in.q_token_stride + (h * G + r - i * G) * in.q_head_stride;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) q[j][ks] = row_frag_global(row, ks, lane);
-        last[j] = kr.last(i + off);
         first[j] = kr.first(i + off);
     }
     // of the wave's rows
@@ -190,10 +189,8 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
 #pragma unroll
                         for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int n = n0 + 16 * tt + 4 * g + i;
-                                if (n > last[j] || (n < first[j] && n >= kr.ns)) s[j][tt][i] = neg_inf();
-                            }
+                            for (int i = 0; i < 4; ++i)
+                                if (kr.hides(n0 + 16 * tt + 4 * g + i, first[j], n0 < kr.ns)) s[j][tt][i] = neg_inf();
                 }
                 if constexpr (PAGED)
                     if (uniform(gaps[t & 3])) {

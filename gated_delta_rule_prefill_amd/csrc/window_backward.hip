@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     const E* vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
 
     v8 q[NQ][KS];
-    int last[NQ], first[NQ];
+    int first[NQ];   // the first key number behind the sinks that the row sees
     float lse2[NQ], dl[NQ], exact[NQ];   // delta from the rounded o, and from this kernel's own weights
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
@@ -82,7 +82,6 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
         dl[j] = group_sum(sum);
         if (lse2[j] == neg_inf()) dl[j] = 0.f;
         exact[j] = 0.f;
-        last[j] = kr.last(i + off);
         first[j] = kr.first(i + off);
     }
     const int w0 = uniform(token(wrow)) + off, w1 = uniform(token(wrow + 16 * NQ - 1)) + off;
@@ -183,11 +182,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 #pragma unroll
                                     for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            const int n = n0 + 16 * tt + 4 * g + i;
-                                            if (n > last[j] || (n < first[j] && n >= kr.ns))
+                                        for (int i = 0; i < 4; ++i)
+                                            if (kr.hides(n0 + 16 * tt + 4 * g + i, first[j], n0 < kr.ns))
                                                 s[j][tt][i] = 0.f, dp[j][tt][i] = 0.f;
-                                        }
                             }
 #pragma unroll
                             for (int j = 0; j < NQ; ++j) {

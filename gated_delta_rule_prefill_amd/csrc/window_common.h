@@ -35,6 +35,12 @@ struct KeyRange {
     __device__ __forceinline__ int last(int p) const { return p - shift; }
     __device__ __forceinline__ int first(int p) const { return p - W + 1 - shift; }
     __device__ __forceinline__ int position(int n) const { return n < ns ? n : n + shift; }
+    // Whether the row whose first key number is `first` does not see number n: one
+    // comparison for the window, where there are no sinks (some: n may be one).
+    __device__ __forceinline__ bool hides(int n, int first, bool some) const {
+        const bool outside = (unsigned)(n - first) >= (unsigned)W;
+        return some ? outside && (n >= ns || n > first + W - 1) : outside;
+    }
     // The tiles [a, b) of n keys that all rows see whole and whose keys lie in one run.
     __device__ __forceinline__ void whole_tiles(int n, int& a, int& b) const {
         a = shift == 0 && first_max <= ns ? 0 : (max(first_max, ns) + n - 1) / n;

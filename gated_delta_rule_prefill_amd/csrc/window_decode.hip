@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_decode_ker
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) q[ks] = row_frag_global(row, ks, lane);
     }
-    const int last = kr.last(i + off), first = kr.first(i + off);
+    const int first = kr.first(i + off);
 
     v8 k[2][KS];
     u32x4 v[VI];
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_decode_ker
                 for (int e = 0; e < 4; ++e) {
                     const int x = 16 * tt + 4 * g + e, n = n0 + x;
                     if (bad >> x & 1) s[tt][e] = __builtin_nanf("");
-                    if (n > last || (n < first && n >= kr.ns) || !(there >> x & 1)) s[tt][e] = neg_inf();
+                    if (kr.hides(n, first, n0 < kr.ns) || !(there >> x & 1)) s[tt][e] = neg_inf();
                 }
         }
         float top = neg_inf();
