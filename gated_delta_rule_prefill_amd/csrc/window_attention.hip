@@ -55,8 +55,8 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
     auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
     const KeyRange kr(uniform(token(tile * BQ)), uniform(token(tile * BQ + BQ - 1)), off, in.window, in.sinks, nk);
     const int nt = (kr.total + BN - 1) / BN;
-    int td = 0, te = 0;   // the tiles [td, te) are seen whole by all rows; tile t lies in even or odd by its distance from td
-    if constexpr (!PAGED) kr.whole_tiles(BN, td, te);
+    int td, te;   // the tiles [td, te) are seen whole by all rows
+    kr.whole_tiles(BN, td, te);
 
     const E *kp, *vp;
     if constexpr (PAGED) {
@@ -82,38 +82,35 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
     const int w0 = uniform(token(wrow)) + off, w1 = uniform(token(wrow + 16 * NQ - 1)) + off;
     const int last_lo = kr.last(w0), last_hi = kr.last(w1), first_lo = kr.first(w0), first_hi = kr.first(w1);
 
-    Stage<E, D, BN, 256> sk, sv;
-    // Tiles that all rows see whole go straight to LDS; the others through registers,
-    // where rows that are not finite are found and taken out.
-    Direct<E, D, BN, 256> direct_k, direct_v;
-    auto load = [&](int t, auto hides, E* to) {
-        if constexpr (!hides) {
-            const int64_t key = (int64_t)t * BN + kr.shift;
-            direct_k.fetch(wave, kp + key * in.k_token_stride, to);
-            direct_v.fetch(wave, vp + key * in.v_token_stride, to + BN * D);
-        } else if constexpr (PAGED) {
+    // Keys that some row does not see weigh 0, and 0 times NaN or Inf is NaN: in the
+    // tiles that are not seen whole such rows are found and taken out.
+    const Tiles<E, D, BN, 256> k_tiles(tid, in.k_token_stride), v_tiles(tid, in.v_token_stride);   // PAGED: strides of 0
+    auto load = [&](int t, E* to) {
+        if constexpr (PAGED) {
             auto row = [&](const E* base) {
                 return [&, base](int r) {
                     const int64_t at = place[t & 3][r];
                     return at < 0 ? zero_row<E>() : base + at;
                 };
             };
-            sk.template load<false>(tid, row(kp));
-            sv.template load<false>(tid, row(vp));
+            k_tiles.fetch_rows(wave, row(kp), to);
+            v_tiles.fetch_rows(wave, row(vp), to + BN * D);
         } else {
-            load_keys(sk, tid, kr, t * BN, kp, in.k_token_stride);
-            load_keys(sv, tid, kr, t * BN, vp, in.v_token_stride);
+            const int64_t n0 = (int64_t)t * BN, key = n0 + kr.shift;
+            const E *kt = kp + key * in.k_token_stride, *vt = vp + key * in.v_token_stride;
+            if (t >= td && t < te) {
+                k_tiles.fetch(wave, kt, to);
+                v_tiles.fetch(wave, vt, to + BN * D);
+            } else {
+                const int split = kr.ns - (int)n0, left = kr.total - (int)n0;
+                k_tiles.fetch_part(wave, kt, kp + n0 * in.k_token_stride, split, left, to);
+                v_tiles.fetch_part(wave, vt, vp + n0 * in.v_token_stride, split, left, to + BN * D);
+            }
         }
     };
-    auto store = [&](auto hides, E* to) {
-        if constexpr (hides) {
-            // a hidden key's weight is 0, and 0 times NaN or Inf is NaN
-            move_bad_rows(tid, sv, sk);
-            sk.store(tid, to);
-            sv.store(tid, to + BN * D);
-        } else {
-            landed();
-        }
+    auto store = [&](int t, E* to) {
+        landed();
+        if (t < td || t >= te) v_tiles.move_bad(tid, to + BN * D, to);
     };
     // PAGED: the cache row of key tid of tile t (tid < BN)
     auto look_up = [&](int t) -> int64_t {
@@ -149,22 +146,19 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
         for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     if (nt > 0) {
-        E* to = td & 1 ? odd : even;
-        load(0, Int<1>(), to);
-        store(Int<1>(), to);
+        load(0, even);
+        store(0, even);
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]);
-    // Tile t of the keys; hides: some row does not see all of the keys of it or of
-    // the next one.
-    auto step = [&](int t, auto hides, const E* K, E* next) {
+    auto step = [&](int t, const E* K, E* next) __attribute__((always_inline)) {
         k_rows.keep(), v_cols.keep();
         const E* V = K + BN * D;
         const int n0 = t * BN;
-        if (t + 1 < nt) load(t + 1, hides, next);
+        if (t + 1 < nt) load(t + 1, next);
         if constexpr (PAGED)
             if (tid < BN) {
                 keep(t + 2, next_place);
@@ -183,7 +177,7 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
             constexpr int E0 = TT * KS;
             v8 p[NQ][TT / 2];
             auto take_weights = [&]() {
-                if (hides && !kr.whole(n0, n0 + BN, last_lo, first_hi)) {
+                if (!kr.whole(n0, n0 + BN, last_lo, first_hi)) {
 #pragma unroll
                     for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -263,24 +257,15 @@ __global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowAr
                     }
                 });
         }
-        if (t + 1 < nt) store(hides, next);
+        if (t + 1 < nt) store(t + 1, next);
         __syncthreads();
     };
-    auto masked = [&](int t) __attribute__((always_inline)) { step(t, Int<1>(), (t - td) & 1 ? odd : even, (t - td) & 1 ? even : odd); };
     int t = 0;
-    if constexpr (!PAGED) {
-        direct_k.rows(tid, in.k_token_stride, BN);
-        direct_v.rows(tid, in.v_token_stride, BN);
-        if (td + 1 < te) {
-            for (; t < td; ++t) masked(t);
-            for (; t + 2 < te; t += 2) {
-                step(t, Int<0>(), even, odd);
-                step(t + 1, Int<0>(), odd, even);
-            }
-            if (t + 1 < te) step(t++, Int<0>(), even, odd);
-        }
+    for (; t + 1 < nt; t += 2) {
+        step(t, even, odd);
+        step(t + 1, odd, even);
     }
-    for (; t < nt; ++t) masked(t);
+    if (t < nt) step(t, even, odd);
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;

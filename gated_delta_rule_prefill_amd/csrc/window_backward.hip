@@ -53,7 +53,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
     const KeyRange kr(uniform(token(tile * BQ)), uniform(token(tile * BQ + BQ - 1)), off, in.window, in.sinks, nk);
     const int nt = (kr.total + BN - 1) / BN;
-    int td, te;   // the tiles [td, te) are seen whole by all rows; tile t lies in even or odd by its distance from td
+    int td, te;   // the tiles [td, te) are seen whole by all rows
     kr.whole_tiles(BN, td, te);
 
     const E* kp = (const E*)in.k + (int64_t)k0 * in.k_token_stride + h * in.k_head_stride;
@@ -87,28 +87,24 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     const int w0 = uniform(token(wrow)) + off, w1 = uniform(token(wrow + 16 * NQ - 1)) + off;
     const int last_lo = kr.last(w0), last_hi = kr.last(w1), first_lo = kr.first(w0), first_hi = kr.first(w1);
 
-    Stage<E, D, BN, 256> sk, sv;
-    // Tiles that all rows see whole go straight to LDS; the others through registers,
-    // where rows that are not finite are found and taken out.
-    Direct<E, D, BN, 256> direct_k, direct_v;
-    auto load = [&](int t, auto hides, E* to) {
-        if constexpr (!hides) {
-            const int64_t key = (int64_t)t * BN + kr.shift;
-            direct_k.fetch(wave, kp + key * in.k_token_stride, to);
-            direct_v.fetch(wave, vp + key * in.v_token_stride, to + BN * D);
-            return;
-        }
-        load_keys(sk, tid, kr, t * BN, kp, in.k_token_stride);
-        load_keys(sv, tid, kr, t * BN, vp, in.v_token_stride);
-    };
-    auto store = [&](auto hides, E* to) {
-        if constexpr (hides) {
-            move_bad_rows(tid, sk, sv);
-            sk.store(tid, to);
-            sv.store(tid, to + BN * D);
+    const Tiles<E, D, BN, 256> k_tiles(tid, in.k_token_stride), v_tiles(tid, in.v_token_stride);
+    auto load = [&](int t, E* to) {
+        const int64_t n0 = (int64_t)t * BN, key = n0 + kr.shift;
+        const E *kt = kp + key * in.k_token_stride, *vt = vp + key * in.v_token_stride;
+        if (t >= td && t < te) {
+            k_tiles.fetch(wave, kt, to);
+            v_tiles.fetch(wave, vt, to + BN * D);
         } else {
-            landed();
+            const int split = kr.ns - (int)n0, left = kr.total - (int)n0;
+            k_tiles.fetch_part(wave, kt, kp + n0 * in.k_token_stride, split, left, to);
+            v_tiles.fetch_part(wave, vt, vp + n0 * in.v_token_stride, split, left, to + BN * D);
         }
+    };
+    // Keys that some row does not see weigh 0, and 0 times NaN or Inf is NaN: in the
+    // tiles that are not seen whole such rows are found and taken out.
+    auto store = [&](int t, E* to) {
+        landed();
+        if (t < td || t >= te) k_tiles.move_bad(tid, to, to + BN * D);
     };
     RowReader<E, D> rows_of(lane);
     ColReader<E, D, D / 16> k_cols(lane);
@@ -119,22 +115,19 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (nt > 0) {
-        E* to = td & 1 ? odd : even;
-        load(0, Int<1>(), to);
-        store(Int<1>(), to);
+        load(0, even);
+        store(0, even);
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]);
-    // Tile t of the keys; hides: some row does not see all of the keys of it or of
-    // the next one.
-    auto step = [&](int t, auto hides, const E* K, E* next) {
+    auto step = [&](int t, const E* K, E* next) __attribute__((always_inline)) {
         rows_of.keep(), k_cols.keep();
         const E* V = K + BN * D;
         const int n0 = t * BN;
-        if (t + 1 < nt) load(t + 1, hides, next);
+        if (t + 1 < nt) load(t + 1, next);
         if (wrow < rows && n0 <= last_hi && (n0 < kr.ns || n0 + BN > first_lo)) {
             f32x4 s[NQ][TT], dp[NQ][TT];
             v8 x[PD + 1];
@@ -176,7 +169,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                         }
                     } else {
                         if (e == E1) {
-                            if (hides && !kr.whole(n0, n0 + BN, last_lo, first_hi)) {   // weights of hidden keys
+                            if (!kr.whole(n0, n0 + BN, last_lo, first_hi)) {   // weights of hidden keys
 #pragma unroll
                                 for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -204,22 +197,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                     }
                 });
         }
-        if (t + 1 < nt) store(hides, next);
+        if (t + 1 < nt) store(t + 1, next);
         __syncthreads();
     };
-    direct_k.rows(tid, in.k_token_stride, BN);
-    direct_v.rows(tid, in.v_token_stride, BN);
-    auto masked = [&](int t) __attribute__((always_inline)) { step(t, Int<1>(), (t - td) & 1 ? odd : even, (t - td) & 1 ? even : odd); };
     int t = 0;
-    if (td + 1 < te) {
-        for (; t < td; ++t) masked(t);
-        for (; t + 2 < te; t += 2) {
-            step(t, Int<0>(), even, odd);
-            step(t + 1, Int<0>(), odd, even);
-        }
-        if (t + 1 < te) step(t++, Int<0>(), even, odd);
+    for (; t + 1 < nt; t += 2) {
+        step(t, even, odd);
+        step(t + 1, odd, even);
     }
-    for (; t < nt; ++t) masked(t);
+    if (t < nt) step(t, even, odd);
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;
@@ -283,6 +269,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     __shared__ __attribute__((aligned(16))) E even[BQ * 2 * D];
     __shared__ __attribute__((aligned(16))) E odd[BQ * 2 * D];
     __shared__ __attribute__((aligned(16))) float srow[2][2 * BQ];   // lse (base 2), then delta
+    __shared__ unsigned bad_rows[2];                                 // a bit for each row to be taken out
 
     int h, want, seq, item;
     key_head_of_block(in.Hk, items, blockIdx.x, h, want);
@@ -316,53 +303,44 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     const E* gp = d_o + ((int64_t)(work.q0 + ta) * in.H + h * G) * D;
     const float* sp = row_stats + 2 * ((int64_t)h * G * in.total_q + work.q0 + ta);
 
-    typedef Stage<E, D, BQ, 256> S;
-    S sq, sg;
-    static_assert(S::P == 1 && S::TPR == 8, "a row per 8 threads");
-    // lse and delta of a row travel with one thread: where all keys are seen the first
-    // BQ threads (few and whole lines to load), else the row's own first thread, which
-    // knows whether the row is finite.
+    // A head's tiles [td, tw): 32 rows that all see all of the workgroup's keys.
+    const int td = max(0, key0 + BK - 1 - (ta + off) + BQ - 1) / BQ;
+    const int tw = min((te - ta) / BQ, max(0, key0 + W - (ta + off)) / BQ);
+    // lse and delta of a row travel with one of the first BQ threads.
     float next_lse = 0.f, next_delta = 0.f;
-    auto carried = [&](bool hides) { return !hides ? tid : tid % S::TPR == 0 ? tid / S::TPR : BQ; };
-    // Tiles of rows that all see all of the keys go straight to LDS; the others
-    // through registers, where rows that are not finite are found and taken out.
-    Direct<E, D, BQ, 256> direct_q, direct_g;
-    auto load = [&](int head, int t, auto hides, E* to) {
-        const int left = te - ta - t * BQ, i = carried(hides);
+    const Tiles<E, D, BQ, 256> q_tiles(tid, in.q_token_stride), g_tiles(tid, (int64_t)in.H * D);
+    auto load = [&](int head, int t, E* to) {
+        const int left = te - ta - t * BQ;
         const E* qt = qp + head * in.q_head_stride + (int64_t)t * BQ * in.q_token_stride;
         const E* gt = gp + (int64_t)head * D + (int64_t)t * BQ * in.H * D;
-        if (i < BQ) {   // rows behind the last weigh nothing: lse = inf
-            const float* at = sp + 2 * ((int64_t)head * in.total_q + t * BQ + min(i, left - 1));
-            next_lse = i < left ? at[0] : __builtin_inff();
-            next_delta = i < left ? at[1] : 0.f;
+        if (tid < BQ) {   // rows behind the last weigh nothing: lse = inf
+            const float* at = sp + 2 * ((int64_t)head * in.total_q + t * BQ + min(tid, left - 1));
+            next_lse = tid < left ? at[0] : __builtin_inff();
+            next_delta = tid < left ? at[1] : 0.f;
         }
-        if constexpr (hides) {
-            sq.load_rows(tid, qt, in.q_token_stride, left);
-            sg.load_rows(tid, gt, (int64_t)in.H * D, left);
+        if (left >= BQ) {
+            q_tiles.fetch(wave, qt, to);
+            g_tiles.fetch(wave, gt, to + BQ * D);
         } else {
-            direct_q.fetch(wave, qt, to);
-            direct_g.fetch(wave, gt, to + BQ * D);
+            q_tiles.fetch_part(wave, qt, qt, 0, left, to);
+            g_tiles.fetch_part(wave, gt, gt, 0, left, to + BQ * D);
         }
     };
-    auto store = [&](int u, auto hides, E* to) {
-        const int i = carried(hides);
-        if constexpr (hides) {
-            const bool bad_delta = i < BQ && !(__builtin_fabsf(next_delta) < __builtin_inff());
-            const bool bad_q = sq.bad_row(tid, 0), bad_g = sg.bad_row(tid, 0, bad_delta);
-            if (bad_q || bad_g) {   // as move_bad_rows: lse becomes NaN
-                sq.fill_row(0, 0u);
-                sg.fill_row(0, 0u);
-                next_lse = __builtin_nanf("");
-                next_delta = 0.f;
-            }
-            sq.store(tid, to);
-            sg.store(tid, to + BQ * D);
+    // A row with q that is not finite has no finite lse, one with g that is not finite
+    // no finite delta (each enters every product of the row's sum, with a factor that
+    // is not finite or a zero that makes NaN of it).  In tiles whose rows do not all
+    // see all keys such rows are taken out, and their lse is NaN: the keys that see
+    // them get NaN, the others a weight of 0 times finite values.
+    auto store = [&](int u, int t) {
+        if (tid < BQ) {
+            const bool bad = tid < te - ta - t * BQ && (!(__builtin_fabsf(next_lse) < __builtin_inff()) ||
+                                                        !(__builtin_fabsf(next_delta) < __builtin_inff()));
+            const unsigned rows = (unsigned)__ballot(bad);
+            srow[u & 1][tid] = bad ? __builtin_nanf("") : next_lse;
+            srow[u & 1][BQ + tid] = bad ? 0.f : next_delta;
+            if (tid == 0) bad_rows[u & 1] = t >= td && t < tw ? 0u : rows;
         }
-        if (i < BQ) {
-            srow[u & 1][i] = next_lse;
-            srow[u & 1][BQ + i] = next_delta;
-        }
-        if constexpr (!hides) landed();
+        landed();
     };
     RowReader<E, D> rows_of(lane);
     ColReader<E, D, D / 16> cols_of(lane);
@@ -370,21 +348,29 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) ak[c] = av[c] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (nu > 0) {
-        load(0, 0, Int<1>(), even);
-        store(0, Int<1>(), even);
+        load(0, 0, even);
+        store(0, 0);
     }
     __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) arrived(k[ks]), arrived(v[ks]);
     // Tile t of a head's tokens, number u of all; the next one is nt of nhead.
-    // hides: some row of it or of the next does not see all of the keys.
-    auto step = [&](int u, int t, int nhead, int nt, auto hides, const E* Q, E* next) {
+    auto step = [&](int u, int t, int nhead, int nt, E* Q, E* next) __attribute__((always_inline)) {
         rows_of.keep(), cols_of.keep();
-        const E* Gt = Q + BQ * D;
+        E* Gt = Q + BQ * D;
         const float* R = srow[u & 1];
         const int p0 = ta + t * BQ + off, p1 = min(p0 + BQ, te + off) - 1;   // positions of the tile's rows
-        if (u + 1 < nu) load(nhead, nt, hides, next);
-        if (!hides || (p1 >= wkey && (p0 - (wkey + 15) < W || wkey < in.sinks))) {
+        if (u + 1 < nu) load(nhead, nt, next);
+        if (const unsigned bad = uniform((int)bad_rows[u & 1])) {
+#pragma unroll
+            for (int i = 0; i < q_tiles.N; ++i)
+                if (bad >> q_tiles.row(i) & 1) {
+                    *reinterpret_cast<u32x4*>(Q + (i * 256 + tid) * q_tiles.CE) = u32x4{0, 0, 0, 0};
+                    *reinterpret_cast<u32x4*>(Gt + (i * 256 + tid) * q_tiles.CE) = u32x4{0, 0, 0, 0};
+                }
+            __syncthreads();
+        }
+        if (p1 >= wkey && (p0 - (wkey + 15) < W || wkey < in.sinks)) {
             f32x4 s[2], dp[2];
             v8 x[PD + 1];
 #pragma unroll
@@ -420,7 +406,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
                         constexpr int c = e - E1;
                         if (c == 0) {
                             // weights of hidden keys
-                            if (hides && (p0 < wkey + 15 || (p1 - wkey >= W && wkey + 15 >= in.sinks))) {
+                            if (p0 < wkey + 15 || (p1 - wkey >= W && wkey + 15 >= in.sinks)) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     const int p = p0 + 16 * (i / 4) + 4 * g + i % 4;
@@ -441,33 +427,22 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
                     }
                 });
         }
-        if (u + 1 < nu) store(u + 1, hides, next);
+        if (u + 1 < nu) store(u + 1, nt);
         __syncthreads();
     };
-    // A head's tiles [td, tw): 32 rows that all see all of the workgroup's keys.
-    const int td = max(0, key0 + BK - 1 - (ta + off) + BQ - 1) / BQ;
-    const int tw = min((te - ta) / BQ, max(0, key0 + W - (ta + off)) / BQ);
-    direct_q.rows(tid, in.q_token_stride, BQ);
-    direct_g.rows(tid, (int64_t)in.H * D, BQ);
-    for (int head = 0, u = 0; head < G; ++head) {
-        int t = 0;
-        auto masked = [&]() __attribute__((always_inline)) {
-            const int nt = t + 1 < per ? t + 1 : 0;
-            step(u, t, nt ? head : head + 1, nt, Int<1>(), u & 1 ? odd : even, u & 1 ? even : odd);
-            ++u, ++t;
-        };
-        auto whole = [&](int n, const E* Q, E* next) __attribute__((always_inline)) { step(u + n, t + n, head, t + n + 1, Int<0>(), Q, next); };
-        if (td + 1 < tw) {
-            while (t < td) masked();
-            if (u & 1) whole(0, odd, even), ++u, ++t;
-            for (; t + 2 < tw; t += 2, u += 2) {
-                whole(0, even, odd);
-                whole(1, odd, even);
-            }
-            if (t + 1 < tw) whole(0, even, odd), ++u, ++t;
-        }
-        while (t < per) masked();
+    int head = 0, t = 0;
+    auto next = [&](int u, E* Q, E* to) __attribute__((always_inline)) {
+        const int nt = t + 1 < per ? t + 1 : 0, nhead = nt ? head : head + 1;
+        step(u, t, nhead, nt, Q, to);
+        t = nt;
+        head = nhead;
+    };
+    int u = 0;
+    for (; u + 1 < nu; u += 2) {
+        next(u, even, odd);
+        next(u + 1, odd, even);
     }
+    if (u < nu) next(u, even, odd);
     if (key >= nk) return;
     const bool sink = key < in.sinks && work.pieces > 0 && key0 == 0;
     if (piece >= 0 && !sink) return;

@@ -52,25 +52,65 @@ struct KeyRange {
     }
 };
 
-// Tile t of the keys (rows `stride` elements apart from base, the sequence's first)
-// into registers: sinks, then the run behind them, zeros behind the last key.  An
-// offset within the tile fits in 32 bits, as strides are below 2^23.
-template <typename S, typename E>
-__device__ __forceinline__ void load_keys(S& st, int tid, const KeyRange& kr, int n0, const E* base, int64_t stride) {
-    const E *sinks = base + n0 * stride, *run = base + ((int64_t)n0 + kr.shift) * stride;
-    const int left = kr.total - n0, split = kr.ns - n0;
+// Tiles of rows from global memory straight into LDS, as Direct, also where some of
+// a tile's rows are not there (`left` of them are; the last one is repeated behind)
+// or do not follow on the others (the first `split` rows lie where `first` says).
+template <typename E, int W, int ROWS, int NT>
+struct Tiles : Direct<E, W, ROWS, NT> {
+    typedef Direct<E, W, ROWS, NT> Base;
+    using Base::CE;
+    using Base::CH;
+    using Base::N;
+    int row0;          // the row of this thread's chunk i is row0 + i NT / CH
+    uint32_t stride;   // in bytes
+    static_assert(NT % CH == 0 && 64 % CH == 0, "whole rows in a wave");
+    __device__ __forceinline__ Tiles(int tid, int64_t stride_) : row0(tid / CH), stride((uint32_t)(stride_ * sizeof(E))) {
+        this->rows(tid, stride_, ROWS);
+    }
+    __device__ __forceinline__ int row(int i) const { return row0 + i * (NT / CH); }
+    __device__ __forceinline__ void fetch_part(int wave, const E* base, const E* first, int split, int left, E* t) const {
+        typedef __attribute__((address_space(1))) const void global_void;
+        typedef __attribute__((address_space(3))) void lds_void;
 #pragma unroll
-    for (int p = 0; p < S::P; ++p) {
-        const int r = tid / S::TPR + S::PASS * p;
-        const uint32_t at = (uint32_t)min(r, left - 1) * (uint32_t)(stride * sizeof(E)) + 16 * (tid % S::TPR);
-        const char* row = reinterpret_cast<const char*>(min(r, left - 1) < split ? sinks : run);
-#pragma unroll
-        for (int s = 0; s < S::S; ++s) {
-            st.r[p][s] = *reinterpret_cast<const u32x4*>(row + at + 16 * S::TPR * s);
-            if (r >= left) st.r[p][s] = u32x4{0, 0, 0, 0};
+        for (int i = 0; i < N; ++i) {
+            const int r = row(i), there = min(r, left - 1);
+            const uint32_t at = this->at[i] - (uint32_t)(r - there) * stride;
+            __builtin_amdgcn_global_load_lds((global_void*)(reinterpret_cast<const char*>(there < split ? first : base) + at),
+                                             (lds_void*)(t + (i * NT + 64 * wave) * CE), 16, 0, 0);
         }
     }
-}
+    // Rows in any order, row(r) being the address of row r (strides are 0).
+    template <typename F>
+    __device__ __forceinline__ void fetch_rows(int wave, F row_at, E* t) const {
+        typedef __attribute__((address_space(1))) const void global_void;
+        typedef __attribute__((address_space(3))) void lds_void;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            __builtin_amdgcn_global_load_lds((global_void*)(reinterpret_cast<const char*>(row_at(row(i))) + this->at[i]),
+                                             (lds_void*)(t + (i * NT + 64 * wave) * CE), 16, 0, 0);
+    }
+    // Fetched tiles in LDS, each thread looking at the chunks it has fetched itself:
+    // rows of `product` with values that are not finite are cleared, and those of
+    // `weights` set to NaN (see move_bad_rows).
+    __device__ __forceinline__ void move_bad(int tid, E* product, E* weights) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            u32x4* at = reinterpret_cast<u32x4*>(product + (i * NT + tid) * CE);
+            const u32x4 x = *at;
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                bad |= (x[e] & 0x7f800000u) == 0x7f800000u;
+                if (sizeof(E) == 2) bad |= (x[e] & 0x7f80u) == 0x7f80u;
+            }
+            const unsigned long long any = __ballot(bad);
+            if (any == 0) continue;
+            if ((any >> (tid & 63 & ~(CH - 1)) & (CH == 64 ? ~0ull : (1ull << CH) - 1)) == 0) continue;
+            *at = u32x4{0, 0, 0, 0};
+            *reinterpret_cast<u32x4*>(weights + (i * NT + tid) * CE) = u32x4{QUIET, QUIET, QUIET, QUIET};
+        }
+    }
+};
 
 // Cached tokens of a sequence.
 __device__ __forceinline__ int cached_tokens(const kda_kv_cache& c, int seq) {
