@@ -55,6 +55,8 @@ struct KeyRange {
 // Tiles of rows from global memory straight into LDS, as Direct, also where some of
 // a tile's rows are not there (`left` of them are; the last one is repeated behind)
 // or do not follow on the others (the first `split` rows lie where `first` says).
+// The loads are buffer loads: behind loads of the global kind the compiler waits for
+// every LDS read in flight before it uses one, as if they came back out of order.
 template <typename E, int W, int ROWS, int NT>
 struct Tiles : Direct<E, W, ROWS, NT> {
     typedef Direct<E, W, ROWS, NT> Base;
@@ -68,15 +70,26 @@ struct Tiles : Direct<E, W, ROWS, NT> {
         this->rows(tid, stride_, ROWS);
     }
     __device__ __forceinline__ int row(int i) const { return row0 + i * (NT / CH); }
-    __device__ __forceinline__ void fetch_part(int wave, const E* base, const E* first, int split, int left, E* t) const {
-        typedef __attribute__((address_space(1))) const void global_void;
+    // 16 bytes a lane from `at` bytes behind the wave's base to 1 KB of LDS.
+    static __device__ __forceinline__ void fetch_chunks(const E* base, uint32_t at, E* to) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host compiler does not know the type of a buffer
         typedef __attribute__((address_space(3))) void lds_void;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(base), 0, -1, 0x00020000),
+                                                 (lds_void*)to, 16, at, 0, 0, 0);   // raw: an offset of 32 bits
+#endif
+    }
+    __device__ __forceinline__ void fetch(int wave, const E* base, E* t) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) fetch_chunks(base, this->at[i], t + (i * NT + 64 * wave) * CE);
+    }
+    __device__ __forceinline__ void fetch_part(int wave, const E* base, const E* first, int split, int left, E* t) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int r = row(i), there = min(r, left - 1);
             const uint32_t at = this->at[i] - (uint32_t)(r - there) * stride;
-            __builtin_amdgcn_global_load_lds((global_void*)(reinterpret_cast<const char*>(there < split ? first : base) + at),
-                                             (lds_void*)(t + (i * NT + 64 * wave) * CE), 16, 0, 0);
+            E* to = t + (i * NT + 64 * wave) * CE;
+            if (there >= split) fetch_chunks(base, at, to);
+            else fetch_chunks(first, at, to);
         }
     }
     // Rows in any order, row(r) being the address of row r (strides are 0).
