@@ -20,7 +20,7 @@ namespace kda {
 // double-buffered in LDS: the next tile's global loads are issued before a tile's
 // products and stored to LDS behind them.
 template <typename E, int D, bool PAGED>
-__global__ __launch_bounds__(256, 2) void window_attention_kernel(const WindowArgs a, int tiles)
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_kernel(const WindowArgs a, int tiles)
 {
     constexpr int BN = 128 / (int)sizeof(E), NQ = LATENT_NQ<E>, BQ = 64 * NQ;
     constexpr int KS = D / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;

@@ -52,44 +52,43 @@ struct KeyRange {
     }
 };
 
-// Tiles of rows from global memory straight into LDS, as Direct, also where some of
+// Tiles of rows from global memory straight into LDS, as Direct (every wave writes 1
+// KB of the tile in a row, its lanes fetch the chunks that belong there), also where some of
 // a tile's rows are not there (`left` of them are; the last one is repeated behind)
 // or do not follow on the others (the first `split` rows lie where `first` says).
 // The loads are buffer loads: behind loads of the global kind the compiler waits for
 // every LDS read in flight before it uses one, as if they came back out of order.
 template <typename E, int W, int ROWS, int NT>
-struct Tiles : Direct<E, W, ROWS, NT> {
-    typedef Direct<E, W, ROWS, NT> Base;
-    using Base::CE;
-    using Base::CH;
-    using Base::N;
-    int row0;          // the row of this thread's chunk i is row0 + i NT / CH
+struct Tiles {
+    static constexpr int CE = CHUNK_ELEMS<E>, CH = W / CE, N = ROWS * CH / NT, STEP = NT / CH;
+    static_assert(ROWS * CH % NT == 0 && 64 % CH == 0 && STEP % 8 == 0, "whole rows in a wave, chunks in place from step to step");
+    int row0;          // the row of this thread's chunk i is row0 + i STEP
     uint32_t stride;   // in bytes
-    static_assert(NT % CH == 0 && 64 % CH == 0, "whole rows in a wave");
+    uint32_t at;       // of chunk 0 from the tile's base
     __device__ __forceinline__ Tiles(int tid, int64_t stride_) : row0(tid / CH), stride((uint32_t)(stride_ * sizeof(E))) {
-        this->rows(tid, stride_, ROWS);
+        at = row0 * stride + 16u * ((tile_at<E, W>(row0, tid % CH) - row0 * W) / CE);
     }
-    __device__ __forceinline__ int row(int i) const { return row0 + i * (NT / CH); }
+    __device__ __forceinline__ int row(int i) const { return row0 + i * STEP; }
     // 16 bytes a lane from `at` bytes behind the wave's base to 1 KB of LDS.
-    static __device__ __forceinline__ void fetch_chunks(const E* base, uint32_t at, E* to) {
+    static __device__ __forceinline__ void fetch_chunks(const E* base, uint32_t at, uint32_t more, E* to) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host compiler does not know the type of a buffer
         typedef __attribute__((address_space(3))) void lds_void;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(base), 0, -1, 0x00020000),
-                                                 (lds_void*)to, 16, at, 0, 0, 0);   // raw: an offset of 32 bits
+                                                 (lds_void*)to, 16, at, more, 0, 0);   // raw: an offset of 32 bits
 #endif
     }
     __device__ __forceinline__ void fetch(int wave, const E* base, E* t) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) fetch_chunks(base, this->at[i], t + (i * NT + 64 * wave) * CE);
+        for (int i = 0; i < N; ++i) fetch_chunks(base, at, i * STEP * stride, t + (i * NT + 64 * wave) * CE);
     }
     __device__ __forceinline__ void fetch_part(int wave, const E* base, const E* first, int split, int left, E* t) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int r = row(i), there = min(r, left - 1);
-            const uint32_t at = this->at[i] - (uint32_t)(r - there) * stride;
+            const int there = min(row(i), left - 1);
+            const uint32_t x = at + (uint32_t)(there - row0) * stride;
             E* to = t + (i * NT + 64 * wave) * CE;
-            if (there >= split) fetch_chunks(base, at, to);
-            else fetch_chunks(first, at, to);
+            if (there >= split) fetch_chunks(base, x, 0, to);
+            else fetch_chunks(first, x, 0, to);
         }
     }
     // Rows in any order, row(r) being the address of row r (strides are 0).
@@ -99,29 +98,30 @@ struct Tiles : Direct<E, W, ROWS, NT> {
         typedef __attribute__((address_space(3))) void lds_void;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            __builtin_amdgcn_global_load_lds((global_void*)(reinterpret_cast<const char*>(row_at(row(i))) + this->at[i]),
+            __builtin_amdgcn_global_load_lds((global_void*)(reinterpret_cast<const char*>(row_at(row(i))) + at),
                                              (lds_void*)(t + (i * NT + 64 * wave) * CE), 16, 0, 0);
     }
-    // Fetched tiles in LDS, each thread looking at the chunks it has fetched itself:
-    // rows of `product` with values that are not finite are cleared, and those of
-    // `weights` set to NaN (see move_bad_rows).
+    // Whether chunk i of a fetched tile in LDS, which this thread has fetched, belongs
+    // to a row with values that are not finite.
+    __device__ __forceinline__ bool bad_row(int tid, const E* t, int i) const {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(t + (i * NT + tid) * CE);
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bad |= (x[e] & 0x7f800000u) == 0x7f800000u;
+            if (sizeof(E) == 2) bad |= (x[e] & 0x7f80u) == 0x7f80u;
+        }
+        const unsigned long long any = __ballot(bad);
+        return (any >> (tid & 63 & ~(CH - 1)) & (CH == 64 ? ~0ull : (1ull << CH) - 1)) != 0;
+    }
+    // Such rows of the tile `product` cleared, and those of `weights` set to NaN (see move_bad_rows).
     __device__ __forceinline__ void move_bad(int tid, E* product, E* weights) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            u32x4* at = reinterpret_cast<u32x4*>(product + (i * NT + tid) * CE);
-            const u32x4 x = *at;
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                bad |= (x[e] & 0x7f800000u) == 0x7f800000u;
-                if (sizeof(E) == 2) bad |= (x[e] & 0x7f80u) == 0x7f80u;
+        for (int i = 0; i < N; ++i)
+            if (bad_row(tid, product, i)) {
+                *reinterpret_cast<u32x4*>(product + (i * NT + tid) * CE) = u32x4{0, 0, 0, 0};
+                *reinterpret_cast<u32x4*>(weights + (i * NT + tid) * CE) = u32x4{QUIET, QUIET, QUIET, QUIET};
             }
-            const unsigned long long any = __ballot(bad);
-            if (any == 0) continue;
-            if ((any >> (tid & 63 & ~(CH - 1)) & (CH == 64 ? ~0ull : (1ull << CH) - 1)) == 0) continue;
-            *at = u32x4{0, 0, 0, 0};
-            *reinterpret_cast<u32x4*>(weights + (i * NT + tid) * CE) = u32x4{QUIET, QUIET, QUIET, QUIET};
-        }
     }
 };
 
