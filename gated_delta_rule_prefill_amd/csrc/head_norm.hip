@@ -46,37 +46,42 @@ struct HeadRow {
         const int i = at[k] - start;
         return inter ? i / 2 : i < half ? i : i - half;
     }
-    static __device__ __forceinline__ void get(const E* p, float* v) {
-        if constexpr (VE == 1) v[0] = to_f32(p[0]);
-        else {
-            const vec x = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-            for (int i = 0; i < VE; ++i) v[i] = to_f32(x[i]);
-        }
-    }
-    static __device__ __forceinline__ void put(E* p, const float* v) {
-        if constexpr (VE == 1) p[0] = from_f32<E>(v[0]);
-        else {
-            vec x;
-#pragma unroll
-            for (int i = 0; i < VE; ++i) x[i] = from_f32<E>(v[i]);
-            *reinterpret_cast<vec*>(p) = x;
-        }
-    }
     static __device__ __forceinline__ void get_weight(const float* w, int at, float* v) {
 #pragma unroll
         for (int i = 0; i < VE; ++i) v[i] = w ? w[at + i] : 1.f;
     }
-    // Chunk k of a row, and the chunk with its pairs' other elements.
-    __device__ __forceinline__ void load(const E* row, float (&v)[NK][VE], float (&p)[NK][VE]) const {
+    // A lane's chunks as they lie in memory; of(): as numbers, 0 where there are none.
+    struct Raw {
+        vec x[NK];
+        __device__ __forceinline__ void of(float (&v)[NK][VE]) const {
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+                for (int i = 0; i < VE; ++i) v[k][i] = to_f32(x[k][i]);
+        }
+    };
+    // A row's chunks, and the chunks with their pairs' other elements.
+    __device__ __forceinline__ void load(const E* row, Raw& own) const {
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
-#pragma unroll
-            for (int i = 0; i < VE; ++i) v[k][i] = p[k][i] = 0.f;
-            if (at[k] < 0) continue;
-            get(row + at[k], v[k]);
-            if (kind[k] == 1 || kind[k] == 2) get(row + other(k), p[k]);
+            own.x[k] = vec{};
+            if (at[k] >= 0) own.x[k] = *reinterpret_cast<const vec*>(row + at[k]);
         }
+    }
+    __device__ __forceinline__ void load_pairs(const E* row, Raw& pairs) const {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            pairs.x[k] = vec{};
+            if (at[k] >= 0 && (kind[k] == 1 || kind[k] == 2)) pairs.x[k] = *reinterpret_cast<const vec*>(row + other(k));
+        }
+    }
+    template <bool FAR>
+    static __device__ __forceinline__ void put(E* p, const float* v) {
+        vec x;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) x[i] = from_f32<E>(v[i]);
+        if constexpr (FAR) __builtin_nontemporal_store(x, reinterpret_cast<vec*>(p));
+        else *reinterpret_cast<vec*>(p) = x;
     }
     // Chunk k turned by its angles (way 1), or back (way -1); p: the other elements.
     __device__ __forceinline__ void turn(int k, float (&v)[VE], const float (&p)[VE], const float2* cs, float way) const {
@@ -128,125 +133,156 @@ __device__ __forceinline__ void put_angles(float2* cs, int nt, int half, const f
     }
 }
 
+// Walks rows first, first + step, ... of nt tokens with H heads each: (token, head)
+// without a division a row.
+struct RowWalk {
+    int t, h;
+    __device__ __forceinline__ RowWalk(int first, int H) : t(first / H), h(first - first / H * H) {}
+    __device__ __forceinline__ void on(int step, int H) {
+        h += step;
+        while (h >= H) h -= H, ++t;
+    }
+};
+
 // -- queries and keys ------------------------------------------------------------
-template <typename E, int VE, int LPR, int NK>
+// A workgroup takes a few tokens: their angles, then the rows of their query heads and
+// those of their key heads, each row loaded while the one before is worked on.
+template <typename E, int VE, int LPR, int NK, bool FAR>
 __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNorm a, int tokens)
 {
     __shared__ float2 cs[NORM_PAIRS];
-    const int sub = threadIdx.x % LPR, half = a.dr / 2, heads = a.q.H + a.k.H;
+    constexpr int STEP = 256 / LPR;
+    const int half = a.dr / 2;
     const int64_t t0 = block_of_grid() * tokens;
     const int nt = (int)max((int64_t)0, min((int64_t)tokens, a.total_tokens - t0));
-    const HeadRow<E, VE, LPR, NK> row(sub, a.d, a.start, a.dr, a.flags & KDA_ROTARY_INTERLEAVED);
-    float w[2][NK][VE], wp[2][NK][VE];   // the weights of the lane's elements, and of their pairs' others
-#pragma unroll
-    for (int k = 0; k < NK; ++k)
-        if (row.at[k] >= 0) {
-            row.get_weight(a.q.weight, row.at[k], w[0][k]);
-            row.get_weight(a.k.weight, row.at[k], w[1][k]);
-            if (row.kind[k] == 1 || row.kind[k] == 2) {
-                row.get_weight(a.q.weight, row.other(k), wp[0][k]);
-                row.get_weight(a.k.weight, row.other(k), wp[1][k]);
-            }
-        }
-    if (half > 0) put_angles(cs, nt, half, a.inv_freq, a.amplitude, [&](int t) { return a.positions[t0 + t]; });
-    __syncthreads();
-    for (int id = threadIdx.x / LPR; id < nt * heads; id += 256 / LPR) {
-        const int t = id / heads, hh = id - t * heads;
-        const bool key = hh >= a.q.H;
-        const int h = key ? hh - a.q.H : hh;
-        const E* x = (const E*)(key ? a.k.x : a.q.x) + (t0 + t) * (key ? a.k.x_token_stride : a.q.x_token_stride) +
-                     h * (key ? a.k.x_head_stride : a.q.x_head_stride);
-        E* y = (E*)(key ? a.k.y : a.q.y) + (t0 + t) * (key ? a.k.y_token_stride : a.q.y_token_stride) +
-               h * (key ? a.k.y_head_stride : a.q.y_head_stride);
-        float v[NK][VE], p[NK][VE];
-        row.load(x, v, p);
-        const float r = row.scale(v, a.eps);
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            if (row.at[k] < 0) continue;
-#pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                v[k][i] *= r * (key ? w[1][k][i] : w[0][k][i]);
-                p[k][i] *= r * (key ? wp[1][k][i] : wp[0][k][i]);
-            }
-            row.turn(k, v[k], p[k], cs + t * half, 1.f);
-        }
+    typedef HeadRow<E, VE, LPR, NK> Row;
+    const Row row(threadIdx.x % LPR, a.d, a.start, a.dr, a.flags & KDA_ROTARY_INTERLEAVED);
+    auto rows = [&](const kda_norm_heads& s, auto first) __attribute__((always_inline)) {
+        const int H = s.H;
+        if (H == 0) return;
+        float w[NK][VE], wp[NK][VE];   // the weights of the lane's elements, and of their pairs' others
 #pragma unroll
         for (int k = 0; k < NK; ++k)
-            if (row.at[k] >= 0) row.put(y + row.at[k], v[k]);
-    }
+            if (row.at[k] >= 0) {
+                row.get_weight(s.weight, row.at[k], w[k]);
+                if (row.kind[k] == 1 || row.kind[k] == 2) row.get_weight(s.weight, row.other(k), wp[k]);
+            }
+        typename Row::Raw own, pairs;
+        auto load = [&](const RowWalk& at) {
+            if (at.t >= nt) return;
+            const E* x = (const E*)s.x + (t0 + at.t) * s.x_token_stride + at.h * s.x_head_stride;
+            row.load(x, own);
+            row.load_pairs(x, pairs);
+        };
+        RowWalk at(threadIdx.x / LPR, H);
+        load(at);
+        if constexpr (first) {   // the first rows are on their way
+            if (half > 0) put_angles(cs, nt, half, a.inv_freq, a.amplitude, [&](int t) { return a.positions[t0 + t]; });
+            __syncthreads();
+        }
+        while (at.t < nt) {
+            float v[NK][VE], p[NK][VE];
+            own.of(v);
+            pairs.of(p);
+            E* y = (E*)s.y + (t0 + at.t) * s.y_token_stride + at.h * s.y_head_stride;
+            const float2* angles = cs + at.t * half;
+            at.on(STEP, H);
+            load(at);
+            const float r = row.scale(v, a.eps);
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                if (row.at[k] < 0) continue;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    v[k][i] *= r * w[k][i];
+                    p[k][i] *= r * wp[k][i];
+                }
+                row.turn(k, v[k], p[k], angles, 1.f);
+                row.template put<FAR>(y + row.at[k], v[k]);
+            }
+        }
+    };
+    rows(a.q, Int<1>());
+    rows(a.k, Int<0>());
 }
 
 // Gradients.  A lane's rows all have its channels: it adds up g n of its own rows, and
 // the workgroup's sums go to part[workgroup][queries, keys][d].
-template <typename E, int VE, int LPR, int NK>
+template <typename E, int VE, int LPR, int NK, bool FAR>
 __global__ __launch_bounds__(256) void qk_norm_backward_kernel(const QkNorm a, int tokens)
 {
     __shared__ float2 cs[NORM_PAIRS];
-    __shared__ float sums[256 / LPR][LPR * NK * VE];
-    const int sub = threadIdx.x % LPR, mine = threadIdx.x / LPR, half = a.dr / 2, heads = a.q.H + a.k.H;
-    const HeadRow<E, VE, LPR, NK> row(sub, a.d, a.start, a.dr, a.flags & KDA_ROTARY_INTERLEAVED);
-    float w[2][NK][VE], dw[2][NK][VE];
+    constexpr int STEP = 256 / LPR;
+    __shared__ float sums[STEP][LPR * NK * VE];
+    const int sub = threadIdx.x % LPR, mine = threadIdx.x / LPR, half = a.dr / 2;
+    typedef HeadRow<E, VE, LPR, NK> Row;
+    const Row row(sub, a.d, a.start, a.dr, a.flags & KDA_ROTARY_INTERLEAVED);
+    float dw[2][NK][VE];
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
+    for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int i = 0; i < VE; ++i) dw[0][k][i] = dw[1][k][i] = 0.f;
-        if (row.at[k] >= 0) {
-            row.get_weight(a.q.weight, row.at[k], w[0][k]);
-            row.get_weight(a.k.weight, row.at[k], w[1][k]);
-        }
-    }
     for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.total_tokens; t0 += (int64_t)gridDim.x * tokens) {
         const int nt = (int)min((int64_t)tokens, a.total_tokens - t0);
-        if (half > 0) {
-            __syncthreads();   // the last tokens' angles are read
-            put_angles(cs, nt, half, a.inv_freq, a.amplitude, [&](int t) { return a.positions[t0 + t]; });
-            __syncthreads();
-        }
-        for (int id = mine; id < nt * heads; id += 256 / LPR) {
-            const int t = id / heads, hh = id - t * heads;
-            const bool key = hh >= a.q.H;
-            const int h = key ? hh - a.q.H : hh;
-            const E* x = (const E*)(key ? a.k.x : a.q.x) + (t0 + t) * (key ? a.k.x_token_stride : a.q.x_token_stride) +
-                         h * (key ? a.k.x_head_stride : a.q.x_head_stride);
-            const E* dy = (const E*)(key ? a.k.dy : a.q.dy) + (t0 + t) * (key ? a.k.dy_token_stride : a.q.dy_token_stride) +
-                          h * (key ? a.k.dy_head_stride : a.q.dy_head_stride);
-            E* dx = (E*)(key ? a.k.dx : a.q.dx) + (t0 + t) * (key ? a.k.dx_token_stride : a.q.dx_token_stride) +
-                    h * (key ? a.k.dx_head_stride : a.q.dx_head_stride);
-            float v[NK][VE], gr[NK][VE], p[NK][VE];
+        auto rows = [&](const kda_norm_heads& s, float (&sum)[NK][VE], auto first) __attribute__((always_inline)) {
+            const int H = s.H;
+            if (H == 0) return;
+            float w[NK][VE];
 #pragma unroll
-            for (int k = 0; k < NK; ++k) {
+            for (int k = 0; k < NK; ++k)
+                if (row.at[k] >= 0) row.get_weight(s.weight, row.at[k], w[k]);
+            typename Row::Raw own, grad, pairs;
+            auto load = [&](const RowWalk& at) {
+                if (at.t >= nt) return;
+                const E* dy = (const E*)s.dy + (t0 + at.t) * s.dy_token_stride + at.h * s.dy_head_stride;
+                row.load((const E*)s.x + (t0 + at.t) * s.x_token_stride + at.h * s.x_head_stride, own);
+                row.load(dy, grad);
+                row.load_pairs(dy, pairs);
+            };
+            RowWalk at(mine, H);
+            load(at);
+            if constexpr (first)
+                if (half > 0) {
+                    __syncthreads();   // the last tokens' angles are read
+                    put_angles(cs, nt, half, a.inv_freq, a.amplitude, [&](int t) { return a.positions[t0 + t]; });
+                    __syncthreads();
+                }
+            while (at.t < nt) {
+                float v[NK][VE], gr[NK][VE], p[NK][VE];
+                own.of(v);
+                grad.of(gr);
+                pairs.of(p);
+                E* dx = (E*)s.dx + (t0 + at.t) * s.dx_token_stride + at.h * s.dx_head_stride;
+                const float2* angles = cs + at.t * half;
+                at.on(STEP, H);
+                load(at);
+                const float r = row.scale(v, a.eps);
+                float dot = 0.f;
 #pragma unroll
-                for (int i = 0; i < VE; ++i) v[k][i] = 0.f;
-                if (row.at[k] >= 0) row.get(x + row.at[k], v[k]);
-            }
-            row.load(dy, gr, p);
-            const float r = row.scale(v, a.eps);
-            float dot = 0.f;
+                for (int k = 0; k < NK; ++k) {
+                    if (row.at[k] < 0) continue;
+                    row.turn(k, gr[k], p[k], angles, -1.f);
 #pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                if (row.at[k] < 0) continue;
-                row.turn(k, gr[k], p[k], cs + t * half, -1.f);
+                    for (int i = 0; i < VE; ++i) {
+                        v[k][i] *= r;
+                        const float gn = gr[k][i] * v[k][i];
+                        sum[k][i] += gn;
+                        dot += gn * w[k][i];
+                        gr[k][i] *= w[k][i];
+                    }
+                }
+                dot = row.sum(dot) / (float)a.d;
 #pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    v[k][i] *= r;
-                    const float gn = gr[k][i] * v[k][i];
-                    dw[0][k][i] += key ? 0.f : gn;
-                    dw[1][k][i] += key ? gn : 0.f;
-                    const float wi = key ? w[1][k][i] : w[0][k][i];
-                    dot += gn * wi;
-                    gr[k][i] *= wi;
+                for (int k = 0; k < NK; ++k) {
+                    if (row.at[k] < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) gr[k][i] = r * (gr[k][i] - v[k][i] * dot);
+                    row.template put<FAR>(dx + row.at[k], gr[k]);
                 }
             }
-            dot = row.sum(dot) / (float)a.d;
-#pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                if (row.at[k] < 0) continue;
-#pragma unroll
-                for (int i = 0; i < VE; ++i) gr[k][i] = r * (gr[k][i] - v[k][i] * dot);
-                row.put(dx + row.at[k], gr[k]);
-            }
-        }
+        };
+        rows(a.q, dw[0], Int<1>());
+        rows(a.k, dw[1], Int<0>());
     }
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
@@ -259,7 +295,7 @@ __global__ __launch_bounds__(256) void qk_norm_backward_kernel(const QkNorm a, i
         for (int c = threadIdx.x; c < a.d; c += 256) {
             float x = 0.f;
 #pragma unroll 8
-            for (int n = 0; n < 256 / LPR; ++n) x += sums[n][c];
+            for (int n = 0; n < STEP; ++n) x += sums[n][c];
             a.part[((int64_t)blockIdx.x * 2 + kind) * a.d + c] = x;
         }
     }
@@ -313,6 +349,11 @@ static int norm_tokens(int64_t total, int heads, int lanes, int half, int each) 
     return (int)std::min<int64_t>(n, half > 0 ? NORM_PAIRS / half : n);
 }
 
+// More than the 256 MB of the last-level cache is stored past the caches.
+static bool far(const QkNorm& a, int es) {
+    return a.total_tokens * (a.q.H + a.k.H) * (int64_t)a.d * es > (int64_t)256 << 20;
+}
+
 template <typename E>
 static hipError_t launch_norm(const QkNorm& a, hipStream_t stream) {
     bool w = wide_sizes(a.d, a.start, a.dr, a.flags, sizeof(E));
@@ -322,8 +363,11 @@ static hipError_t launch_norm(const QkNorm& a, hipStream_t stream) {
                 wide(s->y, s->y_token_stride, s->y_head_stride, sizeof(E));
     by_shape<E>(w, a.d, [&](auto ve, auto lpr, auto nk) {
         const int tokens = norm_tokens(a.total_tokens, a.q.H + a.k.H, lpr, a.dr / 2, 5);
-        hipLaunchKernelGGL((qk_norm_kernel<E, ve, lpr, nk>), grid_of((a.total_tokens + tokens - 1) / tokens), dim3(256), 0,
-                           stream, a, tokens);
+        auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid_of((a.total_tokens + tokens - 1) / tokens), dim3(256), 0, stream, a, tokens);
+        };
+        if (far(a, sizeof(E)) && ve > 1) go(qk_norm_kernel<E, ve, lpr, nk, (ve > 1)>);
+        else go(qk_norm_kernel<E, ve, lpr, nk, false>);
     });
     return launch_result(stream);
 }
@@ -345,9 +389,11 @@ static hipError_t launch_norm_backward(const QkNorm& a, hipStream_t stream) {
     int parts = 0;
     if (a.total_tokens > 0) {
         by_shape<E>(w, a.d, [&](auto ve, auto lpr, auto nk) {
-            const int tokens = norm_tokens(a.total_tokens, a.q.H + a.k.H, lpr, a.dr / 2, 5);
+            const int tokens = norm_tokens(a.total_tokens, a.q.H + a.k.H, lpr, a.dr / 2, 10);
             parts = (int)std::min<int64_t>(NORM_PARTS, (a.total_tokens + tokens - 1) / tokens);
-            hipLaunchKernelGGL((qk_norm_backward_kernel<E, ve, lpr, nk>), dim3(parts), dim3(256), 0, stream, a, tokens);
+            auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(parts), dim3(256), 0, stream, a, tokens); };
+            if (far(a, sizeof(E)) && ve > 1) go(qk_norm_backward_kernel<E, ve, lpr, nk, (ve > 1)>);
+            else go(qk_norm_backward_kernel<E, ve, lpr, nk, false>);
         });
         if (const hipError_t e = launch_result(stream)) return e;
     }
@@ -370,7 +416,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvAppend a, int to
     __shared__ int where[APPEND_TOKENS];       // position, or the least integer outside the sequences
     __shared__ int64_t place[APPEND_TOKENS];   // cache row, -1: none
     constexpr int OUTSIDE = -2147483647 - 1;
-    const int sub = threadIdx.x % LPR, lane = threadIdx.x & 63, half = a.dr / 2;
+    const int lane = threadIdx.x & 63, half = a.dr / 2;
     const int64_t t0 = block_of_grid() * tokens;
     const int nt = (int)max((int64_t)0, min((int64_t)tokens, a.total_tokens - t0));
     for (int x = threadIdx.x >> 6; x < nt; x += 4) {   // a wave per token
@@ -392,7 +438,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvAppend a, int to
             place[x] = position < 0 ? -1 : cached_row(a.pages, seq, position);
         }
     }
-    const HeadRow<E, VE, LPR, NK> row(sub, a.d, a.start, a.dr, a.flags & KDA_ROTARY_INTERLEAVED);
+    constexpr int STEP = 256 / LPR;
+    typedef HeadRow<E, VE, LPR, NK> Row;
+    const Row row(threadIdx.x % LPR, a.d, a.start, a.dr, a.flags & KDA_ROTARY_INTERLEAVED);
     float w[NK][VE], wp[NK][VE];
 #pragma unroll
     for (int k = 0; k < NK; ++k)
@@ -405,41 +453,52 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvAppend a, int to
         put_angles(cs, nt, half, a.inv_freq, a.amplitude, [&](int t) { return where[t]; });
         __syncthreads();
     }
-    // key rows, then value rows of each token
-    for (int id = threadIdx.x / LPR; id < nt * 2 * a.Hk; id += 256 / LPR) {
-        const int t = id / (2 * a.Hk), hh = id - t * 2 * a.Hk;
-        const bool value = hh >= a.Hk;
-        const int h = value ? hh - a.Hk : hh;
-        const int64_t at = place[t];
-        E* cached = at < 0 ? nullptr : (E*)(value ? a.pages.v : a.pages.k) + at + h * a.pages.head_stride;
-        if (value) {
-            if (!cached) continue;
-            const E* v = (const E*)a.v + (t0 + t) * a.v_token_stride + h * a.v_head_stride;
+    // key rows, then value rows
+    typename Row::Raw own, pairs;
+    const int mine = threadIdx.x / LPR;
+    auto cached = [&](void* cache, const RowWalk& at) {
+        return place[at.t] < 0 ? nullptr : (E*)cache + place[at.t] + at.h * a.pages.head_stride;
+    };
+    {
+        auto load = [&](const RowWalk& at) {
+            if (at.t >= nt) return;
+            const E* k = (const E*)a.k + (t0 + at.t) * a.k_token_stride + at.h * a.k_head_stride;
+            row.load(k, own);
+            row.load_pairs(k, pairs);
+        };
+        RowWalk at(mine, a.Hk);
+        load(at);
+        while (at.t < nt) {
+            float v[NK][VE], p[NK][VE];
+            own.of(v);
+            pairs.of(p);
+            E* to = cached(a.pages.k, at);
+            E* dense = a.k_out && where[at.t] != OUTSIDE ? (E*)a.k_out + ((t0 + at.t) * a.Hk + at.h) * a.d : nullptr;
+            const float2* angles = cs + at.t * half;
+            at.on(STEP, a.Hk);
+            load(at);
+            const float r = a.norm_weight ? row.scale(v, a.eps) : 1.f;
 #pragma unroll
-            for (int k = 0; k < NK; ++k)
-                if (row.at[k] >= 0) {
-                    typedef typename HeadRow<E, VE, LPR, NK>::vec vec;
-                    *reinterpret_cast<vec*>(cached + row.at[k]) = *reinterpret_cast<const vec*>(v + row.at[k]);
+            for (int k = 0; k < NK; ++k) {
+                if (row.at[k] < 0) continue;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    v[k][i] *= r * w[k][i];
+                    p[k][i] *= r * wp[k][i];
                 }
-            continue;
-        }
-        E* dense = a.k_out && where[t] != OUTSIDE ? (E*)a.k_out + ((t0 + t) * a.Hk + h) * a.d : nullptr;
-        if (!cached && !dense) continue;
-        float v[NK][VE], p[NK][VE];
-        row.load((const E*)a.k + (t0 + t) * a.k_token_stride + h * a.k_head_stride, v, p);
-        const float r = a.norm_weight ? row.scale(v, a.eps) : 1.f;
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            if (row.at[k] < 0) continue;
-#pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                v[k][i] *= r * w[k][i];
-                p[k][i] *= r * wp[k][i];
+                row.turn(k, v[k], p[k], angles, 1.f);
+                if (to) row.template put<false>(to + row.at[k], v[k]);
+                if (dense) row.template put<false>(dense + row.at[k], v[k]);
             }
-            row.turn(k, v[k], p[k], cs + t * half, 1.f);
-            if (cached) row.put(cached + row.at[k], v[k]);
-            if (dense) row.put(dense + row.at[k], v[k]);
         }
+    }
+    for (RowWalk at(mine, a.Hk); at.t < nt; at.on(STEP, a.Hk)) {
+        E* to = cached(a.pages.v, at);
+        if (!to) continue;
+        row.load((const E*)a.v + (t0 + at.t) * a.v_token_stride + at.h * a.v_head_stride, own);
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+            if (row.at[k] >= 0) *reinterpret_cast<typename Row::vec*>(to + row.at[k]) = own.x[k];
     }
 }
 
