@@ -362,7 +362,7 @@ static hipError_t launch_norm(const QkNorm& a, hipStream_t stream) {
             w = w && wide(s->x, s->x_token_stride, s->x_head_stride, sizeof(E)) &&
                 wide(s->y, s->y_token_stride, s->y_head_stride, sizeof(E));
     by_shape<E>(w, a.d, [&](auto ve, auto lpr, auto nk) {
-        const int tokens = norm_tokens(a.total_tokens, a.q.H + a.k.H, lpr, a.dr / 2, 5);
+        const int tokens = norm_tokens(a.total_tokens, a.q.H + a.k.H, lpr, a.dr / 2, 16);
         auto go = [&](auto kernel) {
             hipLaunchKernelGGL(kernel, grid_of((a.total_tokens + tokens - 1) / tokens), dim3(256), 0, stream, a, tokens);
         };
@@ -389,7 +389,7 @@ static hipError_t launch_norm_backward(const QkNorm& a, hipStream_t stream) {
     int parts = 0;
     if (a.total_tokens > 0) {
         by_shape<E>(w, a.d, [&](auto ve, auto lpr, auto nk) {
-            const int tokens = norm_tokens(a.total_tokens, a.q.H + a.k.H, lpr, a.dr / 2, 10);
+            const int tokens = norm_tokens(a.total_tokens, a.q.H + a.k.H, lpr, a.dr / 2, 20);
             parts = (int)std::min<int64_t>(NORM_PARTS, (a.total_tokens + tokens - 1) / tokens);
             auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(parts), dim3(256), 0, stream, a, tokens); };
             if (far(a, sizeof(E)) && ve > 1) go(qk_norm_backward_kernel<E, ve, lpr, nk, (ve > 1)>);
@@ -506,7 +506,7 @@ template <typename E>
 static hipError_t launch_append(const KvAppend& a, hipStream_t stream) {
     const bool w = wide_sizes(a.d, a.start, a.dr, a.flags, sizeof(E));
     by_shape<E>(w, a.d, [&](auto ve, auto lpr, auto nk) {
-        const int tokens = std::min(APPEND_TOKENS, norm_tokens(a.total_tokens, 2 * a.Hk, lpr, a.dr / 2, 8));
+        const int tokens = std::min(APPEND_TOKENS, norm_tokens(a.total_tokens, 2 * a.Hk, lpr, a.dr / 2, 4));
         hipLaunchKernelGGL((kv_append_kernel<E, ve, lpr, nk>), grid_of((a.total_tokens + tokens - 1) / tokens), dim3(256),
                            0, stream, a, tokens);
     });
