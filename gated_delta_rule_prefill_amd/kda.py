@@ -744,10 +744,22 @@ _NORM_HEADS = struct.Struct("@P2qP2q2P2qP2qPi4x")  # kda_norm_heads
 
 
 def _int32(x, name) -> int:
-    x = int(x)
-    if not -2 ** 31 <= x < 2 ** 31:
+    if type(x) is not int:
+        x = int(x)
+    if not -2147483648 <= x <= 2147483647:
         raise ValueError(f"{name}: {x} does not fit in 32 bits")
     return x
+
+
+def _strides3(t, name, T, H, d, dtype, device):
+    """Token and head strides of a [T, H, d] tensor whose last axis is dense (0 for
+    an axis of one)."""
+    s = t.stride()
+    if (t.shape == (T, H, d) and t.dtype is dtype and t.device == device and
+            (s[2] == 1 or d == 1 or T == 0 or H == 0 or d == 0)):
+        return (s[0] if T > 1 else 0), (s[1] if H > 1 else 0)
+    raise ValueError(f"{name}: expected {dtype} {(T, H, d)} on {device} with a dense last axis, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {s}")
 
 
 def _window_inputs(q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs, scale):
@@ -757,9 +769,9 @@ def _window_inputs(q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs, s
     T, H, d = q.shape
     Tk, Hk, _ = k.shape
     dev, dt = q.device, q.dtype
-    _rows3(q, "q", (T, H, d), dt, dev)
-    _rows3(k, "k", (Tk, Hk, d), dt, dev)
-    _rows3(v, "v", (Tk, Hk, d), dt, dev)
+    qt, qh = _strides3(q, "q", T, H, d, dt, dev)
+    kt, kh = _strides3(k, "k", Tk, Hk, d, dt, dev)
+    vt, vh = _strides3(v, "v", Tk, Hk, d, dt, dev)
     cu = cuk = 0
     if cu_seqlens is not None:
         N = _offsets(cu_seqlens, "cu_seqlens", dev)
@@ -774,9 +786,8 @@ def _window_inputs(q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs, s
         N = 1 if num_seqs is None else _int32(num_seqs, "num_seqs")
     if scale is None:
         scale = d ** -0.5
-    packed = _WINDOW.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), _stride(q, 0), _stride(q, 1), _stride(k, 0),
-                          _stride(k, 1), _stride(v, 0), _stride(v, 1), cu, cuk, T, Tk, N, H, Hk, d, _code(q),
-                          _int32(window, "window"), _int32(sinks, "sinks"), scale)
+    packed = _WINDOW.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), qt, qh, kt, kh, vt, vh, cu, cuk, T, Tk, N, H, Hk, d,
+                          _code(q), _int32(window, "window"), _int32(sinks, "sinks"), scale)
     return packed, (T, Tk, N, H, Hk, d)
 
 
@@ -861,25 +872,26 @@ def window_attention_backward(q, k, v, o, lse, d_o, window: int, sinks: int = 0,
 
 
 def _kv_cache(k_cache, v_cache, block_table, seq_lens, cu_seqlens, num_seqs):
-    """The packed kda_kv_cache, and the number of sequences."""
-    int32, dev = _lib_torch().int32, k_cache.device
-    if k_cache.dim() != 4 or not (k_cache.stride(3) == 1 or k_cache.shape[3] == 1):
+    """The packed kda_kv_cache, the number of sequences, and the cache's heads and
+    channels, type and device."""
+    int32, dev, dt, shape, s = _lib_torch().int32, k_cache.device, k_cache.dtype, k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or not (s[3] == 1 or shape[3] == 1):
         raise ValueError("k_cache: [pages, page_size, heads, channels] with a dense last axis")
-    if not (v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride() and
-            v_cache.dtype is k_cache.dtype and v_cache.device == dev):
+    if not (v_cache.shape == shape and v_cache.stride() == s and v_cache.dtype is dt and v_cache.device == dev):
         raise ValueError("v_cache: shape, strides, type and device of k_cache")
     if cu_seqlens is not None:
         N = _offsets(cu_seqlens, "cu_seqlens", dev)
     else:
         N = _int32(num_seqs, "num_seqs") if num_seqs is not None else seq_lens.shape[0]
-    if not (block_table.dtype is int32 and block_table.dim() == 2 and block_table.shape[0] == N and
-            block_table.device == dev and block_table.is_contiguous()):
+    rows = block_table.shape
+    if not (len(rows) == 2 and rows[0] == N and block_table.dtype is int32 and block_table.device == dev and
+            block_table.is_contiguous()):
         raise ValueError("block_table: contiguous int32 [N, max_pages], on the cache's device")
     _dense(seq_lens, "seq_lens", (N,), int32, dev)
-    P, page = k_cache.shape[:2]
-    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), _stride(k_cache, 0), _stride(k_cache, 1),
-                          _stride(k_cache, 2), block_table.data_ptr(), seq_lens.data_ptr(), P, page,
-                          block_table.shape[1]), N
+    P, page, H, d = shape
+    packed = _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), s[0] if P > 1 else 0, s[1] if page > 1 else 0,
+                            s[2] if H > 1 else 0, block_table.data_ptr(), seq_lens.data_ptr(), P, page, rows[1])
+    return packed, N, H, d, dt, dev
 
 
 def window_decode_workspace_bytes(d: int) -> int:
@@ -900,11 +912,9 @@ def window_decode(q, k_cache, v_cache, block_table, seq_lens, window: int, sinks
     T / N each.  Returns (o [T, H, d], lse [T, H] fp32)."""
     if q.dim() != 3:
         raise ValueError("q: [T, H, d]")
-    T, H, d = q.shape
-    cache, N = _kv_cache(k_cache, v_cache, block_table, seq_lens, cu_seqlens, num_seqs)
-    dev, dt = k_cache.device, k_cache.dtype
-    Hk = k_cache.shape[2]
-    _rows3(q, "q", (T, H, k_cache.shape[3]), dt, dev)
+    T, H, _ = q.shape
+    cache, N, Hk, d, dt, dev = _kv_cache(k_cache, v_cache, block_table, seq_lens, cu_seqlens, num_seqs)
+    qt, qh = _strides3(q, "q", T, H, d, dt, dev)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
@@ -927,7 +937,7 @@ def window_decode(q, k_cache, v_cache, block_table, seq_lens, window: int, sinks
         _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
         need = workspace.numel() * workspace.element_size()
     st = handle.kda_window_decode(
-        cache, q.data_ptr(), _stride(q, 0), _stride(q, 1), _ptr(cu_seqlens), T, N, H, Hk, d, _code(q),
+        cache, q.data_ptr(), qt, qh, None if cu_seqlens is None else cu_seqlens.data_ptr(), T, N, H, Hk, d, _code(q),
         _int32(window, "window"), _int32(sinks, "sinks"), d ** -0.5 if scale is None else scale, out.data_ptr(),
         lse.data_ptr(), workspace.data_ptr() or None, need, _raw_stream(dev))
     if st:
@@ -946,14 +956,13 @@ def kv_append(k_cache, v_cache, k, v, block_table, seq_lens, cu_seqlens=None, nu
     no norm; inv_freq: fp32 [dr / 2], or None for no rotation, of channels [start,
     start + dr); mscale multiplies the rotated part.  k_out: True (allocate) or a
     dense [T, Hk, d] tensor for the keys as they are cached.  Returns k_out."""
-    if k.dim() != 3:
+    if k.dim() != 3 or v.dim() != 3:
         raise ValueError("k, v: [T, Hk, d]")
-    T, Hk, d = k.shape
-    cache, N = _kv_cache(k_cache, v_cache, block_table, seq_lens, cu_seqlens, num_seqs)
-    dev, dt, float32 = k_cache.device, k_cache.dtype, _torch.float32
-    shape = (T, k_cache.shape[2], k_cache.shape[3])
-    _rows3(k, "k", shape, dt, dev)
-    _rows3(v, "v", shape, dt, dev)
+    T = k.shape[0]
+    cache, N, Hk, d, dt, dev = _kv_cache(k_cache, v_cache, block_table, seq_lens, cu_seqlens, num_seqs)
+    float32 = _torch.float32
+    kt, kh = _strides3(k, "k", T, Hk, d, dt, dev)
+    vt, vh = _strides3(v, "v", T, Hk, d, dt, dev)
     if norm_weight is not None:
         _dense(norm_weight, "norm_weight", (d,), float32, dev)
     dr = 0
@@ -972,21 +981,21 @@ def kv_append(k_cache, v_cache, k, v, block_table, seq_lens, cu_seqlens=None, nu
     else:
         _dense(k_out, "k_out", (T, Hk, d), dt, dev)
     st = lib().kda_kv_append(
-        cache, k.data_ptr(), _stride(k, 0), _stride(k, 1), v.data_ptr(), _stride(v, 0), _stride(v, 1), _ptr(cu_seqlens),
-        T, N, Hk, d, _code(k), _ptr(norm_weight), eps, _ptr(inv_freq) if dr else None, _int32(start, "start"), dr, mscale,
+        cache, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, None if cu_seqlens is None else cu_seqlens.data_ptr(), T, N, Hk, d, _code(k), _ptr(norm_weight), eps, _ptr(inv_freq) if dr else None, _int32(start, "start"), dr, mscale,
         KDA_ROTARY_INTERLEAVED if interleaved else 0, _ptr(k_out), _raw_stream(dev))
     if st:
         _check(st, "kda_kv_append")
     return k_out
 
 
-def _norm_tensors(x, name, weight, shape, dtype, device):
-    _rows3(x, name, shape, dtype, device)
-    if weight is not None:
-        _dense(weight, f"{name}_weight", (shape[2],), _torch.float32, device)
+def _norm_weight(weight, name, d, device) -> int:
+    if weight is None:
+        return 0
+    _dense(weight, name, (d,), _torch.float32, device)
+    return weight.data_ptr()
 
 
-def _norm_rotation(q, positions, inv_freq, T, dev):
+def _norm_rotation(positions, inv_freq, T, dev):
     """Rotated channels, with the rotation's arguments checked."""
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq: both or neither")
@@ -1015,12 +1024,15 @@ def qk_norm_rotary(q, k=None, q_weight=None, k_weight=None, positions=None, inv_
     torch = _lib_torch()
     T, H, d = q.shape
     dev, dt = q.device, q.dtype
-    _norm_tensors(q, "q", q_weight, (T, H, d), dt, dev)
+    qt, qh = _strides3(q, "q", T, H, d, dt, dev)
+    qw = _norm_weight(q_weight, "q_weight", d, dev)
     if k is not None:
-        _norm_tensors(k, "k", k_weight, (T, k.shape[1], d), dt, dev)
+        Hk = k.shape[1]
+        kt, kh = _strides3(k, "k", T, Hk, d, dt, dev)
+        kw = _norm_weight(k_weight, "k_weight", d, dev)
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    dr = _norm_rotation(q, positions, inv_freq, T, dev)
+    dr = _norm_rotation(positions, inv_freq, T, dev)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
@@ -1028,18 +1040,18 @@ def qk_norm_rotary(q, k=None, q_weight=None, k_weight=None, positions=None, inv_
                                   k_out)
     if q_out is None:
         q_out = torch.empty((T, H, d), dtype=dt, device=dev)
-    elif q_out is not q:
-        _rows3(q_out, "q_out", (T, H, d), dt, dev)
-    a = _NORM_HEADS.pack(q.data_ptr(), _stride(q, 0), _stride(q, 1), q_out.data_ptr(), _stride(q_out, 0),
-                         _stride(q_out, 1), _ptr(q_weight) or 0, 0, 0, 0, 0, 0, 0, 0, H)
+        ot, oh = H * d, d
+    else:
+        ot, oh = _strides3(q_out, "q_out", T, H, d, dt, dev)
+    a = _NORM_HEADS.pack(q.data_ptr(), qt, qh, q_out.data_ptr(), ot, oh, qw, 0, 0, 0, 0, 0, 0, 0, H)
     b = None
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=dt, device=dev)
-        elif k_out is not k:
-            _rows3(k_out, "k_out", (T, k.shape[1], d), dt, dev)
-        b = _NORM_HEADS.pack(k.data_ptr(), _stride(k, 0), _stride(k, 1), k_out.data_ptr(), _stride(k_out, 0),
-                             _stride(k_out, 1), _ptr(k_weight) or 0, 0, 0, 0, 0, 0, 0, 0, k.shape[1])
+            k_out = torch.empty((T, Hk, d), dtype=dt, device=dev)
+            ot, oh = Hk * d, d
+        else:
+            ot, oh = _strides3(k_out, "k_out", T, Hk, d, dt, dev)
+        b = _NORM_HEADS.pack(k.data_ptr(), kt, kh, k_out.data_ptr(), ot, oh, kw, 0, 0, 0, 0, 0, 0, 0, Hk)
     st = lib().kda_qk_norm_rotary(a, b, _ptr(positions) if dr else None, _ptr(inv_freq) if dr else None, T, d,
                                   _int32(start, "start"), dr, _code(q), eps, mscale,
                                   KDA_ROTARY_INTERLEAVED if interleaved else 0, _raw_stream(dev))
@@ -1066,16 +1078,12 @@ def qk_norm_rotary_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, 
     torch = _lib_torch()
     T, H, d = q.shape
     dev, dt = q.device, q.dtype
-    _norm_tensors(q, "q", q_weight, (T, H, d), dt, dev)
-    _rows3(dq_out, "dq_out", (T, H, d), dt, dev)
-    if k is not None:
-        if dk_out is None:
-            raise ValueError("dk_out: it goes with k")
-        _norm_tensors(k, "k", k_weight, (T, k.shape[1], d), dt, dev)
-        _rows3(dk_out, "dk_out", (T, k.shape[1], d), dt, dev)
-    elif k_weight is not None or dk_out is not None or dk is not None:
-        raise ValueError("k_weight, dk_out and dk need k")
-    dr = _norm_rotation(q, positions, inv_freq, T, dev)
+    if k is None:
+        if k_weight is not None or dk_out is not None or dk is not None:
+            raise ValueError("k_weight, dk_out and dk need k")
+    elif dk_out is None:
+        raise ValueError("dk_out: it goes with k")
+    dr = _norm_rotation(positions, inv_freq, T, dev)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
@@ -1083,18 +1091,20 @@ def qk_norm_rotary_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, 
                                            interleaved, mscale, eps, dq, dk, workspace)
 
     def heads(x, name, dy, dx, weight):
+        H = x.shape[1]
+        xt, xh = _strides3(x, name, T, H, d, dt, dev)
+        yt, yh = _strides3(dy, f"d{name}_out", T, H, d, dt, dev)
+        w = _norm_weight(weight, f"{name}_weight", d, dev)
         if dx is None:
-            dx = torch.empty(x.shape, dtype=dt, device=dev)
-        else:
-            _rows3(dx, name, tuple(x.shape), dt, dev)
+            dx = torch.empty((T, H, d), dtype=dt, device=dev)
+        dt_, dh = _strides3(dx, f"d{name}", T, H, d, dt, dev)
         dw = torch.empty(d, dtype=torch.float32, device=dev) if weight is not None else None
-        packed = _NORM_HEADS.pack(x.data_ptr(), _stride(x, 0), _stride(x, 1), 0, 0, 0, _ptr(weight) or 0, dy.data_ptr(),
-                                  _stride(dy, 0), _stride(dy, 1), dx.data_ptr(), _stride(dx, 0), _stride(dx, 1),
-                                  _ptr(dw) or 0, x.shape[1])
+        packed = _NORM_HEADS.pack(x.data_ptr(), xt, xh, 0, 0, 0, w, dy.data_ptr(), yt, yh, dx.data_ptr(), dt_, dh,
+                                  0 if dw is None else dw.data_ptr(), H)
         return packed, dx, dw
 
-    a, dq, dqw = heads(q, "dq", dq_out, dq, q_weight)
-    b, dk, dkw = heads(k, "dk", dk_out, dk, k_weight) if k is not None else (None, None, None)
+    a, dq, dqw = heads(q, "q", dq_out, dq, q_weight)
+    b, dk, dkw = heads(k, "k", dk_out, dk, k_weight) if k is not None else (None, None, None)
     handle = lib()
     if workspace is None:
         need = handle.kda_qk_norm_rotary_backward_workspace_bytes(d)
