@@ -16,6 +16,15 @@ namespace kda {
 constexpr int DECODE_SLOTS = 1024;   // partial results of 16 rows each
 constexpr int DECODE_KEYS = 32;      // keys of a wave's step
 
+// Where the rows of a row tile whose keys are split belong, for the join: row r is
+// query head r % G of token first + r / G, and r runs from `row` over `rows` (0: there
+// is no such tile).
+struct DecodeTile {
+    int32_t first, row, rows, pad;
+};
+// Workspace: a DecodeTile for each row tile, then its partial results, a split after
+// another, 16 rows of o, m and l each.
+
 // A workgroup takes 16 query rows of a sequence and key head and a run of its
 // blocks of 32 keys; its 4 waves take the blocks in turns, each with its own running
 // maximum, sum and output, and are joined in LDS.  No barrier inside the walk: keys go
@@ -24,8 +33,8 @@ constexpr int DECODE_KEYS = 32;      // keys of a wave's step
 // block's products.
 template <typename E, int D>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_decode_kernel(const WindowArgs a,
-                                                                                   float* __restrict__ part, int tiles,
-                                                                                   int splits)
+                                                                                   DecodeTile* __restrict__ where,
+                                                                                   float* __restrict__ part, int splits)
 {
     constexpr int KS = D / 32, BN = DECODE_KEYS, CE = CHUNK_ELEMS<E>, CH = D / CE;   // 16-byte chunks of a row
     constexpr int RPI = 64 / CH, VI = BN / RPI;   // rows of a wave's load, loads of a block's values
@@ -36,18 +45,41 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_decode_ker
     __shared__ __attribute__((aligned(16))) char buffer[4][TILE > OUT ? TILE : OUT];
     __shared__ int64_t place[4][2][BN];
     __shared__ float stat[4][2][16];
+    __shared__ int found[3], scratch[6];
 
     const kda_window_inputs& in = a.in;
     const int unit = blockIdx.x / splits, split = blockIdx.x - unit * splits;
     const int h = unit % in.Hk, want = unit / in.Hk;
     const int rows_q = (int)(in.total_q / in.num_seqs), G = in.H / in.Hk;
-    int seq, tile;
-    if (!find_tile<16, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, want,
-                            reinterpret_cast<int*>(stat), seq, tile, G))
-        return;
-    int q0, q1;
-    sequence_rows(in.cu_seqlens_q, rows_q, (int)in.total_q, seq, q0, q1);
-    const int nk = uniform(cached_tokens(a.pages, seq)), nq = q1 - q0, off = nk - nq, rows = nq * G;
+    // the sequence, its rows and its cached tokens, looked up at once
+    int seq = -1, tile = 0, q0 = 0, q1 = 0, nk = 0;
+    if (in.cu_seqlens_q) {
+        int a0 = 0, a1 = 0, n = 0, mine = -1;
+        if (find_item<256>(in.num_seqs, want, scratch, seq, tile, [&](int s) {
+                sequence_rows(in.cu_seqlens_q, rows_q, (int)in.total_q, s, a0, a1);
+                n = cached_tokens(a.pages, s);
+                mine = s;
+                return ((a1 - a0) * G + 15) / 16;
+            })) {
+            if (mine == seq) found[0] = a0, found[1] = a1, found[2] = n;
+            __syncthreads();
+            q0 = uniform(found[0]), q1 = uniform(found[1]), nk = uniform(found[2]);
+        }
+    } else {
+        const int per = (rows_q * G + 15) / 16;
+        if (per > 0 && want < per * in.num_seqs) {
+            seq = want / per;
+            tile = want - seq * per;
+            sequence_rows(nullptr, rows_q, (int)in.total_q, seq, q0, q1);
+            nk = uniform(cached_tokens(a.pages, seq));
+        }
+    }
+    const int nq = q1 - q0, off = nk - nq, rows = nq * G;
+    // Row tiles are counted by a bound: behind the last one there is no sequence, and
+    // `tile` says nothing.
+    if (splits > 1 && split == 0 && threadIdx.x == 0)
+        where[unit] = seq < 0 ? DecodeTile{0, 0, 0, 0} : DecodeTile{q0, tile * 16, min(16, rows - tile * 16), 0};
+    if (seq < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
     const float sc = in.scale * LOG2E;
     auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
@@ -228,50 +260,76 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_decode_ker
     }
 }
 
-// Joins the splits' results of 16 rows, 16 threads to a row: with M = max_s m_s,
+// Joins the splits' results of a row tile: with M = max_s m_s,
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  in order.
+// 16 threads to a row; where there are few rows, several such groups share its splits,
+// whose sums are added in LDS.
 template <typename E, int D>
-__global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, const float* __restrict__ part, int splits)
+__global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, const DecodeTile* __restrict__ where,
+                                                          const float* __restrict__ part, int splits)
 {
-    __shared__ int scratch[8];
+    constexpr int PS = D + 4;
+    __shared__ __attribute__((aligned(16))) float joined[16][PS];
     const kda_window_inputs& in = a.in;
-    const int unit = blockIdx.x, h = unit % in.Hk, rows_q = (int)(in.total_q / in.num_seqs), G = in.H / in.Hk;
-    int seq, tile, q0, q1;
-    if (!find_tile<16, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, unit / in.Hk, scratch, seq, tile, G))
-        return;
-    sequence_rows(in.cu_seqlens_q, rows_q, (int)in.total_q, seq, q0, q1);
-    const int row = threadIdx.x >> 4, c0 = threadIdx.x & 15, r = tile * 16 + row;
-    if (r >= (q1 - q0) * G) return;
-    const int i = (int)((unsigned)r / (unsigned)G);
-    const int64_t out = (int64_t)(q0 + i) * in.H + h * G + r - i * G;
-    const float* from = part + ((int64_t)unit * splits * 16 + row) * (D + 4);
+    const int unit = blockIdx.x, h = unit % in.Hk, G = in.H / in.Hk;
+    const DecodeTile x = where[unit];
+    if (x.rows <= 0) return;
+    const int shift = x.rows > 8 ? 4 : x.rows > 4 ? 3 : x.rows > 2 ? 2 : x.rows > 1 ? 1 : 0;
+    const int c0 = threadIdx.x & 15, at = threadIdx.x >> 4, row = at & ((1 << shift) - 1), group = at >> shift,
+              groups = 16 >> shift;
+    const bool there = row < x.rows;
+    f32x4 y[D / 64];
     float top = neg_inf(), sum = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < splits; ++s) top = fmaxf(top, from[s * 16 * (D + 4) + D]);
-    const float base = top == neg_inf() ? 0.f : top;
-    f32x4 x[D / 64];
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) x[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < D / 64; ++c) y[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (there) {
+        const float* from = part + ((int64_t)unit * splits * 16 + row) * PS;
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
-        const float* p = from + s * 16 * (D + 4);
-        const float f = exp2_fast(p[D] - base);
-        sum += f * p[D + 1];
+        for (int s = group; s < splits; s += groups) top = fmaxf(top, from[s * 16 * PS + D]);
+        const float base = top == neg_inf() ? 0.f : top;
+#pragma unroll 8
+        for (int s = group; s < splits; s += groups) {
+            const float* p = from + s * 16 * PS;
+            const float f = exp2_fast(p[D] - base);
+            sum += f * p[D + 1];
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) x[c] += f * *reinterpret_cast<const f32x4*>(p + 64 * c + 4 * c0);
+            for (int c = 0; c < D / 64; ++c) y[c] += f * *reinterpret_cast<const f32x4*>(p + 64 * c + 4 * c0);
+        }
     }
+    if (groups > 1) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) store_vec(&joined[at][64 * c + 4 * c0], y[c]);
+        if (c0 == 0) joined[at][D] = top, joined[at][D + 1] = sum;
+        __syncthreads();
+        if (group > 0) return;
+        for (int i = 1; i < groups; ++i) top = fmaxf(top, joined[(i << shift) + row][D]);
+        const float base = top == neg_inf() ? 0.f : top;
+        sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) y[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < groups; ++i) {
+            const float* p = joined[(i << shift) + row];
+            const float f = exp2_fast(p[D] - base);
+            sum += f * p[D + 1];
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) y[c] += f * *reinterpret_cast<const f32x4*>(p + 64 * c + 4 * c0);
+        }
+    }
+    if (!there) return;
+    const int r = x.row + row, i = (int)((unsigned)r / (unsigned)G);
+    const int64_t out = (int64_t)(x.first + i) * in.H + h * G + r - i * G;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-        typename Vec<E>::v4 y;
+        typename Vec<E>::v4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = from_f32<E>(x[c][e] * inv);
-        store_vec((E*)a.o + out * D + 64 * c + 4 * c0, y);
+        for (int e = 0; e < 4; ++e) v[e] = from_f32<E>(y[c][e] * inv);
+        store_vec((E*)a.o + out * D + 64 * c + 4 * c0, v);
     }
     if (a.lse && c0 == 0) a.lse[out] = sum == 0.f ? neg_inf() : (top + __log2f(sum)) * LN2;
 }
 
-size_t window_decode_workspace(int32_t d) { return (size_t)DECODE_SLOTS * 16 * (d + 4) * 4; }
+size_t window_decode_workspace(int32_t d) { return (size_t)DECODE_SLOTS * (sizeof(DecodeTile) + 16 * (d + 4) * 4); }
 
 template <typename E, int D>
 static hipError_t launch(const WindowArgs& a, void* workspace, hipStream_t stream) {
@@ -283,12 +341,13 @@ static hipError_t launch(const WindowArgs& a, void* workspace, hipStream_t strea
     const int64_t most = std::min((int64_t)in.window + in.sinks + (in.total_q + N - 1) / N,
                                   (int64_t)a.pages.max_pages * a.pages.page_size);
     const int64_t splits = std::max<int64_t>(1, std::min((most + 127) / 128, DECODE_SLOTS / units));
-    hipLaunchKernelGGL((window_decode_kernel<E, D>), dim3((unsigned)(units * splits)), dim3(256), 0, stream, a,
-                       (float*)workspace, (int)tiles, (int)splits);
+    DecodeTile* where = (DecodeTile*)workspace;
+    float* part = (float*)(where + DECODE_SLOTS);
+    hipLaunchKernelGGL((window_decode_kernel<E, D>), dim3((unsigned)(units * splits)), dim3(256), 0, stream, a, where, part,
+                       (int)splits);
     if (const hipError_t e = launch_result(stream)) return e;
     if (splits == 1) return hipSuccess;
-    hipLaunchKernelGGL((window_join_kernel<E, D>), dim3((unsigned)units), dim3(256), 0, stream, a,
-                       (const float*)workspace, (int)splits);
+    hipLaunchKernelGGL((window_join_kernel<E, D>), dim3((unsigned)units), dim3(256), 0, stream, a, where, part, (int)splits);
     return launch_result(stream);
 }
 
