@@ -18,6 +18,18 @@
 
 namespace kda {
 
+// What the rounding of two accumulator tiles to an operand (acc_frag) left of them.
+// bf16: dq takes dz in two parts, 16 bits in all.  With one it was off by 1.5 times
+// what the rounding of dq itself costs (2.5e-3 against 1.65e-3 in the norm, packed
+// documents, window 1,024): by the rounding of dz and by delta, which comes from the
+// rounded o; with two by 1.1 times.  The second part costs 0.16 ms of dq's 1.00.
+__device__ __forceinline__ bf16x8 rest_frag(f32x4 a, f32x4 b, bf16x8 x) {
+    bf16x8 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = (bf16)(a[i] - (float)x[i]), y[4 + i] = (bf16)(b[i] - (float)x[4 + i]);
+    return y;
+}
+
 // dq and delta.  As in the forward kernel the scores are formed transposed (rows =
 // keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.  dq itself
 // takes delta from the rounded o, as its own sum is complete only behind the last
@@ -139,7 +151,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
             // g v^T, between whose products the weights' exponentials run; and,
             // after dz, dq^T += K^T dz.
             constexpr int E0 = TT * KS, E1 = 2 * E0, NS = NQ * TT * 4;
-            v8 y[2][NQ], dz[NQ];
+            v8 y[2][NQ], dz[NQ], rest[NQ];
             auto row_grads = [&](int ks) {
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) y[ks & 1][j] = load_frag(sgo[wave][j][ks], lane);
@@ -189,11 +201,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                                         s[j][tt][i] *= dp[j][tt][i] - dl[j];
                                     }
                                 dz[j] = acc_frag(s[j][0], s[j][1], E());
+                                if constexpr (sizeof(E) == 2) rest[j] = rest_frag(s[j][0], s[j][1], dz[j]);
                             }
                         }
                         constexpr int c = e - E1;
 #pragma unroll
                         for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[e % (PD + 1)], dz[j], acc[j][c]);
+                        if constexpr (sizeof(E) == 2)
+#pragma unroll
+                            for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[e % (PD + 1)], rest[j], acc[j][c]);
                     }
                 });
         }
