@@ -270,8 +270,8 @@ struct KeyWork {
 };
 
 // dk and dv.  A wave owns 16 keys, whose k and v operands and gradients stay in
-// registers; the query rows come 32 tokens of one head at a time, head after head
-// of the group.  The scores are formed with rows = queries, so that the weights and
+// registers; the query rows come 64 tokens of one head at a time (fp32: 32), head after
+// head of the group, and are worked on 32 at a time.  The scores are formed with rows = queries, so that the weights and
 // dz are the operands of dv^T += g^T w and dk^T += q^T dz as they stand.
 template <typename E, int D>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(
@@ -279,13 +279,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
     E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ part, int items)
 {
-    constexpr int BQ = 32, BK = DKV_KEYS, KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int SUBS = sizeof(E) == 2 ? 2 : 1, BQ = 32 * SUBS, BK = DKV_KEYS, KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
     // two arrays, so that a read of one is seen not to wait for loads into the other
     __shared__ __attribute__((aligned(16))) E even[BQ * 2 * D];
     __shared__ __attribute__((aligned(16))) E odd[BQ * 2 * D];
     __shared__ __attribute__((aligned(16))) float srow[2][2 * BQ];   // lse (base 2), then delta
-    __shared__ unsigned bad_rows[2];                                 // a bit for each row to be taken out
+    __shared__ unsigned long long bad_rows[2];                       // a bit for each row to be taken out
 
     int h, want, seq, item;
     key_head_of_block(in.Hk, items, blockIdx.x, h, want);
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     const E* gp = d_o + ((int64_t)(work.q0 + ta) * in.H + h * G) * D;
     const float* sp = row_stats + 2 * ((int64_t)h * G * in.total_q + work.q0 + ta);
 
-    // A head's tiles [td, tw): 32 rows that all see all of the workgroup's keys.
+    // A head's tiles [td, tw): rows that all see all of the workgroup's keys.
     const int td = max(0, key0 + BK - 1 - (ta + off) + BQ - 1) / BQ;
     const int tw = min((te - ta) / BQ, max(0, key0 + W - (ta + off)) / BQ);
     // lse and delta of a row travel with one of the first BQ threads.
@@ -351,10 +351,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
         if (tid < BQ) {
             const bool bad = tid < te - ta - t * BQ && (!(__builtin_fabsf(next_lse) < __builtin_inff()) ||
                                                         !(__builtin_fabsf(next_delta) < __builtin_inff()));
-            const unsigned rows = (unsigned)__ballot(bad);
+            const unsigned long long rows = __ballot(bad);
             srow[u & 1][tid] = bad ? __builtin_nanf("") : next_lse;
             srow[u & 1][BQ + tid] = bad ? 0.f : next_delta;
-            if (tid == 0) bad_rows[u & 1] = t >= td && t < tw ? 0u : rows;
+            if (tid == 0) bad_rows[u & 1] = rows;
         }
         landed();
     };
@@ -374,19 +374,23 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     auto step = [&](int u, int t, int nhead, int nt, E* Q, E* next) __attribute__((always_inline)) {
         rows_of.keep(), cols_of.keep();
         E* Gt = Q + BQ * D;
-        const float* R = srow[u & 1];
-        const int p0 = ta + t * BQ + off, p1 = min(p0 + BQ, te + off) - 1;   // positions of the tile's rows
         if (u + 1 < nu) load(nhead, nt, next);
-        if (const unsigned bad = uniform((int)bad_rows[u & 1])) {
+        if (t < td || t >= tw)
+            if (const unsigned long long bad = (unsigned long long)uniform((int64_t)bad_rows[u & 1])) {
 #pragma unroll
-            for (int i = 0; i < q_tiles.N; ++i)
-                if (bad >> q_tiles.row(i) & 1) {
-                    *reinterpret_cast<u32x4*>(Q + (i * 256 + tid) * q_tiles.CE) = u32x4{0, 0, 0, 0};
-                    *reinterpret_cast<u32x4*>(Gt + (i * 256 + tid) * q_tiles.CE) = u32x4{0, 0, 0, 0};
-                }
-            __syncthreads();
-        }
-        if (p1 >= wkey && (p0 - (wkey + 15) < W || wkey < in.sinks)) {
+                for (int i = 0; i < q_tiles.N; ++i)
+                    if (bad >> q_tiles.row(i) & 1) {
+                        *reinterpret_cast<u32x4*>(Q + (i * 256 + tid) * q_tiles.CE) = u32x4{0, 0, 0, 0};
+                        *reinterpret_cast<u32x4*>(Gt + (i * 256 + tid) * q_tiles.CE) = u32x4{0, 0, 0, 0};
+                    }
+                __syncthreads();
+            }
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub) {
+            const float* R = srow[u & 1] + 32 * sub;
+            // positions of these rows
+            const int p0 = ta + t * BQ + 32 * sub + off, p1 = min(p0 + 32, te + off) - 1;
+            if (p1 < max(p0, wkey) || (p0 - (wkey + 15) >= W && wkey >= in.sinks)) continue;
             f32x4 s[2], dp[2];
             v8 x[PD + 1];
 #pragma unroll
@@ -402,10 +406,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
             ahead<E2 + D / 16, PD>(
                 [&](auto n) {
                     constexpr int e = n;
-                    x[e % (PD + 1)] = e < E0   ? rows_of(Q, 16 * (e % 2), e / 2)
-                                      : e < E1 ? rows_of(Gt, 16 * ((e - E0) % 2), (e - E0) / 2)
-                                      : e < E2 ? cols_of(Gt, 0, 16, e - E1)
-                                               : cols_of(Q, 0, 16, e - E2);
+                    x[e % (PD + 1)] = e < E0   ? rows_of(Q, 32 * sub + 16 * (e % 2), e / 2)
+                                      : e < E1 ? rows_of(Gt, 32 * sub + 16 * ((e - E0) % 2), (e - E0) / 2)
+                                      : e < E2 ? cols_of(Gt, 32 * sub, 32 * sub + 16, e - E1)
+                                               : cols_of(Q, 32 * sub, 32 * sub + 16, e - E2);
                 },
                 [&](auto n) {
                     constexpr int e = n;
