@@ -39,14 +39,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     const kda_window_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
     const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ row_stats, int tiles)
 {
-    constexpr int BN = 32, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
-    constexpr int KS = D / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
+    // keys of a tile, worked on 32 at a time
+    constexpr int SUBS = sizeof(E) == 2 ? 2 : 1, BN = 32 * SUBS, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
+    constexpr int KS = D / 32, TT = 2, PD = sizeof(E) == 2 ? 3 : 1;
     typedef typename Vec<E>::v8 v8;
     // two arrays, so that a read of one is seen not to wait for loads into the other
     __shared__ __attribute__((aligned(16))) E even[BN * 2 * D];
     __shared__ __attribute__((aligned(16))) E odd[BN * 2 * D];
-    // the rows' output gradients: each wave's own, in operand order
-    __shared__ __attribute__((aligned(16))) E sgo[4][NQ][KS][64 * 8];
 
     int h, want, seq, tile;
     key_head_of_block(in.Hk, tiles, blockIdx.x, h, want);
@@ -71,7 +70,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     const E* kp = (const E*)in.k + (int64_t)k0 * in.k_token_stride + h * in.k_head_stride;
     const E* vp = (const E*)in.v + (int64_t)k0 * in.v_token_stride + h * in.v_head_stride;
 
-    v8 q[NQ][KS];
+    v8 q[NQ][KS], go[NQ][KS];   // the rows and their output gradients
     int first[NQ];   // the first key number behind the sinks that the row sees
     float lse2[NQ], dl[NQ], exact[NQ];   // delta from the rounded o, and from this kernel's own weights
 #pragma unroll
@@ -84,10 +83,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
         float sum = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            const v8 gv = row_frag_global(d_o + at * D, ks, lane), ov = row_frag_global(o + at * D, ks, lane);
-            store_frag(sgo[wave][j][ks], lane, gv);
+            go[j][ks] = row_frag_global(d_o + at * D, ks, lane);
+            const v8 ov = row_frag_global(o + at * D, ks, lane);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum += to_f32(gv[e]) * to_f32(ov[e]);
+            for (int e = 0; e < 8; ++e) sum += to_f32(go[j][ks][e]) * to_f32(ov[e]);
         }
         lse2[j] = lse[at] * LOG2E;
         // a row that sees no key has o = 0, and 0 times a d_o of NaN or Inf is NaN
@@ -134,13 +133,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 #pragma unroll
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]);
+        for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]), arrived(go[j][ks]);
     auto step = [&](int t, const E* K, E* next) __attribute__((always_inline)) {
         rows_of.keep(), k_cols.keep();
         const E* V = K + BN * D;
-        const int n0 = t * BN;
         if (t + 1 < nt) load(t + 1, next);
-        if (wrow < rows && n0 <= last_hi && (n0 < kr.ns || n0 + BN > first_lo)) {
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub) {
+            const int n0 = t * BN + 32 * sub;
+            if (wrow >= rows || n0 > last_hi || (n0 >= kr.ns && n0 + 32 <= first_lo)) continue;
             f32x4 s[NQ][TT], dp[NQ][TT];
             v8 x[PD + 1];
 #pragma unroll
@@ -151,29 +152,23 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
             // g v^T, between whose products the weights' exponentials run; and,
             // after dz, dq^T += K^T dz.
             constexpr int E0 = TT * KS, E1 = 2 * E0, NS = NQ * TT * 4;
-            v8 y[2][NQ], dz[NQ], rest[NQ];
-            auto row_grads = [&](int ks) {
-#pragma unroll
-                for (int j = 0; j < NQ; ++j) y[ks & 1][j] = load_frag(sgo[wave][j][ks], lane);
-            };
+            v8 dz[NQ], rest[NQ];
             ahead<E1 + D / 16, PD>(
                 [&](auto n) {
                     constexpr int e = n;
-                    x[e % (PD + 1)] = e < E0   ? rows_of(K, 16 * (e % TT), e / TT)
-                                      : e < E1 ? rows_of(V, 16 * ((e - E0) % TT), (e - E0) / TT)
-                                               : k_cols(K, 0, 16, e - E1);
+                    x[e % (PD + 1)] = e < E0   ? rows_of(K, 32 * sub + 16 * (e % TT), e / TT)
+                                      : e < E1 ? rows_of(V, 32 * sub + 16 * ((e - E0) % TT), (e - E0) / TT)
+                                               : k_cols(K, 32 * sub, 32 * sub + 16, e - E1);
                 },
                 [&](auto n) {
                     constexpr int e = n;
                     if constexpr (e < E0) {
-                        if (e == E0 - TT) row_grads(0);
 #pragma unroll
                         for (int j = 0; j < NQ; ++j) s[j][e % TT] = mma32(x[e % (PD + 1)], q[j][e / TT], s[j][e % TT]);
                     } else if constexpr (e < E1) {
                         constexpr int f = e - E0;
-                        if (f % TT == 0 && f / TT + 1 < KS) row_grads(f / TT + 1);
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j) dp[j][f % TT] = mma32(x[e % (PD + 1)], y[f / TT & 1][j], dp[j][f % TT]);
+                        for (int j = 0; j < NQ; ++j) dp[j][f % TT] = mma32(x[e % (PD + 1)], go[j][f / TT], dp[j][f % TT]);
 #pragma unroll
                         for (int m = NS * f / E0; m < NS * (f + 1) / E0; ++m) {
                             const int j = m / (TT * 4), tt = m / 4 % TT, i = m % 4;
@@ -181,7 +176,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                         }
                     } else {
                         if (e == E1) {
-                            if (!kr.whole(n0, n0 + BN, last_lo, first_hi)) {   // weights of hidden keys
+                            if (!kr.whole(n0, n0 + 32, last_lo, first_hi)) {   // weights of hidden keys
 #pragma unroll
                                 for (int j = 0; j < NQ; ++j)
 #pragma unroll
