@@ -135,6 +135,14 @@ template <int W, int CT> struct ColReader<float, W, CT> {
         }
         return v;
     }
+    // Slots 0 to 3 alone.
+    __device__ __forceinline__ f32x8 half(const float* t, int ra, int ct) const {
+        const int g4 = 4 * (lane >> 4), c = 16 * (ct0 + ct) + (lane & 15);
+        f32x8 v = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = t[tile_at<float, W>(ra + g4 + i, c >> 2) + (c & 3)];
+        return v;
+    }
 };
 
 // Two accumulator tiles (rows 4g + i of two 16-row blocks) as the 8 slots of

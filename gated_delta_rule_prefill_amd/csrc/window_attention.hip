@@ -15,15 +15,18 @@
 
 namespace kda {
 
-// A workgroup: 4 waves of 32 (bf16) or 16 (fp32) query rows, whose operands q and
-// o stay in registers, one key head.  Key and value tiles of BN rows are
-// double-buffered in LDS: the next tile's global loads are issued before a tile's
-// products and stored to LDS behind them.
-template <typename E, int D, bool PAGED>
+// A workgroup of 4 waves, one key head.  A wave has 32 (fp32: 16) query rows, whose
+// operands q and o stay in registers, and walks all keys.  SPLIT (fp32, few rows; see
+// split_waves): the workgroup has 16 rows, a wave walks a quarter of each tile's keys
+// with a maximum and sum of its own, and the four are joined behind the last.  Key and
+// value tiles of BN rows are double-buffered in LDS: the next tile's loads, straight
+// into LDS, are issued before a tile's products.
+template <typename E, int D, bool PAGED, bool SPLIT>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_kernel(const WindowArgs a, int tiles)
 {
-    constexpr int BN = 128 / (int)sizeof(E), NQ = LATENT_NQ<E>, BQ = 64 * NQ;
-    constexpr int KS = D / 32, TT = BN / 16, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int BN = sizeof(E) == 2 || SPLIT ? 64 : 32, NQ = LATENT_NQ<E>, BQ = WINDOW_ROWS<E, SPLIT>;
+    constexpr int KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int TT = SPLIT ? 1 : BN / 16, PAIR = SPLIT ? 1 : 2;   // a wave's key tiles, and those by turns
     typedef typename Vec<E>::v8 v8;
     // two arrays, so that a read of one is seen not to wait for loads into the other
     __shared__ __attribute__((aligned(16))) E even[BN * 2 * D];
@@ -33,7 +36,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
 
     const kda_window_inputs& in = a.in;
     int h, want, seq, tile;
-    key_head_of_block(in.Hk, tiles, blockIdx.x, h, want);
+    if (block_of_grid() >= (int64_t)tiles * in.Hk) return;
+    key_head_of_block(in.Hk, tiles, (int)block_of_grid(), h, want);
     const int rows_q = (int)(in.total_q / in.num_seqs), G = in.H / in.Hk;
     if (!find_tile<BQ, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, tiles - 1 - want,
                             reinterpret_cast<int*>(even), seq, tile, G))
@@ -50,7 +54,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
     }
     const int nq = q1 - q0, off = nk - nq, rows = nq * G;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
-    const int wrow = tile * BQ + 16 * NQ * wave;   // the wave's first row
+    const int wrow = SPLIT ? tile * BQ : tile * BQ + 16 * NQ * wave;   // the wave's first row
     const float sc = in.scale * LOG2E;
     auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
     const KeyRange kr(uniform(token(tile * BQ)), uniform(token(tile * BQ + BQ - 1)), off, in.window, in.sinks, nk);
@@ -157,14 +161,14 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
     auto step = [&](int t, const E* K, E* next) __attribute__((always_inline)) {
         k_rows.keep(), v_cols.keep();
         const E* V = K + BN * D;
-        const int n0 = t * BN;
+        const int r0 = SPLIT ? 16 * wave : 0, n0 = t * BN + r0;   // the wave's first key of the tile
         if (t + 1 < nt) load(t + 1, next);
         if constexpr (PAGED)
             if (tid < BN) {
                 keep(t + 2, next_place);
                 next_place = look_up(t + 3);
             }
-        if (wrow < rows && n0 <= last_hi && (n0 < kr.ns || n0 + BN > first_lo)) {
+        if (wrow < rows && n0 <= last_hi && (n0 < kr.ns || n0 + 16 * TT > first_lo)) {
             f32x4 s[NQ][TT];
             v8 x[PD + 1];
 #pragma unroll
@@ -175,9 +179,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
             // two key tiles by turns so that products in a row do not wait for
             // each other; and, after the weights, the product with the values.
             constexpr int E0 = TT * KS;
-            v8 p[NQ][TT / 2];
+            v8 p[NQ][TT / PAIR];
             auto take_weights = [&]() {
-                if (!kr.whole(n0, n0 + BN, last_lo, first_hi)) {
+                if (!kr.whole(n0, n0 + 16 * TT, last_lo, first_hi)) {
 #pragma unroll
                     for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -192,7 +196,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
                         for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                if (place[t & 3][16 * tt + 4 * g + i] < 0)
+                                if (place[t & 3][r0 + 16 * tt + 4 * g + i] < 0)
 #pragma unroll
                                     for (int j = 0; j < NQ; ++j) s[j][tt][i] = neg_inf();
                     }
@@ -233,27 +237,29 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
                             l[j] += s[j][tt][i];   // the sum takes the weights before their rounding
                         }
 #pragma unroll
-                    for (int b = 0; b < TT / 2; ++b) p[j][b] = acc_frag(s[j][2 * b], s[j][2 * b + 1], E());
+                    for (int b = 0; b < TT / PAIR; ++b)
+                        p[j][b] = acc_frag(s[j][PAIR * b], s[j][PAIR * b + PAIR - 1], E());
                 }
             };
-            ahead<E0 + D / 16 * (TT / 2), PD>(
+            auto tt_of = [](int e) constexpr { return e / (PAIR * KS) * PAIR + e % PAIR; };
+            ahead<E0 + D / 16 * (TT / PAIR), PD>(
                 [&](auto n) {
                     constexpr int e = n, f = e - E0;
-                    if constexpr (e < E0) x[e % (PD + 1)] = k_rows(K, 16 * (e / (2 * KS) * 2 + e % 2), e / 2 % KS);
-                    else x[e % (PD + 1)] = v_cols(V, 32 * (f / (D / 16)), 32 * (f / (D / 16)) + 16, f % (D / 16));
+                    if constexpr (e < E0) x[e % (PD + 1)] = k_rows(K, r0 + 16 * tt_of(e), e / PAIR % KS);
+                    else x[e % (PD + 1)] = cols<PAIR>(v_cols, V, r0 + 16 * PAIR * (f / (D / 16)), f % (D / 16));
                 },
                 [&](auto n) {
                     constexpr int e = n, f = e - E0;
                     if constexpr (e < E0) {
+                        constexpr int tt = tt_of(e);
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j)
-                            s[j][e / (2 * KS) * 2 + e % 2] =
-                                mma32(x[e % (PD + 1)], q[j][e / 2 % KS], s[j][e / (2 * KS) * 2 + e % 2]);
+                        for (int j = 0; j < NQ; ++j) s[j][tt] = mma32(x[e % (PD + 1)], q[j][e / PAIR % KS], s[j][tt]);
                     } else {
                         if constexpr (f == 0) take_weights();
 #pragma unroll
                         for (int j = 0; j < NQ; ++j)
-                            acc[j][f % (D / 16)] = mma32(x[e % (PD + 1)], p[j][f / (D / 16)], acc[j][f % (D / 16)]);
+                            acc[j][f % (D / 16)] =
+                                mma_rows<PAIR>(x[e % (PD + 1)], p[j][f / (D / 16)], acc[j][f % (D / 16)]);
                     }
                 });
         }
@@ -266,6 +272,26 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
         step(t + 1, odd, even);
     }
     if (t < nt) step(t, even, odd);
+    // SPLIT: the four waves' parts brought to the largest maximum and added up in order, a
+    // quarter of the channels each
+    constexpr int OWN = SPLIT ? D / 64 : D / 16;
+    const int own = SPLIT ? wave * OWN : 0;
+    if constexpr (SPLIT) {
+        odd[tid] = m[0];
+        __syncthreads();
+        float top = neg_inf();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, odd[64 * w + lane]);
+        const float f = m[0] == neg_inf() ? 0.f : exp2_fast(m[0] - top);   // no key: its sums are 0
+        m[0] = top;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) acc[0][c] *= f;
+        odd[256 + tid] = l[0] * f;
+        join_waves<E, D>(even, wave, col, g, acc[0]);
+        l[0] = odd[256 + lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) l[0] += odd[256 + 64 * w + lane];
+    }
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;
@@ -274,28 +300,30 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
         const int i = token(r);
         const int64_t out = (int64_t)(q0 + i) * in.H + h * G + r - i * G;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        E* row = (E*)a.o + out * D;
+        E* row = (E*)a.o + out * D + 16 * own;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < OWN; ++c) {
             typename Vec<E>::v4 x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(acc[j][c][i] * inv);
             store_vec(row + 16 * c + 4 * g, x);
         }
-        if (a.lse && g == 0) a.lse[out] = sum == 0.f ? neg_inf() : (m[j] + __log2f(sum)) * LN2;
+        if (a.lse && g == 0 && own == 0) a.lse[out] = sum == 0.f ? neg_inf() : (m[j] + __log2f(sum)) * LN2;
     }
 }
 
-template <typename E, int D, bool PAGED>
-static hipError_t launch(const WindowArgs& a, hipStream_t stream) {
-    constexpr int BQ = 64 * LATENT_NQ<E>;
-    const kda_window_inputs& in = a.in;
-    const int64_t G = in.H / in.Hk;
-    const int64_t tiles = in.cu_seqlens_q ? in.total_q * G / BQ + in.num_seqs
-                                          : (in.total_q / in.num_seqs * G + BQ - 1) / BQ * in.num_seqs;
-    hipLaunchKernelGGL((window_attention_kernel<E, D, PAGED>), dim3((unsigned)(tiles * in.Hk)), dim3(256), 0, stream, a,
+template <typename E, int D, bool PAGED, bool SPLIT>
+static hipError_t launch_as(const WindowArgs& a, hipStream_t stream) {
+    const int64_t tiles = row_tiles(a.in, WINDOW_ROWS<E, SPLIT>);
+    hipLaunchKernelGGL((window_attention_kernel<E, D, PAGED, SPLIT>), grid_of(tiles * a.in.Hk), dim3(256), 0, stream, a,
                        (int)tiles);
     return launch_result(stream);
+}
+template <typename E, int D, bool PAGED>
+static hipError_t launch(const WindowArgs& a, hipStream_t stream) {
+    if constexpr (sizeof(E) == 4)
+        if (split_waves(a.in)) return launch_as<E, D, PAGED, true>(a, stream);
+    return launch_as<E, D, PAGED, false>(a, stream);
 }
 
 hipError_t launch_window_attention(const WindowArgs& a, bool paged, hipStream_t stream) {

@@ -34,21 +34,25 @@ __device__ __forceinline__ bf16x8 rest_frag(f32x4 a, f32x4 b, bf16x8 x) {
 // keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.  dq itself
 // takes delta from the rounded o, as its own sum is complete only behind the last
 // key; the second kernel takes that sum.
-template <typename E, int D>
+// A wave owns 32 rows (fp32: 16) and walks all keys, 32 at a time.  SPLIT (fp32, few
+// rows; see split_waves): the workgroup has 16 rows, a wave walks a quarter of each
+// tile's keys, and the waves' sums are added up in order.
+template <typename E, int D, bool SPLIT>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     const kda_window_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
     const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ row_stats, int tiles)
 {
-    // keys of a tile, worked on 32 at a time
-    constexpr int SUBS = sizeof(E) == 2 ? 2 : 1, BN = 32 * SUBS, NQ = LATENT_NQ<E>, BQ = 64 * NQ;
-    constexpr int KS = D / 32, TT = 2, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int BN = sizeof(E) == 2 || SPLIT ? 64 : 32, NQ = LATENT_NQ<E>, BQ = WINDOW_ROWS<E, SPLIT>;
+    constexpr int KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int TT = SPLIT ? 1 : 2, SUBS = SPLIT ? 1 : BN / 32;   // key tiles worked on at a time, and how often
     typedef typename Vec<E>::v8 v8;
     // two arrays, so that a read of one is seen not to wait for loads into the other
     __shared__ __attribute__((aligned(16))) E even[BN * 2 * D];
     __shared__ __attribute__((aligned(16))) E odd[BN * 2 * D];
 
     int h, want, seq, tile;
-    key_head_of_block(in.Hk, tiles, blockIdx.x, h, want);
+    if (block_of_grid() >= (int64_t)tiles * in.Hk) return;
+    key_head_of_block(in.Hk, tiles, (int)block_of_grid(), h, want);
     const int rows_q = (int)(in.total_q / in.num_seqs), G = in.H / in.Hk;
     if (!find_tile<BQ, 256>(in.cu_seqlens_q, in.num_seqs, rows_q, (int)in.total_q, tiles - 1 - want,
                             reinterpret_cast<int*>(even), seq, tile, G))
@@ -59,7 +63,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                   (int)in.total_k, seq, k0, k1);
     const int nq = q1 - q0, nk = k1 - k0, off = nk - nq, rows = nq * G;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
-    const int wrow = tile * BQ + 16 * NQ * wave;
+    const int wrow = SPLIT ? tile * BQ : tile * BQ + 16 * NQ * wave;
     const float sc = in.scale * LOG2E;
     auto token = [&](int row) { return (int)((unsigned)min(row, rows - 1) / (unsigned)G); };
     const KeyRange kr(uniform(token(tile * BQ)), uniform(token(tile * BQ + BQ - 1)), off, in.window, in.sinks, nk);
@@ -140,8 +144,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
         if (t + 1 < nt) load(t + 1, next);
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub) {
-            const int n0 = t * BN + 32 * sub;
-            if (wrow >= rows || n0 > last_hi || (n0 >= kr.ns && n0 + 32 <= first_lo)) continue;
+            const int r0 = SPLIT ? 16 * wave : 32 * sub, n0 = t * BN + r0;
+            if (wrow >= rows || n0 > last_hi || (n0 >= kr.ns && n0 + 16 * TT <= first_lo)) continue;
             f32x4 s[NQ][TT], dp[NQ][TT];
             v8 x[PD + 1];
 #pragma unroll
@@ -156,9 +160,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
             ahead<E1 + D / 16, PD>(
                 [&](auto n) {
                     constexpr int e = n;
-                    x[e % (PD + 1)] = e < E0   ? rows_of(K, 32 * sub + 16 * (e % TT), e / TT)
-                                      : e < E1 ? rows_of(V, 32 * sub + 16 * ((e - E0) % TT), (e - E0) / TT)
-                                               : k_cols(K, 32 * sub, 32 * sub + 16, e - E1);
+                    x[e % (PD + 1)] = e < E0   ? rows_of(K, r0 + 16 * (e % TT), e / TT)
+                                      : e < E1 ? rows_of(V, r0 + 16 * ((e - E0) % TT), (e - E0) / TT)
+                                               : cols<TT>(k_cols, K, r0, e - E1);
                 },
                 [&](auto n) {
                     constexpr int e = n;
@@ -176,7 +180,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                         }
                     } else {
                         if (e == E1) {
-                            if (!kr.whole(n0, n0 + 32, last_lo, first_hi)) {   // weights of hidden keys
+                            if (!kr.whole(n0, n0 + 16 * TT, last_lo, first_hi)) {   // weights of hidden keys
 #pragma unroll
                                 for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -195,13 +199,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
                                         exact[j] += s[j][tt][i] * dp[j][tt][i];
                                         s[j][tt][i] *= dp[j][tt][i] - dl[j];
                                     }
-                                dz[j] = acc_frag(s[j][0], s[j][1], E());
+                                dz[j] = acc_frag(s[j][0], s[j][TT - 1], E());
                                 if constexpr (sizeof(E) == 2) rest[j] = rest_frag(s[j][0], s[j][1], dz[j]);
                             }
                         }
                         constexpr int c = e - E1;
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[e % (PD + 1)], dz[j], acc[j][c]);
+                        for (int j = 0; j < NQ; ++j) acc[j][c] = mma_rows<TT>(x[e % (PD + 1)], dz[j], acc[j][c]);
                         if constexpr (sizeof(E) == 2)
 #pragma unroll
                             for (int j = 0; j < NQ; ++j) acc[j][c] = mma32(x[e % (PD + 1)], rest[j], acc[j][c]);
@@ -217,20 +221,31 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
         step(t + 1, odd, even);
     }
     if (t < nt) step(t, even, odd);
+    // SPLIT: the waves' sums, a quarter of the channels each
+    constexpr int OWN = SPLIT ? D / 64 : D / 16;
+    const int own = SPLIT ? wave * OWN : 0;
+    if constexpr (SPLIT) {
+        join_waves<E, D>(even, wave, col, g, acc[0]);
+        odd[tid] = exact[0];
+        __syncthreads();
+        exact[0] = odd[lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) exact[0] += odd[64 * w + lane];
+    }
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
         const int r = wrow + 16 * j + col;
         const float sum = group_sum(exact[j]);
         if (r >= rows) continue;
         const int i = token(r), head = h * G + r - i * G;
-        if (g == 0) {
+        if (g == 0 && own == 0) {
             float* stats = row_stats + 2 * ((int64_t)head * in.total_q + q0 + i);
             stats[0] = lse2[j];
             stats[1] = sum;
         }
-        E* row = dq + ((int64_t)(q0 + i) * in.H + head) * D;
+        E* row = dq + ((int64_t)(q0 + i) * in.H + head) * D + 16 * own;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < OWN; ++c) {
             typename Vec<E>::v4 x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = from_f32<E>(acc[j][c][i] * in.scale);
@@ -240,13 +255,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
 }
 
 // Work of a sequence in the second kernel: its key tiles, and behind them the
-// pieces of the sinks' walk.  The first tile walks the tokens before `behind`,
-// piece c those from behind + c WINDOW_PIECE on: no other key of the first tile is
-// in their window.
-constexpr int DKV_KEYS = 64;
-static_assert(WINDOW_MAX_SINKS <= DKV_KEYS, "the sinks lie in the first tile");
+// pieces of the sinks' walk, as many items each as there are tiles with sinks.  Those
+// tiles walk the tokens before `behind`, piece c those from behind + c WINDOW_PIECE
+// on: no key before WINDOW_MAX_SINKS has them in its window.
+template <bool SPLIT> constexpr int DKV_KEYS = SPLIT ? 16 : 64;   // of a tile
+template <int KEYS>
 struct KeyWork {
-    int q0, nq, k0, nk, behind, tiles, pieces;
+    int q0, nq, k0, nk, behind, tiles, pieces, sink_tiles;
     __device__ __forceinline__ KeyWork(const kda_window_inputs& in, int s) {
         int q1, k1;
         sequence_rows(in.cu_seqlens_q, (int)(in.total_q / in.num_seqs), (int)in.total_q, s, q0, q1);
@@ -254,27 +269,30 @@ struct KeyWork {
                       (int)in.total_k, s, k0, k1);
         nq = q1 - q0;
         nk = k1 - k0;
-        tiles = (nk + DKV_KEYS - 1) / DKV_KEYS;
-        // the first token that no key of the first tile has in its window
-        behind = in.sinks > 0 ? min(nq, max(0, min(in.window, nk) + DKV_KEYS - 1 - (nk - nq))) : nq;
+        tiles = (nk + KEYS - 1) / KEYS;
+        behind = in.sinks > 0 ? min(nq, max(0, min(in.window, nk) + WINDOW_MAX_SINKS - 1 - (nk - nq))) : nq;
         pieces = nk > 0 ? (nq - behind + WINDOW_PIECE - 1) / WINDOW_PIECE : 0;
+        sink_tiles = (min(in.sinks, nk) + KEYS - 1) / KEYS;
     }
-    // The first slot of its partial gradients: one for the first tile, then one for
-    // each piece (see window_slots).
+    // The first slot of its partial gradients: one for the tiles with sinks, then one
+    // for each piece (see window_slots).
     __device__ __forceinline__ int64_t slot(int s) const { return q0 / WINDOW_PIECE + 2 * (int64_t)s; }
 };
 
 // dk and dv.  A wave owns 16 keys, whose k and v operands and gradients stay in
 // registers; the query rows come 64 tokens of one head at a time (fp32: 32), head after
-// head of the group, and are worked on 32 at a time.  The scores are formed with rows = queries, so that the weights and
-// dz are the operands of dv^T += g^T w and dk^T += q^T dz as they stand.
-template <typename E, int D>
+// head of the group, and are worked on 32 at a time.  SPLIT (fp32, few keys): the
+// workgroup has 16 keys, a wave walks a quarter of each 64 rows, and the waves' sums are
+// added up in order behind the last.  The scores are formed with rows = queries, so that
+// the weights and dz are the operands of dv^T += g^T w and dk^T += q^T dz as they stand.
+template <typename E, int D, bool SPLIT>
 __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(
     const kda_window_inputs in, const E* __restrict__ d_o, const float* __restrict__ row_stats,
     E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
     E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ part, int items)
 {
-    constexpr int SUBS = sizeof(E) == 2 ? 2 : 1, BQ = 32 * SUBS, BK = DKV_KEYS, KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int BQ = sizeof(E) == 2 || SPLIT ? 64 : 32, BK = DKV_KEYS<SPLIT>, KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int RT = SPLIT ? 1 : 2, SUBS = SPLIT ? 1 : BQ / 32;   // row tiles worked on at a time, and how often
     typedef typename Vec<E>::v8 v8;
     // two arrays, so that a read of one is seen not to wait for loads into the other
     __shared__ __attribute__((aligned(16))) E even[BQ * 2 * D];
@@ -283,23 +301,27 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     __shared__ unsigned long long bad_rows[2];                       // a bit for each row to be taken out
 
     int h, want, seq, item;
-    key_head_of_block(in.Hk, items, blockIdx.x, h, want);
+    if (block_of_grid() >= (int64_t)items * in.Hk) return;
+    key_head_of_block(in.Hk, items, (int)block_of_grid(), h, want);
+    typedef KeyWork<BK> Work;
     if (!find_item<256>(in.num_seqs, want, reinterpret_cast<int*>(even), seq, item, [&](int s) {
-            const KeyWork w(in, s);
-            return w.tiles + w.pieces;
+            const Work w(in, s);
+            return w.tiles + w.pieces * w.sink_tiles;
         }))
         return;
-    const KeyWork work(in, seq);
+    const Work work(in, seq);
     const int nq = work.nq, nk = work.nk, off = nk - nq, G = in.H / in.Hk;
-    const int piece = item < work.tiles ? -1 : item - work.tiles;
+    const int piece = item < work.tiles ? -1 : (item - work.tiles) / work.sink_tiles;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), col = lane & 15, g = lane >> 4;
-    const int key0 = piece < 0 ? item * BK : 0, wkey = key0 + 16 * wave, key = wkey + col;
+    const int key0 = BK * (piece < 0 ? item : item - work.tiles - piece * work.sink_tiles);
+    const int wkey = SPLIT ? key0 : key0 + 16 * wave, key = wkey + col;
     const int W = min(in.window, nk);
     const float sc = in.scale * LOG2E;
     // the tokens [ta, te) to walk
     const int ta = piece < 0 ? min(nq, max(0, key0 - off)) : work.behind + piece * WINDOW_PIECE;
-    const int te = piece >= 0 ? min(nq, ta + WINDOW_PIECE)
-                              : max(ta, (int)min((int64_t)nq, (int64_t)key0 + BK - 1 + W - off));
+    const int te = piece >= 0          ? min(nq, ta + WINDOW_PIECE)
+                   : key0 < in.sinks ? max(ta, work.behind)
+                                     : max(ta, (int)min((int64_t)nq, (int64_t)key0 + BK - 1 + W - off));
     const int per = (te - ta + BQ - 1) / BQ, nu = per * G;   // tiles of a head, and all
 
     v8 k[KS], v[KS];
@@ -382,38 +404,40 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
             }
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub) {
-            const float* R = srow[u & 1] + 32 * sub;
+            const int r0 = SPLIT ? 16 * wave : 32 * sub;   // the first of the tile's rows worked on
+            const float* R = srow[u & 1] + r0;
             // positions of these rows
-            const int p0 = ta + t * BQ + 32 * sub + off, p1 = min(p0 + 32, te + off) - 1;
+            const int p0 = ta + t * BQ + r0 + off, p1 = min(p0 + 16 * RT, te + off) - 1;
             if (p1 < max(p0, wkey) || (p0 - (wkey + 15) >= W && wkey >= in.sinks)) continue;
-            f32x4 s[2], dp[2];
+            f32x4 s[RT], dp[RT], ls[RT], de[RT];
             v8 x[PD + 1];
 #pragma unroll
-            for (int a = 0; a < 2; ++a) s[a] = dp[a] = f32x4{0.f, 0.f, 0.f, 0.f};
-            const f32x4 ls[2] = {*reinterpret_cast<const f32x4*>(R + 4 * g), *reinterpret_cast<const f32x4*>(R + 16 + 4 * g)};
-            const f32x4 de[2] = {*reinterpret_cast<const f32x4*>(R + BQ + 4 * g),
-                                 *reinterpret_cast<const f32x4*>(R + BQ + 16 + 4 * g)};
+            for (int a = 0; a < RT; ++a) {
+                s[a] = dp[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+                ls[a] = *reinterpret_cast<const f32x4*>(R + 16 * a + 4 * g);
+                de[a] = *reinterpret_cast<const f32x4*>(R + BQ + 16 * a + 4 * g);
+            }
             // One sequence of operands, read ahead across its parts: z = q k^T;
             // g v^T, between whose products the weights' exponentials run;
             // dv^T += g^T w, between whose products dz is formed; dk^T += q^T dz.
-            constexpr int E0 = 2 * KS, E1 = 2 * E0, E2 = E1 + D / 16, NS = 8;
+            constexpr int E0 = RT * KS, E1 = 2 * E0, E2 = E1 + D / 16, NS = 4 * RT;
             v8 wf, zf;
             ahead<E2 + D / 16, PD>(
                 [&](auto n) {
                     constexpr int e = n;
-                    x[e % (PD + 1)] = e < E0   ? rows_of(Q, 32 * sub + 16 * (e % 2), e / 2)
-                                      : e < E1 ? rows_of(Gt, 32 * sub + 16 * ((e - E0) % 2), (e - E0) / 2)
-                                      : e < E2 ? cols_of(Gt, 32 * sub, 32 * sub + 16, e - E1)
-                                               : cols_of(Q, 32 * sub, 32 * sub + 16, e - E2);
+                    x[e % (PD + 1)] = e < E0   ? rows_of(Q, r0 + 16 * (e % RT), e / RT)
+                                      : e < E1 ? rows_of(Gt, r0 + 16 * ((e - E0) % RT), (e - E0) / RT)
+                                      : e < E2 ? cols<RT>(cols_of, Gt, r0, e - E1)
+                                               : cols<RT>(cols_of, Q, r0, e - E2);
                 },
                 [&](auto n) {
                     constexpr int e = n;
                     const v8& a = x[e % (PD + 1)];
                     if constexpr (e < E0) {
-                        s[e % 2] = mma32(a, k[e / 2], s[e % 2]);
+                        s[e % RT] = mma32(a, k[e / RT], s[e % RT]);
                     } else if constexpr (e < E1) {
                         constexpr int f = e - E0;
-                        dp[f % 2] = mma32(a, v[f / 2], dp[f % 2]);
+                        dp[f % RT] = mma32(a, v[f / RT], dp[f % RT]);
 #pragma unroll
                         for (int i = NS * f / E0; i < NS * (f + 1) / E0; ++i)
                             s[i / 4][i % 4] = exp2_fast(__builtin_fmaf(s[i / 4][i % 4], sc, -ls[i / 4][i % 4]));
@@ -423,22 +447,22 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
                             // weights of hidden keys
                             if (p0 < wkey + 15 || (p1 - wkey >= W && wkey + 15 >= in.sinks)) {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
+                                for (int i = 0; i < NS; ++i) {
                                     const int p = p0 + 16 * (i / 4) + 4 * g + i % 4;
                                     if (key > p || (p - key >= W && key >= in.sinks))
                                         s[i / 4][i % 4] = 0.f, dp[i / 4][i % 4] = 0.f;
                                 }
                             }
-                            wf = acc_frag(s[0], s[1], E());
+                            wf = acc_frag(s[0], s[RT - 1], E());
                         }
-                        av[c] = mma32(a, wf, av[c]);
+                        av[c] = mma_rows<RT>(a, wf, av[c]);
 #pragma unroll
                         for (int i = NS * c / (D / 16); i < NS * (c + 1) / (D / 16); ++i)
                             dp[i / 4][i % 4] = s[i / 4][i % 4] * (dp[i / 4][i % 4] - de[i / 4][i % 4]);
                     } else {
                         constexpr int c = e - E2;
-                        if (c == 0) zf = acc_frag(dp[0], dp[1], E());
-                        ak[c] = mma32(a, zf, ak[c]);
+                        if (c == 0) zf = acc_frag(dp[0], dp[RT - 1], E());
+                        ak[c] = mma_rows<RT>(a, zf, ak[c]);
                     }
                 });
         }
@@ -458,23 +482,30 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
         next(u + 1, odd, even);
     }
     if (u < nu) next(u, even, odd);
+    // SPLIT: the waves' sums, a quarter of the channels each
+    constexpr int OWN = SPLIT ? D / 64 : D / 16;
+    const int own = SPLIT ? wave * OWN : 0;
+    if constexpr (SPLIT) {
+        join_waves<E, D>(even, wave, col, g, ak);
+        join_waves<E, D>(odd, wave, col, g, av);
+    }
     if (key >= nk) return;
-    const bool sink = key < in.sinks && work.pieces > 0 && key0 == 0;
+    const bool sink = key < in.sinks && work.pieces > 0;
     if (piece >= 0 && !sink) return;
     if (sink) {
-        float* to = part + (((work.slot(seq) + piece + 1) * in.Hk + h) * in.sinks + key) * 2 * D + 4 * g;
+        float* to = part + (((work.slot(seq) + piece + 1) * in.Hk + h) * in.sinks + key) * 2 * D + 16 * own + 4 * g;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < OWN; ++c) {
             store_vec(to + 16 * c, ak[c] * in.scale);
             store_vec(to + D + 16 * c, av[c]);
         }
         return;
     }
     const int64_t row = work.k0 + key;
-    E* kr = dk + row * dk_token_stride + h * dk_head_stride;
-    E* vr = dv + row * dv_token_stride + h * dv_head_stride;
+    E* kr = dk + row * dk_token_stride + h * dk_head_stride + 16 * own;
+    E* vr = dv + row * dv_token_stride + h * dv_head_stride + 16 * own;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
+    for (int c = 0; c < OWN; ++c) {
         typename Vec<E>::v4 kx, vx;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -486,7 +517,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
     }
 }
 
-// The sinks' gradients: the parts of the first key tile and of the pieces, in order,
+// The sinks' gradients: the parts of the key tiles and of the pieces, in order,
 // rounded once.  A workgroup per sequence and key head, a thread per 4 channels.
 template <typename E, int D>
 __global__ __launch_bounds__(256) void window_sinks_kernel(
@@ -495,7 +526,7 @@ __global__ __launch_bounds__(256) void window_sinks_kernel(
 {
     const int seq = (int)(block_of_grid() / in.Hk), h = (int)(block_of_grid() % in.Hk);
     if (seq >= in.num_seqs) return;
-    const KeyWork work(in, seq);
+    const KeyWork<DKV_KEYS<false>> work(in, seq);
     if (work.pieces == 0) return;
     const int64_t stride = (int64_t)in.Hk * in.sinks * 2 * D;   // from slot to slot
     const float* from = part + (work.slot(seq) * in.Hk + h) * in.sinks * 2 * D;
@@ -514,27 +545,56 @@ __global__ __launch_bounds__(256) void window_sinks_kernel(
     }
 }
 
-template <typename E, int D>
-static hipError_t launch(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
-    constexpr int BQ = 64 * LATENT_NQ<E>;
-    const int64_t G = in.H / in.Hk, N = in.num_seqs;
-    const int64_t tq = in.cu_seqlens_q ? in.total_q * G / BQ + N : (in.total_q / N * G + BQ - 1) / BQ * N;
-    // Pieces exist only where a token stands behind the first tile's window.
-    const bool pieces = in.sinks > 0 && in.total_k > (int64_t)in.window + DKV_KEYS - 1;
-    const int64_t items = in.total_k / DKV_KEYS + N + (pieces ? in.total_q / WINDOW_PIECE + N : 0);
-    if (in.total_q > 0) {
-        hipLaunchKernelGGL((window_dq_kernel<E, D>), dim3((unsigned)(tq * in.Hk)), dim3(256), 0, stream, in,
-                           (const E*)a.o, a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, (int)tq);
-        if (const hipError_t e = launch_result(stream)) return e;
-    }
-    if (in.total_k == 0) return hipSuccess;
-    hipLaunchKernelGGL((window_dkv_kernel<E, D>), dim3((unsigned)(items * in.Hk)), dim3(256), 0, stream, in,
+template <typename E, int D, bool SPLIT>
+static hipError_t launch_dq(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
+    const int64_t tiles = row_tiles(in, WINDOW_ROWS<E, SPLIT>);
+    hipLaunchKernelGGL((window_dq_kernel<E, D, SPLIT>), grid_of(tiles * in.Hk), dim3(256), 0, stream, in, (const E*)a.o,
+                       a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, (int)tiles);
+    return launch_result(stream);
+}
+
+// Key tiles and pieces of the second kernel; pieces exist only where a token stands
+// behind the windows of all keys that may be sinks.
+static bool has_pieces(const kda_window_inputs& in) {
+    return in.sinks > 0 && in.total_k > (int64_t)in.window + WINDOW_MAX_SINKS - 1;
+}
+static int64_t key_items(const kda_window_inputs& in, int keys) {
+    return in.total_k / keys + in.num_seqs +
+           (has_pieces(in) ? (in.total_q / WINDOW_PIECE + in.num_seqs) * ((in.sinks + keys - 1) / keys) : 0);
+}
+template <typename E, int D, bool SPLIT>
+static hipError_t launch_dkv(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
+    const int64_t items = key_items(in, DKV_KEYS<SPLIT>);
+    hipLaunchKernelGGL((window_dkv_kernel<E, D, SPLIT>), grid_of(items * in.Hk), dim3(256), 0, stream, in,
                        (const E*)a.d_o, a.row_stats, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv,
                        a.dv_token_stride, a.dv_head_stride, a.part, (int)items);
-    if (const hipError_t e = launch_result(stream)) return e;
-    if (!pieces) return hipSuccess;
-    hipLaunchKernelGGL((window_sinks_kernel<E, D>), grid_of(N * in.Hk), dim3(256), 0, stream, in, a.part, (E*)a.dk,
-                       a.dk_token_stride, a.dk_head_stride, (E*)a.dv, a.dv_token_stride, a.dv_head_stride);
+    return launch_result(stream);
+}
+
+template <typename E, int D>
+static hipError_t launch(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
+    if (in.total_q > 0) {
+        hipError_t e;
+        if constexpr (sizeof(E) == 4)
+            e = split_waves(in) ? launch_dq<E, D, true>(in, a, stream) : launch_dq<E, D, false>(in, a, stream);
+        else
+            e = launch_dq<E, D, false>(in, a, stream);
+        if (e) return e;
+    }
+    if (in.total_k == 0) return hipSuccess;
+    hipError_t e;
+    // fp32: the split form as long as the whole one has two workgroups a CU or fewer (four
+    // with d = 64, half the LDS).  d 128, window 256, 1,024 tokens x 2 key heads: 142
+    // against 428 us; 16 documents of 256: 104 against 154; 17,600 tokens x 8: 4.14 against
+    // 3.65 ms.  d 64, window 512, 12,192 tokens x 4: 651 against 855.
+    if constexpr (sizeof(E) == 4)
+        e = key_items(in, DKV_KEYS<false>) * in.Hk <= 512 * (128 / D) ? launch_dkv<E, D, true>(in, a, stream)
+                                                                        : launch_dkv<E, D, false>(in, a, stream);
+    else
+        e = launch_dkv<E, D, false>(in, a, stream);
+    if (e || !has_pieces(in)) return e;
+    hipLaunchKernelGGL((window_sinks_kernel<E, D>), grid_of((int64_t)in.num_seqs * in.Hk), dim3(256), 0, stream, in,
+                       a.part, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv, a.dv_token_stride, a.dv_head_stride);
     return launch_result(stream);
 }
 

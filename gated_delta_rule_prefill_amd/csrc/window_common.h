@@ -125,6 +125,58 @@ struct Tiles {
     }
 };
 
+// Operands by columns of RT row tiles (RT 1: fp32, whose slots 4 to 7 stay empty), and
+// their products.
+template <int RT, typename Reader, typename E>
+__device__ __forceinline__ auto cols(const Reader& read, const E* t, int row0, int ct) {
+    if constexpr (RT == 2) return read(t, row0, row0 + 16, ct);
+    else return read.half(t, row0, ct);
+}
+template <int RT, typename V>
+__device__ __forceinline__ f32x4 mma_rows(const V& a, const V& b, f32x4 c) {
+    if constexpr (RT == 2) {
+        return mma32(a, b, c);
+    } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m], b[m], c, 0, 0, 0);
+        return c;
+    }
+}
+
+// The sums of four waves, each of 16 rows (lane & 15) and D channels as accumulator
+// tiles, added up in order: wave w is left with channel tiles [w D/64, (w + 1) D/64) in
+// the first D/64 of acc.  lds: 64 D floats that no wave reads any more.
+template <typename E, int D>
+__device__ __forceinline__ void join_waves(E* lds, int wave, int col, int g, f32x4 (&acc)[D / 16]) {
+    auto at = [&](int w, int c) { return reinterpret_cast<f32x4*>(lds) + (w * 16 + col) * (D / 4) + ((4 * c + g) ^ col); };
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) *at(wave, c) = acc[c];
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        acc[c] = *at(0, wave * (D / 64) + c);
+#pragma unroll
+        for (int w = 1; w < 4; ++w) acc[c] += *at(w, wave * (D / 64) + c);
+    }
+}
+
+// Query rows of a workgroup of the forward and dq kernels, and the batch's tiles of
+// so many.
+template <typename E, bool SPLIT> constexpr int WINDOW_ROWS = SPLIT ? 16 : 64 * LATENT_NQ<E>;
+static inline int64_t row_tiles(const kda_window_inputs& in, int rows) {
+    const int64_t G = in.H / in.Hk;
+    return in.cu_seqlens_q ? in.total_q * G / rows + in.num_seqs : (in.total_q / in.num_seqs * G + rows - 1) / rows * in.num_seqs;
+}
+// fp32: whether a workgroup's waves share 16 rows and split their keys rather than own
+// 16 rows each.  The split form has four times the workgroups and a walk of a quarter
+// of the length; it is taken as long as all of them run at once (128 KB of LDS each with
+// d = 128, 64 KB with 64).  Forward with d 128, window 256, 4 documents of 100 tokens x 8
+// heads: 13 against 22 us; 64, 1,024 tokens: 16.6 against 20.1.  Where it takes two rounds
+// it loses: 128, 1,024 tokens 36 against 32, 2,048 tokens 70 against 35.
+static inline bool split_waves(const kda_window_inputs& in) {
+    return row_tiles(in, 64) * in.Hk * 4 <= 256 * (128 / in.d);
+}
+
 // Cached tokens of a sequence.
 __device__ __forceinline__ int cached_tokens(const kda_kv_cache& c, int seq) {
     return (int)max((int64_t)0, min((int64_t)c.seq_lens[seq], (int64_t)c.max_pages * c.page_size));

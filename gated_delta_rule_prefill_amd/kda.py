@@ -981,7 +981,8 @@ def kv_append(k_cache, v_cache, k, v, block_table, seq_lens, cu_seqlens=None, nu
     else:
         _dense(k_out, "k_out", (T, Hk, d), dt, dev)
     st = lib().kda_kv_append(
-        cache, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, None if cu_seqlens is None else cu_seqlens.data_ptr(), T, N, Hk, d, _code(k), _ptr(norm_weight), eps, _ptr(inv_freq) if dr else None, _int32(start, "start"), dr, mscale,
+        cache, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, None if cu_seqlens is None else cu_seqlens.data_ptr(), T, N,
+        Hk, d, _code(k), _ptr(norm_weight), eps, _ptr(inv_freq) if dr else None, _int32(start, "start"), dr, mscale,
         KDA_ROTARY_INTERLEAVED if interleaved else 0, _ptr(k_out), _raw_stream(dev))
     if st:
         _check(st, "kda_kv_append")
