@@ -117,20 +117,18 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
         if (t < td || t >= te) v_tiles.move_bad(tid, to + BN * D, to);
     };
     // PAGED: the cache row of key tid of tile t (tid < BN)
-    auto look_up = [&](int t) -> int64_t {
-        const int n = t * BN + tid;
-        return n < kr.total ? cached_row(a.pages, seq, kr.position(n)) : -1;
-    };
-    auto keep = [&](int t, int64_t at) {
+    auto look_up = [&](int t) { return CachedRow(a.pages, seq, kr, t * BN + tid); };
+    auto keep = [&](int t, const CachedRow& found) {
+        const int64_t at = found.offset(a.pages);
         place[t & 3][tid] = at;
         const bool gap = __any(at < 0);
         if (tid == 0) gaps[t & 3] = gap;
     };
-    int64_t next_place = -1;
+    CachedRow next_place;   // of tile t + 2 in step t
     if constexpr (PAGED) {
         static_assert(BN <= 64, "one wave looks the rows up");
         if (tid < BN) {
-            const int64_t p0 = look_up(0), p1 = look_up(1);
+            const CachedRow p0 = look_up(0), p1 = look_up(1);
             keep(0, p0);
             keep(1, p1);
             next_place = look_up(2);

@@ -181,8 +181,24 @@ static inline bool split_waves(const kda_window_inputs& in) {
 __device__ __forceinline__ int cached_tokens(const kda_kv_cache& c, int seq) {
     return (int)max((int64_t)0, min((int64_t)c.seq_lens[seq], (int64_t)c.max_pages * c.page_size));
 }
-// Offset of position j of a sequence from the cache's k and v (head 0), or -1
-// where its page is absent.
+// The page and the row in it of key number n of a range, or row -1 behind its last.
+// The page is loaded without a branch and looked at only when the row's offset from the
+// cache's k and v (head 0; -1 where it is absent) is asked for, which lets a loop look
+// rows up ahead: a wait for a page is one for all loads before it.
+struct CachedRow {
+    int page = 0, row = -1;
+    __device__ __forceinline__ CachedRow() {}
+    __device__ __forceinline__ CachedRow(const kda_kv_cache& c, int seq, const KeyRange& kr, int n, bool there = true) {
+        const int j = kr.total > 0 ? kr.position(min(n, kr.total - 1)) : 0;
+        const int pg = (int)((unsigned)j / (unsigned)c.page_size);
+        page = c.block_table[(int64_t)seq * c.max_pages + pg];
+        row = there && n < kr.total ? j - pg * c.page_size : -1;
+    }
+    __device__ __forceinline__ int64_t offset(const kda_kv_cache& c) const {
+        return row >= 0 && page >= 0 && page < c.num_pages ? page * c.page_stride + row * c.token_stride : -1;
+    }
+};
+// Offset of position j of a sequence, or -1 where its page is absent.
 __device__ __forceinline__ int64_t cached_row(const kda_kv_cache& c, int seq, int j) {
     const int pg = (int)((unsigned)j / (unsigned)c.page_size);
     const int page = c.block_table[(int64_t)seq * c.max_pages + pg];

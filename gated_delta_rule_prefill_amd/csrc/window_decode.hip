@@ -91,11 +91,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_decode_ker
     const E* vp = (const E*)a.pages.v + h * a.pages.head_stride;
 
     // the cache row of key `lane` (below BN) of block b
-    auto look_up = [&](int b) -> int64_t {
-        const int n = b * BN + lane;
-        return lane < BN && b < b1 && n < kr.total ? cached_row(a.pages, seq, kr.position(n)) : -1;
-    };
-    int64_t next_place = look_up(b0 + wave);
+    auto look_up = [&](int b) { return CachedRow(a.pages, seq, kr, b * BN + lane, lane < BN && b < b1); };
+    CachedRow next_place = look_up(b0 + wave);
 
     const int r = min(tile * 16 + col, rows - 1), i = token(r);
     v8 q[KS];
@@ -111,8 +108,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_decode_ker
     unsigned there = 0, next_there = 0;   // a bit for each key of the block that has a row
     auto load = [&](int b) {              // block b, whose rows next_place holds; then those of the wave's next
         int64_t* at = place[wave][b >> 2 & 1];
-        next_there = (unsigned)__ballot(next_place >= 0);
-        if (lane < BN) at[lane] = next_place;
+        const int64_t mine = next_place.offset(a.pages);
+        next_there = (unsigned)__ballot(mine >= 0);
+        if (lane < BN) at[lane] = mine;
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
