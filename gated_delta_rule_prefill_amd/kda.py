@@ -396,16 +396,17 @@ def _elsewhere(device, stream):
     """Context that a call must enter: its stream argument's, or its tensors'
     device's; None where they are on the current device and stream.  Outputs and
     workspaces the binding allocates belong to the stream the call runs on."""
-    torch = _lib_torch()
+    torch = _torch or _lib_torch()
+    index = device.index   # None on the CPU
+    if stream is None and index is not None and index == torch._C._cuda_getDevice():
+        return None
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {device}")
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream: it belongs to {stream.device}, the tensors are on {device}")
         return torch.cuda.stream(stream)
-    if device.index != torch._C._cuda_getDevice():
-        return torch.cuda.device(device)
-    return None
+    return torch.cuda.device(device)
 
 
 def _raw_stream(device) -> int:
@@ -434,8 +435,8 @@ def _dense(t, name, shape, dtype, device) -> None:
 
 
 def _offsets(cu, name, device) -> int:
-    import torch
-    if cu.dtype is torch.int32 and cu.dim() == 1 and cu.shape[0] >= 2 and cu.device == device and cu.is_contiguous():
+    if (cu.dtype is (_torch or _lib_torch()).int32 and cu.dim() == 1 and cu.shape[0] >= 2 and cu.device == device and
+            cu.is_contiguous()):
         return cu.shape[0] - 1
     raise ValueError(f"{name}: expected contiguous int32 [N+1] on {device}, got {cu.dtype} {tuple(cu.shape)} "
                      f"on {cu.device}")
@@ -810,11 +811,11 @@ def window_attention(q, k, v, window: int, sinks: int = 0, cu_seqlens=None, cu_s
             return window_attention(q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, num_seqs, scale, out, lse)
     torch = _torch
     if out is None:
-        out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+        out = q.new_empty(T, H, d)
     else:
         _dense(out, "out", (T, H, d), q.dtype, dev)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((T, H), dtype=torch.float32)
     else:
         _dense(lse, "lse", (T, H), torch.float32, dev)
     st = lib().kda_window_attention(packed, out.data_ptr(), lse.data_ptr(), _raw_stream(dev))
@@ -848,17 +849,17 @@ def window_attention_backward(q, k, v, o, lse, d_o, window: int, sinks: int = 0,
     _dense(d_o, "d_o", (T, H, d), dt, dev)
     _dense(lse, "lse", (T, H), torch.float32, dev)
     if dk is None and dv is None:
-        dkv = torch.empty((Tk, 2 * Hk, d), dtype=dt, device=dev)
+        dkv = q.new_empty(Tk, 2 * Hk, d)
         dk, dv = dkv[:, :Hk], dkv[:, Hk:]
     else:
         _require(dk is not None and dv is not None, "dk and dv: both or neither")
         _rows3(dk, "dk", (Tk, Hk, d), dt, dev)
         _rows3(dv, "dv", (Tk, Hk, d), dt, dev)
-    dq = torch.empty((T, H, d), dtype=dt, device=dev)
+    dq = q.new_empty(T, H, d)
     handle = lib()
     if workspace is None:
         need = handle.kda_window_attention_backward_workspace_bytes(T, N, H, Hk, d, sinks)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     else:
         _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
         need = workspace.numel() * workspace.element_size()
@@ -922,17 +923,17 @@ def window_decode(q, k_cache, v_cache, block_table, seq_lens, window: int, sinks
                                  out, lse, workspace)
     torch = _torch
     if out is None:
-        out = torch.empty((T, H, d), dtype=dt, device=dev)
+        out = q.new_empty(T, H, d)
     else:
         _dense(out, "out", (T, H, d), dt, dev)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((T, H), dtype=torch.float32)
     else:
         _dense(lse, "lse", (T, H), torch.float32, dev)
     handle = lib()
     if workspace is None:
         need = handle.kda_window_decode_workspace_bytes(d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     else:
         _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
         need = workspace.numel() * workspace.element_size()
@@ -975,7 +976,7 @@ def kv_append(k_cache, v_cache, k, v, block_table, seq_lens, cu_seqlens=None, nu
             return kv_append(k_cache, v_cache, k, v, block_table, seq_lens, cu_seqlens, num_seqs, norm_weight, eps,
                              inv_freq, start, interleaved, mscale, k_out)
     if k_out is True:
-        k_out = _torch.empty((T, Hk, d), dtype=dt, device=dev)
+        k_out = k.new_empty(T, Hk, d)
     elif k_out is None or k_out is False:
         k_out = None
     else:
@@ -1040,7 +1041,7 @@ def qk_norm_rotary(q, k=None, q_weight=None, k_weight=None, positions=None, inv_
             return qk_norm_rotary(q, k, q_weight, k_weight, positions, inv_freq, start, interleaved, mscale, eps, q_out,
                                   k_out)
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=dt, device=dev)
+        q_out = q.new_empty(T, H, d)
         ot, oh = H * d, d
     else:
         ot, oh = _strides3(q_out, "q_out", T, H, d, dt, dev)
@@ -1048,7 +1049,7 @@ def qk_norm_rotary(q, k=None, q_weight=None, k_weight=None, positions=None, inv_
     b = None
     if k is not None:
         if k_out is None:
-            k_out = torch.empty((T, Hk, d), dtype=dt, device=dev)
+            k_out = k.new_empty(T, Hk, d)
             ot, oh = Hk * d, d
         else:
             ot, oh = _strides3(k_out, "k_out", T, Hk, d, dt, dev)
@@ -1097,9 +1098,9 @@ def qk_norm_rotary_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, 
         yt, yh = _strides3(dy, f"d{name}_out", T, H, d, dt, dev)
         w = _norm_weight(weight, f"{name}_weight", d, dev)
         if dx is None:
-            dx = torch.empty((T, H, d), dtype=dt, device=dev)
+            dx = x.new_empty(T, H, d)
         dt_, dh = _strides3(dx, f"d{name}", T, H, d, dt, dev)
-        dw = torch.empty(d, dtype=torch.float32, device=dev) if weight is not None else None
+        dw = x.new_empty(d, dtype=torch.float32) if weight is not None else None
         packed = _NORM_HEADS.pack(x.data_ptr(), xt, xh, 0, 0, 0, w, dy.data_ptr(), yt, yh, dx.data_ptr(), dt_, dh,
                                   0 if dw is None else dw.data_ptr(), H)
         return packed, dx, dw
@@ -1109,7 +1110,7 @@ def qk_norm_rotary_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, 
     handle = lib()
     if workspace is None:
         need = handle.kda_qk_norm_rotary_backward_workspace_bytes(d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     else:
         _require(workspace.device == dev and workspace.is_contiguous(), "workspace: contiguous, same device")
         need = workspace.numel() * workspace.element_size()
