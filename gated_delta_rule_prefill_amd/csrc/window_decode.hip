@@ -7,6 +7,13 @@
 // group share every cached row that is read, G flops per byte: the bytes of the
 // window bound the kernel.  Many rows (chunks of a prompt) go to the forward kernel
 // in its paged form.
+//
+// bf16, d = 128, 32 heads over 8, window 1,024: 256 sequences take 190 us, 5.4 TB/s of
+// cached rows (reads alone reach 6.25; loads past the caches 2 % faster, at the expense
+// of pages that sequences share; three workgroups a CU spill: 230).  One sequence with
+// a window of 4,096: 9.0 us, 256 workgroups with one block of 32 keys a wave, and 4.2 for
+// the join; latency.  (A join by the last workgroup to end needs a fence that writes an
+// XCD's L2 back: 117 us.)
 #include <algorithm>
 
 #include "window_common.h"

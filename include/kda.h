@@ -645,6 +645,8 @@ kda_status kda_window_decode(const kda_kv_cache *cache, const void *q, int64_t q
  * where R turns channels [start, start + dr) and multiplies them by `amplitude`.
  * A token whose position is negative or whose page is outside [0, num_pages) is
  * not written to the cache.
+ * Two new tokens with the same cache row (sequences that share a page they both
+ * write) leave one of the two there, or parts of both.
  *   k, v         [T, Hk, d] dtype, strided (read)
  *   cu_seqlens, total_tokens, num_seqs: as for kda_window_decode
  *   norm_weight  [d] fp32, or NULL: keys are not normalised
@@ -654,7 +656,8 @@ kda_status kda_window_decode(const kda_kv_cache *cache, const void *q, int64_t q
  *   flags        KDA_ROTARY_INTERLEAVED or 0
  *   k_out        [T, Hk, d] dtype, dense, or NULL: the key rows, for the
  *                tokens' own attention (written for every token of a sequence,
- *                whether or not it has a cache row)
+ *                whether or not it has a cache row; must not
+ *                overlap an input)
  * d in {64, 128}, dr even, start + dr <= d.
  */
 kda_status kda_kv_append(const kda_kv_cache *cache, const void *k, int64_t k_token_stride,
