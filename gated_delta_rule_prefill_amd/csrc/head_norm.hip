@@ -352,7 +352,10 @@ static int norm_tokens(int64_t total, int heads, int lanes, int half, int each) 
     return (int)std::min<int64_t>(n, half > 0 ? NORM_PAIRS / half : n);
 }
 
-// More than the 256 MB of the last-level cache is stored past the caches.
+// More than the 256 MB of the last-level cache is stored past the caches: 36,755 tokens,
+// 40 heads of 128, bf16, forwards then back: 149 + 212 us.  With the forward's outputs
+// through the caches 137 + 237, as what they hold back is written during the next kernel;
+// with the gradients too 144 + 228.
 static bool far(const QkNorm& a, int es) {
     return a.total_tokens * (a.q.H + a.k.H) * (int64_t)a.d * es > (int64_t)256 << 20;
 }

@@ -5,8 +5,8 @@
 //   z_rj = scale q_r . k_j,  o_r = sum_j softmax(z_r)_j v_j
 // over the sinks and the window (KeyRange).  With one new token the G rows of a
 // group share every cached row that is read, G flops per byte: the bytes of the
-// window bound the kernel.  Many rows (chunks of a prompt) go to the forward kernel
-// in its paged form.
+// window bound the kernel.  Many rows (chunks of several prompts) go to the forward
+// kernel in its paged form.
 //
 // bf16, d = 128, 32 heads over 8, window 1,024: 256 sequences take 190 us, 5.4 TB/s of
 // cached rows (reads alone reach 6.25; loads past the caches 2 % faster, at the expense
@@ -20,7 +20,7 @@
 
 namespace kda {
 
-constexpr int DECODE_SLOTS = 1024;   // partial results of 16 rows each
+constexpr int DECODE_SLOTS = 512;   // partial results of 16 rows each
 constexpr int DECODE_KEYS = 32;      // keys of a wave's step
 
 // Where the rows of a row tile whose keys are split belong, for the join: row r is
@@ -336,13 +336,18 @@ __global__ __launch_bounds__(256) void window_join_kernel(const WindowArgs a, co
 
 size_t window_decode_workspace(int32_t d) { return (size_t)DECODE_SLOTS * (sizeof(DecodeTile) + 16 * (d + 4) * 4); }
 
+// Row tiles of all key heads.
+static int64_t decode_units(const kda_window_inputs& in) { return row_tiles(in, 16) * in.Hk; }
+
 template <typename E, int D>
 static hipError_t launch(const WindowArgs& a, void* workspace, hipStream_t stream) {
     const kda_window_inputs& in = a.in;
-    const int64_t G = in.H / in.Hk, N = in.num_seqs;
-    const int64_t tiles = in.cu_seqlens_q ? in.total_q * G / 16 + N : (in.total_q / N * G + 15) / 16 * N;
-    const int64_t units = tiles * in.Hk;
-    // Few row tiles have their keys split over workgroups, 128 keys or more each.
+    const int64_t N = in.num_seqs, units = decode_units(in);
+    // Few row tiles have their keys split over workgroups, 128 keys or more each, as long
+    // as all of them run at once, two a CU.  bf16, window 1,024, 32/8 heads, 512 workgroups
+    // against 1,024 in us without the join: 8 sequences 12.0 and 14.5, 16 16.8 and 20.2,
+    // 32 24.9 and 28.0; one, window 16,384, with the join: 21.9 and 28.  One, window 1,024,
+    // with 64 keys or more: 6.2 + 4.7 for 6.8 + 3.6; with 256: 8.1 + 3.2.
     const int64_t most = std::min((int64_t)in.window + in.sinks + (in.total_q + N - 1) / N,
                                   (int64_t)a.pages.max_pages * a.pages.page_size);
     const int64_t splits = std::max<int64_t>(1, std::min((most + 127) / 128, DECODE_SLOTS / units));
@@ -357,9 +362,16 @@ static hipError_t launch(const WindowArgs& a, void* workspace, hipStream_t strea
 }
 
 hipError_t launch_window_decode(const WindowArgs& a, void* workspace, hipStream_t stream) {
-    // Sequences of many rows each share a cached row among 64 rows and more.
+    // The forward kernel shares a cached row among 128 rows (fp32: 64, or 16), but its
+    // walk is not split: it takes batches of many row tiles, more than one of 16 rows a
+    // sequence.  bf16, window 1,024, 32/8 heads, decode against forward in us: 1 sequence
+    // of 128 new tokens 31 and 39, 4 of 64 31 and 40, 16 of 16 31 and 38, of 32 57 and 41, 128 of
+    // 4 108 and 112, of 8 144 and 112.  fp32, window 512, 16/4 heads: 8 of 4 19 and 27, of 8 28
+    // and 27, of 16 38 and 27, of 32 52 and 57, 64 of 4 52 and 57, of 8 67 and 60.
     const int64_t G = a.in.H / a.in.Hk;
-    if (a.in.total_q * G > 32 * (int64_t)a.in.num_seqs) return launch_window_attention(a, true, stream);
+    if (a.in.total_q * G > 16 * (int64_t)a.in.num_seqs &&
+        decode_units(a.in) > (a.in.dtype == KDA_DTYPE_BF16 ? 512 : 64))
+        return launch_window_attention(a, true, stream);
     if (a.in.dtype == KDA_DTYPE_BF16)
         return a.in.d == 128 ? launch<bf16, 128>(a, workspace, stream) : launch<bf16, 64>(a, workspace, stream);
     return a.in.d == 128 ? launch<float, 128>(a, workspace, stream) : launch<float, 64>(a, workspace, stream);

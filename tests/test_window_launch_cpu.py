@@ -42,7 +42,7 @@ CALLS = {   # call -> its launches
     "backward with a window over all": ("w_backward, window=300", 2), "backward in fp32": ("w_backward, bf16=False", 3),
     "backward without a workspace": ("w_backward, ws=None", 3),
     "decode, split": ("w_decode", 2), "decode, short window": ("w_decode, window=64", 1),
-    "decode, many sequences": ("w_decode, T=600, N=600", 1), "decode, many rows": ("w_decode, T=60", 1),
+    "decode, many sequences": ("w_decode, T=600, N=600", 1), "decode, many rows": ("w_decode, T=3000", 1), "decode, a few rows": ("w_decode, T=60", 2),
     "decode without a workspace": ("w_decode, ws=None", 2), "append": ("w_append", 1), "norm": ("w_norm", 1),
     "norm backward": ("w_norm_backward", 2), "norm backward without tokens": ("w_norm_backward, T=0", 1),
     "norm backward without a workspace": ("w_norm_backward, ws=None", 2),
