@@ -246,7 +246,7 @@ kda_status kda_window_attention_backward(const kda_window_inputs* in, const void
         // the second kernel's grid: key tiles and pieces of the sinks
         if ((in->total_k / 64 + in->total_q / kda::WINDOW_PIECE + 2 * (int64_t)in->num_seqs) * in->Hk >= (int64_t)1 << 24)
             return fail(KDA_ERR_INVALID_ARGUMENT,
-                        "too many tiles ((total_k / 64 + total_q / 1024 + 2 num_seqs) * Hk must be below 2^24)");
+                        "too many tiles ((total_k / 64 + total_q / 256 + 2 num_seqs) * Hk must be below 2^24)");
         const BackwardSpace s(in->total_q, in->num_seqs, in->H, in->Hk, in->d, in->sinks);
         if (kda_status st = check_workspace(workspace, workspace_bytes, s.bytes)) return st;
         if (in->total_q == 0 && in->total_k == 0) return KDA_OK;

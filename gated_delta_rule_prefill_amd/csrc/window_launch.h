@@ -35,8 +35,11 @@ struct WindowGrads {
     float* row_stats;
     float* part;
 };
-// Tokens of a piece of the sinks' gradients, and the slots that a batch's pieces take.
-constexpr int WINDOW_PIECE = 1024;
+// Tokens of a piece of the sinks' gradients, and the slots that a batch's pieces take.  Short
+// pieces, as with a small window they are the longest walks: 4,096 tokens, 32/8 heads of
+// 128, window 128, dk and dv in us with 1,024, 512 and 256 tokens: 169, 105, 72; window
+// 1,024: 224, 181, 167.
+constexpr int WINDOW_PIECE = 256;
 inline int64_t window_slots(int64_t total_q, int32_t num_seqs) { return total_q / WINDOW_PIECE + 2 * (int64_t)num_seqs; }
 hipError_t launch_window_attention_backward(const kda_window_inputs& in, const WindowGrads& g, hipStream_t stream);
 

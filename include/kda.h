@@ -531,7 +531,7 @@ kda_status kda_rotary_frequencies(int32_t dr, double base, double factor,
  * d in {64, 128}; Hk divides H; token strides and H * d below 2^23;
  * total_q * H / Hk <= 2^31 - 4096; (rows / 64 + num_seqs) * Hk below 2^24, where
  * rows is the larger of total_q * H / Hk and total_k (backward: also
- * (total_k / 64 + total_q / 1024 + 2 num_seqs) * Hk).
+ * (total_k / 64 + total_q / 256 + 2 num_seqs) * Hk).
  */
 typedef struct {
     const void *q;

@@ -52,12 +52,11 @@ def test_sinks_of_long_sequences(empty, sinks):
 def test_chunks_over_a_cache(empty, d, window, sinks):
     lens, new = [300, 100, 64, 129] + [0] * empty, [100, 100, 1, 65] + [0] * empty
     x = td.make(84, "f32", 8, 2, d, 16, lens, new)
-    T = sum(new)
-    assert T * 4 > 32 * 4      # rows for the kernel of chunks, without the empty sequences
-    if empty:                  # and with them
+    if empty:                  # more rows than the empty sequences have
         lens, new = [n + 700 for n in lens[:4]] + [1] * 40, [700] * 4 + [1] * 40
         x = td.make(85, "f32", 16, 4, d, 16, lens, new)
-        assert sum(new) * 4 > 32 * len(new)
+    # batches that take the kernel of chunks
+    assert sum(new) * 4 > 16 * len(new) and (sum(new) * 4 // 16 + len(new)) * x["k"].shape[2] > 64
     td.check(f"{d} W={window} S={sinks}", x, lens, new, window, sinks)
 
 
