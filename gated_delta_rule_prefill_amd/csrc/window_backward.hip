@@ -287,24 +287,25 @@ struct KeyWork {
 // dk and dv.  A wave owns 16 keys, whose k and v operands and gradients stay in
 // registers; the query rows come 64 tokens of one head at a time (fp32: 32), head after
 // head of the group, and are worked on 32 at a time (32 tokens a time, with twice the
-// barriers: 1.32 ms against 1.20).  SPLIT (fp32, few keys): the
-// workgroup has 16 keys, a wave walks a quarter of each 64 rows, and the waves' sums are
-// added up in order behind the last.  The scores are formed with rows = queries, so that
+// barriers: 1.32 ms against 1.20).  SPLIT (few keys): the workgroup has 16
+// keys, a wave walks a quarter of each 128 rows (fp32: 64), and the waves' sums are added
+// up in order behind the last.  The scores are formed with rows = queries, so that
 // the weights and dz are the operands of dv^T += g^T w and dk^T += q^T dz as they stand.
 template <typename E, int D, bool SPLIT>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel(
+__global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_dkv_kernel(
     const kda_window_inputs in, const E* __restrict__ d_o, const float* __restrict__ row_stats,
     E* __restrict__ dk, int64_t dk_token_stride, int64_t dk_head_stride,
     E* __restrict__ dv, int64_t dv_token_stride, int64_t dv_head_stride, float* __restrict__ part, int items)
 {
-    constexpr int BQ = sizeof(E) == 2 || SPLIT ? 64 : 32, BK = DKV_KEYS<SPLIT>, KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
-    constexpr int RT = SPLIT ? 1 : 2, SUBS = SPLIT ? 1 : BQ / 32;   // row tiles worked on at a time, and how often
+    constexpr int BQ = (sizeof(E) == 2 ? 64 : 32) * (SPLIT ? 2 : 1), BK = DKV_KEYS<SPLIT>;
+    constexpr int KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int RT = BQ == 64 && SPLIT ? 1 : 2, SUBS = SPLIT ? 1 : BQ / 32;   // row tiles worked on at a time, and how often
     typedef typename Vec<E>::v8 v8;
     // two arrays, so that a read of one is seen not to wait for loads into the other
     __shared__ __attribute__((aligned(16))) E even[BQ * 2 * D];
     __shared__ __attribute__((aligned(16))) E odd[BQ * 2 * D];
     __shared__ __attribute__((aligned(16))) float srow[2][2 * BQ];   // lse (base 2), then delta
-    __shared__ unsigned long long bad_rows[2];                       // a bit for each row to be taken out
+    __shared__ unsigned long long bad_rows[2][(BQ + 63) / 64];       // a bit for each row to be taken out
 
     int h, want, seq, item;
     if (block_of_grid() >= (int64_t)items * in.Hk) return;
@@ -377,7 +378,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
             const unsigned long long rows = __ballot(bad);
             srow[u & 1][tid] = bad ? __builtin_nanf("") : next_lse;
             srow[u & 1][BQ + tid] = bad ? 0.f : next_delta;
-            if (tid == 0) bad_rows[u & 1] = rows;
+            if (lane == 0) bad_rows[u & 1][wave] = rows;
         }
         landed();
     };
@@ -398,19 +399,23 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dkv_kernel
         rows_of.keep(), cols_of.keep();
         E* Gt = Q + BQ * D;
         if (u + 1 < nu) load(nhead, nt, next);
-        if (t < td || t >= tw)
-            if (const unsigned long long bad = (unsigned long long)uniform((int64_t)bad_rows[u & 1])) {
+        if (t < td || t >= tw) {
+            unsigned long long any = 0, bad[(BQ + 63) / 64];
+#pragma unroll
+            for (int w = 0; w < (BQ + 63) / 64; ++w) any |= bad[w] = (unsigned long long)uniform((int64_t)bad_rows[u & 1][w]);
+            if (any) {
 #pragma unroll
                 for (int i = 0; i < q_tiles.N; ++i)
-                    if (bad >> q_tiles.row(i) & 1) {
+                    if (bad[i * q_tiles.STEP / 64] >> (q_tiles.row(i) & 63) & 1) {
                         *reinterpret_cast<u32x4*>(Q + (i * 256 + tid) * q_tiles.CE) = u32x4{0, 0, 0, 0};
                         *reinterpret_cast<u32x4*>(Gt + (i * 256 + tid) * q_tiles.CE) = u32x4{0, 0, 0, 0};
                     }
                 __syncthreads();
             }
+        }
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub) {
-            const int r0 = SPLIT ? 16 * wave : 32 * sub;   // the first of the tile's rows worked on
+            const int r0 = SPLIT ? 16 * RT * wave : 32 * sub;   // the first of the tile's rows worked on
             const float* R = srow[u & 1] + r0;
             // positions of these rows
             const int p0 = ta + t * BQ + r0 + off, p1 = min(p0 + 16 * RT, te + off) - 1;
@@ -592,12 +597,15 @@ static hipError_t launch(const kda_window_inputs& in, const WindowGrads& a, hipS
     // fp32: the split form as long as the whole one has two workgroups a CU or fewer (four
     // with d = 64, half the LDS).  d 128, window 256, 1,024 tokens x 2 key heads: 142
     // against 428 us; 16 documents of 256: 104 against 154; 17,600 tokens x 8: 4.14 against
-    // 3.65 ms.  d 64, window 512, 12,192 tokens x 4: 651 against 855.
-    if constexpr (sizeof(E) == 4)
-        e = key_items(in, DKV_KEYS<false>) * in.Hk <= 512 * (128 / D) ? launch_dkv<E, D, true>(in, a, stream)
-                                                                        : launch_dkv<E, D, false>(in, a, stream);
-    else
-        e = launch_dkv<E, D, false>(in, a, stream);
+    // 3.65 ms.  d 64, window 512, 12,192 tokens x 4: 651 against 855.  bf16, whose products
+    // are not what a short walk waits for: as long as the split form's workgroups take
+    // little more than one round.  d 128, 4 query heads a key head, 1,000 tokens x 1 key
+    // head, window 128 and 1,024: 20 against 38 us, 47 against 97; 2,000 x 2: 38 and 38, 56
+    // against 107; 2,000 x 4, window 256: 56 against 41, d 64 28 against 31; 4,000 x 4: 50
+    // against 39.
+    const int64_t whole = key_items(in, DKV_KEYS<false>) * in.Hk;
+    const int64_t most = (sizeof(E) == 4 ? 512 : 96) * (128 / D);
+    e = whole <= most ? launch_dkv<E, D, true>(in, a, stream) : launch_dkv<E, D, false>(in, a, stream);
     if (e || !has_pieces(in)) return e;
     hipLaunchKernelGGL((window_sinks_kernel<E, D>), grid_of((int64_t)in.num_seqs * in.Hk), dim3(256), 0, stream, in,
                        a.part, (E*)a.dk, a.dk_token_stride, a.dk_head_stride, (E*)a.dv, a.dv_token_stride, a.dv_head_stride);
