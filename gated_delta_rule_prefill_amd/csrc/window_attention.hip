@@ -26,17 +26,17 @@
 namespace kda {
 
 // A workgroup of 4 waves, one key head.  A wave has 32 (fp32: 16) query rows, whose
-// operands q and o stay in registers, and walks all keys.  SPLIT (fp32, few rows; see
-// split_waves): the workgroup has 16 rows, a wave walks a quarter of each tile's keys
+// operands q and o stay in registers, and walks all keys.  SPLIT (few rows; see split_waves):
+// the workgroup has 16 rows, a wave walks a quarter of each tile's keys
 // with a maximum and sum of its own, and the four are joined behind the last.  Key and
 // value tiles of BN rows are double-buffered in LDS: the next tile's loads, straight
 // into LDS, are issued before a tile's products.
 template <typename E, int D, bool PAGED, bool SPLIT>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_kernel(const WindowArgs a, int tiles)
+__global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_attention_kernel(const WindowArgs a, int tiles)
 {
-    constexpr int BN = sizeof(E) == 2 || SPLIT ? 64 : 32, NQ = LATENT_NQ<E>, BQ = WINDOW_ROWS<E, SPLIT>;
-    constexpr int KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
-    constexpr int TT = SPLIT ? 1 : BN / 16, PAIR = SPLIT ? 1 : 2;   // a wave's key tiles, and those by turns
+    constexpr int BN = (sizeof(E) == 2 ? 64 : 32) * (SPLIT ? 2 : 1), NQ = SPLIT ? 1 : LATENT_NQ<E>;
+    constexpr int BQ = WINDOW_ROWS<E, SPLIT>, KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    constexpr int TT = BN / (SPLIT ? 64 : 16), PAIR = TT > 1 ? 2 : 1;   // a wave's key tiles, and those by turns
     typedef typename Vec<E>::v8 v8;
     // two arrays, so that a read of one is seen not to wait for loads into the other
     __shared__ __attribute__((aligned(16))) E even[BN * 2 * D];
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
     auto step = [&](int t, const E* K, E* next) __attribute__((always_inline)) {
         k_rows.keep(), v_cols.keep();
         const E* V = K + BN * D;
-        const int r0 = SPLIT ? 16 * wave : 0, n0 = t * BN + r0;   // the wave's first key of the tile
+        const int r0 = SPLIT ? 16 * TT * wave : 0, n0 = t * BN + r0;   // the wave's first key of the tile
         if (t + 1 < nt) load(t + 1, next);
         if constexpr (PAGED)
             if (tid < BN) {
@@ -285,20 +285,21 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_attention_
     constexpr int OWN = SPLIT ? D / 64 : D / 16;
     const int own = SPLIT ? wave * OWN : 0;
     if constexpr (SPLIT) {
-        odd[tid] = m[0];
+        float* stat = reinterpret_cast<float*>(odd);
+        stat[tid] = m[0];
         __syncthreads();
         float top = neg_inf();
 #pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, odd[64 * w + lane]);
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, stat[64 * w + lane]);
         const float f = m[0] == neg_inf() ? 0.f : exp2_fast(m[0] - top);   // no key: its sums are 0
         m[0] = top;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) acc[0][c] *= f;
-        odd[256 + tid] = l[0] * f;
+        stat[256 + tid] = l[0] * f;
         join_waves<E, D>(even, wave, col, g, acc[0]);
-        l[0] = odd[256 + lane];
+        l[0] = stat[256 + lane];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) l[0] += odd[256 + 64 * w + lane];
+        for (int w = 1; w < 4; ++w) l[0] += stat[256 + 64 * w + lane];
     }
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
@@ -329,7 +330,7 @@ static hipError_t launch_as(const WindowArgs& a, hipStream_t stream) {
 }
 template <typename E, int D, bool PAGED>
 static hipError_t launch(const WindowArgs& a, hipStream_t stream) {
-    if constexpr (sizeof(E) == 4)
+    if constexpr (sizeof(E) == 4 || !PAGED)   // few rows over a cache: window_decode.hip
         if (split_waves(a.in)) return launch_as<E, D, PAGED, true>(a, stream);
     return launch_as<E, D, PAGED, false>(a, stream);
 }

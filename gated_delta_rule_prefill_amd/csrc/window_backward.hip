@@ -39,17 +39,18 @@ __device__ __forceinline__ bf16x8 rest_frag(f32x4 a, f32x4 b, bf16x8 x) {
 // keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.  dq itself
 // takes delta from the rounded o, as its own sum is complete only behind the last
 // key; the second kernel takes that sum.
-// A wave owns 32 rows (fp32: 16) and walks all keys, 32 at a time.  SPLIT (fp32, few
-// rows; see split_waves): the workgroup has 16 rows, a wave walks a quarter of each
+// A wave owns 32 rows (fp32: 16) and walks all keys, 32 at a time.  SPLIT (few rows;
+// see split_waves): the workgroup has 16 rows, a wave walks a quarter of each
 // tile's keys, and the waves' sums are added up in order.
 template <typename E, int D, bool SPLIT>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
+__global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_dq_kernel(
     const kda_window_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
     const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ row_stats, int tiles)
 {
-    constexpr int BN = sizeof(E) == 2 || SPLIT ? 64 : 32, NQ = LATENT_NQ<E>, BQ = WINDOW_ROWS<E, SPLIT>;
-    constexpr int KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
-    constexpr int TT = SPLIT ? 1 : 2, SUBS = SPLIT ? 1 : BN / 32;   // key tiles worked on at a time, and how often
+    constexpr int BN = (sizeof(E) == 2 ? 64 : 32) * (SPLIT ? 2 : 1), NQ = SPLIT ? 1 : LATENT_NQ<E>;
+    constexpr int BQ = WINDOW_ROWS<E, SPLIT>, KS = D / 32, PD = sizeof(E) == 2 ? 3 : 1;
+    // key tiles worked on at a time, and how often
+    constexpr int TT = BN == 64 && SPLIT ? 1 : 2, SUBS = SPLIT ? 1 : BN / 32;
     typedef typename Vec<E>::v8 v8;
     // two arrays, so that a read of one is seen not to wait for loads into the other
     __shared__ __attribute__((aligned(16))) E even[BN * 2 * D];
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
         if (t + 1 < nt) load(t + 1, next);
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub) {
-            const int r0 = SPLIT ? 16 * wave : 32 * sub, n0 = t * BN + r0;
+            const int r0 = SPLIT ? 16 * TT * wave : 32 * sub, n0 = t * BN + r0;
             if (wrow >= rows || n0 > last_hi || (n0 >= kr.ns && n0 + 16 * TT <= first_lo)) continue;
             f32x4 s[NQ][TT], dp[NQ][TT];
             v8 x[PD + 1];
@@ -231,11 +232,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void window_dq_kernel(
     const int own = SPLIT ? wave * OWN : 0;
     if constexpr (SPLIT) {
         join_waves<E, D>(even, wave, col, g, acc[0]);
-        odd[tid] = exact[0];
+        float* sums = reinterpret_cast<float*>(odd);
+        sums[tid] = exact[0];
         __syncthreads();
-        exact[0] = odd[lane];
+        exact[0] = sums[lane];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) exact[0] += odd[64 * w + lane];
+        for (int w = 1; w < 4; ++w) exact[0] += sums[64 * w + lane];
     }
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
@@ -585,11 +587,7 @@ static hipError_t launch_dkv(const kda_window_inputs& in, const WindowGrads& a, 
 template <typename E, int D>
 static hipError_t launch(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
     if (in.total_q > 0) {
-        hipError_t e;
-        if constexpr (sizeof(E) == 4)
-            e = split_waves(in) ? launch_dq<E, D, true>(in, a, stream) : launch_dq<E, D, false>(in, a, stream);
-        else
-            e = launch_dq<E, D, false>(in, a, stream);
+        const hipError_t e = split_waves(in) ? launch_dq<E, D, true>(in, a, stream) : launch_dq<E, D, false>(in, a, stream);
         if (e) return e;
     }
     if (in.total_k == 0) return hipSuccess;

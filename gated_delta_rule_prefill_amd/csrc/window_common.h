@@ -167,12 +167,16 @@ static inline int64_t row_tiles(const kda_window_inputs& in, int rows) {
     const int64_t G = in.H / in.Hk;
     return in.cu_seqlens_q ? in.total_q * G / rows + in.num_seqs : (in.total_q / in.num_seqs * G + rows - 1) / rows * in.num_seqs;
 }
-// fp32: whether a workgroup's waves share 16 rows and split their keys rather than own
-// 16 rows each.  The split form has four times the workgroups and a walk of a quarter
-// of the length; it is taken as long as all of them run at once (128 KB of LDS each with
-// d = 128, 64 KB with 64).  Forward with d 128, window 256, 4 documents of 100 tokens x 8
-// heads: 13 against 22 us; 64, 1,024 tokens: 16.6 against 20.1.  Where it takes two rounds
-// it loses: 128, 1,024 tokens 36 against 32, 2,048 tokens 70 against 35.
+// Whether a workgroup's waves share 16 rows and split their keys rather than own rows
+// each.  The split form has a walk of a quarter of the length and four times (bf16:
+// eight times) the workgroups; it is taken as long as all of them run at once (128 KB of
+// LDS each with d = 128, 64 KB with 64).  us, split against whole:
+//   fp32, forward   d 128, 495 tokens x 4 heads, window 100    13 and 22
+//                   d 64 (128), 1,024 tokens x 8, window 256   16.6 and 20.1 (36 and 32)
+//   bf16, forward   d 128, 1,000 tokens x 4 on 1 key head, window 1,024 (128)   17 and 29 (13 and 15)
+//   bf16, dq        the same                                                    18 and 41 (14 and 19)
+// Where it takes more rounds it loses: fp32, d 128, 2,048 tokens x 8 70 and 35; bf16,
+// 2,000 tokens x 8 on 2, window 1,024, 61 and 33, d 64 25 and 25.
 static inline bool split_waves(const kda_window_inputs& in) {
     return row_tiles(in, 64) * in.Hk * 4 <= 256 * (128 / in.d);
 }

@@ -1,5 +1,4 @@
-"""The two forms of the window kernels that small batches choose between (fp32: all of
-them; bf16: dk and dv): waves that share 16 rows (or keys) and split their walk, and
+"""The two forms of the window kernels that small batches choose between: waves that share 16 rows (or keys) and split their walk, and
 waves with rows of their own.  Which one runs follows from the sizes and the number of
 sequences, so that 600 empty sequences behind the others select the second
 (window_common.h, split_waves; the launch of dk and dv in window_backward.hip)."""
