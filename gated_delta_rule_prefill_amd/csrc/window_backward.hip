@@ -19,6 +19,8 @@
 // (four products of 0.24 TFLOP over the visible pairs, as it takes dz twice: 0.99 PFLOP/s),
 // dk and dv 1.13 to 1.18 (four: 0.85, LDS: a wave reads every operand for its 16 keys
 // alone).  One kernel for all would have to add a part of dq for each tile of 64 keys.
+#include <algorithm>
+
 #include "window_common.h"
 
 namespace kda {
@@ -35,6 +37,8 @@ __device__ __forceinline__ bf16x8 rest_frag(f32x4 a, f32x4 b, bf16x8 x) {
     return y;
 }
 
+constexpr int FEW_KEYS = 16;
+
 // dq and delta.  As in the forward kernel the scores are formed transposed (rows =
 // keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.  dq itself
 // takes delta from the rounded o, as its own sum is complete only behind the last
@@ -42,7 +46,7 @@ __device__ __forceinline__ bf16x8 rest_frag(f32x4 a, f32x4 b, bf16x8 x) {
 // A wave owns 32 rows (fp32: 16) and walks all keys, 32 at a time.  SPLIT (few rows;
 // see split_waves): the workgroup has 16 rows, a wave walks a quarter of each
 // tile's keys, and the waves' sums are added up in order.
-template <typename E, int D, bool SPLIT>
+template <typename E, int D, bool SPLIT, bool TWICE>
 __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_dq_kernel(
     const kda_window_inputs in, const E* __restrict__ o, const float* __restrict__ lse,
     const E* __restrict__ d_o, E* __restrict__ dq, float* __restrict__ row_stats, int tiles)
@@ -134,15 +138,6 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
 #pragma unroll
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (nt > 0) {
-        load(0, even);
-        store(0, even);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < NQ; ++j)
-#pragma unroll
         for (int ks = 0; ks < KS; ++ks) arrived(q[j][ks]), arrived(go[j][ks]);
     auto step = [&](int t, const E* K, E* next) __attribute__((always_inline)) {
         rows_of.keep(), k_cols.keep();
@@ -221,12 +216,43 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
         if (t + 1 < nt) store(t + 1, next);
         __syncthreads();
     };
-    int t = 0;
-    for (; t + 1 < nt; t += 2) {
-        step(t, even, odd);
-        step(t + 1, odd, even);
+    // TWICE (bf16): rows that see few keys walk them twice, the second time with the first
+    // one's exact delta.  dq is then a difference of few terms, which the error of delta
+    // (that of the rounded o) moves by more than dq's own rounding: with a window of 3, dq
+    // is off by 2.8e-3 in the norm otherwise, rounded once by 1.65e-3.
+    const int passes = TWICE && min(kr.W + in.sinks, kr.total) <= FEW_KEYS ? 2 : 1;
+    for (int pass = 0; pass < passes; ++pass) {
+        if (pass > 0) {
+            float* sums = reinterpret_cast<float*>(odd);
+            if constexpr (SPLIT) {
+                sums[tid] = exact[0];
+                __syncthreads();
+                exact[0] = sums[lane];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) exact[0] += sums[64 * w + lane];
+                __syncthreads();
+            }
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) dl[j] = group_sum(exact[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            exact[j] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) acc[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        if (nt > 0) {
+            load(0, even);
+            store(0, even);
+        }
+        __syncthreads();
+        int t = 0;
+        for (; t + 1 < nt; t += 2) {
+            step(t, even, odd);
+            step(t + 1, odd, even);
+        }
+        if (t < nt) step(t, even, odd);
     }
-    if (t < nt) step(t, even, odd);
     // SPLIT: the waves' sums, a quarter of the channels each
     constexpr int OWN = SPLIT ? D / 64 : D / 16;
     const int own = SPLIT ? wave * OWN : 0;
@@ -558,10 +584,10 @@ __global__ __launch_bounds__(256) void window_sinks_kernel(
     }
 }
 
-template <typename E, int D, bool SPLIT>
+template <typename E, int D, bool SPLIT, bool TWICE>
 static hipError_t launch_dq(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
     const int64_t tiles = row_tiles(in, WINDOW_ROWS<E, SPLIT>);
-    hipLaunchKernelGGL((window_dq_kernel<E, D, SPLIT>), grid_of(tiles * in.Hk), dim3(256), 0, stream, in, (const E*)a.o,
+    hipLaunchKernelGGL((window_dq_kernel<E, D, SPLIT, TWICE>), grid_of(tiles * in.Hk), dim3(256), 0, stream, in, (const E*)a.o,
                        a.lse, (const E*)a.d_o, (E*)a.dq, a.row_stats, (int)tiles);
     return launch_result(stream);
 }
@@ -587,7 +613,14 @@ static hipError_t launch_dkv(const kda_window_inputs& in, const WindowGrads& a, 
 template <typename E, int D>
 static hipError_t launch(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
     if (in.total_q > 0) {
-        const hipError_t e = split_waves(in) ? launch_dq<E, D, true>(in, a, stream) : launch_dq<E, D, false>(in, a, stream);
+        // few keys for every row, or for the average sequence's: the second walk's form
+        constexpr bool BF16 = sizeof(E) == 2;
+        const bool split = split_waves(in);
+        hipError_t e;
+        if (BF16 && std::min((int64_t)in.window + in.sinks, in.total_k / in.num_seqs) <= FEW_KEYS)
+            e = split ? launch_dq<E, D, true, BF16>(in, a, stream) : launch_dq<E, D, false, BF16>(in, a, stream);
+        else
+            e = split ? launch_dq<E, D, true, false>(in, a, stream) : launch_dq<E, D, false, false>(in, a, stream);
         if (e) return e;
     }
     if (in.total_k == 0) return hipSuccess;
