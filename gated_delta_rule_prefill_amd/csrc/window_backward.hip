@@ -381,10 +381,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
         const int left = te - ta - t * BQ;
         const E* qt = qp + head * in.q_head_stride + (int64_t)t * BQ * in.q_token_stride;
         const E* gt = gp + (int64_t)head * D + (int64_t)t * BQ * in.H * D;
-        if (tid < BQ) {   // rows behind the last weigh nothing: lse = inf
+        if (tid < BQ) {   // behind the last row those of its copies, which are not kept
             const float* at = sp + 2 * ((int64_t)head * in.total_q + t * BQ + min(tid, left - 1));
-            next_lse = tid < left ? at[0] : __builtin_inff();
-            next_delta = tid < left ? at[1] : 0.f;
+            next_lse = at[0];
+            next_delta = at[1];
         }
         if (left >= BQ) {
             q_tiles.fetch(wave, qt, to);
@@ -398,14 +398,16 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
     // no finite delta (each enters every product of the row's sum, with a factor that
     // is not finite or a zero that makes NaN of it).  In tiles whose rows do not all
     // see all keys such rows are taken out, and their lse is NaN: the keys that see
-    // them get NaN, the others a weight of 0 times finite values.
+    // them get NaN, the others a weight of 0 times finite values.  The copies of the
+    // last row behind it are taken out with it; they weigh nothing: lse = inf.
     auto store = [&](int u, int t) {
         if (tid < BQ) {
-            const bool bad = tid < te - ta - t * BQ && (!(__builtin_fabsf(next_lse) < __builtin_inff()) ||
-                                                        !(__builtin_fabsf(next_delta) < __builtin_inff()));
+            const bool there = tid < te - ta - t * BQ;
+            const bool bad = !(__builtin_fabsf(next_lse) < __builtin_inff()) ||
+                             !(__builtin_fabsf(next_delta) < __builtin_inff());
             const unsigned long long rows = __ballot(bad);
-            srow[u & 1][tid] = bad ? __builtin_nanf("") : next_lse;
-            srow[u & 1][BQ + tid] = bad ? 0.f : next_delta;
+            srow[u & 1][tid] = !there ? __builtin_inff() : bad ? __builtin_nanf("") : next_lse;
+            srow[u & 1][BQ + tid] = bad || !there ? 0.f : next_delta;
             if (lane == 0) bad_rows[u & 1][wave] = rows;
         }
         landed();
