@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
 
     // A head's tiles [td, tw): rows that all see all of the workgroup's keys.
     const int td = max(0, key0 + BK - 1 - (ta + off) + BQ - 1) / BQ;
-    const int tw = min((te - ta) / BQ, max(0, key0 + W - (ta + off)) / BQ);
+    const int tw = min((te - ta) / BQ, positions_in_window(key0, W, ta + off) / BQ);
     // lse and delta of a row travel with one of the first BQ threads.
     float next_lse = 0.f, next_delta = 0.f;
     const Tiles<E, D, BQ, 256> q_tiles(tid, in.q_token_stride), g_tiles(tid, (int64_t)in.H * D);

@@ -11,6 +11,13 @@ namespace kda {
 
 constexpr int WINDOW_MAX_SINKS = 64;   // one key tile of the backward pass
 
+// How many of the positions from `from` >= key on have a key in their window.  key + window
+// may pass 32 bits; key - from cannot and is not above 0.
+__host__ __device__ inline int positions_in_window(int key, int window, int from) {
+    const int n = key - from + window;
+    return n > 0 ? n : 0;
+}
+
 // The packed form and the paged one.  Paged: k and v come from the cache, and
 // total_k, cu_seqlens_k and their strides are not looked at.
 struct WindowArgs {
