@@ -37,6 +37,13 @@ __device__ __forceinline__ bf16x8 rest_frag(f32x4 a, f32x4 b, bf16x8 x) {
     return y;
 }
 
+// bf16: dq of a row that sees few keys is a difference of few terms, which the error of
+// delta (that of the rounded o) moves by more than dq's own rounding: with a window of 3,
+// dq is off by 2.8e-3 in the norm, rounded once by 1.65e-3.  Such rows take the exact
+// delta, which their weights give: a wave whose rows see no key behind the first step of
+// 32 has it before it needs it (the first 32 tokens of a sequence, but for those whose
+// wave has the 33rd too); where window and sinks together are no more than FEW_KEYS,
+// every row walks its keys twice.  The lengths of the sequences beside do not matter.
 constexpr int FEW_KEYS = 16;
 
 // dq and delta.  As in the forward kernel the scores are formed transposed (rows =
@@ -196,10 +203,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
 #pragma unroll
                                 for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        exact[j] += s[j][tt][i] * dp[j][tt][i];
-                                        s[j][tt][i] *= dp[j][tt][i] - dl[j];
-                                    }
+                                    for (int i = 0; i < 4; ++i) exact[j] += s[j][tt][i] * dp[j][tt][i];
+                                if (sizeof(E) == 2 && last_hi < 16 * TT) dl[j] = group_sum(exact[j]);   // see FEW_KEYS
+#pragma unroll
+                                for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) s[j][tt][i] *= dp[j][tt][i] - dl[j];
                                 dz[j] = acc_frag(s[j][0], s[j][TT - 1], E());
                                 if constexpr (sizeof(E) == 2) rest[j] = rest_frag(s[j][0], s[j][1], dz[j]);
                             }
@@ -216,11 +225,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
         if (t + 1 < nt) store(t + 1, next);
         __syncthreads();
     };
-    // TWICE (bf16): rows that see few keys walk them twice, the second time with the first
-    // one's exact delta.  dq is then a difference of few terms, which the error of delta
-    // (that of the rounded o) moves by more than dq's own rounding: with a window of 3, dq
-    // is off by 2.8e-3 in the norm otherwise, rounded once by 1.65e-3.
-    const int passes = TWICE && min(kr.W + in.sinks, kr.total) <= FEW_KEYS ? 2 : 1;
+    // TWICE: the second walk has the first one's exact delta.
+    constexpr int passes = TWICE ? 2 : 1;
     for (int pass = 0; pass < passes; ++pass) {
         if (pass > 0) {
             float* sums = reinterpret_cast<float*>(odd);
@@ -615,11 +621,10 @@ static hipError_t launch_dkv(const kda_window_inputs& in, const WindowGrads& a, 
 template <typename E, int D>
 static hipError_t launch(const kda_window_inputs& in, const WindowGrads& a, hipStream_t stream) {
     if (in.total_q > 0) {
-        // few keys for every row, or for the average sequence's: the second walk's form
         constexpr bool BF16 = sizeof(E) == 2;
         const bool split = split_waves(in);
         hipError_t e;
-        if (BF16 && std::min((int64_t)in.window + in.sinks, in.total_k / in.num_seqs) <= FEW_KEYS)
+        if (BF16 && (int64_t)in.window + in.sinks <= FEW_KEYS)
             e = split ? launch_dq<E, D, true, BF16>(in, a, stream) : launch_dq<E, D, false, BF16>(in, a, stream);
         else
             e = split ? launch_dq<E, D, true, false>(in, a, stream) : launch_dq<E, D, false, false>(in, a, stream);
