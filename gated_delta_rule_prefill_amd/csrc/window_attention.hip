@@ -17,10 +17,11 @@
 // that the card grants: bf16, d = 128, 32 heads over 8, window 4,096, 32,768 tokens take
 // 2.0 ms, 1.03 PFLOP/s over the pairs that see each other (a library product of 8192^3:
 // 1.15 to 1.31), and 1.69 ms on inputs of zeros.  16 documents, 36,755 tokens, window
-// 1,024: 0.64 ms, 0.77 PFLOP/s, as more of a shorter walk is masked.  16 chunks of 128
-// tokens over a cache, window 1,024: 60 us.  Without effect: more operands read ahead,
-// the next tile's scores between the exponentials, priorities of the waves; 8 waves and
-// twice the rows spill (2.25 ms).
+// 1,024: 0.64 ms, 0.77 PFLOP/s: of a workgroup's 36 us 13.5 tiles take 28, as many a tile as
+// in the long prompt, its start and end the rest.  16 chunks of 128 tokens over a cache, window
+// 1,024: 55 us in a run of a hundred, 61 as one of a program's first.  Without effect:
+// more operands read ahead, the next tile's scores between the exponentials, priorities
+// of the waves; 8 waves and twice the rows spill (2.25 ms).
 #include "window_common.h"
 
 namespace kda {

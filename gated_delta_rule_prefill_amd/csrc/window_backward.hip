@@ -15,9 +15,9 @@
 // pieces of WINDOW_PIECE tokens behind the window of the first key tile, whose parts
 // of dk and dv a third kernel adds up in order, with the first tile's own.
 //
-// bf16, d = 128, 32 heads over 8, window 1,024, 16 documents (36,755 tokens): dq 0.98 ms
+// bf16, d = 128, 32 heads over 8, window 1,024, 16 documents (36,755 tokens): dq 0.98 to 1.02 ms
 // (four products of 0.24 TFLOP over the visible pairs, as it takes dz twice: 0.99 PFLOP/s),
-// dk and dv 1.13 to 1.18 (four: 0.85, LDS: a wave reads every operand for its 16 keys
+// dk and dv 1.13 to 1.20 (four: 0.85, LDS: a wave reads every operand for its 16 keys
 // alone).  One kernel for all would have to add a part of dq for each tile of 64 keys.
 #include <algorithm>
 

@@ -364,10 +364,14 @@ static hipError_t launch(const WindowArgs& a, void* workspace, hipStream_t strea
 hipError_t launch_window_decode(const WindowArgs& a, void* workspace, hipStream_t stream) {
     // The forward kernel shares a cached row among 128 rows (fp32: 64, or 16), but its
     // walk is not split: it takes batches of many row tiles, more than one of 16 rows a
-    // sequence.  bf16, window 1,024, 32/8 heads, decode against forward in us: 1 sequence
-    // of 128 new tokens 31 and 39, 4 of 64 31 and 40, 16 of 16 31 and 38, of 32 57 and 41, 128 of
-    // 4 108 and 112, of 8 144 and 112.  fp32, window 512, 16/4 heads: 8 of 4 19 and 27, of 8 28
-    // and 27, of 16 38 and 27, of 32 52 and 57, 64 of 4 52 and 57, of 8 67 and 60.
+    // sequence on average.  bf16, window 1,024, 32/8 heads, decode against forward in us: 1
+    // sequence of 128 new tokens 21 and 38, 4 of 64 31 and 40, 16 of 16 31 and 38, of 32 57
+    // and 41, 128 of 4 108 and 113, of 8 142 and 114.  fp32, window 512, 16/4 heads: 8 of 4 19
+    // and 27, of 8 28 and 27, of 16 38 and 27, of 32 52 and 57, 64 of 4 52 and 57, of 8 67 and 60.
+    // Batches of single tokens and one chunk go as a whole: 255 and a chunk of 128 209 and
+    // 231, of 512 244 and 232, of 900 278 and 239, of 2,000 375 and 266; 63 and 2,000 241 and
+    // 117; 31 and 128 37 and 50, 31 and 512 74 and 52.  The rule takes the other kernel for
+    // 255 and 512, 31 and 128.
     const int64_t G = a.in.H / a.in.Hk;
     if (a.in.total_q * G > 16 * (int64_t)a.in.num_seqs &&
         decode_units(a.in) > (a.in.dtype == KDA_DTYPE_BF16 ? 512 : 64))

@@ -512,7 +512,9 @@ kda_status kda_rotary_frequencies(int32_t dr, double base, double factor,
  *              keys that the mask hides, rows behind a sequence's end and unused
  *              cache rows may hold anything.  How far a value that is not finite
  *              spreads within a row that sees it (its other channels, lse) is not
- *              specified.
+ *              specified.  A score of -Inf weighs nothing; a row all of whose
+ *              scores are -Inf gets o = 0 and lse = -inf, as one that sees no
+ *              key, and gradients that are not finite.
  * ---------------------------------------------------------------------------
  */
 
