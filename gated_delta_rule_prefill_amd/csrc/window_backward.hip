@@ -37,6 +37,8 @@ __device__ __forceinline__ bf16x8 rest_frag(f32x4 a, f32x4 b, bf16x8 x) {
     return y;
 }
 
+__device__ __forceinline__ f32x8 rest_frag(f32x4, f32x4, f32x8) { return f32x8{}; }   // nothing, and never asked for
+
 // bf16: dq of a row that sees few keys is a difference of few terms, which the error of
 // delta (that of the rounded o) moves by more than dq's own rounding: with a window of 3,
 // dq is off by 2.8e-3 in the norm, rounded once by 1.65e-3.  Such rows take the exact
@@ -318,6 +320,12 @@ struct KeyWork {
     __device__ __forceinline__ int64_t slot(int s) const { return q0 / WINDOW_PIECE + 2 * (int64_t)s; }
 };
 
+// bf16: walks of no more than so many tokens take the weights and dz in two parts as well:
+// where a few of them make the gradients of all keys their rounding shows (21 documents of
+// 1 to 9 tokens: error of dk 2.6e-3, with two parts 1.7e-3).  In code of its own: a branch
+// at the products cost the long walks 15 % (packed step 1,204 -> 1,440 us).
+constexpr int FEW_ROWS = 32;
+
 // dk and dv.  A wave owns 16 keys, whose k and v operands and gradients stay in
 // registers; the query rows come 64 tokens of one head at a time (fp32: 32), head after
 // head of the group, and are worked on 32 at a time (32 tokens a time, with twice the
@@ -431,7 +439,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) arrived(k[ks]), arrived(v[ks]);
     // Tile t of a head's tokens, number u of all; the next one is nt of nhead.
-    auto step = [&](int u, int t, int nhead, int nt, E* Q, E* next) __attribute__((always_inline)) {
+    auto step = [&](int u, int t, int nhead, int nt, E* Q, E* next, auto few) __attribute__((always_inline)) {
+        constexpr bool FEW = decltype(few)::value != 0;
         rows_of.keep(), cols_of.keep();
         E* Gt = Q + BQ * D;
         if (u + 1 < nu) load(nhead, nt, next);
@@ -468,7 +477,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
             // g v^T, between whose products the weights' exponentials run;
             // dv^T += g^T w, between whose products dz is formed; dk^T += q^T dz.
             constexpr int E0 = RT * KS, E1 = 2 * E0, E2 = E1 + D / 16, NS = 4 * RT;
-            v8 wf, zf;
+            v8 wf, zf, rest;
             ahead<E2 + D / 16, PD>(
                 [&](auto n) {
                     constexpr int e = n;
@@ -501,34 +510,44 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 && !SPLIT ? 2 : 1) void window_
                                 }
                             }
                             wf = acc_frag(s[0], s[RT - 1], E());
+                            if constexpr (FEW) rest = rest_frag(s[0], s[1], wf);
                         }
                         av[c] = mma_rows<RT>(a, wf, av[c]);
+                        if constexpr (FEW) av[c] = mma32(a, rest, av[c]);
 #pragma unroll
                         for (int i = NS * c / (D / 16); i < NS * (c + 1) / (D / 16); ++i)
                             dp[i / 4][i % 4] = s[i / 4][i % 4] * (dp[i / 4][i % 4] - de[i / 4][i % 4]);
                     } else {
                         constexpr int c = e - E2;
-                        if (c == 0) zf = acc_frag(dp[0], dp[RT - 1], E());
+                        if (c == 0) {
+                            zf = acc_frag(dp[0], dp[RT - 1], E());
+                            if constexpr (FEW) rest = rest_frag(dp[0], dp[1], zf);
+                        }
                         ak[c] = mma_rows<RT>(a, zf, ak[c]);
+                        if constexpr (FEW) ak[c] = mma32(a, rest, ak[c]);
                     }
                 });
         }
         if (u + 1 < nu) store(u + 1, nt);
         __syncthreads();
     };
-    int head = 0, t = 0;
-    auto next = [&](int u, E* Q, E* to) __attribute__((always_inline)) {
-        const int nt = t + 1 < per ? t + 1 : 0, nhead = nt ? head : head + 1;
-        step(u, t, nhead, nt, Q, to);
-        t = nt;
-        head = nhead;
+    auto walk = [&](auto few) __attribute__((always_inline)) {
+        int head = 0, t = 0;
+        auto next = [&](int u, E* Q, E* to) __attribute__((always_inline)) {
+            const int nt = t + 1 < per ? t + 1 : 0, nhead = nt ? head : head + 1;
+            step(u, t, nhead, nt, Q, to, few);
+            t = nt;
+            head = nhead;
+        };
+        int u = 0;
+        for (; u + 1 < nu; u += 2) {
+            next(u, even, odd);
+            next(u + 1, odd, even);
+        }
+        if (u < nu) next(u, even, odd);
     };
-    int u = 0;
-    for (; u + 1 < nu; u += 2) {
-        next(u, even, odd);
-        next(u + 1, odd, even);
-    }
-    if (u < nu) next(u, even, odd);
+    if (sizeof(E) == 2 && te - ta <= FEW_ROWS) walk(Int<sizeof(E) == 2>());
+    else walk(Int<0>());
     // SPLIT: the waves' sums, a quarter of the channels each
     constexpr int OWN = SPLIT ? D / 64 : D / 16;
     const int own = SPLIT ? wave * OWN : 0;

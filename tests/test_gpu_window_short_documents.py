@@ -1,4 +1,4 @@
-"""dq of short documents does not lose bits to the documents beside them (bf16)."""
+"""Gradients of short documents, alone and beside long ones (bf16)."""
 import pytest
 import torch
 
@@ -36,3 +36,23 @@ def test_short_documents_beside_long_ones(empty, d, short, long, window, sinks):
             err = float(off[rows].norm() / want[rows].norm())
             print(f"[window] dq, {name}: {err:.2e}", flush=True)
             assert err <= 2.0e-3, name
+
+
+@pytest.mark.parametrize("empty", [0, 600], ids=["split", "whole"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (16, 4)])
+@pytest.mark.parametrize("short,long", [([8] * 30, [1000]), ([31, 5, 17, 32] * 4, [700, 300]), ([1, 3, 2, 4, 9, 5] * 4, [])])
+def test_keys_that_few_rows_see(empty, d, H, Hk, short, long):
+    """dk and dv of documents of at most 32 tokens: few weights make them, so that a
+    rounding of each would show (2.3e-3 in the norm, and up to 2.6e-3 in a small batch).  As
+    for dq above: their own rounding, 1.66e-3, and a fifth more."""
+    lens = short[:len(short) // 2] + long + short[len(short) // 2:] + [0] * empty
+    x = ta.make(212, "bf16", H, Hk, d, lens, lens)
+    got = ta.both(x, lens, lens, 500, 4)
+    want = ref.attention(x["q"], x["k"], x["v"], lens, lens, 500, 4, d_o=x["d_o"])
+    size = torch.cat([torch.full((n,), n) for n in lens])
+    for name in ("dk", "dv"):
+        value = want[name][0][size <= 32]
+        err = float((got[name].double().cpu()[size <= 32] - value).norm() / value.norm())
+        print(f"[window] {name}: {err:.2e}", flush=True)
+        assert err <= 2.0e-3, name
