@@ -51,7 +51,7 @@ constexpr int FEW_KEYS = 16;
 // dq and delta.  As in the forward kernel the scores are formed transposed (rows =
 // keys), so that dz^T is the operand of dq^T += K^T dz^T as it stands.  dq itself
 // takes delta from the rounded o, as its own sum is complete only behind the last
-// key; the second kernel takes that sum.
+// key (but see FEW_KEYS); the second kernel takes that sum.
 // A wave owns 32 rows (fp32: 16) and walks all keys, 32 at a time.  SPLIT (few rows;
 // see split_waves): the workgroup has 16 rows, a wave walks a quarter of each
 // tile's keys, and the waves' sums are added up in order.
